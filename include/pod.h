@@ -385,6 +385,105 @@ pod_status pod_run_static_scratch(pod_handle h, const void* q_p, const void* kv_
  * Library mechanics; no passage. */
 size_t pod_static_scratch_capacity(void);
 
+/* ------------------------------------------------------------------------
+ * Operators around the paged cache.
+ *
+ * Slots: row i of a call lives in slot slots[i] = page * page_size + position
+ * in the page, DEVICE int64 (request r's key t: page kv_indices[kv_indptr[r] +
+ * t / page_size], position t % page_size). A negative slot is a padding row.
+ * A slot at or past num_pages * page_size is treated like a negative one, and
+ * sets bit 4 of *status (DEVICE int32, or NULL for no report; never cleared
+ * here). Rows of one write that name the same slot leave either of their
+ * values, element by element.
+ *
+ * Cache formats (kv_format), both page layouts (kv_layout 0 = NHD, 1 = HND):
+ *  POD_KV_16BIT       the values, in the call's dtype
+ *  POD_KV_E4M3        E4M3 codes with per-tensor scales: value = code *
+ *                     k_scale (v_scale for V), the cache that
+ *                     pod_plan_set_decode_fp8 reads. code = E4M3(x / scale).
+ *  POD_KV_E4M3_BLOCK  E4M3 codes and one exponent byte b for each (token, KV
+ *                     head) of K and of V: value = code * 2^(b - 127), with
+ *                     the smallest b that keeps the head row's codes within
+ *                     +-448. kv_scales holds the bytes,
+ *                     [num_pages, 2, page_size, Hk] or, HND,
+ *                     [num_pages, 2, Hk, page_size].
+ * Codes are rounded to nearest even and saturate at +-448; NaN stays NaN.
+ *
+ * Strides are elements from one token's row to the next, multiples of 8; the
+ * heads of a row are contiguous ([heads, head_dim]), so slices of a fused
+ * projection's output can be passed as they are. Pointers are 16-byte aligned.
+ * head_dim is 64, 128 or 256; dtype is that of every 16-bit tensor of a call.
+ * The calls only launch on `stream` (of the current device) and can be
+ * captured in a CUDA graph; rows = 0 launches nothing.
+ * ------------------------------------------------------------------------ */
+typedef enum { POD_KV_16BIT = 0, POD_KV_E4M3 = 1, POD_KV_E4M3_BLOCK = 2 } pod_kv_format;
+
+/*
+ * pod_qk_norm_rope — RMS norm of every head of q and k, and the rotary
+ * position encoding, in one pass.
+ * y = x * (mean(x^2) + eps)^(-1/2) * weight over the head's elements (no norm
+ * where the weight, [head_dim] in dtype, is NULL); then pair (j, j +
+ * rotary_dim/2), or (2j, 2j+1) with `interleaved`, turns by
+ * (positions[row] / rope_scale) * rope_theta^(-2j/rotary_dim) (the rotation of
+ * pod_plan_set_rope, here over the first rotary_dim elements; 0 = none).
+ * fp32 throughout, rounded once. positions: DEVICE int32 [rows], any sign, NULL
+ * when rotary_dim is 0. num_qo_heads or num_kv_heads may be 0 (then that
+ * tensor is not touched). q_out may be q, and k_out k, with the same stride.
+ * Errors: POD_ERR_INVALID_ARG (NULL, misaligned or overlapping-by-stride rows,
+ * rotary_dim not a multiple of 16 up to head_dim, no heads, bad eps or rope
+ * settings), POD_ERR_UNSUPPORTED (head_dim, dtype), POD_ERR_CUDA.
+ */
+pod_status pod_qk_norm_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
+                            int64_t rows, int32_t num_qo_heads, int32_t num_kv_heads,
+                            int32_t head_dim, const void* q_weight, const void* k_weight, float eps,
+                            const int32_t* positions, int32_t rotary_dim, int32_t interleaved,
+                            float rope_scale, float rope_theta, pod_dtype dtype, void* q_out,
+                            void* k_out, int64_t q_out_stride, int64_t k_out_stride, void* stream);
+
+/*
+ * pod_append_kv — write rows of K and V ([rows, Hk, head_dim]) into their slots
+ * of the cache [num_pages, 2, ...] in the cache's format. Other slots keep
+ * their bytes. k_scale / v_scale count for POD_KV_E4M3 only; kv_scales for
+ * POD_KV_E4M3_BLOCK only (NULL otherwise).
+ * Errors: POD_ERR_INVALID_ARG, POD_ERR_UNSUPPORTED, POD_ERR_CUDA.
+ */
+pod_status pod_append_kv(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                         int64_t rows, const int64_t* slots, void* kv_cache, uint8_t* kv_scales,
+                         int64_t num_pages, int32_t page_size, int32_t num_kv_heads,
+                         int32_t head_dim, int32_t kv_layout, int32_t kv_format, float k_scale,
+                         float v_scale, pod_dtype dtype, int32_t* status, void* stream);
+
+/*
+ * pod_norm_rope_append — pod_qk_norm_rope and pod_append_kv in one pass: q is
+ * normed and rotated into q_out, k is normed, rotated and written into the
+ * cache (from fp32, with no 16-bit rounding in between for the FP8 formats), v
+ * is written as it is. num_qo_heads may be 0. Rows with a negative slot still
+ * give their q_out.
+ */
+pod_status pod_norm_rope_append(const void* q, const void* k, const void* v, int64_t q_stride,
+                                int64_t k_stride, int64_t v_stride, int64_t rows,
+                                const void* q_weight, const void* k_weight, float eps,
+                                const int32_t* positions, int32_t rotary_dim, int32_t interleaved,
+                                float rope_scale, float rope_theta, void* q_out,
+                                int64_t q_out_stride, const int64_t* slots, void* kv_cache,
+                                uint8_t* kv_scales, int64_t num_pages, int32_t page_size,
+                                int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
+                                int32_t kv_layout, int32_t kv_format, float k_scale, float v_scale,
+                                pod_dtype dtype, int32_t* status, void* stream);
+
+/*
+ * pod_gather_kv — read cache rows back: out [rows, 2, Hk, head_dim] (K, then V)
+ * in dtype, value = code * scale rounded to nearest, finite values saturating
+ * at the type's largest; a padding row reads as zeros. `out` is also an NHD
+ * cache of page size 1 (pages 0 .. rows-1), so the 16-bit prefill half can run
+ * over an FP8 cache's context.
+ */
+pod_status pod_gather_kv(const void* kv_cache, const uint8_t* kv_scales, int64_t num_pages,
+                         int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
+                         int32_t kv_layout, int32_t kv_format, float k_scale, float v_scale,
+                         const int64_t* slots, int64_t rows, pod_dtype dtype, void* out,
+                         int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

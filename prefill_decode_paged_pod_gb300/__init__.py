@@ -32,6 +32,7 @@ __all__ = [
     "pod_run_static_scratch", "pod_static_scratch_capacity", "pod_plan_set_decode_fp8",
     "pod_plan_set_prefill_mask", "pod_plan_set_kv_layout", "pod_plan_set_logits_transform",
     "pod_plan_set_rope", "pod_plan_set_graph_capacity", "pod_replan",
+    "pod_qk_norm_rope", "pod_append_kv", "pod_norm_rope_append", "pod_gather_kv", "pod_kv_slots",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -98,6 +99,20 @@ def load_library(path: Optional[str] = None):
     lib.pod_plan_set_graph_capacity.argtypes = [V] + [I32] * 6
     lib.pod_replan.restype = ctypes.c_int
     lib.pod_replan.argtypes = [V, V, V, V, V, I32, V, V, V, V, I32, V]
+    I64, F32 = ctypes.c_int64, ctypes.c_float
+    lib.pod_qk_norm_rope.restype = ctypes.c_int
+    lib.pod_qk_norm_rope.argtypes = [V, V, I64, I64, I64, I32, I32, I32, V, V, F32, V, I32, I32, F32,
+                                     F32, ctypes.c_int, V, V, I64, I64, V]
+    lib.pod_append_kv.restype = ctypes.c_int
+    lib.pod_append_kv.argtypes = [V, V, I64, I64, I64, V, V, V, I64, I32, I32, I32, I32, I32, F32, F32,
+                                  ctypes.c_int, V, V]
+    lib.pod_norm_rope_append.restype = ctypes.c_int
+    lib.pod_norm_rope_append.argtypes = [V, V, V, I64, I64, I64, I64, V, V, F32, V, I32, I32, F32, F32,
+                                         V, I64, V, V, V, I64, I32, I32, I32, I32, I32, I32, F32, F32,
+                                         ctypes.c_int, V, V]
+    lib.pod_gather_kv.restype = ctypes.c_int
+    lib.pod_gather_kv.argtypes = [V, V, I64, I32, I32, I32, I32, I32, F32, F32, V, I64, ctypes.c_int,
+                                  V, V, V]
     if path is None:
         _lib = lib
     return lib
@@ -467,3 +482,253 @@ def pod_replan(h: PodHandle, p_q_indptr, p_kv_indptr, p_kv_indices, p_last_page_
     d_batch = 0 if arrs[4] is None else len(arrs[4]) - 1
     _check(load_library().pod_replan(ctypes.c_void_p(h.ptr), *[_ptr(a) for a in arrs[:4]], p_batch,
                                      *[_ptr(a) for a in arrs[4:]], d_batch, _stream(stream)))
+
+
+# ------------------------------------------------------------------ operators around the cache
+def pod_kv_slots(kv_indptr, kv_indices, page_size: int, request, position):
+    """Slots of key ``position[i]`` of request ``request[i]`` (int64, the
+    ``slots`` of pod_append_kv and the others): numpy arrays or tensors of one
+    device in, the same kind out."""
+    page = kv_indices[kv_indptr[request] + position // page_size]
+    page = page.long() if hasattr(page, "long") else page.astype(np.int64)
+    return page * page_size + position % page_size
+
+
+def _on_device(name, t, dev, dtype, ndim):
+    if t.device != dev or t.dtype != dtype or t.dim() != ndim or not t.is_contiguous():
+        raise PodError(1, f"{name} must be a contiguous {ndim}-d {dtype} tensor on {dev}")
+
+
+def _heads(name, t, dtype, dev, rows=None):
+    """[rows, heads, d] with contiguous heads; returns (rows, heads, d, row stride)."""
+    if t.dim() != 3 or t.dtype != dtype or t.device != dev or not t.is_cuda:
+        raise PodError(1, f"{name} must be a [rows, heads, head_dim] {dtype} CUDA tensor on {dev}")
+    n, h, d = t.shape
+    sn, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and h > 1):
+        raise PodError(1, f"{name}: the heads of a row must be contiguous")
+    if rows is not None and n != rows:
+        raise PodError(1, f"{name} has {n} rows, not {rows}")
+    return n, h, d, sn if n > 1 else max(sn, h * d) // 8 * 8
+
+
+def _weight(name, w, d, dtype, dev):
+    if w is None:
+        return None
+    _on_device(name, w, dev, dtype, 1)
+    if w.numel() != d:
+        raise PodError(1, f"{name} must have head_dim elements")
+    return w.data_ptr()
+
+
+def _positions(positions, rows, rotary_dim, dev):
+    if positions is None:
+        if rotary_dim:
+            raise PodError(1, "the rotation needs positions")
+        return None
+    import torch
+    _on_device("positions", positions, dev, torch.int32, 1)
+    if positions.numel() != rows:
+        raise PodError(1, f"positions has {positions.numel()} rows, not {rows}")
+    return positions.data_ptr()
+
+
+def _status(status, dev):
+    if status is None:
+        return None
+    import torch
+    if status.dtype != torch.int32 or status.device != dev or status.numel() < 1:
+        raise PodError(1, f"status must be an int32 tensor on {dev}")
+    return status.data_ptr()
+
+
+_KV_FORMATS = {"16bit": 0, "scaled": 1, "block": 2}
+
+
+def _cache_args(kv_cache, kv_scales, kv_layout, dtype, dev):
+    """(cache pointer, scales pointer, pages, page size, Hk, d, layout, format)
+    of a paged cache: 16-bit, or E4M3 codes with or without scale bytes."""
+    import torch
+    if kv_layout not in _LAYOUTS:
+        raise PodError(1, f"unknown kv layout {kv_layout!r}")
+    hnd = _LAYOUTS[kv_layout]
+    if (kv_cache.dim() != 5 or kv_cache.shape[1] != 2 or kv_cache.device != dev
+            or not kv_cache.is_contiguous()):
+        raise PodError(1, f"kv_cache must be a contiguous [pages, 2, ...] page pool on {dev}")
+    pages, _, a, b, d = kv_cache.shape
+    ps, hk = (b, a) if hnd else (a, b)
+    if kv_cache.dtype == dtype:
+        fmt = 0
+    elif kv_cache.dtype == torch.float8_e4m3fn:
+        fmt = 1 if kv_scales is None else 2
+    else:
+        raise PodError(2, f"kv_cache must be {dtype} or float8_e4m3fn, not {kv_cache.dtype}")
+    if kv_scales is not None:
+        if fmt == 0:
+            raise PodError(1, "kv_scales given, but the cache is a 16-bit one")
+        if (kv_scales.dtype != torch.uint8 or kv_scales.device != dev
+                or kv_scales.shape != kv_cache.shape[:4] or not kv_scales.is_contiguous()):
+            raise PodError(1, f"kv_scales must be contiguous uint8 {tuple(kv_cache.shape[:4])} on {dev}")
+    return (kv_cache.data_ptr(), None if kv_scales is None else kv_scales.data_ptr(), pages, ps, hk, d,
+            hnd, fmt)
+
+
+class _Launch:
+    """The tensors' device made current (where it is not), and the stream: the
+    given one, or torch's current stream of that device."""
+    __slots__ = ("dev", "prev", "stream")
+
+    def __init__(self, dev, stream):
+        self.dev, self.prev, self.stream = dev, None, stream
+
+    def __enter__(self):
+        import torch
+        now = torch.cuda.current_device()
+        if now != self.dev.index:
+            self.prev = now
+            torch.cuda.set_device(self.dev)
+        if self.stream is None:
+            return torch.cuda.current_stream(self.dev).cuda_stream
+        return self.stream if isinstance(self.stream, int) else self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            import torch
+            torch.cuda.set_device(self.prev)
+
+
+def _device_of(t):
+    if t is None or not t.is_cuda:
+        raise PodError(1, "the tensors must be CUDA tensors")
+    return t.device
+
+
+def _out_rows(name, out, shape, dtype, dev):
+    """An output [rows, heads, d]: a new tensor, or the caller's with its row stride."""
+    if out is None:
+        import torch
+        return torch.empty(shape, dtype=dtype, device=dev), shape[1] * shape[2]
+    n, h, d, stride = _heads(name, out, dtype, dev, shape[0])
+    if (h, d) != (shape[1], shape[2]):
+        raise PodError(1, f"{name} must be {tuple(shape)}")
+    return out, stride
+
+
+def pod_qk_norm_rope(q, k, positions=None, *, q_weight=None, k_weight=None, eps=1e-6, rotary_dim=None,
+                     interleaved=False, rope_scale=1.0, rope_theta=1e4, q_out=None, k_out=None,
+                     stream=None):
+    """RMS norm of every head of q [rows, H, d] and k [rows, Hk, d] (where its
+    weight is given) and the rotation of the first ``rotary_dim`` elements
+    (default all, 0 none) at int32 ``positions``, in one pass. q and k may be
+    slices of a fused projection (any row stride that is a multiple of 8);
+    either may be None. Returns (q_out, k_out); pass q_out=q, k_out=k to work
+    in place."""
+    lib = load_library()
+    t = q if q is not None else k
+    dev, dtype = _device_of(t), t.dtype
+    code = _dtype_code(dtype)
+    rows, H, d, qs = (0, 0, 0, 0) if q is None else _heads("q", q, dtype, dev)
+    if k is not None:
+        rows, Hk, dk, ks = _heads("k", k, dtype, dev, None if q is None else rows)
+        if q is not None and dk != d:
+            raise PodError(1, "q and k have different head_dim")
+        d = dk
+    else:
+        Hk, ks = 0, 0
+    R = d if rotary_dim is None else int(rotary_dim)
+    pos = _positions(positions, rows, R, dev)
+    wq, wk = _weight("q_weight", q_weight, d, dtype, dev), _weight("k_weight", k_weight, d, dtype, dev)
+    qos = kos = 0
+    if q is not None:
+        q_out, qos = _out_rows("q_out", q_out, (rows, H, d), dtype, dev)
+    if k is not None:
+        k_out, kos = _out_rows("k_out", k_out, (rows, Hk, d), dtype, dev)
+    with _Launch(dev, stream) as st:
+        _check(lib.pod_qk_norm_rope(_ptr(q), _ptr(k), qs, ks, rows, H, Hk, d, wq, wk, float(eps), pos, R,
+                                    int(bool(interleaved)), float(rope_scale), float(rope_theta), code,
+                                    _ptr(q_out) if H else None, _ptr(k_out) if Hk else None, qos, kos, st))
+    return (q_out if q is not None else None), (k_out if k is not None else None)
+
+
+def pod_append_kv(k, v, kv_cache, slots, *, kv_scales=None, k_scale=1.0, v_scale=1.0, kv_layout="NHD",
+                  status=None, stream=None):
+    """Write rows of k and v [rows, Hk, d] into the int64 ``slots`` of a paged
+    cache: a cache of k's dtype takes the values, a float8_e4m3fn one E4M3
+    codes, with the per-tensor k_scale and v_scale or, where ``kv_scales``
+    (uint8, the cache's shape without head_dim) is given, a power-of-two scale
+    per token and KV head. Negative slots are skipped."""
+    lib = load_library()
+    dev, dtype = _device_of(k), k.dtype
+    code = _dtype_code(dtype)
+    rows, Hk, d, ks = _heads("k", k, dtype, dev)
+    _, hv, dv, vs = _heads("v", v, dtype, dev, rows)
+    cache, scales, pages, ps, hc, dc, hnd, fmt = _cache_args(kv_cache, kv_scales, kv_layout, dtype, dev)
+    if (hv, dv) != (Hk, d) or (hc, dc) != (Hk, d):
+        raise PodError(1, "k, v and kv_cache differ in heads or head_dim")
+    import torch
+    _on_device("slots", slots, dev, torch.int64, 1)
+    if slots.numel() != rows:
+        raise PodError(1, f"slots has {slots.numel()} rows, not {rows}")
+    with _Launch(dev, stream) as st:
+        _check(lib.pod_append_kv(k.data_ptr(), v.data_ptr(), ks, vs, rows, slots.data_ptr(), cache, scales,
+                                 pages, ps, Hk, d, hnd, fmt, float(k_scale), float(v_scale), code,
+                                 _status(status, dev), st))
+
+
+def pod_norm_rope_append(q, k, v, positions, kv_cache, slots, *, q_weight=None, k_weight=None, eps=1e-6,
+                         rotary_dim=None, interleaved=False, rope_scale=1.0, rope_theta=1e4,
+                         kv_scales=None, k_scale=1.0, v_scale=1.0, kv_layout="NHD", q_out=None,
+                         status=None, stream=None):
+    """pod_qk_norm_rope and pod_append_kv in one pass: returns q normed and
+    rotated (None without q), writes k (normed and rotated) and v into the
+    cache."""
+    lib = load_library()
+    dev, dtype = _device_of(k), k.dtype
+    code = _dtype_code(dtype)
+    rows, Hk, d, ks = _heads("k", k, dtype, dev)
+    _, hv, dv, vs = _heads("v", v, dtype, dev, rows)
+    _, H, dq, qs = (rows, 0, d, 0) if q is None else _heads("q", q, dtype, dev, rows)
+    cache, scales, pages, ps, hc, dc, hnd, fmt = _cache_args(kv_cache, kv_scales, kv_layout, dtype, dev)
+    if (hv, dv) != (Hk, d) or (hc, dc) != (Hk, d) or dq != d:
+        raise PodError(1, "q, k, v and kv_cache differ in heads or head_dim")
+    import torch
+    _on_device("slots", slots, dev, torch.int64, 1)
+    if slots.numel() != rows:
+        raise PodError(1, f"slots has {slots.numel()} rows, not {rows}")
+    R = d if rotary_dim is None else int(rotary_dim)
+    pos = _positions(positions, rows, R, dev)
+    wq, wk = _weight("q_weight", q_weight, d, dtype, dev), _weight("k_weight", k_weight, d, dtype, dev)
+    qos = 0
+    if q is not None:
+        q_out, qos = _out_rows("q_out", q_out, (rows, H, d), dtype, dev)
+    with _Launch(dev, stream) as st:
+        _check(lib.pod_norm_rope_append(
+            _ptr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, rows, wq, wk, float(eps), pos, R,
+            int(bool(interleaved)), float(rope_scale), float(rope_theta), _ptr(q_out) if H else None, qos,
+            slots.data_ptr(), cache, scales, pages, ps, H, Hk, d, hnd, fmt, float(k_scale), float(v_scale),
+            code, _status(status, dev), st))
+    return q_out if q is not None else None
+
+
+def pod_gather_kv(kv_cache, slots, *, dtype, kv_scales=None, k_scale=1.0, v_scale=1.0, kv_layout="NHD",
+                  out=None, status=None, stream=None):
+    """Cache rows of the int64 ``slots`` back as ``dtype`` values:
+    [rows, 2, Hk, d], K then V; a negative slot reads as zeros. The result
+    viewed as [rows, 2, 1, Hk, d] is an NHD cache of page size 1."""
+    import torch
+    lib = load_library()
+    dev = _device_of(kv_cache)
+    code = _dtype_code(dtype)
+    cache, scales, pages, ps, Hk, d, hnd, fmt = _cache_args(kv_cache, kv_scales, kv_layout, dtype, dev)
+    _on_device("slots", slots, dev, torch.int64, 1)
+    rows = slots.numel()
+    if out is None:
+        out = torch.empty((rows, 2, Hk, d), dtype=dtype, device=dev)
+    else:
+        _on_device("out", out, dev, dtype, 4)
+        if tuple(out.shape) != (rows, 2, Hk, d):
+            raise PodError(1, f"out must be {(rows, 2, Hk, d)}")
+    with _Launch(dev, stream) as st:
+        _check(lib.pod_gather_kv(cache, scales, pages, ps, Hk, d, hnd, fmt, float(k_scale), float(v_scale),
+                                 slots.data_ptr(), rows, code, out.data_ptr(), _status(status, dev), st))
+    return out
