@@ -484,6 +484,80 @@ pod_status pod_gather_kv(const void* kv_cache, const uint8_t* kv_scales, int64_t
                          const int64_t* slots, int64_t rows, pod_dtype dtype, void* out,
                          int32_t* status, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Attention of drafted token trees over a paged cache (verification of drafted
+ * tokens): every request's n = q_len tokens are the last n keys of its cache
+ * (written before the run), token i sees every context key (t < kv_len - n)
+ * and the drafted tokens j whose bit (i, j) of the tree mask is set.
+ * ------------------------------------------------------------------------ */
+typedef struct pod_tree_s* pod_tree_handle;
+
+/*
+ * pod_tree_plan — host planner: checks the page tables, cuts the keys of every
+ * (request, KV head, 128 packed rows) into equal work for the CTAs of one
+ * launch, and lays out the workspace. Plan once per step, run once per layer.
+ * The index arrays are HOST int32 (read during the call only): q_indptr
+ * [batch+1], kv_indptr [batch+1], kv_indices, last_page_len [batch], as for
+ * pod_plan. sm_scale <= 0 means 1/sqrt(head_dim). kv_format and kv_layout as
+ * above (k_scale, v_scale count for POD_KV_E4M3). head_dim 64, 128 or 256 in
+ * every format; any number of query heads per KV head and of tokens; any page
+ * size (powers of two from 8 are loaded by TMA, others gathered). num_sms,
+ * workspace, out_handle and required_workspace_bytes as for pod_plan; without
+ * a workspace bind one later. Not capturable in a CUDA graph.
+ * Errors: POD_ERR_INVALID_ARG (tables that do not fit together, an index
+ * outside the pool, fewer keys than tokens, scales that are not finite and
+ * positive), POD_ERR_UNSUPPORTED (head_dim, dtype, heads), POD_ERR_WORKSPACE,
+ * POD_ERR_CUDA. On error *out_handle is NULL.
+ */
+pod_status pod_tree_plan(const int32_t* q_indptr, const int32_t* kv_indptr, const int32_t* kv_indices,
+                         const int32_t* last_page_len, int32_t batch, int32_t num_pages,
+                         int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
+                         int32_t page_size, float sm_scale, pod_dtype dtype, int32_t kv_format,
+                         float k_scale, float v_scale, int32_t kv_layout, int32_t has_sinks,
+                         int32_t num_sms, void* workspace, size_t workspace_bytes, void* stream,
+                         pod_tree_handle* out_handle, size_t* required_workspace_bytes);
+
+/* Bytes of device workspace the plan needs (0 for a NULL handle). */
+size_t pod_tree_workspace_size(pod_tree_handle h);
+
+/* Copy the plan into `workspace` (device, 256-byte aligned) and wait for it. */
+pod_status pod_tree_bind_workspace(pod_tree_handle h, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * pod_tree_run — q, out: [rows, H, head_dim] (dtype); kv: the cache
+ * [num_pages, 2, ...]; kv_scales: exponent bytes of a POD_KV_E4M3_BLOCK cache,
+ * else NULL; lse: fp32 [rows, H] base 2, or NULL; sinks: fp32 [H] exactly when
+ * the plan has them (exp(sink) joins each row's denominator, not its LSE).
+ * tree_mask: DEVICE bits, request r's [n_r, n_r] matrix in row-major order,
+ * the requests end to end, eight bits to a byte, the first lowest (the layout
+ * of pod_plan_set_prefill_mask's); mask_bytes covers ceil(sum n_r^2 / 8), and
+ * no byte past it is read. NULL: token i sees drafted tokens 0..i (a chain).
+ * The diagonal is a bit like the others. A row without visible keys gives
+ * out = 0 and lse = -inf. Slots at or past kv_len may hold anything; the values
+ * of every key below it must be finite (a masked key's weight is 0, and 0
+ * times an infinity is NaN).
+ * The workspace must be the bound one; runs that share it must not overlap.
+ * Launches on `stream` only and can be captured; a replay reads the tensors
+ * again under the same plan, while the workspace still holds it.
+ * Errors: POD_ERR_INVALID_ARG, POD_ERR_WORKSPACE, POD_ERR_CUDA.
+ */
+pod_status pod_tree_run(pod_tree_handle h, const void* q, const void* kv, const uint8_t* kv_scales,
+                        const void* tree_mask, int64_t mask_bytes, const float* sinks, void* workspace,
+                        void* out, float* lse, void* stream);
+
+/* As pod_read_device_status, for a tree plan's workspace. */
+pod_status pod_tree_read_device_status(pod_tree_handle h, void* workspace, void* stream,
+                                       int32_t* device_status);
+
+/* Host copy of a plan table, for inspection and tests: 0 = segments, 1 = first
+ * segment of each CTA, 2 = merge groups (records in csrc/pod_tree.h), 3 = page
+ * table. Copies min(count, capacity) values; out may be NULL. */
+pod_status pod_tree_plan_table(pod_tree_handle h, int32_t which, int32_t* out, int64_t capacity,
+                               int64_t* count);
+
+/* Release the handle (host memory only). NULL is accepted. */
+pod_status pod_tree_destroy(pod_tree_handle h);
+
 #ifdef __cplusplus
 }
 #endif

@@ -33,6 +33,8 @@ __all__ = [
     "pod_plan_set_prefill_mask", "pod_plan_set_kv_layout", "pod_plan_set_logits_transform",
     "pod_plan_set_rope", "pod_plan_set_graph_capacity", "pod_replan",
     "pod_qk_norm_rope", "pod_append_kv", "pod_norm_rope_append", "pod_gather_kv", "pod_kv_slots",
+    "PodTreeHandle", "pod_tree_plan", "pod_tree_run", "pod_tree_workspace_size", "pod_tree_bind_workspace",
+    "pod_tree_read_device_status", "pod_tree_plan_table", "pod_tree_destroy",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -113,6 +115,21 @@ def load_library(path: Optional[str] = None):
     lib.pod_gather_kv.restype = ctypes.c_int
     lib.pod_gather_kv.argtypes = [V, V, I64, I32, I32, I32, I32, I32, F32, F32, V, I64, ctypes.c_int,
                                   V, V, V]
+    lib.pod_tree_plan.restype = ctypes.c_int
+    lib.pod_tree_plan.argtypes = [V, V, V, V, I32, I32, I32, I32, I32, I32, F32, ctypes.c_int, I32, F32, F32,
+                                  I32, I32, I32, V, SZ, V, ctypes.POINTER(V), ctypes.POINTER(SZ)]
+    lib.pod_tree_workspace_size.restype = SZ
+    lib.pod_tree_workspace_size.argtypes = [V]
+    lib.pod_tree_bind_workspace.restype = ctypes.c_int
+    lib.pod_tree_bind_workspace.argtypes = [V, V, SZ, V]
+    lib.pod_tree_run.restype = ctypes.c_int
+    lib.pod_tree_run.argtypes = [V, V, V, V, V, I64, V, V, V, V, V]
+    lib.pod_tree_read_device_status.restype = ctypes.c_int
+    lib.pod_tree_read_device_status.argtypes = [V, V, V, ctypes.POINTER(I32)]
+    lib.pod_tree_plan_table.restype = ctypes.c_int
+    lib.pod_tree_plan_table.argtypes = [V, I32, V, I64, ctypes.POINTER(I64)]
+    lib.pod_tree_destroy.restype = ctypes.c_int
+    lib.pod_tree_destroy.argtypes = [V]
     if path is None:
         _lib = lib
     return lib
@@ -732,3 +749,152 @@ def pod_gather_kv(kv_cache, slots, *, dtype, kv_scales=None, k_scale=1.0, v_scal
         _check(lib.pod_gather_kv(cache, scales, pages, ps, Hk, d, hnd, fmt, float(k_scale), float(v_scale),
                                  slots.data_ptr(), rows, code, out.data_ptr(), _status(status, dev), st))
     return out
+
+
+# ------------------------------------------------------------------ tree attention
+@dataclass
+class PodTreeHandle:
+    """Owns a tree plan of the C library (released by ``pod_tree_destroy``)."""
+    ptr: int
+    workspace_bytes: int
+    rows: int
+    num_qo_heads: int
+    num_kv_heads: int
+    head_dim: int
+    page_size: int
+    num_pages: int
+    dtype: object
+    kv_format: int
+    kv_layout: int
+    mask_bytes: int
+    has_sinks: bool
+    workspace_ptr: Optional[int] = None
+
+    def __del__(self):
+        if self.ptr and _lib is not None:
+            _lib.pod_tree_destroy(ctypes.c_void_p(self.ptr))
+            self.ptr = 0
+
+
+def pod_tree_plan(q_indptr, kv_indptr, kv_indices, last_page_len, num_qo_heads, num_kv_heads, head_dim, page_size,
+                  *, dtype, num_pages, sm_scale=None, kv_format="16bit", k_scale=1.0, v_scale=1.0, kv_layout="NHD",
+                  has_sinks=False, num_sms=0, workspace=None, stream=None) -> PodTreeHandle:
+    """Plan the attention of drafted token trees: request r's
+    q_indptr[r+1] - q_indptr[r] tokens are the last keys of its pages. Index
+    arrays are host int32. ``kv_format``: "16bit", "scaled" (E4M3, per-tensor
+    k_scale and v_scale) or "block" (E4M3 with exponent bytes). Bind a
+    workspace before running (here, or with pod_tree_bind_workspace)."""
+    lib = load_library()
+    arrs = [_i32(x) for x in (q_indptr, kv_indptr, kv_indices, last_page_len)]
+    if kv_format not in _KV_FORMATS or kv_layout not in _LAYOUTS:
+        raise PodError(1, f"unknown kv_format {kv_format!r} or kv_layout {kv_layout!r}")
+    batch = 0 if arrs[0] is None else len(arrs[0]) - 1
+    if batch > 0:
+        if any(a is None for a in arrs):
+            raise PodError(1, "a page table array is missing")
+        if len(arrs[1]) != batch + 1 or len(arrs[3]) != batch or len(arrs[2]) < int(arrs[1][-1]):
+            raise PodError(1, "the page table arrays do not fit together")
+    handle, req = ctypes.c_void_p(), ctypes.c_size_t(0)
+    ws_ptr = None if workspace is None else workspace.data_ptr()
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    code = lib.pod_tree_plan(*[_ptr(a) for a in arrs], max(batch, 0), int(num_pages), int(num_qo_heads),
+                             int(num_kv_heads), int(head_dim), int(page_size),
+                             float(sm_scale) if sm_scale is not None else 0.0, _dtype_code(dtype),
+                             _KV_FORMATS[kv_format], float(k_scale), float(v_scale), _LAYOUTS[kv_layout],
+                             int(bool(has_sinks)), int(num_sms), ws_ptr, ws_bytes,
+                             _stream(stream) if ws_ptr else None, ctypes.byref(handle), ctypes.byref(req))
+    if code != POD_OK:
+        err = PodError(code, pod_last_error())
+        err.required_workspace_bytes = int(req.value)
+        raise err
+    n = np.diff(arrs[0].astype(np.int64)) if batch > 0 else np.zeros(0, np.int64)
+    return PodTreeHandle(ptr=handle.value, workspace_bytes=int(req.value), rows=int(n.sum()),
+                         num_qo_heads=int(num_qo_heads), num_kv_heads=int(num_kv_heads), head_dim=int(head_dim),
+                         page_size=int(page_size), num_pages=int(num_pages), dtype=dtype,
+                         kv_format=_KV_FORMATS[kv_format], kv_layout=_LAYOUTS[kv_layout],
+                         mask_bytes=int((int((n * n).sum()) + 7) // 8), has_sinks=bool(has_sinks),
+                         workspace_ptr=ws_ptr)
+
+
+def pod_tree_workspace_size(h: PodTreeHandle) -> int:
+    return int(load_library().pod_tree_workspace_size(ctypes.c_void_p(h.ptr)))
+
+
+def pod_tree_bind_workspace(h: PodTreeHandle, workspace, stream=None):
+    with _Launch(_device_of(workspace), stream) as st:
+        _check(load_library().pod_tree_bind_workspace(ctypes.c_void_p(h.ptr), workspace.data_ptr(),
+                                                      workspace.numel() * workspace.element_size(), st))
+    h.workspace_ptr = workspace.data_ptr()
+
+
+def pod_tree_run(h: PodTreeHandle, q, kv, workspace, tree_mask=None, kv_scales=None, sinks=None, out=None, lse=None,
+                 stream=None):
+    """Attention of the planned trees: q [rows, H, d], kv the paged cache,
+    ``tree_mask`` uint8 bits (little bit order) of every request's [n, n]
+    matrix end to end (None: chains). Returns (out, lse), lse in base 2."""
+    import torch
+    lib = load_library()
+    dev = _device_of(q)
+    H, d = h.num_qo_heads, h.head_dim
+    shape = (h.rows, H, d)
+    _on_device("q", q, dev, h.dtype, 3)
+    if tuple(q.shape) != shape:
+        raise PodError(1, f"q must be {shape}")
+    inner = (h.num_kv_heads, h.page_size) if h.kv_layout else (h.page_size, h.num_kv_heads)
+    _on_device("kv", kv, dev, h.dtype if h.kv_format == 0 else torch.float8_e4m3fn, 5)
+    if tuple(kv.shape) != (h.num_pages, 2) + inner + (d,):
+        raise PodError(1, f"kv must be {(h.num_pages, 2) + inner + (d,)}")
+    if kv_scales is not None:
+        _on_device("kv_scales", kv_scales, dev, torch.uint8, 4)
+        if tuple(kv_scales.shape) != (h.num_pages, 2) + inner:
+            raise PodError(1, f"kv_scales must be {(h.num_pages, 2) + inner}")
+    if tree_mask is not None:
+        _on_device("tree_mask", tree_mask, dev, torch.uint8, 1)
+    if sinks is not None:
+        _on_device("sinks", sinks, dev, torch.float32, 1)
+        if sinks.numel() != H:
+            raise PodError(1, f"sinks must have {H} elements")
+    if workspace.device != dev:
+        raise PodError(1, f"the workspace must be on {dev}")
+    if out is None:
+        out = torch.empty(shape, dtype=h.dtype, device=dev)
+    else:
+        _on_device("out", out, dev, h.dtype, 3)
+        if tuple(out.shape) != shape:
+            raise PodError(1, f"out must be {shape}")
+    if lse is None:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+    else:
+        _on_device("lse", lse, dev, torch.float32, 2)
+        if tuple(lse.shape) != shape[:2]:
+            raise PodError(1, f"lse must be {shape[:2]}")
+    with _Launch(dev, stream) as st:
+        _check(lib.pod_tree_run(ctypes.c_void_p(h.ptr), q.data_ptr(), kv.data_ptr(), _ptr(kv_scales), _ptr(tree_mask),
+                                0 if tree_mask is None else tree_mask.numel(), _ptr(sinks), workspace.data_ptr(),
+                                out.data_ptr(), lse.data_ptr(), st))
+    return out, lse
+
+
+def pod_tree_read_device_status(h: PodTreeHandle, workspace, stream=None) -> int:
+    v = ctypes.c_int32(0)
+    with _Launch(_device_of(workspace), stream) as st:
+        code = load_library().pod_tree_read_device_status(ctypes.c_void_p(h.ptr), workspace.data_ptr(), st,
+                                                          ctypes.byref(v))
+    if code not in (POD_OK, 5):
+        _check(code)
+    return int(v.value)
+
+
+def pod_tree_plan_table(h: PodTreeHandle, which: int) -> np.ndarray:
+    lib = load_library()
+    n = ctypes.c_int64(0)
+    _check(lib.pod_tree_plan_table(ctypes.c_void_p(h.ptr), int(which), None, 0, ctypes.byref(n)))
+    out = np.zeros(max(n.value, 1), dtype=np.int32)
+    _check(lib.pod_tree_plan_table(ctypes.c_void_p(h.ptr), int(which), out.ctypes.data, n.value, ctypes.byref(n)))
+    return out[:n.value]
+
+
+def pod_tree_destroy(h: PodTreeHandle):
+    if h.ptr:
+        load_library().pod_tree_destroy(ctypes.c_void_p(h.ptr))
+        h.ptr = 0

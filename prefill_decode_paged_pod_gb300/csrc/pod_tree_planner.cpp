@@ -1,0 +1,214 @@
+// pod_tree_planner.cpp — cuts the tree attention of a batch into CTA work.
+//
+// A unit is one (request, KV head, tile of 128 packed rows) and costs its key
+// blocks plus a fixed price for starting it (query load, pipeline fill,
+// epilogue). The units of one tile index form a plane; a plane is laid out in
+// request and head order and cut at equal cost, through the middle of units
+// where it falls so, so every CTA gets the same work up to one block. Planes
+// are cut alike: for wide trees the CTAs at the same place of two planes read
+// the same keys at the same time, the second time from L2. Cut units are merged
+// by a second kernel.
+#include "pod_tree_planner.hpp"
+
+#include <string.h>
+
+#include <algorithm>
+
+#include "../../include/pod.h"
+#include "pod_tree.h"
+
+namespace {
+
+constexpr int kStart = 3;      // price of starting a segment, in key blocks
+constexpr int kMinCut = 5;     // a CTA's share is at least this many blocks and one start
+
+struct Unit {
+  int req, g, blocks;
+};
+
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Walks one plane with a CTA budget of `share`; calls emit(cta, unit, blk0,
+// blk1) for each segment. Returns the number of CTAs used.
+template <typename F>
+int cut(const std::vector<Unit>& units, int share, F emit) {
+  int cta = 0, used = 0;
+  for (size_t u = 0; u < units.size(); ++u) {
+    int at = 0;
+    while (at < units[u].blocks) {
+      const int left = units[u].blocks - at;
+      int room = share - used - kStart;
+      // too little room to be worth a start: the next CTA begins here
+      if (room < 1 || (room < 3 && room < left && used > 0)) {
+        ++cta;
+        used = 0;
+        room = share - kStart;
+      }
+      const int take = std::min(left, room);
+      emit(cta, (int)u, at, at + take);
+      used += kStart + take;
+      at += take;
+    }
+  }
+  return units.empty() ? 0 : cta + 1;
+}
+
+}  // namespace
+
+int pod_tree_build_plan(const PodTreeArgs& a, PodTreePlanHost& o, std::string* err) {
+  auto bad = [&](int code, const std::string& m) {
+    *err = m;
+    return code;
+  };
+  const int INV = POD_ERR_INVALID_ARG, UNS = POD_ERR_UNSUPPORTED;
+  if (a.batch < 0) return bad(INV, "batch is negative");
+  if (a.H < 1 || a.Hk < 1 || a.H % a.Hk != 0)
+    return bad(INV, "num_qo_heads must be a positive multiple of num_kv_heads");
+  if (a.H > 65536 || a.Hk > 4096) return bad(UNS, "too many heads");
+  if (a.d != 64 && a.d != 128 && a.d != 256) return bad(UNS, "head_dim must be 64, 128 or 256");
+  if (a.ps < 1 || a.ps > (1 << 20)) return bad(INV, "page_size must be in [1, 2^20]");
+  if (a.num_pages < 1 && a.batch > 0) return bad(INV, "the page pool is empty");
+  if (a.num_pages >= (1 << 30)) return bad(INV, "the page pool is too large");
+  if (a.batch > 0 && (!a.q_indptr || !a.kv_indptr || !a.last_page_len))
+    return bad(INV, "a page table array is NULL");
+  o.batch = a.batch; o.num_pages = a.num_pages; o.H = a.H; o.Hk = a.Hk; o.G = a.H / a.Hk;
+  o.d = a.d; o.ps = a.ps;
+
+  std::vector<int> n(a.batch), kv(a.batch);
+  std::vector<long long> bit0(a.batch);
+  if (a.batch > 0 && (a.q_indptr[0] != 0 || a.kv_indptr[0] != 0)) return bad(INV, "an indptr does not start at 0");
+  for (int r = 0; r < a.batch; ++r) {
+    const std::string who = "request " + std::to_string(r) + ": ";
+    const long long nq = (long long)a.q_indptr[r + 1] - a.q_indptr[r];
+    const long long np = (long long)a.kv_indptr[r + 1] - a.kv_indptr[r];
+    if (nq < 0 || np < 0) return bad(INV, who + "an indptr decreases");
+    if (np > 0 && (a.last_page_len[r] < 1 || a.last_page_len[r] > a.ps))
+      return bad(INV, who + "last_page_len is outside [1, page_size]");
+    const long long len = np > 0 ? (np - 1) * a.ps + a.last_page_len[r] : 0;
+    if (len > 0x7fffff00ll) return bad(INV, who + "too many keys");
+    if (nq > len) return bad(INV, who + "the tree's tokens must be in the cache (kv_len >= q_len)");
+    if (nq * o.G > 0x7fffff00ll) return bad(INV, who + "too many query rows");
+    if (np > 0 && !a.kv_indices) return bad(INV, "kv_indices is NULL");
+    for (int p = a.kv_indptr[r]; p < a.kv_indptr[r + 1]; ++p)
+      if (a.kv_indices[p] < 0 || a.kv_indices[p] >= a.num_pages)
+        return bad(INV, who + "a page index is outside the pool");
+    n[r] = (int)nq;
+    kv[r] = (int)len;
+    bit0[r] = o.mask_bits;
+    o.mask_bits += nq * nq;
+  }
+  o.rows = a.batch ? a.q_indptr[a.batch] : 0;
+  if ((long long)o.rows * a.H > (1ll << 40)) return bad(INV, "too many query rows");
+  const int npages = a.batch ? a.kv_indptr[a.batch] : 0;
+  o.pages.assign(a.kv_indices ? a.kv_indices : nullptr, a.kv_indices ? a.kv_indices + npages : nullptr);
+
+  // planes of units, and the smallest equal share that the CTA slots allow
+  int max_mt = 0;
+  for (int r = 0; r < a.batch; ++r)
+    max_mt = std::max(max_mt, (int)(((long long)n[r] * o.G + POD_TREE_TILE - 1) / POD_TREE_TILE));
+  std::vector<std::vector<Unit>> planes(max_mt);
+  long long cost = 0, longest = 0;
+  for (int mt = 0; mt < max_mt; ++mt)
+    for (int r = 0; r < a.batch; ++r) {
+      if ((long long)n[r] * o.G <= (long long)mt * POD_TREE_TILE) continue;
+      const int blocks = (kv[r] + POD_TREE_BLOCK - 1) / POD_TREE_BLOCK;
+      for (int g = 0; g < a.Hk; ++g) planes[mt].push_back({r, g, blocks});
+      cost += (long long)a.Hk * (blocks + kStart);
+      longest = std::max(longest, (long long)blocks);
+    }
+  auto ctas = [&](int share) {
+    long long c = 0;
+    for (auto& p : planes) c += cut(p, share, [](int, int, int, int) {});
+    return c;
+  };
+  int lo = (int)std::min<long long>(std::max<long long>(cost / std::max(1, a.slots), kMinCut + kStart), 1 << 29);
+  int hi = (int)std::min<long long>(cost + kStart + 1, (1ll << 30));
+  hi = std::max(hi, lo);
+  if (ctas(lo) > a.slots) {
+    // more planes than slots are possible: the largest share then runs in waves
+    while (lo + 1 < hi) {
+      const int mid = lo + (hi - lo) / 2;
+      if (ctas(mid) <= a.slots) hi = mid;
+      else lo = mid;
+    }
+    // (a plane is one CTA at least; without a share that fits, take the balanced one)
+    if (ctas(hi) > a.slots) hi = (int)std::min<long long>(std::max<long long>(cost / std::max(1, a.slots), longest + kStart), 1 << 29);
+    lo = hi;
+  }
+  const int share = lo;
+
+  // segments in CTA order; split tiles get partial rows and a merge group
+  struct Seg {
+    int cta, unit, b0, b1;
+  };
+  std::vector<int32_t> rec;
+  o.cta_ptr.assign(1, 0);
+  long long prows = 0, mrows = 0;
+  for (int mt = 0; mt < max_mt; ++mt) {
+    std::vector<Seg> s;
+    cut(planes[mt], share, [&](int c, int u, int b0, int b1) { s.push_back({c, u, b0, b1}); });
+    for (size_t i = 0; i < s.size();) {
+      size_t e = i;
+      while (e < s.size() && s[e].unit == s[i].unit) ++e;
+      const Unit& un = planes[mt][s[i].unit];
+      const int rows = std::min(POD_TREE_TILE, n[un.req] * o.G - mt * POD_TREE_TILE);
+      const bool split = e - i > 1;
+      if (split) {
+        const int32_t g[TG_REC] = {un.g, mt * POD_TREE_TILE, rows, (int32_t)prows, (int32_t)(e - i),
+                                   a.q_indptr[un.req], (int32_t)mrows, 0};
+        o.groups.insert(o.groups.end(), g, g + TG_REC);
+        mrows += rows;
+      }
+      for (size_t j = i; j < e; ++j) {
+        int32_t r[TS_REC] = {};
+        r[TS_G] = un.g;
+        r[TS_ROW0] = mt * POD_TREE_TILE;
+        r[TS_NROWS] = rows;
+        r[TS_BLK0] = s[j].b0;
+        r[TS_BLK1] = s[j].b1;
+        r[TS_PROW] = split ? (int32_t)prows : -1;
+        r[TS_KVLEN] = kv[un.req];
+        r[TS_NTOK] = n[un.req];
+        r[TS_QROW0] = a.q_indptr[un.req];
+        r[TS_PAGE0] = a.kv_indptr[un.req];
+        r[TS_NPAGES] = a.kv_indptr[un.req + 1] - a.kv_indptr[un.req];
+        r[TS_BIT_LO] = (int32_t)(uint32_t)(bit0[un.req] & 0xffffffffll);
+        r[TS_BIT_HI] = (int32_t)(bit0[un.req] >> 32);
+        r[TS_COPIES] = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
+        if (split) prows += rows;
+        rec.insert(rec.end(), r, r + TS_REC);
+        const bool last = j + 1 == s.size() || s[j + 1].cta != s[j].cta;
+        if (last) o.cta_ptr.push_back((int32_t)(rec.size() / TS_REC));
+      }
+      i = e;
+    }
+  }
+  if (prows > 0x7fffffff || mrows > 0x7fffffff) return bad(INV, "too many split rows");
+  o.segs = std::move(rec);
+  o.n_cta = (int)o.cta_ptr.size() - 1;
+  o.n_prows = (int)prows;
+  o.n_mrows = (int)mrows;
+
+  size_t at = TREE_ST_INTS * sizeof(int32_t);
+  auto put = [&](size_t bytes) {
+    const size_t r = up256(at);
+    at = r + bytes;
+    return r;
+  };
+  o.off_segs = put(o.segs.size() * 4);
+  o.off_cta = put(o.cta_ptr.size() * 4);
+  o.off_pages = put(o.pages.size() * 4);
+  o.off_groups = put(o.groups.size() * 4);
+  o.image.assign(up256(at), 0);
+  auto copy = [&](size_t off, const std::vector<int32_t>& v) {
+    if (!v.empty()) memcpy(o.image.data() + off, v.data(), v.size() * 4);
+  };
+  copy(o.off_segs, o.segs);
+  copy(o.off_cta, o.cta_ptr);
+  copy(o.off_pages, o.pages);
+  copy(o.off_groups, o.groups);
+  o.off_part_o = put((size_t)o.n_prows * a.d * 4);
+  o.off_part_lse = put((size_t)o.n_prows * 4);
+  o.total = up256(at);
+  return POD_OK;
+}
