@@ -141,6 +141,12 @@ POD_DEV bool softmax_vote(bool ok) {
   return all != 0;
 }
 
+// one lane of the converged warp, always the same
+POD_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
 POD_DEV uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -516,7 +522,8 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
   extern __shared__ __align__(1024) uint8_t smem[];
   // the merge kernel may be scheduled now; it waits for this grid's completion
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (uniform, and known to be)
   const uint32_t sbase = smem_u32(smem), bar0 = sbase + L::BAR_OFF;
   static_assert(TB_COUNT * 8 <= 176, "barriers overlap the TMEM slot");
   if ((sbase & 1023u) != 0u) {                       // 128B-swizzle atoms need 1024-byte alignment
@@ -570,72 +577,85 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
   } else if (warp == 4) {
     // ---------------------------------------------------------- MMA issuer
     // Per segment: QK_0, [QK_1, PV_0], ..., PV_{nb-1}. QK_{j+2} reuses the
-    // columns of S_j / P_j; MMAs issued by one thread run in order.
-    if (lane == 0) {
-      const uint32_t id_qk = idesc_f16(Pack<E>::kBF16, 128, BK, false, false);
-      const uint32_t id_pv = idesc_f16(Pack<E>::kBF16, 128, D, false, true);
-      // V stage: 16-key steps inside a box of vb keys ([box][64-column part][key])
-      const int vb = KV == 0 && tma ? P.kbx : BK;
-      const uint32_t v_lbo = (uint32_t)vb * 128u, v_sbo = vb >= 16 ? 1024u : (uint32_t)L::NKB * 1024u;
-      int kuse = 0, vuse = 0, sc0 = 0;
-      for (int i = seg0; i < seg1 && ok; ++i) {
-        const int32_t* seg = P.segs + (size_t)i * TS_REC;
-        const int blk0 = seg[TS_BLK0], nb = seg[TS_BLK1] - blk0, kv_len = seg[TS_KVLEN];
-        if (!mbar_wait(BAR(TB_QFULL), (i - seg0) & 1, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        for (int j = 0; j <= nb; ++j) {
-          if (j < nb) {
-            const int s = kuse % L::NK;
-            if (!mbar_wait(BAR(TB_KFULL + s), (kuse / L::NK) & 1, abort_flag)) { ok = false; break; }
-            tc_fence_after();
-            if (KV == 0 && !tma) fence_proxy_async();
-            const int b = (sc0 + j) & 1;
-            const uint32_t qa = sbase + L::Q_OFF, ka = sbase + L::K_OFF + s * L::STAGE;
+    // columns of S_j / P_j; MMAs issued by one thread run in order. The whole
+    // warp walks the loop and one elected lane issues: addresses and
+    // descriptors then stay in uniform registers (a loop under `lane == 0`
+    // moved each of them there for every MMA: 85 clocks an instruction).
+    const uint32_t id_qk = idesc_f16(Pack<E>::kBF16, 128, BK, false, false);
+    const uint32_t id_pv = idesc_f16(Pack<E>::kBF16, 128, D, false, true);
+    // V stage: 16-key steps inside a box of vb keys ([box][64-column part][key])
+    const int vb = KV == 0 && tma ? P.kbx : BK;
+    const uint32_t v_box = (uint32_t)(vb * L::NKB * 128);
+    const uint64_t v_desc0 = sdesc_sw128(sbase + L::V_OFF, (uint32_t)vb * 128u,
+                                         vb >= 16 ? 1024u : (uint32_t)L::NKB * 1024u);
+    uint32_t v_step[BK / 16];
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint64_t ad = sdesc_sw128(qa + (k >> 2) * L::QBLK + (k & 3) * 32, 16, 1024);
-              const uint64_t bd = sdesc_sw128(ka + (k >> 2) * L::KVBLK + (k & 3) * 32, 16, 1024);
-              mma_f16_ss(tmem + L::TM_S + b * BK, ad, bd, id_qk, k > 0 ? 1u : 0u);
-            }
+    for (int k = 0; k < BK / 16; ++k) v_step[k] = (uint32_t)(k * 16 / vb) * v_box + (uint32_t)(k * 16 % vb) * 128u;
+    const uint64_t q_desc0 = sdesc_sw128(sbase + L::Q_OFF, 16, 1024);
+    const uint64_t k_desc0 = sdesc_sw128(sbase + L::K_OFF, 16, 1024);
+    int ks = 0, vs = 0;                              // ring positions, and their phases
+    uint32_t kph = 0, vph = 0;
+    int sc0 = 0;
+    for (int i = seg0; i < seg1 && ok; ++i) {
+      const int32_t* seg = P.segs + (size_t)i * TS_REC;
+      const int blk0 = seg[TS_BLK0], nb = seg[TS_BLK1] - blk0, kv_len = seg[TS_KVLEN];
+      if (!tree_wait(BAR(TB_QFULL), (i - seg0) & 1, abort_flag)) { ok = false; break; }
+      tc_fence_after();
+      for (int j = 0; j <= nb; ++j) {
+        if (j < nb) {
+          if (!tree_wait(BAR(TB_KFULL + ks), kph, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          if (KV == 0 && !tma) fence_proxy_async();
+          const int b = (sc0 + j) & 1;
+          const uint32_t d_s = tmem + L::TM_S + b * BK;
+          const uint64_t kd = k_desc0 + (uint32_t)(ks * L::STAGE >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_f16_ss(d_s, q_desc0 + (((k >> 2) * L::QBLK + (k & 3) * 32) >> 4),
+                         kd + (((k >> 2) * L::KVBLK + (k & 3) * 32) >> 4), id_qk, k > 0 ? 1u : 0u);
             mma_commit(BAR(TB_SFULL + b));
-            mma_commit(BAR(TB_KEMPTY + s));
-            ++kuse;
+            mma_commit(BAR(TB_KEMPTY + ks));
           }
-          if (j > 0) {
-            const int sc = sc0 + j - 1, b = sc & 1, s = vuse % L::NV;
-            if (!mbar_wait(BAR(TB_VFULL + s), (vuse / L::NV) & 1, abort_flag)) { ok = false; break; }
-            if (!mbar_wait(BAR(TB_PFULL + b), (sc >> 1) & 1, abort_flag)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t va = sbase + L::V_OFF + s * L::STAGE;
-            // 16-key steps past kv_len carry P = 0: skip them. Rows at or past
-            // kv_len in the last step are unused slots of the last page, or
-            // nothing: zero them, so that P = 0 never meets a non-finite value.
-            const int kb = (blk0 + j - 1) * BK;
-            const int keys = min(kv_len - kb, BK), ksteps = (keys + 15) >> 4;
-            auto row_at = [&](int r) { return (uint32_t)(r / vb * vb * L::NKB * 128); };
-            bool fence = KV == 0 && !tma;
-            if (KV == 0 && (keys & 15)) {
-              for (int r = keys; r < ksteps * 16; ++r)
-                for (int h = 0; h < L::NKB; ++h)
-                  for (int c = 0; c < 8; ++c)
-                    sts128(va + row_at(r) + h * vb * 128 + sw128_off(r % vb, c), make_uint4(0, 0, 0, 0));
-              fence = true;
-            }
-            if (fence) fence_proxy_async();
-            for (int k = 0; k < ksteps; ++k) {
-              const uint64_t bd = sdesc_sw128(va + row_at(k * 16) + (k * 16 % vb) * 128, v_lbo, v_sbo);
-              mma_f16_ts(tmem + L::TM_O, tmem + L::TM_S + b * BK + k * 8, bd, id_pv,
-                         (j > 1 || k > 0) ? 1u : 0u);
-            }
-            mma_commit(BAR(TB_PVDONE + b));
-            mma_commit(BAR(TB_VEMPTY + s));
-            ++vuse;
-          }
+          __syncwarp();
+          if (++ks == L::NK) { ks = 0; kph ^= 1; }
         }
-        sc0 += nb;
+        if (j > 0) {
+          const int sc = sc0 + j - 1, b = sc & 1;
+          if (!tree_wait(BAR(TB_VFULL + vs), vph, abort_flag)) { ok = false; break; }
+          if (!tree_wait(BAR(TB_PFULL + b), (sc >> 1) & 1, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          // 16-key steps past kv_len carry P = 0: skip them. Rows at or past
+          // kv_len in the last step are unused slots of the last page, or
+          // nothing: zero them, so that P = 0 never meets a non-finite value.
+          const int keys = min(kv_len - (blk0 + j - 1) * BK, BK), ksteps = (keys + 15) >> 4;
+          if (KV == 0 && (keys & 15)) {
+            const uint32_t va = sbase + L::V_OFF + vs * L::STAGE;
+            for (int x = lane; x < (ksteps * 16 - keys) * L::NKB * 8; x += 32) {
+              const int r = keys + x / (L::NKB * 8), h = x / 8 % L::NKB, c = x % 8;
+              sts128(va + (uint32_t)(r / vb) * v_box + h * vb * 128 + sw128_off(r % vb, c), make_uint4(0, 0, 0, 0));
+            }
+            fence_proxy_async();
+            __syncwarp();
+          } else if (KV == 0 && !tma) {
+            fence_proxy_async();
+          }
+          const uint64_t vd = v_desc0 + (uint32_t)(vs * L::STAGE >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < BK / 16; ++k)
+              if (k < ksteps)
+                mma_f16_ts(tmem + L::TM_O, tmem + L::TM_S + b * BK + k * 8, vd + (v_step[k] >> 4), id_pv,
+                           (j > 1 || k > 0) ? 1u : 0u);
+            mma_commit(BAR(TB_PVDONE + b));
+            mma_commit(BAR(TB_VEMPTY + vs));
+          }
+          __syncwarp();
+          if (++vs == L::NV) { vs = 0; vph ^= 1; }
+        }
       }
+      sc0 += nb;
     }
-    ok = __all_sync(0xffffffffu, ok);
   } else if (KV == 0 && tma) {
     // ---------------------------------------------------------- K and V boxes
     if (warp < 7) {
@@ -832,7 +852,7 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
   tc_fence_before();
   __syncthreads();
   if (warp == 4) {
-    if (lane == 0) mma_commit(BAR(TB_FINAL));
+    if (elect_one()) mma_commit(BAR(TB_FINAL));
     __syncwarp();
     mbar_wait(BAR(TB_FINAL), 0, &never);
     tc_fence_after();
