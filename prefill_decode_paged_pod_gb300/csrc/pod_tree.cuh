@@ -10,14 +10,13 @@
 // loaded serves them all. Warp roles of a CTA (256 threads, two CTAs per SM,
 // one at head_dim 256):
 //   warps 0-3  one TMEM lane (row) per thread: Q into shared memory, then per
-//              64-key block tcgen05.ld of S, mask, softmax, P back into TMEM;
+//              key block tcgen05.ld of S, mask, softmax, P back into TMEM;
 //              final output or fp32 partial;
-//   warp 4     one thread issues tcgen05.mma: S = Q K^T (two S buffers), then
-//              O += P V with P read from TMEM;
-//   warp 5     K (FP8: K and V codes) as TMA boxes through the page table;
-//   warp 6     V boxes (16-bit); FP8: warps 6 and 7 widen the codes to fp16.
-//   Page sizes that are not a power of two of at least 8 are gathered with
-//   cp.async by the loader warps.
+//   warp 4     one lane issues tcgen05.mma: S = Q K^T, then O += P V with P read
+//              from TMEM;
+//   warp 5, 6  K and V as TMA boxes through the page table; page sizes that are
+//              not a power of two of at least 8 are gathered by warps 5-7 with
+//              cp.async.
 //
 // Few rows: a tile of at most 32 (64) rows is held 4 (2) times in the 128
 // lanes, and copy c works on its own quarter (half) of every block's keys, with
@@ -25,13 +24,20 @@
 // would cost 128 rows whatever their number, a quarter (half) of it; the copies
 // are joined at the end like split key ranges.
 //
-// FP8 caches: E4M3 codes are exact in fp16, so both products run in fp16
-// (P with 11 significant bits). A query row is scaled by the power of two that
-// brings its largest value to [2^13, 2^14): exact down to 2^-27 of that value.
-// Per-tensor scales are constants of the softmax and of the output. Block
-// scales are powers of two per key: K's multiplies the key's column of S, V's
-// the column of P relative to the largest V scale met so far (O is rescaled
-// when that one grows, as for the running maximum).
+// FP8 caches go into the products as they are (kind::f8f6f4, E4M3 operands),
+// with 128 keys a block. A query row is scaled by the power of two that brings
+// its largest value to [128, 256) and split into E4M3 parts, two for bf16 rows
+// (4 + 4 significant bits, all it has), three for fp16 rows (11 bits); parts
+// below 2^-17 of the row's largest value lose bits. P (the largest
+// between 2^6 and 2^8.5) is carried in two E4M3 parts by Veltkamp splitting: 4
+// bits, then the remainder to 4 bits, at most 2^-9 of p off, and 2^-15 of the
+// largest weight at the bottom. (An
+// earlier form widened the codes to fp16 in shared memory; the two warps that
+// did it set the pace: 620 us for 96 requests of 8192 keys.) Per-tensor scales
+// are constants of the softmax and of the output. Block scales are powers of
+// two per key: K's multiplies the key's column of S, V's the column of P
+// relative to the largest V scale met so far (O is rescaled when that one
+// grows, as for the running maximum).
 #pragma once
 #include <cuda_runtime.h>
 #include <math.h>
@@ -48,38 +54,63 @@ using namespace pod;
 namespace {
 
 constexpr int kTreeThreads = 256;
-constexpr int BK = POD_TREE_BLOCK;
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int D, int KV>
+template <typename T, int D, int KV>
 struct TLayout {
-  static constexpr int NKB = D / 64;
-  static constexpr int QBLK = POD_TREE_TILE * 128;   // 128 rows x 64 elements
-  static constexpr int KVBLK = BK * 128;             // 64 keys x 64 elements
-  static constexpr int STAGE = NKB * KVBLK;          // one block of K or V, 16-bit
-  static constexpr int NK = KV == 0 ? 3 : 2, NV = KV == 0 ? 2 : 1;
-  static constexpr int RAW = BK * D;                 // one block of K or V codes
-  static constexpr int NR = KV == 0 ? 0 : 2;         // raw ring (K and V codes)
+  static constexpr bool F8 = KV != 0;
+  static constexpr int BK = F8 ? POD_TREE_BLOCK8 : POD_TREE_BLOCK;   // keys per block
+  static constexpr int ES = F8 ? 1 : 2;                // operand bytes
+  static constexpr int ROWB = D * ES < 128 ? D * ES : 128;   // bytes of a row part
+  static constexpr int PARTS = D * ES / ROWB;          // row parts
+  static constexpr int PEL = ROWB / ES;                // elements of a row part
+  static constexpr int QP = !F8 ? 1 : Pack<T>::kBF16 ? 2 : 3;   // precision parts of Q
+  static constexpr int QPART = POD_TREE_TILE * ROWB;   // one row part of one precision part
+  static constexpr int KVPART = BK * ROWB;             // one row part of a block of K or V
+  static constexpr int STAGE = PARTS * KVPART;
+  static constexpr int NK = F8 ? 2 : 3, NV = 2;
   static constexpr int Q_OFF = 0;
-  static constexpr int K_OFF = NKB * QBLK;
+  static constexpr int Q_BYTES = QP * PARTS * QPART;
+  static constexpr int K_OFF = Q_BYTES;
   static constexpr int V_OFF = K_OFF + NK * STAGE;
-  static constexpr int R_OFF = V_OFF + NV * STAGE;
-  static constexpr int BAR_OFF = R_OFF + NR * 2 * RAW;
-  // BAR_OFF + 0: barriers, +176: TMEM address, +180: abort flag, +192: block
-  // factors of two blocks (K as floats, V as halves)
+  static constexpr int BAR_OFF = V_OFF + NV * STAGE;
+  // BAR_OFF + 0: barriers, +152: TMEM address, +156: abort flag, +160: the
+  // warps' largest V exponents of two blocks, +192: the block's factors (K,
+  // then V)
+  static constexpr int WM_OFF = BAR_OFF + 160;
   static constexpr int FAC_OFF = BAR_OFF + 192;
-  static constexpr int FAC_K = BK * 4, FAC_V = BK * 2;
-  static constexpr int END = FAC_OFF + (KV == 2 ? 2 * (FAC_K + FAC_V) : 0);
+  // (floats; bf16 beside the three Q parts of fp16 rows of 128 elements, which
+  // leave no room for more)
+  static constexpr int FACB = QP == 3 && D == 128 ? 2 : 4;
+  static constexpr int END = FAC_OFF + (KV == 2 ? 2 * BK * FACB : 0);
   // The copies' join holds 32 output columns of the 128 lanes (16 KB) in the Q
-  // region, and m and l of the lanes behind them (at head_dim 64 Q has no room
-  // for these).
+  // region, and m and l of the lanes behind them, or at the end where Q has no
+  // room for these.
   static constexpr int JOIN = 32;
-  static constexpr int JOIN_BYTES = POD_TREE_TILE * JOIN * 4;
-  static constexpr int ML_OFF = NKB > 1 ? Q_OFF + JOIN_BYTES : END;
-  static constexpr int TOTAL = NKB > 1 ? END : END + POD_TREE_TILE * 8;
-  static constexpr int TM_S = 0, TM_O = 2 * BK;
+  static constexpr int JOIN_BYTES = POD_TREE_TILE * JOIN * 4, ML_BYTES = POD_TREE_TILE * 8;
+  static constexpr bool ML_IN_Q = Q_BYTES >= JOIN_BYTES + ML_BYTES;
+  static constexpr int ML_OFF = ML_IN_Q ? Q_OFF + JOIN_BYTES : END;
+  static constexpr int TOTAL = ML_IN_Q ? END : END + ML_BYTES;
+  static_assert(JOIN_BYTES <= Q_BYTES, "the join must fit the Q region");
+  // TMEM: S buffers, then O. Two buffers let Q K^T of the next block run beside
+  // the softmax of this one; FP8 blocks of 128 keys leave room for one where
+  // two CTAs share the SM (these overlap each other).
+  static constexpr int NSB = F8 && D <= 128 ? 1 : 2;
+  static constexpr int TM_S = 0, TM_O = NSB * BK;
   static constexpr int TMEM_COLS = TM_O + D <= 256 ? 256 : 512;
-  static_assert(JOIN_BYTES <= NKB * QBLK, "the join must fit the Q region");
+  static_assert(TM_O + D <= 512 && (D > 128 || TMEM_COLS == 256), "TMEM columns");
+  // MMA steps: 32 bytes of a K-major row, KSTEP keys of V
+  static constexpr int DSTEPS = D * ES / 32, KSTEP = 32 / ES, KSTEPS = BK / KSTEP;
+  // P = 2^(x - m): the reference m is set so that the largest P is 2^TOP, and
+  // moves (O is rescaled) when one would pass 2^LIMIT. E4M3 ends at 448; TOP well
+  // below it spares most of the rescaling (at TOP = 7 every other block of 128
+  // random keys had a row that needed it).
+  static constexpr float TOP = F8 ? 6.f : 0.f, LIMIT = F8 ? 8.5f : 8.f;
+
+  static POD_DEV uint32_t swz(int r, int c) { return ROWB == 128 ? sw128_off(r, c) : sw64_off(r, c); }
+  static POD_DEV uint64_t desc(uint32_t a, uint32_t lbo, uint32_t sbo) {
+    return ROWB == 128 ? sdesc_sw128(a, lbo, sbo) : sdesc_sw64(a, lbo, sbo);
+  }
 };
 
 enum {
@@ -91,10 +122,8 @@ enum {
   TB_SFULL = 11,   // [2]
   TB_PFULL = 13,   // [2]
   TB_PVDONE = 15,  // [2]
-  TB_RFULL = 17,   // [2]
-  TB_REMPTY = 19,  // [2]
-  TB_FINAL = 21,
-  TB_COUNT = 22
+  TB_FINAL = 17,
+  TB_COUNT = 18
 };
 
 // W (16, 32 or 64) consecutive TMEM columns of the warp's 32 lanes
@@ -121,7 +150,6 @@ POD_DEV void tmem_st8(uint32_t a, const uint32_t* u) {
                "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
                : "memory");
 }
-
 POD_DEV bool tree_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
 }
@@ -157,47 +185,86 @@ POD_DEV void sts128(uint32_t a, const uint4& v) {
                : "memory");
 }
 POD_DEV void stsf(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
-
-POD_DEV void sts_half(uint32_t a, float v) {
-  asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(__half_as_ushort(__float2half_rn(v))) : "memory");
+POD_DEV void sts16(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"((unsigned short)v) : "memory");
 }
-POD_DEV uint32_t hmul2_u32(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
+// bf16 of a power of two (exact, subnormals too): its upper 16 bits
+POD_DEV uint32_t pow2_bf16(float v) { return __float_as_uint(v) >> 16; }
+
+// Four values below 448 (two pairs) as E4M3 words hi + lo (byte i: value i).
+// Veltkamp splitting: hi is x to 4 significant bits, lo the remainder to 4 bits.
+POD_DEV void e4m3_split4(uint64_t x01, uint64_t x23, uint32_t& hi, uint32_t& lo) {
+  const uint64_t c = pack2(1048577.f, 1048577.f), neg = pack2(-1.f, -1.f);   // 2^20 + 1
+  const uint64_t x[2] = {x01, x23};
+  uint32_t h[2], l[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t t = mul2(x[i], c);
+    const uint64_t v = add2(t, fma2(t, neg, x[i]));  // (products with -1 are exact)
+    const uint64_t r = fma2(v, neg, x[i]);
+    float a, b;
+    unpack2(v, a, b);
+    h[i] = f32x2_to_e4m3x2(a, b);
+    unpack2(r, a, b);
+    l[i] = f32x2_to_e4m3x2(a, b);
+  }
+  hi = h[0] | (h[1] << 16);
+  lo = l[0] | (l[1] << 16);
 }
 
 // exponent byte -> 2^(byte - 127), and 2^(byte - ref) for byte <= ref
 POD_DEV float exp_byte(int b) { return b == 0 ? 5.877471754111438e-39f : __uint_as_float((uint32_t)b << 23); }
 POD_DEV float exp_below(int b, int ref) { return __uint_as_float((uint32_t)max(127 - (ref - b), 0) << 23); }
 
-// Page-table view of one segment: the cache row of key t.
+// Factors of keys key .. key + 3, as two pairs.
+template <int FACB>
+POD_DEV void factors4(uint32_t base, int key, uint64_t* f) {
+  if constexpr (FACB == 4) {
+    const uint4 v = lds128(base + 4 * key);
+    f[0] = pack2(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = pack2(__uint_as_float(v.z), __uint_as_float(v.w));
+  } else {
+    const uint2 v = ld_shared_v2(base + 2 * key);
+    f[0] = pack2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u));
+    f[1] = pack2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+  }
+}
+
+// Page-table view of one segment: the cache row (in rows of D elements, K) of
+// key t and KV head g.
 struct KeyAt {
   const int32_t* pages;
-  int npages, ps, shift;
-  POD_DEV int page(int t) const {
+  int npages, ps, shift, hk, hnd, g;
+  POD_DEV long long row(int t) const {
     const int i = shift >= 0 ? t >> shift : t / ps;
-    return __ldg(pages + (i < npages ? i : npages - 1));
+    const int slot = shift >= 0 ? t & (ps - 1) : t - i * ps;
+    const long long page = __ldg(pages + (i < npages ? i : npages - 1));
+    return page * 2 * ps * hk + (hnd ? (long long)g * ps + slot : (long long)slot * hk + g);
   }
-  POD_DEV int slot(int t) const { return shift >= 0 ? t & (ps - 1) : t % ps; }
 };
+POD_DEV KeyAt key_at(const PodTreeParams& P, const int32_t* seg) {
+  return KeyAt{P.pages + seg[TS_PAGE0], seg[TS_NPAGES], P.ps, P.ps_shift, P.Hk, P.hnd, seg[TS_G]};
+}
 
 // ============================================================ softmax warps
 // One segment for tiles held C times. Returns false when a wait ran out.
-template <typename T, typename E, int D, int KV, int C>
+template <typename T, int D, int KV, int C>
 __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tmem, const int32_t* seg,
                              int& sc0, volatile int* abort_flag) {
-  using L = TLayout<D, KV>;
-  constexpr int RB = 128 / C, W = BK / C;           // rows and columns of a copy
+  using L = TLayout<T, D, KV>;
+  constexpr int BK = L::BK, NSB = L::NSB;
+  constexpr int RB = 128 / C;                        // rows of a copy
+  constexpr int TW = BK / C;                         // its keys in a block,
+  constexpr int W = TW < 64 ? TW : 64, NH = TW / W;  // in NH runs of W columns
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sbase = smem_u32(smem), bar0 = sbase + L::BAR_OFF;
   auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-  const int cp = tid / RB, rr = tid % RB;           // copy (uniform per warp) and row of the tile
+  const int cp = tid / RB, rr = tid % RB;            // copy (uniform per warp) and row of the tile
   const int nrows = seg[TS_NROWS], kv_len = seg[TS_KVLEN], ntok = seg[TS_NTOK];
   const int blk0 = seg[TS_BLK0], nb = seg[TS_BLK1] - blk0;
   const int prow = seg[TS_PROW];
-  const int G = P.G, H = P.H, D8 = D / 8;
+  const int G = P.G, H = P.H;
   const bool valid = rr < nrows;
   const int packed = seg[TS_ROW0] + (valid ? rr : 0);
   const int tok = packed / G, head = seg[TS_G] * G + packed % G;
@@ -208,11 +275,17 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
   float qscale = P.scale_log2;
   {
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(P.q) + grow * D);
-    float up = 1.f;
-    if constexpr (KV != 0) {
+    if constexpr (!L::F8) {
+#pragma unroll 4
+      for (int c = 0; c < D / 8; ++c) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (valid) v = __ldg(src + c);
+        sts128(sbase + L::Q_OFF + (c >> 3) * L::QPART + L::swz(tid, c & 7), v);
+      }
+    } else {
       float amax = 0.f;
 #pragma unroll 4
-      for (int c = 0; c < D8; ++c) {
+      for (int c = 0; c < D / 8; ++c) {
         const uint4 v = __ldg(src + c);
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -221,27 +294,41 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
           amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
         }
       }
-      // 2^e with amax * 2^e in [2^13, 2^14), the factor kept a normal float
-      const int ex = (int)(__float_as_uint(amax) >> 23);      // biased exponent
-      int e = 13 - (ex - 127);
+      // 2^e with amax * 2^e in [128, 256), both factors normal floats
+      int e = 7 - ((int)(__float_as_uint(amax) >> 23) - 127);
       e = amax > 0.f ? min(max(e, -126), 126) : 0;
-      up = __uint_as_float((uint32_t)(127 + e) << 23);
+      const float up = valid ? __uint_as_float((uint32_t)(127 + e) << 23) : 0.f;
       qscale *= __uint_as_float((uint32_t)(127 - e) << 23);
-    }
-#pragma unroll 4
-    for (int c = 0; c < D8; ++c) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (valid) v = __ldg(src + c);
-      if constexpr (KV != 0) {
-        uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll 2
+      for (int c = 0; c < D / 16; ++c) {             // 16 elements: one 16-byte chunk of each part
+        float x[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = Pack<T>::unpack(u[i]);
-          u[i] = Pack<__half>::two(f.x * up, f.y * up);
+        for (int h = 0; h < 2; ++h) {
+          const uint4 v = __ldg(src + 2 * c + h);
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = Pack<T>::unpack(u[i]);
+            x[8 * h + 2 * i] = f.x * up;
+            x[8 * h + 2 * i + 1] = f.y * up;
+          }
         }
-        v = make_uint4(u[0], u[1], u[2], u[3]);
+        const int part = c / (L::ROWB / 16), cc = c % (L::ROWB / 16);
+#pragma unroll
+        for (int p = 0; p < L::QP; ++p) {            // part p: what parts 0..p-1 left, to E4M3
+          uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t code = f32x2_to_e4m3x2(x[2 * i], x[2 * i + 1]);
+            w[i >> 1] |= code << (16 * (i & 1));
+            const float2 f = Pack<__half>::unpack(e4m3x2_to<__half>((uint16_t)code));
+            x[2 * i] -= f.x;
+            x[2 * i + 1] -= f.y;
+          }
+          sts128(sbase + L::Q_OFF + (p * L::PARTS + part) * L::QPART + L::swz(tid, cc),
+                 make_uint4(w[0], w[1], w[2], w[3]));
+        }
       }
-      sts128(sbase + L::Q_OFF + (c >> 3) * L::QBLK + sw128_off(tid, c & 7), v);
     }
     fence_proxy_async();
     mbar_arrive(BAR(TB_QFULL));
@@ -249,23 +336,15 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
 
   const long long bit0 = ((long long)seg[TS_BIT_HI] << 32) | (uint32_t)seg[TS_BIT_LO];
   const int ctx = kv_len - ntok;
-  KeyAt at{P.pages + seg[TS_PAGE0], seg[TS_NPAGES], P.ps, P.ps_shift};
-  const uint32_t kfac0 = sbase + L::FAC_OFF, vfac0 = kfac0 + 2 * L::FAC_K;
-  // block scales: this lane's exponent bytes of the next block (keys lane and
-  // lane + 32; keys past the last read the last)
-  int kb0 = 0, kb1 = 0, vb0 = 0, vb1 = 0, vref = 0;
+  // block scales: the exponent bytes of this thread's key (tid) of the next
+  // block; keys past the last read the last
+  const uint32_t kfac = sbase + L::FAC_OFF, vfac = kfac + BK * L::FACB;
+  int kbyte = 0, vbyte = 0, vref = 0;
+  const KeyAt at = key_at(P, seg);
   auto load_bytes = [&](int blk) {
-    const int t0 = min(blk * BK + lane, kv_len - 1), t1 = min(blk * BK + 32 + lane, kv_len - 1);
-    const size_t vstep = (size_t)P.ps * P.Hk;
-    auto off = [&](int t) {
-      const size_t p = (size_t)at.page(t) * 2 * vstep;
-      return p + (P.hnd ? (size_t)seg[TS_G] * P.ps + at.slot(t) : (size_t)at.slot(t) * P.Hk + seg[TS_G]);
-    };
-    const size_t o0 = off(t0), o1 = off(t1);
-    kb0 = __ldg(P.scales + o0);
-    kb1 = __ldg(P.scales + o1);
-    vb0 = __ldg(P.scales + o0 + vstep);
-    vb1 = __ldg(P.scales + o1 + vstep);
+    const long long r = at.row(min(blk * BK + tid, kv_len - 1));
+    kbyte = __ldg(P.scales + r);
+    vbyte = __ldg(P.scales + r + (long long)P.ps * P.Hk);
   };
   if constexpr (KV == 2) load_bytes(blk0);
 
@@ -274,98 +353,149 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
   bool ok = true;
   for (int j = 0; j < nb; ++j) {
     const int kb = (blk0 + j) * BK;
-    const int sc = sc0 + j, b = sc & 1;
+    const int sc = sc0 + j, b = sc % NSB;
     float o_scale = 1.f;
     if constexpr (KV == 2) {
-      const int top = __reduce_max_sync(0xffffffffu, max(vb0, vb1));
+      // The warps meet twice a block: at the first meeting all of them have read
+      // the last block's factors and written their largest V exponent, at the
+      // second the factors are there.
+      volatile int* wm = reinterpret_cast<volatile int*>(smem + L::WM_OFF) + 4 * (j & 1);
+      const int top_w = __reduce_max_sync(0xffffffffu, vbyte);
+      if (lane == 0) wm[warp] = top_w;
+      if (!softmax_vote(ok)) return false;
+      const int top = max(max(wm[0], wm[1]), max(wm[2], wm[3]));
       if (top > vref) {                              // O is kept in units of 2^(vref - 127)
         o_scale = exp_below(vref, top);
         vref = top;
       }
-      // warps 0 and 1 write the keys' factors. The warps meet once a block:
-      // the factors of block j + 2 are written after the meeting of j + 1, which
-      // every warp reaches after its reads of block j.
-      if (warp < 2) {
-        const int key = warp * 32 + lane, eb = warp ? kb1 : kb0, ev = warp ? vb1 : vb0;
-        stsf(kfac0 + (j & 1) * L::FAC_K + 4 * key, exp_byte(eb));
-        sts_half(vfac0 + (j & 1) * L::FAC_V + 2 * key, exp_below(ev, vref));
+      if constexpr (L::FACB == 4) {
+        stsf(kfac + 4 * tid, exp_byte(kbyte));
+        stsf(vfac + 4 * tid, exp_below(vbyte, vref));
+      } else {
+        sts16(kfac + 2 * tid, pow2_bf16(exp_byte(kbyte)));
+        sts16(vfac + 2 * tid, pow2_bf16(exp_below(vbyte, vref)));
       }
-      if (!softmax_vote(ok)) return false;
       if (j + 1 < nb) load_bytes(blk0 + j + 1);
+      softmax_sync();
     }
-    if (!tree_wait(BAR(TB_SFULL + b), (sc >> 1) & 1, abort_flag)) {
+    if (!tree_wait(BAR(TB_SFULL + b), (sc / NSB) & 1, abort_flag)) {
       ok = false;
       if (KV == 2) continue;
       break;
     }
     tc_fence_after();
     const uint32_t s_addr = tmem + lane_base + L::TM_S + b * BK;
+    const int my0 = cp * TW;                         // this copy's first column
+    // S of run h: raw products with the keys' factors, hidden keys at -inf
+    auto load_s = [&](int h, float* s) {
+      const int col = my0 + h * W;
+      tmem_ldw<W>(s_addr + col, s);
+      if constexpr (KV == 2) {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) {
+          uint64_t f[2];
+          factors4<L::FACB>(kfac, col + i, f);
+          unpack2(mul2(pack2(s[i], s[i + 1]), f[0]), s[i], s[i + 1]);
+          unpack2(mul2(pack2(s[i + 2], s[i + 3]), f[1]), s[i + 2], s[i + 3]);
+        }
+      }
+      const int c0 = kb + col;                       // first key of the run
+      if (c0 + W > ctx) {
+        // keys of the tree, or past the last: bit i says whether key c0 + i is seen
+        uint64_t see = 0;
+        const int skip = max(ctx - c0, 0);           // context keys at the front
+        const int j0 = c0 + skip - ctx;              // first tree key of the run
+        if (j0 < ntok) {
+          see = P.mask ? load_bits64(P.mask, P.mask_bytes, bit0 + (long long)tok * ntok + j0)
+                       : (tok - j0 >= 63 ? ~0ull : tok < j0 ? 0ull : (2ull << (tok - j0)) - 1ull);
+          const int left = ntok - j0;
+          if (left < 64) see &= (1ull << left) - 1ull;
+        }
+        if (skip) see = skip < 64 ? (see << skip) | ((1ull << skip) - 1ull) : ~0ull;
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+          if (!((see >> i) & 1ull)) s[i] = NEG_INF;
+      }
+    };
+    auto max_s = [&](const float* s) {
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int i = 4; i < W; i += 8) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          mx[u] = i + 4 + u < W ? max3(mx[u], s[i + u], s[i + 4 + u]) : fmaxf(mx[u], s[i + u]);
+      }
+      return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+    };
     float s[W];
-    tmem_ldw<W>(s_addr + cp * W, s);
-    if constexpr (KV == 2) {
+    float bmax = NEG_INF;
 #pragma unroll
-      for (int i = 0; i < W; i += 4) {
-        const uint4 f = lds128(kfac0 + (j & 1) * L::FAC_K + 4 * (cp * W + i));
-        s[i] *= __uint_as_float(f.x);
-        s[i + 1] *= __uint_as_float(f.y);
-        s[i + 2] *= __uint_as_float(f.z);
-        s[i + 3] *= __uint_as_float(f.w);
-      }
+    for (int h = NH - 1; h >= 0; --h) {              // (run 0 stays in registers)
+      load_s(h, s);
+      bmax = fmaxf(bmax, max_s(s));
     }
-    const int c0 = kb + cp * W;                      // first key of this copy's columns
-    if (c0 + W > ctx) {
-      // keys of the tree, or past the last: bit i says whether key c0 + i is seen
-      uint64_t see = 0;
-      const int skip = max(ctx - c0, 0);             // context keys at the front
-      const int j0 = c0 + skip - ctx;                // first tree key of the columns
-      if (j0 < ntok) {
-        see = P.mask ? load_bits64(P.mask, P.mask_bytes, bit0 + (long long)tok * ntok + j0)
-                     : (tok - j0 >= 63 ? ~0ull : tok < j0 ? 0ull : (2ull << (tok - j0)) - 1ull);
-        const int left = ntok - j0;
-        if (left < 64) see &= (1ull << left) - 1ull;
-      }
-      if (skip) see = skip < 64 ? (see << skip) | ((1ull << skip) - 1ull) : ~0ull;
-#pragma unroll
-      for (int i = 0; i < W; ++i)
-        if (!((see >> i) & 1ull)) s[i] = NEG_INF;
-    }
-    float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-    for (int i = 4; i < W; i += 8) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        mx[u] = i + 4 + u < W ? max3(mx[u], s[i + u], s[i + 4 + u]) : fmaxf(mx[u], s[i + u]);
-    }
-    const float bmax = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-    const float m_new = fmaxf(m_ref, bmax * qscale);
-    const bool rescale = m_new > m_ref + 8.0f;       // also for the first finite maximum
-    const float m_use = rescale ? m_new : m_ref;
+    const float top = bmax * qscale;
+    const bool rescale = top > m_ref + L::LIMIT;     // also for the first finite maximum
+    const float m_use = rescale ? top - L::TOP : m_ref;
     const float m_sub = m_use == NEG_INF ? 0.f : m_use;
-    float rs = 0.f;
-    uint32_t pk[W / 2];
+    // P goes over S: 16-bit, two keys a column; E4M3, four keys a column, BK / 4
+    // columns of high parts, then as many of low parts. Run h of P lies over
+    // columns of S that run h or an earlier one has read.
+    const uint64_t qs2 = pack2(qscale, qscale), ms2 = pack2(-m_sub, -m_sub);
+    uint64_t rs[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < W; i += 4) {
-      const float e0 = ex2(fmaf(s[i], qscale, -m_sub)), e1 = ex2(fmaf(s[i + 1], qscale, -m_sub));
-      const float e2 = ex2(fmaf(s[i + 2], qscale, -m_sub)), e3 = ex2(fmaf(s[i + 3], qscale, -m_sub));
-      rs += (e0 + e1) + (e2 + e3);
-      pk[i / 2] = Pack<E>::two(e0, e1);
-      pk[i / 2 + 1] = Pack<E>::two(e2, e3);
-    }
-    if constexpr (KV == 2) {
+    for (int h = 0; h < NH; ++h) {
+      if (h > 0) load_s(h, s);
+      constexpr int N = L::F8 ? 32 : 16;             // keys of 8 columns
 #pragma unroll
-      for (int i = 0; i < W; i += 8) {               // (exact, down to fp16's subnormals)
-        const uint4 f = lds128(vfac0 + (j & 1) * L::FAC_V + 2 * (cp * W + i));
-        pk[i / 2] = hmul2_u32(pk[i / 2], f.x);
-        pk[i / 2 + 1] = hmul2_u32(pk[i / 2 + 1], f.y);
-        pk[i / 2 + 2] = hmul2_u32(pk[i / 2 + 2], f.z);
-        pk[i / 2 + 3] = hmul2_u32(pk[i / 2 + 3], f.w);
+      for (int q = 0; q < W; q += N) {
+        uint64_t e[N / 2];
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+          float a, b2;
+          unpack2(fma2(pack2(s[q + i], s[q + i + 1]), qs2, ms2), a, b2);
+          e[i / 2] = pack2(ex2(a), ex2(b2));
+          rs[i / 2 & 1] = add2(rs[i / 2 & 1], e[i / 2]);
+        }
+        uint32_t hi[8];
+        const uint32_t col = (uint32_t)(my0 + h * W + q) / (N / 8);
+        if constexpr (!L::F8) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float a, b2;
+            unpack2(e[i], a, b2);
+            hi[i] = Pack<T>::two(a, b2);
+          }
+        } else {
+          if constexpr (KV == 2) {
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+              uint64_t f[2];
+              factors4<L::FACB>(vfac, my0 + h * W + q + i, f);
+              e[i / 2] = mul2(e[i / 2], f[0]);
+              e[i / 2 + 1] = mul2(e[i / 2 + 1], f[1]);
+            }
+          }
+          uint32_t lo[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) e4m3_split4(e[2 * i], e[2 * i + 1], hi[i], lo[i]);
+          tmem_st8(s_addr + BK / 4 + col, lo);
+        }
+        tmem_st8(s_addr + col, hi);
       }
+    }
+    if constexpr (C > 1) {                           // zeros for the other copies' keys
+      const uint32_t zero[8] = {};
+      constexpr int PART = L::F8 ? BK / 4 : BK / 2;
+#pragma unroll
+      for (int c = 0; c < BK / 2; c += 8)
+        if (c % PART / (PART / C) != cp) tmem_st8(s_addr + c, zero);
     }
     const bool need = (rescale && m_ref != NEG_INF) || (KV == 2 && o_scale != 1.f);
     if (j > 0 && __any_sync(0xffffffffu, need)) {
       // O holds P V up to the last block: wait for it, then rescale in TMEM
       const int sp = sc - 1;
-      if (!tree_wait(BAR(TB_PVDONE + (sp & 1)), (sp >> 1) & 1, abort_flag)) {
+      if (!tree_wait(BAR(TB_PVDONE + sp % NSB), (sp / NSB) & 1, abort_flag)) {
         ok = false;
         if (KV == 2) continue;
         break;
@@ -384,17 +514,10 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
       l *= a_m;
     }
     m_ref = m_use;
-    l += rs;
-    // P over the first 32 columns of S: this copy's keys, zeros for the others'
-    if constexpr (C == 1) {
-      tmem_st32u(s_addr, pk);
-    } else {
-      const uint32_t zero[8] = {};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if constexpr (C == 4) tmem_st8(s_addr + 8 * c, c == cp ? pk : zero);
-        else tmem_st8(s_addr + 8 * c, (c >> 1) == cp ? pk + 8 * (c & 1) : zero);
-      }
+    {
+      float a, b2;
+      unpack2(add2(rs[0], rs[1]), a, b2);
+      l += a + b2;
     }
     tmem_wait_st();
     tc_fence_before();
@@ -402,7 +525,7 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
   }
   if (ok) {
     const int sl = sc0 + nb - 1;
-    ok = tree_wait(BAR(TB_PVDONE + (sl & 1)), (sl >> 1) & 1, abort_flag);
+    ok = tree_wait(BAR(TB_PVDONE + sl % NSB), (sl / NSB) & 1, abort_flag);
   }
   if (C > 1 || KV == 2) ok = softmax_vote(ok);
   if (!ok) return false;
@@ -453,14 +576,13 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
 #pragma unroll 1
     for (int c0 = 0; c0 < D; c0 += L::JOIN) {
       softmax_sync();                                // the last part has been read
-#pragma unroll 1
-      for (int c = 0; c < L::JOIN; c += 32) {
+      {
         float o[32];
-        tmem_ld32(tmem + lane_base + L::TM_O + c0 + c, o);
+        tmem_ld32(tmem + lane_base + L::TM_O + c0, o);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           // (chunks turned by the lane: eight lanes of a store meet eight bank groups)
-          const int ch = (c / 4 + i + tid) & (CH - 1);
+          const int ch = (i + tid) & (CH - 1);
           sts128(sbase + L::Q_OFF + tid * (CH * 16) + ch * 16, *reinterpret_cast<uint4*>(o + 4 * i));
         }
       }
@@ -517,41 +639,39 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
 template <typename T, int D, int KV>
 __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
     pod_tree_kernel(const __grid_constant__ PodTreeParams P) {
-  using L = TLayout<D, KV>;
-  using E = typename std::conditional<KV == 0, T, __half>::type;   // operand type of the MMAs
+  using L = TLayout<T, D, KV>;
+  constexpr int BK = L::BK, NSB = L::NSB;
   extern __shared__ __align__(1024) uint8_t smem[];
   // the merge kernel may be scheduled now; it waits for this grid's completion
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (uniform, and known to be)
   const uint32_t sbase = smem_u32(smem), bar0 = sbase + L::BAR_OFF;
-  static_assert(TB_COUNT * 8 <= 176, "barriers overlap the TMEM slot");
+  static_assert(TB_COUNT * 8 <= 152, "barriers overlap the TMEM slot");
   if ((sbase & 1023u) != 0u) {                       // 128B-swizzle atoms need 1024-byte alignment
     if (tid == 0) atomicOr(P.status, POD_STATUS_ALIGN);
     return;
   }
   auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::BAR_OFF + 180);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::BAR_OFF + 156);
   if (warp == 4) {
-    tmem_alloc(sbase + L::BAR_OFF + 176, L::TMEM_COLS);
+    tmem_alloc(sbase + L::BAR_OFF + 152, L::TMEM_COLS);
     tmem_relinquish();
   }
   const bool tma = P.kbx > 0;
   if (tid == 0) {
-    const uint32_t load16 = tma ? 1u : 96u;          // gather: three warps
+    const uint32_t loads = tma ? 1u : 96u;           // gather: three warps
     mbar_init(BAR(TB_QFULL), 128);
     for (int s = 0; s < 3; ++s) {
-      mbar_init(BAR(TB_KFULL + s), KV == 0 ? load16 : 64u);
+      mbar_init(BAR(TB_KFULL + s), loads);
       mbar_init(BAR(TB_KEMPTY + s), 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(BAR(TB_VFULL + s), KV == 0 ? load16 : 64u);
+      mbar_init(BAR(TB_VFULL + s), loads);
       mbar_init(BAR(TB_VEMPTY + s), 1);
       mbar_init(BAR(TB_SFULL + s), 1);
       mbar_init(BAR(TB_PFULL + s), 128);
       mbar_init(BAR(TB_PVDONE + s), 1);
-      mbar_init(BAR(TB_RFULL + s), tma ? 1u : 32u);
-      mbar_init(BAR(TB_REMPTY + s), 64);
     }
     mbar_init(BAR(TB_FINAL), 1);
     *abort_flag = 0;
@@ -560,7 +680,7 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::BAR_OFF + 176);
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::BAR_OFF + 152);
   const int seg0 = P.cta_ptr[blockIdx.x], seg1 = P.cta_ptr[blockIdx.x + 1];
   bool ok = true;
   volatile int never = 0;                            // an abort flag that nobody raises
@@ -570,99 +690,122 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
     for (int i = seg0; i < seg1 && ok; ++i) {
       const int32_t* seg = P.segs + (size_t)i * TS_REC;
       const int copies = seg[TS_COPIES];
-      ok = copies == 4   ? tree_softmax<T, E, D, KV, 4>(P, smem, tmem, seg, sc0, abort_flag)
-           : copies == 2 ? tree_softmax<T, E, D, KV, 2>(P, smem, tmem, seg, sc0, abort_flag)
-                         : tree_softmax<T, E, D, KV, 1>(P, smem, tmem, seg, sc0, abort_flag);
+      ok = copies == 4   ? tree_softmax<T, D, KV, 4>(P, smem, tmem, seg, sc0, abort_flag)
+           : copies == 2 ? tree_softmax<T, D, KV, 2>(P, smem, tmem, seg, sc0, abort_flag)
+                         : tree_softmax<T, D, KV, 1>(P, smem, tmem, seg, sc0, abort_flag);
     }
   } else if (warp == 4) {
     // ---------------------------------------------------------- MMA issuer
-    // Per segment: QK_0, [QK_1, PV_0], ..., PV_{nb-1}. QK_{j+2} reuses the
-    // columns of S_j / P_j; MMAs issued by one thread run in order. The whole
-    // warp walks the loop and one elected lane issues: addresses and
-    // descriptors then stay in uniform registers (a loop under `lane == 0`
-    // moved each of them there for every MMA: 85 clocks an instruction).
-    const uint32_t id_qk = idesc_f16(Pack<E>::kBF16, 128, BK, false, false);
-    const uint32_t id_pv = idesc_f16(Pack<E>::kBF16, 128, D, false, true);
-    // V stage: 16-key steps inside a box of vb keys ([box][64-column part][key])
-    const int vb = KV == 0 && tma ? P.kbx : BK;
-    const uint32_t v_box = (uint32_t)(vb * L::NKB * 128);
-    const uint64_t v_desc0 = sdesc_sw128(sbase + L::V_OFF, (uint32_t)vb * 128u,
-                                         vb >= 16 ? 1024u : (uint32_t)L::NKB * 1024u);
-    uint32_t v_step[BK / 16];
+    // Two S buffers: QK_0, [QK_1, PV_0], ..., PV_{nb-1}; QK_{j+2} reuses the
+    // columns of S_j / P_j, and MMAs issued by one thread run in order. One S
+    // buffer: QK_0, [PV_0, QK_1], ... The whole warp walks the loop and one
+    // elected lane issues: addresses and descriptors then stay in uniform
+    // registers (a loop under `lane == 0` moved each of them there for every
+    // MMA: 85 clocks an instruction).
+    const uint32_t id_qk = L::F8 ? idesc_e4m3(128, BK, false, false) : idesc_f16(Pack<T>::kBF16, 128, BK, false, false);
+    const uint32_t id_pv = L::F8 ? idesc_e4m3(128, D, false, true) : idesc_f16(Pack<T>::kBF16, 128, D, false, true);
+    // V stage: 16-bit TMA boxes of vb keys lie as [box][row part][key], anything
+    // else as [row part][key]
+    const int vb = !L::F8 && tma ? P.kbx : BK;
+    const uint32_t v_box = (uint32_t)(vb * L::PARTS * L::ROWB);
+    const uint64_t v_desc0 = L::desc(sbase + L::V_OFF, (uint32_t)(vb * L::ROWB),
+                                     vb >= L::KSTEP ? 8u * L::ROWB : 8u * L::ROWB * L::PARTS);
+    uint32_t v_step[L::KSTEPS];
 #pragma unroll
-    for (int k = 0; k < BK / 16; ++k) v_step[k] = (uint32_t)(k * 16 / vb) * v_box + (uint32_t)(k * 16 % vb) * 128u;
-    const uint64_t q_desc0 = sdesc_sw128(sbase + L::Q_OFF, 16, 1024);
-    const uint64_t k_desc0 = sdesc_sw128(sbase + L::K_OFF, 16, 1024);
-    int ks = 0, vs = 0;                              // ring positions, and their phases
+    for (int k = 0; k < L::KSTEPS; ++k)
+      v_step[k] = ((uint32_t)(k * L::KSTEP / vb) * v_box + (uint32_t)(k * L::KSTEP % vb) * L::ROWB) >> 4;
+    const uint64_t q_desc0 = L::desc(sbase + L::Q_OFF, 16, 8 * L::ROWB);
+    const uint64_t k_desc0 = L::desc(sbase + L::K_OFF, 16, 8 * L::ROWB);
+    int ks = 0, vs = 0, sc0 = 0;                     // ring positions, with their phases
     uint32_t kph = 0, vph = 0;
-    int sc0 = 0;
     for (int i = seg0; i < seg1 && ok; ++i) {
       const int32_t* seg = P.segs + (size_t)i * TS_REC;
       const int blk0 = seg[TS_BLK0], nb = seg[TS_BLK1] - blk0, kv_len = seg[TS_KVLEN];
       if (!tree_wait(BAR(TB_QFULL), (i - seg0) & 1, abort_flag)) { ok = false; break; }
       tc_fence_after();
-      for (int j = 0; j <= nb; ++j) {
-        if (j < nb) {
-          if (!tree_wait(BAR(TB_KFULL + ks), kph, abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          if (KV == 0 && !tma) fence_proxy_async();
-          const int b = (sc0 + j) & 1;
-          const uint32_t d_s = tmem + L::TM_S + b * BK;
-          const uint64_t kd = k_desc0 + (uint32_t)(ks * L::STAGE >> 4);
-          if (elect_one()) {
+      auto qk = [&](int j) -> bool {
+        if (!tree_wait(BAR(TB_KFULL + ks), kph, abort_flag)) return false;
+        tc_fence_after();
+        if (!tma) fence_proxy_async();
+        const int b = (sc0 + j) % NSB;
+        const uint32_t d_s = tmem + L::TM_S + b * BK;
+        const uint64_t kd = k_desc0 + (uint32_t)(ks * L::STAGE >> 4);
+        if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_f16_ss(d_s, q_desc0 + (((k >> 2) * L::QBLK + (k & 3) * 32) >> 4),
-                         kd + (((k >> 2) * L::KVBLK + (k & 3) * 32) >> 4), id_qk, k > 0 ? 1u : 0u);
-            mma_commit(BAR(TB_SFULL + b));
-            mma_commit(BAR(TB_KEMPTY + ks));
-          }
-          __syncwarp();
-          if (++ks == L::NK) { ks = 0; kph ^= 1; }
-        }
-        if (j > 0) {
-          const int sc = sc0 + j - 1, b = sc & 1;
-          if (!tree_wait(BAR(TB_VFULL + vs), vph, abort_flag)) { ok = false; break; }
-          if (!tree_wait(BAR(TB_PFULL + b), (sc >> 1) & 1, abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          // 16-key steps past kv_len carry P = 0: skip them. Rows at or past
-          // kv_len in the last step are unused slots of the last page, or
-          // nothing: zero them, so that P = 0 never meets a non-finite value.
-          const int keys = min(kv_len - (blk0 + j - 1) * BK, BK), ksteps = (keys + 15) >> 4;
-          if (KV == 0 && (keys & 15)) {
-            const uint32_t va = sbase + L::V_OFF + vs * L::STAGE;
-            for (int x = lane; x < (ksteps * 16 - keys) * L::NKB * 8; x += 32) {
-              const int r = keys + x / (L::NKB * 8), h = x / 8 % L::NKB, c = x % 8;
-              sts128(va + (uint32_t)(r / vb) * v_box + h * vb * 128 + sw128_off(r % vb, c), make_uint4(0, 0, 0, 0));
+          for (int p = 0; p < L::QP; ++p)
+#pragma unroll
+            for (int k = 0; k < L::DSTEPS; ++k) {
+              constexpr int SPP = L::ROWB / 32;      // steps of a row part
+              const uint64_t qd = q_desc0 + (((p * L::PARTS + k / SPP) * L::QPART + (k % SPP) * 32) >> 4);
+              const uint64_t bd = kd + (((k / SPP) * L::KVPART + (k % SPP) * 32) >> 4);
+              if constexpr (L::F8) mma_f8_ss(d_s, qd, bd, id_qk, p + k > 0 ? 1u : 0u);
+              else mma_f16_ss(d_s, qd, bd, id_qk, k > 0 ? 1u : 0u);
             }
-            fence_proxy_async();
-            __syncwarp();
-          } else if (KV == 0 && !tma) {
-            fence_proxy_async();
-          }
-          const uint64_t vd = v_desc0 + (uint32_t)(vs * L::STAGE >> 4);
-          if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < BK / 16; ++k)
-              if (k < ksteps)
-                mma_f16_ts(tmem + L::TM_O, tmem + L::TM_S + b * BK + k * 8, vd + (v_step[k] >> 4), id_pv,
-                           (j > 1 || k > 0) ? 1u : 0u);
-            mma_commit(BAR(TB_PVDONE + b));
-            mma_commit(BAR(TB_VEMPTY + vs));
-          }
-          __syncwarp();
-          if (++vs == L::NV) { vs = 0; vph ^= 1; }
+          mma_commit(BAR(TB_SFULL + b));
+          mma_commit(BAR(TB_KEMPTY + ks));
         }
+        __syncwarp();
+        if (++ks == L::NK) { ks = 0; kph ^= 1; }
+        return true;
+      };
+      auto pv = [&](int j) -> bool {
+        const int sc = sc0 + j, b = sc % NSB;
+        if (!tree_wait(BAR(TB_VFULL + vs), vph, abort_flag)) return false;
+        // Key steps past kv_len carry P = 0: skip them. Rows at or past kv_len in
+        // the last step are unused slots of the last page, or nothing: zero them,
+        // so that P = 0 never meets a non-finite value.
+        const int keys = min(kv_len - (blk0 + j) * BK, BK), ksteps = (keys + L::KSTEP - 1) / L::KSTEP;
+        const uint64_t vd = v_desc0 + (uint32_t)(vs * L::STAGE >> 4);
+        const uint32_t a_p = tmem + L::TM_S + b * BK;
+        if (keys % L::KSTEP) {
+          const uint32_t va = sbase + L::V_OFF + vs * L::STAGE;
+          constexpr int CPP = L::ROWB / 16;          // 16-byte chunks of a row part
+          for (int x = lane; x < (ksteps * L::KSTEP - keys) * L::PARTS * CPP; x += 32) {
+            const int r = keys + x / (L::PARTS * CPP), h = x / CPP % L::PARTS, c = x % CPP;
+            sts128(va + (uint32_t)(r / vb) * v_box + (h * vb + r % vb) * L::ROWB + c * 16, make_uint4(0, 0, 0, 0));
+          }
+          fence_proxy_async();
+          __syncwarp();
+        } else if (!tma) {
+          fence_proxy_async();
+        }
+        if (!tree_wait(BAR(TB_PFULL + b), (sc / NSB) & 1, abort_flag)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < L::KSTEPS; ++k)
+            if (k < ksteps) {
+              if constexpr (L::F8) {
+                mma_f8_ts(tmem + L::TM_O, a_p + k * 8, vd + v_step[k], id_pv, (j > 0 || k > 0) ? 1u : 0u);
+                mma_f8_ts(tmem + L::TM_O, a_p + BK / 4 + k * 8, vd + v_step[k], id_pv, 1u);
+              } else {
+                mma_f16_ts(tmem + L::TM_O, a_p + k * 8, vd + v_step[k], id_pv, (j > 0 || k > 0) ? 1u : 0u);
+              }
+            }
+          mma_commit(BAR(TB_PVDONE + b));
+          mma_commit(BAR(TB_VEMPTY + vs));
+        }
+        __syncwarp();
+        if (++vs == L::NV) { vs = 0; vph ^= 1; }
+        return true;
+      };
+      for (int j = 0; j <= nb && ok; ++j) {
+        if (NSB > 1 && j < nb) ok = qk(j);
+        if (j > 0 && ok) ok = pv(j - 1);
+        if (NSB == 1 && j < nb && ok) ok = qk(j);
       }
       sc0 += nb;
     }
-  } else if (KV == 0 && tma) {
+  } else if (tma) {
     // ---------------------------------------------------------- K and V boxes
     if (warp < 7) {
       const bool is_v = warp == 6;
       const void* tm = is_v ? &P.tm_v : &P.tm_k;
       const int NS = is_v ? L::NV : L::NK;
-      const int groups = BK / P.kbx, per = is_v ? 1 : L::NKB;     // boxes of a block: groups x per
+      // boxes of a block: groups of kbx keys, a box for each row part; a 16-bit V
+      // box holds every part
+      const bool whole = is_v && !L::F8;
+      const int groups = BK / P.kbx, per = whole ? 1 : L::PARTS;
       const int gi = lane / per, part = lane - gi * per;
       const bool mine = gi < groups;
       // keys are read once unless another tile of the request reads them too
@@ -688,8 +831,9 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
           __syncwarp();
           if (mine) {
             const int tin = (blk * BK + gi * P.kbx) & (P.ps - 1);
-            const uint32_t dst = is_v ? sbase + L::V_OFF + s * L::STAGE + gi * P.kbx * L::NKB * 128
-                                      : sbase + L::K_OFF + s * L::STAGE + part * L::KVBLK + gi * P.kbx * 128;
+            const uint32_t stage = sbase + (is_v ? L::V_OFF : L::K_OFF) + s * L::STAGE;
+            const uint32_t dst = stage + (whole ? gi * P.kbx * L::PARTS * L::ROWB
+                                                : part * L::KVPART + gi * P.kbx * L::ROWB);
             // (a page past the request's last is out of the pool: TMA fills zeros)
             if (shared_keys)
               tma_load_5d(dst, tm, 0, tin, part, g, 2 * page + (is_v ? 1 : 0), BAR(full));
@@ -704,143 +848,56 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
       for (int f = max(fill - NS, 0); f < fill; ++f)
         tree_wait(BAR((is_v ? TB_VFULL : TB_KFULL) + f % NS), (f / NS) & 1, &never);
     }
-  } else if (KV == 0) {
-    // ---------------------------------------------------------- gather, 16-bit
-    const int lt = tid - 160;                        // 0..95
-    const T* __restrict__ kvg = static_cast<const T*>(P.kv);
-    const size_t vstep = (size_t)P.ps * P.Hk * D;
-    constexpr int CPR = D / 8, CH = BK * CPR;
-    int fill = 0, vfill = 0;
-    for (int i = seg0; i < seg1 && ok; ++i) {
-      const int32_t* seg = P.segs + (size_t)i * TS_REC;
-      const int g = seg[TS_G], kv_len = seg[TS_KVLEN], b1 = seg[TS_BLK1];
-      KeyAt at{P.pages + seg[TS_PAGE0], seg[TS_NPAGES], P.ps, P.ps_shift};
-      auto gather = [&](int blk, bool is_v, uint32_t dst) {
-#pragma unroll 4
-        for (int x = lt; x < CH; x += 96) {
-          const int key = x / CPR, c = x - key * CPR, t = blk * BK + key;
-          const int tt = t < kv_len ? t : kv_len - 1;
-          const size_t page = (size_t)at.page(tt);
-          const int slot = at.slot(tt);
-          const T* src = kvg + (page * 2 * P.ps * P.Hk + (P.hnd ? (size_t)g * P.ps + slot : (size_t)slot * P.Hk + g)) * D +
-                         (is_v ? vstep : 0) + c * 8;
-          cp_async16(dst + (c >> 3) * L::KVBLK + sw128_off(key, c & 7), src, t < kv_len ? 16u : 0u);
-        }
-      };
-      for (int blk = seg[TS_BLK0]; blk < b1; ++blk) {
-        const int s = fill % L::NK;
-        if (!tree_wait(BAR(TB_KEMPTY + s), ((fill / L::NK) & 1) ^ 1, abort_flag)) { ok = false; break; }
-        gather(blk, false, sbase + L::K_OFF + s * L::STAGE);
-        cp_async_mbar_arrive(BAR(TB_KFULL + s));
-        ++fill;
-        const int v = vfill % L::NV;
-        if (!tree_wait(BAR(TB_VEMPTY + v), ((vfill / L::NV) & 1) ^ 1, abort_flag)) { ok = false; break; }
-        gather(blk, true, sbase + L::V_OFF + v * L::STAGE);
-        cp_async_mbar_arrive(BAR(TB_VFULL + v));
-        ++vfill;
-      }
-    }
-    cp_async_wait_all();
-  } else if (warp == 5) {
-    // ---------------------------------------------------------- FP8 codes, K and V
+  } else {
+    // ---------------------------------------------------------- gather
+    // Every lane finds the rows of BK / 32 keys of the next block while the
+    // copies of this one are issued; a warp copies 32 / CPR keys at a time,
+    // their rows passed by shuffle.
+    constexpr int CPR = D * L::ES / 16;              // 16-byte chunks of a row
+    constexpr int KPI = 32 / CPR, NQ = BK / 32;
+    const int w = warp - 5;
     const uint8_t* __restrict__ kvg = static_cast<const uint8_t*>(P.kv);
-    const size_t vstep = (size_t)P.ps * P.Hk * D;
-    const int groups = tma ? BK / P.kbx : 0;
-    const int gi = lane >> 1, is_v = lane & 1;
-    const bool mine = gi < groups;
-    const uint64_t pol = l2_policy_evict_first();
-    int fill = 0;
-    for (int i = seg0; i < seg1 && ok; ++i) {
-      const int32_t* seg = P.segs + (size_t)i * TS_REC;
-      const int g = seg[TS_G], npages = seg[TS_NPAGES], kv_len = seg[TS_KVLEN], b1 = seg[TS_BLK1];
-      const bool shared_keys = (long long)seg[TS_NTOK] * P.G > POD_TREE_TILE;
-      KeyAt at{P.pages + seg[TS_PAGE0], npages, P.ps, P.ps_shift};
-      auto page_of = [&](int blk) {
-        const int p = (blk * BK + gi * P.kbx) >> P.ps_shift;
-        return mine && p < npages ? __ldg(at.pages + p) : P.num_pages;
-      };
-      int page = tma ? page_of(seg[TS_BLK0]) : 0;
-      for (int blk = seg[TS_BLK0]; blk < b1; ++blk) {
-        const int s = fill % 2;
-        if (!tree_wait(BAR(TB_REMPTY + s), ((fill / 2) & 1) ^ 1, abort_flag)) { ok = false; break; }
-        const uint32_t dst = sbase + L::R_OFF + s * 2 * L::RAW;
-        if (tma) {
-          if (lane == 0) mbar_arrive_expect_tx(BAR(TB_RFULL + s), 2 * L::RAW);
-          __syncwarp();
-          if (mine) {
-            const int tin = (blk * BK + gi * P.kbx) & (P.ps - 1);
-            const uint32_t a = dst + is_v * L::RAW + gi * P.kbx * D;
-            if (shared_keys) tma_load_4d(a, &P.tm_k, 0, tin, g, 2 * page + is_v, BAR(TB_RFULL + s));
-            else tma_load_4d_hint(a, &P.tm_k, 0, tin, g, 2 * page + is_v, BAR(TB_RFULL + s), pol);
-          }
-          if (blk + 1 < b1) page = page_of(blk + 1);
-        } else {
-          constexpr int CPR = D / 16;
-#pragma unroll 4
-          for (int x = lane; x < BK * CPR; x += 32) {
-            const int key = x / CPR, c = x - key * CPR, t = blk * BK + key;
-            const int tt = t < kv_len ? t : kv_len - 1;
-            const int slot = at.slot(tt);
-            const uint8_t* src = kvg + ((size_t)at.page(tt) * 2 * P.ps * P.Hk +
-                                        (P.hnd ? (size_t)g * P.ps + slot : (size_t)slot * P.Hk + g)) * D + c * 16;
-            cp_async16(dst + key * D + c * 16, src, t < kv_len ? 16u : 0u);
-            cp_async16(dst + L::RAW + key * D + c * 16, src + vstep, t < kv_len ? 16u : 0u);
-          }
-          cp_async_mbar_arrive(BAR(TB_RFULL + s));
-        }
-        ++fill;
-      }
-    }
-    if (!tma) cp_async_wait_all();
-    for (int f = max(fill - 2, 0); f < fill; ++f)    // no copy is in flight when the CTA ends
-      tree_wait(BAR(TB_RFULL + f % 2), (f / 2) & 1, &never);
-  } else if constexpr (KV != 0) {
-    // ---------------------------------------------------------- widen the codes
-    // Thread = key: its K row, then its V row, 16 codes at a time into the
-    // swizzled fp16 stages. The chunk order is turned by the key, so the 8
-    // lanes of a load or store phase meet different banks. V rows at or past
-    // kv_len become zeros.
-    const int key = tid - 192;
+    const long long vstep = (long long)P.ps * P.Hk;
+    const int sub = lane / CPR, c = lane % CPR;
+    const int part = c / (L::ROWB / 16), cc = c % (L::ROWB / 16);
     int fill = 0;
     for (int i = seg0; i < seg1 && ok; ++i) {
       const int32_t* seg = P.segs + (size_t)i * TS_REC;
       const int kv_len = seg[TS_KVLEN], b1 = seg[TS_BLK1];
+      const KeyAt at = key_at(P, seg);
+      long long row[NQ], next[NQ];
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) next[q] = at.row(min(seg[TS_BLK0] * BK + q * 32 + lane, kv_len - 1));
       for (int blk = seg[TS_BLK0]; blk < b1; ++blk) {
-        const int r = fill % 2, s = fill % L::NK, v = fill % L::NV;
-        if (!tree_wait(BAR(TB_RFULL + r), (fill / 2) & 1, abort_flag)) { ok = false; break; }
-        const uint32_t raw = sbase + L::R_OFF + r * 2 * L::RAW + key * D;
-        const bool live = blk * BK + key < kv_len;
-        auto widen = [&](uint32_t src, uint32_t dst, bool keep) {
-          constexpr int NCH = D / 16;
 #pragma unroll
-          for (int c = 0; c < NCH; ++c) {
-            const int ch = (c + key) & (NCH - 1);
-            uint4 w = lds128(src + ch * 16);
-            if (!keep) w = make_uint4(0, 0, 0, 0);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-            uint32_t h[8];
+        for (int q = 0; q < NQ; ++q) {
+          row[q] = next[q];
+          if (blk + 1 < b1) next[q] = at.row(min((blk + 1) * BK + q * 32 + lane, kv_len - 1));
+        }
+        const int left = kv_len - blk * BK;
+        auto copy = [&](uint32_t dst, long long step) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              h[2 * q] = e4m3x2_to<__half>((uint16_t)(u[q] & 0xffffu));
-              h[2 * q + 1] = e4m3x2_to<__half>((uint16_t)(u[q] >> 16));
+          for (int q = 0; q < NQ; ++q) {
+#pragma unroll 4
+            for (int x = w; x < 32 / KPI; x += 3) {
+              const int k = x * KPI + sub, key = q * 32 + k;
+              const long long r = __shfl_sync(0xffffffffu, row[q], k) + step;
+              cp_async16(dst + part * L::KVPART + L::swz(key, cc), kvg + r * (D * L::ES) + c * 16,
+                         key < left ? 16u : 0u);
             }
-            const uint32_t part = dst + (ch >> 2) * L::KVBLK;
-            const int c2 = (ch & 3) * 2;
-            sts128(part + sw128_off(key, c2), make_uint4(h[0], h[1], h[2], h[3]));
-            sts128(part + sw128_off(key, c2 + 1), make_uint4(h[4], h[5], h[6], h[7]));
           }
-          fence_proxy_async();
         };
+        const int s = fill % L::NK, v = fill % L::NV;
         if (!tree_wait(BAR(TB_KEMPTY + s), ((fill / L::NK) & 1) ^ 1, abort_flag)) { ok = false; break; }
-        widen(raw, sbase + L::K_OFF + s * L::STAGE, true);
-        mbar_arrive(BAR(TB_KFULL + s));
+        copy(sbase + L::K_OFF + s * L::STAGE, 0);
+        cp_async_mbar_arrive(BAR(TB_KFULL + s));
         if (!tree_wait(BAR(TB_VEMPTY + v), ((fill / L::NV) & 1) ^ 1, abort_flag)) { ok = false; break; }
-        widen(raw + L::RAW, sbase + L::V_OFF + v * L::STAGE, live);
-        mbar_arrive(BAR(TB_VFULL + v));
-        mbar_arrive(BAR(TB_REMPTY + r));
+        copy(sbase + L::V_OFF + v * L::STAGE, vstep);
+        cp_async_mbar_arrive(BAR(TB_VFULL + v));
         ++fill;
       }
     }
+    cp_async_wait_all();
   }
   if (!ok) {
     *abort_flag = 1;
@@ -862,7 +919,7 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
 
 template <typename T, int D, int KV>
 cudaError_t launch_tree(const PodTreeParams& P, cudaStream_t stream) {
-  constexpr int SMEM = TLayout<D, KV>::TOTAL;
+  constexpr int SMEM = TLayout<T, D, KV>::TOTAL;
   static_assert(SMEM <= (D == 256 ? 232448 : 115712), "shared memory of the CTAs on an SM");
   // the attributes belong to each device: set once per device
   static std::atomic<unsigned long long> done{0ull};

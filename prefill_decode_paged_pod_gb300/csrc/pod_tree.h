@@ -5,7 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#define POD_TREE_BLOCK 64     // keys per block (one S buffer, one stage)
+#define POD_TREE_BLOCK 64     // keys per block (one S buffer, one stage), 16-bit caches
+#define POD_TREE_BLOCK8 128   // the same for FP8 caches
 #define POD_TREE_TILE 128     // packed query rows per tile (TMEM lanes)
 
 // Segment record, one for each run of key blocks that a CTA works through for
@@ -32,7 +33,7 @@ enum PodTreeGroup { TG_G = 0, TG_ROW0, TG_NROWS, TG_PROW0, TG_NSEG, TG_QROW0, TG
 enum { TREE_ST_STATUS = 0, TREE_ST_INTS = 64 };
 
 struct PodTreeParams {
-  CUtensorMap tm_k, tm_v;        // 16-bit: K and V boxes; FP8: tm_k holds both (raw codes)
+  CUtensorMap tm_k, tm_v;        // boxes of K and of V
   const void *q, *kv;
   const uint8_t* scales;         // block-scaled cache: exponent bytes
   const uint8_t* mask;           // packed tree mask, nullptr: a chain

@@ -111,27 +111,22 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// 16-bit cache as [64][slot][d/64][Hk][2 * page + kv]: a box holds `kbx` keys of
-// one head, `parts` 64-element parts of them ([part][key][64] in shared memory)
-CUresult encode_16(CUtensorMap* m, const void* kv, const PodTreePlanHost& P, int hnd, int kbx, int parts, int dtype) {
-  const cuuint64_t row = (cuuint64_t)P.d * 2, ps = P.ps, Hk = P.Hk;
-  cuuint64_t dims[5] = {64, ps, (cuuint64_t)P.d / 64, Hk, 2 * (cuuint64_t)P.num_pages};
-  cuuint64_t strides[4] = {hnd ? row : row * Hk, 128, hnd ? row * ps : row, row * Hk * ps};
-  cuuint32_t box[5] = {64, (cuuint32_t)kbx, (cuuint32_t)parts, 1, 1}, es[5] = {1, 1, 1, 1, 1};
-  return encode_fn()(m, dtype ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
-                     const_cast<void*>(kv), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-}
-// E4M3 codes as [d][slot][Hk][2 * page + kv]; a box holds `kbx` keys ([key][d])
-CUresult encode_8(CUtensorMap* m, const void* kv, const PodTreePlanHost& P, int hnd, int kbx) {
-  const cuuint64_t row = (cuuint64_t)P.d, ps = P.ps, Hk = P.Hk;
-  cuuint64_t dims[4] = {row, ps, Hk, 2 * (cuuint64_t)P.num_pages};
-  cuuint64_t strides[3] = {hnd ? row : row * Hk, hnd ? row * ps : row, row * Hk * ps};
-  cuuint32_t box[4] = {(cuuint32_t)P.d, (cuuint32_t)kbx, 1, 1}, es[4] = {1, 1, 1, 1};
-  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(kv), dims, strides, box, es,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+// The cache as [row part][slot][d / part][Hk][2 * page + kv], a row part 128
+// bytes (or the whole row where that is shorter): a box holds `kbx` keys of one
+// head, `parts` row parts of them ([part][key][bytes] in shared memory),
+// swizzled by the hardware.
+CUresult encode(CUtensorMap* m, const void* kv, const PodTreePlanHost& P, int hnd, int kbx, bool whole, int dtype,
+                bool f8) {
+  const cuuint64_t row = (cuuint64_t)P.d * (f8 ? 1 : 2), ps = P.ps, Hk = P.Hk;
+  const cuuint64_t partb = row < 128 ? row : 128, el = partb / (f8 ? 1 : 2), np = row / partb;
+  cuuint64_t dims[5] = {el, ps, np, Hk, 2 * (cuuint64_t)P.num_pages};
+  cuuint64_t strides[4] = {hnd ? row : row * Hk, partb, hnd ? row * ps : row, row * Hk * ps};
+  cuuint32_t box[5] = {(cuuint32_t)el, (cuuint32_t)kbx, whole ? (cuuint32_t)np : 1u, 1, 1}, es[5] = {1, 1, 1, 1, 1};
+  return encode_fn()(m, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                           : dtype ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                     5, const_cast<void*>(kv), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     partb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 }  // namespace
@@ -193,6 +188,7 @@ pod_status pod_tree_plan(const int32_t* q_indptr, const int32_t* kv_indptr, cons
   PodTreeArgs a;
   a.q_indptr = q_indptr; a.kv_indptr = kv_indptr; a.kv_indices = kv_indices; a.last_page_len = last_page_len;
   a.batch = batch; a.num_pages = num_pages; a.H = num_qo_heads; a.Hk = num_kv_heads; a.d = head_dim;
+  a.block = kv_format == POD_KV_16BIT ? POD_TREE_BLOCK : POD_TREE_BLOCK8;
   a.ps = page_size; a.slots = num_sms * (head_dim == 256 ? 1 : 2);
   std::string err;
   int rc;
@@ -263,18 +259,15 @@ pod_status pod_tree_run(pod_tree_handle h, const void* q, const void* kv, const 
   K.ps_shift = -1;
   for (int s = 0; s < 31; ++s)
     if ((1 << s) == P.ps) K.ps_shift = s;
-  K.kbx = K.ps_shift >= 3 ? (P.ps < POD_TREE_BLOCK ? P.ps : POD_TREE_BLOCK) : 0;
+  const int block = h->format == POD_KV_16BIT ? POD_TREE_BLOCK : POD_TREE_BLOCK8;
+  K.kbx = K.ps_shift >= 3 ? (P.ps < block ? P.ps : block) : 0;
   K.n_cta = P.n_cta; K.n_groups = (int)(P.groups.size() / TG_REC); K.n_mrows = P.n_mrows;
   K.scale_log2 = h->scale_log2; K.v_scale = h->v_scale;
   if (K.kbx) {
     if (!encode_fn()) return fail(POD_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-    CUresult r;
-    if (h->format == POD_KV_16BIT) {
-      r = encode_16(&K.tm_k, kv, P, h->hnd, K.kbx, 1, h->dtype);
-      if (r == CUDA_SUCCESS) r = encode_16(&K.tm_v, kv, P, h->hnd, K.kbx, P.d / 64, h->dtype);
-    } else {
-      r = encode_8(&K.tm_k, kv, P, h->hnd, K.kbx);
-    }
+    const bool f8 = h->format != POD_KV_16BIT;
+    CUresult r = encode(&K.tm_k, kv, P, h->hnd, K.kbx, false, h->dtype, f8);
+    if (r == CUDA_SUCCESS) r = encode(&K.tm_v, kv, P, h->hnd, K.kbx, !f8, h->dtype, f8);
     if (r != CUDA_SUCCESS) return fail(POD_ERR_CUDA, "cuTensorMapEncodeTiled(tree) failed: " + std::to_string((int)r));
   }
   cudaStream_t st = (cudaStream_t)stream;

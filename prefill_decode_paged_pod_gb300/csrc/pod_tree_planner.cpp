@@ -19,8 +19,8 @@
 
 namespace {
 
-constexpr int kStart = 3;      // price of starting a segment, in key blocks
-constexpr int kMinCut = 5;     // a CTA's share is at least this many blocks and one start
+// price of starting a segment, and least keys of a CTA's share, in keys
+constexpr int kStartKeys = 192, kMinKeys = 320;
 
 struct Unit {
   int req, g, blocks;
@@ -31,7 +31,7 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 // Walks one plane with a CTA budget of `share`; calls emit(cta, unit, blk0,
 // blk1) for each segment. Returns the number of CTAs used.
 template <typename F>
-int cut(const std::vector<Unit>& units, int share, F emit) {
+int cut(const std::vector<Unit>& units, int share, int kStart, F emit) {
   int cta = 0, used = 0;
   for (size_t u = 0; u < units.size(); ++u) {
     int at = 0;
@@ -102,6 +102,7 @@ int pod_tree_build_plan(const PodTreeArgs& a, PodTreePlanHost& o, std::string* e
   const int npages = a.batch ? a.kv_indptr[a.batch] : 0;
   o.pages.assign(a.kv_indices ? a.kv_indices : nullptr, a.kv_indices ? a.kv_indices + npages : nullptr);
 
+  const int kStart = (kStartKeys + a.block - 1) / a.block, kMinCut = (kMinKeys + a.block - 1) / a.block;
   // planes of units, and the smallest equal share that the CTA slots allow
   int max_mt = 0;
   for (int r = 0; r < a.batch; ++r)
@@ -111,14 +112,14 @@ int pod_tree_build_plan(const PodTreeArgs& a, PodTreePlanHost& o, std::string* e
   for (int mt = 0; mt < max_mt; ++mt)
     for (int r = 0; r < a.batch; ++r) {
       if ((long long)n[r] * o.G <= (long long)mt * POD_TREE_TILE) continue;
-      const int blocks = (kv[r] + POD_TREE_BLOCK - 1) / POD_TREE_BLOCK;
+      const int blocks = (kv[r] + a.block - 1) / a.block;
       for (int g = 0; g < a.Hk; ++g) planes[mt].push_back({r, g, blocks});
       cost += (long long)a.Hk * (blocks + kStart);
       longest = std::max(longest, (long long)blocks);
     }
   auto ctas = [&](int share) {
     long long c = 0;
-    for (auto& p : planes) c += cut(p, share, [](int, int, int, int) {});
+    for (auto& p : planes) c += cut(p, share, kStart, [](int, int, int, int) {});
     return c;
   };
   int lo = (int)std::min<long long>(std::max<long long>(cost / std::max(1, a.slots), kMinCut + kStart), 1 << 29);
@@ -146,7 +147,7 @@ int pod_tree_build_plan(const PodTreeArgs& a, PodTreePlanHost& o, std::string* e
   long long prows = 0, mrows = 0;
   for (int mt = 0; mt < max_mt; ++mt) {
     std::vector<Seg> s;
-    cut(planes[mt], share, [&](int c, int u, int b0, int b1) { s.push_back({c, u, b0, b1}); });
+    cut(planes[mt], share, kStart, [&](int c, int u, int b0, int b1) { s.push_back({c, u, b0, b1}); });
     for (size_t i = 0; i < s.size();) {
       size_t e = i;
       while (e < s.size() && s[e].unit == s[i].unit) ++e;

@@ -9,6 +9,7 @@
 struct PodTreeArgs {
   const int32_t *q_indptr, *kv_indptr, *kv_indices, *last_page_len;
   int batch, num_pages, H, Hk, d, ps;
+  int block;                       // keys per block
   int slots;                       // CTAs that run at once
 };
 
