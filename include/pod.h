@@ -418,40 +418,53 @@ size_t pod_static_scratch_capacity(void);
  * ------------------------------------------------------------------------ */
 typedef enum { POD_KV_16BIT = 0, POD_KV_E4M3 = 1, POD_KV_E4M3_BLOCK = 2 } pod_kv_format;
 
+/* Arguments of the four calls; each reads the fields that its text names. */
+typedef struct pod_io_args {
+    const void* q;              /* [rows, num_qo_heads, head_dim], q_stride */
+    const void* k;              /* [rows, num_kv_heads, head_dim], k_stride */
+    const void* v;              /* the same, v_stride */
+    const void* q_weight;       /* [head_dim] in dtype, or NULL: no norm */
+    const void* k_weight;
+    const int32_t* positions;   /* [rows] */
+    const int64_t* slots;       /* [rows] */
+    void* q_out;                /* as q, q_out_stride */
+    void* k_out;                /* as k, k_out_stride; pod_gather_kv: its output */
+    void* kv_cache;             /* [num_pages, 2, ...] */
+    uint8_t* kv_scales;         /* exponent bytes of a POD_KV_E4M3_BLOCK cache, else NULL */
+    int32_t* status;            /* or NULL */
+    int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+    int64_t rows, num_pages;
+    int32_t page_size, num_qo_heads, num_kv_heads, head_dim;
+    int32_t kv_layout, kv_format, dtype;      /* dtype: pod_dtype */
+    int32_t rotary_dim, interleaved;
+    float eps, rope_scale, rope_theta, k_scale, v_scale;
+} pod_io_args;
+
 /*
  * pod_qk_norm_rope — RMS norm of every head of q and k, and the rotary
  * position encoding, in one pass.
  * y = x * (mean(x^2) + eps)^(-1/2) * weight over the head's elements (no norm
- * where the weight, [head_dim] in dtype, is NULL); then pair (j, j +
- * rotary_dim/2), or (2j, 2j+1) with `interleaved`, turns by
+ * where the weight is NULL); then pair (j, j + rotary_dim/2), or (2j, 2j+1)
+ * with `interleaved`, turns by
  * (positions[row] / rope_scale) * rope_theta^(-2j/rotary_dim) (the rotation of
  * pod_plan_set_rope, here over the first rotary_dim elements; 0 = none).
- * fp32 throughout, rounded once. positions: DEVICE int32 [rows], any sign, NULL
- * when rotary_dim is 0. num_qo_heads or num_kv_heads may be 0 (then that
- * tensor is not touched). q_out may be q, and k_out k, with the same stride.
- * Errors: POD_ERR_INVALID_ARG (NULL, misaligned or overlapping-by-stride rows,
- * rotary_dim not a multiple of 16 up to head_dim, no heads, bad eps or rope
- * settings), POD_ERR_UNSUPPORTED (head_dim, dtype), POD_ERR_CUDA.
+ * fp32 throughout, rounded once. Positions may have any sign (NULL when
+ * rotary_dim is 0). num_qo_heads or num_kv_heads may be 0 (then that tensor is
+ * not touched). q_out may be q, and k_out k, with the same stride.
+ * Errors: POD_ERR_INVALID_ARG (NULL or misaligned tensors, a stride that does
+ * not hold the heads, rotary_dim not a multiple of 16 up to head_dim, no heads,
+ * bad eps or rope settings), POD_ERR_UNSUPPORTED (head_dim, dtype),
+ * POD_ERR_CUDA.
  */
-pod_status pod_qk_norm_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
-                            int64_t rows, int32_t num_qo_heads, int32_t num_kv_heads,
-                            int32_t head_dim, const void* q_weight, const void* k_weight, float eps,
-                            const int32_t* positions, int32_t rotary_dim, int32_t interleaved,
-                            float rope_scale, float rope_theta, pod_dtype dtype, void* q_out,
-                            void* k_out, int64_t q_out_stride, int64_t k_out_stride, void* stream);
+pod_status pod_qk_norm_rope(const pod_io_args* args, void* stream);
 
 /*
- * pod_append_kv — write rows of K and V ([rows, Hk, head_dim]) into their slots
- * of the cache [num_pages, 2, ...] in the cache's format. Other slots keep
- * their bytes. k_scale / v_scale count for POD_KV_E4M3 only; kv_scales for
- * POD_KV_E4M3_BLOCK only (NULL otherwise).
+ * pod_append_kv — write rows of K and V into their slots of the cache in the
+ * cache's format. Other slots keep their bytes. k_scale / v_scale count for
+ * POD_KV_E4M3 only; kv_scales for POD_KV_E4M3_BLOCK only (NULL otherwise).
  * Errors: POD_ERR_INVALID_ARG, POD_ERR_UNSUPPORTED, POD_ERR_CUDA.
  */
-pod_status pod_append_kv(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
-                         int64_t rows, const int64_t* slots, void* kv_cache, uint8_t* kv_scales,
-                         int64_t num_pages, int32_t page_size, int32_t num_kv_heads,
-                         int32_t head_dim, int32_t kv_layout, int32_t kv_format, float k_scale,
-                         float v_scale, pod_dtype dtype, int32_t* status, void* stream);
+pod_status pod_append_kv(const pod_io_args* args, void* stream);
 
 /*
  * pod_norm_rope_append — pod_qk_norm_rope and pod_append_kv in one pass: q is
@@ -460,29 +473,16 @@ pod_status pod_append_kv(const void* k, const void* v, int64_t k_stride, int64_t
  * is written as it is. num_qo_heads may be 0. Rows with a negative slot still
  * give their q_out.
  */
-pod_status pod_norm_rope_append(const void* q, const void* k, const void* v, int64_t q_stride,
-                                int64_t k_stride, int64_t v_stride, int64_t rows,
-                                const void* q_weight, const void* k_weight, float eps,
-                                const int32_t* positions, int32_t rotary_dim, int32_t interleaved,
-                                float rope_scale, float rope_theta, void* q_out,
-                                int64_t q_out_stride, const int64_t* slots, void* kv_cache,
-                                uint8_t* kv_scales, int64_t num_pages, int32_t page_size,
-                                int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
-                                int32_t kv_layout, int32_t kv_format, float k_scale, float v_scale,
-                                pod_dtype dtype, int32_t* status, void* stream);
+pod_status pod_norm_rope_append(const pod_io_args* args, void* stream);
 
 /*
- * pod_gather_kv — read cache rows back: out [rows, 2, Hk, head_dim] (K, then V)
- * in dtype, value = code * scale rounded to nearest, finite values saturating
- * at the type's largest; a padding row reads as zeros. `out` is also an NHD
- * cache of page size 1 (pages 0 .. rows-1), so the 16-bit prefill half can run
- * over an FP8 cache's context.
+ * pod_gather_kv — read cache rows back: k_out [rows, 2, Hk, head_dim] (K, then
+ * V, contiguous) in dtype, value = code * scale rounded to nearest, finite
+ * values saturating at the type's largest; a padding row reads as zeros. The
+ * result is also an NHD cache of page size 1 (pages 0 .. rows-1), so the 16-bit
+ * prefill half can run over an FP8 cache's context.
  */
-pod_status pod_gather_kv(const void* kv_cache, const uint8_t* kv_scales, int64_t num_pages,
-                         int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
-                         int32_t kv_layout, int32_t kv_format, float k_scale, float v_scale,
-                         const int64_t* slots, int64_t rows, pod_dtype dtype, void* out,
-                         int32_t* status, void* stream);
+pod_status pod_gather_kv(const pod_io_args* args, void* stream);
 
 /* ------------------------------------------------------------------------
  * Attention of drafted token trees over a paged cache (verification of drafted

@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -102,19 +103,9 @@ def load_library(path: Optional[str] = None):
     lib.pod_replan.restype = ctypes.c_int
     lib.pod_replan.argtypes = [V, V, V, V, V, I32, V, V, V, V, I32, V]
     I64, F32 = ctypes.c_int64, ctypes.c_float
-    lib.pod_qk_norm_rope.restype = ctypes.c_int
-    lib.pod_qk_norm_rope.argtypes = [V, V, I64, I64, I64, I32, I32, I32, V, V, F32, V, I32, I32, F32,
-                                     F32, ctypes.c_int, V, V, I64, I64, V]
-    lib.pod_append_kv.restype = ctypes.c_int
-    lib.pod_append_kv.argtypes = [V, V, I64, I64, I64, V, V, V, I64, I32, I32, I32, I32, I32, F32, F32,
-                                  ctypes.c_int, V, V]
-    lib.pod_norm_rope_append.restype = ctypes.c_int
-    lib.pod_norm_rope_append.argtypes = [V, V, V, I64, I64, I64, I64, V, V, F32, V, I32, I32, F32, F32,
-                                         V, I64, V, V, V, I64, I32, I32, I32, I32, I32, I32, F32, F32,
-                                         ctypes.c_int, V, V]
-    lib.pod_gather_kv.restype = ctypes.c_int
-    lib.pod_gather_kv.argtypes = [V, V, I64, I32, I32, I32, I32, I32, F32, F32, V, I64, ctypes.c_int,
-                                  V, V, V]
+    for fn in (lib.pod_qk_norm_rope, lib.pod_append_kv, lib.pod_norm_rope_append, lib.pod_gather_kv):
+        fn.restype = ctypes.c_int
+        fn.argtypes = [ctypes.c_char_p, V]
     lib.pod_tree_plan.restype = ctypes.c_int
     lib.pod_tree_plan.argtypes = [V, V, V, V, I32, I32, I32, I32, I32, I32, F32, ctypes.c_int, I32, F32, F32,
                                   I32, I32, I32, V, SZ, V, ctypes.POINTER(V), ctypes.POINTER(SZ)]
@@ -518,8 +509,8 @@ def _on_device(name, t, dev, dtype, ndim):
 
 def _heads(name, t, dtype, dev, rows=None):
     """[rows, heads, d] with contiguous heads; returns (rows, heads, d, row stride)."""
-    if t.dim() != 3 or t.dtype != dtype or t.device != dev or not t.is_cuda:
-        raise PodError(1, f"{name} must be a [rows, heads, head_dim] {dtype} CUDA tensor on {dev}")
+    if t.dim() != 3 or t.dtype != dtype or t.device != dev:
+        raise PodError(1, f"{name} must be a [rows, heads, head_dim] {dtype} tensor on {dev}")
     n, h, d = t.shape
     sn, sh, sd = t.stride()
     if (sd != 1 and d > 1) or (sh != d and h > 1):
@@ -529,32 +520,27 @@ def _heads(name, t, dtype, dev, rows=None):
     return n, h, d, sn if n > 1 else max(sn, h * d) // 8 * 8
 
 
-def _weight(name, w, d, dtype, dev):
-    if w is None:
-        return None
-    _on_device(name, w, dev, dtype, 1)
-    if w.numel() != d:
-        raise PodError(1, f"{name} must have head_dim elements")
-    return w.data_ptr()
+def _vector(name, t, n, dtype, dev):
+    """Pointer of a contiguous [n] tensor."""
+    if t.dtype != dtype or t.device != dev or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise PodError(1, f"{name} must be a contiguous {dtype} tensor of {n} elements on {dev}")
+    return t.data_ptr()
 
 
-def _positions(positions, rows, rotary_dim, dev):
+def _rotation(positions, rows, rotary_dim, d, dev):
+    """(positions pointer, rotary_dim)."""
+    R = d if rotary_dim is None else int(rotary_dim)
     if positions is None:
-        if rotary_dim:
+        if R:
             raise PodError(1, "the rotation needs positions")
-        return None
-    import torch
-    _on_device("positions", positions, dev, torch.int32, 1)
-    if positions.numel() != rows:
-        raise PodError(1, f"positions has {positions.numel()} rows, not {rows}")
-    return positions.data_ptr()
+        return 0, R
+    return _vector("positions", positions, rows, _torch().int32, dev), R
 
 
 def _status(status, dev):
     if status is None:
-        return None
-    import torch
-    if status.dtype != torch.int32 or status.device != dev or status.numel() < 1:
+        return 0
+    if status.dtype != _torch().int32 or status.device != dev or status.numel() < 1:
         raise PodError(1, f"status must be an int32 tensor on {dev}")
     return status.data_ptr()
 
@@ -565,53 +551,63 @@ _KV_FORMATS = {"16bit": 0, "scaled": 1, "block": 2}
 def _cache_args(kv_cache, kv_scales, kv_layout, dtype, dev):
     """(cache pointer, scales pointer, pages, page size, Hk, d, layout, format)
     of a paged cache: 16-bit, or E4M3 codes with or without scale bytes."""
-    import torch
-    if kv_layout not in _LAYOUTS:
+    hnd = _LAYOUTS.get(kv_layout)
+    if hnd is None:
         raise PodError(1, f"unknown kv layout {kv_layout!r}")
-    hnd = _LAYOUTS[kv_layout]
-    if (kv_cache.dim() != 5 or kv_cache.shape[1] != 2 or kv_cache.device != dev
-            or not kv_cache.is_contiguous()):
+    shape, kt = kv_cache.shape, kv_cache.dtype
+    if len(shape) != 5 or shape[1] != 2 or kv_cache.device != dev or not kv_cache.is_contiguous():
         raise PodError(1, f"kv_cache must be a contiguous [pages, 2, ...] page pool on {dev}")
-    pages, _, a, b, d = kv_cache.shape
+    pages, _, a, b, d = shape
     ps, hk = (b, a) if hnd else (a, b)
-    if kv_cache.dtype == dtype:
+    if kt == dtype:
         fmt = 0
-    elif kv_cache.dtype == torch.float8_e4m3fn:
+    elif kt == _torch().float8_e4m3fn:
         fmt = 1 if kv_scales is None else 2
     else:
-        raise PodError(2, f"kv_cache must be {dtype} or float8_e4m3fn, not {kv_cache.dtype}")
+        raise PodError(2, f"kv_cache must be {dtype} or float8_e4m3fn, not {kt}")
+    sp = 0
     if kv_scales is not None:
         if fmt == 0:
             raise PodError(1, "kv_scales given, but the cache is a 16-bit one")
-        if (kv_scales.dtype != torch.uint8 or kv_scales.device != dev
-                or kv_scales.shape != kv_cache.shape[:4] or not kv_scales.is_contiguous()):
-            raise PodError(1, f"kv_scales must be contiguous uint8 {tuple(kv_cache.shape[:4])} on {dev}")
-    return (kv_cache.data_ptr(), None if kv_scales is None else kv_scales.data_ptr(), pages, ps, hk, d,
-            hnd, fmt)
+        if (kv_scales.dtype != _torch().uint8 or kv_scales.device != dev or kv_scales.shape != shape[:4]
+                or not kv_scales.is_contiguous()):
+            raise PodError(1, f"kv_scales must be contiguous uint8 {tuple(shape[:4])} on {dev}")
+        sp = kv_scales.data_ptr()
+    return kv_cache.data_ptr(), sp, pages, ps, hk, d, hnd, fmt
 
 
-class _Launch:
-    """The tensors' device made current (where it is not), and the stream: the
-    given one, or torch's current stream of that device."""
-    __slots__ = ("dev", "prev", "stream")
+_torch_module = None
 
-    def __init__(self, dev, stream):
-        self.dev, self.prev, self.stream = dev, None, stream
 
-    def __enter__(self):
+def _torch():
+    global _torch_module
+    if _torch_module is None:
         import torch
-        now = torch.cuda.current_device()
-        if now != self.dev.index:
-            self.prev = now
-            torch.cuda.set_device(self.dev)
-        if self.stream is None:
-            return torch.cuda.current_stream(self.dev).cuda_stream
-        return self.stream if isinstance(self.stream, int) else self.stream.cuda_stream
+        _torch_module = torch
+    return _torch_module
 
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            import torch
-            torch.cuda.set_device(self.prev)
+
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream) with the tensors' device current (it is made so where
+    it is not) and, without a given stream, torch's current stream of that
+    device. Small calls take as long as their host side, so the usual case asks
+    torch as little as it can."""
+    torch = _torch()
+    index = dev.index
+    if stream is None:
+        try:
+            s = torch._C._cuda_getCurrentRawStream(index)
+        except AttributeError:
+            s = torch.cuda.current_stream(dev).cuda_stream
+    else:
+        s = stream if isinstance(stream, int) else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        code = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, s)
+    if code != POD_OK:
+        raise PodError(code, pod_last_error())
 
 
 def _device_of(t):
@@ -620,15 +616,18 @@ def _device_of(t):
     return t.device
 
 
-def _out_rows(name, out, shape, dtype, dev):
+def _out_rows(name, out, rows, heads, d, dtype, dev):
     """An output [rows, heads, d]: a new tensor, or the caller's with its row stride."""
     if out is None:
-        import torch
-        return torch.empty(shape, dtype=dtype, device=dev), shape[1] * shape[2]
-    n, h, d, stride = _heads(name, out, dtype, dev, shape[0])
-    if (h, d) != (shape[1], shape[2]):
-        raise PodError(1, f"{name} must be {tuple(shape)}")
+        return _torch().empty((rows, heads, d), dtype=dtype, device=dev), heads * d
+    n, h, dd, stride = _heads(name, out, dtype, dev, rows)
+    if (h, dd) != (heads, d):
+        raise PodError(1, f"{name} must be {(rows, heads, d)}")
     return out, stride
+
+
+# struct pod_io_args: 12 pointers, 7 int64, 9 int32, 5 floats
+_IO_ARGS = struct.Struct("@12Q7q9i5f")
 
 
 def pod_qk_norm_rope(q, k, positions=None, *, q_weight=None, k_weight=None, eps=1e-6, rotary_dim=None,
@@ -640,31 +639,40 @@ def pod_qk_norm_rope(q, k, positions=None, *, q_weight=None, k_weight=None, eps=
     slices of a fused projection (any row stride that is a multiple of 8);
     either may be None. Returns (q_out, k_out); pass q_out=q, k_out=k to work
     in place."""
-    lib = load_library()
+    lib = _lib or load_library()
     t = q if q is not None else k
     dev, dtype = _device_of(t), t.dtype
     code = _dtype_code(dtype)
-    rows, H, d, qs = (0, 0, 0, 0) if q is None else _heads("q", q, dtype, dev)
+    H = Hk = qs = ks = qos = kos = qp = kp = qop = kop = 0
+    if q is not None:
+        rows, H, d, qs = _heads("q", q, dtype, dev)
+        q_out, qos = _out_rows("q_out", q_out, rows, H, d, dtype, dev)
+        qp, qop = q.data_ptr(), q_out.data_ptr()
     if k is not None:
         rows, Hk, dk, ks = _heads("k", k, dtype, dev, None if q is None else rows)
         if q is not None and dk != d:
             raise PodError(1, "q and k have different head_dim")
         d = dk
-    else:
-        Hk, ks = 0, 0
-    R = d if rotary_dim is None else int(rotary_dim)
-    pos = _positions(positions, rows, R, dev)
-    wq, wk = _weight("q_weight", q_weight, d, dtype, dev), _weight("k_weight", k_weight, d, dtype, dev)
-    qos = kos = 0
-    if q is not None:
-        q_out, qos = _out_rows("q_out", q_out, (rows, H, d), dtype, dev)
-    if k is not None:
-        k_out, kos = _out_rows("k_out", k_out, (rows, Hk, d), dtype, dev)
-    with _Launch(dev, stream) as st:
-        _check(lib.pod_qk_norm_rope(_ptr(q), _ptr(k), qs, ks, rows, H, Hk, d, wq, wk, float(eps), pos, R,
-                                    int(bool(interleaved)), float(rope_scale), float(rope_theta), code,
-                                    _ptr(q_out) if H else None, _ptr(k_out) if Hk else None, qos, kos, st))
+        k_out, kos = _out_rows("k_out", k_out, rows, Hk, d, dtype, dev)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    pos, R = _rotation(positions, rows, rotary_dim, d, dev)
+    wq = 0 if q_weight is None else _vector("q_weight", q_weight, d, dtype, dev)
+    wk = 0 if k_weight is None else _vector("k_weight", k_weight, d, dtype, dev)
+    _call(lib.pod_qk_norm_rope, dev, stream, _IO_ARGS.pack(
+        qp, kp, 0, wq, wk, pos, 0, qop, kop, 0, 0, 0, qs, ks, 0, qos, kos, rows, 0, 0, H, Hk, d, 0, 0, code, R,
+        bool(interleaved), eps, rope_scale, rope_theta, 1.0, 1.0))
     return (q_out if q is not None else None), (k_out if k is not None else None)
+
+
+def _written(k, v, kv_cache, kv_scales, kv_layout, slots):
+    """Checks of the rows of a write: (device, dtype, rows, k stride, v stride, slots pointer, cache args)."""
+    dev, dtype = _device_of(k), k.dtype
+    rows, hk, d, ks = _heads("k", k, dtype, dev)
+    _, hv, dv, vs = _heads("v", v, dtype, dev, rows)
+    cache = _cache_args(kv_cache, kv_scales, kv_layout, dtype, dev)
+    if hv != hk or dv != d or cache[4] != hk or cache[5] != d:
+        raise PodError(1, "k, v and kv_cache differ in heads or head_dim")
+    return dev, dtype, rows, ks, vs, _vector("slots", slots, rows, _torch().int64, dev), cache
 
 
 def pod_append_kv(k, v, kv_cache, slots, *, kv_scales=None, k_scale=1.0, v_scale=1.0, kv_layout="NHD",
@@ -674,22 +682,12 @@ def pod_append_kv(k, v, kv_cache, slots, *, kv_scales=None, k_scale=1.0, v_scale
     codes, with the per-tensor k_scale and v_scale or, where ``kv_scales``
     (uint8, the cache's shape without head_dim) is given, a power-of-two scale
     per token and KV head. Negative slots are skipped."""
-    lib = load_library()
-    dev, dtype = _device_of(k), k.dtype
-    code = _dtype_code(dtype)
-    rows, Hk, d, ks = _heads("k", k, dtype, dev)
-    _, hv, dv, vs = _heads("v", v, dtype, dev, rows)
-    cache, scales, pages, ps, hc, dc, hnd, fmt = _cache_args(kv_cache, kv_scales, kv_layout, dtype, dev)
-    if (hv, dv) != (Hk, d) or (hc, dc) != (Hk, d):
-        raise PodError(1, "k, v and kv_cache differ in heads or head_dim")
-    import torch
-    _on_device("slots", slots, dev, torch.int64, 1)
-    if slots.numel() != rows:
-        raise PodError(1, f"slots has {slots.numel()} rows, not {rows}")
-    with _Launch(dev, stream) as st:
-        _check(lib.pod_append_kv(k.data_ptr(), v.data_ptr(), ks, vs, rows, slots.data_ptr(), cache, scales,
-                                 pages, ps, Hk, d, hnd, fmt, float(k_scale), float(v_scale), code,
-                                 _status(status, dev), st))
+    lib = _lib or load_library()
+    dev, dtype, rows, ks, vs, sl, (cache, scales, pages, ps, hk, d, hnd, fmt) = \
+        _written(k, v, kv_cache, kv_scales, kv_layout, slots)
+    _call(lib.pod_append_kv, dev, stream, _IO_ARGS.pack(
+        0, k.data_ptr(), v.data_ptr(), 0, 0, 0, sl, 0, 0, cache, scales, _status(status, dev), 0, ks, vs, 0, 0,
+        rows, pages, ps, 0, hk, d, hnd, fmt, _dtype_code(dtype), 0, 0, 0.0, 1.0, 1.0, k_scale, v_scale))
 
 
 def pod_norm_rope_append(q, k, v, positions, kv_cache, slots, *, q_weight=None, k_weight=None, eps=1e-6,
@@ -699,31 +697,23 @@ def pod_norm_rope_append(q, k, v, positions, kv_cache, slots, *, q_weight=None, 
     """pod_qk_norm_rope and pod_append_kv in one pass: returns q normed and
     rotated (None without q), writes k (normed and rotated) and v into the
     cache."""
-    lib = load_library()
-    dev, dtype = _device_of(k), k.dtype
-    code = _dtype_code(dtype)
-    rows, Hk, d, ks = _heads("k", k, dtype, dev)
-    _, hv, dv, vs = _heads("v", v, dtype, dev, rows)
-    _, H, dq, qs = (rows, 0, d, 0) if q is None else _heads("q", q, dtype, dev, rows)
-    cache, scales, pages, ps, hc, dc, hnd, fmt = _cache_args(kv_cache, kv_scales, kv_layout, dtype, dev)
-    if (hv, dv) != (Hk, d) or (hc, dc) != (Hk, d) or dq != d:
-        raise PodError(1, "q, k, v and kv_cache differ in heads or head_dim")
-    import torch
-    _on_device("slots", slots, dev, torch.int64, 1)
-    if slots.numel() != rows:
-        raise PodError(1, f"slots has {slots.numel()} rows, not {rows}")
-    R = d if rotary_dim is None else int(rotary_dim)
-    pos = _positions(positions, rows, R, dev)
-    wq, wk = _weight("q_weight", q_weight, d, dtype, dev), _weight("k_weight", k_weight, d, dtype, dev)
-    qos = 0
+    lib = _lib or load_library()
+    dev, dtype, rows, ks, vs, sl, (cache, scales, pages, ps, hk, d, hnd, fmt) = \
+        _written(k, v, kv_cache, kv_scales, kv_layout, slots)
+    H = qs = qos = qp = qop = 0
     if q is not None:
-        q_out, qos = _out_rows("q_out", q_out, (rows, H, d), dtype, dev)
-    with _Launch(dev, stream) as st:
-        _check(lib.pod_norm_rope_append(
-            _ptr(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, rows, wq, wk, float(eps), pos, R,
-            int(bool(interleaved)), float(rope_scale), float(rope_theta), _ptr(q_out) if H else None, qos,
-            slots.data_ptr(), cache, scales, pages, ps, H, Hk, d, hnd, fmt, float(k_scale), float(v_scale),
-            code, _status(status, dev), st))
+        _, H, dq, qs = _heads("q", q, dtype, dev, rows)
+        if dq != d:
+            raise PodError(1, "q and k have different head_dim")
+        q_out, qos = _out_rows("q_out", q_out, rows, H, d, dtype, dev)
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    pos, R = _rotation(positions, rows, rotary_dim, d, dev)
+    wq = 0 if q_weight is None else _vector("q_weight", q_weight, d, dtype, dev)
+    wk = 0 if k_weight is None else _vector("k_weight", k_weight, d, dtype, dev)
+    _call(lib.pod_norm_rope_append, dev, stream, _IO_ARGS.pack(
+        qp, k.data_ptr(), v.data_ptr(), wq, wk, pos, sl, qop, 0, cache, scales, _status(status, dev), qs, ks, vs,
+        qos, 0, rows, pages, ps, H, hk, d, hnd, fmt, _dtype_code(dtype), R, bool(interleaved), eps, rope_scale,
+        rope_theta, k_scale, v_scale))
     return q_out if q is not None else None
 
 
@@ -732,22 +722,22 @@ def pod_gather_kv(kv_cache, slots, *, dtype, kv_scales=None, k_scale=1.0, v_scal
     """Cache rows of the int64 ``slots`` back as ``dtype`` values:
     [rows, 2, Hk, d], K then V; a negative slot reads as zeros. The result
     viewed as [rows, 2, 1, Hk, d] is an NHD cache of page size 1."""
-    import torch
-    lib = load_library()
+    lib = _lib or load_library()
+    torch = _torch()
     dev = _device_of(kv_cache)
     code = _dtype_code(dtype)
-    cache, scales, pages, ps, Hk, d, hnd, fmt = _cache_args(kv_cache, kv_scales, kv_layout, dtype, dev)
-    _on_device("slots", slots, dev, torch.int64, 1)
-    rows = slots.numel()
+    cache, scales, pages, ps, hk, d, hnd, fmt = _cache_args(kv_cache, kv_scales, kv_layout, dtype, dev)
+    rows = slots.shape[0] if slots.dim() == 1 else -1
+    sl = _vector("slots", slots, rows, torch.int64, dev)
     if out is None:
-        out = torch.empty((rows, 2, Hk, d), dtype=dtype, device=dev)
+        out = torch.empty((rows, 2, hk, d), dtype=dtype, device=dev)
     else:
         _on_device("out", out, dev, dtype, 4)
-        if tuple(out.shape) != (rows, 2, Hk, d):
-            raise PodError(1, f"out must be {(rows, 2, Hk, d)}")
-    with _Launch(dev, stream) as st:
-        _check(lib.pod_gather_kv(cache, scales, pages, ps, Hk, d, hnd, fmt, float(k_scale), float(v_scale),
-                                 slots.data_ptr(), rows, code, out.data_ptr(), _status(status, dev), st))
+        if tuple(out.shape) != (rows, 2, hk, d):
+            raise PodError(1, f"out must be {(rows, 2, hk, d)}")
+    _call(lib.pod_gather_kv, dev, stream, _IO_ARGS.pack(
+        0, 0, 0, 0, 0, 0, sl, 0, out.data_ptr(), cache, scales, _status(status, dev), 0, 0, 0, 0, 0, rows, pages, ps,
+        0, hk, d, hnd, fmt, code, 0, 0, 0.0, 1.0, 1.0, k_scale, v_scale))
     return out
 
 
@@ -768,6 +758,7 @@ class PodTreeHandle:
     kv_layout: int
     mask_bytes: int
     has_sinks: bool
+    pool_shape: tuple = ()
     workspace_ptr: Optional[int] = None
 
     def __del__(self):
@@ -813,7 +804,9 @@ def pod_tree_plan(q_indptr, kv_indptr, kv_indices, last_page_len, num_qo_heads, 
                          page_size=int(page_size), num_pages=int(num_pages), dtype=dtype,
                          kv_format=_KV_FORMATS[kv_format], kv_layout=_LAYOUTS[kv_layout],
                          mask_bytes=int((int((n * n).sum()) + 7) // 8), has_sinks=bool(has_sinks),
-                         workspace_ptr=ws_ptr)
+                         pool_shape=(int(num_pages), 2) + ((int(num_kv_heads), int(page_size)) if _LAYOUTS[kv_layout]
+                                                           else (int(page_size), int(num_kv_heads)))
+                         + (int(head_dim),), workspace_ptr=ws_ptr)
 
 
 def pod_tree_workspace_size(h: PodTreeHandle) -> int:
@@ -821,9 +814,8 @@ def pod_tree_workspace_size(h: PodTreeHandle) -> int:
 
 
 def pod_tree_bind_workspace(h: PodTreeHandle, workspace, stream=None):
-    with _Launch(_device_of(workspace), stream) as st:
-        _check(load_library().pod_tree_bind_workspace(ctypes.c_void_p(h.ptr), workspace.data_ptr(),
-                                                      workspace.numel() * workspace.element_size(), st))
+    _call(load_library().pod_tree_bind_workspace, _device_of(workspace), stream, h.ptr, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
     h.workspace_ptr = workspace.data_ptr()
 
 
@@ -832,56 +824,51 @@ def pod_tree_run(h: PodTreeHandle, q, kv, workspace, tree_mask=None, kv_scales=N
     """Attention of the planned trees: q [rows, H, d], kv the paged cache,
     ``tree_mask`` uint8 bits (little bit order) of every request's [n, n]
     matrix end to end (None: chains). Returns (out, lse), lse in base 2."""
-    import torch
-    lib = load_library()
-    dev = _device_of(q)
-    H, d = h.num_qo_heads, h.head_dim
-    shape = (h.rows, H, d)
-    _on_device("q", q, dev, h.dtype, 3)
-    if tuple(q.shape) != shape:
-        raise PodError(1, f"q must be {shape}")
-    inner = (h.num_kv_heads, h.page_size) if h.kv_layout else (h.page_size, h.num_kv_heads)
-    _on_device("kv", kv, dev, h.dtype if h.kv_format == 0 else torch.float8_e4m3fn, 5)
-    if tuple(kv.shape) != (h.num_pages, 2) + inner + (d,):
-        raise PodError(1, f"kv must be {(h.num_pages, 2) + inner + (d,)}")
+    lib = _lib or load_library()
+    torch = _torch()
+    dev, dtype = _device_of(q), h.dtype
+    shape, pool = (h.rows, h.num_qo_heads, h.head_dim), h.pool_shape
+    if q.shape != shape or q.dtype != dtype or not q.is_contiguous():
+        raise PodError(1, f"q must be contiguous {dtype} {shape}")
+    if kv.shape != pool or kv.dtype != (torch.float8_e4m3fn if h.kv_format else dtype) or kv.device != dev \
+            or not kv.is_contiguous():
+        raise PodError(1, f"kv must be a contiguous {pool} cache of the plan's format on {dev}")
+    sp = mp = mn = kp = 0
     if kv_scales is not None:
-        _on_device("kv_scales", kv_scales, dev, torch.uint8, 4)
-        if tuple(kv_scales.shape) != (h.num_pages, 2) + inner:
-            raise PodError(1, f"kv_scales must be {(h.num_pages, 2) + inner}")
+        if kv_scales.shape != pool[:4] or kv_scales.dtype != torch.uint8 or kv_scales.device != dev \
+                or not kv_scales.is_contiguous():
+            raise PodError(1, f"kv_scales must be contiguous uint8 {pool[:4]} on {dev}")
+        sp = kv_scales.data_ptr()
     if tree_mask is not None:
-        _on_device("tree_mask", tree_mask, dev, torch.uint8, 1)
+        mn = tree_mask.numel()
+        mp = _vector("tree_mask", tree_mask, mn, torch.uint8, dev)
+        if mp == 0 and mn == 0 and h.mask_bytes:
+            raise PodError(1, f"tree_mask needs {h.mask_bytes} bytes")
     if sinks is not None:
-        _on_device("sinks", sinks, dev, torch.float32, 1)
-        if sinks.numel() != H:
-            raise PodError(1, f"sinks must have {H} elements")
+        kp = _vector("sinks", sinks, h.num_qo_heads, torch.float32, dev)
     if workspace.device != dev:
         raise PodError(1, f"the workspace must be on {dev}")
     if out is None:
-        out = torch.empty(shape, dtype=h.dtype, device=dev)
-    else:
-        _on_device("out", out, dev, h.dtype, 3)
-        if tuple(out.shape) != shape:
-            raise PodError(1, f"out must be {shape}")
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    elif out.shape != shape or out.dtype != dtype or out.device != dev or not out.is_contiguous():
+        raise PodError(1, f"out must be contiguous {dtype} {shape} on {dev}")
     if lse is None:
         lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
-    else:
-        _on_device("lse", lse, dev, torch.float32, 2)
-        if tuple(lse.shape) != shape[:2]:
-            raise PodError(1, f"lse must be {shape[:2]}")
-    with _Launch(dev, stream) as st:
-        _check(lib.pod_tree_run(ctypes.c_void_p(h.ptr), q.data_ptr(), kv.data_ptr(), _ptr(kv_scales), _ptr(tree_mask),
-                                0 if tree_mask is None else tree_mask.numel(), _ptr(sinks), workspace.data_ptr(),
-                                out.data_ptr(), lse.data_ptr(), st))
+    elif lse.shape != shape[:2] or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
+        raise PodError(1, f"lse must be contiguous float32 {shape[:2]} on {dev}")
+    _call(lib.pod_tree_run, dev, stream, h.ptr, q.data_ptr(), kv.data_ptr(), sp, mp, mn, kp, workspace.data_ptr(),
+          out.data_ptr(), lse.data_ptr())
     return out, lse
 
 
 def pod_tree_read_device_status(h: PodTreeHandle, workspace, stream=None) -> int:
     v = ctypes.c_int32(0)
-    with _Launch(_device_of(workspace), stream) as st:
-        code = load_library().pod_tree_read_device_status(ctypes.c_void_p(h.ptr), workspace.data_ptr(), st,
-                                                          ctypes.byref(v))
-    if code not in (POD_OK, 5):
-        _check(code)
+    try:
+        _call(lambda st: load_library().pod_tree_read_device_status(h.ptr, workspace.data_ptr(), st, ctypes.byref(v)),
+              _device_of(workspace), stream)
+    except PodError as e:
+        if e.code != 5:
+            raise
     return int(v.value)
 
 

@@ -457,14 +457,6 @@ cudaError_t launch_read(IoParams& P, int fmt, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-pod_status check_common(int64_t rows, int head_dim, pod_dtype dtype) {
-  if (rows < 0 || rows > 0x7fffffff) return fail(POD_ERR_INVALID_ARG, "rows must be in [0, 2^31)");
-  if (dtype != POD_F16 && dtype != POD_BF16) return fail(POD_ERR_UNSUPPORTED, "dtype must be fp16 or bf16");
-  if (head_dim != 64 && head_dim != 128 && head_dim != 256)
-    return fail(POD_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256");
-  return POD_OK;
-}
-
 pod_status check_rows(const char* what, const void* p, int64_t stride, int64_t heads, int d) {
   if (!p) return fail(POD_ERR_INVALID_ARG, std::string(what) + " is NULL");
   if (!aligned16(p)) return fail(POD_ERR_INVALID_ARG, std::string(what) + " must be 16-byte aligned");
@@ -475,41 +467,88 @@ pod_status check_rows(const char* what, const void* p, int64_t stride, int64_t h
   return POD_OK;
 }
 
-pod_status check_cache(const void* cache, const void* scales, int64_t num_pages, int page_size,
-                       int Hk, int layout, int fmt, float k_scale, float v_scale) {
+pod_status check_common(const pod_io_args& a) {
+  if (a.rows < 0 || a.rows > 0x7fffffff) return fail(POD_ERR_INVALID_ARG, "rows must be in [0, 2^31)");
+  if (a.dtype != POD_F16 && a.dtype != POD_BF16) return fail(POD_ERR_UNSUPPORTED, "dtype must be fp16 or bf16");
+  if (a.head_dim != 64 && a.head_dim != 128 && a.head_dim != 256)
+    return fail(POD_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256");
+  return POD_OK;
+}
+
+// norm and rotation: settings, q, weights
+pod_status check_rope(const pod_io_args& a) {
+  const int R = a.rotary_dim;
+  if (a.num_qo_heads < 0 || a.num_qo_heads > 65536) return fail(POD_ERR_INVALID_ARG, "no heads, or too many");
+  if (R < 0 || R > a.head_dim || R % 16 != 0)
+    return fail(POD_ERR_INVALID_ARG, "rotary_dim must be a multiple of 16 in [0, head_dim]");
+  if (R && a.rows && !a.positions) return fail(POD_ERR_INVALID_ARG, "positions is NULL");
+  if (R && !(a.rope_scale > 0.f && a.rope_theta > 0.f && isfinite(a.rope_scale) && isfinite(a.rope_theta)))
+    return fail(POD_ERR_INVALID_ARG, "rope_scale and rope_theta must be finite and positive");
+  if (!(a.eps >= 0.f) || !isfinite(a.eps)) return fail(POD_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (a.rows && a.num_qo_heads) {
+    pod_status st = check_rows("q", a.q, a.q_stride, a.num_qo_heads, a.head_dim);
+    if (st == POD_OK) st = check_rows("q_out", a.q_out, a.q_out_stride, a.num_qo_heads, a.head_dim);
+    if (st != POD_OK) return st;
+  }
+  if (!aligned16(a.q_weight) || !aligned16(a.k_weight))
+    return fail(POD_ERR_INVALID_ARG, "the norm weights must be 16-byte aligned");
+  return POD_OK;
+}
+
+pod_status check_cache(const pod_io_args& a) {
+  const int fmt = a.kv_format;
   if (fmt != FMT_16 && fmt != FMT_SCALED && fmt != FMT_BLOCK)
     return fail(POD_ERR_INVALID_ARG, "unknown cache format");
-  if (layout != 0 && layout != 1) return fail(POD_ERR_INVALID_ARG, "kv_layout must be 0 (NHD) or 1 (HND)");
-  if (Hk < 1 || Hk > 4096) return fail(POD_ERR_INVALID_ARG, "num_kv_heads must be in [1, 4096]");
-  if (page_size < 1 || num_pages < 1) return fail(POD_ERR_INVALID_ARG, "the page pool is empty");
+  if (a.kv_layout != 0 && a.kv_layout != 1) return fail(POD_ERR_INVALID_ARG, "kv_layout must be 0 (NHD) or 1 (HND)");
+  if (a.num_kv_heads < 1 || a.num_kv_heads > 4096) return fail(POD_ERR_INVALID_ARG, "num_kv_heads must be in [1, 4096]");
+  if (a.page_size < 1 || a.num_pages < 1) return fail(POD_ERR_INVALID_ARG, "the page pool is empty");
   // (the element offset of the pool's end has to fit 63 bits)
-  if (num_pages > (1ll << 50) / ((int64_t)page_size * Hk))
+  if (a.num_pages > (1ll << 50) / ((int64_t)a.page_size * a.num_kv_heads))
     return fail(POD_ERR_INVALID_ARG, "the page pool is too large");
-  if (!cache || !aligned16(cache)) return fail(POD_ERR_INVALID_ARG, "the cache must be a 16-byte aligned pointer");
-  if (fmt == FMT_BLOCK && !scales) return fail(POD_ERR_INVALID_ARG, "a block-scaled cache needs its scales");
-  if (fmt != FMT_BLOCK && scales) return fail(POD_ERR_INVALID_ARG, "scales given, but the cache format has none");
-  if (fmt == FMT_SCALED &&
-      !(k_scale > 0.f && v_scale > 0.f && isfinite(k_scale) && isfinite(v_scale)))
+  if (!a.kv_cache || !aligned16(a.kv_cache))
+    return fail(POD_ERR_INVALID_ARG, "the cache must be a 16-byte aligned pointer");
+  if (fmt == FMT_BLOCK && !a.kv_scales) return fail(POD_ERR_INVALID_ARG, "a block-scaled cache needs its scales");
+  if (fmt != FMT_BLOCK && a.kv_scales) return fail(POD_ERR_INVALID_ARG, "scales given, but the cache format has none");
+  if (fmt == FMT_SCALED && !(a.k_scale > 0.f && a.v_scale > 0.f && isfinite(a.k_scale) && isfinite(a.v_scale)))
     return fail(POD_ERR_INVALID_ARG, "k_scale and v_scale must be finite and positive");
   return POD_OK;
 }
 
-pod_status check_rope(int R, int d, float scale, float theta, float eps, bool have_pos) {
-  if (R < 0 || R > d || R % 16 != 0)
-    return fail(POD_ERR_INVALID_ARG, "rotary_dim must be a multiple of 16 in [0, head_dim]");
-  if (R && !have_pos) return fail(POD_ERR_INVALID_ARG, "positions is NULL");
-  if (R && !(scale > 0.f && theta > 0.f && isfinite(scale) && isfinite(theta)))
-    return fail(POD_ERR_INVALID_ARG, "rope_scale and rope_theta must be finite and positive");
-  if (!(eps >= 0.f) || !isfinite(eps)) return fail(POD_ERR_INVALID_ARG, "eps must be finite and not negative");
-  return POD_OK;
+// the rows of a write
+pod_status check_written(const pod_io_args& a) {
+  if (!a.rows) return POD_OK;
+  if (!a.slots) return fail(POD_ERR_INVALID_ARG, "slots is NULL");
+  const pod_status st = check_rows("k", a.k, a.k_stride, a.num_kv_heads, a.head_dim);
+  return st != POD_OK ? st : check_rows("v", a.v, a.v_stride, a.num_kv_heads, a.head_dim);
 }
 
-pod_status run_io(IoParams& P, int d, int fmt, bool fused, float rope_scale, float rope_theta,
-                  pod_dtype dtype, void* stream, const char* what) {
+IoParams params_of(const pod_io_args& a, bool fused, bool cache) {
+  IoParams P = {};
+  P.rows = (int)a.rows;
+  P.k = a.k; P.k_stride = a.k_stride;
+  P.k_out = a.k_out; P.ko_stride = a.k_out_stride;
+  P.Hk = a.num_kv_heads; P.ps = 1;
+  if (fused) {
+    P.q = a.q; P.q_out = a.q_out; P.q_stride = a.q_stride; P.qo_stride = a.q_out_stride;
+    P.qw = a.q_weight; P.kw = a.k_weight; P.pos = a.positions;
+    P.H = a.num_qo_heads; P.R = a.rotary_dim; P.interleaved = a.interleaved != 0; P.eps = a.eps;
+  }
+  if (cache) {
+    P.v = a.v; P.v_stride = a.v_stride;
+    P.slots = a.slots; P.cache = a.kv_cache; P.scales = a.kv_scales; P.status = a.status;
+    P.num_slots = a.num_pages * a.page_size;
+    P.ps = a.page_size; P.hnd = a.kv_layout;
+    P.k_scale = a.k_scale; P.v_scale = a.v_scale;
+  }
+  return P;
+}
+
+pod_status run_io(IoParams& P, const pod_io_args& a, int fmt, bool fused, void* stream, const char* what) {
   if (P.rows == 0) return POD_OK;
-  const IoFreq& f = freq_of(fused ? P.R : 0, rope_scale, rope_theta);
-  cudaError_t e = dtype == POD_BF16 ? launch_d<__nv_bfloat16>(P, d, fmt, fused, f, (cudaStream_t)stream)
-                                    : launch_d<__half>(P, d, fmt, fused, f, (cudaStream_t)stream);
+  const IoFreq& f = freq_of(P.R, a.rope_scale, a.rope_theta);
+  cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t e = a.dtype == POD_BF16 ? launch_d<__nv_bfloat16>(P, a.head_dim, fmt, fused, f, st)
+                                            : launch_d<__half>(P, a.head_dim, fmt, fused, f, st);
   if (e != cudaSuccess) return fail(POD_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
   return POD_OK;
 }
@@ -524,129 +563,62 @@ pod_status run_io(IoParams& P, int d, int fmt, bool fused, float rope_scale, flo
 
 extern "C" {
 
-pod_status pod_qk_norm_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
-                            int64_t rows, int32_t num_qo_heads, int32_t num_kv_heads,
-                            int32_t head_dim, const void* q_weight, const void* k_weight, float eps,
-                            const int32_t* positions, int32_t rotary_dim, int32_t interleaved,
-                            float rope_scale, float rope_theta, pod_dtype dtype, void* q_out,
-                            void* k_out, int64_t q_out_stride, int64_t k_out_stride, void* stream) {
+pod_status pod_qk_norm_rope(const pod_io_args* a, void* stream) {
   pod_set_last_error("");
-  POD_TRY(check_common(rows, head_dim, dtype));
-  if (num_qo_heads < 0 || num_kv_heads < 0 || num_qo_heads + (int64_t)num_kv_heads < 1 ||
-      num_qo_heads > 65536 || num_kv_heads > 4096)
+  if (!a) return fail(POD_ERR_INVALID_ARG, "args is NULL");
+  POD_TRY(check_common(*a));
+  if (a->num_kv_heads < 0 || a->num_kv_heads > 4096 || a->num_qo_heads + (int64_t)a->num_kv_heads < 1)
     return fail(POD_ERR_INVALID_ARG, "no heads, or too many");
-  POD_TRY(check_rope(rotary_dim, head_dim, rope_scale, rope_theta, eps, rows == 0 || positions));
-  if (rows && num_qo_heads) {
-    POD_TRY(check_rows("q", q, q_stride, num_qo_heads, head_dim));
-    POD_TRY(check_rows("q_out", q_out, q_out_stride, num_qo_heads, head_dim));
+  POD_TRY(check_rope(*a));
+  if (a->rows && a->num_kv_heads) {
+    POD_TRY(check_rows("k", a->k, a->k_stride, a->num_kv_heads, a->head_dim));
+    POD_TRY(check_rows("k_out", a->k_out, a->k_out_stride, a->num_kv_heads, a->head_dim));
   }
-  if (rows && num_kv_heads) {
-    POD_TRY(check_rows("k", k, k_stride, num_kv_heads, head_dim));
-    POD_TRY(check_rows("k_out", k_out, k_out_stride, num_kv_heads, head_dim));
-  }
-  if (!aligned16(q_weight) || !aligned16(k_weight))
-    return fail(POD_ERR_INVALID_ARG, "the norm weights must be 16-byte aligned");
-  IoParams P = {};
-  P.q = q; P.k = k; P.q_out = q_out; P.k_out = k_out;
-  P.qw = q_weight; P.kw = k_weight; P.pos = positions;
-  P.q_stride = q_stride; P.k_stride = k_stride; P.qo_stride = q_out_stride; P.ko_stride = k_out_stride;
-  P.rows = (int)rows; P.H = num_qo_heads; P.Hk = num_kv_heads; P.ps = 1;
-  P.R = rotary_dim; P.interleaved = interleaved != 0; P.eps = eps;
-  return run_io(P, head_dim, FMT_NONE, true, rope_scale, rope_theta, dtype, stream, "norm and rotation launch");
+  IoParams P = params_of(*a, true, false);
+  return run_io(P, *a, FMT_NONE, true, stream, "norm and rotation launch");
 }
 
-pod_status pod_append_kv(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
-                         int64_t rows, const int64_t* slots, void* kv_cache, uint8_t* kv_scales,
-                         int64_t num_pages, int32_t page_size, int32_t num_kv_heads,
-                         int32_t head_dim, int32_t kv_layout, int32_t kv_format, float k_scale,
-                         float v_scale, pod_dtype dtype, int32_t* status, void* stream) {
+pod_status pod_append_kv(const pod_io_args* a, void* stream) {
   pod_set_last_error("");
-  POD_TRY(check_common(rows, head_dim, dtype));
-  POD_TRY(check_cache(kv_cache, kv_scales, num_pages, page_size, num_kv_heads, kv_layout, kv_format,
-                      k_scale, v_scale));
-  if (rows) {
-    if (!slots) return fail(POD_ERR_INVALID_ARG, "slots is NULL");
-    POD_TRY(check_rows("k", k, k_stride, num_kv_heads, head_dim));
-    POD_TRY(check_rows("v", v, v_stride, num_kv_heads, head_dim));
-  }
-  IoParams P = {};
-  P.k = k; P.v = v; P.slots = slots; P.cache = kv_cache; P.scales = kv_scales; P.status = status;
-  P.k_stride = k_stride; P.v_stride = v_stride;
-  P.num_slots = num_pages * page_size;
-  P.rows = (int)rows; P.Hk = num_kv_heads; P.ps = page_size; P.hnd = kv_layout;
-  P.k_scale = k_scale; P.v_scale = v_scale;
-  return run_io(P, head_dim, kv_format, false, 1.f, 1.f, dtype, stream, "cache write launch");
+  if (!a) return fail(POD_ERR_INVALID_ARG, "args is NULL");
+  POD_TRY(check_common(*a));
+  POD_TRY(check_cache(*a));
+  POD_TRY(check_written(*a));
+  IoParams P = params_of(*a, false, true);
+  return run_io(P, *a, a->kv_format, false, stream, "cache write launch");
 }
 
-pod_status pod_norm_rope_append(const void* q, const void* k, const void* v, int64_t q_stride,
-                                int64_t k_stride, int64_t v_stride, int64_t rows,
-                                const void* q_weight, const void* k_weight, float eps,
-                                const int32_t* positions, int32_t rotary_dim, int32_t interleaved,
-                                float rope_scale, float rope_theta, void* q_out,
-                                int64_t q_out_stride, const int64_t* slots, void* kv_cache,
-                                uint8_t* kv_scales, int64_t num_pages, int32_t page_size,
-                                int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
-                                int32_t kv_layout, int32_t kv_format, float k_scale, float v_scale,
-                                pod_dtype dtype, int32_t* status, void* stream) {
+pod_status pod_norm_rope_append(const pod_io_args* a, void* stream) {
   pod_set_last_error("");
-  POD_TRY(check_common(rows, head_dim, dtype));
-  POD_TRY(check_cache(kv_cache, kv_scales, num_pages, page_size, num_kv_heads, kv_layout, kv_format,
-                      k_scale, v_scale));
-  if (num_qo_heads < 0 || num_qo_heads > 65536) return fail(POD_ERR_INVALID_ARG, "num_qo_heads out of range");
-  POD_TRY(check_rope(rotary_dim, head_dim, rope_scale, rope_theta, eps, rows == 0 || positions));
-  if (rows) {
-    if (!slots) return fail(POD_ERR_INVALID_ARG, "slots is NULL");
-    if (num_qo_heads) {
-      POD_TRY(check_rows("q", q, q_stride, num_qo_heads, head_dim));
-      POD_TRY(check_rows("q_out", q_out, q_out_stride, num_qo_heads, head_dim));
-    }
-    POD_TRY(check_rows("k", k, k_stride, num_kv_heads, head_dim));
-    POD_TRY(check_rows("v", v, v_stride, num_kv_heads, head_dim));
-  }
-  if (!aligned16(q_weight) || !aligned16(k_weight))
-    return fail(POD_ERR_INVALID_ARG, "the norm weights must be 16-byte aligned");
-  IoParams P = {};
-  P.q = q; P.k = k; P.v = v; P.q_out = q_out;
-  P.qw = q_weight; P.kw = k_weight; P.pos = positions;
-  P.slots = slots; P.cache = kv_cache; P.scales = kv_scales; P.status = status;
-  P.q_stride = q_stride; P.k_stride = k_stride; P.v_stride = v_stride; P.qo_stride = q_out_stride;
-  P.num_slots = num_pages * page_size;
-  P.rows = (int)rows; P.H = num_qo_heads; P.Hk = num_kv_heads; P.ps = page_size; P.hnd = kv_layout;
-  P.R = rotary_dim; P.interleaved = interleaved != 0; P.eps = eps;
-  P.k_scale = k_scale; P.v_scale = v_scale;
-  return run_io(P, head_dim, kv_format, true, rope_scale, rope_theta, dtype, stream,
-                "norm, rotation and cache write launch");
+  if (!a) return fail(POD_ERR_INVALID_ARG, "args is NULL");
+  POD_TRY(check_common(*a));
+  POD_TRY(check_cache(*a));
+  POD_TRY(check_rope(*a));
+  POD_TRY(check_written(*a));
+  IoParams P = params_of(*a, true, true);
+  return run_io(P, *a, a->kv_format, true, stream, "norm, rotation and cache write launch");
 }
 
-pod_status pod_gather_kv(const void* kv_cache, const uint8_t* kv_scales, int64_t num_pages,
-                         int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
-                         int32_t kv_layout, int32_t kv_format, float k_scale, float v_scale,
-                         const int64_t* slots, int64_t rows, pod_dtype dtype, void* out,
-                         int32_t* status, void* stream) {
+pod_status pod_gather_kv(const pod_io_args* a, void* stream) {
   pod_set_last_error("");
-  POD_TRY(check_common(rows, head_dim, dtype));
-  POD_TRY(check_cache(kv_cache, kv_scales, num_pages, page_size, num_kv_heads, kv_layout, kv_format,
-                      k_scale, v_scale));
-  if (rows == 0) return POD_OK;
-  if (!slots) return fail(POD_ERR_INVALID_ARG, "slots is NULL");
-  POD_TRY(check_rows("out", out, 2ll * num_kv_heads * head_dim, 2ll * num_kv_heads, head_dim));
-  IoParams P = {};
-  P.cache = const_cast<void*>(kv_cache);
-  P.scales = const_cast<uint8_t*>(kv_scales);
-  P.slots = slots; P.status = status; P.k_out = out;
-  P.num_slots = num_pages * page_size;
-  P.rows = (int)rows; P.Hk = num_kv_heads; P.ps = page_size; P.hnd = kv_layout;
-  P.k_scale = k_scale; P.v_scale = v_scale;
+  if (!a) return fail(POD_ERR_INVALID_ARG, "args is NULL");
+  POD_TRY(check_common(*a));
+  POD_TRY(check_cache(*a));
+  if (a->rows == 0) return POD_OK;
+  if (!a->slots) return fail(POD_ERR_INVALID_ARG, "slots is NULL");
+  POD_TRY(check_rows("k_out", a->k_out, 2ll * a->num_kv_heads * a->head_dim, 2ll * a->num_kv_heads, a->head_dim));
+  IoParams P = params_of(*a, false, true);
   cudaStream_t st = (cudaStream_t)stream;
+  const int fmt = a->kv_format, d = a->head_dim;
   cudaError_t e;
-  if (dtype == POD_BF16)
-    e = head_dim == 64 ? launch_read<__nv_bfloat16, 64>(P, kv_format, st)
-        : head_dim == 128 ? launch_read<__nv_bfloat16, 128>(P, kv_format, st)
-                          : launch_read<__nv_bfloat16, 256>(P, kv_format, st);
+  if (a->dtype == POD_BF16)
+    e = d == 64 ? launch_read<__nv_bfloat16, 64>(P, fmt, st)
+        : d == 128 ? launch_read<__nv_bfloat16, 128>(P, fmt, st)
+                   : launch_read<__nv_bfloat16, 256>(P, fmt, st);
   else
-    e = head_dim == 64 ? launch_read<__half, 64>(P, kv_format, st)
-        : head_dim == 128 ? launch_read<__half, 128>(P, kv_format, st)
-                          : launch_read<__half, 256>(P, kv_format, st);
+    e = d == 64 ? launch_read<__half, 64>(P, fmt, st)
+        : d == 128 ? launch_read<__half, 128>(P, fmt, st)
+                   : launch_read<__half, 256>(P, fmt, st);
   if (e != cudaSuccess) return fail(POD_ERR_CUDA, std::string("cache read launch: ") + cudaGetErrorString(e));
   return POD_OK;
 }

@@ -8,8 +8,8 @@ rsqrtf (2 ulp), and cos / sin from an angle that is off by at most 2^-25 half
 turns (float) + pos * 2^-53 turns, under 2^-21 radians at |pos| < 2^31. Together
 below 2^-17 of the row's largest value.
 """
-import ctypes
 import math
+import struct
 
 import numpy as np
 import pytest
@@ -455,13 +455,22 @@ def _err(code, want, text):
     assert code == want and text in pod.pod_last_error(), (code, pod.pod_last_error())
 
 
+FIELDS = ("q", "k", "v", "qw", "kw", "pos", "slots", "qo", "ko", "kv", "sc", "st", "qs", "ks", "vs", "qos", "kos",
+          "rows", "pages", "ps", "H", "Hk", "d", "lay", "fmt", "dt", "R", "il", "eps", "rs", "th", "k_scale", "v_scale")
+
+
+def io_call(name, a, kw):
+    """The C entry point with pod_io_args packed field by field (its documented order)."""
+    a = {**dict.fromkeys(FIELDS, 0), "dt": 1, "rs": 1.0, "th": 1e4, "k_scale": 1.0, "v_scale": 1.0, **a, **kw}
+    assert len(a) == len(FIELDS)
+    kinds = "Q" * 12 + "q" * 7 + "i" * 9 + "f" * 5
+    packed = struct.pack("@" + kinds, *[0 if a[f] is None else a[f] for f in FIELDS])
+    return getattr(pod.load_library(), name)(packed, None)
+
+
 def norm_call(**kw):
-    a = dict(q=P, k=P, qs=1024, ks=256, rows=4, H=8, Hk=2, d=128, qw=P, kw=P, eps=1e-6, pos=P, R=128, il=0,
-             rs=1.0, th=1e4, dt=1, qo=P, ko=P, qos=1024, kos=256)
-    a.update(kw)
-    return pod.load_library().pod_qk_norm_rope(*[a[n] for n in (
-        "q", "k", "qs", "ks", "rows", "H", "Hk", "d", "qw", "kw", "eps", "pos", "R", "il", "rs", "th", "dt",
-        "qo", "ko", "qos", "kos")], None)
+    return io_call("pod_qk_norm_rope", dict(q=P, k=P, qs=1024, ks=256, rows=4, H=8, Hk=2, d=128, qw=P, kw=P, eps=1e-6,
+                                            pos=P, R=128, qo=P, ko=P, qos=1024, kos=256), kw)
 
 
 @pytest.mark.parametrize("kw,code,text", [
@@ -481,22 +490,20 @@ def test_no_rows_need_no_tensors():
     assert norm_call(rows=0, q=None, k=None, qo=None, ko=None, pos=None) == 0
 
 
+CACHE = dict(kv=P, pages=10, ps=16, Hk=2, d=128, slots=P, rows=4)
+
+
 def append_call(**kw):
-    a = dict(k=P, v=P, ks=256, vs=256, rows=4, slots=P, kv=P, sc=None, pages=10, ps=16, Hk=2, d=128, lay=0,
-             fmt=0, k_scale=1.0, v_scale=1.0, dt=1)
-    a.update(kw)
-    return pod.load_library().pod_append_kv(*[a[n] for n in (
-        "k", "v", "ks", "vs", "rows", "slots", "kv", "sc", "pages", "ps", "Hk", "d", "lay", "fmt", "k_scale",
-        "v_scale", "dt")], None, None)
+    return io_call("pod_append_kv", dict(CACHE, k=P, v=P, ks=256, vs=256), kw)
+
+
+def fused_call(**kw):
+    return io_call("pod_norm_rope_append", dict(CACHE, k=P, v=P, ks=256, vs=256, q=P, qo=P, qs=1024, qos=1024, H=8,
+                                                pos=P, R=128, eps=1e-6), kw)
 
 
 def gather_call(**kw):
-    a = dict(kv=P, sc=None, pages=10, ps=16, Hk=2, d=128, lay=0, fmt=0, k_scale=1.0, v_scale=1.0, slots=P,
-             rows=4, dt=1, out=P)
-    a.update(kw)
-    return pod.load_library().pod_gather_kv(*[a[n] for n in (
-        "kv", "sc", "pages", "ps", "Hk", "d", "lay", "fmt", "k_scale", "v_scale", "slots", "rows", "dt",
-        "out")], None, None)
+    return io_call("pod_gather_kv", dict(CACHE, ko=P), kw)
 
 
 CACHE_REFUSALS = [
@@ -512,6 +519,7 @@ CACHE_REFUSALS = [
 @pytest.mark.parametrize("kw,code,text", CACHE_REFUSALS)
 def test_cache_refusals(kw, code, text):
     _err(append_call(**kw), code, text)
+    _err(fused_call(**kw), code, text)
     _err(gather_call(**kw), code, text)
 
 
@@ -519,11 +527,24 @@ def test_cache_refusals(kw, code, text):
     (dict(k=None), "k is NULL"), (dict(v=P + 4), "v must be"), (dict(ks=128), "row stride")])
 def test_append_refusals(kw, text):
     _err(append_call(**kw), 1, text)
+    _err(fused_call(**kw), 1, text)
+
+
+@pytest.mark.parametrize("kw,text", [
+    (dict(q=None), "q is NULL"), (dict(qo=P + 8), "q_out must"), (dict(R=40), "rotary_dim"), (dict(pos=None), "positions"),
+    (dict(kw=P + 2), "weights"), (dict(H=-1), "heads"), (dict(eps=math.inf), "eps")])
+def test_fused_refusals(kw, text):
+    _err(fused_call(**kw), 1, text)
+
+
+def test_no_arguments():
+    for name in ("pod_qk_norm_rope", "pod_append_kv", "pod_norm_rope_append", "pod_gather_kv"):
+        _err(getattr(pod.load_library(), name)(None, None), 1, "args is NULL")
 
 
 def test_gather_refuses_a_missing_output():
-    _err(gather_call(out=None), 1, "out is NULL")
-    assert gather_call(rows=0, out=None, slots=None) == 0 and append_call(rows=0, k=None, v=None, slots=None) == 0
+    _err(gather_call(ko=None), 1, "k_out is NULL")
+    assert gather_call(rows=0, ko=None, slots=None) == 0 and append_call(rows=0, k=None, v=None, slots=None) == 0
 
 
 def test_binding_refuses_host_tensors():
