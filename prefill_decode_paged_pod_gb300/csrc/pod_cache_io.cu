@@ -19,11 +19,23 @@
 // against the exact quotient amax / 448 (at most one of its 17 binades), the
 // product with it is exact, and it is stored in one byte (exponent + 127).
 //
-// Work split. A head row is read by d/8 lanes with one 16-byte load each; the
-// lane groups of a block walk the (token, head) tasks of a few tokens, four
-// loads in flight a thread. The rotation's partner elements come by shuffle,
-// cos and sin from a table that the block computes once per token. All of it
-// is bound by HBM for long calls and by the launch for short ones.
+// Work split. A head row is read by d/16 lanes with two 16-byte loads each. Where
+// the halves of the head are paired, a lane takes the 16-byte chunks c and
+// c + R/16, so it holds both elements of its 8 pairs; the chunks past the rotated
+// part go two neighbours to a lane. A block works on queries, keys or values
+// only: some heads of some tokens, two head rows in flight a lane group, the
+// first of them asked for before the block makes its tables (cos and sin once
+// per token, the norm weights) in shared memory. fp32 arithmetic is paired
+// (f32x2). A first form held one 16-byte chunk a lane and turned pairs by
+// shuffles: 230 instructions per 8 elements, and bound by them (below, in
+// brackets).
+//
+// Measured on a GB300, back to back in a graph, with the share of the measured
+// copy rate: norm and rotation of 8796 rows of 64/8 heads of 128, bf16: 57 us,
+// 85 % (84); 4096 rows of 64/8 heads normed, turned and written: 29.7 us, 85 %
+// (45); 16384 rows of 8 heads written with block scales: 18.4 us, 82 % (26.6);
+// 65536 rows read back: 64 us, 95 %. Calls of a few hundred rows take 3.5 to 5
+// us, the launch and two dependent trips to memory.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <string.h>
@@ -40,8 +52,9 @@ using namespace pod;
 namespace {
 
 constexpr int kIoThreads = 256;
-constexpr int kMaxTok = 8;        // tokens per block
-constexpr int kUnroll = 4;        // head rows in flight per lane group
+constexpr int kMaxTok = 16;       // tokens per block
+constexpr int kUnroll = 4;        // cache rows in flight per lane group (read)
+constexpr int kTasks = 2;         // head rows in flight per lane group (write)
 constexpr int kStatusSlot = 4;    // status bit: a slot outside the pool
 
 enum { FMT_NONE = -1, FMT_16 = POD_KV_16BIT, FMT_SCALED = POD_KV_E4M3, FMT_BLOCK = POD_KV_E4M3_BLOCK };
@@ -58,8 +71,14 @@ struct IoParams {
   long long q_stride, k_stride, v_stride, qo_stride, ko_stride;   // elements per token
   long long num_slots;
   int rows, H, Hk, ps, hnd, R, interleaved;
-  int tok, heads_per_block;
+  // how each kind of row (queries, keys, values; reads: keys then values) is cut
+  // into blocks: tokens and heads of a block, head ranges per token group, first
+  // block of the grid
+  struct Cut {
+    int tok, heads, ranges, first;
+  } cut[3];
   float eps, k_scale, v_scale;
+  float k_inv, v_inv;            // reciprocals, rounded to nearest; 0: divide
 };
 struct IoFreq {
   uint64_t f[128];
@@ -77,7 +96,7 @@ POD_DEV SlotMap slot_steps(int ps, int Hk, int D, int hnd) {
   return m;
 }
 POD_DEV long long slot_base(long long slot, int ps, int Hk, int D, int hnd) {
-  const long long page = slot / ps;
+  const long long page = (ps & (ps - 1)) == 0 ? slot >> (__ffs(ps) - 1) : slot / ps;
   const int in = (int)(slot - page * ps);
   return (page * 2 * ps * Hk + (hnd ? (long long)in : (long long)in * Hk)) * D;
 }
@@ -99,203 +118,302 @@ POD_DEV float scale_of(int byte) {
 }
 
 template <typename T>
-POD_DEV void unpack8(const uint4& r, float* x) {
-  const uint32_t u[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = Pack<T>::unpack(u[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
-}
-template <typename T>
 POD_DEV uint4 pack8(const float* x) {
   return make_uint4(Pack<T>::two(x[0], x[1]), Pack<T>::two(x[2], x[3]), Pack<T>::two(x[4], x[5]),
                     Pack<T>::two(x[6], x[7]));
 }
-POD_DEV uint2 codes8(const float* x) {
-  return make_uint2(f32x2_to_e4m3x2(x[0], x[1]) | (f32x2_to_e4m3x2(x[2], x[3]) << 16),
-                    f32x2_to_e4m3x2(x[4], x[5]) | (f32x2_to_e4m3x2(x[6], x[7]) << 16));
+// 8 values of a 16-byte chunk as 4 fp32 pairs, and back
+template <typename T>
+POD_DEV void unpack8(const uint4& r, uint64_t* x) {
+  const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = Pack<T>::unpack(u[i]);
+    x[i] = pack2(f.x, f.y);
+  }
+}
+template <typename T>
+POD_DEV uint4 pack8(const uint64_t* x) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unpack2(x[i], a, b);
+    u[i] = Pack<T>::two(a, b);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+POD_DEV uint2 codes8(const uint64_t* x) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    unpack2(x[i], a, b);
+    u[i] = f32x2_to_e4m3x2(a, b);
+  }
+  return make_uint2(u[0] | (u[1] << 16), u[2] | (u[3] << 16));
 }
 
-// One pass over q, k and (with a cache) v. FUSED: norm and rotation of q and
-// k; without it the rows are only written.
-template <typename T, int D, int FMT, bool FUSED>
-__global__ void __launch_bounds__(kIoThreads) cache_io_kernel(const __grid_constant__ IoParams P,
-                                                              const __grid_constant__ IoFreq F) {
-  constexpr int LPR = D / 8;                     // lanes per head row
-  constexpr int NG = kIoThreads / LPR;           // head rows per pass of the block
-  constexpr bool CACHE = FMT != FMT_NONE;
-  __shared__ float4 cs[FUSED ? kMaxTok * D / 4 : 1];
-  __shared__ long long base[kMaxTok];
-  const int tid = threadIdx.x, lane = tid % LPR;
-  const int tok0 = blockIdx.x * P.tok, ntok = min(P.tok, P.rows - tok0);
-  const int half = P.R >> 1;
+// x / s rounded to nearest, from y = 1 / s rounded to nearest (Markstein: q = x y
+// is within an ulp of the quotient, and q + (x - q s) y rounds it correctly).
+// Quotients past 2^100, where the remainder may overflow, stay as q: they
+// saturate either way. The host gives y = 0 for scales whose products could leave
+// the normal range: then divide.
+POD_DEV uint64_t div2(uint64_t x, float s, float y) {
+  float a, b;
+  if (y == 0.f) {
+    unpack2(x, a, b);
+    return pack2(__fdiv_rn(a, s), __fdiv_rn(b, s));
+  }
+  const uint64_t y2 = pack2(y, y), q = mul2(x, y2);
+  const uint64_t r = fma2(fma2(q, pack2(-s, -s), x), y2, q);
+  float qa, qb;
+  unpack2(q, qa, qb);
+  unpack2(r, a, b);
+  return pack2(fabsf(qa) < 1.2676506002282294e30f ? a : qa, fabsf(qb) < 1.2676506002282294e30f ? b : qb);
+}
 
+enum { IO_Q, IO_K, IO_V, IO_KV };
+
+// The tables of a block: cos and sin of its tokens, and the norm weights. Chunked so that the lanes of a head row read neighbouring 16 bytes.
+template <int D>
+struct IoTables {
+  float4 cs[kMaxTok * D / 4];    // [token][4 (2 interleaved, per chunk)][lane]: c, c', s, s'
+  float4 w[4][D / 16];           // [quarter of a lane's 16 elements][lane]
+};
+
+// The block's tokens: where their rows go, and cos and sin of their positions.
+template <typename T, int D, bool CACHE, bool TURN>
+POD_DEV void io_tables(const IoParams& P, const IoFreq& F, IoTables<TURN ? D : 16>& S, long long* base, int tok0,
+                       int ntok, const T* weight, bool report) {
+  const int tid = threadIdx.x;
   if (CACHE && tid < ntok) {
     const long long s = P.slots[tok0 + tid];
     long long b = -1;
     if (s >= 0 && s < P.num_slots) b = slot_base(s, P.ps, P.Hk, D, P.hnd);
-    else if (s >= P.num_slots && P.status && blockIdx.y == 0) atomicOr(P.status, kStatusSlot);
+    else if (s >= P.num_slots && P.status && report) atomicOr(P.status, kStatusSlot);
     base[tid] = b;
   }
-  if (FUSED) {
-    // (cos, sin) of pair j of a token, stored so that the lanes of a head row
-    // read neighbouring 16-byte chunks: chunk c of lane l holds its pairs 2c, 2c+1
-    float2* t2 = reinterpret_cast<float2*>(cs);
-    const int per = P.interleaved ? 4 : 8;       // pairs a lane reads
-    const int nl = P.R ? half / per : 1;         // lanes that hold distinct pairs
+  if constexpr (TURN) {
+    const int half = P.R >> 1, turning = P.R >> 4;
+    float* cs = reinterpret_cast<float*>(S.cs);
     for (int i = tid; i < ntok * half; i += kIoThreads) {
       const int t = i / half, j = i - t * half;
       const uint64_t ph = (uint64_t)(int64_t)P.pos[tok0 + t] * F.f[j];
       const float fr = (float)(int32_t)(ph >> 32) * 4.656612873077393e-10f;   // half turns: 2^-31
       float sn, c;
       sincospif(fr, &sn, &c);
-      const int l = j / per, i8 = j - l * per;
-      t2[t * half + ((i8 >> 1) * nl + l) * 2 + (i8 & 1)] = make_float2(c, sn);
+      // a lane's 8 pairs: j = 8 lane + 0..7 in either pairing
+      const int l = j >> 3, i8 = j & 7;
+      float* at = cs + 4 * (t * (half / 2) + (i8 >> 1) * turning + l) + (i8 & 1);
+      at[0] = c;
+      at[2] = sn;
+    }
+    if (weight && tid < D) {
+      // element e lies in chunk e / 8: which lane takes it, and as which of its 16?
+      const int e = tid, c = e >> 3;
+      int l = c >> 1, second = c & 1;
+      if (!P.interleaved && c < 2 * turning) {
+        second = c >= turning;
+        l = second ? c - turning : c;
+      }
+      const int k = second * 8 + (e & 7);
+      reinterpret_cast<float*>(&S.w[k >> 2][l])[k & 3] = (float)weight[e];
     }
   }
-  if (CACHE || FUSED) __syncthreads();
+}
 
-  const int HT = P.H + P.Hk + (CACHE ? P.Hk : 0);
-  const int h0 = blockIdx.y * P.heads_per_block, nh = min(P.heads_per_block, HT - h0);
-  const int n = ntok * nh;
-  const T* __restrict__ q = static_cast<const T*>(P.q);
-  const T* __restrict__ k = static_cast<const T*>(P.k);
-  const T* __restrict__ v = static_cast<const T*>(P.v);
+// One block's tasks: some heads of one kind (IO_KV: K heads, then V heads) for
+// some tokens. The rows of the first tasks are asked for before the tables are
+// made.
+template <typename T, int D, int FMT, int KIND, bool FUSED>
+POD_DEV void io_pass(const IoParams& P, const IoFreq& F, const IoParams::Cut& cut) {
+  constexpr int LPR = D / 16, NG = kIoThreads / LPR;
+  constexpr bool TURN = FUSED && (KIND == IO_Q || KIND == IO_K);
+  constexpr bool TO_CACHE = FMT != FMT_NONE && KIND != IO_Q;
+  __shared__ IoTables<TURN ? D : 16> S;
+  __shared__ long long base[kMaxTok];            // cache offset of the tokens' slots, -1: none
+  const int blk = (int)blockIdx.x - cut.first, group = blk / cut.ranges;
+  const int heads = KIND == IO_Q ? P.H : KIND == IO_KV ? 2 * P.Hk : P.Hk;
+  const int tok0 = group * cut.tok, ntok = min(cut.tok, P.rows - tok0);
+  const int h0 = (blk - group * cut.ranges) * cut.heads, h1 = min(h0 + cut.heads, heads);
+  const int nh = h1 - h0, n = ntok * nh;
+  const int lane = threadIdx.x % LPR;
+  const int half = P.R >> 1, turning = P.R >> 4;           // lanes that turn pairs
+  // this lane's two chunks
+  const bool turns = FUSED && lane < turning;
+  const bool split = turns && !P.interleaved;
+  const int ca = split ? lane : 2 * lane, cb = split ? lane + turning : 2 * lane + 1;
   const SlotMap sm = slot_steps(P.ps, P.Hk, D, P.hnd);
-  const int e0 = lane * 8;
-
-  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-  if (FUSED) {
-    if (P.qw) wq = *reinterpret_cast<const uint4*>(static_cast<const T*>(P.qw) + e0);
-    if (P.kw) wk = *reinterpret_cast<const uint4*>(static_cast<const T*>(P.kw) + e0);
-  }
-  // a task index advances by NG: (token, head) advance by these steps
+  const T* weight = static_cast<const T*>(KIND == IO_Q ? P.qw : P.kw);
   const int dt = NG / nh, dh = NG - dt * nh;
-  int idx = tid / LPR, t = idx / nh, h = idx - t * nh;
-  for (int first = 0; first < n; first += NG * kUnroll) {
-    uint4 raw[kUnroll];
-    int tk[kUnroll], hd[kUnroll];
+  int idx = threadIdx.x / LPR, t = idx / nh, h = idx - t * nh;
+  for (int first = 0; first < n; first += NG * kTasks) {
+    uint4 ra[kTasks], rb[kTasks];
+    int tk[kTasks], hd[kTasks];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      raw[u] = make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < kTasks; ++u) {
+      ra[u] = rb[u] = make_uint4(0, 0, 0, 0);
       tk[u] = -1;
       hd[u] = h0 + h;
       if (idx < n) {
         tk[u] = t;
         const long long r = tok0 + t;
         const int hh = h0 + h;
-        const T* src = hh < P.H ? q + r * P.q_stride + hh * D
-                       : hh < P.H + P.Hk ? k + r * P.k_stride + (hh - P.H) * D
-                                         : v + r * P.v_stride + (hh - P.H - P.Hk) * D;
-        raw[u] = __ldcs(reinterpret_cast<const uint4*>(src + e0));   // read once
+        const T* src;
+        if constexpr (KIND == IO_Q) src = static_cast<const T*>(P.q) + r * P.q_stride + hh * D;
+        else if constexpr (KIND == IO_K) src = static_cast<const T*>(P.k) + r * P.k_stride + hh * D;
+        else if constexpr (KIND == IO_V) src = static_cast<const T*>(P.v) + r * P.v_stride + hh * D;
+        else
+          src = hh < P.Hk ? static_cast<const T*>(P.k) + r * P.k_stride + hh * D
+                          : static_cast<const T*>(P.v) + r * P.v_stride + (hh - P.Hk) * D;
+        ra[u] = __ldcs(reinterpret_cast<const uint4*>(src) + ca);       // read once
+        rb[u] = __ldcs(reinterpret_cast<const uint4*>(src) + cb);
       }
       idx += NG;
       t += dt;
       h += dh;
       if (h >= nh) { h -= nh; ++t; }
     }
+    if (first == 0) {
+      io_tables<T, D, TO_CACHE, TURN>(P, F, S, base, tok0, ntok, weight, h0 == 0 && KIND != IO_V);
+      __syncthreads();
+    }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (first + u * NG >= n) break;            // (uniform over the block)
+    for (int u = 0; u < kTasks; ++u) {
+      if (first + u * NG >= n) break;                      // (uniform over the block)
       const bool live = tk[u] >= 0;
-      const int hh = hd[u];
-      const bool is_q = hh < P.H, is_k = !is_q && hh < P.H + P.Hk;
-      float x[8];
-      unpack8<T>(raw[u], x);
-      if (FUSED) {
-        // the shuffles run for every row of the warp, their results are used
-        // by the q and k rows
-        const bool norm = is_q ? P.qw != nullptr : (is_k && P.kw != nullptr);
-        float ss = 0.f;
+      constexpr bool COPY = FMT == FMT_16 && !TURN;        // values go as they are
+      uint64_t x[8];                                       // 4 pairs of chunk a, 4 of chunk b
+      if constexpr (!COPY) {
+        unpack8<T>(ra[u], x);
+        unpack8<T>(rb[u], x + 4);
+      }
+      if constexpr (TURN) {
+        if (weight) {
+          uint64_t q2 = mul2(x[0], x[0]), q3 = mul2(x[1], x[1]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+          for (int i = 2; i < 8; i += 2) {
+            q2 = fma2(x[i], x[i], q2);
+            q3 = fma2(x[i + 1], x[i + 1], q3);
+          }
+          float a, b;
+          unpack2(add2(q2, q3), a, b);
+          float ss = a + b;
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, LPR);
-        if (norm) {
+          for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, LPR);
           const float rs = rsqrtf(ss * (1.f / D) + P.eps);
-          float w[8];
-          unpack8<T>(is_q ? wq : wk, w);
+          const uint64_t rs2 = pack2(rs, rs);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = x[i] * rs * w[i];
+          for (int i = 0; i < 4; ++i) {
+            const float4 w = S.w[i][lane];
+            x[2 * i] = mul2(mul2(x[2 * i], rs2), pack2(w.x, w.y));
+            x[2 * i + 1] = mul2(mul2(x[2 * i + 1], rs2), pack2(w.z, w.w));
+          }
         }
-        if (P.R) {
-          const bool rot = (is_q || is_k) && live && e0 < P.R;
-          const float4* tc = cs + (live ? tk[u] : 0) * (half / 2);
-          if (P.interleaved) {
-            if (rot) {
-              const int nl = half / 4;
+        if (turns) {
+          const float4* tc = S.cs + (live ? tk[u] : 0) * (half / 2);
+          if (split) {
+            // pairs (chunk a, chunk b), element by element
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const float4 a = tc[c * nl + lane];
-                const float x0 = x[4 * c], x1 = x[4 * c + 1], x2 = x[4 * c + 2], x3 = x[4 * c + 3];
-                x[4 * c] = x0 * a.x - x1 * a.y;
-                x[4 * c + 1] = x1 * a.x + x0 * a.y;
-                x[4 * c + 2] = x2 * a.z - x3 * a.w;
-                x[4 * c + 3] = x3 * a.z + x2 * a.w;
-              }
+            for (int i = 0; i < 4; ++i) {
+              const float4 c = tc[i * turning + lane];
+              const uint64_t c2 = pack2(c.x, c.y), s2 = pack2(c.z, c.w), n2 = pack2(-c.z, -c.w);
+              const uint64_t a = x[i], b = x[4 + i];
+              x[i] = fma2(a, c2, mul2(b, n2));
+              x[4 + i] = fma2(b, c2, mul2(a, s2));
             }
           } else {
-            const int nl = half / 8;             // lanes in the first half of the pairs
-            const bool low = lane < nl;
-            const int partner = rot ? (low ? lane + nl : lane - nl) : lane;
-            float y[8];
+            // neighbouring elements
 #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], partner, LPR);
-            if (rot) {
-              const int l = low ? lane : lane - nl;
-              const float sg = low ? -1.f : 1.f;
+            for (int i = 0; i < 4; ++i) {
+              const float4 c = tc[i * turning + lane];
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const float4 a = tc[c * nl + l];
-                x[2 * c] = fmaf(x[2 * c], a.x, sg * y[2 * c] * a.y);
-                x[2 * c + 1] = fmaf(x[2 * c + 1], a.z, sg * y[2 * c + 1] * a.w);
+              for (int k = 0; k < 2; ++k) {
+                float a, b;
+                unpack2(x[2 * i + k], a, b);
+                const float cc = k ? c.y : c.x, ss = k ? c.w : c.z;
+                x[2 * i + k] = pack2(fmaf(a, cc, -b * ss), fmaf(b, cc, a * ss));
               }
             }
           }
         }
       }
       int ebyte = 0;
-      if (FMT == FMT_BLOCK) {
+      if constexpr (TO_CACHE && FMT == FMT_BLOCK) {
         float am = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) am = fmaxf(am, fabsf(x[i]));
+        for (int i = 0; i < 8; ++i) {
+          float a, b;
+          unpack2(x[i], a, b);
+          am = fmaxf(am, fmaxf(fabsf(a), fabsf(b)));
+        }
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o, LPR));
         ebyte = block_exp(am);
       }
       if (!live) continue;
       const long long r = tok0 + tk[u];
-      if (is_q) {
-        *reinterpret_cast<uint4*>(static_cast<T*>(P.q_out) + r * P.qo_stride + hh * D + e0) = pack8<T>(x);
-      } else if (!CACHE) {
-        *reinterpret_cast<uint4*>(static_cast<T*>(P.k_out) + r * P.ko_stride + (hh - P.H) * D + e0) =
-            pack8<T>(x);
+      if constexpr (!TO_CACHE) {
+        T* dst = KIND == IO_Q ? static_cast<T*>(P.q_out) + r * P.qo_stride + hd[u] * D
+                              : static_cast<T*>(P.k_out) + r * P.ko_stride + hd[u] * D;
+        reinterpret_cast<uint4*>(dst)[ca] = pack8<T>(x);
+        reinterpret_cast<uint4*>(dst)[cb] = pack8<T>(x + 4);
       } else {
         const long long b = base[tk[u]];
-        if (b >= 0) {
-          const int hk = is_k ? hh - P.H : hh - P.H - P.Hk;
-          const long long off = b + hk * sm.head + (is_k ? 0 : sm.half);
-          if (FMT == FMT_16) {
-            *reinterpret_cast<uint4*>(static_cast<T*>(P.cache) + off + e0) =
-                FUSED && is_k ? pack8<T>(x) : raw[u];
+        if (b < 0) continue;
+        const bool is_v = KIND == IO_V || (KIND == IO_KV && hd[u] >= P.Hk);
+        const int hk = KIND == IO_KV && is_v ? hd[u] - P.Hk : hd[u];
+        const long long off = b + hk * sm.head + (is_v ? sm.half : 0);
+        if constexpr (FMT == FMT_16) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(P.cache) + off);
+          if constexpr (COPY) {
+            dst[ca] = ra[u];
+            dst[cb] = rb[u];
           } else {
-            if (FMT == FMT_SCALED) {
-              const float s = is_k ? P.k_scale : P.v_scale;
+            dst[ca] = pack8<T>(x);
+            dst[cb] = pack8<T>(x + 4);
+          }
+        } else {
+          if constexpr (FMT == FMT_SCALED) {
+            const float s = is_v ? P.v_scale : P.k_scale, y = is_v ? P.v_inv : P.k_inv;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) x[i] = __fdiv_rn(x[i], s);
-            } else {
-              const float s = inv_scale_of(ebyte);
+            for (int i = 0; i < 8; ++i) x[i] = div2(x[i], s, y);
+          } else {
+            const float s = inv_scale_of(ebyte);
+            const uint64_t s2 = pack2(s, s);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) x[i] *= s;
-              if (lane == 0) P.scales[off / D] = (uint8_t)ebyte;
-            }
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(P.cache) + off + e0) = codes8(x);
+            for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], s2);
+            if (lane == 0) P.scales[off / D] = (uint8_t)ebyte;
+          }
+          const uint2 qa = codes8(x), qb = codes8(x + 4);
+          uint8_t* dst = static_cast<uint8_t*>(P.cache) + off;
+          if (split) {
+            *reinterpret_cast<uint2*>(dst + 8 * ca) = qa;
+            *reinterpret_cast<uint2*>(dst + 8 * cb) = qb;
+          } else {
+            *reinterpret_cast<uint4*>(dst + 8 * ca) = make_uint4(qa.x, qa.y, qb.x, qb.y);
           }
         }
       }
     }
+  }
+}
+
+// One launch over q, k and (with a cache) v; a block works on one of them.
+// FUSED: norm and rotation of q and k; without it the rows are only written.
+template <typename T, int D, int FMT, bool FUSED>
+__global__ void __launch_bounds__(kIoThreads) cache_io_kernel(const __grid_constant__ IoParams P,
+                                                              const __grid_constant__ IoFreq F) {
+  if constexpr (FUSED) {
+    if ((int)blockIdx.x < P.cut[1].first)
+      io_pass<T, D, FMT, IO_Q, true>(P, F, P.cut[0]);
+    else if (FMT == FMT_NONE || (int)blockIdx.x < P.cut[2].first)
+      io_pass<T, D, FMT, IO_K, true>(P, F, P.cut[1]);
+    else
+      io_pass<T, D, FMT == FMT_NONE ? FMT_16 : FMT, IO_V, true>(P, F, P.cut[2]);
+  } else {
+    io_pass<T, D, FMT, IO_KV, false>(P, F, P.cut[0]);
   }
 }
 
@@ -303,23 +421,24 @@ __global__ void __launch_bounds__(kIoThreads) cache_io_kernel(const __grid_const
 // bytes of cache: 16 codes, or 8 values of a 16-bit cache. Finite values past
 // the largest of T saturate. A negative slot gives a row of zeros.
 template <typename T, int D, int FMT>
-__global__ void __launch_bounds__(kIoThreads) cache_read_kernel(const __grid_constant__ IoParams P) {
+__global__ void __launch_bounds__(kIoThreads, 4) cache_read_kernel(const __grid_constant__ IoParams P) {
   constexpr int EPL = FMT == FMT_16 ? 8 : 16;    // elements per lane
   constexpr int LPR = D / EPL, NG = kIoThreads / LPR;
   __shared__ long long base[kMaxTok];
   const int tid = threadIdx.x, lane = tid % LPR, e0 = lane * EPL;
-  const int tok0 = blockIdx.x * P.tok, ntok = min(P.tok, P.rows - tok0);
+  const IoParams::Cut& cut = P.cut[0];
+  const int group = (int)blockIdx.x / cut.ranges, h0 = ((int)blockIdx.x - group * cut.ranges) * cut.heads;
+  const int tok0 = group * cut.tok, ntok = min(cut.tok, P.rows - tok0);
   if (tid < ntok) {
     const long long s = P.slots[tok0 + tid];
     long long b = -1;
     if (s >= 0 && s < P.num_slots) b = slot_base(s, P.ps, P.Hk, D, P.hnd);
-    else if (s >= P.num_slots && P.status && blockIdx.y == 0) atomicOr(P.status, kStatusSlot);
+    else if (s >= P.num_slots && P.status && h0 == 0) atomicOr(P.status, kStatusSlot);
     base[tid] = b;
   }
   __syncthreads();
   const int HT = 2 * P.Hk;
-  const int h0 = blockIdx.y * P.heads_per_block, nh = min(P.heads_per_block, HT - h0);
-  const int n = ntok * nh;
+  const int nh = min(cut.heads, HT - h0), n = ntok * nh;
   const SlotMap sm = slot_steps(P.ps, P.Hk, D, P.hnd);
   const int dt = NG / nh, dh = NG - dt * nh;
   int idx = tid / LPR, t = idx / nh, h = idx - t * nh;
@@ -382,21 +501,27 @@ pod_status fail(pod_status code, const std::string& msg) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Tokens per block and heads per block: a block should have a few head rows
-// for each lane group, and a short call should still reach every SM.
-void shape_of(IoParams& P, int heads, int ng, dim3* grid) {
-  const long long total = (long long)P.rows * heads;
-  const long long want = 152 * 4;                             // blocks that fill the GPU
-  long long per = (total + want - 1) / want;                  // head rows per block
-  per = per < ng ? ng : per > ng * 16 ? ng * 16 : per;
-  int tok = (int)(per / heads);
+// How `heads` rows a token are cut into blocks of about `tasks` head rows: whole
+// tokens, or a range of one token's heads. Returns the number of blocks.
+long long cut_of(IoParams::Cut& c, long long first, int rows, int heads, long long tasks) {
+  if (tasks < 1) tasks = 1;
+  long long tok = tasks / heads;
   tok = tok < 1 ? 1 : tok > kMaxTok ? kMaxTok : tok;
-  int split = 1;
-  if (tok == 1) split = (int)((heads + per - 1) / per);
-  P.tok = tok;
-  P.heads_per_block = (heads + split - 1) / split;
-  *grid = dim3((unsigned)((P.rows + tok - 1) / tok),
-               (unsigned)((heads + P.heads_per_block - 1) / P.heads_per_block));
+  const long long ranges = heads > tasks ? (heads + tasks - 1) / tasks : 1;
+  c.tok = (int)tok;
+  c.heads = (int)((heads + ranges - 1) / ranges);
+  c.ranges = (heads + c.heads - 1) / c.heads;
+  c.first = (int)first;
+  return (rows + tok - 1) / tok * c.ranges;
+}
+
+// Head rows of a block: one round of its lane groups for short calls, so that
+// every SM gets some, up to `most` where that still leaves several blocks per SM
+// (the tables of a block then serve more rows).
+long long tasks_of(const IoParams& P, long long heads, int round, int most) {
+  const long long total = (long long)P.rows * heads, wave = 152 * 4;
+  long long t = (total + wave - 1) / wave;
+  return t < round ? round : t > most * round ? most * round : t;
 }
 
 // Frequencies in turns as 64-bit fractions. They depend on the rotation's
@@ -424,11 +549,23 @@ const IoFreq& freq_of(int R, float scale, float theta) {
 
 template <typename T, int D, int FMT>
 cudaError_t launch_io(IoParams& P, bool fused, const IoFreq& f, cudaStream_t st) {
-  dim3 grid;
-  shape_of(P, P.H + P.Hk + (FMT == FMT_NONE ? 0 : P.Hk), kIoThreads / (D / 8), &grid);
+  constexpr int round = kIoThreads / (D / 16) * kTasks;
+  constexpr bool cache = FMT != FMT_NONE;
+  const long long tasks = tasks_of(P, P.H + P.Hk + (cache ? P.Hk : 0), round, fused ? 4 : 2);
+  long long blocks = 0;
+  if (fused) {
+    if (P.H) blocks += cut_of(P.cut[0], blocks, P.rows, P.H, tasks);
+    P.cut[1].first = P.cut[2].first = (int)blocks;
+    if (P.Hk) blocks += cut_of(P.cut[1], blocks, P.rows, P.Hk, tasks);
+    if (cache) blocks += cut_of(P.cut[2], blocks, P.rows, P.Hk, tasks);
+  } else {
+    blocks = cut_of(P.cut[0], 0, P.rows, 2 * P.Hk, tasks);
+  }
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const unsigned grid = (unsigned)blocks;
   if (fused)
     cache_io_kernel<T, D, FMT, true><<<grid, kIoThreads, 0, st>>>(P, f);
-  else if constexpr (FMT != FMT_NONE)
+  else if constexpr (cache)
     cache_io_kernel<T, D, FMT, false><<<grid, kIoThreads, 0, st>>>(P, f);
   return cudaGetLastError();
 }
@@ -449,8 +586,10 @@ cudaError_t launch_d(IoParams& P, int d, int fmt, bool fused, const IoFreq& f, c
 }
 template <typename T, int D>
 cudaError_t launch_read(IoParams& P, int fmt, cudaStream_t st) {
-  dim3 grid;
-  shape_of(P, 2 * P.Hk, kIoThreads / (D / (fmt == FMT_16 ? 8 : 16)), &grid);
+  const int round = kIoThreads / (D / (fmt == FMT_16 ? 8 : 16)) * kUnroll;
+  const long long blocks = cut_of(P.cut[0], 0, P.rows, 2 * P.Hk, tasks_of(P, 2 * P.Hk, round, 2));
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const unsigned grid = (unsigned)blocks;
   if (fmt == FMT_16) cache_read_kernel<T, D, FMT_16><<<grid, kIoThreads, 0, st>>>(P);
   else if (fmt == FMT_SCALED) cache_read_kernel<T, D, FMT_SCALED><<<grid, kIoThreads, 0, st>>>(P);
   else cache_read_kernel<T, D, FMT_BLOCK><<<grid, kIoThreads, 0, st>>>(P);
@@ -539,6 +678,10 @@ IoParams params_of(const pod_io_args& a, bool fused, bool cache) {
     P.num_slots = a.num_pages * a.page_size;
     P.ps = a.page_size; P.hnd = a.kv_layout;
     P.k_scale = a.k_scale; P.v_scale = a.v_scale;
+    // products of scales within 2^+-60 and fp32 values that matter stay normal
+    auto inv = [](float s) { return s > 8.7e-19f && s < 1.15e18f ? 1.f / s : 0.f; };
+    P.k_inv = inv(a.k_scale);
+    P.v_inv = inv(a.v_scale);
   }
   return P;
 }
