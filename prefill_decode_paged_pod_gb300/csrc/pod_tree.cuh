@@ -68,21 +68,21 @@ struct TLayout {
   static constexpr int QPART = POD_TREE_TILE * ROWB;   // one row part of one precision part
   static constexpr int KVPART = BK * ROWB;             // one row part of a block of K or V
   static constexpr int STAGE = PARTS * KVPART;
-  static constexpr int NK = F8 ? 2 : 3, NV = 2;
+  static constexpr int NK = F8 ? 2 : 3, NV = F8 && QP == 2 && D <= 128 ? 3 : 2;
   static constexpr int Q_OFF = 0;
   static constexpr int Q_BYTES = QP * PARTS * QPART;
   static constexpr int K_OFF = Q_BYTES;
   static constexpr int V_OFF = K_OFF + NK * STAGE;
   static constexpr int BAR_OFF = V_OFF + NV * STAGE;
-  // BAR_OFF + 0: barriers, +152: TMEM address, +156: abort flag, +160: the
-  // warps' largest V exponents of two blocks, +192: the block's factors (K,
+  // BAR_OFF + 0: barriers, +160: TMEM address, +164: abort flag, +168: the
+  // warps' largest V exponents of two blocks, +208: the block's factors (K,
   // then V)
-  static constexpr int WM_OFF = BAR_OFF + 160;
-  static constexpr int FAC_OFF = BAR_OFF + 192;
-  // (floats; bf16 beside the three Q parts of fp16 rows of 128 elements, which
-  // leave no room for more)
-  static constexpr int FACB = QP == 3 && D == 128 ? 2 : 4;
-  static constexpr int END = FAC_OFF + (KV == 2 ? 2 * BK * FACB : 0);
+  static constexpr int WM_OFF = BAR_OFF + 168;
+  static constexpr int FAC_OFF = BAR_OFF + 208;
+  // (K floats, or bf16 beside the three Q parts of fp16 rows of 128 elements,
+  // which leave no room for more; V bf16)
+  static constexpr int FACK = QP == 3 && D == 128 ? 2 : 4, FACV = 2;
+  static constexpr int END = FAC_OFF + (KV == 2 ? BK * (FACK + FACV) : 0);
   // The copies' join holds 32 output columns of the 128 lanes (16 KB) in the Q
   // region, and m and l of the lanes behind them, or at the end where Q has no
   // room for these.
@@ -117,13 +117,13 @@ enum {
   TB_QFULL = 0,
   TB_KFULL = 1,    // [3]
   TB_KEMPTY = 4,   // [3]
-  TB_VFULL = 7,    // [2]
-  TB_VEMPTY = 9,   // [2]
-  TB_SFULL = 11,   // [2]
-  TB_PFULL = 13,   // [2]
-  TB_PVDONE = 15,  // [2]
-  TB_FINAL = 17,
-  TB_COUNT = 18
+  TB_VFULL = 7,    // [3]
+  TB_VEMPTY = 10,  // [3]
+  TB_SFULL = 13,   // [2]
+  TB_PFULL = 15,   // [2]
+  TB_PVDONE = 17,  // [2]
+  TB_FINAL = 19,
+  TB_COUNT = 20
 };
 
 // W (16, 32 or 64) consecutive TMEM columns of the warp's 32 lanes
@@ -255,7 +255,8 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
   constexpr int BK = L::BK, NSB = L::NSB;
   constexpr int RB = 128 / C;                        // rows of a copy
   constexpr int TW = BK / C;                         // its keys in a block,
-  constexpr int W = TW < 64 ? TW : 64, NH = TW / W;  // in NH runs of W columns
+  // in NH runs of W columns (FP8: what stays in registers beside the parts of P)
+  constexpr int WM = L::F8 ? 32 : 64, W = TW < WM ? TW : WM, NH = TW / W;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sbase = smem_u32(smem), bar0 = sbase + L::BAR_OFF;
   auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
@@ -338,7 +339,7 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
   const int ctx = kv_len - ntok;
   // block scales: the exponent bytes of this thread's key (tid) of the next
   // block; keys past the last read the last
-  const uint32_t kfac = sbase + L::FAC_OFF, vfac = kfac + BK * L::FACB;
+  const uint32_t kfac = sbase + L::FAC_OFF, vfac = kfac + BK * L::FACK;
   int kbyte = 0, vbyte = 0, vref = 0;
   const KeyAt at = key_at(P, seg);
   auto load_bytes = [&](int blk) {
@@ -368,13 +369,9 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
         o_scale = exp_below(vref, top);
         vref = top;
       }
-      if constexpr (L::FACB == 4) {
-        stsf(kfac + 4 * tid, exp_byte(kbyte));
-        stsf(vfac + 4 * tid, exp_below(vbyte, vref));
-      } else {
-        sts16(kfac + 2 * tid, pow2_bf16(exp_byte(kbyte)));
-        sts16(vfac + 2 * tid, pow2_bf16(exp_below(vbyte, vref)));
-      }
+      if constexpr (L::FACK == 4) stsf(kfac + 4 * tid, exp_byte(kbyte));
+      else sts16(kfac + 2 * tid, pow2_bf16(exp_byte(kbyte)));
+      sts16(vfac + 2 * tid, pow2_bf16(exp_below(vbyte, vref)));
       if (j + 1 < nb) load_bytes(blk0 + j + 1);
       softmax_sync();
     }
@@ -394,7 +391,7 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
 #pragma unroll
         for (int i = 0; i < W; i += 4) {
           uint64_t f[2];
-          factors4<L::FACB>(kfac, col + i, f);
+          factors4<L::FACK>(kfac, col + i, f);
           unpack2(mul2(pack2(s[i], s[i + 1]), f[0]), s[i], s[i + 1]);
           unpack2(mul2(pack2(s[i + 2], s[i + 3]), f[1]), s[i + 2], s[i + 3]);
         }
@@ -438,9 +435,9 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
     const bool rescale = top > m_ref + L::LIMIT;     // also for the first finite maximum
     const float m_use = rescale ? top - L::TOP : m_ref;
     const float m_sub = m_use == NEG_INF ? 0.f : m_use;
-    // P goes over S: 16-bit, two keys a column; E4M3, four keys a column, BK / 4
-    // columns of high parts, then as many of low parts. Run h of P lies over
-    // columns of S that run h or an earlier one has read.
+    // P goes over S: 16-bit, two keys a column; E4M3, four keys a column, 8
+    // columns of high parts and 8 of low parts for each 32 keys. Run h of P lies
+    // over columns of S that run h or an earlier one has read.
     const uint64_t qs2 = pack2(qscale, qscale), ms2 = pack2(-m_sub, -m_sub);
     uint64_t rs[2] = {0, 0};
 #pragma unroll
@@ -458,7 +455,7 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
           rs[i / 2 & 1] = add2(rs[i / 2 & 1], e[i / 2]);
         }
         uint32_t hi[8];
-        const uint32_t col = (uint32_t)(my0 + h * W + q) / (N / 8);
+        const uint32_t col = (uint32_t)(my0 + h * W + q) / (L::F8 ? 2 : N / 8);
         if constexpr (!L::F8) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -471,7 +468,7 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
 #pragma unroll
             for (int i = 0; i < N; i += 4) {
               uint64_t f[2];
-              factors4<L::FACB>(vfac, my0 + h * W + q + i, f);
+              factors4<L::FACV>(vfac, my0 + h * W + q + i, f);
               e[i / 2] = mul2(e[i / 2], f[0]);
               e[i / 2 + 1] = mul2(e[i / 2 + 1], f[1]);
             }
@@ -479,17 +476,16 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
           uint32_t lo[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) e4m3_split4(e[2 * i], e[2 * i + 1], hi[i], lo[i]);
-          tmem_st8(s_addr + BK / 4 + col, lo);
+          tmem_st8(s_addr + col + 8, lo);
         }
         tmem_st8(s_addr + col, hi);
       }
     }
     if constexpr (C > 1) {                           // zeros for the other copies' keys
       const uint32_t zero[8] = {};
-      constexpr int PART = L::F8 ? BK / 4 : BK / 2;
 #pragma unroll
       for (int c = 0; c < BK / 2; c += 8)
-        if (c % PART / (PART / C) != cp) tmem_st8(s_addr + c, zero);
+        if (c / (BK / 2 / C) != cp) tmem_st8(s_addr + c, zero);
     }
     const bool need = (rescale && m_ref != NEG_INF) || (KV == 2 && o_scale != 1.f);
     if (j > 0 && __any_sync(0xffffffffu, need)) {
@@ -647,15 +643,15 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (uniform, and known to be)
   const uint32_t sbase = smem_u32(smem), bar0 = sbase + L::BAR_OFF;
-  static_assert(TB_COUNT * 8 <= 152, "barriers overlap the TMEM slot");
+  static_assert(TB_COUNT * 8 <= 160, "barriers overlap the TMEM slot");
   if ((sbase & 1023u) != 0u) {                       // 128B-swizzle atoms need 1024-byte alignment
     if (tid == 0) atomicOr(P.status, POD_STATUS_ALIGN);
     return;
   }
   auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::BAR_OFF + 156);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::BAR_OFF + 164);
   if (warp == 4) {
-    tmem_alloc(sbase + L::BAR_OFF + 152, L::TMEM_COLS);
+    tmem_alloc(sbase + L::BAR_OFF + 160, L::TMEM_COLS);
     tmem_relinquish();
   }
   const bool tma = P.kbx > 0;
@@ -665,10 +661,10 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
     for (int s = 0; s < 3; ++s) {
       mbar_init(BAR(TB_KFULL + s), loads);
       mbar_init(BAR(TB_KEMPTY + s), 1);
-    }
-    for (int s = 0; s < 2; ++s) {
       mbar_init(BAR(TB_VFULL + s), loads);
       mbar_init(BAR(TB_VEMPTY + s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(BAR(TB_SFULL + s), 1);
       mbar_init(BAR(TB_PFULL + s), 128);
       mbar_init(BAR(TB_PVDONE + s), 1);
@@ -680,7 +676,7 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::BAR_OFF + 152);
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::BAR_OFF + 160);
   const int seg0 = P.cta_ptr[blockIdx.x], seg1 = P.cta_ptr[blockIdx.x + 1];
   bool ok = true;
   volatile int never = 0;                            // an abort flag that nobody raises
@@ -723,34 +719,25 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
       const int blk0 = seg[TS_BLK0], nb = seg[TS_BLK1] - blk0, kv_len = seg[TS_KVLEN];
       if (!tree_wait(BAR(TB_QFULL), (i - seg0) & 1, abort_flag)) { ok = false; break; }
       tc_fence_after();
-      auto qk = [&](int j) -> bool {
-        if (!tree_wait(BAR(TB_KFULL + ks), kph, abort_flag)) return false;
-        tc_fence_after();
-        if (!tma) fence_proxy_async();
-        const int b = (sc0 + j) % NSB;
-        const uint32_t d_s = tmem + L::TM_S + b * BK;
-        const uint64_t kd = k_desc0 + (uint32_t)(ks * L::STAGE >> 4);
-        if (elect_one()) {
+      // issue Q K^T of block j into its S buffer (K has arrived)
+      auto issue_qk = [&](int b, uint64_t kd, int kslot) {
 #pragma unroll
-          for (int p = 0; p < L::QP; ++p)
+        for (int p = 0; p < L::QP; ++p)
 #pragma unroll
-            for (int k = 0; k < L::DSTEPS; ++k) {
-              constexpr int SPP = L::ROWB / 32;      // steps of a row part
-              const uint64_t qd = q_desc0 + (((p * L::PARTS + k / SPP) * L::QPART + (k % SPP) * 32) >> 4);
-              const uint64_t bd = kd + (((k / SPP) * L::KVPART + (k % SPP) * 32) >> 4);
-              if constexpr (L::F8) mma_f8_ss(d_s, qd, bd, id_qk, p + k > 0 ? 1u : 0u);
-              else mma_f16_ss(d_s, qd, bd, id_qk, k > 0 ? 1u : 0u);
-            }
-          mma_commit(BAR(TB_SFULL + b));
-          mma_commit(BAR(TB_KEMPTY + ks));
-        }
-        __syncwarp();
-        if (++ks == L::NK) { ks = 0; kph ^= 1; }
-        return true;
+          for (int k = 0; k < L::DSTEPS; ++k) {
+            constexpr int SPP = L::ROWB / 32;        // steps of a row part
+            const uint64_t qd = q_desc0 + (((p * L::PARTS + k / SPP) * L::QPART + (k % SPP) * 32) >> 4);
+            const uint64_t bd = kd + (((k / SPP) * L::KVPART + (k % SPP) * 32) >> 4);
+            const uint32_t d_s = tmem + L::TM_S + b * BK;
+            if constexpr (L::F8) mma_f8_ss(d_s, qd, bd, id_qk, p + k > 0 ? 1u : 0u);
+            else mma_f16_ss(d_s, qd, bd, id_qk, k > 0 ? 1u : 0u);
+          }
+        mma_commit(BAR(TB_SFULL + b));
+        mma_commit(BAR(TB_KEMPTY + kslot));
       };
-      auto pv = [&](int j) -> bool {
-        const int sc = sc0 + j, b = sc % NSB;
-        if (!tree_wait(BAR(TB_VFULL + vs), vph, abort_flag)) return false;
+      // O += P V of block j (its S buffer b), and with `qk` the next block's Q K^T
+      // right behind it
+      auto pv = [&](int j, int b, uint32_t parity, bool qk, int qb, uint64_t kd) -> bool {
         // Key steps past kv_len carry P = 0: skip them. Rows at or past kv_len in
         // the last step are unused slots of the last page, or nothing: zero them,
         // so that P = 0 never meets a non-finite value.
@@ -769,30 +756,61 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
         } else if (!tma) {
           fence_proxy_async();
         }
-        if (!tree_wait(BAR(TB_PFULL + b), (sc / NSB) & 1, abort_flag)) return false;
+        if (!tree_wait(BAR(TB_PFULL + b), parity, abort_flag)) return false;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < L::KSTEPS; ++k)
             if (k < ksteps) {
               if constexpr (L::F8) {
-                mma_f8_ts(tmem + L::TM_O, a_p + k * 8, vd + v_step[k], id_pv, (j > 0 || k > 0) ? 1u : 0u);
-                mma_f8_ts(tmem + L::TM_O, a_p + BK / 4 + k * 8, vd + v_step[k], id_pv, 1u);
+                mma_f8_ts(tmem + L::TM_O, a_p + k * 16, vd + v_step[k], id_pv, (j > 0 || k > 0) ? 1u : 0u);
+                mma_f8_ts(tmem + L::TM_O, a_p + k * 16 + 8, vd + v_step[k], id_pv, 1u);
               } else {
                 mma_f16_ts(tmem + L::TM_O, a_p + k * 8, vd + v_step[k], id_pv, (j > 0 || k > 0) ? 1u : 0u);
               }
             }
           mma_commit(BAR(TB_PVDONE + b));
           mma_commit(BAR(TB_VEMPTY + vs));
+          if (qk) issue_qk(qb, kd, ks);
         }
         __syncwarp();
         if (++vs == L::NV) { vs = 0; vph ^= 1; }
         return true;
       };
-      for (int j = 0; j <= nb && ok; ++j) {
-        if (NSB > 1 && j < nb) ok = qk(j);
-        if (j > 0 && ok) ok = pv(j - 1);
-        if (NSB == 1 && j < nb && ok) ok = qk(j);
+      auto wait_k = [&]() -> bool {
+        if (!tree_wait(BAR(TB_KFULL + ks), kph, abort_flag)) return false;
+        if (!tma) fence_proxy_async();
+        return true;
+      };
+      auto next_k = [&]() {
+        if (++ks == L::NK) { ks = 0; kph ^= 1; }
+      };
+      for (int j = NSB > 1 ? 0 : -1; j < nb; ++j) {
+        // two S buffers: QK_j, then PV_{j-1}; one: PV_j, then QK_{j+1}
+        const int jq = NSB > 1 ? j : j + 1, jv = NSB > 1 ? j - 1 : j;
+        const uint64_t kd = k_desc0 + (uint32_t)(ks * L::STAGE >> 4);
+        const bool has_k = jq < nb;
+        if (has_k && !wait_k()) { ok = false; break; }
+        if constexpr (NSB > 1) {
+          tc_fence_after();
+          if (elect_one()) issue_qk((sc0 + jq) % NSB, kd, ks);
+          __syncwarp();
+          next_k();
+        }
+        if (jv >= 0) {
+          const int sc = sc0 + jv, b = sc % NSB;
+          if (!tree_wait(BAR(TB_VFULL + vs), vph, abort_flag)) { ok = false; break; }
+          if (!pv(jv, b, (sc / NSB) & 1, NSB == 1 && has_k, (sc + 1) % NSB, kd)) { ok = false; break; }
+        } else if (NSB == 1) {
+          tc_fence_after();
+          if (elect_one()) issue_qk(sc0 % NSB, kd, ks);
+          __syncwarp();
+        }
+        if (NSB == 1 && has_k) next_k();
+      }
+      if (NSB > 1 && ok) {
+        const int sc = sc0 + nb - 1;
+        ok = tree_wait(BAR(TB_VFULL + vs), vph, abort_flag) && pv(nb - 1, sc % NSB, (sc / NSB) & 1, false, 0, 0);
       }
       sc0 += nb;
     }

@@ -2,12 +2,16 @@
 //
 // A unit is one (request, KV head, tile of 128 packed rows) and costs its key
 // blocks plus a fixed price for starting it (query load, pipeline fill,
-// epilogue). The units of one tile index form a plane; a plane is laid out in
-// request and head order and cut at equal cost, through the middle of units
-// where it falls so, so every CTA gets the same work up to one block. Planes
-// are cut alike: for wide trees the CTAs at the same place of two planes read
-// the same keys at the same time, the second time from L2. Cut units are merged
-// by a second kernel.
+// epilogue). The units of one KV head and tile index form a plane; a plane is laid
+// out in request order and cut at equal cost, through the middle of units where
+// it falls so, so every CTA gets the same work up to one block. Planes are cut
+// alike: the CTAs at the same place of two planes read the same tokens at the
+// same time, other heads' rows beside theirs in memory (an FP8 row of an NHD
+// cache is 128 bytes, too little by itself for HBM: 96 requests of 8192 keys took
+// 404 us with the heads one after another in one plane), and for wide trees the
+// same keys, the second time from L2. Where so many planes leave too many CTA
+// slots over, a plane takes all heads, one after another. Cut units are merged by
+// a second kernel.
 #include "pod_tree_planner.hpp"
 
 #include <string.h>
@@ -23,7 +27,7 @@ namespace {
 constexpr int kStartKeys = 192, kMinKeys = 320;
 
 struct Unit {
-  int req, g, blocks;
+  int req, g, mt, blocks;
 };
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -107,36 +111,51 @@ int pod_tree_build_plan(const PodTreeArgs& a, PodTreePlanHost& o, std::string* e
   int max_mt = 0;
   for (int r = 0; r < a.batch; ++r)
     max_mt = std::max(max_mt, (int)(((long long)n[r] * o.G + POD_TREE_TILE - 1) / POD_TREE_TILE));
-  std::vector<std::vector<Unit>> planes(max_mt);
+  using Planes = std::vector<std::vector<Unit>>;
   long long cost = 0, longest = 0;
-  for (int mt = 0; mt < max_mt; ++mt)
-    for (int r = 0; r < a.batch; ++r) {
-      if ((long long)n[r] * o.G <= (long long)mt * POD_TREE_TILE) continue;
-      const int blocks = (kv[r] + a.block - 1) / a.block;
-      for (int g = 0; g < a.Hk; ++g) planes[mt].push_back({r, g, blocks});
-      cost += (long long)a.Hk * (blocks + kStart);
-      longest = std::max(longest, (long long)blocks);
-    }
-  auto ctas = [&](int share) {
-    long long c = 0;
-    for (auto& p : planes) c += cut(p, share, kStart, [](int, int, int, int) {});
-    return c;
+  auto planes_of = [&](bool by_head) {
+    Planes planes((size_t)max_mt * (by_head ? a.Hk : 1));
+    cost = longest = 0;
+    for (int mt = 0; mt < max_mt; ++mt)
+      for (int r = 0; r < a.batch; ++r) {
+        if ((long long)n[r] * o.G <= (long long)mt * POD_TREE_TILE) continue;
+        const int blocks = (kv[r] + a.block - 1) / a.block;
+        for (int g = 0; g < a.Hk; ++g)
+          planes[by_head ? (size_t)mt * a.Hk + g : mt].push_back({r, g, mt, blocks});
+        cost += (long long)a.Hk * (blocks + kStart);
+        longest = std::max(longest, (long long)blocks);
+      }
+    return planes;
   };
-  int lo = (int)std::min<long long>(std::max<long long>(cost / std::max(1, a.slots), kMinCut + kStart), 1 << 29);
-  int hi = (int)std::min<long long>(cost + kStart + 1, (1ll << 30));
-  hi = std::max(hi, lo);
-  if (ctas(lo) > a.slots) {
-    // more planes than slots are possible: the largest share then runs in waves
+  auto share_of = [&](const Planes& planes) {
+    auto ctas = [&](int share) {
+      long long c = 0;
+      for (auto& p : planes) c += cut(p, share, kStart, [](int, int, int, int) {});
+      return c;
+    };
+    const long long most = 1 << 29, even = cost / std::max(1, a.slots);
+    int lo = (int)std::min(std::max(even, (long long)kMinCut + kStart), most);
+    int hi = (int)std::max((long long)lo, std::min(cost + kStart + 1, most));
+    if (ctas(lo) <= a.slots) return lo;
     while (lo + 1 < hi) {
       const int mid = lo + (hi - lo) / 2;
       if (ctas(mid) <= a.slots) hi = mid;
       else lo = mid;
     }
-    // (a plane is one CTA at least; without a share that fits, take the balanced one)
-    if (ctas(hi) > a.slots) hi = (int)std::min<long long>(std::max<long long>(cost / std::max(1, a.slots), longest + kStart), 1 << 29);
-    lo = hi;
+    // (a plane is one CTA at least: with more planes than slots the CTAs run in
+    // waves, and the balanced share is taken)
+    return ctas(hi) <= a.slots ? hi : (int)std::min(std::max(even, longest + kStart), most);
+  };
+  Planes planes = planes_of(false);
+  int share = share_of(planes);
+  if (a.Hk > 1 && (long long)max_mt * a.Hk <= a.slots) {
+    Planes by_head = planes_of(true);
+    const int s = share_of(by_head);
+    if (s <= share + share / 32) {       // up to 3 % more work a CTA
+      planes = std::move(by_head);
+      share = s;
+    }
   }
-  const int share = lo;
 
   // segments in CTA order; split tiles get partial rows and a merge group
   struct Seg {
@@ -145,13 +164,14 @@ int pod_tree_build_plan(const PodTreeArgs& a, PodTreePlanHost& o, std::string* e
   std::vector<int32_t> rec;
   o.cta_ptr.assign(1, 0);
   long long prows = 0, mrows = 0;
-  for (int mt = 0; mt < max_mt; ++mt) {
+  for (const auto& plane : planes) {
     std::vector<Seg> s;
-    cut(planes[mt], share, kStart, [&](int c, int u, int b0, int b1) { s.push_back({c, u, b0, b1}); });
+    cut(plane, share, kStart, [&](int c, int u, int b0, int b1) { s.push_back({c, u, b0, b1}); });
     for (size_t i = 0; i < s.size();) {
       size_t e = i;
       while (e < s.size() && s[e].unit == s[i].unit) ++e;
-      const Unit& un = planes[mt][s[i].unit];
+      const Unit& un = plane[s[i].unit];
+      const int mt = un.mt;
       const int rows = std::min(POD_TREE_TILE, n[un.req] * o.G - mt * POD_TREE_TILE);
       const bool split = e - i > 1;
       if (split) {
