@@ -27,8 +27,10 @@ enum PodTreeSeg {
   TS_COPIES,       // 1, 2 or 4: how many key slices the tile's lanes hold
   TS_REC = 16
 };
-// Merge group: the segments' partial rows of one split tile.
-enum PodTreeGroup { TG_G = 0, TG_ROW0, TG_NROWS, TG_PROW0, TG_NSEG, TG_QROW0, TG_MROW0, TG_REC = 8 };
+// Merge group: the segments' partial rows of one split tile. Tiles in more than
+// POD_TREE_FEW segments are listed first.
+#define POD_TREE_FEW 4
+enum PodTreeGroup { TG_G = 0, TG_ROW0, TG_NROWS, TG_PROW0, TG_NSEG, TG_QROW0, TG_REC = 8 };
 // Status block (int32) at the start of the workspace.
 enum { TREE_ST_STATUS = 0, TREE_ST_INTS = 64 };
 
@@ -46,7 +48,7 @@ struct PodTreeParams {
   int32_t* status;
   int H, Hk, G, ps, ps_shift, hnd, num_pages;
   int kbx;                       // keys per TMA box, 0: gather
-  int n_cta, n_groups, n_mrows;
+  int n_cta, n_groups, n_big;    // merge groups, those of many segments
   float scale_log2;              // sm_scale * log2(e) (* k_scale)
   float v_scale;
 };

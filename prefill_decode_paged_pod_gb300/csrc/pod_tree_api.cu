@@ -27,36 +27,84 @@ struct pod_tree_s {
 
 namespace {
 
-// One warp per row of a split tile: o = sum 2^(lse_i - M) o_i / sum, in the
-// segments' order; the sink enters once, here. Bound by its launch: the
-// partial rows come from L2.
+// Split tiles: o = sum 2^(lse_i - M) o_i / sum over a row's pieces, in a fixed
+// order; the sink enters once, here. The partial rows come from L2, and the
+// kernel is bound by how many of them are asked for at once. (One warp a row,
+// finding its group by bisection, took 30 us for 65536 rows of two pieces. The
+// CTA that finishes a tile last merging it on the spot cost the attention loop
+// its registers: 419 -> 510 us for 96 block-scaled requests.)
+//
+// Few pieces: 32 rows a block, 8 threads a row, all pieces of a row in flight.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ PodTreeParams P) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= P.n_mrows) return;
-  int lo = 0, hi = P.n_groups - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (P.groups[mid * TG_REC + TG_MROW0] <= row) lo = mid;
-    else hi = mid - 1;
+POD_DEV void merge_few(const PodTreeParams& P, const int32_t* g, int chunk) {
+  constexpr int NV = D / 32;                         // 16-byte runs a thread
+  const int nseg = g[TG_NSEG], nrows = g[TG_NROWS], r = chunk * 32 + (threadIdx.x >> 3), l8 = threadIdx.x & 7;
+  if (r >= nrows) return;
+  const size_t pr0 = (size_t)g[TG_PROW0] + r;
+  float w[POD_TREE_FEW];
+  float4 v[POD_TREE_FEW][NV];
+#pragma unroll
+  for (int j = 0; j < POD_TREE_FEW; ++j) {
+    w[j] = -INFINITY;
+    if (j < nseg) {
+      const size_t pr = pr0 + (size_t)j * nrows;
+      w[j] = P.part_lse[pr];
+#pragma unroll
+      for (int k = 0; k < NV; ++k) v[j][k] = reinterpret_cast<const float4*>(P.part_o + pr * D)[l8 + 8 * k];
+    }
   }
-  const int32_t* g = P.groups + (size_t)lo * TG_REC;
-  const int r = row - g[TG_MROW0], nrows = g[TG_NROWS], nseg = g[TG_NSEG];
+  const float M = fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])), Ms = M == -INFINITY ? 0.f : M;
+  static_assert(POD_TREE_FEW == 4, "the maximum above is over four pieces");
+  float wsum = 0.f;
+#pragma unroll
+  for (int j = 0; j < POD_TREE_FEW; ++j) {
+    w[j] = j < nseg ? ex2(w[j] - Ms) : 0.f;
+    wsum += w[j];
+  }
   const int packed = g[TG_ROW0] + r, head = g[TG_G] * P.G + packed % P.G;
   const size_t out_row = (size_t)(g[TG_QROW0] + packed / P.G) * P.H + head;
-  const float* lse = P.part_lse + g[TG_PROW0] + r;
+  float denom = wsum;
+  if (P.sinks) denom += ex2(P.sinks[head] * 1.4426950408889634f - Ms);
+  const float inv = denom == 0.f ? 0.f : 1.f / denom;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < POD_TREE_FEW; ++j)
+      if (j < nseg) {
+        a.x = fmaf(w[j], v[j][k].x, a.x);
+        a.y = fmaf(w[j], v[j][k].y, a.y);
+        a.z = fmaf(w[j], v[j][k].z, a.z);
+        a.w = fmaf(w[j], v[j][k].w, a.w);
+      }
+    reinterpret_cast<uint2*>(static_cast<T*>(P.out) + out_row * D)[l8 + 8 * k] =
+        make_uint2(Pack<T>::two(a.x * inv, a.y * inv), Pack<T>::two(a.z * inv, a.w * inv));
+  }
+  if (l8 == 0 && P.lse) P.lse[out_row] = wsum == 0.f ? -INFINITY : M + log2f(wsum);
+}
+
+// Many pieces (a long request): two rows a block, four warps a row, each over
+// every fourth piece, joined through shared memory.
+template <typename T, int D>
+POD_DEV void merge_many(const PodTreeParams& P, const int32_t* g, int chunk) {
+  constexpr int PER = D / 32, SLICES = 4;
+  __shared__ float part[2][SLICES][D];
+  __shared__ float sum[2][SLICES];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp >> 2, slice = warp & 3;
+  const int nrows = g[TG_NROWS], nseg = g[TG_NSEG], r = chunk * 2 + sub;
+  if (chunk * 2 >= nrows) return;
+  const bool live = r < nrows;
+  const size_t pr0 = (size_t)g[TG_PROW0] + (live ? r : nrows - 1);
   float M = -INFINITY;
-  for (int j = lane; j < nseg; j += 32) M = fmaxf(M, lse[(size_t)j * nrows]);
+  for (int j = lane; j < nseg; j += 32) M = fmaxf(M, P.part_lse[pr0 + (size_t)j * nrows]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const float Ms = M == -INFINITY ? 0.f : M;
-  constexpr int PER = D / 32;
   float acc[PER] = {};
   float wsum = 0.f;
-#pragma unroll 4
-  for (int j = 0; j < nseg; ++j) {
-    const size_t pr = (size_t)g[TG_PROW0] + (size_t)j * nrows + r;
+#pragma unroll 8
+  for (int j = slice; j < nseg; j += SLICES) {
+    const size_t pr = pr0 + (size_t)j * nrows;
     const float w = ex2(P.part_lse[pr] - Ms);
     wsum += w;
     const float* src = P.part_o + pr * D + lane * PER;
@@ -67,20 +115,48 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
       acc[i + 1] = fmaf(w, v.y, acc[i + 1]);
     }
   }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) part[sub][slice][lane * PER + i] = acc[i];
+  if (lane == 0) sum[sub][slice] = wsum;
+  __syncthreads();
+  if (slice != 0 || !live) return;
+  wsum = (sum[sub][0] + sum[sub][1]) + (sum[sub][2] + sum[sub][3]);
+  const int packed = g[TG_ROW0] + r, head = g[TG_G] * P.G + packed % P.G;
+  const size_t out_row = (size_t)(g[TG_QROW0] + packed / P.G) * P.H + head;
   float denom = wsum;
   if (P.sinks) denom += ex2(P.sinks[head] * 1.4426950408889634f - Ms);
   const float inv = denom == 0.f ? 0.f : 1.f / denom;
   T* out = static_cast<T*>(P.out) + out_row * D + lane * PER;
 #pragma unroll
-  for (int i = 0; i < PER; i += 2)
-    *reinterpret_cast<uint32_t*>(out + i) = Pack<T>::two(acc[i] * inv, acc[i + 1] * inv);
+  for (int i = 0; i < PER; i += 2) {
+    const int c = lane * PER + i;
+    float v[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      v[k] = ((part[sub][0][c + k] + part[sub][1][c + k]) + (part[sub][2][c + k] + part[sub][3][c + k])) * inv;
+    *reinterpret_cast<uint32_t*>(out + i) = Pack<T>::two(v[0], v[1]);
+  }
   if (lane == 0 && P.lse) P.lse[out_row] = wsum == 0.f ? -INFINITY : M + log2f(wsum);
+}
+
+constexpr int kManyChunks = POD_TREE_TILE / 2, kFewChunks = POD_TREE_TILE / 32;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ PodTreeParams P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int many = P.n_big * kManyChunks, b = (int)blockIdx.x;
+  if (b < many)
+    merge_many<T, D>(P, P.groups + (size_t)(b / kManyChunks) * TG_REC, b % kManyChunks);
+  else
+    merge_few<T, D>(P, P.groups + (size_t)(P.n_big + (b - many) / kFewChunks) * TG_REC, (b - many) % kFewChunks);
 }
 
 template <typename T, int D>
 cudaError_t merge_d(const PodTreeParams& P, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((P.n_mrows + 7) / 8));
+  const long long blocks = (long long)P.n_big * kManyChunks + (long long)(P.n_groups - P.n_big) * kFewChunks;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -261,7 +337,7 @@ pod_status pod_tree_run(pod_tree_handle h, const void* q, const void* kv, const 
     if ((1 << s) == P.ps) K.ps_shift = s;
   const int block = h->format == POD_KV_16BIT ? POD_TREE_BLOCK : POD_TREE_BLOCK8;
   K.kbx = K.ps_shift >= 3 ? (P.ps < block ? P.ps : block) : 0;
-  K.n_cta = P.n_cta; K.n_groups = (int)(P.groups.size() / TG_REC); K.n_mrows = P.n_mrows;
+  K.n_cta = P.n_cta; K.n_groups = (int)(P.groups.size() / TG_REC); K.n_big = P.n_big;
   K.scale_log2 = h->scale_log2; K.v_scale = h->v_scale;
   if (K.kbx) {
     if (!encode_fn()) return fail(POD_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
@@ -275,7 +351,7 @@ pod_status pod_tree_run(pod_tree_handle h, const void* q, const void* kv, const 
                   : h->format == POD_KV_E4M3 ? pod_tree_k8(K, h->dtype, P.d, st)
                                              : pod_tree_k8b(K, h->dtype, P.d, st);
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
-  if (K.n_mrows > 0) {
+  if (K.n_groups > 0) {
     e = pod_tree_merge(K, h->dtype, P.d, st);
     if (e != cudaSuccess) return cuda_fail(e, "tree merge launch");
   }

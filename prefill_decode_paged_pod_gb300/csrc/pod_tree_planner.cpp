@@ -10,8 +10,8 @@
 // cache is 128 bytes, too little by itself for HBM: 96 requests of 8192 keys took
 // 404 us with the heads one after another in one plane), and for wide trees the
 // same keys, the second time from L2. Where so many planes leave too many CTA
-// slots over, a plane takes all heads, one after another. Cut units are merged by
-// a second kernel.
+// slots over, a plane takes all heads, one after another. Cut units are merged
+// by a second kernel.
 #include "pod_tree_planner.hpp"
 
 #include <string.h>
@@ -161,9 +161,9 @@ int pod_tree_build_plan(const PodTreeArgs& a, PodTreePlanHost& o, std::string* e
   struct Seg {
     int cta, unit, b0, b1;
   };
-  std::vector<int32_t> rec;
+  std::vector<int32_t> rec, few;
   o.cta_ptr.assign(1, 0);
-  long long prows = 0, mrows = 0;
+  long long prows = 0;
   for (const auto& plane : planes) {
     std::vector<Seg> s;
     cut(plane, share, kStart, [&](int c, int u, int b0, int b1) { s.push_back({c, u, b0, b1}); });
@@ -171,23 +171,21 @@ int pod_tree_build_plan(const PodTreeArgs& a, PodTreePlanHost& o, std::string* e
       size_t e = i;
       while (e < s.size() && s[e].unit == s[i].unit) ++e;
       const Unit& un = plane[s[i].unit];
-      const int mt = un.mt;
-      const int rows = std::min(POD_TREE_TILE, n[un.req] * o.G - mt * POD_TREE_TILE);
-      const bool split = e - i > 1;
-      if (split) {
-        const int32_t g[TG_REC] = {un.g, mt * POD_TREE_TILE, rows, (int32_t)prows, (int32_t)(e - i),
-                                   a.q_indptr[un.req], (int32_t)mrows, 0};
-        o.groups.insert(o.groups.end(), g, g + TG_REC);
-        mrows += rows;
+      const int rows = std::min(POD_TREE_TILE, n[un.req] * o.G - un.mt * POD_TREE_TILE);
+      const int pieces = (int)(e - i);
+      if (pieces > 1) {
+        const int32_t g[TG_REC] = {un.g, un.mt * POD_TREE_TILE, rows, (int32_t)prows, pieces, a.q_indptr[un.req], 0, 0};
+        std::vector<int32_t>& to = pieces > POD_TREE_FEW ? o.groups : few;
+        to.insert(to.end(), g, g + TG_REC);
       }
       for (size_t j = i; j < e; ++j) {
         int32_t r[TS_REC] = {};
         r[TS_G] = un.g;
-        r[TS_ROW0] = mt * POD_TREE_TILE;
+        r[TS_ROW0] = un.mt * POD_TREE_TILE;
         r[TS_NROWS] = rows;
         r[TS_BLK0] = s[j].b0;
         r[TS_BLK1] = s[j].b1;
-        r[TS_PROW] = split ? (int32_t)prows : -1;
+        r[TS_PROW] = pieces > 1 ? (int32_t)prows : -1;
         r[TS_KVLEN] = kv[un.req];
         r[TS_NTOK] = n[un.req];
         r[TS_QROW0] = a.q_indptr[un.req];
@@ -196,7 +194,7 @@ int pod_tree_build_plan(const PodTreeArgs& a, PodTreePlanHost& o, std::string* e
         r[TS_BIT_LO] = (int32_t)(uint32_t)(bit0[un.req] & 0xffffffffll);
         r[TS_BIT_HI] = (int32_t)(bit0[un.req] >> 32);
         r[TS_COPIES] = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
-        if (split) prows += rows;
+        if (pieces > 1) prows += rows;
         rec.insert(rec.end(), r, r + TS_REC);
         const bool last = j + 1 == s.size() || s[j + 1].cta != s[j].cta;
         if (last) o.cta_ptr.push_back((int32_t)(rec.size() / TS_REC));
@@ -204,11 +202,13 @@ int pod_tree_build_plan(const PodTreeArgs& a, PodTreePlanHost& o, std::string* e
       i = e;
     }
   }
-  if (prows > 0x7fffffff || mrows > 0x7fffffff) return bad(INV, "too many split rows");
+  // groups of many pieces first, then those of a few
+  o.n_big = (int)(o.groups.size() / TG_REC);
+  o.groups.insert(o.groups.end(), few.begin(), few.end());
+  if (prows > 0x7fffffff) return bad(INV, "too many split rows");
   o.segs = std::move(rec);
   o.n_cta = (int)o.cta_ptr.size() - 1;
   o.n_prows = (int)prows;
-  o.n_mrows = (int)mrows;
 
   size_t at = TREE_ST_INTS * sizeof(int32_t);
   auto put = [&](size_t bytes) {

@@ -17,7 +17,7 @@ struct PodTreePlanHost {
   int batch = 0, num_pages = 0, H = 0, Hk = 0, G = 0, d = 0, ps = 0, rows = 0;
   long long mask_bits = 0;
   std::vector<int32_t> segs, cta_ptr, pages, groups;
-  int n_cta = 0, n_mrows = 0, n_prows = 0;
+  int n_cta = 0, n_big = 0, n_prows = 0;
   // workspace layout (bytes)
   size_t off_segs = 0, off_cta = 0, off_pages = 0, off_groups = 0, off_part_o = 0, off_part_lse = 0,
          total = 0;

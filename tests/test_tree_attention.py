@@ -395,12 +395,17 @@ def test_plan_covers_every_block_once(name, sms):
     tiles = {(r, g, m) for r in range(len(c.n)) for g in range(c.Hk) for m in range(0, c.n[r] * G, 128)}
     assert set(seen) == tiles
     prows = set()
+    pieces = [int(x[4]) for x in groups]
+    n_big = sum(p > 4 for p in pieces)
+    assert all(p > 4 for p in pieces[:n_big]) and all(2 <= p <= 4 for p in pieces[n_big:])
     for (r, g, row0), parts in seen.items():
         at = 0
         for b0, b1, prow, nrows in parts:
             assert b0 == at
             at = b1
             assert (prow < 0) == (len(parts) == 1)
+            if prow >= 0 and b0 == 0:
+                assert [g, row0, nrows, prow, len(parts), int(c.q_indptr[r])] in groups[:, :6].tolist()
             if prow >= 0:
                 mine = set(range(prow, prow + nrows))
                 assert not mine & prows
