@@ -68,7 +68,7 @@ struct TLayout {
   static constexpr int QPART = POD_TREE_TILE * ROWB;   // one row part of one precision part
   static constexpr int KVPART = BK * ROWB;             // one row part of a block of K or V
   static constexpr int STAGE = PARTS * KVPART;
-  static constexpr int NK = F8 ? 2 : 3, NV = F8 && QP == 2 && D <= 128 ? 3 : 2;
+  static constexpr int NK = F8 ? 2 : 3, NV = KV == 1 && QP == 2 && D <= 128 ? 3 : 2;
   static constexpr int Q_OFF = 0;
   static constexpr int Q_BYTES = QP * PARTS * QPART;
   static constexpr int K_OFF = Q_BYTES;
@@ -76,13 +76,16 @@ struct TLayout {
   static constexpr int BAR_OFF = V_OFF + NV * STAGE;
   // BAR_OFF + 0: barriers, +160: TMEM address, +164: abort flag, +168: the
   // warps' largest V exponents of two blocks, +208: the block's factors (K,
-  // then V)
+  // then V). One set for the CTA: a set for each warp would spare the meetings,
+  // and a loader warp for the exponent bytes the loads, but both made the code
+  // larger than the instruction cache and the loop slower (405 us as it is, 409
+  // and 430 us for 96 requests of 8192 keys).
   static constexpr int WM_OFF = BAR_OFF + 168;
   static constexpr int FAC_OFF = BAR_OFF + 208;
-  // (K floats, or bf16 beside the three Q parts of fp16 rows of 128 elements,
-  // which leave no room for more; V bf16)
-  static constexpr int FACK = QP == 3 && D == 128 ? 2 : 4, FACV = 2;
-  static constexpr int END = FAC_OFF + (KV == 2 ? BK * (FACK + FACV) : 0);
+  // (floats, or bf16 beside the three Q parts of fp16 rows of 128 elements, which
+  // leave no room for more)
+  static constexpr int FAC = QP == 3 && D == 128 ? 2 : 4;
+  static constexpr int END = FAC_OFF + (KV == 2 ? 2 * BK * FAC : 0);
   // The copies' join holds 32 output columns of the 128 lanes (16 KB) in the Q
   // region, and m and l of the lanes behind them, or at the end where Q has no
   // room for these.
@@ -235,11 +238,13 @@ POD_DEV void factors4(uint32_t base, int key, uint64_t* f) {
 struct KeyAt {
   const int32_t* pages;
   int npages, ps, shift, hk, hnd, g;
-  POD_DEV long long row(int t) const {
+  POD_DEV int page(int t) const {
     const int i = shift >= 0 ? t >> shift : t / ps;
-    const int slot = shift >= 0 ? t & (ps - 1) : t - i * ps;
-    const long long page = __ldg(pages + (i < npages ? i : npages - 1));
-    return page * 2 * ps * hk + (hnd ? (long long)g * ps + slot : (long long)slot * hk + g);
+    return __ldg(pages + (i < npages ? i : npages - 1));
+  }
+  POD_DEV long long row(int t, int page) const {
+    const int slot = shift >= 0 ? t & (ps - 1) : t % ps;
+    return (long long)page * 2 * ps * hk + (hnd ? (long long)g * ps + slot : (long long)slot * hk + g);
   }
 };
 POD_DEV KeyAt key_at(const PodTreeParams& P, const int32_t* seg) {
@@ -338,16 +343,22 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
   const long long bit0 = ((long long)seg[TS_BIT_HI] << 32) | (uint32_t)seg[TS_BIT_LO];
   const int ctx = kv_len - ntok;
   // block scales: the exponent bytes of this thread's key (tid) of the next
-  // block; keys past the last read the last
-  const uint32_t kfac = sbase + L::FAC_OFF, vfac = kfac + BK * L::FACK;
-  int kbyte = 0, vbyte = 0, vref = 0;
+  // block, and its page of the one after (a byte's address waits for its page);
+  // keys past the last read the last
+  const uint32_t kfac = sbase + L::FAC_OFF, vfac = kfac + BK * L::FAC;
+  int kbyte = 0, vbyte = 0, page = 0, vref = 0;
   const KeyAt at = key_at(P, seg);
+  auto my_key = [&](int blk) { return min(blk * BK + tid, kv_len - 1); };
   auto load_bytes = [&](int blk) {
-    const long long r = at.row(min(blk * BK + tid, kv_len - 1));
+    const long long r = at.row(my_key(blk), page);
     kbyte = __ldg(P.scales + r);
     vbyte = __ldg(P.scales + r + (long long)P.ps * P.Hk);
+    page = at.page(my_key(blk + 1));                 // (for the block after)
   };
-  if constexpr (KV == 2) load_bytes(blk0);
+  if constexpr (KV == 2) {
+    page = at.page(my_key(blk0));
+    load_bytes(blk0);
+  }
 
   const float NEG_INF = -INFINITY;
   float m_ref = NEG_INF, l = 0.f;
@@ -369,9 +380,13 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
         o_scale = exp_below(vref, top);
         vref = top;
       }
-      if constexpr (L::FACK == 4) stsf(kfac + 4 * tid, exp_byte(kbyte));
-      else sts16(kfac + 2 * tid, pow2_bf16(exp_byte(kbyte)));
-      sts16(vfac + 2 * tid, pow2_bf16(exp_below(vbyte, vref)));
+      if constexpr (L::FAC == 4) {
+        stsf(kfac + 4 * tid, exp_byte(kbyte));
+        stsf(vfac + 4 * tid, exp_below(vbyte, vref));
+      } else {
+        sts16(kfac + 2 * tid, pow2_bf16(exp_byte(kbyte)));
+        sts16(vfac + 2 * tid, pow2_bf16(exp_below(vbyte, vref)));
+      }
       if (j + 1 < nb) load_bytes(blk0 + j + 1);
       softmax_sync();
     }
@@ -391,7 +406,7 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
 #pragma unroll
         for (int i = 0; i < W; i += 4) {
           uint64_t f[2];
-          factors4<L::FACK>(kfac, col + i, f);
+          factors4<L::FAC>(kfac, col + i, f);
           unpack2(mul2(pack2(s[i], s[i + 1]), f[0]), s[i], s[i + 1]);
           unpack2(mul2(pack2(s[i + 2], s[i + 3]), f[1]), s[i + 2], s[i + 3]);
         }
@@ -468,7 +483,7 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
 #pragma unroll
             for (int i = 0; i < N; i += 4) {
               uint64_t f[2];
-              factors4<L::FACV>(vfac, my0 + h * W + q + i, f);
+              factors4<L::FAC>(vfac, my0 + h * W + q + i, f);
               e[i / 2] = mul2(e[i / 2], f[0]);
               e[i / 2 + 1] = mul2(e[i / 2 + 1], f[1]);
             }
@@ -883,14 +898,16 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
       const int32_t* seg = P.segs + (size_t)i * TS_REC;
       const int kv_len = seg[TS_KVLEN], b1 = seg[TS_BLK1];
       const KeyAt at = key_at(P, seg);
-      long long row[NQ], next[NQ];
+      long long row[NQ];
+      int page[NQ];
+      auto my_key = [&](int blk, int q) { return min(blk * BK + q * 32 + lane, kv_len - 1); };
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) next[q] = at.row(min(seg[TS_BLK0] * BK + q * 32 + lane, kv_len - 1));
+      for (int q = 0; q < NQ; ++q) page[q] = at.page(my_key(seg[TS_BLK0], q));
       for (int blk = seg[TS_BLK0]; blk < b1; ++blk) {
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
-          row[q] = next[q];
-          if (blk + 1 < b1) next[q] = at.row(min((blk + 1) * BK + q * 32 + lane, kv_len - 1));
+          row[q] = at.row(my_key(blk, q), page[q]);
+          if (blk + 1 < b1) page[q] = at.page(my_key(blk + 1, q));
         }
         const int left = kv_len - blk * BK;
         auto copy = [&](uint32_t dst, long long step) {
