@@ -12,10 +12,10 @@
 //   warps 0-3  one TMEM lane (row) per thread: Q into shared memory, then per
 //              key block tcgen05.ld of S, mask, softmax, P back into TMEM;
 //              final output or fp32 partial;
-//   warp 4     one lane issues tcgen05.mma: S = Q K^T, then O += P V with P read
-//              from TMEM;
+//   warp 4     one lane issues tcgen05.mma: S = Q K^T, and O += P V with P read
+//              from TMEM (double-buffered S: warp 7 issues these);
 //   warp 5, 6  K and V as TMA boxes through the page table; page sizes that are
-//              not a power of two of at least 8 are gathered by warps 5-7 with
+//              not a power of two of at least 8 are gathered by the other warps with
 //              cp.async.
 //
 // Few rows: a tile of at most 32 (64) rows is held 4 (2) times in the 128
@@ -99,6 +99,8 @@ struct TLayout {
   // the softmax of this one; FP8 blocks of 128 keys leave room for one where
   // two CTAs share the SM (these overlap each other).
   static constexpr int NSB = F8 && D <= 128 ? 1 : 2;
+  // (with two, warp 7 issues MMAs and two warps gather; else three)
+  static constexpr int GW = NSB > 1 ? 2 : 3;
   static constexpr int TM_S = 0, TM_O = NSB * BK;
   static constexpr int TMEM_COLS = TM_O + D <= 256 ? 256 : 512;
   static_assert(TM_O + D <= 512 && (D > 128 || TMEM_COLS == 256), "TMEM columns");
@@ -671,7 +673,7 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
   }
   const bool tma = P.kbx > 0;
   if (tid == 0) {
-    const uint32_t loads = tma ? 1u : 96u;           // gather: three warps
+    const uint32_t loads = tma ? 1u : 32u * L::GW;   // gather: two or three warps
     mbar_init(BAR(TB_QFULL), 128);
     for (int s = 0; s < 3; ++s) {
       mbar_init(BAR(TB_KFULL + s), loads);
@@ -684,7 +686,7 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
       mbar_init(BAR(TB_PFULL + s), 128);
       mbar_init(BAR(TB_PVDONE + s), 1);
     }
-    mbar_init(BAR(TB_FINAL), 1);
+    mbar_init(BAR(TB_FINAL), NSB);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -705,14 +707,17 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
            : copies == 2 ? tree_softmax<T, D, KV, 2>(P, smem, tmem, seg, sc0, abort_flag)
                          : tree_softmax<T, D, KV, 1>(P, smem, tmem, seg, sc0, abort_flag);
     }
-  } else if (warp == 4) {
-    // ---------------------------------------------------------- MMA issuer
-    // Two S buffers: QK_0, [QK_1, PV_0], ..., PV_{nb-1}; QK_{j+2} reuses the
-    // columns of S_j / P_j, and MMAs issued by one thread run in order. One S
-    // buffer: QK_0, [PV_0, QK_1], ... The whole warp walks the loop and one
-    // elected lane issues: addresses and descriptors then stay in uniform
-    // registers (a loop under `lane == 0` moved each of them there for every
-    // MMA: 85 clocks an instruction).
+  } else if (warp == 4 || (NSB > 1 && warp == 7)) {
+    // ---------------------------------------------------------- MMA issuers
+    // Two S buffers: warp 4 issues the Q K^T, as soon as the P V that reads the
+    // buffer's last P has finished, warp 7 the P V. One S buffer: warp 4 issues
+    // PV_j and QK_{j+1} in turn (MMAs issued by one thread run in order). A whole
+    // warp walks its loop and one elected lane issues: addresses and descriptors
+    // then stay in uniform registers (a loop under `lane == 0` moved each of them
+    // there for every MMA: 85 clocks an instruction). The second warp takes the
+    // waits of one product off the other's: 16 requests of 64 tokens and 4100 keys
+    // went from 137 to 129 us with pages of 64; with pages of 16 they stay at 136,
+    // bound by their 12 boxes a block.
     const uint32_t id_qk = L::F8 ? idesc_e4m3(128, BK, false, false) : idesc_f16(Pack<T>::kBF16, 128, BK, false, false);
     const uint32_t id_pv = L::F8 ? idesc_e4m3(128, D, false, true) : idesc_f16(Pack<T>::kBF16, 128, D, false, true);
     // V stage: 16-bit TMA boxes of vb keys lie as [box][row part][key], anything
@@ -729,103 +734,110 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
     const uint64_t k_desc0 = L::desc(sbase + L::K_OFF, 16, 8 * L::ROWB);
     int ks = 0, vs = 0, sc0 = 0;                     // ring positions, with their phases
     uint32_t kph = 0, vph = 0;
+    // Q K^T of the block in K stage `slot` into S buffer b
+    auto issue_qk = [&](int b, uint64_t kd, int slot) {
+#pragma unroll
+      for (int p = 0; p < L::QP; ++p)
+#pragma unroll
+        for (int k = 0; k < L::DSTEPS; ++k) {
+          constexpr int SPP = L::ROWB / 32;          // steps of a row part
+          const uint64_t qd = q_desc0 + (((p * L::PARTS + k / SPP) * L::QPART + (k % SPP) * 32) >> 4);
+          const uint64_t bd = kd + (((k / SPP) * L::KVPART + (k % SPP) * 32) >> 4);
+          const uint32_t d_s = tmem + L::TM_S + b * BK;
+          if constexpr (L::F8) mma_f8_ss(d_s, qd, bd, id_qk, p + k > 0 ? 1u : 0u);
+          else mma_f16_ss(d_s, qd, bd, id_qk, k > 0 ? 1u : 0u);
+        }
+      mma_commit(BAR(TB_SFULL + b));
+      mma_commit(BAR(TB_KEMPTY + slot));
+    };
+    auto wait_k = [&]() -> bool {
+      if (!tree_wait(BAR(TB_KFULL + ks), kph, abort_flag)) return false;
+      if (!tma) fence_proxy_async();
+      return true;
+    };
+    auto next_k = [&]() {
+      if (++ks == L::NK) { ks = 0; kph ^= 1; }
+    };
+    // O += P V of a block (its S buffer b, `keys` keys below kv_len), and with
+    // `qk` the next block's Q K^T right behind it
+    auto pv = [&](bool first, int keys, int b, uint32_t parity, bool qk, int qb, uint64_t kd) -> bool {
+      if (!tree_wait(BAR(TB_VFULL + vs), vph, abort_flag)) return false;
+      // Key steps past kv_len carry P = 0: skip them. Rows at or past kv_len in
+      // the last step are unused slots of the last page, or nothing: zero them,
+      // so that P = 0 never meets a non-finite value.
+      const int ksteps = (keys + L::KSTEP - 1) / L::KSTEP;
+      const uint64_t vd = v_desc0 + (uint32_t)(vs * L::STAGE >> 4);
+      const uint32_t a_p = tmem + L::TM_S + b * BK;
+      if (keys % L::KSTEP) {
+        const uint32_t va = sbase + L::V_OFF + vs * L::STAGE;
+        constexpr int CPP = L::ROWB / 16;            // 16-byte chunks of a row part
+        for (int x = lane; x < (ksteps * L::KSTEP - keys) * L::PARTS * CPP; x += 32) {
+          const int r = keys + x / (L::PARTS * CPP), h = x / CPP % L::PARTS, c = x % CPP;
+          sts128(va + (uint32_t)(r / vb) * v_box + (h * vb + r % vb) * L::ROWB + c * 16, make_uint4(0, 0, 0, 0));
+        }
+        fence_proxy_async();
+        __syncwarp();
+      } else if (!tma) {
+        fence_proxy_async();
+      }
+      if (!tree_wait(BAR(TB_PFULL + b), parity, abort_flag)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < L::KSTEPS; ++k)
+          if (k < ksteps) {
+            if constexpr (L::F8) {
+              mma_f8_ts(tmem + L::TM_O, a_p + k * 16, vd + v_step[k], id_pv, (!first || k > 0) ? 1u : 0u);
+              mma_f8_ts(tmem + L::TM_O, a_p + k * 16 + 8, vd + v_step[k], id_pv, 1u);
+            } else {
+              mma_f16_ts(tmem + L::TM_O, a_p + k * 8, vd + v_step[k], id_pv, (!first || k > 0) ? 1u : 0u);
+            }
+          }
+        mma_commit(BAR(TB_PVDONE + b));
+        mma_commit(BAR(TB_VEMPTY + vs));
+        if (qk) issue_qk(qb, kd, ks);
+      }
+      __syncwarp();
+      if (++vs == L::NV) { vs = 0; vph ^= 1; }
+      return true;
+    };
     for (int i = seg0; i < seg1 && ok; ++i) {
       const int32_t* seg = P.segs + (size_t)i * TS_REC;
       const int blk0 = seg[TS_BLK0], nb = seg[TS_BLK1] - blk0, kv_len = seg[TS_KVLEN];
-      if (!tree_wait(BAR(TB_QFULL), (i - seg0) & 1, abort_flag)) { ok = false; break; }
-      tc_fence_after();
-      // issue Q K^T of block j into its S buffer (K has arrived)
-      auto issue_qk = [&](int b, uint64_t kd, int kslot) {
-#pragma unroll
-        for (int p = 0; p < L::QP; ++p)
-#pragma unroll
-          for (int k = 0; k < L::DSTEPS; ++k) {
-            constexpr int SPP = L::ROWB / 32;        // steps of a row part
-            const uint64_t qd = q_desc0 + (((p * L::PARTS + k / SPP) * L::QPART + (k % SPP) * 32) >> 4);
-            const uint64_t bd = kd + (((k / SPP) * L::KVPART + (k % SPP) * 32) >> 4);
-            const uint32_t d_s = tmem + L::TM_S + b * BK;
-            if constexpr (L::F8) mma_f8_ss(d_s, qd, bd, id_qk, p + k > 0 ? 1u : 0u);
-            else mma_f16_ss(d_s, qd, bd, id_qk, k > 0 ? 1u : 0u);
-          }
-        mma_commit(BAR(TB_SFULL + b));
-        mma_commit(BAR(TB_KEMPTY + kslot));
-      };
-      // O += P V of block j (its S buffer b), and with `qk` the next block's Q K^T
-      // right behind it
-      auto pv = [&](int j, int b, uint32_t parity, bool qk, int qb, uint64_t kd) -> bool {
-        // Key steps past kv_len carry P = 0: skip them. Rows at or past kv_len in
-        // the last step are unused slots of the last page, or nothing: zero them,
-        // so that P = 0 never meets a non-finite value.
-        const int keys = min(kv_len - (blk0 + j) * BK, BK), ksteps = (keys + L::KSTEP - 1) / L::KSTEP;
-        const uint64_t vd = v_desc0 + (uint32_t)(vs * L::STAGE >> 4);
-        const uint32_t a_p = tmem + L::TM_S + b * BK;
-        if (keys % L::KSTEP) {
-          const uint32_t va = sbase + L::V_OFF + vs * L::STAGE;
-          constexpr int CPP = L::ROWB / 16;          // 16-byte chunks of a row part
-          for (int x = lane; x < (ksteps * L::KSTEP - keys) * L::PARTS * CPP; x += 32) {
-            const int r = keys + x / (L::PARTS * CPP), h = x / CPP % L::PARTS, c = x % CPP;
-            sts128(va + (uint32_t)(r / vb) * v_box + (h * vb + r % vb) * L::ROWB + c * 16, make_uint4(0, 0, 0, 0));
-          }
-          fence_proxy_async();
-          __syncwarp();
-        } else if (!tma) {
-          fence_proxy_async();
-        }
-        if (!tree_wait(BAR(TB_PFULL + b), parity, abort_flag)) return false;
+      auto keys_of = [&](int j) { return min(kv_len - (blk0 + j) * BK, BK); };
+      if (warp == 4) {
+        if (!tree_wait(BAR(TB_QFULL), (i - seg0) & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < L::KSTEPS; ++k)
-            if (k < ksteps) {
-              if constexpr (L::F8) {
-                mma_f8_ts(tmem + L::TM_O, a_p + k * 16, vd + v_step[k], id_pv, (j > 0 || k > 0) ? 1u : 0u);
-                mma_f8_ts(tmem + L::TM_O, a_p + k * 16 + 8, vd + v_step[k], id_pv, 1u);
-              } else {
-                mma_f16_ts(tmem + L::TM_O, a_p + k * 8, vd + v_step[k], id_pv, (j > 0 || k > 0) ? 1u : 0u);
-              }
-            }
-          mma_commit(BAR(TB_PVDONE + b));
-          mma_commit(BAR(TB_VEMPTY + vs));
-          if (qk) issue_qk(qb, kd, ks);
-        }
-        __syncwarp();
-        if (++vs == L::NV) { vs = 0; vph ^= 1; }
-        return true;
-      };
-      auto wait_k = [&]() -> bool {
-        if (!tree_wait(BAR(TB_KFULL + ks), kph, abort_flag)) return false;
-        if (!tma) fence_proxy_async();
-        return true;
-      };
-      auto next_k = [&]() {
-        if (++ks == L::NK) { ks = 0; kph ^= 1; }
-      };
-      for (int j = NSB > 1 ? 0 : -1; j < nb; ++j) {
-        // two S buffers: QK_j, then PV_{j-1}; one: PV_j, then QK_{j+1}
-        const int jq = NSB > 1 ? j : j + 1, jv = NSB > 1 ? j - 1 : j;
-        const uint64_t kd = k_desc0 + (uint32_t)(ks * L::STAGE >> 4);
-        const bool has_k = jq < nb;
-        if (has_k && !wait_k()) { ok = false; break; }
-        if constexpr (NSB > 1) {
-          tc_fence_after();
-          if (elect_one()) issue_qk((sc0 + jq) % NSB, kd, ks);
-          __syncwarp();
-          next_k();
-        }
-        if (jv >= 0) {
-          const int sc = sc0 + jv, b = sc % NSB;
-          if (!tree_wait(BAR(TB_VFULL + vs), vph, abort_flag)) { ok = false; break; }
-          if (!pv(jv, b, (sc / NSB) & 1, NSB == 1 && has_k, (sc + 1) % NSB, kd)) { ok = false; break; }
-        } else if (NSB == 1) {
-          tc_fence_after();
-          if (elect_one()) issue_qk(sc0 % NSB, kd, ks);
-          __syncwarp();
-        }
-        if (NSB == 1 && has_k) next_k();
       }
-      if (NSB > 1 && ok) {
-        const int sc = sc0 + nb - 1;
-        ok = tree_wait(BAR(TB_VFULL + vs), vph, abort_flag) && pv(nb - 1, sc % NSB, (sc / NSB) & 1, false, 0, 0);
+      if constexpr (NSB > 1) {
+        for (int j = 0; j < nb && ok; ++j) {
+          const int sc = sc0 + j, b = sc % NSB;
+          if (warp == 4) {
+            const uint64_t kd = k_desc0 + (uint32_t)(ks * L::STAGE >> 4);
+            ok = wait_k() && (sc < NSB || tree_wait(BAR(TB_PVDONE + b), (sc / NSB - 1) & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) issue_qk(b, kd, ks);
+            __syncwarp();
+            next_k();
+          } else {
+            ok = pv(j == 0, keys_of(j), b, (sc / NSB) & 1, false, 0, 0);
+          }
+        }
+      } else {
+        for (int j = -1; j < nb; ++j) {
+          const uint64_t kd = k_desc0 + (uint32_t)(ks * L::STAGE >> 4);
+          const bool has_k = j + 1 < nb;
+          if (has_k && !wait_k()) { ok = false; break; }
+          if (j >= 0) {
+            if (!pv(j == 0, keys_of(j), 0, (sc0 + j) & 1, has_k, 0, kd)) { ok = false; break; }
+          } else {
+            tc_fence_after();
+            if (elect_one()) issue_qk(0, kd, ks);
+            __syncwarp();
+          }
+          if (has_k) next_k();
+        }
       }
       sc0 += nb;
     }
@@ -914,7 +926,7 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
 #pragma unroll
           for (int q = 0; q < NQ; ++q) {
 #pragma unroll 4
-            for (int x = w; x < 32 / KPI; x += 3) {
+            for (int x = w; x < 32 / KPI; x += L::GW) {
               const int k = x * KPI + sub, key = q * 32 + k;
               const long long r = __shfl_sync(0xffffffffu, row[q], k) + step;
               cp_async16(dst + part * L::KVPART + L::swz(key, cc), kvg + r * (D * L::ES) + c * 16,
@@ -943,6 +955,10 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
   // every MMA has finished before TMEM is given back
   tc_fence_before();
   __syncthreads();
+  if (NSB > 1 && warp == 7) {
+    if (elect_one()) mma_commit(BAR(TB_FINAL));
+    __syncwarp();
+  }
   if (warp == 4) {
     if (elect_one()) mma_commit(BAR(TB_FINAL));
     __syncwarp();
