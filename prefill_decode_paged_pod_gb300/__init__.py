@@ -610,16 +610,27 @@ def _call(fn, dev, stream, *args):
         raise PodError(code, pod_last_error())
 
 
+def _empty(shape, dtype, dev, stream):
+    """A new output: memory of the stream that the call writes it on."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _device_of(t):
     if t is None or not t.is_cuda:
         raise PodError(1, "the tensors must be CUDA tensors")
     return t.device
 
 
-def _out_rows(name, out, rows, heads, d, dtype, dev):
+def _out_rows(name, out, rows, heads, d, dtype, dev, stream):
     """An output [rows, heads, d]: a new tensor, or the caller's with its row stride."""
     if out is None:
-        return _torch().empty((rows, heads, d), dtype=dtype, device=dev), heads * d
+        return _empty((rows, heads, d), dtype, dev, stream), heads * d
     n, h, dd, stride = _heads(name, out, dtype, dev, rows)
     if (h, dd) != (heads, d):
         raise PodError(1, f"{name} must be {(rows, heads, d)}")
@@ -646,14 +657,14 @@ def pod_qk_norm_rope(q, k, positions=None, *, q_weight=None, k_weight=None, eps=
     H = Hk = qs = ks = qos = kos = qp = kp = qop = kop = 0
     if q is not None:
         rows, H, d, qs = _heads("q", q, dtype, dev)
-        q_out, qos = _out_rows("q_out", q_out, rows, H, d, dtype, dev)
+        q_out, qos = _out_rows("q_out", q_out, rows, H, d, dtype, dev, stream)
         qp, qop = q.data_ptr(), q_out.data_ptr()
     if k is not None:
         rows, Hk, dk, ks = _heads("k", k, dtype, dev, None if q is None else rows)
         if q is not None and dk != d:
             raise PodError(1, "q and k have different head_dim")
         d = dk
-        k_out, kos = _out_rows("k_out", k_out, rows, Hk, d, dtype, dev)
+        k_out, kos = _out_rows("k_out", k_out, rows, Hk, d, dtype, dev, stream)
         kp, kop = k.data_ptr(), k_out.data_ptr()
     pos, R = _rotation(positions, rows, rotary_dim, d, dev)
     wq = 0 if q_weight is None else _vector("q_weight", q_weight, d, dtype, dev)
@@ -705,7 +716,7 @@ def pod_norm_rope_append(q, k, v, positions, kv_cache, slots, *, q_weight=None, 
         _, H, dq, qs = _heads("q", q, dtype, dev, rows)
         if dq != d:
             raise PodError(1, "q and k have different head_dim")
-        q_out, qos = _out_rows("q_out", q_out, rows, H, d, dtype, dev)
+        q_out, qos = _out_rows("q_out", q_out, rows, H, d, dtype, dev, stream)
         qp, qop = q.data_ptr(), q_out.data_ptr()
     pos, R = _rotation(positions, rows, rotary_dim, d, dev)
     wq = 0 if q_weight is None else _vector("q_weight", q_weight, d, dtype, dev)
@@ -730,7 +741,7 @@ def pod_gather_kv(kv_cache, slots, *, dtype, kv_scales=None, k_scale=1.0, v_scal
     rows = slots.shape[0] if slots.dim() == 1 else -1
     sl = _vector("slots", slots, rows, torch.int64, dev)
     if out is None:
-        out = torch.empty((rows, 2, hk, d), dtype=dtype, device=dev)
+        out = _empty((rows, 2, hk, d), dtype, dev, stream)
     else:
         _on_device("out", out, dev, dtype, 4)
         if tuple(out.shape) != (rows, 2, hk, d):
@@ -849,11 +860,11 @@ def pod_tree_run(h: PodTreeHandle, q, kv, workspace, tree_mask=None, kv_scales=N
     if workspace.device != dev:
         raise PodError(1, f"the workspace must be on {dev}")
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
+        out = _empty(shape, dtype, dev, stream)
     elif out.shape != shape or out.dtype != dtype or out.device != dev or not out.is_contiguous():
         raise PodError(1, f"out must be contiguous {dtype} {shape} on {dev}")
     if lse is None:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+        lse = _empty(shape[:2], torch.float32, dev, stream)
     elif lse.shape != shape[:2] or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
         raise PodError(1, f"lse must be contiguous float32 {shape[:2]} on {dev}")
     _call(lib.pod_tree_run, dev, stream, h.ptr, q.data_ptr(), kv.data_ptr(), sp, mp, mn, kp, workspace.data_ptr(),

@@ -229,10 +229,10 @@ POD_DEV uint32_t idesc_f16(bool bf16, int M, int N, bool a_mn, bool b_mn) {
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Instruction descriptor for kind::f8f6f4 with E4M3 operands (format 0 of A
-// and B) and fp32 accumulation; the other bits as above.
-POD_DEV uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {
-  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+// Instruction descriptor for kind::f8f6f4 with fp32 accumulation: B is E4M3
+// (format 0), A E4M3 or E5M2 (format 1); the other bits as above.
+POD_DEV uint32_t idesc_f8(bool a_e5m2, int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_e5m2 ? 1u : 0u) << 7) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
@@ -482,6 +482,12 @@ POD_DEV void mma16832_e4m3(float* c, const uint32_t* a, uint32_t b0, uint32_t b1
 POD_DEV uint32_t f32x2_to_e4m3x2(float lo, float hi) {
   uint16_t d;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// the same to E5M2
+POD_DEV uint32_t f32x2_to_e5m2x2(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
   return d;
 }
 // a packed fp16 pair to two E4M3 codes, the low half to the low byte

@@ -29,9 +29,11 @@
 // its largest value to [128, 256) and split into E4M3 parts, two for bf16 rows
 // (4 + 4 significant bits, all it has), three for fp16 rows (11 bits); parts
 // below 2^-17 of the row's largest value lose bits. P (the largest
-// between 2^6 and 2^8.5) is carried in two E4M3 parts by Veltkamp splitting: 4
-// bits, then the remainder to 4 bits, at most 2^-9 of p off, and 2^-15 of the
-// largest weight at the bottom. (An
+// between 2^6 and 2^8.5) is carried in parts by Veltkamp splitting. bf16 results:
+// two E4M3 parts, 4 bits and the remainder to 4 bits, at most 2^-9 of p off, and
+// 2^-15 of the largest weight at the bottom. fp16 results: 4 bits in E4M3 and
+// twice 3 bits in E5M2, whose range goes on below, 2^-11 of p and 2^-23 of the
+// largest weight. (An
 // earlier form widened the codes to fp16 in shared memory; the two warps that
 // did it set the pace: 620 us for 96 requests of 8192 keys.) Per-tensor scales
 // are constants of the softmax and of the output. Block scales are powers of
@@ -65,6 +67,7 @@ struct TLayout {
   static constexpr int PARTS = D * ES / ROWB;          // row parts
   static constexpr int PEL = ROWB / ES;                // elements of a row part
   static constexpr int QP = !F8 ? 1 : Pack<T>::kBF16 ? 2 : 3;   // precision parts of Q
+  static constexpr int PP = QP;                        // parts of P
   static constexpr int QPART = POD_TREE_TILE * ROWB;   // one row part of one precision part
   static constexpr int KVPART = BK * ROWB;             // one row part of a block of K or V
   static constexpr int STAGE = PARTS * KVPART;
@@ -196,25 +199,45 @@ POD_DEV void sts16(uint32_t a, uint32_t v) {
 // bf16 of a power of two (exact, subnormals too): its upper 16 bits
 POD_DEV uint32_t pow2_bf16(float v) { return __float_as_uint(v) >> 16; }
 
-// Four values below 448 (two pairs) as E4M3 words hi + lo (byte i: value i).
-// Veltkamp splitting: hi is x to 4 significant bits, lo the remainder to 4 bits.
-POD_DEV void e4m3_split4(uint64_t x01, uint64_t x23, uint32_t& hi, uint32_t& lo) {
-  const uint64_t c = pack2(1048577.f, 1048577.f), neg = pack2(-1.f, -1.f);   // 2^20 + 1
+// x to BITS significant bits by Veltkamp splitting.
+template <int BITS>
+POD_DEV uint64_t head2(uint64_t x) {
+  const float c = (float)((1 << (24 - BITS)) + 1);
+  const uint64_t t = mul2(x, pack2(c, c));
+  return add2(t, fma2(t, pack2(-1.f, -1.f), x));     // (products with -1 are exact)
+}
+// Four values below 448 (two pairs) in parts whose sum they are (byte i: value i):
+// two E4M3 words, or (three parts) an E4M3 and two E5M2 words.
+template <int PARTS>
+POD_DEV void split4(uint64_t x01, uint64_t x23, uint32_t* w) {
+  const uint64_t neg = pack2(-1.f, -1.f);
   const uint64_t x[2] = {x01, x23};
-  uint32_t h[2], l[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint64_t t = mul2(x[i], c);
-    const uint64_t v = add2(t, fma2(t, neg, x[i]));  // (products with -1 are exact)
-    const uint64_t r = fma2(v, neg, x[i]);
+    uint64_t v = head2<4>(x[i]);
+    // three parts: below E4M3's normal range the head is a multiple of 2^-9, so
+    // that the code is exactly it and the rest goes to the other parts
+    if (PARTS == 3) v = add2(add2(v, pack2(24576.f, 24576.f)), pack2(-24576.f, -24576.f));
+    uint64_t r = fma2(v, neg, x[i]);
     float a, b;
     unpack2(v, a, b);
-    h[i] = f32x2_to_e4m3x2(a, b);
-    unpack2(r, a, b);
-    l[i] = f32x2_to_e4m3x2(a, b);
+    const uint32_t h = f32x2_to_e4m3x2(a, b);
+    w[0] = i ? w[0] | (h << 16) : h;
+    if constexpr (PARTS == 2) {
+      unpack2(r, a, b);
+      const uint32_t l = f32x2_to_e4m3x2(a, b);
+      w[1] = i ? w[1] | (l << 16) : l;
+    } else {
+      const uint64_t m = head2<3>(r);
+      r = fma2(m, neg, r);
+      unpack2(m, a, b);
+      const uint32_t l = f32x2_to_e5m2x2(a, b);
+      w[1] = i ? w[1] | (l << 16) : l;
+      unpack2(r, a, b);
+      const uint32_t k = f32x2_to_e5m2x2(a, b);
+      w[2] = i ? w[2] | (k << 16) : k;
+    }
   }
-  hi = h[0] | (h[1] << 16);
-  lo = l[0] | (l[1] << 16);
 }
 
 // exponent byte -> 2^(byte - 127), and 2^(byte - ref) for byte <= ref
@@ -452,9 +475,9 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
     const bool rescale = top > m_ref + L::LIMIT;     // also for the first finite maximum
     const float m_use = rescale ? top - L::TOP : m_ref;
     const float m_sub = m_use == NEG_INF ? 0.f : m_use;
-    // P goes over S: 16-bit, two keys a column; E4M3, four keys a column, 8
-    // columns of high parts and 8 of low parts for each 32 keys. Run h of P lies
-    // over columns of S that run h or an earlier one has read.
+    // P goes over S: 16-bit, two keys a column; FP8, four keys a column, 8 columns
+    // of each part for each 32 keys. Run h of P lies over columns of S that run h
+    // or an earlier one has read.
     const uint64_t qs2 = pack2(qscale, qscale), ms2 = pack2(-m_sub, -m_sub);
     uint64_t rs[2] = {0, 0};
 #pragma unroll
@@ -471,14 +494,14 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
           e[i / 2] = pack2(ex2(a), ex2(b2));
           rs[i / 2 & 1] = add2(rs[i / 2 & 1], e[i / 2]);
         }
-        uint32_t hi[8];
-        const uint32_t col = (uint32_t)(my0 + h * W + q) / (L::F8 ? 2 : N / 8);
+        const uint32_t col = (uint32_t)(my0 + h * W + q) / N * (8 * L::PP);
+        uint32_t parts[L::PP][8];
         if constexpr (!L::F8) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             float a, b2;
             unpack2(e[i], a, b2);
-            hi[i] = Pack<T>::two(a, b2);
+            parts[0][i] = Pack<T>::two(a, b2);
           }
         } else {
           if constexpr (KV == 2) {
@@ -490,19 +513,25 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
               e[i / 2 + 1] = mul2(e[i / 2 + 1], f[1]);
             }
           }
-          uint32_t lo[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) e4m3_split4(e[2 * i], e[2 * i + 1], hi[i], lo[i]);
-          tmem_st8(s_addr + col + 8, lo);
+          for (int i = 0; i < 8; ++i) {
+            uint32_t w[L::PP];
+            split4<L::PP>(e[2 * i], e[2 * i + 1], w);
+#pragma unroll
+            for (int p = 0; p < L::PP; ++p) parts[p][i] = w[p];
+          }
         }
-        tmem_st8(s_addr + col, hi);
+#pragma unroll
+        for (int p = 0; p < L::PP; ++p) tmem_st8(s_addr + col + 8 * p, parts[p]);
       }
     }
     if constexpr (C > 1) {                           // zeros for the other copies' keys
       const uint32_t zero[8] = {};
 #pragma unroll
-      for (int c = 0; c < BK / 2; c += 8)
-        if (c / (BK / 2 / C) != cp) tmem_st8(s_addr + c, zero);
+      for (int c = 0; c < BK / L::KSTEP; ++c)        // key steps
+        if (c / (BK / L::KSTEP / C) != cp)
+#pragma unroll
+          for (int p = 0; p < L::PP; ++p) tmem_st8(s_addr + 8 * (c * L::PP + p), zero);
     }
     const bool need = (rescale && m_ref != NEG_INF) || (KV == 2 && o_scale != 1.f);
     if (j > 0 && __any_sync(0xffffffffu, need)) {
@@ -718,8 +747,8 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
     // waits of one product off the other's: 16 requests of 64 tokens and 4100 keys
     // went from 137 to 129 us with pages of 64; with pages of 16 they stay at 136,
     // bound by their 12 boxes a block.
-    const uint32_t id_qk = L::F8 ? idesc_e4m3(128, BK, false, false) : idesc_f16(Pack<T>::kBF16, 128, BK, false, false);
-    const uint32_t id_pv = L::F8 ? idesc_e4m3(128, D, false, true) : idesc_f16(Pack<T>::kBF16, 128, D, false, true);
+    const uint32_t id_qk = L::F8 ? idesc_f8(false, 128, BK, false, false) : idesc_f16(Pack<T>::kBF16, 128, BK, false, false);
+    const uint32_t id_pv = L::F8 ? idesc_f8(false, 128, D, false, true) : idesc_f16(Pack<T>::kBF16, 128, D, false, true);
     // V stage: 16-bit TMA boxes of vb keys lie as [box][row part][key], anything
     // else as [row part][key]
     const int vb = !L::F8 && tma ? P.kbx : BK;
@@ -787,8 +816,11 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
         for (int k = 0; k < L::KSTEPS; ++k)
           if (k < ksteps) {
             if constexpr (L::F8) {
-              mma_f8_ts(tmem + L::TM_O, a_p + k * 16, vd + v_step[k], id_pv, (!first || k > 0) ? 1u : 0u);
-              mma_f8_ts(tmem + L::TM_O, a_p + k * 16 + 8, vd + v_step[k], id_pv, 1u);
+#pragma unroll
+              for (int p = 0; p < L::PP; ++p)
+                mma_f8_ts(tmem + L::TM_O, a_p + 8 * (k * L::PP + p), vd + v_step[k],
+                          p > 0 && L::PP == 3 ? idesc_f8(true, 128, D, false, true) : id_pv,
+                          (!first || k > 0 || p > 0) ? 1u : 0u);
             } else {
               mma_f16_ts(tmem + L::TM_O, a_p + k * 8, vd + v_step[k], id_pv, (!first || k > 0) ? 1u : 0u);
             }

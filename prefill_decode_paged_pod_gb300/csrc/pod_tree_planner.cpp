@@ -89,7 +89,7 @@ int pod_tree_build_plan(const PodTreeArgs& a, PodTreePlanHost& o, std::string* e
     if (np > 0 && (a.last_page_len[r] < 1 || a.last_page_len[r] > a.ps))
       return bad(INV, who + "last_page_len is outside [1, page_size]");
     const long long len = np > 0 ? (np - 1) * a.ps + a.last_page_len[r] : 0;
-    if (len > 0x7fffff00ll) return bad(INV, who + "too many keys");
+    if (len > (1ll << 30)) return bad(INV, who + "more than 2^30 keys");   // (key numbers stay below 2^31 in the kernels)
     if (nq > len) return bad(INV, who + "the tree's tokens must be in the cache (kv_len >= q_len)");
     if (nq * o.G > 0x7fffff00ll) return bad(INV, who + "too many query rows");
     if (np > 0 && !a.kv_indices) return bad(INV, "kv_indices is NULL");

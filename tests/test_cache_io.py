@@ -388,6 +388,30 @@ def test_graph_and_stream():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("as_int", [False, True])
+def test_a_stream_of_the_callers(as_int):
+    """Given streams are launched on, and own the outputs made for them."""
+    x = rows_of((50, 6, 64), torch.float16, 1).cuda()
+    pos = torch.arange(50, dtype=torch.int32).cuda()
+    want = pod.pod_qk_norm_rope(x[:, :4], x[:, 4:], pos)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    s = side.cuda_stream if as_int else side
+    hold = torch.zeros(1 << 24, device="cuda")
+    for _ in range(3):
+        got = pod.pod_qk_norm_rope(x[:, :4], x[:, 4:], pos, stream=s)
+        junk = [torch.full((50, 4, 64), 9.0, dtype=torch.float16, device="cuda") for _ in range(4)]
+        hold.add_(1)
+        side.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        del junk, got
+    with torch.cuda.stream(side):
+        got = pod.pod_qk_norm_rope(x[:, :4], x[:, 4:], pos)
+    side.synchronize()
+    assert torch.equal(got[0], want[0])
+
+
+@pytest.mark.gpu
 def test_serving_step_over_a_written_cache():
     """Rows written with per-tensor scales are what the FP8 decode half reads,
     and the same cache read back runs in the 16-bit prefill half."""

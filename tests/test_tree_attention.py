@@ -9,7 +9,10 @@ Tolerances, fixed before the first run. An output is sum_t p_t v_t / l:
     significant bits leaves at most 2^-4 of x's binade 2^e, 4 bits of that leave
     2^-9 * 2^e, so 2^-9 of x; below E4M3's normal range (2^-6) the parts are
     multiples of 2^-9, at most 2^-10 off each, together 2^-9, which is 2^-15 of
-    the largest weight. With
+    the largest weight. With fp16 results the remainder is two E5M2 parts of 3
+    bits instead: 3 bits of at most 2^-4 * 2^e leave 2^-8 * 2^e, 3 bits of that
+    2^-12 * 2^e; E5M2 ends at multiples of 2^-16, 2^-17 off, 2^-23 of the largest
+    weight (2^-22 for the two). With
     block scales the weights are relative to the largest V scale. So at most
     u * sum p |v| / l + floor * sum |v in those units| / l;
   - the logits: products are exact in fp32, their sum of d terms is off by at
@@ -123,8 +126,11 @@ class Case:
     def check(self, out, lse, rows=None):
         out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
         G = self.H // self.Hk
-        u_p = 2.0 ** -9 if self.fmt != "16bit" else 2.0 ** -8 if self.dtype == torch.bfloat16 else 2.0 ** -11
-        tiny = 2.0 ** -15 if self.fmt != "16bit" else 0.0 if self.dtype == torch.bfloat16 else 2.0 ** -25
+        bf = self.dtype == torch.bfloat16
+        if self.fmt == "16bit":
+            u_p, tiny = (2.0 ** -8, 0.0) if bf else (2.0 ** -11, 2.0 ** -25)
+        else:
+            u_p, tiny = (2.0 ** -9, 2.0 ** -15) if bf else (2.0 ** -12, 2.0 ** -22)
         eps = torch.finfo(self.dtype).eps / 2
         for r in range(len(self.n)):
             n, L = self.n[r], self.kv_len[r]
@@ -464,7 +470,7 @@ def plan_call(**kw):
     (dict(qi=[0, 4, 3]), 1, "decreases"), (dict(ki=[0, 3, 2]), 1, "decreases"), (dict(qi=None), 1, "NULL"),
     (dict(idx=None), 1, "NULL"), (dict(dt=3), 2, "dtype"), (dict(fmt=3), 1, "format"), (dict(lay=2), 1, "kv_layout"),
     (dict(fmt=1, ks=0.0), 1, "k_scale"), (dict(fmt=1, vs=math.inf), 1, "v_scale"), (dict(scale=math.nan), 1, "sm_scale"),
-    (dict(batch=-1), 1, "batch"), (dict(pages=2 ** 30), 1, "too large"),
+    (dict(ki=[0, 2, 2 ** 30 // 16 + 4], idx=[0] * (2 ** 30 // 16 + 4)), 1, "2^30 keys"), (dict(batch=-1), 1, "batch"), (dict(pages=2 ** 30), 1, "too large"),
 ])
 def test_plan_refusals(kw, code, text):
     assert plan_call(**kw) == code and text in pod.pod_last_error(), pod.pod_last_error()
