@@ -502,17 +502,40 @@ def pod_kv_slots(kv_indptr, kv_indices, page_size: int, request, position):
     return page * page_size + position % page_size
 
 
-def _on_device(name, t, dev, dtype, ndim):
-    if t.device != dev or t.dtype != dtype or t.dim() != ndim or not t.is_contiguous():
-        raise PodError(1, f"{name} must be a contiguous {ndim}-d {dtype} tensor on {dev}")
+_KV_FORMATS = {"16bit": 0, "scaled": 1, "block": 2}
+_torch_module = None
+
+
+def _torch():
+    """torch, imported on first use, with what the calls below ask of it every
+    time: the current device and its current stream (small calls take as long as
+    their host side)."""
+    global _torch_module, _raw_stream, _current_device
+    if _torch_module is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _current_device = torch.cuda.current_device
+        _torch_module = torch
+    return _torch_module
+
+
+def _device_of(t):
+    """Index of a CUDA tensor's device."""
+    if t is None or not t.is_cuda:
+        raise PodError(1, "the tensors must be CUDA tensors")
+    return t.get_device()
 
 
 def _heads(name, t, dtype, dev, rows=None):
     """[rows, heads, d] with contiguous heads; returns (rows, heads, d, row stride)."""
-    if t.dim() != 3 or t.dtype != dtype or t.device != dev:
-        raise PodError(1, f"{name} must be a [rows, heads, head_dim] {dtype} tensor on {dev}")
-    n, h, d = t.shape
-    sn, sh, sd = t.stride()
+    try:
+        n, h, d = t.shape
+        sn, sh, sd = t.stride()
+    except ValueError:
+        n = -1
+    if n < 0 or t.dtype != dtype or t.get_device() != dev:
+        raise PodError(1, f"{name} must be a [rows, heads, head_dim] {dtype} tensor on cuda:{dev}")
     if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise PodError(1, f"{name}: the heads of a row must be contiguous")
     if rows is not None and n != rows:
@@ -520,10 +543,10 @@ def _heads(name, t, dtype, dev, rows=None):
     return n, h, d, sn if n > 1 else max(sn, h * d) // 8 * 8
 
 
-def _vector(name, t, n, dtype, dev):
-    """Pointer of a contiguous [n] tensor."""
-    if t.dtype != dtype or t.device != dev or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise PodError(1, f"{name} must be a contiguous {dtype} tensor of {n} elements on {dev}")
+def _whole(name, t, shape, dtype, dev):
+    """Pointer of a contiguous tensor of this shape."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        raise PodError(1, f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on cuda:{dev}")
     return t.data_ptr()
 
 
@@ -534,18 +557,15 @@ def _rotation(positions, rows, rotary_dim, d, dev):
         if R:
             raise PodError(1, "the rotation needs positions")
         return 0, R
-    return _vector("positions", positions, rows, _torch().int32, dev), R
+    return _whole("positions", positions, (rows,), _torch_module.int32, dev), R
 
 
 def _status(status, dev):
     if status is None:
         return 0
-    if status.dtype != _torch().int32 or status.device != dev or status.numel() < 1:
-        raise PodError(1, f"status must be an int32 tensor on {dev}")
+    if status.dtype != _torch_module.int32 or status.get_device() != dev or status.numel() < 1:
+        raise PodError(1, f"status must be an int32 tensor on cuda:{dev}")
     return status.data_ptr()
-
-
-_KV_FORMATS = {"16bit": 0, "scaled": 1, "block": 2}
 
 
 def _cache_args(kv_cache, kv_scales, kv_layout, dtype, dev):
@@ -555,84 +575,59 @@ def _cache_args(kv_cache, kv_scales, kv_layout, dtype, dev):
     if hnd is None:
         raise PodError(1, f"unknown kv layout {kv_layout!r}")
     shape, kt = kv_cache.shape, kv_cache.dtype
-    if len(shape) != 5 or shape[1] != 2 or kv_cache.device != dev or not kv_cache.is_contiguous():
-        raise PodError(1, f"kv_cache must be a contiguous [pages, 2, ...] page pool on {dev}")
-    pages, _, a, b, d = shape
-    ps, hk = (b, a) if hnd else (a, b)
+    if len(shape) != 5 or shape[1] != 2 or kv_cache.get_device() != dev or not kv_cache.is_contiguous():
+        raise PodError(1, f"kv_cache must be a contiguous [pages, 2, ...] page pool on cuda:{dev}")
+    pages, _, ps, hk, d = shape
+    if hnd:
+        ps, hk = hk, ps
+    sp = 0
     if kt == dtype:
         fmt = 0
-    elif kt == _torch().float8_e4m3fn:
-        fmt = 1 if kv_scales is None else 2
-    else:
-        raise PodError(2, f"kv_cache must be {dtype} or float8_e4m3fn, not {kt}")
-    sp = 0
-    if kv_scales is not None:
-        if fmt == 0:
+        if kv_scales is not None:
             raise PodError(1, "kv_scales given, but the cache is a 16-bit one")
-        if (kv_scales.dtype != _torch().uint8 or kv_scales.device != dev or kv_scales.shape != shape[:4]
-                or not kv_scales.is_contiguous()):
-            raise PodError(1, f"kv_scales must be contiguous uint8 {tuple(shape[:4])} on {dev}")
-        sp = kv_scales.data_ptr()
+    elif kt != _torch_module.float8_e4m3fn:
+        raise PodError(2, f"kv_cache must be {dtype} or float8_e4m3fn, not {kt}")
+    elif kv_scales is None:
+        fmt = 1
+    else:
+        fmt = 2
+        sp = _whole("kv_scales", kv_scales, shape[:4], _torch_module.uint8, dev)
     return kv_cache.data_ptr(), sp, pages, ps, hk, d, hnd, fmt
 
 
-_torch_module = None
-
-
-def _torch():
-    global _torch_module
-    if _torch_module is None:
-        import torch
-        _torch_module = torch
-    return _torch_module
-
-
 def _call(fn, dev, stream, *args):
-    """fn(*args, stream) with the tensors' device current (it is made so where
-    it is not) and, without a given stream, torch's current stream of that
-    device. Small calls take as long as their host side, so the usual case asks
-    torch as little as it can."""
-    torch = _torch()
-    index = dev.index
+    """fn(*args, stream) with device `dev` current (it is made so where it is
+    not) and, without a given stream, torch's current stream of that device."""
     if stream is None:
-        try:
-            s = torch._C._cuda_getCurrentRawStream(index)
-        except AttributeError:
-            s = torch.cuda.current_stream(dev).cuda_stream
+        s = _raw_stream(dev)
     else:
         s = stream if isinstance(stream, int) else stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    if _current_device() == dev:
         code = fn(*args, s)
     else:
-        with torch.cuda.device(dev):
+        with _torch_module.cuda.device(dev):
             code = fn(*args, s)
     if code != POD_OK:
         raise PodError(code, pod_last_error())
 
 
-def _empty(shape, dtype, dev, stream):
-    """A new output: memory of the stream that the call writes it on."""
-    torch = _torch()
+def _empty(shape, dtype, t, stream):
+    """A new output on t's device: memory of the stream that the call writes it on."""
+    torch = _torch_module
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=t.device)
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+        stream = torch.cuda.ExternalStream(stream, device=t.device) if stream else torch.cuda.default_stream(t.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=t.device)
 
 
-def _device_of(t):
-    if t is None or not t.is_cuda:
-        raise PodError(1, "the tensors must be CUDA tensors")
-    return t.device
-
-
-def _out_rows(name, out, rows, heads, d, dtype, dev, stream):
-    """An output [rows, heads, d]: a new tensor, or the caller's with its row stride."""
+def _out_rows(name, out, like, rows, heads, d, dtype, dev, stream):
+    """(output [rows, heads, d], its row stride): new, or the caller's."""
     if out is None:
-        return _empty((rows, heads, d), dtype, dev, stream), heads * d
+        return _empty((rows, heads, d), dtype, like, stream), heads * d
     n, h, dd, stride = _heads(name, out, dtype, dev, rows)
-    if (h, dd) != (heads, d):
+    if h != heads or dd != d:
         raise PodError(1, f"{name} must be {(rows, heads, d)}")
     return out, stride
 
@@ -651,24 +646,25 @@ def pod_qk_norm_rope(q, k, positions=None, *, q_weight=None, k_weight=None, eps=
     either may be None. Returns (q_out, k_out); pass q_out=q, k_out=k to work
     in place."""
     lib = _lib or load_library()
+    _torch()
     t = q if q is not None else k
     dev, dtype = _device_of(t), t.dtype
     code = _dtype_code(dtype)
     H = Hk = qs = ks = qos = kos = qp = kp = qop = kop = 0
     if q is not None:
         rows, H, d, qs = _heads("q", q, dtype, dev)
-        q_out, qos = _out_rows("q_out", q_out, rows, H, d, dtype, dev, stream)
+        q_out, qos = _out_rows("q_out", q_out, t, rows, H, d, dtype, dev, stream)
         qp, qop = q.data_ptr(), q_out.data_ptr()
     if k is not None:
         rows, Hk, dk, ks = _heads("k", k, dtype, dev, None if q is None else rows)
         if q is not None and dk != d:
             raise PodError(1, "q and k have different head_dim")
         d = dk
-        k_out, kos = _out_rows("k_out", k_out, rows, Hk, d, dtype, dev, stream)
+        k_out, kos = _out_rows("k_out", k_out, t, rows, Hk, d, dtype, dev, stream)
         kp, kop = k.data_ptr(), k_out.data_ptr()
     pos, R = _rotation(positions, rows, rotary_dim, d, dev)
-    wq = 0 if q_weight is None else _vector("q_weight", q_weight, d, dtype, dev)
-    wk = 0 if k_weight is None else _vector("k_weight", k_weight, d, dtype, dev)
+    wq = 0 if q_weight is None else _whole("q_weight", q_weight, (d,), dtype, dev)
+    wk = 0 if k_weight is None else _whole("k_weight", k_weight, (d,), dtype, dev)
     _call(lib.pod_qk_norm_rope, dev, stream, _IO_ARGS.pack(
         qp, kp, 0, wq, wk, pos, 0, qop, kop, 0, 0, 0, qs, ks, 0, qos, kos, rows, 0, 0, H, Hk, d, 0, 0, code, R,
         bool(interleaved), eps, rope_scale, rope_theta, 1.0, 1.0))
@@ -677,13 +673,14 @@ def pod_qk_norm_rope(q, k, positions=None, *, q_weight=None, k_weight=None, eps=
 
 def _written(k, v, kv_cache, kv_scales, kv_layout, slots):
     """Checks of the rows of a write: (device, dtype, rows, k stride, v stride, slots pointer, cache args)."""
+    torch = _torch()
     dev, dtype = _device_of(k), k.dtype
     rows, hk, d, ks = _heads("k", k, dtype, dev)
     _, hv, dv, vs = _heads("v", v, dtype, dev, rows)
     cache = _cache_args(kv_cache, kv_scales, kv_layout, dtype, dev)
     if hv != hk or dv != d or cache[4] != hk or cache[5] != d:
         raise PodError(1, "k, v and kv_cache differ in heads or head_dim")
-    return dev, dtype, rows, ks, vs, _vector("slots", slots, rows, _torch().int64, dev), cache
+    return dev, dtype, rows, ks, vs, _whole("slots", slots, (rows,), torch.int64, dev), cache
 
 
 def pod_append_kv(k, v, kv_cache, slots, *, kv_scales=None, k_scale=1.0, v_scale=1.0, kv_layout="NHD",
@@ -716,11 +713,11 @@ def pod_norm_rope_append(q, k, v, positions, kv_cache, slots, *, q_weight=None, 
         _, H, dq, qs = _heads("q", q, dtype, dev, rows)
         if dq != d:
             raise PodError(1, "q and k have different head_dim")
-        q_out, qos = _out_rows("q_out", q_out, rows, H, d, dtype, dev, stream)
+        q_out, qos = _out_rows("q_out", q_out, k, rows, H, d, dtype, dev, stream)
         qp, qop = q.data_ptr(), q_out.data_ptr()
     pos, R = _rotation(positions, rows, rotary_dim, d, dev)
-    wq = 0 if q_weight is None else _vector("q_weight", q_weight, d, dtype, dev)
-    wk = 0 if k_weight is None else _vector("k_weight", k_weight, d, dtype, dev)
+    wq = 0 if q_weight is None else _whole("q_weight", q_weight, (d,), dtype, dev)
+    wk = 0 if k_weight is None else _whole("k_weight", k_weight, (d,), dtype, dev)
     _call(lib.pod_norm_rope_append, dev, stream, _IO_ARGS.pack(
         qp, k.data_ptr(), v.data_ptr(), wq, wk, pos, sl, qop, 0, cache, scales, _status(status, dev), qs, ks, vs,
         qos, 0, rows, pages, ps, H, hk, d, hnd, fmt, _dtype_code(dtype), R, bool(interleaved), eps, rope_scale,
@@ -738,16 +735,15 @@ def pod_gather_kv(kv_cache, slots, *, dtype, kv_scales=None, k_scale=1.0, v_scal
     dev = _device_of(kv_cache)
     code = _dtype_code(dtype)
     cache, scales, pages, ps, hk, d, hnd, fmt = _cache_args(kv_cache, kv_scales, kv_layout, dtype, dev)
-    rows = slots.shape[0] if slots.dim() == 1 else -1
-    sl = _vector("slots", slots, rows, torch.int64, dev)
+    rows = slots.numel()
+    sl = _whole("slots", slots, (rows,), torch.int64, dev)
     if out is None:
-        out = _empty((rows, 2, hk, d), dtype, dev, stream)
+        out = _empty((rows, 2, hk, d), dtype, kv_cache, stream)
+        op = out.data_ptr()
     else:
-        _on_device("out", out, dev, dtype, 4)
-        if tuple(out.shape) != (rows, 2, hk, d):
-            raise PodError(1, f"out must be {(rows, 2, hk, d)}")
+        op = _whole("out", out, (rows, 2, hk, d), dtype, dev)
     _call(lib.pod_gather_kv, dev, stream, _IO_ARGS.pack(
-        0, 0, 0, 0, 0, 0, sl, 0, out.data_ptr(), cache, scales, _status(status, dev), 0, 0, 0, 0, 0, rows, pages, ps,
+        0, 0, 0, 0, 0, 0, sl, 0, op, cache, scales, _status(status, dev), 0, 0, 0, 0, 0, rows, pages, ps,
         0, hk, d, hnd, fmt, code, 0, 0, 0.0, 1.0, 1.0, k_scale, v_scale))
     return out
 
@@ -825,6 +821,7 @@ def pod_tree_workspace_size(h: PodTreeHandle) -> int:
 
 
 def pod_tree_bind_workspace(h: PodTreeHandle, workspace, stream=None):
+    _torch()
     _call(load_library().pod_tree_bind_workspace, _device_of(workspace), stream, h.ptr, workspace.data_ptr(),
           workspace.numel() * workspace.element_size())
     h.workspace_ptr = workspace.data_ptr()
@@ -839,41 +836,37 @@ def pod_tree_run(h: PodTreeHandle, q, kv, workspace, tree_mask=None, kv_scales=N
     torch = _torch()
     dev, dtype = _device_of(q), h.dtype
     shape, pool = (h.rows, h.num_qo_heads, h.head_dim), h.pool_shape
-    if q.shape != shape or q.dtype != dtype or not q.is_contiguous():
-        raise PodError(1, f"q must be contiguous {dtype} {shape}")
-    if kv.shape != pool or kv.dtype != (torch.float8_e4m3fn if h.kv_format else dtype) or kv.device != dev \
-            or not kv.is_contiguous():
-        raise PodError(1, f"kv must be a contiguous {pool} cache of the plan's format on {dev}")
+    qp = _whole("q", q, shape, dtype, dev)
+    cp = _whole("kv", kv, pool, torch.float8_e4m3fn if h.kv_format else dtype, dev)
     sp = mp = mn = kp = 0
     if kv_scales is not None:
-        if kv_scales.shape != pool[:4] or kv_scales.dtype != torch.uint8 or kv_scales.device != dev \
-                or not kv_scales.is_contiguous():
-            raise PodError(1, f"kv_scales must be contiguous uint8 {pool[:4]} on {dev}")
-        sp = kv_scales.data_ptr()
+        sp = _whole("kv_scales", kv_scales, pool[:4], torch.uint8, dev)
     if tree_mask is not None:
         mn = tree_mask.numel()
-        mp = _vector("tree_mask", tree_mask, mn, torch.uint8, dev)
-        if mp == 0 and mn == 0 and h.mask_bytes:
+        mp = _whole("tree_mask", tree_mask, (mn,), torch.uint8, dev)
+        if mn < h.mask_bytes:
             raise PodError(1, f"tree_mask needs {h.mask_bytes} bytes")
     if sinks is not None:
-        kp = _vector("sinks", sinks, h.num_qo_heads, torch.float32, dev)
-    if workspace.device != dev:
-        raise PodError(1, f"the workspace must be on {dev}")
+        kp = _whole("sinks", sinks, (h.num_qo_heads,), torch.float32, dev)
+    if workspace.get_device() != dev:
+        raise PodError(1, f"the workspace must be on cuda:{dev}")
     if out is None:
-        out = _empty(shape, dtype, dev, stream)
-    elif out.shape != shape or out.dtype != dtype or out.device != dev or not out.is_contiguous():
-        raise PodError(1, f"out must be contiguous {dtype} {shape} on {dev}")
+        out = _empty(shape, dtype, q, stream)
+        op = out.data_ptr()
+    else:
+        op = _whole("out", out, shape, dtype, dev)
     if lse is None:
-        lse = _empty(shape[:2], torch.float32, dev, stream)
-    elif lse.shape != shape[:2] or lse.dtype != torch.float32 or lse.device != dev or not lse.is_contiguous():
-        raise PodError(1, f"lse must be contiguous float32 {shape[:2]} on {dev}")
-    _call(lib.pod_tree_run, dev, stream, h.ptr, q.data_ptr(), kv.data_ptr(), sp, mp, mn, kp, workspace.data_ptr(),
-          out.data_ptr(), lse.data_ptr())
+        lse = _empty(shape[:2], torch.float32, q, stream)
+        lp = lse.data_ptr()
+    else:
+        lp = _whole("lse", lse, shape[:2], torch.float32, dev)
+    _call(lib.pod_tree_run, dev, stream, h.ptr, qp, cp, sp, mp, mn, kp, workspace.data_ptr(), op, lp)
     return out, lse
 
 
 def pod_tree_read_device_status(h: PodTreeHandle, workspace, stream=None) -> int:
     v = ctypes.c_int32(0)
+    _torch()
     try:
         _call(lambda st: load_library().pod_tree_read_device_status(h.ptr, workspace.data_ptr(), st, ctypes.byref(v)),
               _device_of(workspace), stream)

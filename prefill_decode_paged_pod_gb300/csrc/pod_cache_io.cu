@@ -80,8 +80,9 @@ struct IoParams {
   float eps, k_scale, v_scale;
   float k_inv, v_inv;            // reciprocals, rounded to nearest; 0: divide
 };
-struct IoFreq {
-  uint64_t f[128];
+template <int D>
+struct IoFreq {                  // (a kernel parameter: no longer than it has to be)
+  uint64_t f[D / 2];
 };
 
 // Element offset of (slot, K half, head 0) in the cache, and the steps to the
@@ -156,8 +157,8 @@ POD_DEV uint2 codes8(const uint64_t* x) {
 
 // x / s rounded to nearest, from y = 1 / s rounded to nearest (Markstein: q = x y
 // is within an ulp of the quotient, and q + (x - q s) y rounds it correctly).
-// Quotients past 2^100, where the remainder may overflow, stay as q: they
-// saturate either way. The host gives y = 0 for scales whose products could leave
+// Quotients past 2^100, where the remainder may overflow, stay as q, for they
+// saturate either way, and so do zeros, for their sign. The host gives y = 0 for scales whose products could leave
 // the normal range: then divide.
 POD_DEV uint64_t div2(uint64_t x, float s, float y) {
   float a, b;
@@ -170,7 +171,8 @@ POD_DEV uint64_t div2(uint64_t x, float s, float y) {
   float qa, qb;
   unpack2(q, qa, qb);
   unpack2(r, a, b);
-  return pack2(fabsf(qa) < 1.2676506002282294e30f ? a : qa, fabsf(qb) < 1.2676506002282294e30f ? b : qb);
+  auto in = [](float v) { return (__float_as_uint(v) & 0x7fffffffu) - 1u < 0x71800000u - 1u; };   // (0, 2^100)
+  return pack2(in(qa) ? a : qa, in(qb) ? b : qb);
 }
 
 enum { IO_Q, IO_K, IO_V, IO_KV };
@@ -183,8 +185,8 @@ struct IoTables {
 };
 
 // The block's tokens: where their rows go, and cos and sin of their positions.
-template <typename T, int D, bool CACHE, bool TURN>
-POD_DEV void io_tables(const IoParams& P, const IoFreq& F, IoTables<TURN ? D : 16>& S, long long* base, int tok0,
+template <typename T, int D, bool CACHE, bool TURN, int FD>
+POD_DEV void io_tables(const IoParams& P, const IoFreq<FD>& F, IoTables<TURN ? D : 16>& S, long long* base, int tok0,
                        int ntok, const T* weight, bool report) {
   const int tid = threadIdx.x;
   if (CACHE && tid < ntok) {
@@ -227,7 +229,7 @@ POD_DEV void io_tables(const IoParams& P, const IoFreq& F, IoTables<TURN ? D : 1
 // some tokens. The rows of the first tasks are asked for before the tables are
 // made.
 template <typename T, int D, int FMT, int KIND, bool FUSED>
-POD_DEV void io_pass(const IoParams& P, const IoFreq& F, const IoParams::Cut& cut) {
+POD_DEV void io_pass(const IoParams& P, const IoFreq<FUSED ? D : 2>& F, const IoParams::Cut& cut) {
   constexpr int LPR = D / 16, NG = kIoThreads / LPR;
   constexpr bool TURN = FUSED && (KIND == IO_Q || KIND == IO_K);
   constexpr bool TO_CACHE = FMT != FMT_NONE && KIND != IO_Q;
@@ -404,7 +406,7 @@ POD_DEV void io_pass(const IoParams& P, const IoFreq& F, const IoParams::Cut& cu
 // FUSED: norm and rotation of q and k; without it the rows are only written.
 template <typename T, int D, int FMT, bool FUSED>
 __global__ void __launch_bounds__(kIoThreads) cache_io_kernel(const __grid_constant__ IoParams P,
-                                                              const __grid_constant__ IoFreq F) {
+                                                              const __grid_constant__ IoFreq<FUSED ? D : 2> F) {
   if constexpr (FUSED) {
     if ((int)blockIdx.x < P.cut[1].first)
       io_pass<T, D, FMT, IO_Q, true>(P, F, P.cut[0]);
@@ -527,11 +529,11 @@ long long tasks_of(const IoParams& P, long long heads, int round, int most) {
 // Frequencies in turns as 64-bit fractions. They depend on the rotation's
 // settings only; the last settings' table is kept per host thread (computing
 // it takes longer than a short launch).
-const IoFreq& freq_of(int R, float scale, float theta) {
+const IoFreq<256>& freq_of(int R, float scale, float theta) {
   struct Kept {
     int R = -1;
     float scale = 0.f, theta = 0.f;
-    IoFreq f;
+    IoFreq<256> f;
   };
   static thread_local Kept kept;
   if (kept.R != R || kept.scale != scale || kept.theta != theta) {
@@ -548,7 +550,7 @@ const IoFreq& freq_of(int R, float scale, float theta) {
 }
 
 template <typename T, int D, int FMT>
-cudaError_t launch_io(IoParams& P, bool fused, const IoFreq& f, cudaStream_t st) {
+cudaError_t launch_io(IoParams& P, bool fused, const IoFreq<256>& f, cudaStream_t st) {
   constexpr int round = kIoThreads / (D / 16) * kTasks;
   constexpr bool cache = FMT != FMT_NONE;
   const long long tasks = tasks_of(P, P.H + P.Hk + (cache ? P.Hk : 0), round, fused ? 4 : 2);
@@ -563,14 +565,17 @@ cudaError_t launch_io(IoParams& P, bool fused, const IoFreq& f, cudaStream_t st)
   }
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const unsigned grid = (unsigned)blocks;
-  if (fused)
-    cache_io_kernel<T, D, FMT, true><<<grid, kIoThreads, 0, st>>>(P, f);
-  else if constexpr (cache)
-    cache_io_kernel<T, D, FMT, false><<<grid, kIoThreads, 0, st>>>(P, f);
+  if (fused) {
+    IoFreq<D> fd;
+    memcpy(&fd, &f, sizeof(fd));
+    cache_io_kernel<T, D, FMT, true><<<grid, kIoThreads, 0, st>>>(P, fd);
+  } else if constexpr (cache) {
+    cache_io_kernel<T, D, FMT, false><<<grid, kIoThreads, 0, st>>>(P, IoFreq<2>{});
+  }
   return cudaGetLastError();
 }
 template <typename T, int D>
-cudaError_t launch_fmt(IoParams& P, int fmt, bool fused, const IoFreq& f, cudaStream_t st) {
+cudaError_t launch_fmt(IoParams& P, int fmt, bool fused, const IoFreq<256>& f, cudaStream_t st) {
   switch (fmt) {
     case FMT_16: return launch_io<T, D, FMT_16>(P, fused, f, st);
     case FMT_SCALED: return launch_io<T, D, FMT_SCALED>(P, fused, f, st);
@@ -579,7 +584,7 @@ cudaError_t launch_fmt(IoParams& P, int fmt, bool fused, const IoFreq& f, cudaSt
   }
 }
 template <typename T>
-cudaError_t launch_d(IoParams& P, int d, int fmt, bool fused, const IoFreq& f, cudaStream_t st) {
+cudaError_t launch_d(IoParams& P, int d, int fmt, bool fused, const IoFreq<256>& f, cudaStream_t st) {
   return d == 64 ? launch_fmt<T, 64>(P, fmt, fused, f, st)
          : d == 128 ? launch_fmt<T, 128>(P, fmt, fused, f, st)
                     : launch_fmt<T, 256>(P, fmt, fused, f, st);
@@ -688,7 +693,7 @@ IoParams params_of(const pod_io_args& a, bool fused, bool cache) {
 
 pod_status run_io(IoParams& P, const pod_io_args& a, int fmt, bool fused, void* stream, const char* what) {
   if (P.rows == 0) return POD_OK;
-  const IoFreq& f = freq_of(P.R, a.rope_scale, a.rope_theta);
+  const IoFreq<256>& f = freq_of(P.R, a.rope_scale, a.rope_theta);
   cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t e = a.dtype == POD_BF16 ? launch_d<__nv_bfloat16>(P, a.head_dim, fmt, fused, f, st)
                                             : launch_d<__half>(P, a.head_dim, fmt, fused, f, st);

@@ -210,9 +210,11 @@ def test_write_and_read(case):
     pages = rows // ps + 5
     cache, scales = empty_cache(pages, ps, hk, d, layout, fmt, dt, 3)
     kv = rows_of((rows, 3 * hk, d), dt, rows)
-    # magnitudes over many binades; a zero head row, NaN and infinities
-    kv = (kv.float() * torch.exp2(torch.randint(-12, 6, (rows, 3 * hk, 1)).float())).to(dt)
+    # magnitudes over many binades; a zero head row, negative zeros, NaN and infinities
+    g = torch.Generator().manual_seed(rows + d)
+    kv = (kv.float() * torch.exp2(torch.randint(-12, 6, (rows, 3 * hk, 1), generator=g).float())).to(dt)
     kv[0, 0] = 0
+    kv[0, hk, 1::2] = -0.0                     # (its sign is kept)
     if fmt != "16bit" and rows > 3:
         kv[1, 0, 5], kv[2, hk, 0], kv[3, 0, 1] = math.nan, math.inf, -math.inf
     k, v = kv[:, :hk], kv[:, hk:2 * hk]
