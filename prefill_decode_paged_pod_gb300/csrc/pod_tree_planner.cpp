@@ -25,6 +25,10 @@ namespace {
 
 // price of starting a segment, and least keys of a CTA's share, in keys
 constexpr int kStartKeys = 192, kMinKeys = 320;
+// Units stay whole where the longest is at most this many keys more than the cut
+// share, for the merge is a second launch: 3 us in a graph, 6 us in a stream,
+// about 1 us for each 100 keys that a lone CTA works through.
+constexpr int kWholeKeys = 384;
 
 struct Unit {
   int req, g, mt, blocks;
@@ -32,10 +36,11 @@ struct Unit {
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Walks one plane with a CTA budget of `share`; calls emit(cta, unit, blk0,
-// blk1) for each segment. Returns the number of CTAs used.
+// Walks one plane with a CTA budget of `share` (units are not cut with `whole`);
+// calls emit(cta, unit, blk0, blk1) for each segment. Returns the number of CTAs
+// used.
 template <typename F>
-int cut(const std::vector<Unit>& units, int share, int kStart, F emit) {
+int cut(const std::vector<Unit>& units, int share, bool whole, int kStart, F emit) {
   int cta = 0, used = 0;
   for (size_t u = 0; u < units.size(); ++u) {
     int at = 0;
@@ -43,7 +48,7 @@ int cut(const std::vector<Unit>& units, int share, int kStart, F emit) {
       const int left = units[u].blocks - at;
       int room = share - used - kStart;
       // too little room to be worth a start: the next CTA begins here
-      if (room < 1 || (room < 3 && room < left && used > 0)) {
+      if (room < 1 || (room < left && used > 0 && (whole || room < 3))) {
         ++cta;
         used = 0;
         room = share - kStart;
@@ -130,7 +135,7 @@ int pod_tree_build_plan(const PodTreeArgs& a, PodTreePlanHost& o, std::string* e
   auto share_of = [&](const Planes& planes) {
     auto ctas = [&](int share) {
       long long c = 0;
-      for (auto& p : planes) c += cut(p, share, kStart, [](int, int, int, int) {});
+      for (auto& p : planes) c += cut(p, share, false, kStart, [](int, int, int, int) {});
       return c;
     };
     const long long most = 1 << 29, even = cost / std::max(1, a.slots);
@@ -157,6 +162,17 @@ int pod_tree_build_plan(const PodTreeArgs& a, PodTreePlanHost& o, std::string* e
     }
   }
 
+  bool whole = false;
+  if (!planes.empty() && (longest + kStart - share) * a.block <= kWholeKeys) {
+    const int all = (int)std::max<long long>(longest + kStart, share);
+    long long c = 0;
+    for (auto& p : planes) c += cut(p, all, true, kStart, [](int, int, int, int) {});
+    if (c <= a.slots) {
+      share = all;
+      whole = true;
+    }
+  }
+
   // segments in CTA order; split tiles get partial rows and a merge group
   struct Seg {
     int cta, unit, b0, b1;
@@ -166,7 +182,7 @@ int pod_tree_build_plan(const PodTreeArgs& a, PodTreePlanHost& o, std::string* e
   long long prows = 0;
   for (const auto& plane : planes) {
     std::vector<Seg> s;
-    cut(plane, share, kStart, [&](int c, int u, int b0, int b1) { s.push_back({c, u, b0, b1}); });
+    cut(plane, share, whole, kStart, [&](int c, int u, int b0, int b1) { s.push_back({c, u, b0, b1}); });
     for (size_t i = 0; i < s.size();) {
       size_t e = i;
       while (e < s.size() && s[e].unit == s[i].unit) ++e;

@@ -442,6 +442,15 @@ def test_plan_balances_long_requests():
     assert n
 
 
+def test_plan_keeps_short_units_whole():
+    """No merge launch where the longest unit is little more than a share."""
+    c = Case(n=[5, 8, 6, 7], kv_len=[600, 17, 333, 400], H=32, Hk=8, d=128, ps=16)
+    segs, ctas, groups, _ = tables(c, 152)
+    assert len(groups) == 0 and (segs[:, 5] == -1).all() and len(segs) == 32
+    c = Case(n=[5], kv_len=[3000], H=32, Hk=8, d=128, ps=16)
+    assert len(tables(c, 152)[2]) == 8
+
+
 P = 1 << 20
 
 
