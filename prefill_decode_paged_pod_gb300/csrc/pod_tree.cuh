@@ -89,15 +89,11 @@ struct TLayout {
   // leave no room for more)
   static constexpr int FAC = QP == 3 && D == 128 ? 2 : 4;
   static constexpr int END = FAC_OFF + (KV == 2 ? 2 * BK * FAC : 0);
-  // The copies' join holds 32 output columns of the 128 lanes (16 KB) in the Q
-  // region, and m and l of the lanes behind them, or at the end where Q has no
-  // room for these.
-  static constexpr int JOIN = 32;
-  static constexpr int JOIN_BYTES = POD_TREE_TILE * JOIN * 4, ML_BYTES = POD_TREE_TILE * 8;
-  static constexpr bool ML_IN_Q = Q_BYTES >= JOIN_BYTES + ML_BYTES;
-  static constexpr int ML_OFF = ML_IN_Q ? Q_OFF + JOIN_BYTES : END;
-  static constexpr int TOTAL = ML_IN_Q ? END : END + ML_BYTES;
-  static_assert(JOIN_BYTES <= Q_BYTES, "the join must fit the Q region");
+  // The copies' join goes through the Q region: first m, l and V scale of the 128
+  // lanes, then twice half of their output columns.
+  static constexpr int JOIN = D / 2;
+  static constexpr int TOTAL = END;
+  static_assert(POD_TREE_TILE * JOIN * 4 <= Q_BYTES && POD_TREE_TILE * 12 <= Q_BYTES, "the join must fit the Q region");
   // TMEM: S buffers, then O. Two buffers let Q K^T of the next block run beside
   // the softmax of this one; FP8 blocks of 128 keys leave room for one where
   // two CTAs share the SM (these overlap each other).
@@ -307,15 +303,15 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
   {
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(P.q) + grow * D);
     if constexpr (!L::F8) {
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
+#pragma unroll 16
+      for (int c = 0; c < D / 8; ++c) {              // (a row of 128 elements at once)
         uint4 v = make_uint4(0, 0, 0, 0);
         if (valid) v = __ldg(src + c);
         sts128(sbase + L::Q_OFF + (c >> 3) * L::QPART + L::swz(tid, c & 7), v);
       }
     } else {
       float amax = 0.f;
-#pragma unroll 4
+#pragma unroll 16
       for (int c = 0; c < D / 8; ++c) {
         const uint4 v = __ldg(src + c);
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -610,64 +606,87 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
       }
     }
   } else {
-    // join the copies through the Q region, JOIN columns at a time
-    float* ml = reinterpret_cast<float*>(smem + L::ML_OFF);
+    // join the copies through the Q region. 8 threads a row, 16 rows at a time:
+    // a thread's rows, their weights and places are made once.
+    float* ml = reinterpret_cast<float*>(smem + L::Q_OFF);
+    int* vr = reinterpret_cast<int*>(ml + 2 * POD_TREE_TILE);
     ml[2 * tid] = m_ref;
     ml[2 * tid + 1] = l;
+    if (KV == 2) vr[tid] = vref;
+    softmax_sync();
+    constexpr int RT = RB / 16;                      // rows of a thread
+    const int l8 = tid & 7;
+    float w[RT][C];
+    size_t at[RT];
+#pragma unroll
+    for (int k = 0; k < RT; ++k) {
+      const int r = (tid >> 3) + 16 * k;
+      float M = NEG_INF;
+      int vtop = 0;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        M = fmaxf(M, ml[2 * (c * RB + r)]);
+        if (KV == 2) vtop = max(vtop, vr[c * RB + r]);
+      }
+      const float Ms = M == NEG_INF ? 0.f : M;
+      float wsum = 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        w[k][c] = ex2(ml[2 * (c * RB + r)] - Ms);
+        wsum += w[k][c] * ml[2 * (c * RB + r) + 1];
+        if (KV == 2) w[k][c] *= exp_below(vr[c * RB + r], vtop);
+      }
+      const int pr = seg[TS_ROW0] + min(r, nrows - 1), tk = pr / G, hd = seg[TS_G] * G + pr - tk * G;
+      const size_t gr = (size_t)(seg[TS_QROW0] + tk) * H + hd;
+      float denom = wsum;
+      if (P.sinks && prow < 0) denom += ex2(P.sinks[hd] * kLog2e - Ms);
+      const float inv = denom == 0.f ? 0.f : (KV == 2 ? exp_byte(vtop) : v_scale) / denom;
+#pragma unroll
+      for (int c = 0; c < C; ++c) w[k][c] *= inv;
+      at[k] = prow < 0 ? gr : (size_t)(prow + r);
+      if (l8 == 0 && r < nrows) {
+        const float lse = wsum == 0.f ? NEG_INF : M + log2f(wsum);
+        if (prow >= 0) P.part_lse[at[k]] = lse;
+        else if (P.lse) P.lse[gr] = lse;
+      }
+    }
     constexpr int CH = L::JOIN / 4;                  // 16-byte chunks of a lane's part
 #pragma unroll 1
     for (int c0 = 0; c0 < D; c0 += L::JOIN) {
-      softmax_sync();                                // the last part has been read
-      {
+      softmax_sync();                                // what was there has been read
+#pragma unroll 1
+      for (int c = 0; c < L::JOIN; c += 32) {
         float o[32];
-        tmem_ld32(tmem + lane_base + L::TM_O + c0, o);
+        tmem_ld32(tmem + lane_base + L::TM_O + c0 + c, o);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           // (chunks turned by the lane: eight lanes of a store meet eight bank groups)
-          const int ch = (i + tid) & (CH - 1);
+          const int ch = (c / 4 + i + tid) & (CH - 1);
           sts128(sbase + L::Q_OFF + tid * (CH * 16) + ch * 16, *reinterpret_cast<uint4*>(o + 4 * i));
         }
       }
       softmax_sync();
-      for (int idx = tid; idx < nrows * CH; idx += 128) {
-        const int r = idx / CH, ch = idx - r * CH;
-        float M = NEG_INF;
 #pragma unroll
-        for (int c = 0; c < C; ++c) M = fmaxf(M, ml[2 * (c * RB + r)]);
-        const float Ms = M == NEG_INF ? 0.f : M;
-        float wsum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < RT; ++k) {
+        const int r = (tid >> 3) + 16 * k;
+        if (r >= nrows) break;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const int ln = c * RB + r;
-          const float w = ex2(ml[2 * ln] - Ms);
-          wsum += w * ml[2 * ln + 1];
-          const uint4 u = lds128(sbase + L::Q_OFF + ln * (CH * 16) + ((ch + ln) & (CH - 1)) * 16);
-          acc.x = fmaf(w, __uint_as_float(u.x), acc.x);
-          acc.y = fmaf(w, __uint_as_float(u.y), acc.y);
-          acc.z = fmaf(w, __uint_as_float(u.z), acc.z);
-          acc.w = fmaf(w, __uint_as_float(u.w), acc.w);
-        }
-        const int pr = seg[TS_ROW0] + r;
-        const int hd = seg[TS_G] * G + pr % G;
-        const size_t gr = (size_t)(seg[TS_QROW0] + pr / G) * H + hd;
-        float denom = wsum;
-        if (P.sinks && prow < 0) denom += ex2(P.sinks[hd] * kLog2e - Ms);
-        const float inv = denom == 0.f ? 0.f : v_scale / denom;
-        const int col = c0 + ch * 4;
-        if (prow < 0)
-          *reinterpret_cast<uint2*>(outg + gr * D + col) =
-              make_uint2(Pack<T>::two(acc.x * inv, acc.y * inv), Pack<T>::two(acc.z * inv, acc.w * inv));
-        else
-          *reinterpret_cast<float4*>(P.part_o + (size_t)(prow + r) * D + col) =
-              make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        if (col == 0) {
-          const float lse = wsum == 0.f ? NEG_INF : M + log2f(wsum);
-          if (prow < 0) {
-            if (P.lse) P.lse[gr] = lse;
-          } else {
-            P.part_lse[prow + r] = lse;
+        for (int ch = l8; ch < CH; ch += 8) {
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            const int ln = c * RB + r;
+            const uint4 u = lds128(sbase + L::Q_OFF + ln * (CH * 16) + ((ch + ln) & (CH - 1)) * 16);
+            acc.x = fmaf(w[k][c], __uint_as_float(u.x), acc.x);
+            acc.y = fmaf(w[k][c], __uint_as_float(u.y), acc.y);
+            acc.z = fmaf(w[k][c], __uint_as_float(u.z), acc.z);
+            acc.w = fmaf(w[k][c], __uint_as_float(u.w), acc.w);
           }
+          const size_t to = at[k] * D + c0 + ch * 4;
+          if (prow < 0)
+            *reinterpret_cast<uint2*>(outg + to) = make_uint2(Pack<T>::two(acc.x, acc.y), Pack<T>::two(acc.z, acc.w));
+          else
+            *reinterpret_cast<float4*>(P.part_o + to) = acc;
         }
       }
     }
@@ -694,6 +713,9 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
     if (tid == 0) atomicOr(P.status, POD_STATUS_ALIGN);
     return;
   }
+  // (asked for before the set-up below, which takes as long)
+  const int seg0 = P.cta_ptr[blockIdx.x], seg1 = P.cta_ptr[blockIdx.x + 1];
+  if (warp == 5 && lane < 2 && P.kbx > 0) tma_prefetch_desc(lane ? &P.tm_v : &P.tm_k);
   auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::BAR_OFF + 164);
   if (warp == 4) {
@@ -719,11 +741,11 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
     *abort_flag = 0;
     fence_mbar_init();
   }
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(P.segs + (size_t)seg0 * TS_REC));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::BAR_OFF + 160);
-  const int seg0 = P.cta_ptr[blockIdx.x], seg1 = P.cta_ptr[blockIdx.x + 1];
   bool ok = true;
   volatile int never = 0;                            // an abort flag that nobody raises
 
@@ -888,7 +910,6 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
       // keys are read once unless another tile of the request reads them too
       const uint64_t pol = l2_policy_evict_first();
       int fill = 0;
-      if (lane == 0) tma_prefetch_desc(tm);
       for (int i = seg0; i < seg1 && ok; ++i) {
         const int32_t* seg = P.segs + (size_t)i * TS_REC;
         const int g = seg[TS_G], npages = seg[TS_NPAGES];
