@@ -188,6 +188,9 @@ POD_DEV void sts128(uint32_t a, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
 }
+POD_DEV void sts64(uint32_t a, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
 POD_DEV void stsf(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
 POD_DEV void sts16(uint32_t a, uint32_t v) {
   asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"((unsigned short)v) : "memory");
@@ -301,62 +304,81 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
   // with it: its last S has been read)
   float qscale = P.scale_log2;
   {
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(P.q) + grow * D);
-    if constexpr (!L::F8) {
-#pragma unroll 16
-      for (int c = 0; c < D / 8; ++c) {              // (a row of 128 elements at once)
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (valid) v = __ldg(src + c);
-        sts128(sbase + L::Q_OFF + (c >> 3) * L::QPART + L::swz(tid, c & 7), v);
-      }
-    } else {
-      float amax = 0.f;
-#pragma unroll 16
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 v = __ldg(src + c);
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    // A warp brings its 32 lanes' rows together, D / 8 lanes a row: a thread that
+    // reads its own row alone takes 16 bytes of a line at a time, and the 2048
+    // line visits took 2700 clocks a segment.
+    constexpr int LPQ = D / 8, RPI = 32 / LPQ;       // lanes of a row, rows at a time
+    const int sub = lane / LPQ, ch = lane % LPQ;
+    const uint32_t live = __ballot_sync(0xffffffffu, valid);
+    int my_e = 0;
+    constexpr int NI = 32 / RPI, GRP = L::F8 ? 4 : NI < 16 ? NI : 16;
+    uint4 next[GRP];
+    auto ask = [&](int i0) {                         // rows of iterations i0 .. i0 + GRP - 1
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = Pack<T>::unpack(u[i]);
+      for (int k = 0; k < GRP; ++k) {
+        const int ln = (i0 + k) * RPI + sub;
+        const size_t g = (size_t)__shfl_sync(0xffffffffu, (unsigned long long)grow, ln);
+        next[k] = make_uint4(0, 0, 0, 0);
+        if ((live >> ln) & 1) next[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(P.q) + g * D) + ch);
+      }
+    };
+    auto put = [&](int i, const uint4& v) {          // the rows of iteration i into shared memory
+      const int row = warp * 32 + i * RPI + sub;
+      if constexpr (!L::F8) {
+        sts128(sbase + L::Q_OFF + (ch >> 3) * L::QPART + L::swz(row, ch & 7), v);
+      } else {
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        float x[8], amax = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = Pack<T>::unpack(u[k]);
+          x[2 * k] = f.x;
+          x[2 * k + 1] = f.y;
           amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
         }
-      }
-      // 2^e with amax * 2^e in [128, 256), both factors normal floats
-      int e = 7 - ((int)(__float_as_uint(amax) >> 23) - 127);
-      e = amax > 0.f ? min(max(e, -126), 126) : 0;
-      const float up = valid ? __uint_as_float((uint32_t)(127 + e) << 23) : 0.f;
-      qscale *= __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll 2
-      for (int c = 0; c < D / 16; ++c) {             // 16 elements: one 16-byte chunk of each part
-        float x[16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 v = __ldg(src + 2 * c + h);
-          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        for (int o = LPQ / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o, LPQ));
+        // 2^e with amax * 2^e in [128, 256), both factors normal floats
+        int e = 7 - ((int)(__float_as_uint(amax) >> 23) - 127);
+        e = amax > 0.f ? min(max(e, -126), 126) : 0;
+        // (a row with an infinity becomes NaN, as its logits are, not a saturated code)
+        const float up = __uint_as_float(amax == INFINITY ? 0x7fffffffu : (uint32_t)(127 + e) << 23);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = Pack<T>::unpack(u[i]);
-            x[8 * h + 2 * i] = f.x * up;
-            x[8 * h + 2 * i + 1] = f.y * up;
-          }
+        for (int k = 0; k < RPI; ++k) {
+          const int ek = __shfl_sync(0xffffffffu, e, k * LPQ);
+          if (lane == i * RPI + k) my_e = ek;
         }
-        const int part = c / (L::ROWB / 16), cc = c % (L::ROWB / 16);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] *= up;
+        const int part = ch * 8 / L::ROWB, cc = ch * 8 % L::ROWB / 16;
 #pragma unroll
         for (int p = 0; p < L::QP; ++p) {            // part p: what parts 0..p-1 left, to E4M3
-          uint32_t w[4] = {0, 0, 0, 0};
+          uint32_t w[2] = {0, 0};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t code = f32x2_to_e4m3x2(x[2 * i], x[2 * i + 1]);
-            w[i >> 1] |= code << (16 * (i & 1));
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t code = f32x2_to_e4m3x2(x[2 * k], x[2 * k + 1]);
+            w[k >> 1] |= code << (16 * (k & 1));
             const float2 f = Pack<__half>::unpack(e4m3x2_to<__half>((uint16_t)code));
-            x[2 * i] -= f.x;
-            x[2 * i + 1] -= f.y;
+            x[2 * k] -= f.x;
+            x[2 * k + 1] -= f.y;
           }
-          sts128(sbase + L::Q_OFF + (p * L::PARTS + part) * L::QPART + L::swz(tid, cc),
-                 make_uint4(w[0], w[1], w[2], w[3]));
+          sts64(sbase + L::Q_OFF + (p * L::PARTS + part) * L::QPART + L::swz(row, cc) + (ch & 1) * 8, w[0], w[1]);
         }
       }
+    };
+    ask(0);
+    // (FP8: four rows' worth of code, not the whole tile's: run once a segment, it
+    // would come from beyond the instruction cache)
+#pragma unroll 1
+    for (int i0 = 0; i0 < NI; i0 += GRP) {
+      uint4 vs[GRP];
+#pragma unroll
+      for (int k = 0; k < GRP; ++k) vs[k] = next[k];
+      if (i0 + GRP < NI) ask(i0 + GRP);
+#pragma unroll
+      for (int k = 0; k < GRP; ++k) put(i0 + k, vs[k]);
     }
+    if constexpr (L::F8) qscale *= __uint_as_float((uint32_t)(127 - my_e) << 23);
     fence_proxy_async();
     mbar_arrive(BAR(TB_QFULL));
   }
@@ -606,8 +628,8 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
       }
     }
   } else {
-    // join the copies through the Q region. 8 threads a row, 16 rows at a time:
-    // a thread's rows, their weights and places are made once.
+    // Join the copies through the Q region, 8 threads a row, 16 rows at a time: a
+    // thread's rows, their weights and places are made once.
     float* ml = reinterpret_cast<float*>(smem + L::Q_OFF);
     int* vr = reinterpret_cast<int*>(ml + 2 * POD_TREE_TILE);
     ml[2 * tid] = m_ref;

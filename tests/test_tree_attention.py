@@ -195,6 +195,14 @@ class Case:
         return res
 
 
+def run_once(c):
+    h = c.plan()
+    ws = torch.empty(max(256, pod.pod_tree_workspace_size(h)), dtype=torch.uint8, device="cuda")
+    pod.pod_tree_bind_workspace(h, ws)
+    q, kv, more = c.args()
+    return pod.pod_tree_run(h, q, kv, ws, **more)
+
+
 BF, HF = torch.bfloat16, torch.float16
 CASES = {
     # smallest: one token and one key; a chain without a mask; keys at a block's edge
@@ -284,6 +292,20 @@ def test_masked_keys_may_hold_anything_in_k(fmt):
     raw[pg, 0, t % 16, 0, 1::2] = 0xFF if fmt == "block" else math.nan
     got = c.run()
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["16bit", "scaled", "block"])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_a_bad_query_stays_in_its_row(fmt, bad):
+    c = Case(n=[6], kv_len=[300], H=4, Hk=1, d=128, ps=16, fmt=fmt, seed=1)
+    want = c.run()
+    c.q[2, 1, 7] = bad
+    got = run_once(c)
+    assert got[0][2, 1].isnan().all()
+    keep = torch.ones((6, 4), dtype=torch.bool)
+    keep[2, 1] = False
+    assert torch.equal(got[0].cpu()[keep], want[0].cpu()[keep]) and torch.equal(got[1].cpu()[keep], want[1].cpu()[keep])
 
 
 @pytest.mark.gpu
