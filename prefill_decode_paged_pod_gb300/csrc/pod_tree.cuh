@@ -35,11 +35,10 @@
 // twice 3 bits in E5M2, whose range goes on below, 2^-11 of p and 2^-23 of the
 // largest weight. (An
 // earlier form widened the codes to fp16 in shared memory; the two warps that
-// did it set the pace: 620 us for 96 requests of 8192 keys.) Per-tensor scales
+// did it set the pace: 620 us for 96 requests of 8192 keys, now 425.) Per-tensor scales
 // are constants of the softmax and of the output. Block scales are powers of
 // two per key: K's multiplies the key's column of S, V's the column of P
-// relative to the largest V scale met so far (O is rescaled when that one
-// grows, as for the running maximum).
+// relative to the largest V scale met so far.
 #pragma once
 #include <cuda_runtime.h>
 #include <math.h>
@@ -81,19 +80,19 @@ struct TLayout {
   // warps' largest V exponents of two blocks, +208: the block's factors (K,
   // then V). One set for the CTA: a set for each warp would spare the meetings,
   // and a loader warp for the exponent bytes the loads, but both made the code
-  // larger than the instruction cache and the loop slower (405 us as it is, 409
-  // and 430 us for 96 requests of 8192 keys).
+  // larger than the instruction cache and the loop slower (when the loop took 405 us
+  // for 96 requests of 8192 keys: 409 and 430).
   static constexpr int WM_OFF = BAR_OFF + 168;
   static constexpr int FAC_OFF = BAR_OFF + 208;
   // (floats, or bf16 beside the three Q parts of fp16 rows of 128 elements, which
   // leave no room for more)
   static constexpr int FAC = QP == 3 && D == 128 ? 2 : 4;
   static constexpr int END = FAC_OFF + (KV == 2 ? 2 * BK * FAC : 0);
-  // The copies' join goes through the Q region: first m, l and V scale of the 128
-  // lanes, then twice half of their output columns.
+  // The copies' join goes through the Q region: first m and l of the 128 lanes,
+  // then twice half of their output columns.
   static constexpr int JOIN = D / 2;
   static constexpr int TOTAL = END;
-  static_assert(POD_TREE_TILE * JOIN * 4 <= Q_BYTES && POD_TREE_TILE * 12 <= Q_BYTES, "the join must fit the Q region");
+  static_assert(POD_TREE_TILE * JOIN * 4 <= Q_BYTES && POD_TREE_TILE * 8 <= Q_BYTES, "the join must fit the Q region");
   // TMEM: S buffers, then O. Two buffers let Q K^T of the next block run beside
   // the softmax of this one; FP8 blocks of 128 keys leave room for one where
   // two CTAs share the SM (these overlap each other).
@@ -110,6 +109,10 @@ struct TLayout {
   // below it spares most of the rescaling (at TOP = 7 every other block of 128
   // random keys had a row that needed it).
   static constexpr float TOP = F8 ? 6.f : 0.f, LIMIT = F8 ? 8.5f : 8.f;
+  // Block scales: where the V factors differ by no more binades, the largest logit
+  // sets m, and the smallest parts of P stay at or below their rounding (2^-15 of
+  // the largest weight beside 2^-9 of each; with three parts 2^-22 beside 2^-12).
+  static constexpr int SPREAD = PP == 3 ? 10 : 6;
 
   static POD_DEV uint32_t swz(int r, int c) { return ROWB == 128 ? sw128_off(r, c) : sw64_off(r, c); }
   static POD_DEV uint64_t desc(uint32_t a, uint32_t lbo, uint32_t sbo) {
@@ -275,6 +278,60 @@ POD_DEV KeyAt key_at(const PodTreeParams& P, const int32_t* seg) {
   return KeyAt{P.pages + seg[TS_PAGE0], seg[TS_NPAGES], P.ps, P.ps_shift, P.Hk, P.hnd, seg[TS_G]};
 }
 
+// What one row sees at the end of its request.
+struct TreeView {
+  const uint8_t* mask;
+  long long mask_bytes, bit0;                        // the row's first bit
+  int ctx, ntok, tok;
+  // bit i says whether key c0 + i is seen
+  POD_DEV uint64_t seen(int c0) const {
+    uint64_t see = 0;
+    const int skip = max(ctx - c0, 0);               // context keys at the front
+    const int j0 = c0 + skip - ctx;                  // first tree key
+    if (j0 < ntok) {
+      see = mask ? load_bits64(mask, mask_bytes, bit0 + j0)
+                 : (tok - j0 >= 63 ? ~0ull : tok < j0 ? 0ull : (2ull << (tok - j0)) - 1ull);
+      const int left = ntok - j0;
+      if (left < 64) see &= (1ull << left) - 1ull;
+    }
+    if (skip) see = skip < 64 ? (see << skip) | ((1ull << skip) - 1ull) : ~0ull;
+    return see;
+  }
+};
+
+// Block scales: the row's largest logit + log2(V factor) over N columns of S (col0:
+// the first one's place in the block, which starts at key kb). Rarely needed, and
+// a call, so that the loop around it keeps its registers.
+template <int FACB, int N>
+__device__ __noinline__ float weighted_max(uint32_t s_addr, uint32_t kfac, uint32_t vfac, int col0, float qscale,
+                                           int kb, const TreeView& tv) {
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < N; c += 16) {
+    float x[16];
+    tmem_ldw<16>(s_addr + c, x);
+    const int c0 = kb + col0 + c;
+    const uint64_t see = c0 + 16 > tv.ctx ? tv.seen(c0) : ~0ull;
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      uint64_t k[2], v[2];
+      factors4<FACB>(kfac, col0 + c + i, k);
+      factors4<FACB>(vfac, col0 + c + i, v);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float s[2], g[2];
+        unpack2(mul2(pack2(x[i + 2 * u], x[i + 2 * u + 1]), k[u]), s[0], s[1]);
+        unpack2(v[u], g[0], g[1]);
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          if ((see >> (i + 2 * u + w)) & 1ull)
+            top = fmaxf(top, fmaf(s[w], qscale, (float)((int)(__float_as_uint(g[w]) >> 23) - 127)));
+      }
+    }
+  }
+  return top;
+}
+
 // ============================================================ softmax warps
 // One segment for tiles held C times. Returns false when a wait ran out.
 template <typename T, int D, int KV, int C>
@@ -383,8 +440,9 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
     mbar_arrive(BAR(TB_QFULL));
   }
 
-  const long long bit0 = ((long long)seg[TS_BIT_HI] << 32) | (uint32_t)seg[TS_BIT_LO];
   const int ctx = kv_len - ntok;
+  const TreeView tv{P.mask, P.mask_bytes,
+                    (((long long)seg[TS_BIT_HI] << 32) | (uint32_t)seg[TS_BIT_LO]) + (long long)tok * ntok, ctx, ntok, tok};
   // block scales: the exponent bytes of this thread's key (tid) of the next
   // block, and its page of the one after (a byte's address waits for its page);
   // keys past the last read the last
@@ -410,19 +468,28 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
     const int kb = (blk0 + j) * BK;
     const int sc = sc0 + j, b = sc % NSB;
     float o_scale = 1.f;
+    bool wide = false;                               // V factors of many binades
     if constexpr (KV == 2) {
       // The warps meet twice a block: at the first meeting all of them have read
-      // the last block's factors and written their largest V exponent, at the
-      // second the factors are there.
-      volatile int* wm = reinterpret_cast<volatile int*>(smem + L::WM_OFF) + 4 * (j & 1);
-      const int top_w = __reduce_max_sync(0xffffffffu, vbyte);
-      if (lane == 0) wm[warp] = top_w;
+      // the last block's factors and written their largest and smallest V
+      // exponent, at the second the factors are there.
+      volatile uint32_t* wm = reinterpret_cast<volatile uint32_t*>(smem + L::WM_OFF) + 4 * (j & 1);
+      const int hi_w = __reduce_max_sync(0xffffffffu, vbyte), lo_w = __reduce_min_sync(0xffffffffu, vbyte);
+      if (lane == 0) wm[warp] = (uint32_t)hi_w << 16 | (uint32_t)(255 - lo_w);
       if (!softmax_vote(ok)) return false;
-      const int top = max(max(wm[0], wm[1]), max(wm[2], wm[3]));
-      if (top > vref) {                              // O is kept in units of 2^(vref - 127)
-        o_scale = exp_below(vref, top);
-        vref = top;
+      const uint32_t w4 = __vmaxu2(__vmaxu2(wm[0], wm[1]), __vmaxu2(wm[2], wm[3]));
+      const int hi = (int)(w4 >> 16), lo = 255 - (int)(w4 & 0xffffu);
+      if (hi > vref) {
+        // O is kept in units of 2^(m_ref + vref): what vref gains m_ref loses,
+        // as far as l, in units of 2^m_ref, keeps its range
+        const int gain = hi - vref, room = max(100 - ((int)(__float_as_uint(l) >> 23 & 255u) - 127), 0);
+        const int d = min(min(gain, room), 120);
+        o_scale = exp_below(d, gain);
+        m_ref -= (float)d;
+        l *= __uint_as_float((uint32_t)(127 + d) << 23);
+        vref = hi;
       }
+      wide = vref - lo > L::SPREAD;
       if constexpr (L::FAC == 4) {
         stsf(kfac + 4 * tid, exp_byte(kbyte));
         stsf(vfac + 4 * tid, exp_below(vbyte, vref));
@@ -441,9 +508,8 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
     tc_fence_after();
     const uint32_t s_addr = tmem + lane_base + L::TM_S + b * BK;
     const int my0 = cp * TW;                         // this copy's first column
-    // S of run h: raw products with the keys' factors, hidden keys at -inf
-    auto load_s = [&](int h, float* s) {
-      const int col = my0 + h * W;
+    // S of W columns: raw products with the keys' factors, hidden keys at -inf
+    auto load_s = [&](int col, float* s) {
       tmem_ldw<W>(s_addr + col, s);
       if constexpr (KV == 2) {
 #pragma unroll
@@ -455,18 +521,8 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
         }
       }
       const int c0 = kb + col;                       // first key of the run
-      if (c0 + W > ctx) {
-        // keys of the tree, or past the last: bit i says whether key c0 + i is seen
-        uint64_t see = 0;
-        const int skip = max(ctx - c0, 0);           // context keys at the front
-        const int j0 = c0 + skip - ctx;              // first tree key of the run
-        if (j0 < ntok) {
-          see = P.mask ? load_bits64(P.mask, P.mask_bytes, bit0 + (long long)tok * ntok + j0)
-                       : (tok - j0 >= 63 ? ~0ull : tok < j0 ? 0ull : (2ull << (tok - j0)) - 1ull);
-          const int left = ntok - j0;
-          if (left < 64) see &= (1ull << left) - 1ull;
-        }
-        if (skip) see = skip < 64 ? (see << skip) | ((1ull << skip) - 1ull) : ~0ull;
+      if (c0 + W > ctx) {                            // keys of the tree, or past the last
+        const uint64_t see = tv.seen(c0);
 #pragma unroll
         for (int i = 0; i < W; ++i)
           if (!((see >> i) & 1ull)) s[i] = NEG_INF;
@@ -482,14 +538,23 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
       }
       return fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
     };
+    // The reference m has to suit P, which holds V's factors too: a key of a large
+    // factor that this row does not see, or hardly, must not push the others' P
+    // out of E4M3's range. Factors within SPREAD binades of the largest: the
+    // logits' maximum does. Else it is the maximum of logit plus factor, at most
+    // 96 below the former (l, a sum without the factors, stays below 2^127).
+    float far = NEG_INF;
+    if constexpr (KV == 2)
+      if (wide) far = weighted_max<L::FAC, TW>(s_addr + my0, kfac, vfac, my0, qscale, kb, tv);
     float s[W];
     float bmax = NEG_INF;
 #pragma unroll
     for (int h = NH - 1; h >= 0; --h) {              // (run 0 stays in registers)
-      load_s(h, s);
+      load_s(my0 + h * W, s);
       bmax = fmaxf(bmax, max_s(s));
     }
-    const float top = bmax * qscale;
+    float top = bmax * qscale;
+    if (KV == 2 && wide) top = fmaxf(far, top - 96.f);
     const bool rescale = top > m_ref + L::LIMIT;     // also for the first finite maximum
     const float m_use = rescale ? top - L::TOP : m_ref;
     const float m_sub = m_use == NEG_INF ? 0.f : m_use;
@@ -500,7 +565,7 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
     uint64_t rs[2] = {0, 0};
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
-      if (h > 0) load_s(h, s);
+      if (h > 0) load_s(my0 + h * W, s);
       constexpr int N = L::F8 ? 32 : 16;             // keys of 8 columns
 #pragma unroll
       for (int q = 0; q < W; q += N) {
@@ -631,10 +696,8 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
     // Join the copies through the Q region, 8 threads a row, 16 rows at a time: a
     // thread's rows, their weights and places are made once.
     float* ml = reinterpret_cast<float*>(smem + L::Q_OFF);
-    int* vr = reinterpret_cast<int*>(ml + 2 * POD_TREE_TILE);
     ml[2 * tid] = m_ref;
     ml[2 * tid + 1] = l;
-    if (KV == 2) vr[tid] = vref;
     softmax_sync();
     constexpr int RT = RB / 16;                      // rows of a thread
     const int l8 = tid & 7;
@@ -644,25 +707,20 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
     for (int k = 0; k < RT; ++k) {
       const int r = (tid >> 3) + 16 * k;
       float M = NEG_INF;
-      int vtop = 0;
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        M = fmaxf(M, ml[2 * (c * RB + r)]);
-        if (KV == 2) vtop = max(vtop, vr[c * RB + r]);
-      }
+      for (int c = 0; c < C; ++c) M = fmaxf(M, ml[2 * (c * RB + r)]);
       const float Ms = M == NEG_INF ? 0.f : M;
       float wsum = 0.f;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         w[k][c] = ex2(ml[2 * (c * RB + r)] - Ms);
         wsum += w[k][c] * ml[2 * (c * RB + r) + 1];
-        if (KV == 2) w[k][c] *= exp_below(vr[c * RB + r], vtop);
       }
       const int pr = seg[TS_ROW0] + min(r, nrows - 1), tk = pr / G, hd = seg[TS_G] * G + pr - tk * G;
       const size_t gr = (size_t)(seg[TS_QROW0] + tk) * H + hd;
       float denom = wsum;
       if (P.sinks && prow < 0) denom += ex2(P.sinks[hd] * kLog2e - Ms);
-      const float inv = denom == 0.f ? 0.f : (KV == 2 ? exp_byte(vtop) : v_scale) / denom;
+      const float inv = denom == 0.f ? 0.f : v_scale / denom;
 #pragma unroll
       for (int c = 0; c < C; ++c) w[k][c] *= inv;
       at[k] = prow < 0 ? gr : (size_t)(prow + r);

@@ -8,7 +8,7 @@
 // alike: the CTAs at the same place of two planes read the same tokens at the
 // same time, other heads' rows beside theirs in memory (an FP8 row of an NHD
 // cache is 128 bytes, too little by itself for HBM: 96 requests of 8192 keys took
-// 404 us with the heads one after another in one plane), and for wide trees the
+// 406 us with the heads one after another in one plane, 352 so), and for wide trees the
 // same keys, the second time from L2. Where so many planes leave too many CTA
 // slots over, a plane takes all heads, one after another. Cut units are merged
 // by a second kernel.
