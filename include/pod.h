@@ -393,8 +393,8 @@ size_t pod_static_scratch_capacity(void);
  * t / page_size], position t % page_size). A negative slot is a padding row.
  * A slot at or past num_pages * page_size is treated like a negative one, and
  * sets bit 4 of *status (DEVICE int32, or NULL for no report; never cleared
- * here). Rows of one write that name the same slot leave either of their
- * values, element by element.
+ * here). Where rows of one write name the same slot, each code, value and
+ * exponent byte of it is left by one of them, not all by the same one.
  *
  * Cache formats (kv_format), both page layouts (kv_layout 0 = NHD, 1 = HND):
  *  POD_KV_16BIT       the values, in the call's dtype

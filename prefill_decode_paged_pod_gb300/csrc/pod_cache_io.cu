@@ -158,8 +158,8 @@ POD_DEV uint2 codes8(const uint64_t* x) {
 // x / s rounded to nearest, from y = 1 / s rounded to nearest (Markstein: q = x y
 // is within an ulp of the quotient, and q + (x - q s) y rounds it correctly).
 // Quotients past 2^100, where the remainder may overflow, stay as q, for they
-// saturate either way, and so do zeros, for their sign. The host gives y = 0 for scales whose products could leave
-// the normal range: then divide.
+// saturate either way, and so do zeros, for their sign. The host gives y = 0 for
+// scales whose products could leave the normal range: then divide.
 POD_DEV uint64_t div2(uint64_t x, float s, float y) {
   float a, b;
   if (y == 0.f) {
@@ -177,7 +177,8 @@ POD_DEV uint64_t div2(uint64_t x, float s, float y) {
 
 enum { IO_Q, IO_K, IO_V, IO_KV };
 
-// The tables of a block: cos and sin of its tokens, and the norm weights. Chunked so that the lanes of a head row read neighbouring 16 bytes.
+// The tables of a block: cos and sin of its tokens, and the norm weights, chunked
+// so that the lanes of a head row read neighbouring 16 bytes.
 template <int D>
 struct IoTables {
   float4 cs[kMaxTok * D / 4];    // [token][4 (2 interleaved, per chunk)][lane]: c, c', s, s'
