@@ -24,8 +24,8 @@
 // would cost 128 rows whatever their number, a quarter (half) of it; the copies
 // are joined at the end like split key ranges.
 //
-// FP8 caches go into the products as they are (kind::f8f6f4, E4M3 operands),
-// with 128 keys a block. A query row is scaled by the power of two that brings
+// FP8 caches go into the products as they are (kind::f8f6f4, E4M3 operands).
+// A query row is scaled by the power of two that brings
 // its largest value to [128, 256) and split into E4M3 parts, two for bf16 rows
 // (4 + 4 significant bits, all it has), three for fp16 rows (11 bits); parts
 // below 2^-17 of the row's largest value lose bits. P (the largest
@@ -35,8 +35,8 @@
 // twice 3 bits in E5M2, whose range goes on below, 2^-11 of p and 2^-23 of the
 // largest weight. (An
 // earlier form widened the codes to fp16 in shared memory; the two warps that
-// did it set the pace: 620 us for 96 requests of 8192 keys, now 425.) Per-tensor scales
-// are constants of the softmax and of the output. Block scales are powers of
+// did it set the pace: 620 us for 96 requests of 8192 keys, now 418, and 326 with
+// per-tensor scales.) These are constants of the softmax and of the output. Block scales are powers of
 // two per key: K's multiplies the key's column of S, V's the column of P
 // relative to the largest V scale met so far.
 #pragma once
@@ -60,7 +60,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 template <typename T, int D, int KV>
 struct TLayout {
   static constexpr bool F8 = KV != 0;
-  static constexpr int BK = F8 ? POD_TREE_BLOCK8 : POD_TREE_BLOCK;   // keys per block
+  static constexpr int BK = KV == 2 ? POD_TREE_BLOCKB : POD_TREE_BLOCK;   // keys per block
   static constexpr int ES = F8 ? 1 : 2;                // operand bytes
   static constexpr int ROWB = D * ES < 128 ? D * ES : 128;   // bytes of a row part
   static constexpr int PARTS = D * ES / ROWB;          // row parts
@@ -70,20 +70,21 @@ struct TLayout {
   static constexpr int QPART = POD_TREE_TILE * ROWB;   // one row part of one precision part
   static constexpr int KVPART = BK * ROWB;             // one row part of a block of K or V
   static constexpr int STAGE = PARTS * KVPART;
-  static constexpr int NK = F8 ? 2 : 3, NV = KV == 1 && QP == 2 && D <= 128 ? 3 : 2;
+  static constexpr int NK = KV == 2 ? 2 : KV == 1 ? 4 : 3;
+  static constexpr int NV = KV != 1 ? 2 : QP == 3 && D == 128 ? 3 : 4;
   static constexpr int Q_OFF = 0;
   static constexpr int Q_BYTES = QP * PARTS * QPART;
   static constexpr int K_OFF = Q_BYTES;
   static constexpr int V_OFF = K_OFF + NK * STAGE;
   static constexpr int BAR_OFF = V_OFF + NV * STAGE;
-  // BAR_OFF + 0: barriers, +160: TMEM address, +164: abort flag, +168: the
-  // warps' largest V exponents of two blocks, +208: the block's factors (K,
+  // BAR_OFF + 0: barriers, +192: TMEM address, +196: abort flag, +200: the
+  // warps' largest V exponents of two blocks, +240: the block's factors (K,
   // then V). One set for the CTA: a set for each warp would spare the meetings,
   // and a loader warp for the exponent bytes the loads, but both made the code
   // larger than the instruction cache and the loop slower (when the loop took 405 us
   // for 96 requests of 8192 keys: 409 and 430).
-  static constexpr int WM_OFF = BAR_OFF + 168;
-  static constexpr int FAC_OFF = BAR_OFF + 208;
+  static constexpr int WM_OFF = BAR_OFF + 200;
+  static constexpr int FAC_OFF = BAR_OFF + 240;
   // (floats, or bf16 beside the three Q parts of fp16 rows of 128 elements, which
   // leave no room for more)
   static constexpr int FAC = QP == 3 && D == 128 ? 2 : 4;
@@ -94,9 +95,11 @@ struct TLayout {
   static constexpr int TOTAL = END;
   static_assert(POD_TREE_TILE * JOIN * 4 <= Q_BYTES && POD_TREE_TILE * 8 <= Q_BYTES, "the join must fit the Q region");
   // TMEM: S buffers, then O. Two buffers let Q K^T of the next block run beside
-  // the softmax of this one; FP8 blocks of 128 keys leave room for one where
-  // two CTAs share the SM (these overlap each other).
-  static constexpr int NSB = F8 && D <= 128 ? 1 : 2;
+  // the softmax of this one: 96 requests of 8192 keys with per-tensor scales took
+  // 352 us in blocks of 128 keys with one, 326 in blocks of 64 with two. Block
+  // scales cost the softmax warps a meeting a block, so these keep blocks of 128
+  // (418 us; 487 with 64), which leave room for one where two CTAs share the SM.
+  static constexpr int NSB = KV == 2 && D <= 128 ? 1 : 2;
   // (with two, warp 7 issues MMAs and two warps gather; else three)
   static constexpr int GW = NSB > 1 ? 2 : 3;
   static constexpr int TM_S = 0, TM_O = NSB * BK;
@@ -122,15 +125,15 @@ struct TLayout {
 
 enum {
   TB_QFULL = 0,
-  TB_KFULL = 1,    // [3]
-  TB_KEMPTY = 4,   // [3]
-  TB_VFULL = 7,    // [3]
-  TB_VEMPTY = 10,  // [3]
-  TB_SFULL = 13,   // [2]
-  TB_PFULL = 15,   // [2]
-  TB_PVDONE = 17,  // [2]
-  TB_FINAL = 19,
-  TB_COUNT = 20
+  TB_KFULL = 1,    // [4]
+  TB_KEMPTY = 5,   // [4]
+  TB_VFULL = 9,    // [4]
+  TB_VEMPTY = 13,  // [4]
+  TB_SFULL = 17,   // [2]
+  TB_PFULL = 19,   // [2]
+  TB_PVDONE = 21,  // [2]
+  TB_FINAL = 23,
+  TB_COUNT = 24
 };
 
 // W (16, 32 or 64) consecutive TMEM columns of the warp's 32 lanes
@@ -261,21 +264,20 @@ POD_DEV void factors4(uint32_t base, int key, uint64_t* f) {
 }
 
 // Page-table view of one segment: the cache row (in rows of D elements, K) of
-// key t and KV head g.
+// key t (below kv_len) and KV head g.
 struct KeyAt {
   const int32_t* pages;
-  int npages, ps, shift, hk, hnd, g;
-  POD_DEV int page(int t) const {
-    const int i = shift >= 0 ? t >> shift : t / ps;
-    return __ldg(pages + (i < npages ? i : npages - 1));
-  }
-  POD_DEV long long row(int t, int page) const {
+  long long page_rows;                               // rows of a page, K and V
+  int ps, shift, hk, hnd, g;
+  POD_DEV int page(int t) const { return __ldg(pages + (shift >= 0 ? t >> shift : t / ps)); }
+  POD_DEV int in_page(int t) const {
     const int slot = shift >= 0 ? t & (ps - 1) : t % ps;
-    return (long long)page * 2 * ps * hk + (hnd ? (long long)g * ps + slot : (long long)slot * hk + g);
+    return hnd ? g * ps + slot : slot * hk + g;
   }
+  POD_DEV long long row(int t, int page) const { return page * page_rows + in_page(t); }
 };
 POD_DEV KeyAt key_at(const PodTreeParams& P, const int32_t* seg) {
-  return KeyAt{P.pages + seg[TS_PAGE0], seg[TS_NPAGES], P.ps, P.ps_shift, P.Hk, P.hnd, seg[TS_G]};
+  return KeyAt{P.pages + seg[TS_PAGE0], P.page_rows, P.ps, P.ps_shift, P.Hk, P.hnd, seg[TS_G]};
 }
 
 // What one row sees at the end of its request.
@@ -566,7 +568,7 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
 #pragma unroll
     for (int h = 0; h < NH; ++h) {
       if (h > 0) load_s(my0 + h * W, s);
-      constexpr int N = L::F8 ? 32 : 16;             // keys of 8 columns
+      constexpr int N = L::F8 && W >= 32 ? 32 : 16;  // keys of 8 columns (of 4: half a step)
 #pragma unroll
       for (int q = 0; q < W; q += N) {
         uint64_t e[N / 2];
@@ -577,7 +579,7 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
           e[i / 2] = pack2(ex2(a), ex2(b2));
           rs[i / 2 & 1] = add2(rs[i / 2 & 1], e[i / 2]);
         }
-        const uint32_t col = (uint32_t)(my0 + h * W + q) / N * (8 * L::PP);
+        const uint32_t col = (uint32_t)(my0 + h * W + q) / L::KSTEP * (8 * L::PP);
         uint32_t parts[L::PP][8];
         if constexpr (!L::F8) {
 #pragma unroll
@@ -597,11 +599,18 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
             }
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < N / 4; ++i) {
             uint32_t w[L::PP];
             split4<L::PP>(e[2 * i], e[2 * i + 1], w);
 #pragma unroll
-            for (int p = 0; p < L::PP; ++p) parts[p][i] = w[p];
+            for (int p = 0; p < L::PP; ++p) {
+              if (N == 32) {
+                parts[p][i] = w[p];
+              } else {                               // (zeros for the neighbour copy's keys)
+                parts[p][i] = cp & 1 ? 0u : w[p];
+                parts[p][i + 4] = cp & 1 ? w[p] : 0u;
+              }
+            }
           }
         }
 #pragma unroll
@@ -612,7 +621,7 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
       const uint32_t zero[8] = {};
 #pragma unroll
       for (int c = 0; c < BK / L::KSTEP; ++c)        // key steps
-        if (c / (BK / L::KSTEP / C) != cp)
+        if (TW < L::KSTEP ? c != cp >> 1 : c / (TW < L::KSTEP ? 1 : TW / L::KSTEP) != cp)
 #pragma unroll
           for (int p = 0; p < L::PP; ++p) tmem_st8(s_addr + 8 * (c * L::PP + p), zero);
     }
@@ -788,7 +797,7 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (uniform, and known to be)
   const uint32_t sbase = smem_u32(smem), bar0 = sbase + L::BAR_OFF;
-  static_assert(TB_COUNT * 8 <= 160, "barriers overlap the TMEM slot");
+  static_assert(TB_COUNT * 8 <= 192, "barriers overlap the TMEM slot");
   if ((sbase & 1023u) != 0u) {                       // 128B-swizzle atoms need 1024-byte alignment
     if (tid == 0) atomicOr(P.status, POD_STATUS_ALIGN);
     return;
@@ -797,16 +806,16 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
   const int seg0 = P.cta_ptr[blockIdx.x], seg1 = P.cta_ptr[blockIdx.x + 1];
   if (warp == 5 && lane < 2 && P.kbx > 0) tma_prefetch_desc(lane ? &P.tm_v : &P.tm_k);
   auto BAR = [&](int i) { return bar0 + 8u * (uint32_t)i; };
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::BAR_OFF + 164);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::BAR_OFF + 196);
   if (warp == 4) {
-    tmem_alloc(sbase + L::BAR_OFF + 160, L::TMEM_COLS);
+    tmem_alloc(sbase + L::BAR_OFF + 192, L::TMEM_COLS);
     tmem_relinquish();
   }
   const bool tma = P.kbx > 0;
   if (tid == 0) {
     const uint32_t loads = tma ? 1u : 32u * L::GW;   // gather: two or three warps
     mbar_init(BAR(TB_QFULL), 128);
-    for (int s = 0; s < 3; ++s) {
+    for (int s = 0; s < 4; ++s) {
       mbar_init(BAR(TB_KFULL + s), loads);
       mbar_init(BAR(TB_KEMPTY + s), 1);
       mbar_init(BAR(TB_VFULL + s), loads);
@@ -825,7 +834,7 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::BAR_OFF + 160);
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::BAR_OFF + 192);
   bool ok = true;
   volatile int never = 0;                            // an abort flag that nobody raises
 

@@ -5,8 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#define POD_TREE_BLOCK 64     // keys per block (one S buffer, one stage), 16-bit caches
-#define POD_TREE_BLOCK8 128   // the same for FP8 caches
+#define POD_TREE_BLOCK 64     // keys per block (one S buffer, one stage)
+#define POD_TREE_BLOCKB 128   // the same for block-scaled caches
 #define POD_TREE_TILE 128     // packed query rows per tile (TMEM lanes)
 
 // Segment record, one for each run of key blocks that a CTA works through for
@@ -46,6 +46,7 @@ struct PodTreeParams {
   const int32_t *segs, *cta_ptr, *pages, *groups;
   float *part_o, *part_lse;
   int32_t* status;
+  long long page_rows;           // cache rows of a page, K and V
   int H, Hk, G, ps, ps_shift, hnd, num_pages;
   int kbx;                       // keys per TMA box, 0: gather
   int n_cta, n_groups, n_big;    // merge groups, those of many segments

@@ -264,7 +264,7 @@ pod_status pod_tree_plan(const int32_t* q_indptr, const int32_t* kv_indptr, cons
   PodTreeArgs a;
   a.q_indptr = q_indptr; a.kv_indptr = kv_indptr; a.kv_indices = kv_indices; a.last_page_len = last_page_len;
   a.batch = batch; a.num_pages = num_pages; a.H = num_qo_heads; a.Hk = num_kv_heads; a.d = head_dim;
-  a.block = kv_format == POD_KV_16BIT ? POD_TREE_BLOCK : POD_TREE_BLOCK8;
+  a.block = kv_format == POD_KV_E4M3_BLOCK ? POD_TREE_BLOCKB : POD_TREE_BLOCK;
   a.ps = page_size; a.slots = num_sms * (head_dim == 256 ? 1 : 2);
   std::string err;
   int rc;
@@ -332,10 +332,11 @@ pod_status pod_tree_run(pod_tree_handle h, const void* q, const void* kv, const 
   K.part_lse = reinterpret_cast<float*>(ws + P.off_part_lse);
   K.status = reinterpret_cast<int32_t*>(ws);
   K.H = P.H; K.Hk = P.Hk; K.G = P.G; K.ps = P.ps; K.hnd = h->hnd; K.num_pages = P.num_pages;
+  K.page_rows = 2ll * P.ps * P.Hk;
   K.ps_shift = -1;
   for (int s = 0; s < 31; ++s)
     if ((1 << s) == P.ps) K.ps_shift = s;
-  const int block = h->format == POD_KV_16BIT ? POD_TREE_BLOCK : POD_TREE_BLOCK8;
+  const int block = h->format == POD_KV_E4M3_BLOCK ? POD_TREE_BLOCKB : POD_TREE_BLOCK;
   K.kbx = K.ps_shift >= 3 ? (P.ps < block ? P.ps : block) : 0;
   K.n_cta = P.n_cta; K.n_groups = (int)(P.groups.size() / TG_REC); K.n_big = P.n_big;
   K.scale_log2 = h->scale_log2; K.v_scale = h->v_scale;

@@ -85,6 +85,8 @@ class Case:
         sel = ~used[:, None, :, None].expand(-1, 2, -1, Hk) if layout == "NHD" else \
             ~used[:, None, None, :].expand(-1, 2, Hk, -1)
         flat[sel] = math.nan if fmt == "16bit" else 0x7F
+        if self.scales is not None:
+            self.scales[sel] = 0xFF
         # masks
         self.bits = []
         for x in n:
@@ -470,7 +472,7 @@ def test_plan_covers_every_block_once(name, sms):
                 mine = set(range(prow, prow + nrows))
                 assert not mine & prows
                 prows |= mine
-        blk = 64 if c.fmt == "16bit" else 128
+        blk = 128 if c.fmt == "block" else 64
         assert at == (c.kv_len[r] + blk - 1) // blk
     assert prows == set(range(len(prows)))
     assert ctas[0] == 0 and ctas[-1] == len(segs) and (np.diff(ctas) > 0).all()
