@@ -29,13 +29,13 @@
 // its largest value to [128, 256) and split into E4M3 parts, two for bf16 rows
 // (4 + 4 significant bits, all it has), three for fp16 rows (11 bits); parts
 // below 2^-17 of the row's largest value lose bits. P (the largest
-// between 2^6 and 2^8.5) is carried in parts by Veltkamp splitting. bf16 results:
-// two E4M3 parts, 4 bits and the remainder to 4 bits, at most 2^-9 of p off, and
-// 2^-15 of the largest weight at the bottom. fp16 results: 4 bits in E4M3 and
-// twice 3 bits in E5M2, whose range goes on below, 2^-11 of p and 2^-23 of the
+// between 2^6 and 2^8.5) is carried in parts. bf16 results:
+// two E4M3 parts, 4 bits and the fp16 remainder to 4 bits, at most 2^-9 + 2^-11 of
+// p off, and 2^-15 of the largest weight at the bottom. fp16 results, by Veltkamp
+// splitting: 4 bits in E4M3 and twice 3 bits in E5M2, whose range goes on below, 2^-11 of p and 2^-23 of the
 // largest weight. (An
 // earlier form widened the codes to fp16 in shared memory; the two warps that
-// did it set the pace: 620 us for 96 requests of 8192 keys, now 418, and 326 with
+// did it set the pace: 620 us for 96 requests of 8192 keys, now 410, and 330 with
 // per-tensor scales.) These are constants of the softmax and of the output. Block scales are powers of
 // two per key: K's multiplies the key's column of S, V's the column of P
 // relative to the largest V scale met so far.
@@ -98,7 +98,7 @@ struct TLayout {
   // the softmax of this one: 96 requests of 8192 keys with per-tensor scales took
   // 352 us in blocks of 128 keys with one, 326 in blocks of 64 with two. Block
   // scales cost the softmax warps a meeting a block, so these keep blocks of 128
-  // (418 us; 487 with 64), which leave room for one where two CTAs share the SM.
+  // (427 us; 487 with 64), which leave room for one where two CTAs share the SM.
   static constexpr int NSB = KV == 2 && D <= 128 ? 1 : 2;
   // (with two, warp 7 issues MMAs and two warps gather; else three)
   static constexpr int GW = NSB > 1 ? 2 : 3;
@@ -212,36 +212,38 @@ POD_DEV uint64_t head2(uint64_t x) {
   return add2(t, fma2(t, pack2(-1.f, -1.f), x));     // (products with -1 are exact)
 }
 // Four values below 448 (two pairs) in parts whose sum they are (byte i: value i):
-// two E4M3 words, or (three parts) an E4M3 and two E5M2 words.
+// two E4M3 words (the second of the difference to the fp16 value), or (three parts)
+// an E4M3 and two E5M2 words. Two parts by splitting in fp32, as the three are
+// made, took 5 % longer over a block-scaled cache.
 template <int PARTS>
 POD_DEV void split4(uint64_t x01, uint64_t x23, uint32_t* w) {
+  if constexpr (PARTS == 2) {
+    float x[4];
+    unpack2(x01, x[0], x[1]);
+    unpack2(x23, x[2], x[3]);
+    e4m3_hi_lo4(x[0], x[1], x[2], x[3], w[0], w[1]);
+    return;
+  }
   const uint64_t neg = pack2(-1.f, -1.f);
   const uint64_t x[2] = {x01, x23};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    uint64_t v = head2<4>(x[i]);
-    // three parts: below E4M3's normal range the head is a multiple of 2^-9, so
-    // that the code is exactly it and the rest goes to the other parts
-    if (PARTS == 3) v = add2(add2(v, pack2(24576.f, 24576.f)), pack2(-24576.f, -24576.f));
+    // below E4M3's normal range the head is a multiple of 2^-9, so that the code is
+    // exactly it and the rest goes to the other parts
+    const uint64_t v = add2(add2(head2<4>(x[i]), pack2(24576.f, 24576.f)), pack2(-24576.f, -24576.f));
     uint64_t r = fma2(v, neg, x[i]);
+    const uint64_t m = head2<3>(r);
+    r = fma2(m, neg, r);
     float a, b;
     unpack2(v, a, b);
     const uint32_t h = f32x2_to_e4m3x2(a, b);
+    unpack2(m, a, b);
+    const uint32_t l = f32x2_to_e5m2x2(a, b);
+    unpack2(r, a, b);
+    const uint32_t k = f32x2_to_e5m2x2(a, b);
     w[0] = i ? w[0] | (h << 16) : h;
-    if constexpr (PARTS == 2) {
-      unpack2(r, a, b);
-      const uint32_t l = f32x2_to_e4m3x2(a, b);
-      w[1] = i ? w[1] | (l << 16) : l;
-    } else {
-      const uint64_t m = head2<3>(r);
-      r = fma2(m, neg, r);
-      unpack2(m, a, b);
-      const uint32_t l = f32x2_to_e5m2x2(a, b);
-      w[1] = i ? w[1] | (l << 16) : l;
-      unpack2(r, a, b);
-      const uint32_t k = f32x2_to_e5m2x2(a, b);
-      w[2] = i ? w[2] | (k << 16) : k;
-    }
+    w[1] = i ? w[1] | (l << 16) : l;
+    w[PARTS - 1] = i ? w[PARTS - 1] | (k << 16) : k;
   }
 }
 

@@ -7,7 +7,8 @@ Tolerances, fixed before the first run. An output is sum_t p_t v_t / l:
     fp16 2^-11, or 2^-25 of the largest weight below its normal range. For FP8
     caches it is two E4M3 parts of P, the largest P at least 2^6: x rounded to 4
     significant bits leaves at most 2^-4 of x's binade 2^e, 4 bits of that leave
-    2^-9 * 2^e, so 2^-9 of x; below E4M3's normal range (2^-6) the parts are
+    2^-9 * 2^e, and the remainder is taken from x in fp16, off by 2^-11 * 2^e: so
+    2^-9 + 2^-11 of x; below E4M3's normal range (2^-6) the parts are
     multiples of 2^-9, at most 2^-10 off each, together 2^-9, which is 2^-15 of
     the largest weight. With fp16 results the remainder is two E5M2 parts of 3
     bits instead: 3 bits of at most 2^-4 * 2^e leave 2^-8 * 2^e, 3 bits of that
@@ -132,7 +133,7 @@ class Case:
         if self.fmt == "16bit":
             u_p, tiny = (2.0 ** -8, 0.0) if bf else (2.0 ** -11, 2.0 ** -25)
         else:
-            u_p, tiny = (2.0 ** -9, 2.0 ** -15) if bf else (2.0 ** -12, 2.0 ** -22)
+            u_p, tiny = (2.0 ** -9 + 2.0 ** -11, 2.0 ** -15) if bf else (2.0 ** -12, 2.0 ** -22)
         eps = torch.finfo(self.dtype).eps / 2
         for r in range(len(self.n)):
             n, L = self.n[r], self.kv_len[r]
