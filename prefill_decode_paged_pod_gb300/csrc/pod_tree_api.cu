@@ -143,6 +143,8 @@ constexpr int kManyChunks = POD_TREE_TILE / 2, kFewChunks = POD_TREE_TILE / 32;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ PodTreeParams P) {
+  // the next call's kernel may set itself up beside this one
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int many = P.n_big * kManyChunks, b = (int)blockIdx.x;
   if (b < many)

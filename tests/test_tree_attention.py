@@ -432,6 +432,38 @@ def test_verification_step(fmt):
     assert ((back[:, 0].float() - k).abs() <= (step + 2.0 ** -7) * k.abs() + 0.01 * (fmt != "16bit")).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["16bit", "scaled", "block"])
+def test_calls_right_behind_each_other(fmt):
+    """Layers on one stream: each call's queries are the last one's output, its
+    new keys are written by the call before; nothing waits on the host. The
+    kernels may overlap, the results may not differ from waiting for each."""
+    c = Case(n=[9, 30, 4], kv_len=[2500, 700, 40], H=8, Hk=2, d=128, ps=16, fmt=fmt, seed=2)
+    h = c.plan(num_sms=20)                            # (few CTAs: cut units, a merge a call)
+    assert len(pod.pod_tree_plan_table(h, 2)) > 0
+    ws = torch.empty(pod.pod_tree_workspace_size(h), dtype=torch.uint8, device="cuda")
+    pod.pod_tree_bind_workspace(h, ws)
+    rows = sum(c.n)
+    req = np.repeat(np.arange(3), c.n)
+    at = np.concatenate([np.arange(a - b, a) for a, b in zip(c.kv_len, c.n)])
+    slots = torch.from_numpy(pod.pod_kv_slots(c.kv_indptr, c.kv_indices, c.ps, req, at)).cuda()
+
+    def layers(wait):
+        q, kv, more = c.args()
+        for _ in range(8):
+            new = q[:, :2].contiguous()
+            pod.pod_append_kv(new, new, kv, slots, kv_scales=more["kv_scales"], k_scale=c.ks, v_scale=c.vs)
+            if wait:
+                torch.cuda.synchronize()
+            q, lse = pod.pod_tree_run(h, q, kv, ws, **more)
+            if wait:
+                torch.cuda.synchronize()
+        return q, lse
+    want, got = layers(True), layers(False)
+    assert rows == len(got[0]) and torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    assert got[0].isfinite().all()
+
+
 # ------------------------------------------------------------------ planner (host)
 def tables(c, sms):
     h = c.plan(num_sms=sms)
