@@ -85,6 +85,27 @@ struct IoFreq {                  // (a kernel parameter: no longer than it has t
   uint64_t f[D / 2];
 };
 
+// The kernels are launched beside the one before (programmatic stream
+// serialization) and wait for it here; so may the next. One call after another:
+// 16384 block-scaled rows written 20.1 -> 18.2 us, 4096 rows normed and written 32.7
+// -> 30.8, 65536 read 66.5 -> 64.3.
+POD_DEV void after_the_last_kernel() {
+  asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+}
+template <typename... A, typename... B>
+cudaError_t launch_beside(void (*kernel)(A...), unsigned grid, cudaStream_t st, const B&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kIoThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Element offset of (slot, K half, head 0) in the cache, and the steps to the
 // next head and to the V half.
 struct SlotMap {
@@ -408,6 +429,7 @@ POD_DEV void io_pass(const IoParams& P, const IoFreq<FUSED ? D : 2>& F, const Io
 template <typename T, int D, int FMT, bool FUSED>
 __global__ void __launch_bounds__(kIoThreads) cache_io_kernel(const __grid_constant__ IoParams P,
                                                               const __grid_constant__ IoFreq<FUSED ? D : 2> F) {
+  after_the_last_kernel();
   if constexpr (FUSED) {
     if ((int)blockIdx.x < P.cut[1].first)
       io_pass<T, D, FMT, IO_Q, true>(P, F, P.cut[0]);
@@ -425,6 +447,7 @@ __global__ void __launch_bounds__(kIoThreads) cache_io_kernel(const __grid_const
 // the largest of T saturate. A negative slot gives a row of zeros.
 template <typename T, int D, int FMT>
 __global__ void __launch_bounds__(kIoThreads, 4) cache_read_kernel(const __grid_constant__ IoParams P) {
+  after_the_last_kernel();
   constexpr int EPL = FMT == FMT_16 ? 8 : 16;    // elements per lane
   constexpr int LPR = D / EPL, NG = kIoThreads / LPR;
   __shared__ long long base[kMaxTok];
@@ -569,11 +592,11 @@ cudaError_t launch_io(IoParams& P, bool fused, const IoFreq<256>& f, cudaStream_
   if (fused) {
     IoFreq<D> fd;
     memcpy(&fd, &f, sizeof(fd));
-    cache_io_kernel<T, D, FMT, true><<<grid, kIoThreads, 0, st>>>(P, fd);
+    return launch_beside(cache_io_kernel<T, D, FMT, true>, grid, st, P, fd);
   } else if constexpr (cache) {
-    cache_io_kernel<T, D, FMT, false><<<grid, kIoThreads, 0, st>>>(P, IoFreq<2>{});
+    return launch_beside(cache_io_kernel<T, D, FMT, false>, grid, st, P, IoFreq<2>{});
   }
-  return cudaGetLastError();
+  return cudaErrorInvalidValue;                  // (a write without a cache is not asked for)
 }
 template <typename T, int D>
 cudaError_t launch_fmt(IoParams& P, int fmt, bool fused, const IoFreq<256>& f, cudaStream_t st) {
@@ -596,10 +619,9 @@ cudaError_t launch_read(IoParams& P, int fmt, cudaStream_t st) {
   const long long blocks = cut_of(P.cut[0], 0, P.rows, 2 * P.Hk, tasks_of(P, 2 * P.Hk, round, 2));
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const unsigned grid = (unsigned)blocks;
-  if (fmt == FMT_16) cache_read_kernel<T, D, FMT_16><<<grid, kIoThreads, 0, st>>>(P);
-  else if (fmt == FMT_SCALED) cache_read_kernel<T, D, FMT_SCALED><<<grid, kIoThreads, 0, st>>>(P);
-  else cache_read_kernel<T, D, FMT_BLOCK><<<grid, kIoThreads, 0, st>>>(P);
-  return cudaGetLastError();
+  return fmt == FMT_16 ? launch_beside(cache_read_kernel<T, D, FMT_16>, grid, st, P)
+         : fmt == FMT_SCALED ? launch_beside(cache_read_kernel<T, D, FMT_SCALED>, grid, st, P)
+                             : launch_beside(cache_read_kernel<T, D, FMT_BLOCK>, grid, st, P);
 }
 
 pod_status check_rows(const char* what, const void* p, int64_t stride, int64_t heads, int d) {

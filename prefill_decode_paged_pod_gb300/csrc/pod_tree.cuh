@@ -285,6 +285,20 @@ POD_DEV KeyAt key_at(const PodTreeParams& P, const int32_t* seg) {
   return KeyAt{P.pages + seg[TS_PAGE0], P.page_rows, P.ps, P.ps_shift, P.Hk, P.hnd, seg[TS_G]};
 }
 
+// 64 bits of a packed array from bit `pos`; bytes at or past `nbytes` read as zero.
+// (Plain loads, here and of Q: a kernel that starts beside the one before must not
+// take what that one writes for constant.)
+POD_DEV uint64_t tree_bits64(const uint8_t* m, long long nbytes, long long pos) {
+  const long long b0 = pos >> 3;
+  const int sh = (int)(pos & 7);
+  uint64_t lo = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (b0 + k < nbytes) lo |= (uint64_t)m[b0 + k] << (8 * k);
+  const uint64_t hi = b0 + 8 < nbytes ? (uint64_t)m[b0 + 8] : 0ull;
+  return sh ? (lo >> sh) | (hi << (64 - sh)) : lo;
+}
+
 // What one row sees at the end of its request.
 struct TreeView {
   const uint8_t* mask;
@@ -296,7 +310,7 @@ struct TreeView {
     const int skip = max(ctx - c0, 0);               // context keys at the front
     const int j0 = c0 + skip - ctx;                  // first tree key
     if (j0 < ntok) {
-      see = mask ? load_bits64(mask, mask_bytes, bit0 + j0)
+      see = mask ? tree_bits64(mask, mask_bytes, bit0 + j0)
                  : (tok - j0 >= 63 ? ~0ull : tok < j0 ? 0ull : (2ull << (tok - j0)) - 1ull);
       const int left = ntok - j0;
       if (left < 64) see &= (1ull << left) - 1ull;
@@ -383,7 +397,7 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
         const int ln = (i0 + k) * RPI + sub;
         const size_t g = (size_t)__shfl_sync(0xffffffffu, (unsigned long long)grow, ln);
         next[k] = make_uint4(0, 0, 0, 0);
-        if ((live >> ln) & 1) next[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(P.q) + g * D) + ch);
+        if ((live >> ln) & 1) next[k] = reinterpret_cast<const uint4*>(static_cast<const T*>(P.q) + g * D)[ch];
       }
     };
     auto put = [&](int i, const uint4& v) {          // the rows of iteration i into shared memory
