@@ -224,9 +224,14 @@ POD_DEV void io_tables(const IoParams& P, const IoFreq<FD>& F, IoTables<TURN ? D
     for (int i = tid; i < ntok * half; i += kIoThreads) {
       const int t = i / half, j = i - t * half;
       const uint64_t ph = (uint64_t)(int64_t)P.pos[tok0 + t] * F.f[j];
-      const float fr = (float)(int32_t)(ph >> 32) * 4.656612873077393e-10f;   // half turns: 2^-31
-      float sn, c;
-      sincospif(fr, &sn, &c);
+      // the nearest quarter turn, and what is left of the angle: at most an eighth of
+      // a turn, so that its rounding to fp32 is below that of cos and sin
+      const int quarter = (int)((ph + (1ull << 61)) >> 62);
+      const float fr = (float)(int)((long long)(ph - ((uint64_t)quarter << 62)) >> 30) * 0x1p-33f;   // half turns
+      float s0, c0;
+      sincospif(fr, &s0, &c0);
+      const float c = __uint_as_float(__float_as_uint(quarter & 1 ? s0 : c0) ^ (uint32_t)((quarter + 1) & 2) << 30);
+      const float sn = __uint_as_float(__float_as_uint(quarter & 1 ? c0 : s0) ^ (uint32_t)(quarter & 2) << 30);
       // a lane's 8 pairs: j = 8 lane + 0..7 in either pairing
       const int l = j >> 3, i8 = j & 7;
       float* at = cs + 4 * (t * (half / 2) + (i8 >> 1) * turning + l) + (i8 & 1);
@@ -326,7 +331,7 @@ POD_DEV void io_pass(const IoParams& P, const IoFreq<FUSED ? D : 2>& F, const Io
           float ss = a + b;
 #pragma unroll
           for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, LPR);
-          const float rs = rsqrtf(ss * (1.f / D) + P.eps);
+          const float rs = __frsqrt_rn(ss * (1.f / D) + P.eps);
           const uint64_t rs2 = pack2(rs, rs);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {

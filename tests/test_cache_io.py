@@ -171,6 +171,29 @@ def test_norm_rope(case):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_cos_and_sin_are_fp32_ones(interleaved):
+    """Pairs (1, 0) turn into (cos, sin): the nearest fp16 value, unless the true one
+    is that near to a tie. The angle left of the nearest quarter turn is at most 1/4
+    half turn, so its rounding is off by 2^-27 of a half turn, 2^-25.3 radians; cos
+    and sin of it by an ulp below 1, 2^-24: together 2^-23.4."""
+    d, rows = 64, 3000
+    r = np.random.RandomState(3)
+    pos = r.randint(-131072, 131073, rows).astype(np.int32)
+    pos[:2] = [0, 1]
+    k = torch.zeros((rows, 1, d), dtype=torch.float16)
+    first = np.arange(0, d, 2) if interleaved else np.arange(d // 2)
+    second = first + (1 if interleaved else d // 2)
+    k[:, :, torch.from_numpy(first)] = 1
+    out = pod.pod_qk_norm_rope(None, k.cuda(), torch.from_numpy(pos).cuda(), interleaved=interleaved)[1]
+    out = out[:, 0].double().cpu().numpy()
+    angle = pos.astype(np.float64)[:, None] * 1e4 ** (-2.0 * np.arange(d // 2) / d)
+    for got, want in ((out[:, first], np.cos(angle)), (out[:, second], np.sin(angle))):
+        step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(want), 2.0 ** -14))) - 10)
+        assert (np.abs(got - want) <= step / 2 + 2.0 ** -23.4).all(), np.abs(got - want).max()
+
+
+@pytest.mark.gpu
 def test_norm_special_values():
     """Zeros stay zeros, a NaN stays in its head, no rows launch nothing."""
     x = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
