@@ -33,8 +33,8 @@
 // Measured on a GB300, back to back in a graph, with the share of the measured
 // copy rate: norm and rotation of 8796 rows of 64/8 heads of 128, bf16: 57 us,
 // 85 % (84); 4096 rows of 64/8 heads normed, turned and written: 29.7 us, 85 %
-// (45); 16384 rows of 8 heads written with block scales: 18.4 us, 82 % (26.6);
-// 65536 rows read back: 64 us, 95 %. Calls of a few hundred rows take 3.5 to 5
+// (45); 16384 rows of 8 heads written with block scales: 18.0 us, 84 % (26.6);
+// 65536 rows read back: 63 us, 96 %. Calls of a few hundred rows take 3.5 to 5
 // us, the launch and two dependent trips to memory.
 #include <cuda_runtime.h>
 #include <math.h>
