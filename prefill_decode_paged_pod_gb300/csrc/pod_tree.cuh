@@ -878,8 +878,7 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
     // then stay in uniform registers (a loop under `lane == 0` moved each of them
     // there for every MMA: 85 clocks an instruction). The second warp takes the
     // waits of one product off the other's: 16 requests of 64 tokens and 4100 keys
-    // went from 137 to 129 us with pages of 64; with pages of 16 they stay at 136,
-    // bound by their 12 boxes a block.
+    // went from 137 to 129 us with pages of 64; with pages of 16 they stayed at 136.
     const uint32_t id_qk = L::F8 ? idesc_f8(false, 128, BK, false, false) : idesc_f16(Pack<T>::kBF16, 128, BK, false, false);
     const uint32_t id_pv = L::F8 ? idesc_f8(false, 128, D, false, true) : idesc_f16(Pack<T>::kBF16, 128, D, false, true);
     // V stage: 16-bit TMA boxes of vb keys lie as [box][row part][key], anything
@@ -1013,18 +1012,17 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
       const void* tm = is_v ? &P.tm_v : &P.tm_k;
       const int NS = is_v ? L::NV : L::NK;
       // boxes of a block: groups of kbx keys, a box for each row part; a 16-bit V
-      // box holds every part
+      // box holds every part. (No eviction hint: with evict-first where a key serves
+      // one tile only, and so two forms of the load, wide trees took 134 us, not 129,
+      // 64 ragged requests 386, not 383.)
       const bool whole = is_v && !L::F8;
       const int groups = BK / P.kbx, per = whole ? 1 : L::PARTS;
       const int gi = lane / per, part = lane - gi * per;
       const bool mine = gi < groups;
-      // keys are read once unless another tile of the request reads them too
-      const uint64_t pol = l2_policy_evict_first();
       int fill = 0;
       for (int i = seg0; i < seg1 && ok; ++i) {
         const int32_t* seg = P.segs + (size_t)i * TS_REC;
         const int g = seg[TS_G], npages = seg[TS_NPAGES];
-        const bool shared_keys = (long long)seg[TS_NTOK] * P.G > POD_TREE_TILE;
         const int32_t* pages = P.pages + seg[TS_PAGE0];
         const int b1 = seg[TS_BLK1];
         auto page_of = [&](int blk) {
@@ -1044,10 +1042,7 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
             const uint32_t dst = stage + (whole ? gi * P.kbx * L::PARTS * L::ROWB
                                                 : part * L::KVPART + gi * P.kbx * L::ROWB);
             // (a page past the request's last is out of the pool: TMA fills zeros)
-            if (shared_keys)
-              tma_load_5d(dst, tm, 0, tin, part, g, 2 * page + (is_v ? 1 : 0), BAR(full));
-            else
-              tma_load_5d_hint(dst, tm, 0, tin, part, g, 2 * page + (is_v ? 1 : 0), BAR(full), pol);
+            tma_load_5d(dst, tm, 0, tin, part, g, 2 * page + (is_v ? 1 : 0), BAR(full));
           }
           ++fill;
           if (blk + 1 < b1) page = page_of(blk + 1);
