@@ -336,8 +336,8 @@ POD_DEV void io_pass(const IoParams& P, const IoFreq<FUSED ? D : 2>& F, const Io
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float4 w = S.w[i][lane];
-            x[2 * i] = mul2(mul2(x[2 * i], rs2), pack2(w.x, w.y));
-            x[2 * i + 1] = mul2(mul2(x[2 * i + 1], rs2), pack2(w.z, w.w));
+            x[2 * i] = mul2(mul2(x[2 * i], pack2(w.x, w.y)), rs2);   // (the first product is exact)
+            x[2 * i + 1] = mul2(mul2(x[2 * i + 1], pack2(w.z, w.w)), rs2);
           }
         }
         if (turns) {
