@@ -811,8 +811,6 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
   using L = TLayout<T, D, KV>;
   constexpr int BK = L::BK, NSB = L::NSB;
   extern __shared__ __align__(1024) uint8_t smem[];
-  // the merge kernel may be scheduled now; it waits for this grid's completion
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // (uniform, and known to be)
   const uint32_t sbase = smem_u32(smem), bar0 = sbase + L::BAR_OFF;
@@ -852,6 +850,10 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
   asm volatile("prefetch.global.L1 [%0];" ::"l"(P.segs + (size_t)seg0 * TS_REC));
   tc_fence_before();
   __syncthreads();
+  // The next kernel (the merge, or another call's) may be scheduled now; it waits for
+  // this grid's completion. Not before: a next tree kernel takes tensor memory before
+  // it waits, and must not take what a CTA of this one, which it waits for, still needs.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // (launched while the kernel before may still run: the plan, which only copies
   // write, may be read before this, tensors and the partial rows not)
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1127,10 +1129,23 @@ __global__ void __launch_bounds__(kTreeThreads, D == 256 ? 1 : 2)
   }
 }
 
+// Shared memory asked for: at least 88 KB, so that an SM holds two CTAs of 256 TMEM
+// columns and no third, whatever registers they take, nor two beside one of
+// pod_kernel's (57728 bytes or more): a CTA of the kernel before that has no columns
+// yet never meets two of this one that hold all 512 and wait for it. (The L1 does
+// not lose by it: the carve-out is the largest in any case.)
+template <typename T, int D, int KV>
+constexpr int tree_smem() {
+  return TLayout<T, D, KV>::TOTAL > 88 * 1024 ? TLayout<T, D, KV>::TOTAL : 88 * 1024;
+}
+
 template <typename T, int D, int KV>
 cudaError_t launch_tree(const PodTreeParams& P, cudaStream_t stream) {
-  constexpr int SMEM = TLayout<T, D, KV>::TOTAL;
-  static_assert(SMEM <= (D == 256 ? 232448 : 115712), "shared memory of the CTAs on an SM");
+  constexpr int SMEM = tree_smem<T, D, KV>();
+  constexpr int SM_BYTES = 228 * 1024, CTA_BYTES = SMEM + 1024, CTAS = TLayout<T, D, KV>::TMEM_COLS == 512 ? 1 : 2;
+  static_assert(CTAS * CTA_BYTES <= SM_BYTES, "shared memory of the CTAs on an SM");
+  static_assert((CTAS + 1) * CTA_BYTES > SM_BYTES && CTAS * CTA_BYTES + 57728 > SM_BYTES,
+                "CTAs on an SM beyond its tensor memory");
   // the attributes belong to each device: set once per device
   static std::atomic<unsigned long long> done{0ull};
   static std::mutex mu;
