@@ -86,11 +86,14 @@ int pod_tree_build_plan(const PodTreeArgs& a, PodTreePlanHost& o, std::string* e
   std::vector<int> n(a.batch), kv(a.batch);
   std::vector<long long> bit0(a.batch);
   if (a.batch > 0 && (a.q_indptr[0] != 0 || a.kv_indptr[0] != 0)) return bad(INV, "an indptr does not start at 0");
+  // (all of them before a page is looked at: kv_indices ends where kv_indptr does)
+  for (int r = 0; r < a.batch; ++r)
+    if (a.q_indptr[r + 1] < a.q_indptr[r] || a.kv_indptr[r + 1] < a.kv_indptr[r])
+      return bad(INV, "request " + std::to_string(r) + ": an indptr decreases");
   for (int r = 0; r < a.batch; ++r) {
     const std::string who = "request " + std::to_string(r) + ": ";
     const long long nq = (long long)a.q_indptr[r + 1] - a.q_indptr[r];
     const long long np = (long long)a.kv_indptr[r + 1] - a.kv_indptr[r];
-    if (nq < 0 || np < 0) return bad(INV, who + "an indptr decreases");
     if (np > 0 && (a.last_page_len[r] < 1 || a.last_page_len[r] > a.ps))
       return bad(INV, who + "last_page_len is outside [1, page_size]");
     const long long len = np > 0 ? (np - 1) * a.ps + a.last_page_len[r] : 0;
