@@ -496,10 +496,25 @@ def pod_replan(h: PodHandle, p_q_indptr, p_kv_indptr, p_kv_indices, p_last_page_
 def pod_kv_slots(kv_indptr, kv_indices, page_size: int, request, position):
     """Slots of key ``position[i]`` of request ``request[i]`` (int64, the
     ``slots`` of pod_append_kv and the others): numpy arrays or tensors of one
-    device in, the same kind out."""
-    page = kv_indices[kv_indptr[request] + position // page_size]
-    page = page.long() if hasattr(page, "long") else page.astype(np.int64)
-    return page * page_size + position % page_size
+    device in, the same kind out. A position outside the request's pages (so any
+    negative one), and a request that is not in the table, give -1, the slot of a
+    padding row; nothing outside the table is read."""
+    if hasattr(kv_indptr, "data_ptr"):
+        xp = _torch()
+        ask = lambda x: xp.as_tensor(x, device=kv_indptr.device).long()   # noqa: E731
+    else:
+        xp = np
+        ask = lambda x: np.asarray(x).astype(np.int64)                    # noqa: E731
+    indptr, indices, request, position = ask(kv_indptr), ask(kv_indices), ask(request), ask(position)
+    batch, pages = indptr.shape[0] - 1, indices.shape[0]
+    if batch < 1 or pages < 1:
+        return xp.full_like(request + position, -1)
+    known = (request >= 0) & (request < batch)
+    request = xp.where(known, request, 0)
+    at = indptr[request] + position // page_size
+    inside = known & (position >= 0) & (at < indptr[request + 1]) & (at < pages)
+    slots = indices[xp.where(inside, at, 0)] * page_size + position % page_size
+    return xp.where(inside, slots, -1)
 
 
 _KV_FORMATS = {"16bit": 0, "scaled": 1, "block": 2}
