@@ -692,7 +692,9 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
   if constexpr (C == 1) {
     float denom = l;
     if (P.sinks && prow < 0) denom += ex2(P.sinks[head] * kLog2e - m_ref);
-    const float inv = denom == 0.f ? 0.f : v_scale / denom;   // (a NaN row stays NaN)
+    // a row without keys is 0, whatever its sink (-inf less the reference, -inf too, is
+    // NaN; a large V scale over a low one's 2^x infinite); a NaN row stays NaN
+    const float inv = l == 0.f ? 0.f : v_scale / denom;
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
       float o[32];
@@ -748,7 +750,7 @@ __device__ bool tree_softmax(const PodTreeParams& P, uint8_t* smem, uint32_t tme
       const size_t gr = (size_t)(seg[TS_QROW0] + tk) * H + hd;
       float denom = wsum;
       if (P.sinks && prow < 0) denom += ex2(P.sinks[hd] * kLog2e - Ms);
-      const float inv = denom == 0.f ? 0.f : v_scale / denom;
+      const float inv = wsum == 0.f ? 0.f : v_scale / denom;
 #pragma unroll
       for (int c = 0; c < C; ++c) w[k][c] *= inv;
       at[k] = prow < 0 ? gr : (size_t)(prow + r);

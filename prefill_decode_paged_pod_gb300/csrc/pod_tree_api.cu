@@ -65,7 +65,7 @@ POD_DEV void merge_few(const PodTreeParams& P, const int32_t* g, int chunk) {
   const size_t out_row = (size_t)(g[TG_QROW0] + packed / P.G) * P.H + head;
   float denom = wsum;
   if (P.sinks) denom += ex2(P.sinks[head] * 1.4426950408889634f - Ms);
-  const float inv = denom == 0.f ? 0.f : 1.f / denom;
+  const float inv = wsum == 0.f ? 0.f : 1.f / denom;   // (no keys: 0, whatever the sink)
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -125,7 +125,7 @@ POD_DEV void merge_many(const PodTreeParams& P, const int32_t* g, int chunk) {
   const size_t out_row = (size_t)(g[TG_QROW0] + packed / P.G) * P.H + head;
   float denom = wsum;
   if (P.sinks) denom += ex2(P.sinks[head] * 1.4426950408889634f - Ms);
-  const float inv = denom == 0.f ? 0.f : 1.f / denom;
+  const float inv = wsum == 0.f ? 0.f : 1.f / denom;   // (no keys: 0, whatever the sink)
   T* out = static_cast<T*>(P.out) + out_row * D + lane * PER;
 #pragma unroll
   for (int i = 0; i < PER; i += 2) {
