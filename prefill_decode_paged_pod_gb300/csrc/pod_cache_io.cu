@@ -7,6 +7,7 @@
 // Mathematics. A head row x of d elements becomes
 //   y = x * (mean(x^2) + eps)^(-1/2) * w, then the pairs (j, j + R/2) or
 //   (2j, 2j + 1), j < R/2, turn by the angle pos / rope_scale * theta^(-2j/R).
+// Rows and weights may have any magnitude of their type (see io_pass).
 // The angle is kept in turns as a 64-bit fixed-point fraction: the per-turn
 // frequency F = theta^(-2j/R) / (2 pi rope_scale) * 2^64 is an integer, and
 // pos * F modulo 2^64 is the exact fraction of a turn for that F (whole turns
@@ -207,10 +208,13 @@ struct IoTables {
 };
 
 // The block's tokens: where their rows go, and cos and sin of their positions.
+// Returns whether this thread's norm weight is out of the ordinary: neither 0 nor
+// within 2^+-30.
 template <typename T, int D, bool CACHE, bool TURN, int FD>
-POD_DEV void io_tables(const IoParams& P, const IoFreq<FD>& F, IoTables<TURN ? D : 16>& S, long long* base, int tok0,
+POD_DEV bool io_tables(const IoParams& P, const IoFreq<FD>& F, IoTables<TURN ? D : 16>& S, long long* base, int tok0,
                        int ntok, const T* weight, bool report) {
   const int tid = threadIdx.x;
+  bool far_weight = false;
   if (CACHE && tid < ntok) {
     const long long s = P.slots[tok0 + tid];
     long long b = -1;
@@ -247,9 +251,43 @@ POD_DEV void io_tables(const IoParams& P, const IoFreq<FD>& F, IoTables<TURN ? D
         l = second ? c - turning : c;
       }
       const int k = second * 8 + (e & 7);
-      reinterpret_cast<float*>(&S.w[k >> 2][l])[k & 3] = (float)weight[e];
+      const float w = (float)weight[e];
+      reinterpret_cast<float*>(&S.w[k >> 2][l])[k & 3] = w;
+      far_weight = w != 0.f && !(fabsf(w) >= 0x1p-30f && fabsf(w) <= 0x1p30f);
     }
   }
+  return far_weight;
+}
+
+// Sum of the squares of a head row, of which each of LPR lanes holds 16 elements.
+template <int LPR>
+POD_DEV float squares(const uint64_t* x) {
+  uint64_t q2 = mul2(x[0], x[0]), q3 = mul2(x[1], x[1]);
+#pragma unroll
+  for (int i = 2; i < 8; i += 2) {
+    q2 = fma2(x[i], x[i], q2);
+    q3 = fma2(x[i + 1], x[i + 1], q3);
+  }
+  float a, b;
+  unpack2(add2(q2, q3), a, b);
+  float ss = a + b;
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, LPR);
+  return ss;
+}
+// Largest magnitude of a head row; NaN does not count.
+template <int LPR>
+POD_DEV float largest(const uint64_t* x) {
+  float am = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float a, b;
+    unpack2(x[i], a, b);
+    am = fmaxf(am, fmaxf(fabsf(a), fabsf(b)));
+  }
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o, LPR));
+  return am;
 }
 
 // One block's tasks: some heads of one kind (IO_KV: K heads, then V heads) for
@@ -276,6 +314,7 @@ POD_DEV void io_pass(const IoParams& P, const IoFreq<FUSED ? D : 2>& F, const Io
   const SlotMap sm = slot_steps(P.ps, P.Hk, D, P.hnd);
   const T* weight = static_cast<const T*>(KIND == IO_Q ? P.qw : P.kw);
   const int dt = NG / nh, dh = NG - dt * nh;
+  bool far_weights = false;                                // (of the block)
   int idx = threadIdx.x / LPR, t = idx / nh, h = idx - t * nh;
   for (int first = 0; first < n; first += NG * kTasks) {
     uint4 ra[kTasks], rb[kTasks];
@@ -305,8 +344,9 @@ POD_DEV void io_pass(const IoParams& P, const IoFreq<FUSED ? D : 2>& F, const Io
       if (h >= nh) { h -= nh; ++t; }
     }
     if (first == 0) {
-      io_tables<T, D, TO_CACHE, TURN>(P, F, S, base, tok0, ntok, weight, h0 == 0 && KIND != IO_V);
-      __syncthreads();
+      const bool far = io_tables<T, D, TO_CACHE, TURN>(P, F, S, base, tok0, ntok, weight, h0 == 0 && KIND != IO_V);
+      if constexpr (TURN && Pack<T>::kBF16) far_weights = __syncthreads_or(far);
+      else __syncthreads();
     }
 #pragma unroll
     for (int u = 0; u < kTasks; ++u) {
@@ -320,18 +360,23 @@ POD_DEV void io_pass(const IoParams& P, const IoFreq<FUSED ? D : 2>& F, const Io
       }
       if constexpr (TURN) {
         if (weight) {
-          uint64_t q2 = mul2(x[0], x[0]), q3 = mul2(x[1], x[1]);
+          float mean = squares<LPR>(x) * (1.f / D) + P.eps;
+          // Squares, or products with the weights, that may leave fp32's range: the row
+          // by a power of two that brings its largest element, or the root of eps where
+          // that is more, near 1, which the norm undoes. (Zeros under an eps, the usual
+          // padding, are not of these, and no fp16 row is.)
+          const bool far = far_weights || !(mean >= 0x1p-64f && mean <= 0x1p64f);
+          if (Pack<T>::kBF16 && __any_sync(0xffffffffu, far)) {
+            const int ex = (int)(__float_as_uint(largest<LPR>(x)) >> 23) - 127;
+            const int half_eps = P.eps == 0.f ? -127 : ((int)(__float_as_uint(P.eps) >> 23) - 127) >> 1;
+            const int e = far ? min(max(max(ex, half_eps), -126), 126) : 0;
+            const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+            const uint64_t f2 = pack2(f, f);
 #pragma unroll
-          for (int i = 2; i < 8; i += 2) {
-            q2 = fma2(x[i], x[i], q2);
-            q3 = fma2(x[i + 1], x[i + 1], q3);
+            for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], f2);
+            mean = squares<LPR>(x) * (1.f / D) + P.eps * f * f;
           }
-          float a, b;
-          unpack2(add2(q2, q3), a, b);
-          float ss = a + b;
-#pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, LPR);
-          const float rs = __frsqrt_rn(ss * (1.f / D) + P.eps);
+          const float rs = __frsqrt_rn(mean);
           const uint64_t rs2 = pack2(rs, rs);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -370,16 +415,7 @@ POD_DEV void io_pass(const IoParams& P, const IoFreq<FUSED ? D : 2>& F, const Io
       }
       int ebyte = 0;
       if constexpr (TO_CACHE && FMT == FMT_BLOCK) {
-        float am = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float a, b;
-          unpack2(x[i], a, b);
-          am = fmaxf(am, fmaxf(fabsf(a), fabsf(b)));
-        }
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o, LPR));
-        ebyte = block_exp(am);
+        ebyte = block_exp(largest<LPR>(x));
       }
       if (!live) continue;
       const long long r = tok0 + tk[u];

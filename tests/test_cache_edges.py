@@ -44,3 +44,70 @@ def test_slots_of_an_empty_table_and_past_32_bits(tensors):
     pos = np.array([5], np.int32)               # (32-bit positions, a slot of 36 bits)
     s = pod.pod_kv_slots(conv(np.array([0, 1], np.int32)), conv(big), 16, conv(np.array([0], np.int32)), conv(pos))
     assert s.tolist() == [(2 ** 31 - 1) * 16 + 5]
+
+
+# ------------------------------------------------------------------ norm of any magnitude
+BF = torch.bfloat16
+
+
+def magnitudes(rows, heads, d, seed):
+    """bf16 rows from the smallest numbers to the largest, and ordinary ones between."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((rows, heads, d), generator=g, dtype=torch.float64).clamp(-4, 4)
+    e = torch.tensor([-130, -126, -110, -80, -65, -63, -33, -31, 0, 3, 31, 40, 63, 66, 100, 125])
+    at = torch.randint(0, len(e), (rows, heads, 1), generator=g)
+    at.view(-1)[:len(e)] = torch.arange(len(e))
+    return (x * torch.exp2(e[at].double())).to(BF)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 1e-30, 1e-41, 1e3])
+@pytest.mark.parametrize("w_exp", [0, 90, -90, 124])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_norm_of_rows_of_any_magnitude(eps, w_exp, d):
+    """Squares, and products with the weights, that leave fp32's range on the way
+    to values that do not. fp32's own subnormal results carry their step."""
+    from test_cache_io import ATOL, norm_rope_64
+    rows, H, Hk, R = 37, 3, 2, 32
+    x = magnitudes(rows, H + Hk, d, d)
+    g = torch.Generator().manual_seed(1)
+    w = (torch.exp2(torch.full((d,), w_exp).double()) * (1 + 0.3 * torch.randn(d, generator=g).double())).to(BF)
+    w[3] = 0
+    pos = np.arange(rows, dtype=np.int32)
+    q, k = pod.pod_qk_norm_rope(x[:, :H].cuda(), x[:, H:].cuda(), torch.from_numpy(pos).cuda(), q_weight=w.cuda(),
+                                k_weight=w.cuda(), eps=eps, rotary_dim=R)
+    eps32 = float(np.float32(eps))
+    for got, part in ((q, x[:, :H]), (k, x[:, H:])):
+        want = norm_rope_64(part, w, pos, R, False, eps=eps32)
+        got = got.double().cpu().numpy()
+        over = np.abs(want) > torch.finfo(BF).max * (1 - 2.0 ** -9)
+        tol = np.abs(want) * 2.0 ** -8 * (1 + 2.0 ** -7) + ATOL * np.abs(want).max(-1, keepdims=True) + 2.0 ** -126
+        bad = ~over & ~(np.abs(got - want) <= tol)
+        assert not bad.any(), (np.argwhere(bad)[0], got[bad][0], want[bad][0])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["16bit", "block"])
+def test_fused_write_of_rows_of_any_magnitude(fmt):
+    """The same through the write: K rows of 2^-80 to 2^100 come out near the weights,
+    and rows without a value, infinities and NaN stay what they were."""
+    from test_cache_io import norm_rope_64
+    rows, hk, d = 40, 2, 128
+    x = magnitudes(rows, hk, d, 7)
+    x[20], x[21, 0, 5], x[22, 1, 9] = 0, torch.inf, torch.nan
+    w = torch.ones(d, dtype=BF)
+    kv = torch.zeros((rows, 2, 1, hk, d), dtype=BF if fmt == "16bit" else torch.float8_e4m3fn, device="cuda")
+    sc = None if fmt == "16bit" else torch.zeros((rows, 2, 1, hk), dtype=torch.uint8, device="cuda")
+    slots = torch.arange(rows).cuda()
+    pod.pod_norm_rope_append(None, x.cuda(), x.cuda(), None, kv, slots, k_weight=w.cuda(), eps=1e-30, rotary_dim=0,
+                             kv_scales=sc)
+    got = pod.pod_gather_kv(kv, slots, dtype=BF, kv_scales=sc)[:, 0].double().cpu().numpy()
+    want = norm_rope_64(x, w, None, 0, False, eps=1e-30)
+    plain = np.ones(rows, dtype=bool)
+    plain[20:23] = False
+    step = 2.0 ** -8 if fmt == "16bit" else 2.0 ** -4 + 2.0 ** -8
+    tol = np.abs(want) * step * (1 + 2.0 ** -7) + (2.0 ** -16 if fmt == "16bit" else 2.0 ** -9) * np.abs(want).max(-1, keepdims=True)
+    assert (np.abs(got - want)[plain] <= tol[plain]).all()
+    assert (got[20] == 0).all()
+    assert (np.delete(got[21, 0], 5) == 0).all() and np.isnan(got[21, 0, 5])
+    assert np.isnan(got[22, 1]).all() and np.isfinite(got[22, 0]).all()
