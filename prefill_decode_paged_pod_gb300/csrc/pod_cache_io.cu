@@ -11,9 +11,10 @@
 // The angle is kept in turns as a 64-bit fixed-point fraction: the per-turn
 // frequency F = theta^(-2j/R) / (2 pi rope_scale) * 2^64 is an integer, and
 // pos * F modulo 2^64 is the exact fraction of a turn for that F (whole turns
-// drop out by themselves, for negative positions too). Its error is pos * 2^-56
-// of a turn, so far positions cost no 64-bit floating point, of which this GPU
-// has little. Everything else runs in fp32 and is rounded once, at the store.
+// drop out by themselves, for negative positions too). F is off by a unit, so the
+// angle by pos * 2^-64 of a turn: far positions cost no 64-bit floating point, of
+// which this GPU has little. Everything else runs in fp32 and is rounded once, at
+// the store.
 //
 // A power-of-two block scale 2^e is the smallest with amax <= 448 * 2^e. E4M3
 // is a floating-point format, so a power of two costs no significant bit
@@ -45,6 +46,7 @@
 
 #include "../../include/pod.h"
 #include "pod_device.cuh"
+#include "pod_turns.h"
 
 void pod_set_last_error(const std::string& msg);
 
@@ -594,28 +596,24 @@ long long tasks_of(const IoParams& P, long long heads, int round, int most) {
 // Frequencies in turns as 64-bit fractions. They depend on the rotation's
 // settings only; the last settings' table is kept per host thread (computing
 // it takes longer than a short launch).
-const IoFreq<256>& freq_of(int R, float scale, float theta) {
+const Turns& freq_of(int R, float scale, float theta) {
   struct Kept {
     int R = -1;
     float scale = 0.f, theta = 0.f;
-    IoFreq<256> f;
+    Turns turns;
   };
   static thread_local Kept kept;
   if (kept.R != R || kept.scale != scale || kept.theta != theta) {
-    memset(&kept.f, 0, sizeof(kept.f));
-    for (int j = 0; j < R / 2; ++j) {
-      const double turns = pow((double)theta, -2.0 * j / R) / (2.0 * 3.14159265358979323846 * scale);
-      kept.f.f[j] = (uint64_t)ldexp(turns - floor(turns), 64);
-    }
+    make_turns(R, scale, theta, &kept.turns);
     kept.R = R;
     kept.scale = scale;
     kept.theta = theta;
   }
-  return kept.f;
+  return kept.turns;
 }
 
 template <typename T, int D, int FMT>
-cudaError_t launch_io(IoParams& P, bool fused, const IoFreq<256>& f, cudaStream_t st) {
+cudaError_t launch_io(IoParams& P, bool fused, const Turns& f, cudaStream_t st) {
   constexpr int round = kIoThreads / (D / 16) * kTasks;
   constexpr bool cache = FMT != FMT_NONE;
   const long long tasks = tasks_of(P, P.H + P.Hk + (cache ? P.Hk : 0), round, fused ? 4 : 2);
@@ -632,7 +630,7 @@ cudaError_t launch_io(IoParams& P, bool fused, const IoFreq<256>& f, cudaStream_
   const unsigned grid = (unsigned)blocks;
   if (fused) {
     IoFreq<D> fd;
-    memcpy(&fd, &f, sizeof(fd));
+    memcpy(&fd, f.f, sizeof(fd));
     return launch_beside(cache_io_kernel<T, D, FMT, true>, grid, st, P, fd);
   } else if constexpr (cache) {
     return launch_beside(cache_io_kernel<T, D, FMT, false>, grid, st, P, IoFreq<2>{});
@@ -640,7 +638,7 @@ cudaError_t launch_io(IoParams& P, bool fused, const IoFreq<256>& f, cudaStream_
   return cudaErrorInvalidValue;                  // (a write without a cache is not asked for)
 }
 template <typename T, int D>
-cudaError_t launch_fmt(IoParams& P, int fmt, bool fused, const IoFreq<256>& f, cudaStream_t st) {
+cudaError_t launch_fmt(IoParams& P, int fmt, bool fused, const Turns& f, cudaStream_t st) {
   switch (fmt) {
     case FMT_16: return launch_io<T, D, FMT_16>(P, fused, f, st);
     case FMT_SCALED: return launch_io<T, D, FMT_SCALED>(P, fused, f, st);
@@ -649,7 +647,7 @@ cudaError_t launch_fmt(IoParams& P, int fmt, bool fused, const IoFreq<256>& f, c
   }
 }
 template <typename T>
-cudaError_t launch_d(IoParams& P, int d, int fmt, bool fused, const IoFreq<256>& f, cudaStream_t st) {
+cudaError_t launch_d(IoParams& P, int d, int fmt, bool fused, const Turns& f, cudaStream_t st) {
   return d == 64 ? launch_fmt<T, 64>(P, fmt, fused, f, st)
          : d == 128 ? launch_fmt<T, 128>(P, fmt, fused, f, st)
                     : launch_fmt<T, 256>(P, fmt, fused, f, st);
@@ -757,7 +755,7 @@ IoParams params_of(const pod_io_args& a, bool fused, bool cache) {
 
 pod_status run_io(IoParams& P, const pod_io_args& a, int fmt, bool fused, void* stream, const char* what) {
   if (P.rows == 0) return POD_OK;
-  const IoFreq<256>& f = freq_of(P.R, a.rope_scale, a.rope_theta);
+  const Turns& f = freq_of(P.R, a.rope_scale, a.rope_theta);
   cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t e = a.dtype == POD_BF16 ? launch_d<__nv_bfloat16>(P, a.head_dim, fmt, fused, f, st)
                                             : launch_d<__half>(P, a.head_dim, fmt, fused, f, st);

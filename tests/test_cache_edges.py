@@ -2,6 +2,11 @@
 of positions that no page holds, rows of any magnitude, angles of far positions,
 caches past 4 GB, and kernels that start beside the one before.
 """
+import os
+import subprocess
+from decimal import Decimal, localcontext
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -111,3 +116,76 @@ def test_fused_write_of_rows_of_any_magnitude(fmt):
     assert (got[20] == 0).all()
     assert (np.delete(got[21, 0], 5) == 0).all() and np.isnan(got[21, 0, 5])
     assert np.isnan(got[22, 1]).all() and np.isfinite(got[22, 0]).all()
+
+
+# ------------------------------------------------------------------ frequencies of the rotation
+def exact_turns(R, scale, theta, j):
+    """theta^(-2j/R) / (2 pi scale) as a Decimal of 60 digits."""
+    def arctan_inv(n):
+        x = s = Decimal(1) / n
+        k = 1
+        while abs(x) > Decimal(10) ** -70:
+            x, k = -x / (n * n), k + 2
+            s += x / k
+        return s
+    with localcontext() as c:
+        c.prec = 75
+        pi = 4 * (4 * arctan_inv(5) - arctan_inv(239))
+        th, sc = Decimal(float(np.float32(theta))), Decimal(float(np.float32(scale)))
+        return (th.ln() * Decimal(-2 * j) / R).exp() / (2 * pi * sc)
+
+
+@pytest.fixture(scope="module")
+def turns_client(tmp_path_factory):
+    from prefill_decode_paged_pod_gb300 import _build
+    here = os.path.dirname(os.path.abspath(__file__))
+    exe = str(tmp_path_factory.mktemp("turns") / "turns_client")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-I", _build.CSRC, os.path.join(here, "csrc", "turns_client.cpp"),
+                    "-o", exe], check=True)
+
+    def call(mode, *settings):
+        args = [repr(x) if isinstance(x, float) else str(x) for s in settings for x in s]
+        return [int(x) for x in subprocess.run([exe, mode] + args, check=True, capture_output=True,
+                                               text=True).stdout.split()]
+    return call
+
+
+@pytest.mark.parametrize("R,scale,theta", [(128, 1.0, 1e4), (64, 1.0, 5e5), (256, 32.0, 1e6), (48, 1.0, 1e4),
+                                           (96, 0.5, 1.5), (16, 4.0, 0.5), (128, 1e-3, 1e4), (256, 1.0, 1e30),
+                                           (80, 1.0, 1.0), (112, 3.0, 7.7), (32, 1.0, 1e-6)])
+def test_frequencies_to_a_unit_of_64_bits(turns_client, R, scale, theta):
+    got = turns_client("F", (R, scale, theta))
+    assert len(got) == R // 2
+    for j, f in enumerate(got):
+        t = exact_turns(R, scale, theta, j)
+        with localcontext() as c:
+            c.prec = 75
+            assert t < 2 ** 30
+            off = (f - t * 2 ** 64) % 2 ** 64
+        assert min(off, 2 ** 64 - off) <= 1, (j, off)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale,theta", [(1.0, 1e4), (1.0, 1e6), (0.25, 500.0)])
+def test_cos_and_sin_of_far_positions(scale, theta):
+    """As near to the true ones at +-2^31 as at 0: pairs (1, 0) turn into (cos, sin),
+    rounded to fp16 once, within 2^-23.4 before that (a turn's fraction to 2^-34, fp32
+    afterwards)."""
+    d, rows = 64, 2000
+    r = np.random.RandomState(4)
+    pos = np.concatenate([2 ** 31 - 1 - np.arange(rows), -(2 ** 31) + np.arange(rows),
+                          r.randint(-(2 ** 31), 2 ** 31, rows)]).astype(np.int32)
+    k = torch.zeros((len(pos), 1, d), dtype=torch.float16)
+    k[:, :, :d // 2] = 1
+    out = pod.pod_qk_norm_rope(None, k.cuda(), torch.from_numpy(pos).cuda(), rope_scale=scale, rope_theta=theta)[1]
+    out = out[:, 0].double().cpu().numpy()
+    for j in range(d // 2):
+        with localcontext() as c:
+            c.prec = 75
+            f = int(exact_turns(d, scale, theta, j) * 2 ** 120)
+        turn = np.array([float(Fraction(int(p) * f % 2 ** 120, 2 ** 120)) for p in pos])
+        turn = 2 * np.pi * (turn - np.round(turn))
+        for got, want in ((out[:, j], np.cos(turn)), (out[:, j + d // 2], np.sin(turn))):
+            step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(want), 2.0 ** -14))) - 10)
+            off = np.abs(got - want) - step / 2
+            assert (off <= 2.0 ** -23.4).all(), (j, off.max())
