@@ -593,25 +593,6 @@ long long tasks_of(const IoParams& P, long long heads, int round, int most) {
   return t < round ? round : t > most * round ? most * round : t;
 }
 
-// Frequencies in turns as 64-bit fractions. They depend on the rotation's
-// settings only; the last settings' table is kept per host thread (computing
-// it takes longer than a short launch).
-const Turns& freq_of(int R, float scale, float theta) {
-  struct Kept {
-    int R = -1;
-    float scale = 0.f, theta = 0.f;
-    Turns turns;
-  };
-  static thread_local Kept kept;
-  if (kept.R != R || kept.scale != scale || kept.theta != theta) {
-    make_turns(R, scale, theta, &kept.turns);
-    kept.R = R;
-    kept.scale = scale;
-    kept.theta = theta;
-  }
-  return kept.turns;
-}
-
 template <typename T, int D, int FMT>
 cudaError_t launch_io(IoParams& P, bool fused, const Turns& f, cudaStream_t st) {
   constexpr int round = kIoThreads / (D / 16) * kTasks;
@@ -755,7 +736,9 @@ IoParams params_of(const pod_io_args& a, bool fused, bool cache) {
 
 pod_status run_io(IoParams& P, const pod_io_args& a, int fmt, bool fused, void* stream, const char* what) {
   if (P.rows == 0) return POD_OK;
-  const Turns& f = freq_of(P.R, a.rope_scale, a.rope_theta);
+  // (the frequencies depend on the rotation's settings only; a write has R = 0)
+  static thread_local KeptTurns kept;
+  const Turns& f = kept.of(P.R, a.rope_scale, a.rope_theta);
   cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t e = a.dtype == POD_BF16 ? launch_d<__nv_bfloat16>(P, a.head_dim, fmt, fused, f, st)
                                             : launch_d<__half>(P, a.head_dim, fmt, fused, f, st);

@@ -58,4 +58,33 @@ inline void make_turns(int R, float scale, float theta, Turns* out) {
   for (int j = 0; j < R / 2; ++j, turn = mul(turn, y)) out->f[j] = fraction(turn);
 }
 
+// The tables of the last few settings: making one takes longer than a short launch
+// does. R = 0 needs none and displaces none.
+class KeptTurns {
+ public:
+  const Turns& of(int R, float scale, float theta) {
+    static const Turns none = {};
+    if (R == 0) return none;
+    for (const Entry& e : kept_)
+      if (e.R == R && e.scale == scale && e.theta == theta) return e.turns;
+    Entry& e = kept_[made_++ % kEntries];
+    make_turns(R, scale, theta, &e.turns);
+    e.R = R;
+    e.scale = scale;
+    e.theta = theta;
+    return e.turns;
+  }
+  unsigned made() const { return made_; }
+
+ private:
+  static constexpr unsigned kEntries = 4;
+  struct Entry {
+    int R = 0;
+    float scale = 0.f, theta = 0.f;
+    Turns turns;
+  };
+  Entry kept_[kEntries];
+  unsigned made_ = 0;
+};
+
 }  // namespace pod

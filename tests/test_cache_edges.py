@@ -165,6 +165,18 @@ def test_frequencies_to_a_unit_of_64_bits(turns_client, R, scale, theta):
         assert min(off, 2 ** 64 - off) <= 1, (j, off)
 
 
+def test_kept_tables(turns_client):
+    """A layer's calls, a write among them (R = 0), and a model's few settings make
+    each table once; the fifth setting takes the place of the first."""
+    a, b, c, d, e = (128, 1.0, 1e4), (128, 1.0, 1e6), (64, 1.0, 1e4), (128, 2.0, 1e4), (32, 1.0, 1e4)
+    write = (0, 1.0, 1.0)
+    assert turns_client("N", *[a, write] * 5) == [1]
+    assert turns_client("N", *[a, b, write, c, d] * 3) == [4]
+    assert turns_client("N", a, b, c, d, e, b, c, d, e, a) == [6]
+    assert turns_client("N", write, write) == [0]
+    assert turns_client("F", a, b, write)[64:] == turns_client("F", b)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("scale,theta", [(1.0, 1e4), (1.0, 1e6), (0.25, 500.0)])
 def test_cos_and_sin_of_far_positions(scale, theta):
