@@ -201,3 +201,72 @@ def test_cos_and_sin_of_far_positions(scale, theta):
             step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(want), 2.0 ** -14))) - 10)
             off = np.abs(got - want) - step / 2
             assert (off <= 2.0 ** -23.4).all(), (j, off.max())
+
+
+# ------------------------------------------------------------------ caches past 4 GB
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,layout", [("block", "NHD"), ("block", "HND"), ("16bit", "NHD"), ("scaled", "HND")])
+def test_byte_offsets_past_32_bits(fmt, layout):
+    """Rows behind the first 2^32 bytes, and at its end, lie where they should: a
+    short pool's bytes, and nothing else in the long one."""
+    from test_cache_io import rows_of
+    ps, hk, d = 16, 8, 128
+    page = 2 * ps * hk * d * (2 if fmt == "16bit" else 1)
+    pages = 2 ** 32 // page + 4001
+    inner = (ps, hk) if layout == "NHD" else (hk, ps)
+    kind = BF if fmt == "16bit" else torch.float8_e4m3fn
+    edge = 2 ** 32 // page                       # the page that begins at 2^32 bytes
+    at = torch.tensor([pages - 1, 0, edge, edge - 1, edge + 1, edge + 3000])
+    kw = dict(kv_layout=layout, **(dict(k_scale=0.02, v_scale=0.03) if fmt == "scaled" else {}))
+    k, v = rows_of((len(at), hk, d), BF, 1).cuda(), rows_of((len(at), hk, d), BF, 2).cuda()
+    pools = []
+    for n, where in ((pages, at), (len(at), torch.arange(len(at)))):
+        kv = torch.zeros((n, 2) + inner + (d,), dtype=kind, device="cuda")
+        sc = torch.zeros((n, 2) + inner, dtype=torch.uint8, device="cuda") if fmt == "block" else None
+        slots = (where * ps + torch.arange(len(at)) % ps).cuda()
+        pod.pod_append_kv(k, v, kv, slots, kv_scales=sc, **kw)
+        pools.append((kv.view(torch.uint8), sc, pod.pod_gather_kv(kv, slots, dtype=BF, kv_scales=sc, **kw)))
+    (long, long_s, long_r), (short, short_s, short_r) = pools
+    assert torch.equal(long_r, short_r) and torch.equal(long[at.cuda()], short)
+    assert sum(int(torch.count_nonzero(x)) for x in long.split(4096)) == int(torch.count_nonzero(short))
+    if fmt == "block":
+        assert torch.equal(long_s[at.cuda()], short_s) and int(torch.count_nonzero(long_s)) == int(torch.count_nonzero(short_s))
+
+
+# ------------------------------------------------------------------ behind pod_run
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[9000, 400, 7000], [700] * 300], ids=["merged", "many"])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_write_right_behind_pod_run(lens, fp8):
+    """The write may start while pod_run's kernel still reads the cache that it
+    writes into: it may not touch it before. Nothing waits between the two."""
+    H, hk, d, ps = 16, 2, 128, 16
+    npg = [(n + ps - 1) // ps for n in lens]
+    indptr = np.concatenate([[0], np.cumsum(npg)]).astype(np.int32)
+    pages = int(indptr[-1])
+    last = np.array([(n - 1) % ps + 1 for n in lens], dtype=np.int32)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    old = torch.randn((pages, 2, ps, hk, d), generator=g, device="cuda")
+    old = (old * 20).to(torch.float8_e4m3fn) if fp8 else old.to(BF)
+    q = torch.randn((len(lens), H, d), generator=g, device="cuda").to(BF)
+    h = pod.pod_plan(None, None, None, None, np.arange(len(lens) + 1, dtype=np.int32), indptr,
+                     np.arange(pages, dtype=np.int32), last, H, hk, d, ps, True, -1, None, dtype=BF, p_num_pages=0,
+                     d_num_pages=pages)
+    kw = dict(k_scale=0.05, v_scale=0.05) if fp8 else {}
+    if fp8:
+        pod.pod_plan_set_decode_fp8(h, 0.05, 0.05)
+    ws = torch.empty(pod.pod_workspace_size(h), dtype=torch.uint8, device="cuda")
+    pod.pod_bind_workspace(h, ws)
+    slots = torch.arange(pages * ps, device="cuda")
+    new = torch.full((pages * ps, hk, d), 3.0, dtype=BF, device="cuda")
+    kv = old.clone()
+    want = pod.pod_run(h, None, None, q, kv, ws)[2:]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        kv = old.clone()
+        torch.cuda.synchronize()
+        got = pod.pod_run(h, None, None, q, kv, ws)[2:]
+        pod.pod_append_kv(new, new, kv, slots, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert (kv.float() * (0.05 if fp8 else 1) - 3).abs().max() < 0.2

@@ -62,3 +62,101 @@ def test_split_rows_without_keys_are_zero_whatever_their_sink(L, pieces):
     empty = c.bits[0].sum(1) == 0
     assert (out.cpu()[empty] == 0).all() and (lse.cpu()[empty] == -torch.inf).all()
     c.check(out, lse)
+
+
+# ------------------------------------------------------------------ caches past 4 GB
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,ps,layout", [("16bit", 16, "NHD"), ("16bit", 3, "HND"), ("block", 16, "HND"),
+                                           ("block", 3, "NHD"), ("scaled", 16, "NHD"), ("scaled", 1, "NHD")])
+def test_pages_behind_the_first_4_gb(fmt, ps, layout):
+    """The few used pages at the end of a pool of more than 2^32 bytes, loaded by TMA
+    and gathered: the result of a short pool."""
+    c = tree_case(n=[7, 30], kv_len=[300, 64], H=16, Hk=8, d=128, ps=ps, fmt=fmt, layout=layout, seed=3)
+    want = c.run()
+    c.check(*want)
+    page = 2 * ps * c.Hk * c.d * (2 if fmt == "16bit" else 1)
+    first = 2 ** 32 // page + 1000
+    q, kv, more = c.args()
+    big = torch.zeros((first + c.pages,) + tuple(kv.shape[1:]), dtype=kv.dtype, device="cuda")
+    big[first:] = kv
+    if more["kv_scales"] is not None:
+        s = torch.zeros((first + c.pages,) + tuple(c.scales.shape[1:]), dtype=torch.uint8, device="cuda")
+        s[first:] = more["kv_scales"]
+        more["kv_scales"] = s
+    c.kv_indices = c.kv_indices + np.int32(first)
+    c.pages += first
+    h = c.plan()
+    ws = torch.empty(pod.pod_tree_workspace_size(h), dtype=torch.uint8, device="cuda")
+    pod.pod_tree_bind_workspace(h, ws)
+    out, lse = pod.pod_tree_run(h, q, big, ws, **more)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+# ------------------------------------------------------------------ one behind the other
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["16bit", "scaled", "block"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("long", [1200, 500], ids=["merged", "whole"])
+def test_nothing_but_these_kernels_in_the_stream(fmt, d, long):
+    """Layers whose stream holds no other kernel: a write of the last output's rows,
+    read where they lie, and the attention over it, into kept buffers. The merge of one
+    layer lies right before the write and the attention of the next, which rewrite the
+    cache and the partial rows; results are those of waiting for each call."""
+    c = tree_case(n=[9, 30, 4], kv_len=[long, 400, 40], H=8, Hk=2, d=d, ps=16, fmt=fmt, seed=2)
+    h = c.plan(num_sms=152)
+    assert (len(pod.pod_tree_plan_table(h, 2)) > 0) == (long == 1200)
+    ws = torch.empty(pod.pod_tree_workspace_size(h), dtype=torch.uint8, device="cuda")
+    pod.pod_tree_bind_workspace(h, ws)
+    req = np.repeat(np.arange(3), c.n)
+    at = np.concatenate([np.arange(a - b, a) for a, b in zip(c.kv_len, c.n)])
+    slots = torch.from_numpy(pod.pod_kv_slots(c.kv_indptr, c.kv_indices, c.ps, req, at)).cuda()
+
+    def layers(wait, n=12):
+        q, kv, more = c.args()
+        outs = [q] + [torch.empty_like(q) for _ in range(n)]
+        lses = [torch.empty(q.shape[:2], dtype=torch.float32, device="cuda") for _ in range(n)]
+        torch.cuda.synchronize()
+        for i in range(n):
+            new = outs[i][:, 2 * (i % 3):2 * (i % 3) + 2]
+            pod.pod_append_kv(new, new, kv, slots, kv_scales=more["kv_scales"], k_scale=c.ks, v_scale=c.vs)
+            if wait:
+                torch.cuda.synchronize()
+            pod.pod_tree_run(h, outs[i], kv, ws, out=outs[i + 1], lse=lses[i], **more)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return outs[1:], lses
+    want, got = layers(True), layers(False)
+    for w, x in zip(want, got):
+        assert all(torch.equal(a, b) for a, b in zip(w, x))
+    assert got[0][-1].isfinite().all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["16bit", "scaled", "block"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("long", [1200, 500], ids=["merged", "whole"])
+def test_runs_on_one_workspace_right_behind_each_other(fmt, d, long):
+    """Runs of one plan with different queries, nothing between them: an attention
+    right behind the merge before, which reads the partial rows that it rewrites, or
+    right behind another attention."""
+    c = tree_case(n=[9, 30, 4], kv_len=[long, 400, 40], H=8, Hk=2, d=d, ps=16, fmt=fmt, seed=2)
+    h = c.plan(num_sms=152)
+    assert (len(pod.pod_tree_plan_table(h, 2)) > 0) == (long == 1200)
+    ws = torch.empty(pod.pod_tree_workspace_size(h), dtype=torch.uint8, device="cuda")
+    pod.pod_tree_bind_workspace(h, ws)
+    q, kv, more = c.args()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    qs = [torch.randn(q.shape, generator=g, device="cuda").to(c.dtype) for _ in range(16)]
+    want = []
+    for x in qs:
+        want.append(pod.pod_tree_run(h, x, kv, ws, **more))
+        torch.cuda.synchronize()
+    got = [(torch.empty_like(a), torch.empty_like(b)) for a, b in want]
+    torch.cuda.synchronize()
+    for x, (o, l) in zip(qs, got):
+        pod.pod_tree_run(h, x, kv, ws, out=o, lse=l, **more)
+    torch.cuda.synchronize()
+    for (a, b), (o, l) in zip(want, got):
+        assert torch.equal(a, o) and torch.equal(b, l)
+    assert pod.pod_tree_read_device_status(h, ws) == 0
