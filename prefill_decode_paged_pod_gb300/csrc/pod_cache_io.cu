@@ -133,10 +133,9 @@ POD_DEV int block_exp(float amax) {
   const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
   return max(e, -127) + 127;
 }
-// 2^(127 - byte): the factor that takes a value to its code's range
-POD_DEV float inv_scale_of(int byte) {
-  return byte == 254 ? 5.877471754111438e-39f : __uint_as_float((uint32_t)(254 - byte) << 23);
-}
+// 2^(127 - byte): the factor that takes a value to its code's range (block_exp ends at
+// 247, an infinite amax)
+POD_DEV float inv_scale_of(int byte) { return __uint_as_float((uint32_t)(254 - byte) << 23); }
 // 2^(byte - 127) (2^-127 is subnormal)
 POD_DEV float scale_of(int byte) {
   return byte == 0 ? 5.877471754111438e-39f : __uint_as_float((uint32_t)byte << 23);

@@ -59,4 +59,3 @@ cudaError_t pod_tree_k16(const PodTreeParams& P, int dtype, int d, cudaStream_t 
 cudaError_t pod_tree_k8(const PodTreeParams& P, int dtype, int d, cudaStream_t stream);
 cudaError_t pod_tree_k8b(const PodTreeParams& P, int dtype, int d, cudaStream_t stream);
 cudaError_t pod_tree_merge(const PodTreeParams& P, int dtype, int d, cudaStream_t stream);
-int pod_tree_ctas_per_sm(int d);

@@ -270,3 +270,25 @@ def test_a_write_right_behind_pod_run(lens, fp8):
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert (kv.float() * (0.05 if fp8 else 1) - 3).abs().max() < 0.2
+
+
+@pytest.mark.gpu
+def test_slots_of_device_tables():
+    """The host's slots, nothing read outside the table (an index out of range would end
+    the process), also in a graph."""
+    req = np.array([0, 0, 0, 1, 2, 2, 2, -1, 3, 2, 0])
+    pos = np.array([-1, 7, 8, 0, -4, 11, 12, 0, 0, 1 << 40, 0])
+    want = pod.pod_kv_slots(INDPTR, INDICES, 4, req, pos).tolist()
+    args = [torch.from_numpy(x).cuda() for x in (INDPTR, INDICES, req, pos)]
+    call = lambda: pod.pod_kv_slots(args[0], args[1], 4, args[2], args[3])   # noqa: E731
+    assert call().tolist() == want
+    none = torch.zeros(0, dtype=torch.int32).cuda()
+    assert pod.pod_kv_slots(torch.zeros(3, dtype=torch.int32).cuda(), none, 4, args[2], args[3]).tolist() == [-1] * 11
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        out = call()
+    args[3] -= 4
+    g.replay()
+    torch.cuda.synchronize()
+    assert out.tolist() == pod.pod_kv_slots(INDPTR, INDICES, 4, req, pos - 4).tolist()
