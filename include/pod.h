@@ -520,7 +520,10 @@ pod_status pod_tree_plan(const int32_t* q_indptr, const int32_t* kv_indptr, cons
 /* Bytes of device workspace the plan needs (0 for a NULL handle). */
 size_t pod_tree_workspace_size(pod_tree_handle h);
 
-/* Copy the plan into `workspace` (device, 256-byte aligned) and wait for it. */
+/* Copy the plan into `workspace` (device, 256-byte aligned) and wait for it. The
+ * workspace then holds this plan only: a run of one that was bound to it before is
+ * refused until that one is bound again (a replay of a captured run is not, and must
+ * not happen). */
 pod_status pod_tree_bind_workspace(pod_tree_handle h, void* workspace, size_t workspace_bytes, void* stream);
 
 /*

@@ -20,6 +20,7 @@
 #include "pod_launch.h"
 #include "pod_planner.hpp"
 #include "pod_rope.h"
+#include "pod_tree.h"
 
 struct pod_plan_s {
   PodPlanHost plan;
@@ -74,6 +75,7 @@ pod_status upload(pod_plan_s* h, void* ws, size_t bytes, void* stream) {
                                           std::to_string(P.total_bytes));
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
     return set_err(POD_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  pod_tree_workspace_lost(ws);
   cudaError_t e = cudaMemcpyAsync(ws, P.int_image.data(), P.int_image.size(),
                                   cudaMemcpyHostToDevice, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_err(e, "cudaMemcpyAsync(plan metadata)");

@@ -58,4 +58,6 @@ struct PodTreeParams {
 cudaError_t pod_tree_k16(const PodTreeParams& P, int dtype, int d, cudaStream_t stream);
 cudaError_t pod_tree_k8(const PodTreeParams& P, int dtype, int d, cudaStream_t stream);
 cudaError_t pod_tree_k8b(const PodTreeParams& P, int dtype, int d, cudaStream_t stream);
+// A workspace holds another plan from now on: tree plans bound to it have lost it.
+void pod_tree_workspace_lost(void* workspace);
 cudaError_t pod_tree_merge(const PodTreeParams& P, int dtype, int d, cudaStream_t stream);

@@ -6,8 +6,10 @@
 #include <string.h>
 
 #include <exception>
+#include <mutex>
 #include <new>
 #include <string>
+#include <unordered_map>
 
 #include "../../include/pod.h"
 #include "pod_device.cuh"
@@ -177,6 +179,24 @@ pod_status cuda_fail(cudaError_t e, const char* what) {
   return fail(POD_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
 
+// Which tree plan a workspace holds: the one bound to it last. A run of an earlier one
+// would take the other's tables for its own, so it is refused. (Never destroyed:
+// handles may outlive static objects.)
+struct Owners {
+  std::mutex mu;
+  std::unordered_map<const void*, pod_tree_handle> of;
+};
+Owners& owners() {
+  static Owners* o = new Owners;
+  return *o;
+}
+void give_up(pod_tree_handle h) {
+  std::lock_guard<std::mutex> lock(owners().mu);
+  auto it = owners().of.find(h->workspace);
+  if (it != owners().of.end() && it->second == h) owners().of.erase(it);
+  h->workspace = nullptr;
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     cudaDriverEntryPointQueryResult q;
@@ -209,6 +229,11 @@ CUresult encode(CUtensorMap* m, const void* kv, const PodTreePlanHost& P, int hn
 
 }  // namespace
 
+void pod_tree_workspace_lost(void* workspace) {
+  std::lock_guard<std::mutex> lock(owners().mu);
+  owners().of.erase(workspace);
+}
+
 cudaError_t pod_tree_merge(const PodTreeParams& P, int dtype, int d, cudaStream_t st) {
   if (dtype == 1)
     return d == 64 ? merge_d<__nv_bfloat16, 64>(P, st)
@@ -228,11 +253,19 @@ pod_status pod_tree_bind_workspace(pod_tree_handle h, void* workspace, size_t wo
                                        " bytes is smaller than the plan's " + std::to_string(P.total));
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return fail(POD_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  give_up(h);
+  pod_tree_workspace_lost(workspace);
   cudaError_t e = cudaMemcpyAsync(workspace, P.image.data(), P.image.size(), cudaMemcpyHostToDevice, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "cudaMemcpyAsync(tree plan)");
   // the copy reads pageable host memory that the handle owns
   e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize(tree plan)");
+  try {
+    std::lock_guard<std::mutex> lock(owners().mu);
+    owners().of[workspace] = h;
+  } catch (const std::exception&) {
+    return fail(POD_ERR_INVALID_ARG, "out of host memory");
+  }
   h->workspace = workspace;
   return POD_OK;
 }
@@ -309,6 +342,12 @@ pod_status pod_tree_run(pod_tree_handle h, const void* q, const void* kv, const 
   const PodTreePlanHost& P = h->plan;
   if (!h->workspace) return fail(POD_ERR_WORKSPACE, "the plan has no bound workspace");
   if (workspace != h->workspace) return fail(POD_ERR_WORKSPACE, "workspace differs from the one the plan was bound to");
+  {
+    std::lock_guard<std::mutex> lock(owners().mu);
+    auto it = owners().of.find(workspace);
+    if (it == owners().of.end() || it->second != h)
+      return fail(POD_ERR_WORKSPACE, "another plan has been bound to the workspace since: bind this one again");
+  }
   if (h->has_sinks && !sinks) return fail(POD_ERR_INVALID_ARG, "plan has sinks but sinks is NULL");
   if (!h->has_sinks && sinks) return fail(POD_ERR_INVALID_ARG, "sinks given but the plan was made without sinks");
   if (h->format == POD_KV_E4M3_BLOCK ? !kv_scales : kv_scales != nullptr)
@@ -387,6 +426,7 @@ pod_status pod_tree_plan_table(pod_tree_handle h, int32_t which, int32_t* out, i
 }
 
 pod_status pod_tree_destroy(pod_tree_handle h) {
+  if (h) give_up(h);
   delete h;
   return POD_OK;
 }

@@ -160,3 +160,46 @@ def test_runs_on_one_workspace_right_behind_each_other(fmt, d, long):
     for (a, b), (o, l) in zip(want, got):
         assert torch.equal(a, o) and torch.equal(b, l)
     assert pod.pod_tree_read_device_status(h, ws) == 0
+
+
+# ------------------------------------------------------------------ one workspace, several plans
+@pytest.mark.gpu
+def test_a_workspace_holds_the_plan_bound_last():
+    """A run of a plan whose workspace holds another one by now would read that one's
+    tables: it is refused, and runs again once it is bound again."""
+    a = tree_case(n=[9, 30, 4], kv_len=[1200, 400, 40], H=8, Hk=2, d=128, ps=16, seed=2)
+    b = tree_case(n=[3], kv_len=[70], H=8, Hk=2, d=128, ps=16, seed=3)
+    plans = [x.plan() for x in (a, b)]
+    ws = torch.empty(max(pod.pod_tree_workspace_size(h) for h in plans), dtype=torch.uint8, device="cuda")
+    tensors = [x.args() for x in (a, b)]
+
+    def run(i, w=ws):
+        q, kv, more = tensors[i]
+        return pod.pod_tree_run(plans[i], q, kv, w, **more)
+    pod.pod_tree_bind_workspace(plans[0], ws)
+    a.check(*run(0))
+    pod.pod_tree_bind_workspace(plans[1], ws)
+    with pytest.raises(pod.PodError, match="another plan has been bound"):
+        run(0)
+    b.check(*run(1))
+    pod.pod_tree_bind_workspace(plans[0], ws)
+    with pytest.raises(pod.PodError, match="another plan has been bound"):
+        run(1)
+    a.check(*run(0))
+    # a plan of pod_run takes it too
+    h = pod.pod_plan(None, None, None, None, [0, 1], [0, 1], [0], [16], 8, 2, 128, 16, True, -1, None,
+                     dtype=torch.bfloat16, p_num_pages=0, d_num_pages=1)
+    other = torch.empty(max(ws.numel(), pod.pod_workspace_size(h)), dtype=torch.uint8, device="cuda")
+    pod.pod_tree_bind_workspace(plans[0], other)
+    pod.pod_bind_workspace(h, other)
+    with pytest.raises(pod.PodError, match="another plan has been bound"):
+        run(0, other)
+    # the plan that took it is gone, and this one has moved on and come back
+    pod.pod_tree_bind_workspace(plans[1], ws)
+    pod.pod_tree_bind_workspace(plans[0], ws)
+    pod.pod_tree_destroy(plans[1])
+    a.check(*run(0))
+    pod.pod_tree_bind_workspace(plans[0], other)
+    with pytest.raises(pod.PodError, match="differs"):
+        run(0)
+    a.check(*run(0, other))
