@@ -789,6 +789,14 @@ class PodTreeHandle:
             self.ptr = 0
 
 
+def _workspace(workspace):
+    """(pointer, bytes) of a tree plan's workspace. A view with gaps or repeats counts
+    more bytes than lie behind its first."""
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise PodError(1, "the workspace must be a contiguous CUDA tensor")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def pod_tree_plan(q_indptr, kv_indptr, kv_indices, last_page_len, num_qo_heads, num_kv_heads, head_dim, page_size,
                   *, dtype, num_pages, sm_scale=None, kv_format="16bit", k_scale=1.0, v_scale=1.0, kv_layout="NHD",
                   has_sinks=False, num_sms=0, workspace=None, stream=None) -> PodTreeHandle:
@@ -808,8 +816,7 @@ def pod_tree_plan(q_indptr, kv_indptr, kv_indices, last_page_len, num_qo_heads, 
         if len(arrs[1]) != batch + 1 or len(arrs[3]) != batch or len(arrs[2]) < int(arrs[1][-1]):
             raise PodError(1, "the page table arrays do not fit together")
     handle, req = ctypes.c_void_p(), ctypes.c_size_t(0)
-    ws_ptr = None if workspace is None else workspace.data_ptr()
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_ptr, ws_bytes = (None, 0) if workspace is None else _workspace(workspace)
     code = lib.pod_tree_plan(*[_ptr(a) for a in arrs], max(batch, 0), int(num_pages), int(num_qo_heads),
                              int(num_kv_heads), int(head_dim), int(page_size),
                              float(sm_scale) if sm_scale is not None else 0.0, _dtype_code(dtype),
@@ -837,9 +844,9 @@ def pod_tree_workspace_size(h: PodTreeHandle) -> int:
 
 def pod_tree_bind_workspace(h: PodTreeHandle, workspace, stream=None):
     _torch()
-    _call(load_library().pod_tree_bind_workspace, _device_of(workspace), stream, h.ptr, workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
-    h.workspace_ptr = workspace.data_ptr()
+    ptr, size = _workspace(workspace)
+    _call(load_library().pod_tree_bind_workspace, _device_of(workspace), stream, h.ptr, ptr, size)
+    h.workspace_ptr = ptr
 
 
 def pod_tree_run(h: PodTreeHandle, q, kv, workspace, tree_mask=None, kv_scales=None, sinks=None, out=None, lse=None,

@@ -203,3 +203,24 @@ def test_a_workspace_holds_the_plan_bound_last():
     with pytest.raises(pod.PodError, match="differs"):
         run(0)
     a.check(*run(0, other))
+
+
+def test_a_workspace_is_a_whole_piece_of_the_device():
+    """A host tensor, and an expanded one that is shorter than its elements, are refused
+    before anything is copied."""
+    c = tree_case(n=[3], kv_len=[70], H=8, Hk=2, d=128, ps=16, seed=3)
+    h = c.plan(num_sms=4)
+    n = pod.pod_tree_workspace_size(h)
+    host = torch.empty(n, dtype=torch.uint8)
+
+    class OnDevice:                                   # (what is asked of a tensor before its pointer)
+        is_cuda = True
+
+        def __init__(self, t):
+            self.is_contiguous, self.data_ptr, self.numel = t.is_contiguous, t.data_ptr, t.numel
+            self.element_size, self.get_device = t.element_size, lambda: 0
+    for ws in (host, OnDevice(host[:1].expand(n)), OnDevice(torch.empty(2 * n, dtype=torch.uint8)[::2])):
+        with pytest.raises(pod.PodError, match="contiguous CUDA tensor"):
+            pod.pod_tree_bind_workspace(h, ws)
+        with pytest.raises(pod.PodError, match="contiguous CUDA tensor"):
+            c.plan(num_sms=4, workspace=ws)
