@@ -392,7 +392,7 @@ size_t pod_static_scratch_capacity(void);
  * in the page, DEVICE int64 (request r's key t: page kv_indices[kv_indptr[r] +
  * t / page_size], position t % page_size). A negative slot is a padding row.
  * A slot at or past num_pages * page_size is treated like a negative one, and
- * sets bit 4 of *status (DEVICE int32, or NULL for no report; never cleared
+ * joins the value 4 into *status by OR (DEVICE int32, or NULL for no report; never cleared
  * here). Where rows of one write name the same slot, each code, value and
  * exponent byte of it is left by one of them, not all by the same one.
  *
@@ -448,7 +448,9 @@ typedef struct pod_io_args {
  * with `interleaved`, turns by
  * (positions[row] / rope_scale) * rope_theta^(-2j/rotary_dim) (the rotation of
  * pod_plan_set_rope, here over the first rotary_dim elements; 0 = none).
- * fp32 throughout, rounded once. Positions may have any sign (NULL when
+ * fp32 throughout, rounded once; rows and weights of any magnitude of their type.
+ * Positions may have any sign and size: cos and sin are off by at most 2^-23.4 while
+ * rope_theta^(-2j/rotary_dim) / rope_scale stays below 2^30 (NULL when
  * rotary_dim is 0). num_qo_heads or num_kv_heads may be 0 (then that tensor is
  * not touched). q_out may be q, and k_out k, with the same stride.
  * Errors: POD_ERR_INVALID_ARG (NULL or misaligned tensors, a stride that does
@@ -477,7 +479,7 @@ pod_status pod_norm_rope_append(const pod_io_args* args, void* stream);
 
 /*
  * pod_gather_kv — read cache rows back: k_out [rows, 2, Hk, head_dim] (K, then
- * V, contiguous) in dtype, value = code * scale rounded to nearest, finite
+ * V, contiguous) in dtype, value = code * scale in fp32, rounded to nearest, finite
  * values saturating at the type's largest; a padding row reads as zeros. The
  * result is also an NHD cache of page size 1 (pages 0 .. rows-1), so the 16-bit
  * prefill half can run over an FP8 cache's context.
@@ -536,12 +538,19 @@ pod_status pod_tree_bind_workspace(pod_tree_handle h, void* workspace, size_t wo
  * of pod_plan_set_prefill_mask's); mask_bytes covers ceil(sum n_r^2 / 8), and
  * no byte past it is read. NULL: token i sees drafted tokens 0..i (a chain).
  * The diagonal is a bit like the others. A row without visible keys gives
- * out = 0 and lse = -inf. Slots at or past kv_len may hold anything; the values
+ * out = 0 and lse = -inf, whatever its sink. Slots at or past kv_len may hold anything; the values
  * of every key below it must be finite (a masked key's weight is 0, and 0
  * times an infinity is NaN).
- * The workspace must be the bound one; runs that share it must not overlap.
- * Launches on `stream` only and can be captured; a replay reads the tensors
- * again under the same plan, while the workspace still holds it.
+ * Precision: logits, sums and the output's accumulation are fp32. The weights
+ * P = exp(logit - max) are an operand of the matrix unit: over a 16-bit cache each is
+ * rounded once to its type (off by 2^-8 of it in bf16, 2^-11 in fp16); over an FP8
+ * cache it is carried in E4M3 parts, off by 2^-9 + 2^-11 (bf16 results; 2^-15 of the
+ * largest weight at the bottom) or 2^-12 (fp16 results; 2^-22 at the bottom), and q
+ * is carried in parts too: all its bits, but for 2^-17 of a row's largest magnitude.
+ * The workspace must be the bound one and hold this plan; runs that share it must not
+ * overlap. Launches on `stream` only and can be captured; a replay reads the tensors
+ * again under the same plan, while the workspace still holds it (one step's layers:
+ * another step has another plan).
  * Errors: POD_ERR_INVALID_ARG, POD_ERR_WORKSPACE, POD_ERR_CUDA.
  */
 pod_status pod_tree_run(pod_tree_handle h, const void* q, const void* kv, const uint8_t* kv_scales,

@@ -32,12 +32,12 @@
 // shuffles: 230 instructions per 8 elements, and bound by them (below, in
 // brackets).
 //
-// Measured on a GB300, back to back in a graph, with the share of the measured
-// copy rate: norm and rotation of 8796 rows of 64/8 heads of 128, bf16: 57 us,
-// 85 % (84); 4096 rows of 64/8 heads normed, turned and written: 29.7 us, 85 %
-// (45); 16384 rows of 8 heads written with block scales: 18.0 us, 84 % (26.6);
-// 65536 rows read back: 63 us, 96 %. Calls of a few hundred rows take 3.5 to 5
-// us, the launch and two dependent trips to memory.
+// Measured on a GB300, back to back in a graph over several inputs, with the share of
+// the measured copy rate: norm and rotation of 8796 rows of 64/8 heads of 128, bf16:
+// 58.8 us, 83 % (84); 4096 rows of 64/8 heads normed, turned and written: 30.7 us, 82 %
+// (45); 16384 rows of 8 heads written with block scales: 18.8 us, 81 % (26.6); 65536
+// rows read back: 63.7 us, 95 %. Calls of a few hundred rows take 4 to 5 us, the
+// launch and two dependent trips to memory.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <string.h>

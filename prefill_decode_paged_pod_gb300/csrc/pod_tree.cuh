@@ -35,10 +35,10 @@
 // between 2^6 and 2^8.5) is carried in parts. bf16 results:
 // two E4M3 parts, 4 bits and the fp16 remainder to 4 bits, at most 2^-9 + 2^-11 of
 // p off, and 2^-15 of the largest weight at the bottom. fp16 results, by Veltkamp
-// splitting: 4 bits in E4M3 and twice 3 bits in E5M2, whose range goes on below, 2^-11 of p and 2^-23 of the
+// splitting: 4 bits in E4M3 and twice 3 bits in E5M2, whose range goes on below, 2^-12 of p and 2^-22 of the
 // largest weight. (An
 // earlier form widened the codes to fp16 in shared memory; the two warps that
-// did it set the pace: 620 us for 96 requests of 8192 keys, now 410, and 330 with
+// did it set the pace: 620 us for 96 requests of 8192 keys, now 412, and 321 with
 // per-tensor scales.) These are constants of the softmax and of the output. Block scales are powers of
 // two per key: K's multiplies the key's column of S, V's the column of P
 // relative to the largest V scale met so far.
