@@ -570,6 +570,159 @@ pod_status pod_tree_plan_table(pod_tree_handle h, int32_t which, int32_t* out, i
 /* Release the handle (host memory only). NULL is accepted. */
 pod_status pod_tree_destroy(pod_tree_handle h);
 
+/* ------------------------------------------------------------------------
+ * Decode steps whose tables live on the device: request lengths, block table
+ * and free pages are DEVICE memory, the calls read them there, and nothing is
+ * planned on the host. A step captured in a CUDA graph therefore serves every
+ * later step, whatever its lengths.
+ *
+ * Block table: int32 [batch, table_width], rows table_stride apart; entry p of
+ * a request is the page of its keys p * page_size ... Entries behind a
+ * request's ceil(len / page_size) pages may hold anything. A page at or past
+ * num_pages (or negative) in front of that reads as if its keys were masked,
+ * and joins the value 4 into *status by OR, as does a length outside
+ * [0, table_width * page_size], which is cut to that range. status, streams
+ * and pointers' alignment as above; table_width * page_size is at most 2^30.
+ * ------------------------------------------------------------------------ */
+
+/* Arguments of pod_step_tables. All pointers DEVICE. */
+typedef struct pod_step_args {
+    int32_t* block_table;       /* [batch, table_width], table_stride; updated */
+    const int32_t* kv_lens;     /* [batch] keys before the step */
+    const int32_t* new_lens;    /* [batch] tokens of the step; negative: keys taken back */
+    int32_t* kv_lens_out;       /* [batch] keys after it; may be kv_lens */
+    int32_t* free_pages;        /* [free_capacity], a stack: the top is entry *free_count - 1 */
+    const int32_t* free_count;  /* [1] */
+    int32_t* free_count_out;    /* [1]; may be free_count */
+    int32_t* q_indptr;          /* [batch + 1] */
+    int32_t* requests;          /* [max_rows] */
+    int32_t* positions;         /* [max_rows] */
+    int64_t* slots;             /* [max_rows] */
+    int32_t* kv_indptr;         /* [batch + 1]; with the next two, or all three NULL */
+    int32_t* kv_indices;        /* [max_pages] */
+    int32_t* last_page_len;     /* [batch] */
+    int32_t* status;            /* or NULL */
+    int64_t table_stride;
+    int32_t batch, table_width, page_size, free_capacity, max_rows, max_pages;
+} pod_step_args;
+
+/*
+ * pod_step_tables — the start of a step: pages for its tokens, and the arrays
+ * that the other calls read.
+ *
+ * Request r had L = kv_lens[r] keys and gets n = new_lens[r] more (n < 0: its
+ * last -n keys are taken back, down to none). First every request that shrinks
+ * pushes the pages that it no longer needs onto the stack, requests in order,
+ * pages in the order of the table; then every request that grows pops what it
+ * needs off the top, in the same order, into the next entries of its table row.
+ * kv_lens_out[r] = max(0, L + n).
+ * Rows: the tokens of growing requests end to end; q_indptr[r] is the first row
+ * of request r, and row i has its request, its position (L, L + 1, ...) and its
+ * slot. Rows from q_indptr[batch] to max_rows are padding rows: request -1,
+ * position 0, slot -1.
+ * kv_indptr, kv_indices, last_page_len: the page table after the step, as
+ * pod_plan reads it (from the host); entries of kv_indices behind
+ * kv_indptr[batch] are -1.
+ * What does not fit: a request whose keys would pass its table row keeps its
+ * length and gets no rows, and so does the first growing request that would
+ * need more pages than the stack holds or more rows than max_rows, and every
+ * growing one behind it; each joins the value 8 into *status by OR. Pages past
+ * free_capacity are not pushed and entries past max_pages not written, with
+ * the value 8 too. Everything else of the call is as if they had not asked.
+ * Errors: POD_ERR_INVALID_ARG (NULL arrays, bad sizes), POD_ERR_CUDA.
+ */
+pod_status pod_step_tables(const pod_step_args* args, void* stream);
+
+/* Arguments of the calls below; each reads the fields that its text names. All
+ * pointers DEVICE, 16-byte aligned. */
+typedef struct pod_decode_args {
+    const void* q;              /* [batch, num_qo_heads, head_dim], q_stride */
+    const void* kv_cache;       /* [num_pages, 2, ...] */
+    const uint8_t* kv_scales;   /* exponent bytes of a POD_KV_E4M3_BLOCK cache, else NULL */
+    void* bounds;               /* [num_pages, num_kv_heads, 2, head_dim] in dtype */
+    const int32_t* block_table; /* [batch, table_width], table_stride */
+    const int32_t* kv_lens;     /* [batch], the keys of this step among them */
+    int32_t* pages;             /* [batch, num_kv_heads, num_selected], or NULL */
+    const int64_t* slots;       /* [rows] */
+    const float* sinks;         /* [num_qo_heads], or NULL */
+    void* out;                  /* as q, out_stride */
+    float* lse;                 /* [batch, num_qo_heads], or NULL */
+    void* workspace;
+    int32_t* status;            /* or NULL */
+    int64_t q_stride, out_stride, table_stride, num_pages, rows;
+    size_t workspace_bytes;
+    int32_t batch, table_width, page_size, num_qo_heads, num_kv_heads, head_dim;
+    int32_t kv_layout, kv_format, dtype;
+    int32_t num_selected, keep_first, keep_last, window_left;
+    float sm_scale, k_scale, v_scale;
+} pod_decode_args;
+
+/*
+ * pod_page_bounds — the bounds of the pages that a write touched: after
+ * pod_append_kv (or pod_norm_rope_append), with its slots, the smallest and
+ * largest value of every channel over the keys of each page,
+ * bounds[page][head][0 and 1][channel].
+ * Rows of one page stand next to each other in `slots`, in ascending order, as
+ * pod_step_tables lists them; the keys of a page are those up to its last row
+ * here, all read from the cache (so the call can be repeated, and what keys
+ * taken back left behind goes with the next write). Values are code * scale in fp32,
+ * rounded outward to dtype within its finite values; NaN does not count. Bounds of other pages are
+ * left as they are. Padding rows are skipped; a slot past the pool joins 4 into
+ * *status.
+ * Reads kv_cache, kv_scales, slots, rows, num_pages, page_size, num_kv_heads,
+ * head_dim, kv_layout, kv_format, dtype, k_scale, status; writes bounds.
+ * Errors: POD_ERR_INVALID_ARG, POD_ERR_UNSUPPORTED, POD_ERR_CUDA.
+ */
+pod_status pod_page_bounds(const pod_decode_args* args, void* stream);
+
+/*
+ * pod_select_pages — for every request and KV head the num_selected pages that
+ * promise its query the largest logits.
+ * The score of a page is the sum over the KV head's query heads and the
+ * channels of max(q * smallest, q * largest): what the query's logits with the
+ * page's keys can reach, before sm_scale. The first keep_first and the last
+ * keep_last pages of a request are chosen whatever their score (the two are at
+ * most num_selected together), then the others by their score; equal scores go
+ * to the lower position, NaN counts as the largest. The choice is that of the scores in
+ * 64 bits. pages [batch, num_kv_heads, num_selected]: the positions of the
+ * chosen pages in the request's table row, ascending, -1 behind them.
+ * Reads q, bounds, block_table, kv_lens, num_pages, table sizes, heads,
+ * head_dim, dtype, num_selected, keep_first, keep_last, status, workspace.
+ * A page outside the pool scores minus infinity.
+ * Errors: POD_ERR_INVALID_ARG, POD_ERR_UNSUPPORTED (head_dim, dtype),
+ * POD_ERR_WORKSPACE, POD_ERR_CUDA.
+ */
+pod_status pod_select_pages(const pod_decode_args* args, void* stream);
+
+/* Bytes of workspace of pod_select_pages. 0 for sizes that it refuses. */
+size_t pod_select_pages_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t table_width);
+
+/*
+ * pod_paged_decode — attention of one token per request: query row r over keys
+ * t < kv_lens[r] of request r, with window_left >= 0 over
+ * t >= kv_lens[r] - 1 - window_left only, or, where `pages` is given, over the
+ * keys of these pages (positions in the table row, per KV head; entries that
+ * are negative or past the request's pages are skipped, and a page listed
+ * twice counts twice; of a request with fewer than num_selected pages only as many entries as
+ * it has pages are read). A row may be any query whose last key is its own.
+ * The cache in any format and layout, any page size, any number of query heads
+ * per KV head; head_dim 64, 128 or 256. sm_scale <= 0 means 1/sqrt(head_dim).
+ * lse: base 2, without the sink; a row without visible keys gives out = 0 and
+ * lse = -inf, whatever its sink. Slots past a request's keys may hold anything.
+ * Logits, sums and the output are fp32; the softmax weights are two 16-bit
+ * parts (off by 2^-17 of a weight in bf16, 2^-22 in fp16); over FP8 caches
+ * fp16 carries q (all bits but for 2^-38 of a row's largest magnitude) and V.
+ * workspace: pod_paged_decode_workspace_size bytes, 256-byte aligned, whose contents
+ * need not survive between calls; calls that share it must not overlap.
+ * Two calls with the same inputs give the same bits.
+ * Errors: POD_ERR_INVALID_ARG (a window together with pages among them),
+ * POD_ERR_UNSUPPORTED (head_dim, dtype), POD_ERR_WORKSPACE, POD_ERR_CUDA.
+ */
+pod_status pod_paged_decode(const pod_decode_args* args, void* stream);
+
+/* Bytes of workspace of pod_paged_decode. 0 for sizes that it refuses. */
+size_t pod_paged_decode_workspace_size(int32_t batch, int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,7 +22,7 @@ import ctypes
 import os
 import struct
 from dataclasses import dataclass
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import numpy as np
 
@@ -36,6 +36,8 @@ __all__ = [
     "pod_qk_norm_rope", "pod_append_kv", "pod_norm_rope_append", "pod_gather_kv", "pod_kv_slots",
     "PodTreeHandle", "pod_tree_plan", "pod_tree_run", "pod_tree_workspace_size", "pod_tree_bind_workspace",
     "pod_tree_read_device_status", "pod_tree_plan_table", "pod_tree_destroy",
+    "PodStep", "pod_step_tables", "pod_page_bounds", "pod_select_pages", "pod_select_pages_workspace_size",
+    "pod_paged_decode", "pod_paged_decode_workspace_size",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -103,9 +105,14 @@ def load_library(path: Optional[str] = None):
     lib.pod_replan.restype = ctypes.c_int
     lib.pod_replan.argtypes = [V, V, V, V, V, I32, V, V, V, V, I32, V]
     I64, F32 = ctypes.c_int64, ctypes.c_float
-    for fn in (lib.pod_qk_norm_rope, lib.pod_append_kv, lib.pod_norm_rope_append, lib.pod_gather_kv):
+    for fn in (lib.pod_qk_norm_rope, lib.pod_append_kv, lib.pod_norm_rope_append, lib.pod_gather_kv,
+               lib.pod_step_tables, lib.pod_page_bounds, lib.pod_select_pages, lib.pod_paged_decode):
         fn.restype = ctypes.c_int
         fn.argtypes = [ctypes.c_char_p, V]
+    lib.pod_select_pages_workspace_size.restype = SZ
+    lib.pod_select_pages_workspace_size.argtypes = [I32, I32, I32]
+    lib.pod_paged_decode_workspace_size.restype = SZ
+    lib.pod_paged_decode_workspace_size.argtypes = [I32, I32, I32, I32]
     lib.pod_tree_plan.restype = ctypes.c_int
     lib.pod_tree_plan.argtypes = [V, V, V, V, I32, I32, I32, I32, I32, I32, F32, ctypes.c_int, I32, F32, F32,
                                   I32, I32, I32, V, SZ, V, ctypes.POINTER(V), ctypes.POINTER(SZ)]
@@ -911,3 +918,213 @@ def pod_tree_destroy(h: PodTreeHandle):
     if h.ptr:
         load_library().pod_tree_destroy(ctypes.c_void_p(h.ptr))
         h.ptr = 0
+
+
+# ------------------------------------------------------------------ decode steps planned on the device
+# struct pod_step_args: 15 pointers, 1 int64, 6 int32
+_STEP_ARGS = struct.Struct("@15Qq6i")
+# struct pod_decode_args: 13 pointers, 5 int64, 1 size_t, 13 int32, 3 floats
+_DECODE_ARGS = struct.Struct("@13Q5qQ13i3f")
+
+
+class PodStep(NamedTuple):
+    """The arrays of a step (CUDA tensors), as pod_step_tables writes them."""
+    kv_lens: object          # [batch] int32, keys after the step
+    q_indptr: object         # [batch + 1] int32, first row of every request
+    requests: object         # [max_rows] int32, -1 behind the last row
+    positions: object        # [max_rows] int32, 0 behind the last row
+    slots: object            # [max_rows] int64, -1 behind the last row
+    kv_indptr: object = None      # [batch + 1] int32, with max_pages
+    kv_indices: object = None     # [max_pages] int32, -1 behind the last page
+    last_page_len: object = None  # [batch] int32
+
+
+def _table(t, rows, dev):
+    """(pointer, width, row stride) of an int32 block table [rows, width]."""
+    if t.dtype != _torch_module.int32 or t.dim() != 2 or t.get_device() != dev or t.shape[0] != rows:
+        raise PodError(1, f"block_table must be an int32 tensor [{rows}, pages] on cuda:{dev}")
+    width, (sr, sc) = t.shape[1], t.stride()
+    if (sc != 1 and width > 1) or (rows > 1 and sr < width):
+        raise PodError(1, "the entries of a block table row must be contiguous, its rows apart")
+    return t.data_ptr(), width, sr if rows > 1 else max(sr, width)
+
+
+def pod_step_tables(block_table, kv_lens, new_lens, free_pages, free_count, page_size: int, *, max_rows: int,
+                    max_pages: int = 0, kv_lens_out=None, free_count_out=None, out: Optional[PodStep] = None,
+                    status=None, stream=None) -> PodStep:
+    """The start of a step on the device. Request r had ``kv_lens[r]`` keys and gets
+    ``new_lens[r]`` more (a negative number takes keys back); pages come from and
+    go to the stack ``free_pages`` (its top is entry ``free_count[0] - 1``), and
+    ``block_table`` [batch, pages] is updated. Returns the rows of the step for
+    the other calls, up to ``max_rows``, and with ``max_pages`` > 0 the page table
+    end to end. ``kv_lens`` and ``free_count`` are updated in place unless their
+    ``_out`` is given; ``out`` is an earlier PodStep to write into (its kv_lens is
+    not used). A step that does not fit joins 8 into ``status``."""
+    lib = _lib or load_library()
+    torch = _torch()
+    i32 = torch.int32
+    dev = _device_of(kv_lens)
+    batch = kv_lens.numel()
+    lens = _whole("kv_lens", kv_lens, (batch,), i32, dev)
+    news = _whole("new_lens", new_lens, (batch,), i32, dev)
+    count = _whole("free_count", free_count, (1,), i32, dev)
+    table, width, ts = _table(block_table, batch, dev)
+    capacity, rows, pages = free_pages.numel(), int(max_rows), int(max_pages)
+    stack = _whole("free_pages", free_pages, (capacity,), i32, dev)
+    if rows < 0 or pages < 0:
+        raise PodError(1, "max_rows and max_pages must not be negative")
+    if kv_lens_out is None:
+        kv_lens_out = kv_lens
+    if free_count_out is None:
+        free_count_out = free_count
+    lo = _whole("kv_lens_out", kv_lens_out, (batch,), i32, dev)
+    co = _whole("free_count_out", free_count_out, (1,), i32, dev)
+    if out is None:
+        # one allocation for the int32 arrays, each 16-byte aligned
+        a, b, r, p = ((n + 3) // 4 * 4 for n in (batch + 1, batch, rows, pages))
+        buf = _empty((a + 2 * r + (a + b + p if pages else 0),), i32, kv_lens, stream)
+        slots = _empty((rows,), torch.int64, kv_lens, stream)
+        q_indptr, requests, positions = buf[:batch + 1], buf[a:a + rows], buf[a + r:a + r + rows]
+        indptr = indices = last = None
+        if pages:
+            o = a + 2 * r
+            indptr, last, indices = buf[o:o + batch + 1], buf[o + a:o + a + batch], buf[o + a + b:o + a + b + pages]
+        base = buf.data_ptr()
+        qi, rq, po, sl = base, base + 4 * a, base + 4 * (a + r), slots.data_ptr()
+        ip, la, ix = (base + 4 * o, base + 4 * (o + a), base + 4 * (o + a + b)) if pages else (0, 0, 0)
+    else:
+        _, q_indptr, requests, positions, slots, indptr, indices, last = out
+        qi = _whole("q_indptr", q_indptr, (batch + 1,), i32, dev)
+        rq = _whole("requests", requests, (rows,), i32, dev)
+        po = _whole("positions", positions, (rows,), i32, dev)
+        sl = _whole("slots", slots, (rows,), torch.int64, dev)
+        ip = la = ix = 0
+        if pages:
+            if indptr is None or indices is None or last is None:
+                raise PodError(1, "out has no page table, but max_pages asks for one")
+            ip = _whole("kv_indptr", indptr, (batch + 1,), i32, dev)
+            ix = _whole("kv_indices", indices, (pages,), i32, dev)
+            la = _whole("last_page_len", last, (batch,), i32, dev)
+        else:
+            indptr = indices = last = None
+    _call(lib.pod_step_tables, dev, stream, _STEP_ARGS.pack(
+        table, lens, news, lo, stack, count, co, qi, rq, po, sl, ip, ix, la, _status(status, dev), ts, batch, width,
+        int(page_size), capacity, rows, pages))
+    return PodStep(kv_lens_out, q_indptr, requests, positions, slots, indptr, indices, last)
+
+
+def pod_page_bounds(kv_cache, bounds, slots, *, kv_scales=None, k_scale=1.0, kv_layout="NHD", status=None,
+                    stream=None):
+    """Smallest and largest key of every page that a write touched, per KV head
+    and channel: ``bounds`` [pages, Hk, 2, d] (fp16 or bf16) is updated for the
+    pages of the int64 ``slots`` that pod_append_kv or pod_norm_rope_append wrote
+    (rows of a page next to each other, ascending). Returns ``bounds``."""
+    lib = _lib or load_library()
+    torch = _torch()
+    dev, dtype = _device_of(kv_cache), bounds.dtype
+    code = _dtype_code(dtype)
+    cache, scales, pages, ps, hk, d, hnd, fmt = _cache_args(kv_cache, kv_scales, kv_layout, dtype, dev)
+    bp = _whole("bounds", bounds, (pages, hk, 2, d), dtype, dev)
+    rows = slots.numel()
+    sl = _whole("slots", slots, (rows,), torch.int64, dev)
+    _call(lib.pod_page_bounds, dev, stream, _DECODE_ARGS.pack(
+        0, cache, scales, bp, 0, 0, 0, sl, 0, 0, 0, 0, _status(status, dev), 0, 0, 0, pages, rows, 0, 0, 0, ps, 0, hk,
+        d, hnd, fmt, code, 0, 0, 0, -1, 0.0, k_scale, 1.0))
+    return bounds
+
+
+def _scratch(workspace, need, like, dev, stream):
+    """(tensor, pointer, bytes) of a call's workspace: the caller's, or a new one."""
+    if workspace is None:
+        workspace = _empty((max(need, 256),), _torch_module.uint8, like, stream)
+    elif workspace.get_device() != dev:
+        raise PodError(1, f"the workspace must be on cuda:{dev}")
+    return (workspace,) + _workspace(workspace)
+
+
+def pod_select_pages_workspace_size(batch: int, num_kv_heads: int, table_width: int) -> int:
+    """Bytes of workspace of pod_select_pages."""
+    return int((_lib or load_library()).pod_select_pages_workspace_size(int(batch), int(num_kv_heads),
+                                                                        int(table_width)))
+
+
+def pod_select_pages(q, bounds, block_table, kv_lens, num_selected: int, page_size: int, *, keep_first=0, keep_last=1,
+                     pages=None, workspace=None, status=None, stream=None):
+    """The ``num_selected`` pages of every request and KV head whose ``bounds``
+    (pod_page_bounds) promise the heads of q [batch, H, d] the largest logits:
+    int32 [batch, Hk, num_selected], positions in the request's ``block_table``
+    row, ascending, -1 behind them. The first ``keep_first`` and the last
+    ``keep_last`` pages are among them whatever their score."""
+    lib = _lib or load_library()
+    torch = _torch()
+    dev, dtype = _device_of(q), q.dtype
+    code = _dtype_code(dtype)
+    batch, H, d, qs = _heads("q", q, dtype, dev)
+    if bounds.dim() != 4 or bounds.shape[3] != d:
+        raise PodError(1, f"bounds must be [pages, kv heads, 2, {d}]")
+    n, hk = bounds.shape[:2]
+    bp = _whole("bounds", bounds, (n, hk, 2, d), dtype, dev)
+    lens = _whole("kv_lens", kv_lens, (batch,), torch.int32, dev)
+    table, width, ts = _table(block_table, batch, dev)
+    k = int(num_selected)
+    if k < 1:
+        raise PodError(1, "num_selected must be positive")
+    if pages is None:
+        pages = _empty((batch, hk, k), torch.int32, q, stream)
+        pp = pages.data_ptr()
+    else:
+        pp = _whole("pages", pages, (batch, hk, k), torch.int32, dev)
+    ws, wp, wn = _scratch(workspace, 0 if workspace is not None else
+                          lib.pod_select_pages_workspace_size(batch, hk, width), q, dev, stream)
+    _call(lib.pod_select_pages, dev, stream, _DECODE_ARGS.pack(
+        q.data_ptr(), 0, 0, bp, table, lens, pp, 0, 0, 0, 0, wp, _status(status, dev), qs, 0, ts, n, 0, wn, batch,
+        width, int(page_size), H, hk, d, 0, 0, code, k, int(keep_first), int(keep_last), -1, 0.0, 1.0, 1.0))
+    return pages
+
+
+def pod_paged_decode_workspace_size(batch: int, num_qo_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    """Bytes of workspace of pod_paged_decode."""
+    return int((_lib or load_library()).pod_paged_decode_workspace_size(int(batch), int(num_qo_heads),
+                                                                        int(num_kv_heads), int(head_dim)))
+
+
+def pod_paged_decode(q, kv_cache, block_table, kv_lens, *, pages=None, sm_scale=None, window_left=-1, sinks=None,
+                     kv_scales=None, k_scale=1.0, v_scale=1.0, kv_layout="NHD", out=None, lse=None, workspace=None,
+                     status=None, stream=None):
+    """Attention of one token per request, q [batch, H, d] (any row stride that is
+    a multiple of 8), over the first ``kv_lens`` keys of its pages, over the last
+    ``window_left`` + 1 of them, or over the selected ``pages``
+    (pod_select_pages). The cache is a 16-bit or an FP8 one, as for
+    pod_append_kv. Lengths and tables are read on the device, so a captured call
+    serves every later step. Returns (out, lse), lse in base 2."""
+    lib = _lib or load_library()
+    torch = _torch()
+    dev, dtype = _device_of(q), q.dtype
+    code = _dtype_code(dtype)
+    batch, H, d, qs = _heads("q", q, dtype, dev)
+    cache, scales, n, ps, hk, dk, hnd, fmt = _cache_args(kv_cache, kv_scales, kv_layout, dtype, dev)
+    if dk != d:
+        raise PodError(1, "q and kv_cache have different head_dim")
+    lens = _whole("kv_lens", kv_lens, (batch,), torch.int32, dev)
+    table, width, ts = _table(block_table, batch, dev)
+    pp = k = sp = 0
+    if pages is not None:
+        k = pages.shape[-1] if pages.dim() == 3 else 0
+        if k < 1:                        # (an empty tensor has no pointer: it would read as no pages)
+            raise PodError(1, "pages must be [batch, kv heads, num_selected]")
+        pp = _whole("pages", pages, (batch, hk, k), torch.int32, dev)
+    if sinks is not None:
+        sp = _whole("sinks", sinks, (H,), torch.float32, dev)
+    out, os_ = _out_rows("out", out, q, batch, H, d, dtype, dev, stream)
+    if lse is None:
+        lse = _empty((batch, H), torch.float32, q, stream)
+        lp = lse.data_ptr()
+    else:
+        lp = _whole("lse", lse, (batch, H), torch.float32, dev)
+    ws, wp, wn = _scratch(workspace, 0 if workspace is not None else
+                          lib.pod_paged_decode_workspace_size(batch, H, hk, d), q, dev, stream)
+    _call(lib.pod_paged_decode, dev, stream, _DECODE_ARGS.pack(
+        q.data_ptr(), cache, scales, 0, table, lens, pp, 0, sp, out.data_ptr(), lp, wp, _status(status, dev), qs, os_,
+        ts, n, 0, wn, batch, width, ps, H, hk, d, hnd, fmt, code, k, 0, 0, int(window_left),
+        0.0 if sm_scale is None else sm_scale, k_scale, v_scale))
+    return out, lse

@@ -18,7 +18,9 @@ OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libpod_gb300.so")
 SOURCES = ["pod_k1_plain.cu", "pod_k1_lt.cu", "pod_k1_rope.cu", "pod_launch.cu", "pod_api.cu",
            "pod_planner.cpp", "pod_noalloc.cu", "pod_rope.cu", "pod_cache_io.cu",
-           "pod_tree_k16.cu", "pod_tree_k8.cu", "pod_tree_k8b.cu", "pod_tree_api.cu", "pod_tree_planner.cpp"]
+           "pod_tree_k16.cu", "pod_tree_k8.cu", "pod_tree_k8b.cu", "pod_tree_api.cu", "pod_tree_planner.cpp",
+           "pod_step.cu", "pod_select.cu", "pod_decode_16.cu", "pod_decode_scaled.cu", "pod_decode_block.cu",
+           "pod_decode_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,724 @@
+// pod_decode.cuh — attention of one token per request over its paged cache, with
+// lengths, block table and (optionally) selected pages on the device.
+//
+// Mathematics. For the G query heads of a KV head: x = s q.k over the visible keys,
+// p = 2^(x - m), l = sum p, o = sum p v / l. m is a reference that is at most 2^8
+// below the running maximum: it moves, and O with it, only when a logit passes it by
+// more than 8 (one vote a tile instead of shuffles for the maximum; the lag is a factor
+// that l and O share). Pieces of a request's keys join by their base-2 LSE. Over a
+// block-scaled cache O has a reference of its own, that of p * 2^(V's exponent).
+//
+// Layout. Both products run transposed, S^T = K Q^T and O^T = V^T P^T, as
+// mma.sync m16n8k16 with keys (then head elements) in the 16 rows and the query
+// heads of a KV head in the 8 columns: a decode step has few query heads, and this
+// wastes none of 8. (tcgen05 has 64 or 128 rows to fill, and the step reads each key
+// once: it is bound by memory.) The order of the reduced index is free in a product,
+// and so is that of the rows of O^T: so a lane takes 16 contiguous bytes of a key as
+// its elements of K's fragments, and of V's as rows, and K and V go from memory to the
+// matrix unit without shared memory in between. P^T changes from accumulator to operand by
+// movmatrix. P is carried in two 16-bit parts (off by 2^-17 of a weight in bf16, 2^-22 in
+// fp16): the matrix unit has time. Codes of FP8 caches are widened to fp16, exactly.
+//
+// Work split. The keys of every (KV head, request) are cut into units of one tile a
+// warp; the units of all, laid out head by head, are dealt to the CTAs of one
+// launch in equal runs. Every CTA finds its run from the lengths on the device, so
+// nothing is planned on the host and a captured launch serves later lengths. A
+// run's pieces of a request that is cut go to the workspace; the merge kernel joins them in
+// the order of the keys.
+#pragma once
+#include <math.h>
+
+#include "pod_decode.h"
+#include "pod_device.cuh"
+
+namespace pod {
+namespace {
+
+constexpr float kLag = 8.f;                        // log2 of how far m may lie below the maximum
+
+template <int D, int FMT, int NT>
+struct DecodeShape {
+  static constexpr int E = FMT == POD_KV_16BIT ? 2 : 1;           // bytes of an element
+  static constexpr int MT = FMT == POD_KV_16BIT ? (D == 64 ? 2 : 1) : (D == 64 ? 4 : D == 128 ? 2 : 1);
+  static constexpr int TK = 16 * MT;                              // keys of a warp's tile
+  static constexpr int U = TK * kDecodeWarps;                     // keys of a unit
+  static constexpr int HT = 8 * NT;                               // query heads of a tile
+  static constexpr int CK = 16 / E;                               // elements of a lane's chunk of K
+  static constexpr int NK = D / (4 * CK);                         // chunks of K a lane takes of a key
+  static constexpr int CV = D / 8 < CK ? D / 8 : CK;              // of V
+  static constexpr int NV = D / (8 * CV);
+  static constexpr int WV = CV * E / 4;                           // 32-bit words of a chunk of V
+  // Weights leave the exponential times 2^kUp: fp16's small weights keep their bits
+  // (2^(7 + kLag) is below its largest value), and sums of the largest bf16 values
+  // stay below fp32's.
+  static constexpr int IDX = (TK + 31) / 32;                      // tile keys of a lane
+};
+
+POD_DEV uint4 load16(const uint8_t* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+POD_DEV uint2 load8(const uint8_t* p) {
+  uint2 r;
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+  return r;
+}
+// 8 x 8 matrix of 16-bit values, a register's pair in row lane / 4: its transpose
+POD_DEV uint32_t turn8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+POD_DEV uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
+// 2^(byte - 127)
+POD_DEV float pow2_of(int byte) {
+  return byte == 0 ? 5.877471754111438e-39f : __uint_as_float((uint32_t)byte << 23);
+}
+
+// Keys of request r that the call reads, as indices v in [0, count): key first + v
+// of the cache, or slot v % ps of the selected page v / ps.
+struct Keys {
+  int len, first, count;
+};
+POD_DEV Keys keys_of(const DecodeParams& P, int r) {
+  Keys k;
+  k.len = min(max(P.lens[r], 0), P.width * P.ps);   // (the product is at most 2^30)
+  if (P.pages) {
+    k.first = 0;
+    k.count = min((k.len + P.ps - 1) / P.ps, P.num_selected) * P.ps;
+  } else {
+    k.first = P.window < 0 ? 0 : max(0, k.len - 1 - P.window);
+    k.count = k.len - k.first;
+  }
+  return k;
+}
+
+// LSE and output scale of a row under its sink: exp(sink) joins the denominator
+POD_DEV float sink_factor(float lse, float sink) {
+  const float s = sink * 1.4426950408889634f;
+  return s > lse ? ex2(lse - s) / (1.f + ex2(lse - s)) : 1.f / (1.f + ex2(s - lse));
+}
+
+template <typename T, int D>
+POD_DEV void store_row4(T* dst, float4 o) {
+  *reinterpret_cast<uint2*>(dst) = make_uint2(Pack<T>::two(o.x, o.y), Pack<T>::two(o.z, o.w));
+}
+
+template <typename T, int D, int FMT, int NT>
+__global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
+    decode_kernel(const __grid_constant__ DecodeParams P) {
+  using S = DecodeShape<D, FMT, NT>;
+  using M = typename std::conditional<FMT == POD_KV_16BIT, T, __half>::type;   // operands of the products
+  constexpr bool MBF = Pack<M>::kBF16;
+  constexpr float kUp = MBF ? -24.f : 7.f;
+  constexpr int MT = S::MT, TK = S::TK, HT = S::HT;
+  __shared__ float sh_o[kDecodeWarps][HT][D];
+  __shared__ float sh_m[3][kDecodeWarps][HT];
+  __shared__ long long sh_scan[kDecodeWarps + 2];
+  __shared__ int sh_row;
+
+  asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+
+  // ---- this CTA's run of units
+  long long total = 0;                             // units of a plane
+  for (int r = tid; r < P.batch; r += kDecodeThreads) total += (keys_of(P, r).count + S::U - 1) / S::U;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) sh_scan[warp] = total;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kDecodeWarps; ++w) total += sh_scan[w];
+  if (blockIdx.x == 0 && tid == 0) *P.total = total;
+  const long long all = total * P.planes, runs = min((long long)P.grid, all);
+  if (blockIdx.x >= runs) return;                  // (as many runs as units at most: none is empty)
+  long long u = all * blockIdx.x / runs;
+  const long long u_end = all * (blockIdx.x + 1) / runs, u_start = u;
+  int plane = (int)(u / total);
+  // the request of the first unit
+  long long at = u - (long long)plane * total;     // unit within the plane
+  long long before = 0;                            // units of the requests up to here
+  int row = 0;
+  for (int base = 0;; base += kDecodeThreads) {
+    const int r = base + tid;
+    const long long n = r < P.batch ? (keys_of(P, r).count + S::U - 1) / S::U : 0;
+    long long x = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();                               // (sh_scan is read above, and by the round before)
+    if (lane == 31) sh_scan[warp] = x;
+    if (tid == 0) sh_row = -1;
+    __syncthreads();
+    long long off = before;
+#pragma unroll
+    for (int w = 0; w < kDecodeWarps; ++w)
+      if (w < warp) off += sh_scan[w];
+    if (at >= off + x - n && at < off + x) {
+      sh_row = r;
+      sh_scan[kDecodeWarps] = off + x - n;
+    }
+#pragma unroll
+    for (int w = 0; w < kDecodeWarps; ++w) before += sh_scan[w];
+    __syncthreads();
+    if (sh_row >= 0 || base + kDecodeThreads >= P.batch) break;
+  }
+  row = sh_row;
+  long long row_first = sh_scan[kDecodeWarps];     // first unit of the request in its plane
+
+  // ---- segments: the units of one (plane, request)
+  while (u < u_end) {
+    const Keys K = keys_of(P, row);
+    const int units = (K.count + S::U - 1) / S::U;
+    if (units == 0) {                              // (an empty request: the merge kernel's)
+      if (++row == P.batch) { row = 0; row_first = 0; ++plane; }
+      continue;
+    }
+    const long long seg0 = (long long)plane * total + row_first;      // of the whole request
+    const int ua = (int)(u - seg0), ub = (int)min((long long)units, u_end - seg0);
+    const int v0 = ua * S::U, v1 = (int)min((long long)K.count, (long long)ub * S::U);
+    const int hk = plane % P.Hk, h0 = hk * P.G + plane / P.Hk * HT;
+    const int heads = min(HT, P.G - plane / P.Hk * HT);
+    if (tid == 0 && plane == 0 && ua == 0) P.first[row] = row_first;
+
+    // ---- Q as the columns of S^T, and the factor that takes a column to base-2 logits
+    uint32_t qf[NT][S::NK][S::CK / 2];
+    float xs[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int h = n * 8 + g;
+      const T* src = static_cast<const T*>(P.q) + (long long)row * P.q_stride + (long long)(h0 + h) * D;
+      uint32_t w[S::NK][S::CK / 2];
+#pragma unroll
+      for (int b = 0; b < S::NK; ++b)
+#pragma unroll
+        for (int c = 0; c < S::CK / 8; ++c) {
+          uint4 r = make_uint4(0, 0, 0, 0);
+          if (h < heads) r = *reinterpret_cast<const uint4*>(src + (b * 4 + t) * S::CK + c * 8);
+          w[b][4 * c] = r.x; w[b][4 * c + 1] = r.y; w[b][4 * c + 2] = r.z; w[b][4 * c + 3] = r.w;
+        }
+      if constexpr (FMT == POD_KV_16BIT) {
+        xs[n][0] = xs[n][1] = P.scale_log2;
+#pragma unroll
+        for (int b = 0; b < S::NK; ++b)
+#pragma unroll
+          for (int i = 0; i < S::CK / 2; ++i) qf[n][b][i] = w[b][i];
+      } else {
+        // fp16 operands: the row by the power of two that brings its largest element to
+        // [2^14, 2^15), so that bf16 rows keep all bits down to 2^-38 of it
+        float am = 0.f;
+#pragma unroll
+        for (int b = 0; b < S::NK; ++b)
+#pragma unroll
+          for (int i = 0; i < S::CK / 2; ++i) {
+            const float2 f = Pack<T>::unpack(w[b][i]);
+            am = fmaxf(am, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+        const int ex = (int)(__float_as_uint(am) >> 23) - 127;            // (-127: zeros and subnormals)
+        const int e = ex >= 128 ? 0 : min(14 - ex, 126);
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23), down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int b = 0; b < S::NK; ++b)
+#pragma unroll
+          for (int i = 0; i < S::CK / 2; ++i) {
+            const float2 f = Pack<T>::unpack(w[b][i]);
+            qf[n][b][i] = Pack<M>::two(f.x * up, f.y * up);
+          }
+        const float d0 = __shfl_sync(0xffffffffu, down, 8 * t), d1 = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+        xs[n][0] = d0 * P.scale_log2;
+        xs[n][1] = d1 * P.scale_log2;
+      }
+    }
+
+    float o[NT][S::NV][S::CV / 2][4], m[NT][2], mv[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int b = 0; b < S::NV; ++b)
+#pragma unroll
+        for (int i = 0; i < S::CV / 2; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[n][b][i][c] = 0.f;
+      m[n][0] = m[n][1] = mv[n][0] = mv[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+    }
+
+    // ---- addresses: rows of d elements; a key's K row is index * key_step + rows of the head
+    const long long row_bytes = (long long)D * S::E;
+    const long long key_step = P.hnd ? row_bytes : row_bytes * P.Hk;
+    const long long v_off = (long long)P.ps * P.Hk * row_bytes;
+    const uint8_t* kbase = P.cache + (P.hnd ? (long long)hk * P.ps : (long long)hk) * row_bytes;
+    const unsigned page_step = 2u * (unsigned)P.ps * (P.hnd ? (unsigned)P.Hk : 1u);
+    const int32_t* table = P.table + (long long)row * P.table_stride;
+    const int32_t* sel = P.pages ? P.pages + ((long long)row * P.Hk + hk) * P.num_selected : nullptr;
+
+    // Tile key i of a tile at v: its place in the table (stage 1), then its row (stage
+    // 2), each asked for a tile ahead of its use. 0xffffffff: not visible.
+    struct Place {
+      int page, in;
+    };
+    auto place = [&](int v) {
+      Place p;
+      p.page = -1;
+      p.in = 0;
+      if (v < v1) {
+        const int w = v + K.first, at_page = w / P.ps;
+        p.in = w - at_page * P.ps;
+        p.page = at_page;
+        if (sel) {
+          p.page = sel[at_page];
+          // (a page past the request's last, or a slot past its last key: not visible)
+          if (p.page >= 0 && (p.page >= P.width || p.page * P.ps + p.in >= K.len)) p.page = -1;
+        }
+      }
+      return p;
+    };
+    auto index_of = [&](Place p) {
+      if (p.page < 0) return 0xffffffffu;
+      const unsigned page = (unsigned)table[p.page];
+      if (page >= P.num_pages) {
+        if (P.status) atomicOr(P.status, kStatusSlot);
+        return 0xffffffffu;
+      }
+      return page * page_step + (unsigned)p.in;
+    };
+
+    uint4 kr[MT][2][S::NK];
+    uint32_t vr[MT][4][S::NV][S::WV];
+    unsigned idx[S::IDX];                          // rows of the tile in flight, lane i: key i
+    Place nxt[S::IDX];
+    auto load_k = [&](const unsigned* ix) {
+#pragma unroll
+      for (int s = 0; s < MT; ++s)
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          const unsigned i = __shfl_sync(0xffffffffu, ix[s / 2], (s & 1) * 16 + a * 8 + g);
+          const uint8_t* p = kbase + (long long)i * key_step + t * 16;
+#pragma unroll
+          for (int b = 0; b < S::NK; ++b) {
+            kr[s][a][b] = make_uint4(0, 0, 0, 0);
+            if (i != 0xffffffffu) kr[s][a][b] = load16(p + b * 64);
+          }
+        }
+    };
+    auto load_v = [&](const unsigned* ix) {
+#pragma unroll
+      for (int s = 0; s < MT; ++s)
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const unsigned i = __shfl_sync(0xffffffffu, ix[s / 2], (s & 1) * 16 + (a >> 1) * 8 + 2 * t + (a & 1));
+          const uint8_t* p = kbase + v_off + (long long)i * key_step + g * (S::WV * 4);
+#pragma unroll
+          for (int b = 0; b < S::NV; ++b) {
+            if constexpr (S::WV == 4) {
+              uint4 r = make_uint4(0, 0, 0, 0);
+              if (i != 0xffffffffu) r = load16(p + b * 128);
+              vr[s][a][b][0] = r.x; vr[s][a][b][1] = r.y; vr[s][a][b][2] = r.z; vr[s][a][b][3] = r.w;
+            } else {
+              uint2 r = make_uint2(0, 0);
+              if (i != 0xffffffffu) r = load8(p + b * 64);
+              vr[s][a][b][0] = r.x; vr[s][a][b][1] = r.y;
+            }
+          }
+        }
+    };
+    // exponent bytes of K (low) and V of the tile's keys, a lane's own
+    auto load_e = [&](const unsigned* ix, int* eb) {
+      if constexpr (FMT == POD_KV_E4M3_BLOCK) {
+#pragma unroll
+        for (int j = 0; j < S::IDX; ++j) {
+          eb[j] = 127 | 127 << 8;
+          if (ix[j] != 0xffffffffu) {
+            const uint8_t* p = P.scales + (P.hnd ? (long long)ix[j] + (long long)hk * P.ps : (long long)ix[j] * P.Hk + hk);
+            eb[j] = p[0] | p[(long long)P.ps * P.Hk] << 8;
+          }
+        }
+      }
+    };
+
+    int v = v0 + warp * TK;
+    int eb[S::IDX], eb_next[S::IDX];
+#pragma unroll
+    for (int j = 0; j < S::IDX; ++j) {
+      const bool mine = TK >= 32 || lane < TK;
+      idx[j] = index_of(mine ? place(v + j * 32 + lane) : Place{-1, 0});
+      nxt[j] = mine ? place(v + S::U + j * 32 + lane) : Place{-1, 0};
+    }
+    if (v < v1) {
+      load_k(idx);
+      load_e(idx, eb);
+      load_v(idx);
+    }
+    for (; v < v1; v += S::U) {
+      unsigned idx_next[S::IDX];
+#pragma unroll
+      for (int j = 0; j < S::IDX; ++j) {
+        const bool mine = TK >= 32 || lane < TK;
+        idx_next[j] = index_of(nxt[j]);
+        nxt[j] = mine ? place(v + 2 * S::U + j * 32 + lane) : Place{-1, 0};
+      }
+      // ---- S^T, a key a row (g, g + 8 of every 16), the heads 2t and 2t + 1 of every 8
+      float x[MT][NT][4];
+#pragma unroll
+      for (int s = 0; s < MT; ++s) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[s][n][c] = 0.f;
+#pragma unroll
+        for (int b = 0; b < S::NK; ++b) {
+          const uint32_t w0[4] = {kr[s][0][b].x, kr[s][0][b].y, kr[s][0][b].z, kr[s][0][b].w};
+          const uint32_t w1[4] = {kr[s][1][b].x, kr[s][1][b].y, kr[s][1][b].z, kr[s][1][b].w};
+          if constexpr (FMT == POD_KV_16BIT) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t a[4] = {w0[2 * i], w1[2 * i], w0[2 * i + 1], w1[2 * i + 1]};
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma16816<MBF>(x[s][n], a, qf[n][b][2 * i], qf[n][b][2 * i + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t a[4] = {e4m3x2_to<__half>((uint16_t)w0[i]), e4m3x2_to<__half>((uint16_t)w1[i]),
+                                     e4m3x2_to<__half>((uint16_t)(w0[i] >> 16)),
+                                     e4m3x2_to<__half>((uint16_t)(w1[i] >> 16))};
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma16816<MBF>(x[s][n], a, qf[n][b][2 * i], qf[n][b][2 * i + 1]);
+            }
+          }
+        }
+      }
+      load_k(idx_next);
+      load_e(idx_next, eb_next);
+      // ---- logits, the references, the weights
+      float xe[MT][2];                             // V's exponents of the lane's keys
+      bool past = false;
+#pragma unroll
+      for (int s = 0; s < MT; ++s)
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          const int src = (s & 1) * 16 + a * 8 + g;
+          const bool live = __shfl_sync(0xffffffffu, idx[s / 2], src) != 0xffffffffu;
+          float ks = 1.f;
+          xe[s][a] = 0.f;
+          if constexpr (FMT == POD_KV_E4M3_BLOCK) {
+            const int e = __shfl_sync(0xffffffffu, eb[s / 2], src);
+            ks = pow2_of(e & 255);
+            xe[s][a] = (float)((e >> 8) - 127);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float& y = x[s][n][2 * a + c];
+              if constexpr (FMT == POD_KV_E4M3_BLOCK) y = live ? y * ks * xs[n][c] : -INFINITY;
+              else y = live ? y * xs[n][c] : -INFINITY;
+              past |= y > m[n][c] + kLag;
+              if constexpr (FMT == POD_KV_E4M3_BLOCK) past |= y + xe[s][a] > mv[n][c] + kLag;
+            }
+        }
+      if (__any_sync(0xffffffffu, past)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float top = m[n][c], topv = mv[n][c];
+#pragma unroll
+            for (int s = 0; s < MT; ++s)
+#pragma unroll
+              for (int a = 0; a < 2; ++a) {
+                top = fmaxf(top, x[s][n][2 * a + c]);
+                if constexpr (FMT == POD_KV_E4M3_BLOCK) topv = fmaxf(topv, x[s][n][2 * a + c] + xe[s][a]);
+              }
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+              if constexpr (FMT == POD_KV_E4M3_BLOCK) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, d));
+            }
+            const float f = top == -INFINITY ? 1.f : ex2(m[n][c] - top);
+            m[n][c] = top;
+            l[n][c] *= f;
+            float fo = f;
+            if constexpr (FMT == POD_KV_E4M3_BLOCK) {
+              fo = topv == -INFINITY ? 1.f : ex2(mv[n][c] - topv);
+              mv[n][c] = topv;
+            }
+#pragma unroll
+            for (int b = 0; b < S::NV; ++b)
+#pragma unroll
+              for (int i = 0; i < S::CV / 2; ++i) {
+                o[n][b][i][c] *= fo;
+                o[n][b][i][2 + c] *= fo;
+              }
+          }
+      }
+      uint32_t ph[MT][NT][2], pl[MT][NT][2];       // P^T as operand: keys 2t.., 2t + 8..; head g
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float r0 = (m[n][0] == -INFINITY ? 0.f : m[n][0]) - kUp, r1 = (m[n][1] == -INFINITY ? 0.f : m[n][1]) - kUp;
+        float rv0 = r0, rv1 = r1;
+        if constexpr (FMT == POD_KV_E4M3_BLOCK) {
+          rv0 = (mv[n][0] == -INFINITY ? 0.f : mv[n][0]) - kUp;
+          rv1 = (mv[n][1] == -INFINITY ? 0.f : mv[n][1]) - kUp;
+        }
+#pragma unroll
+        for (int s = 0; s < MT; ++s)
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
+            float p0 = ex2(x[s][n][2 * a] - r0), p1 = ex2(x[s][n][2 * a + 1] - r1);
+            l[n][0] += p0;
+            l[n][1] += p1;
+            if constexpr (FMT == POD_KV_E4M3_BLOCK) {
+              p0 = ex2(x[s][n][2 * a] + xe[s][a] - rv0);
+              p1 = ex2(x[s][n][2 * a + 1] + xe[s][a] - rv1);
+            }
+            uint32_t hi, lo;
+            Pack<M>::split(p0, p1, hi, lo);
+            ph[s][n][a] = turn8x8(hi);
+            pl[s][n][a] = turn8x8(lo);
+          }
+      }
+      // ---- O^T += V^T P^T
+#pragma unroll
+      for (int s = 0; s < MT; ++s)
+#pragma unroll
+        for (int b = 0; b < S::NV; ++b)
+#pragma unroll
+          for (int w = 0; w < S::WV; ++w) {
+            const uint32_t v0w = vr[s][0][b][w], v1w = vr[s][1][b][w], v2w = vr[s][2][b][w], v3w = vr[s][3][b][w];
+            if constexpr (FMT == POD_KV_16BIT) {
+              const uint32_t a[4] = {prmt(v0w, v1w, 0x5410), prmt(v0w, v1w, 0x7632), prmt(v2w, v3w, 0x5410),
+                                     prmt(v2w, v3w, 0x7632)};
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                mma16816<MBF>(o[n][b][w], a, ph[s][n][0], ph[s][n][1]);
+                mma16816<MBF>(o[n][b][w], a, pl[s][n][0], pl[s][n][1]);
+              }
+            } else {
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const uint32_t lo = prmt(v0w, v1w, q ? 0x7362 : 0x5140), hi = prmt(v2w, v3w, q ? 0x7362 : 0x5140);
+                const uint32_t a[4] = {e4m3x2_to<__half>((uint16_t)lo), e4m3x2_to<__half>((uint16_t)(lo >> 16)),
+                                       e4m3x2_to<__half>((uint16_t)hi), e4m3x2_to<__half>((uint16_t)(hi >> 16))};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  mma16816<MBF>(o[n][b][2 * w + q], a, ph[s][n][0], ph[s][n][1]);
+                  mma16816<MBF>(o[n][b][2 * w + q], a, pl[s][n][0], pl[s][n][1]);
+                }
+              }
+            }
+          }
+      load_v(idx_next);
+#pragma unroll
+      for (int j = 0; j < S::IDX; ++j) {
+        idx[j] = idx_next[j];
+        eb[j] = eb_next[j];
+      }
+    }
+
+    // ---- the warps' sums join
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], d);
+        if (g == 0) {
+          const int h = n * 8 + 2 * t + c;
+          sh_m[0][warp][h] = m[n][c];
+          sh_m[1][warp][h] = l[n][c];
+          sh_m[2][warp][h] = FMT == POD_KV_E4M3_BLOCK ? mv[n][c] : m[n][c];
+        }
+      }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float* dst = sh_o[warp][n * 8 + 2 * t + c];
+#pragma unroll
+        for (int b = 0; b < S::NV; ++b)
+#pragma unroll
+          for (int i = 0; i < S::CV / 4; ++i)
+            *reinterpret_cast<float4*>(dst + (b * 8 + g) * S::CV + 4 * i) =
+                make_float4(o[n][b][2 * i][c], o[n][b][2 * i][2 + c], o[n][b][2 * i + 1][c], o[n][b][2 * i + 1][2 + c]);
+      }
+    __syncthreads();
+    const bool whole = ua == 0 && ub == units;
+    const int slot = (int)blockIdx.x * 2 + (u == u_start ? 0 : 1);
+    for (int i = tid; i < heads * (D / 4); i += kDecodeThreads) {
+      const int h = i / (D / 4), c4 = i - h * (D / 4);
+      float top = -INFINITY, topv = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kDecodeWarps; ++w) {
+        top = fmaxf(top, sh_m[0][w][h]);
+        topv = fmaxf(topv, sh_m[2][w][h]);
+      }
+      const float z = top == -INFINITY ? 0.f : top, zv = topv == -INFINITY ? 0.f : topv;
+      float sum = 0.f;
+      float4 acc = make_float4(0, 0, 0, 0);
+#pragma unroll
+      for (int w = 0; w < kDecodeWarps; ++w) {
+        const float f = ex2(sh_m[0][w][h] - z), fv = ex2(sh_m[2][w][h] - zv);
+        const float4 p = *reinterpret_cast<const float4*>(&sh_o[w][h][4 * c4]);
+        sum += sh_m[1][w][h] * f;
+        acc.x += p.x * fv; acc.y += p.y * fv; acc.z += p.z * fv; acc.w += p.w * fv;
+      }
+      // (sum == 0: no visible key; a NaN stays one)
+      const float lse = sum == 0.f ? -INFINITY : z + log2f(sum) - kUp;
+      float f = sum == 0.f ? 0.f : P.v_scale / sum;
+      if (whole && P.sinks && sum != 0.f) f *= sink_factor(lse, P.sinks[h0 + h]);
+      acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+      if constexpr (FMT == POD_KV_E4M3_BLOCK) {
+        const float back = ex2(zv - z);            // O's own reference
+        acc.x *= back; acc.y *= back; acc.z *= back; acc.w *= back;
+      }
+      if (whole) {
+        store_row4<T, D>(static_cast<T*>(P.out) + (long long)row * P.out_stride + (long long)(h0 + h) * D + 4 * c4, acc);
+        if (c4 == 0 && P.lse) P.lse[(long long)row * P.H + h0 + h] = lse;
+      } else {
+        *reinterpret_cast<float4*>(P.piece_o + ((long long)slot * HT + h) * D + 4 * c4) = acc;
+        if (c4 == 0) P.piece_lse[slot * HT + h] = lse;
+      }
+    }
+    __syncthreads();                               // (the buffers are the next segment's)
+    u = seg0 + ub;
+    row_first += units;
+    if (++row == P.batch) { row = 0; row_first = 0; ++plane; }
+  }
+}
+
+// Rows whose keys were cut: the pieces in the order of the keys, weighted by
+// 2^(lse - M). Rows without keys: 0 and -inf. WPR warps work on a (request, head).
+template <typename T, int D, int HT, int UNIT, int WPR>
+__global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant__ DecodeParams P) {
+  constexpr int PL = D / 32 < 4 ? D / 32 : 4, NP = D / (32 * PL);      // elements and chunks of a lane
+  __shared__ float sh[WPR > 1 ? WPR : 1][D];
+  __shared__ float sh_w[WPR > 1 ? WPR : 1][2];
+  asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long item = WPR > 1 ? (long long)blockIdx.x : (long long)blockIdx.x * 4 + warp;
+  if (item >= (long long)P.batch * P.H) return;    // (uniform over the block where its warps meet)
+  const int row = (int)(item / P.H), head = (int)(item - (long long)row * P.H);
+  const Keys K = keys_of(P, row);
+  const int units = (K.count + UNIT - 1) / UNIT;
+  T* out = static_cast<T*>(P.out) + (long long)row * P.out_stride + (long long)head * D;
+  if (head == 0 && (threadIdx.x & (WPR * 32 - 1)) == 0 && P.status && P.lens[row] != K.len) atomicOr(P.status, kStatusSlot);
+  if (units == 0) {
+    if (WPR > 1 && warp) return;
+#pragma unroll
+    for (int j = 0; j < NP; ++j)
+#pragma unroll
+      for (int e = 0; e < PL; e += 2)
+        *reinterpret_cast<uint32_t*>(out + (j * 32 + lane) * PL + e) = 0u;
+    if (lane == 0 && P.lse) P.lse[item] = -INFINITY;
+    return;
+  }
+  const int hk = head / P.G, gh = head - hk * P.G, h = gh % HT;
+  const long long plane = (long long)(gh / HT) * P.Hk + hk, total = *P.total, all = total * P.planes;
+  const long long runs = min((long long)P.grid, all);
+  const long long g0 = plane * total + P.first[row], g1 = g0 + units;
+  const int c0 = (int)(((g0 + 1) * runs - 1) / all), c1 = (int)((g1 * runs - 1) / all);   // CTAs of the first and last unit
+  if (c0 == c1) return;                            // written whole
+  const int w0 = WPR > 1 ? warp : 0;
+  float top = -INFINITY, sum = 0.f;
+  float acc[NP][PL];
+#pragma unroll
+  for (int j = 0; j < NP; ++j)
+#pragma unroll
+    for (int e = 0; e < PL; ++e) acc[j][e] = 0.f;
+  // the largest LSE first (its loads all at once), then the weighted sum
+  auto slot_of = [&](int c) { return c > c0 || all * c / runs == g0 ? 2 * c : 2 * c + 1; };
+  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, P.piece_lse[(long long)slot_of(c) * HT + h]);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const float z = top == -INFINITY ? 0.f : top;
+#pragma unroll 4
+  for (int c = c0 + w0; c <= c1; c += WPR) {
+    const long long s = (long long)slot_of(c) * HT + h;
+    const float f = ex2(P.piece_lse[s] - z);
+    sum += f;
+    const float* src = P.piece_o + s * D;
+#pragma unroll
+    for (int j = 0; j < NP; ++j)
+#pragma unroll
+      for (int e = 0; e < PL; ++e) acc[j][e] += src[(j * 32 + lane) * PL + e] * f;
+  }
+  if constexpr (WPR > 1) {
+#pragma unroll
+    for (int j = 0; j < NP; ++j)
+#pragma unroll
+      for (int e = 0; e < PL; ++e) sh[warp][(j * 32 + lane) * PL + e] = acc[j][e];
+    if (lane == 0) sh_w[warp][0] = sum;
+    __syncthreads();
+    if (warp) return;
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) sum += sh_w[w][0];
+#pragma unroll
+    for (int j = 0; j < NP; ++j)
+#pragma unroll
+      for (int e = 0; e < PL; ++e) {
+        acc[j][e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < WPR; ++w) acc[j][e] += sh[w][(j * 32 + lane) * PL + e];
+      }
+  }
+  const float lse = sum == 0.f ? -INFINITY : z + log2f(sum);
+  float f = sum == 0.f ? 0.f : 1.f / sum;
+  if (P.sinks && sum != 0.f) f *= sink_factor(lse, P.sinks[head]);
+#pragma unroll
+  for (int j = 0; j < NP; ++j)
+#pragma unroll
+    for (int e = 0; e < PL; e += 2)
+      *reinterpret_cast<uint32_t*>(out + (j * 32 + lane) * PL + e) = Pack<T>::two(acc[j][e] * f, acc[j][e + 1] * f);
+  if (lane == 0 && P.lse) P.lse[item] = lse;
+}
+
+template <typename... A, typename... B>
+cudaError_t launch_beside(void (*kernel)(A...), unsigned grid, unsigned threads, cudaStream_t st, const B&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename T, int D, int FMT, int NT>
+cudaError_t launch_decode_nt(DecodeParams& P, cudaStream_t st) {
+  using S = DecodeShape<D, FMT, NT>;
+  const int tiles = (P.G + S::HT - 1) / S::HT;
+  P.planes = P.Hk * tiles;
+  constexpr int per_sm = (D == 256 || NT == 2) ? 2 : 3;
+  P.grid = 152 * per_sm;
+  cudaError_t e = launch_beside(decode_kernel<T, D, FMT, NT>, (unsigned)P.grid, kDecodeThreads, st, P);
+  if (e != cudaSuccess) return e;
+  // a warp for each (request, head), or a block of four where a row may have many pieces
+  const long long items = (long long)P.batch * P.H;
+  if (items <= 2048) return launch_beside(decode_merge_kernel<T, D, S::HT, S::U, 4>, (unsigned)items, 128, st, P);
+  return launch_beside(decode_merge_kernel<T, D, S::HT, S::U, 1>, (unsigned)((items + 3) / 4), 128, st, P);
+}
+
+template <typename T, int FMT>
+cudaError_t launch_decode(int d, DecodeParams& P, cudaStream_t st) {
+  const bool wide = P.G > 8;
+  switch (d) {
+    case 64: return wide ? launch_decode_nt<T, 64, FMT, 2>(P, st) : launch_decode_nt<T, 64, FMT, 1>(P, st);
+    case 128: return wide ? launch_decode_nt<T, 128, FMT, 2>(P, st) : launch_decode_nt<T, 128, FMT, 1>(P, st);
+    default: return launch_decode_nt<T, 256, FMT, 1>(P, st);   // (O of 16 heads would not fit the registers)
+  }
+}
+
+}  // namespace
+}  // namespace pod

@@ -1,0 +1,315 @@
+// pod_step.cu — the start of a decode step whose tables live on the device: pages
+// taken from and returned to a free stack, positions and slots of the new tokens,
+// the page table end to end.
+//
+// Mathematics. A request with L keys that gets n more needs
+// ceil((L + n) / ps) - ceil(L / ps) pages; prefix sums over the requests give
+// every one its place on the stack, in the rows and in the page table. The sums
+// are 64 bits wide, so no lengths can wrap them.
+//
+// Work split. The prefix sums depend on all requests, so one block makes them, a thread
+// a request (in rounds past its threads), and moves the pages, a warp a request. Where
+// the step may have many rows, or the page table is asked for, a second kernel
+// of many blocks writes them (a thread an entry, which finds its request by bisection
+// of the offsets); otherwise the first block does it too and the launch is spared.
+// Bound by latency: a chain of some ten trips to L2 and as many block barriers.
+#include <cuda_runtime.h>
+#include <limits.h>
+
+#include <string>
+
+#include "../../include/pod.h"
+#include "pod_decode.h"
+#include "pod_device.cuh"
+
+void pod_set_last_error(const std::string& msg);
+
+using namespace pod;
+
+namespace {
+
+constexpr int kStepThreads = 1024;
+constexpr int kRowThreads = 256;
+
+struct StepParams {
+  int32_t* table;
+  const int32_t* lens;
+  const int32_t* news;
+  int32_t* lens_out;
+  int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* free_count_out;
+  int32_t* q_indptr;
+  int32_t* requests;
+  int32_t* positions;
+  int64_t* slots;
+  int32_t* kv_indptr;
+  int32_t* kv_indices;
+  int32_t* last_page_len;
+  int32_t* status;
+  long long table_stride;
+  int batch, width, ps, capacity, max_rows, max_pages, rows_here;
+};
+
+// Sum of x over the threads before this one, and over all of them.
+POD_DEV long long block_scan(long long x, long long& all, long long* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  long long s = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  __syncthreads();                                 // (sh may still be read)
+  if (lane == 31) sh[warp] = s;
+  __syncthreads();
+  const long long w = lane < warps ? sh[lane] : 0;
+  long long t = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, t, o);
+    if (lane >= o) t += y;
+  }
+  all = __shfl_sync(0xffffffffu, t, 31);
+  return s - x + (warp ? __shfl_sync(0xffffffffu, t, (warp + 31) & 31) : 0);
+}
+
+struct Step {
+  int had, has;                                    // pages before and after
+  long long old, now;                              // keys
+  bool wants;                                      // grows
+  int status;                                      // bits for a length out of range, or past its row
+};
+POD_DEV Step step_of(const StepParams& P, int r) {
+  Step s;
+  const long long most = (long long)P.width * P.ps;
+  const int len = P.lens[r], n = P.news[r];
+  s.old = min(max((long long)len, 0ll), most);
+  s.status = len != s.old ? kStatusSlot : 0;
+  s.now = max(0ll, s.old + n);
+  s.wants = n > 0;
+  if (s.now > most) {
+    s.wants = false;
+    s.status |= kStatusNoRoom;
+    s.now = s.old;
+  }
+  s.had = (int)((s.old + P.ps - 1) / P.ps);
+  s.has = (int)((s.now + P.ps - 1) / P.ps);
+  return s;
+}
+
+// last i with at[i] <= x (at ascending from 0; x < at[n])
+POD_DEV int find_row(const int32_t* at, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (at[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+POD_DEV void write_row(const StepParams& P, int i, int rows, const int32_t* indptr, const int32_t* lens_out) {
+  int req = -1, pos = 0;
+  long long slot = -1;
+  if (i < rows) {
+    req = find_row(indptr, P.batch, i);
+    pos = lens_out[req] - (indptr[req + 1] - i);
+    const int at = pos / P.ps, page = P.table[req * P.table_stride + at];
+    if (page >= 0) slot = (long long)page * P.ps + (pos - at * P.ps);
+  }
+  P.requests[i] = req;
+  P.positions[i] = pos;
+  P.slots[i] = slot;
+}
+
+__global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constant__ StepParams P) {
+  __shared__ long long sh[32];
+  __shared__ long long sh_off[kStepThreads];
+  __shared__ int sh_n[kStepThreads], sh_first[kStepThreads];
+  asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x;
+  const long long count = min(max((long long)*P.free_count, 0ll), (long long)P.capacity);
+  int bad = 0;                                     // status bits
+  // ---- pages of shrinking requests go onto the stack
+  long long given = 0;
+  for (int base = 0; base < P.batch; base += T) {
+    const int r = base + tid;
+    int n = 0, first = 0;
+    if (r < P.batch) {
+      const Step s = step_of(P, r);
+      n = max(0, s.had - s.has);
+      first = s.has;
+    }
+    if (!__syncthreads_or(n)) continue;            // (most steps take nothing back)
+    long long all;
+    const long long off = given + block_scan(n, all, sh);
+    sh_off[tid] = off;
+    sh_n[tid] = n;
+    sh_first[tid] = first;
+    __syncwarp();                                  // a warp moves its own lanes' requests
+    for (unsigned m = __ballot_sync(0xffffffffu, n > 0); m; m &= m - 1) {
+      const int k = warp * 32 + __ffs(m) - 1;
+      const int32_t* src = P.table + (long long)(base + k) * P.table_stride + sh_first[k];
+      for (int i = lane; i < sh_n[k]; i += 32) {
+        const long long to = count + sh_off[k] + i;
+        if (to < P.capacity) P.free_pages[to] = src[i];
+        else bad |= kStatusNoRoom;
+      }
+    }
+    given += all;
+  }
+  const long long top = min(count + given, (long long)P.capacity);
+  // ---- growing requests take theirs off its top (pages pushed above are seen behind
+  // the barriers of the scans)
+  long long pages = 0, rows = 0, kv = 0, pages_taken = 0, rows_taken = 0;
+  for (int base = 0; base < P.batch; base += T) {
+    const int r = base + tid;
+    Step s = {};
+    if (r < P.batch) s = step_of(P, r);
+    bad |= s.status;
+    const int need = s.wants ? s.has - s.had : 0;
+    const long long n = s.wants ? s.now - s.old : 0;
+    long long all_pages, all_rows, all_kv, taken;
+    const long long p0 = pages + block_scan(need, all_pages, sh);
+    const long long r0 = rows + block_scan(n, all_rows, sh);
+    const bool granted = s.wants && p0 + need <= top && r0 + n <= P.max_rows;
+    if (s.wants && !granted) {
+      bad |= kStatusNoRoom;
+      s.now = s.old;
+      s.has = s.had;
+    }
+    // (the granted ones come before every refused one)
+    block_scan(granted ? need : 0, taken, sh);
+    pages_taken += taken;
+    block_scan(granted ? n : 0, taken, sh);
+    rows_taken += taken;
+    const long long k0 = kv + block_scan(r < P.batch ? s.has : 0, all_kv, sh);
+    if (r < P.batch) {
+      P.lens_out[r] = (int)s.now;
+      P.q_indptr[r + 1] = (int)min(r0 + n, rows_taken);
+      if (P.kv_indptr) {
+        P.kv_indptr[r + 1] = (int)min(k0 + s.has, (long long)INT_MAX);
+        P.last_page_len[r] = s.now ? (int)((s.now - 1) % P.ps) + 1 : 0;
+      }
+    }
+    sh_off[tid] = top - 1 - p0;
+    sh_n[tid] = need;
+    sh_first[tid] = s.had;
+    __syncwarp();
+    for (unsigned m = __ballot_sync(0xffffffffu, granted && need > 0); m; m &= m - 1) {
+      const int k = warp * 32 + __ffs(m) - 1;
+      int32_t* dst = P.table + (long long)(base + k) * P.table_stride + sh_first[k];
+      for (int i = lane; i < sh_n[k]; i += 32) dst[i] = P.free_pages[sh_off[k] - i];
+    }
+    pages += all_pages;
+    rows += all_rows;
+    kv += all_kv;
+    __syncwarp();
+  }
+  if (P.kv_indptr && kv > P.max_pages) bad |= kStatusNoRoom;
+  if (tid == 0) {
+    *P.free_count_out = (int)(top - pages_taken);
+    P.q_indptr[0] = 0;
+    if (P.kv_indptr) P.kv_indptr[0] = 0;
+  }
+  if (__syncthreads_or(bad) && P.status) {          // (the rows below read what the block wrote above)
+    const int bits = __reduce_or_sync(0xffffffffu, bad);
+    if (lane == 0 && bits) atomicOr(P.status, bits);
+  }
+  if (P.rows_here)
+    for (int i = tid; i < P.max_rows; i += T) write_row(P, i, (int)rows_taken, P.q_indptr, P.lens_out);
+}
+
+// rows first, then entries of the page table
+__global__ void __launch_bounds__(kRowThreads) step_rows_kernel(const __grid_constant__ StepParams P) {
+  asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+  const long long stride = (long long)gridDim.x * kRowThreads, n = (long long)P.max_rows + (P.kv_indptr ? P.max_pages : 0);
+  const int rows = P.q_indptr[P.batch], pages = P.kv_indptr ? P.kv_indptr[P.batch] : 0;
+  for (long long i = (long long)blockIdx.x * kRowThreads + threadIdx.x; i < n; i += stride) {
+    if (i < P.max_rows) {
+      write_row(P, (int)i, rows, P.q_indptr, P.lens_out);
+    } else {
+      const int j = (int)(i - P.max_rows);
+      int page = -1;
+      if (j < pages) {
+        const int r = find_row(P.kv_indptr, P.batch, j);
+        page = P.table[r * P.table_stride + j - P.kv_indptr[r]];
+      }
+      P.kv_indices[j] = page;
+    }
+  }
+}
+
+pod_status fail(pod_status code, const std::string& msg) {
+  pod_set_last_error(msg);
+  return code;
+}
+
+template <typename... A, typename... B>
+cudaError_t launch_beside(void (*kernel)(A...), unsigned grid, unsigned threads, cudaStream_t st, const B&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace
+
+extern "C" pod_status pod_step_tables(const pod_step_args* a, void* stream) {
+  pod_set_last_error("");
+  if (!a) return fail(POD_ERR_INVALID_ARG, "args is NULL");
+  if (a->batch < 0 || a->max_rows < 0 || a->max_pages < 0 || a->free_capacity < 0)
+    return fail(POD_ERR_INVALID_ARG, "batch, max_rows, max_pages and free_capacity must not be negative");
+  if (a->page_size < 1 || a->table_width < 1 || (int64_t)a->table_width * a->page_size > (1 << 30))
+    return fail(POD_ERR_INVALID_ARG, "table_width and page_size must be positive, their product at most 2^30");
+  if (a->batch > 1 && a->table_stride < a->table_width)
+    return fail(POD_ERR_INVALID_ARG, "table_stride must hold table_width entries");
+  if (!a->free_count || !a->free_count_out || !a->q_indptr ||
+      (a->batch && (!a->block_table || !a->kv_lens || !a->new_lens || !a->kv_lens_out)) ||
+      (a->free_capacity && !a->free_pages) || (a->max_rows && (!a->requests || !a->positions || !a->slots)))
+    return fail(POD_ERR_INVALID_ARG, "an array is NULL");
+  if (!a->kv_indptr != !a->last_page_len || (a->kv_indptr && a->max_pages && !a->kv_indices))
+    return fail(POD_ERR_INVALID_ARG, "kv_indptr, kv_indices and last_page_len come together");
+  StepParams P = {};
+  P.table = a->block_table;
+  P.lens = a->kv_lens;
+  P.news = a->new_lens;
+  P.lens_out = a->kv_lens_out;
+  P.free_pages = a->free_pages;
+  P.free_count = a->free_count;
+  P.free_count_out = a->free_count_out;
+  P.q_indptr = a->q_indptr;
+  P.requests = a->requests;
+  P.positions = a->positions;
+  P.slots = a->slots;
+  P.kv_indptr = a->kv_indptr;
+  P.kv_indices = a->kv_indices;
+  P.last_page_len = a->last_page_len;
+  P.status = a->status;
+  P.table_stride = a->table_stride;
+  P.batch = a->batch;
+  P.width = a->table_width;
+  P.ps = a->page_size;
+  P.capacity = a->free_capacity;
+  P.max_rows = a->max_rows;
+  P.max_pages = a->max_pages;
+  // few rows: the first block writes them, a few each thread
+  P.rows_here = !a->kv_indptr && a->max_rows <= 2 * kStepThreads;
+  cudaStream_t st = (cudaStream_t)stream;
+  const int threads = a->batch <= 128 ? 128 : a->batch >= kStepThreads ? kStepThreads : (a->batch + 31) / 32 * 32;
+  cudaError_t e = launch_beside(step_kernel, 1, (unsigned)threads, st, P);
+  const int64_t entries = (int64_t)a->max_rows + (a->kv_indptr ? a->max_pages : 0);
+  if (e == cudaSuccess && !P.rows_here && entries) {
+    const int64_t blocks = (entries + kRowThreads - 1) / kRowThreads;
+    e = launch_beside(step_rows_kernel, (unsigned)(blocks < 152 * 8 ? blocks : 152 * 8), kRowThreads, st, P);
+  }
+  if (e != cudaSuccess) return fail(POD_ERR_CUDA, std::string("step tables launch: ") + cudaGetErrorString(e));
+  return POD_OK;
+}
