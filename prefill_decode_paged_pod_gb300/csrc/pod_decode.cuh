@@ -26,6 +26,7 @@
 // run's pieces of a request that is cut go to the workspace; the merge kernel joins them in
 // the order of the keys.
 #pragma once
+#include <limits.h>
 #include <math.h>
 
 #include "pod_decode.h"
@@ -34,6 +35,7 @@
 namespace pod {
 namespace {
 
+constexpr int kShortUnits = 4;                     // units of a CTA of the kernel for short rows
 constexpr float kLag = 8.f;                        // log2 of how far m may lie below the maximum
 
 template <int D, int FMT, int NT>
@@ -48,9 +50,6 @@ struct DecodeShape {
   static constexpr int CV = D / 8 < CK ? D / 8 : CK;              // of V
   static constexpr int NV = D / (8 * CV);
   static constexpr int WV = CV * E / 4;                           // 32-bit words of a chunk of V
-  // Weights leave the exponential times 2^kUp: fp16's small weights keep their bits
-  // (2^(7 + kLag) is below its largest value), and sums of the largest bf16 values
-  // stay below fp32's.
   static constexpr int IDX = (TK + 31) / 32;                      // tile keys of a lane
 };
 
@@ -77,6 +76,14 @@ POD_DEV float pow2_of(int byte) {
   return byte == 0 ? 5.877471754111438e-39f : __uint_as_float((uint32_t)byte << 23);
 }
 
+// Weights leave the exponential times 2^this: fp16's small weights keep their bits
+// (2^(7 + kLag) is below its largest value), and sums of the largest bf16 values stay
+// below fp32's.
+template <typename T, int FMT>
+constexpr float weight_up() {
+  return FMT == POD_KV_16BIT && Pack<T>::kBF16 ? -24.f : 7.f;
+}
+
 // Keys of request r that the call reads, as indices v in [0, count): key first + v
 // of the cache, or slot v % ps of the selected page v / ps.
 struct Keys {
@@ -101,26 +108,464 @@ POD_DEV float sink_factor(float lse, float sink) {
   return s > lse ? ex2(lse - s) / (1.f + ex2(lse - s)) : 1.f / (1.f + ex2(s - lse));
 }
 
-template <typename T, int D>
-POD_DEV void store_row4(T* dst, float4 o) {
+// What the four warps of a CTA leave in shared memory: sums under references of their own.
+template <int D, int HT>
+struct alignas(16) DecodeShared {
+  float o[kDecodeWarps][HT][D];
+  float m[3][kDecodeWarps][HT];    // m, l, and O's reference
+};
+
+template <int D, int HT>
+POD_DEV int offsetof_m(int what, int w, int h) {
+  return (kDecodeWarps * HT * D + (what * kDecodeWarps + w) * HT + h) * 4;
+}
+
+// Keys v0 to v1 of a request, for `heads` query heads from h0 on, dealt to the warps tile by tile.
+template <typename T, int D, int FMT, int NT>
+POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h0, int heads, int v0, int v1,
+                    DecodeShared<D, 8 * NT>& sh) {
+  using S = DecodeShape<D, FMT, NT>;
+  using M = typename std::conditional<FMT == POD_KV_16BIT, T, __half>::type;   // operands of the products
+  constexpr bool MBF = Pack<M>::kBF16;
+  constexpr float kUp = weight_up<T, FMT>();
+  constexpr int MT = S::MT, TK = S::TK;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  // ---- Q as the columns of S^T, and the factor that takes a column to base-2 logits
+  uint32_t qf[NT][S::NK][S::CK / 2];
+  float xs[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int h = n * 8 + g;
+    const T* src = static_cast<const T*>(P.q) + (long long)row * P.q_stride + (long long)(h0 + h) * D;
+    uint32_t w[S::NK][S::CK / 2];
+#pragma unroll
+    for (int b = 0; b < S::NK; ++b)
+#pragma unroll
+      for (int c = 0; c < S::CK / 8; ++c) {
+        uint4 r = make_uint4(0, 0, 0, 0);
+        if (h < heads) r = *reinterpret_cast<const uint4*>(src + (b * 4 + t) * S::CK + c * 8);
+        w[b][4 * c] = r.x; w[b][4 * c + 1] = r.y; w[b][4 * c + 2] = r.z; w[b][4 * c + 3] = r.w;
+      }
+    if constexpr (FMT == POD_KV_16BIT) {
+      xs[n][0] = xs[n][1] = P.scale_log2;
+#pragma unroll
+      for (int b = 0; b < S::NK; ++b)
+#pragma unroll
+        for (int i = 0; i < S::CK / 2; ++i) qf[n][b][i] = w[b][i];
+    } else {
+      // fp16 operands: the row by the power of two that brings its largest element to
+      // [2^14, 2^15), so that bf16 rows keep all bits down to 2^-38 of it
+      float am = 0.f;
+#pragma unroll
+      for (int b = 0; b < S::NK; ++b)
+#pragma unroll
+        for (int i = 0; i < S::CK / 2; ++i) {
+          const float2 f = Pack<T>::unpack(w[b][i]);
+          am = fmaxf(am, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+      am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+      const int ex = (int)(__float_as_uint(am) >> 23) - 127;            // (-127: zeros and subnormals)
+      const int e = ex >= 128 ? 0 : min(14 - ex, 126);
+      const float up = __uint_as_float((uint32_t)(127 + e) << 23), down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+      for (int b = 0; b < S::NK; ++b)
+#pragma unroll
+        for (int i = 0; i < S::CK / 2; ++i) {
+          const float2 f = Pack<T>::unpack(w[b][i]);
+          qf[n][b][i] = Pack<M>::two(f.x * up, f.y * up);
+        }
+      const float d0 = __shfl_sync(0xffffffffu, down, 8 * t), d1 = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+      xs[n][0] = d0 * P.scale_log2;
+      xs[n][1] = d1 * P.scale_log2;
+    }
+  }
+
+  float o[NT][S::NV][S::CV / 2][4], m[NT][2], mv[NT][2], l[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int b = 0; b < S::NV; ++b)
+#pragma unroll
+      for (int i = 0; i < S::CV / 2; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[n][b][i][c] = 0.f;
+    m[n][0] = m[n][1] = mv[n][0] = mv[n][1] = -INFINITY;
+    l[n][0] = l[n][1] = 0.f;
+  }
+
+  // ---- addresses: rows of d elements; a key's K row is index * key_step + rows of the head
+  const long long row_bytes = (long long)D * S::E;
+  const long long key_step = P.hnd ? row_bytes : row_bytes * P.Hk;
+  const long long v_off = (long long)P.ps * P.Hk * row_bytes;
+  const uint8_t* kbase = P.cache + (P.hnd ? (long long)hk * P.ps : (long long)hk) * row_bytes;
+  const unsigned page_step = 2u * (unsigned)P.ps * (P.hnd ? (unsigned)P.Hk : 1u);
+  const int32_t* table = P.table + (long long)row * P.table_stride;
+  const int32_t* sel = P.pages ? P.pages + ((long long)row * P.Hk + hk) * P.num_selected : nullptr;
+
+  // Tile key i of a tile at v: its place in the table (stage 1), then its row (stage
+  // 2), each asked for a tile ahead of its use. 0xffffffff: not visible.
+  struct Place {
+    int page, in;
+  };
+  auto place = [&](int v) {
+    Place p;
+    p.page = -1;
+    p.in = 0;
+    if (v < v1) {
+      const int w = v + K.first, at_page = w / P.ps;
+      p.in = w - at_page * P.ps;
+      p.page = at_page;
+      if (sel) {
+        p.page = sel[at_page];
+        // (a page past the request's last, or a slot past its last key: not visible)
+        if (p.page >= 0 && (p.page >= P.width || p.page * P.ps + p.in >= K.len)) p.page = -1;
+      }
+    }
+    return p;
+  };
+  auto index_of = [&](Place p) {
+    if (p.page < 0) return 0xffffffffu;
+    const unsigned page = (unsigned)table[p.page];
+    if (page >= P.num_pages) {
+      if (P.status) atomicOr(P.status, kStatusSlot);
+      return 0xffffffffu;
+    }
+    return page * page_step + (unsigned)p.in;
+  };
+
+  uint4 kr[MT][2][S::NK];
+  uint32_t vr[MT][4][S::NV][S::WV];
+  unsigned idx[S::IDX];                          // rows of the tile in flight, lane i: key i
+  Place nxt[S::IDX];
+  auto load_k = [&](const unsigned* ix) {
+#pragma unroll
+    for (int s = 0; s < MT; ++s)
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const unsigned i = __shfl_sync(0xffffffffu, ix[s / 2], (s & 1) * 16 + a * 8 + g);
+        const uint8_t* p = kbase + (long long)i * key_step + t * 16;
+#pragma unroll
+        for (int b = 0; b < S::NK; ++b) {
+          kr[s][a][b] = make_uint4(0, 0, 0, 0);
+          if (i != 0xffffffffu) kr[s][a][b] = load16(p + b * 64);
+        }
+      }
+  };
+  auto load_v = [&](const unsigned* ix) {
+#pragma unroll
+    for (int s = 0; s < MT; ++s)
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const unsigned i = __shfl_sync(0xffffffffu, ix[s / 2], (s & 1) * 16 + (a >> 1) * 8 + 2 * t + (a & 1));
+        const uint8_t* p = kbase + v_off + (long long)i * key_step + g * (S::WV * 4);
+#pragma unroll
+        for (int b = 0; b < S::NV; ++b) {
+          if constexpr (S::WV == 4) {
+            uint4 r = make_uint4(0, 0, 0, 0);
+            if (i != 0xffffffffu) r = load16(p + b * 128);
+            vr[s][a][b][0] = r.x; vr[s][a][b][1] = r.y; vr[s][a][b][2] = r.z; vr[s][a][b][3] = r.w;
+          } else {
+            uint2 r = make_uint2(0, 0);
+            if (i != 0xffffffffu) r = load8(p + b * 64);
+            vr[s][a][b][0] = r.x; vr[s][a][b][1] = r.y;
+          }
+        }
+      }
+  };
+  // exponent bytes of K (low) and V of the tile's keys, a lane's own
+  auto load_e = [&](const unsigned* ix, int* eb) {
+    if constexpr (FMT == POD_KV_E4M3_BLOCK) {
+#pragma unroll
+      for (int j = 0; j < S::IDX; ++j) {
+        eb[j] = 127 | 127 << 8;
+        if (ix[j] != 0xffffffffu) {
+          const uint8_t* p = P.scales + (P.hnd ? (long long)ix[j] + (long long)hk * P.ps : (long long)ix[j] * P.Hk + hk);
+          eb[j] = p[0] | p[(long long)P.ps * P.Hk] << 8;
+        }
+      }
+    }
+  };
+
+  int v = v0 + warp * TK;
+  int eb[S::IDX], eb_next[S::IDX];
+#pragma unroll
+  for (int j = 0; j < S::IDX; ++j) {
+    const bool mine = TK >= 32 || lane < TK;
+    idx[j] = index_of(mine ? place(v + j * 32 + lane) : Place{-1, 0});
+    nxt[j] = mine ? place(v + S::U + j * 32 + lane) : Place{-1, 0};
+  }
+  if (v < v1) {
+    load_k(idx);
+    load_e(idx, eb);
+    load_v(idx);
+  }
+  for (; v < v1; v += S::U) {
+    unsigned idx_next[S::IDX];
+#pragma unroll
+    for (int j = 0; j < S::IDX; ++j) {
+      const bool mine = TK >= 32 || lane < TK;
+      idx_next[j] = index_of(nxt[j]);
+      nxt[j] = mine ? place(v + 2 * S::U + j * 32 + lane) : Place{-1, 0};
+    }
+    // ---- S^T, a key a row (g, g + 8 of every 16), the heads 2t and 2t + 1 of every 8
+    float x[MT][NT][4];
+#pragma unroll
+    for (int s = 0; s < MT; ++s) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[s][n][c] = 0.f;
+#pragma unroll
+      for (int b = 0; b < S::NK; ++b) {
+        const uint32_t w0[4] = {kr[s][0][b].x, kr[s][0][b].y, kr[s][0][b].z, kr[s][0][b].w};
+        const uint32_t w1[4] = {kr[s][1][b].x, kr[s][1][b].y, kr[s][1][b].z, kr[s][1][b].w};
+        if constexpr (FMT == POD_KV_16BIT) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t a[4] = {w0[2 * i], w1[2 * i], w0[2 * i + 1], w1[2 * i + 1]};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<MBF>(x[s][n], a, qf[n][b][2 * i], qf[n][b][2 * i + 1]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t a[4] = {e4m3x2_to<__half>((uint16_t)w0[i]), e4m3x2_to<__half>((uint16_t)w1[i]),
+                                   e4m3x2_to<__half>((uint16_t)(w0[i] >> 16)),
+                                   e4m3x2_to<__half>((uint16_t)(w1[i] >> 16))};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<MBF>(x[s][n], a, qf[n][b][2 * i], qf[n][b][2 * i + 1]);
+          }
+        }
+      }
+    }
+    load_k(idx_next);
+    load_e(idx_next, eb_next);
+    // ---- logits, the references, the weights
+    float xe[MT][2];                             // V's exponents of the lane's keys
+    bool past = false;
+#pragma unroll
+    for (int s = 0; s < MT; ++s)
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const int src = (s & 1) * 16 + a * 8 + g;
+        const bool live = __shfl_sync(0xffffffffu, idx[s / 2], src) != 0xffffffffu;
+        float ks = 1.f;
+        xe[s][a] = 0.f;
+        if constexpr (FMT == POD_KV_E4M3_BLOCK) {
+          const int e = __shfl_sync(0xffffffffu, eb[s / 2], src);
+          ks = pow2_of(e & 255);
+          xe[s][a] = (float)((e >> 8) - 127);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float& y = x[s][n][2 * a + c];
+            if constexpr (FMT == POD_KV_E4M3_BLOCK) y = live ? y * ks * xs[n][c] : -INFINITY;
+            else y = live ? y * xs[n][c] : -INFINITY;
+            past |= y > m[n][c] + kLag;
+            if constexpr (FMT == POD_KV_E4M3_BLOCK) past |= y + xe[s][a] > mv[n][c] + kLag;
+          }
+      }
+    if (__any_sync(0xffffffffu, past)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float top = m[n][c], topv = mv[n][c];
+#pragma unroll
+          for (int s = 0; s < MT; ++s)
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+              top = fmaxf(top, x[s][n][2 * a + c]);
+              if constexpr (FMT == POD_KV_E4M3_BLOCK) topv = fmaxf(topv, x[s][n][2 * a + c] + xe[s][a]);
+            }
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            if constexpr (FMT == POD_KV_E4M3_BLOCK) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, d));
+          }
+          const float f = top == -INFINITY ? 1.f : ex2(m[n][c] - top);
+          m[n][c] = top;
+          l[n][c] *= f;
+          float fo = f;
+          if constexpr (FMT == POD_KV_E4M3_BLOCK) {
+            fo = topv == -INFINITY ? 1.f : ex2(mv[n][c] - topv);
+            mv[n][c] = topv;
+          }
+#pragma unroll
+          for (int b = 0; b < S::NV; ++b)
+#pragma unroll
+            for (int i = 0; i < S::CV / 2; ++i) {
+              o[n][b][i][c] *= fo;
+              o[n][b][i][2 + c] *= fo;
+            }
+        }
+    }
+    uint32_t ph[MT][NT][2], pl[MT][NT][2];       // P^T as operand: keys 2t.., 2t + 8..; head g
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float r0 = (m[n][0] == -INFINITY ? 0.f : m[n][0]) - kUp, r1 = (m[n][1] == -INFINITY ? 0.f : m[n][1]) - kUp;
+      float rv0 = r0, rv1 = r1;
+      if constexpr (FMT == POD_KV_E4M3_BLOCK) {
+        rv0 = (mv[n][0] == -INFINITY ? 0.f : mv[n][0]) - kUp;
+        rv1 = (mv[n][1] == -INFINITY ? 0.f : mv[n][1]) - kUp;
+      }
+#pragma unroll
+      for (int s = 0; s < MT; ++s)
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          float p0 = ex2(x[s][n][2 * a] - r0), p1 = ex2(x[s][n][2 * a + 1] - r1);
+          l[n][0] += p0;
+          l[n][1] += p1;
+          if constexpr (FMT == POD_KV_E4M3_BLOCK) {
+            p0 = ex2(x[s][n][2 * a] + xe[s][a] - rv0);
+            p1 = ex2(x[s][n][2 * a + 1] + xe[s][a] - rv1);
+          }
+          uint32_t hi, lo;
+          Pack<M>::split(p0, p1, hi, lo);
+          ph[s][n][a] = turn8x8(hi);
+          pl[s][n][a] = turn8x8(lo);
+        }
+    }
+    // ---- O^T += V^T P^T
+#pragma unroll
+    for (int s = 0; s < MT; ++s)
+#pragma unroll
+      for (int b = 0; b < S::NV; ++b)
+#pragma unroll
+        for (int w = 0; w < S::WV; ++w) {
+          const uint32_t v0w = vr[s][0][b][w], v1w = vr[s][1][b][w], v2w = vr[s][2][b][w], v3w = vr[s][3][b][w];
+          if constexpr (FMT == POD_KV_16BIT) {
+            const uint32_t a[4] = {prmt(v0w, v1w, 0x5410), prmt(v0w, v1w, 0x7632), prmt(v2w, v3w, 0x5410),
+                                   prmt(v2w, v3w, 0x7632)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma16816<MBF>(o[n][b][w], a, ph[s][n][0], ph[s][n][1]);
+              mma16816<MBF>(o[n][b][w], a, pl[s][n][0], pl[s][n][1]);
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const uint32_t lo = prmt(v0w, v1w, q ? 0x7362 : 0x5140), hi = prmt(v2w, v3w, q ? 0x7362 : 0x5140);
+              const uint32_t a[4] = {e4m3x2_to<__half>((uint16_t)lo), e4m3x2_to<__half>((uint16_t)(lo >> 16)),
+                                     e4m3x2_to<__half>((uint16_t)hi), e4m3x2_to<__half>((uint16_t)(hi >> 16))};
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                mma16816<MBF>(o[n][b][2 * w + q], a, ph[s][n][0], ph[s][n][1]);
+                mma16816<MBF>(o[n][b][2 * w + q], a, pl[s][n][0], pl[s][n][1]);
+              }
+            }
+          }
+        }
+    load_v(idx_next);
+#pragma unroll
+    for (int j = 0; j < S::IDX; ++j) {
+      idx[j] = idx_next[j];
+      eb[j] = eb_next[j];
+    }
+  }
+
+  // ---- the warps' sums join
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], d);
+      if (g == 0) {
+        const int h = n * 8 + 2 * t + c;
+        sh.m[0][warp][h] = m[n][c];
+        sh.m[1][warp][h] = l[n][c];
+        sh.m[2][warp][h] = FMT == POD_KV_E4M3_BLOCK ? mv[n][c] : m[n][c];
+      }
+    }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float* dst = sh.o[warp][n * 8 + 2 * t + c];
+#pragma unroll
+      for (int b = 0; b < S::NV; ++b)
+#pragma unroll
+        for (int i = 0; i < S::CV / 4; ++i)
+          *reinterpret_cast<float4*>(dst + (b * 8 + g) * S::CV + 4 * i) =
+              make_float4(o[n][b][2 * i][c], o[n][b][2 * i][2 + c], o[n][b][2 * i + 1][c], o[n][b][2 * i + 1][2 + c]);
+    }
+  __syncthreads();
+}
+
+// The sum of a CTA's four pieces at one float4 of a row, normalised, and the row's LSE;
+// `lanes` neighbouring lanes with four pieces each share it. Piece w has its m, l and O's
+// reference at stat(w, 0..2) and its O at value(w).
+template <int FMT, typename A, typename B>
+POD_DEV float4 join(int lanes, float up, float v_scale, float& lse, A stat, B value) {
+  float m[kDecodeWarps], mo[kDecodeWarps], l[kDecodeWarps];
+  float4 p[kDecodeWarps];
+  float top = -INFINITY, topv = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kDecodeWarps; ++w) {
+    m[w] = stat(w, 0);
+    l[w] = stat(w, 1);
+    mo[w] = stat(w, 2);
+    p[w] = value(w);
+    top = fmaxf(top, m[w]);
+    topv = fmaxf(topv, mo[w]);
+  }
+  for (int o = 1; o < lanes; o <<= 1) {
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, o));
+  }
+  const float z = top == -INFINITY ? 0.f : top, zv = topv == -INFINITY ? 0.f : topv;
+  float sum = 0.f;
+  float4 acc = make_float4(0, 0, 0, 0);
+#pragma unroll
+  for (int w = 0; w < kDecodeWarps; ++w) {
+    const float f = ex2(m[w] - z), fv = ex2(mo[w] - zv);
+    sum += l[w] * f;
+    acc.x += p[w].x * fv; acc.y += p[w].y * fv; acc.z += p[w].z * fv; acc.w += p[w].w * fv;
+  }
+  for (int o = 1; o < lanes; o <<= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
+    acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
+    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
+    acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
+  }
+  // (sum == 0: no visible key; a NaN stays one)
+  lse = sum == 0.f ? -INFINITY : z + log2f(sum) - up;
+  const float f = sum == 0.f ? 0.f : v_scale / sum;
+  acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
+  if constexpr (FMT == POD_KV_E4M3_BLOCK) {
+    const float back = ex2(zv - z);                // O's own reference
+    acc.x *= back; acc.y *= back; acc.z *= back; acc.w *= back;
+  }
+  return acc;
+}
+
+template <typename T>
+POD_DEV void store_out(const DecodeParams& P, int row, int head, int D, int c4, float4 o, float lse) {
+  if (P.sinks && lse != -INFINITY) {
+    const float f = sink_factor(lse, P.sinks[head]);
+    o.x *= f; o.y *= f; o.z *= f; o.w *= f;
+  }
+  T* dst = static_cast<T*>(P.out) + (long long)row * P.out_stride + (long long)head * D + 4 * c4;
   *reinterpret_cast<uint2*>(dst) = make_uint2(Pack<T>::two(o.x, o.y), Pack<T>::two(o.z, o.w));
+  if (c4 == 0 && P.lse) P.lse[(long long)row * P.H + head] = lse;
 }
 
 template <typename T, int D, int FMT, int NT>
 __global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
     decode_kernel(const __grid_constant__ DecodeParams P) {
   using S = DecodeShape<D, FMT, NT>;
-  using M = typename std::conditional<FMT == POD_KV_16BIT, T, __half>::type;   // operands of the products
-  constexpr bool MBF = Pack<M>::kBF16;
-  constexpr float kUp = MBF ? -24.f : 7.f;
-  constexpr int MT = S::MT, TK = S::TK, HT = S::HT;
-  __shared__ float sh_o[kDecodeWarps][HT][D];
-  __shared__ float sh_m[3][kDecodeWarps][HT];
+  constexpr int HT = S::HT;
+  __shared__ DecodeShared<D, HT> sh;
   __shared__ long long sh_scan[kDecodeWarps + 2];
   __shared__ int sh_row;
 
   asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   // ---- this CTA's run of units
   long long total = 0;                             // units of a plane
@@ -181,409 +626,22 @@ __global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
     }
     const long long seg0 = (long long)plane * total + row_first;      // of the whole request
     const int ua = (int)(u - seg0), ub = (int)min((long long)units, u_end - seg0);
-    const int v0 = ua * S::U, v1 = (int)min((long long)K.count, (long long)ub * S::U);
     const int hk = plane % P.Hk, h0 = hk * P.G + plane / P.Hk * HT;
     const int heads = min(HT, P.G - plane / P.Hk * HT);
     if (tid == 0 && plane == 0 && ua == 0) P.first[row] = row_first;
-
-    // ---- Q as the columns of S^T, and the factor that takes a column to base-2 logits
-    uint32_t qf[NT][S::NK][S::CK / 2];
-    float xs[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int h = n * 8 + g;
-      const T* src = static_cast<const T*>(P.q) + (long long)row * P.q_stride + (long long)(h0 + h) * D;
-      uint32_t w[S::NK][S::CK / 2];
-#pragma unroll
-      for (int b = 0; b < S::NK; ++b)
-#pragma unroll
-        for (int c = 0; c < S::CK / 8; ++c) {
-          uint4 r = make_uint4(0, 0, 0, 0);
-          if (h < heads) r = *reinterpret_cast<const uint4*>(src + (b * 4 + t) * S::CK + c * 8);
-          w[b][4 * c] = r.x; w[b][4 * c + 1] = r.y; w[b][4 * c + 2] = r.z; w[b][4 * c + 3] = r.w;
-        }
-      if constexpr (FMT == POD_KV_16BIT) {
-        xs[n][0] = xs[n][1] = P.scale_log2;
-#pragma unroll
-        for (int b = 0; b < S::NK; ++b)
-#pragma unroll
-          for (int i = 0; i < S::CK / 2; ++i) qf[n][b][i] = w[b][i];
-      } else {
-        // fp16 operands: the row by the power of two that brings its largest element to
-        // [2^14, 2^15), so that bf16 rows keep all bits down to 2^-38 of it
-        float am = 0.f;
-#pragma unroll
-        for (int b = 0; b < S::NK; ++b)
-#pragma unroll
-          for (int i = 0; i < S::CK / 2; ++i) {
-            const float2 f = Pack<T>::unpack(w[b][i]);
-            am = fmaxf(am, fmaxf(fabsf(f.x), fabsf(f.y)));
-          }
-        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-        const int ex = (int)(__float_as_uint(am) >> 23) - 127;            // (-127: zeros and subnormals)
-        const int e = ex >= 128 ? 0 : min(14 - ex, 126);
-        const float up = __uint_as_float((uint32_t)(127 + e) << 23), down = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-        for (int b = 0; b < S::NK; ++b)
-#pragma unroll
-          for (int i = 0; i < S::CK / 2; ++i) {
-            const float2 f = Pack<T>::unpack(w[b][i]);
-            qf[n][b][i] = Pack<M>::two(f.x * up, f.y * up);
-          }
-        const float d0 = __shfl_sync(0xffffffffu, down, 8 * t), d1 = __shfl_sync(0xffffffffu, down, 8 * t + 4);
-        xs[n][0] = d0 * P.scale_log2;
-        xs[n][1] = d1 * P.scale_log2;
-      }
-    }
-
-    float o[NT][S::NV][S::CV / 2][4], m[NT][2], mv[NT][2], l[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int b = 0; b < S::NV; ++b)
-#pragma unroll
-        for (int i = 0; i < S::CV / 2; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) o[n][b][i][c] = 0.f;
-      m[n][0] = m[n][1] = mv[n][0] = mv[n][1] = -INFINITY;
-      l[n][0] = l[n][1] = 0.f;
-    }
-
-    // ---- addresses: rows of d elements; a key's K row is index * key_step + rows of the head
-    const long long row_bytes = (long long)D * S::E;
-    const long long key_step = P.hnd ? row_bytes : row_bytes * P.Hk;
-    const long long v_off = (long long)P.ps * P.Hk * row_bytes;
-    const uint8_t* kbase = P.cache + (P.hnd ? (long long)hk * P.ps : (long long)hk) * row_bytes;
-    const unsigned page_step = 2u * (unsigned)P.ps * (P.hnd ? (unsigned)P.Hk : 1u);
-    const int32_t* table = P.table + (long long)row * P.table_stride;
-    const int32_t* sel = P.pages ? P.pages + ((long long)row * P.Hk + hk) * P.num_selected : nullptr;
-
-    // Tile key i of a tile at v: its place in the table (stage 1), then its row (stage
-    // 2), each asked for a tile ahead of its use. 0xffffffff: not visible.
-    struct Place {
-      int page, in;
-    };
-    auto place = [&](int v) {
-      Place p;
-      p.page = -1;
-      p.in = 0;
-      if (v < v1) {
-        const int w = v + K.first, at_page = w / P.ps;
-        p.in = w - at_page * P.ps;
-        p.page = at_page;
-        if (sel) {
-          p.page = sel[at_page];
-          // (a page past the request's last, or a slot past its last key: not visible)
-          if (p.page >= 0 && (p.page >= P.width || p.page * P.ps + p.in >= K.len)) p.page = -1;
-        }
-      }
-      return p;
-    };
-    auto index_of = [&](Place p) {
-      if (p.page < 0) return 0xffffffffu;
-      const unsigned page = (unsigned)table[p.page];
-      if (page >= P.num_pages) {
-        if (P.status) atomicOr(P.status, kStatusSlot);
-        return 0xffffffffu;
-      }
-      return page * page_step + (unsigned)p.in;
-    };
-
-    uint4 kr[MT][2][S::NK];
-    uint32_t vr[MT][4][S::NV][S::WV];
-    unsigned idx[S::IDX];                          // rows of the tile in flight, lane i: key i
-    Place nxt[S::IDX];
-    auto load_k = [&](const unsigned* ix) {
-#pragma unroll
-      for (int s = 0; s < MT; ++s)
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          const unsigned i = __shfl_sync(0xffffffffu, ix[s / 2], (s & 1) * 16 + a * 8 + g);
-          const uint8_t* p = kbase + (long long)i * key_step + t * 16;
-#pragma unroll
-          for (int b = 0; b < S::NK; ++b) {
-            kr[s][a][b] = make_uint4(0, 0, 0, 0);
-            if (i != 0xffffffffu) kr[s][a][b] = load16(p + b * 64);
-          }
-        }
-    };
-    auto load_v = [&](const unsigned* ix) {
-#pragma unroll
-      for (int s = 0; s < MT; ++s)
-#pragma unroll
-        for (int a = 0; a < 4; ++a) {
-          const unsigned i = __shfl_sync(0xffffffffu, ix[s / 2], (s & 1) * 16 + (a >> 1) * 8 + 2 * t + (a & 1));
-          const uint8_t* p = kbase + v_off + (long long)i * key_step + g * (S::WV * 4);
-#pragma unroll
-          for (int b = 0; b < S::NV; ++b) {
-            if constexpr (S::WV == 4) {
-              uint4 r = make_uint4(0, 0, 0, 0);
-              if (i != 0xffffffffu) r = load16(p + b * 128);
-              vr[s][a][b][0] = r.x; vr[s][a][b][1] = r.y; vr[s][a][b][2] = r.z; vr[s][a][b][3] = r.w;
-            } else {
-              uint2 r = make_uint2(0, 0);
-              if (i != 0xffffffffu) r = load8(p + b * 64);
-              vr[s][a][b][0] = r.x; vr[s][a][b][1] = r.y;
-            }
-          }
-        }
-    };
-    // exponent bytes of K (low) and V of the tile's keys, a lane's own
-    auto load_e = [&](const unsigned* ix, int* eb) {
-      if constexpr (FMT == POD_KV_E4M3_BLOCK) {
-#pragma unroll
-        for (int j = 0; j < S::IDX; ++j) {
-          eb[j] = 127 | 127 << 8;
-          if (ix[j] != 0xffffffffu) {
-            const uint8_t* p = P.scales + (P.hnd ? (long long)ix[j] + (long long)hk * P.ps : (long long)ix[j] * P.Hk + hk);
-            eb[j] = p[0] | p[(long long)P.ps * P.Hk] << 8;
-          }
-        }
-      }
-    };
-
-    int v = v0 + warp * TK;
-    int eb[S::IDX], eb_next[S::IDX];
-#pragma unroll
-    for (int j = 0; j < S::IDX; ++j) {
-      const bool mine = TK >= 32 || lane < TK;
-      idx[j] = index_of(mine ? place(v + j * 32 + lane) : Place{-1, 0});
-      nxt[j] = mine ? place(v + S::U + j * 32 + lane) : Place{-1, 0};
-    }
-    if (v < v1) {
-      load_k(idx);
-      load_e(idx, eb);
-      load_v(idx);
-    }
-    for (; v < v1; v += S::U) {
-      unsigned idx_next[S::IDX];
-#pragma unroll
-      for (int j = 0; j < S::IDX; ++j) {
-        const bool mine = TK >= 32 || lane < TK;
-        idx_next[j] = index_of(nxt[j]);
-        nxt[j] = mine ? place(v + 2 * S::U + j * 32 + lane) : Place{-1, 0};
-      }
-      // ---- S^T, a key a row (g, g + 8 of every 16), the heads 2t and 2t + 1 of every 8
-      float x[MT][NT][4];
-#pragma unroll
-      for (int s = 0; s < MT; ++s) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) x[s][n][c] = 0.f;
-#pragma unroll
-        for (int b = 0; b < S::NK; ++b) {
-          const uint32_t w0[4] = {kr[s][0][b].x, kr[s][0][b].y, kr[s][0][b].z, kr[s][0][b].w};
-          const uint32_t w1[4] = {kr[s][1][b].x, kr[s][1][b].y, kr[s][1][b].z, kr[s][1][b].w};
-          if constexpr (FMT == POD_KV_16BIT) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t a[4] = {w0[2 * i], w1[2 * i], w0[2 * i + 1], w1[2 * i + 1]};
-#pragma unroll
-              for (int n = 0; n < NT; ++n) mma16816<MBF>(x[s][n], a, qf[n][b][2 * i], qf[n][b][2 * i + 1]);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t a[4] = {e4m3x2_to<__half>((uint16_t)w0[i]), e4m3x2_to<__half>((uint16_t)w1[i]),
-                                     e4m3x2_to<__half>((uint16_t)(w0[i] >> 16)),
-                                     e4m3x2_to<__half>((uint16_t)(w1[i] >> 16))};
-#pragma unroll
-              for (int n = 0; n < NT; ++n) mma16816<MBF>(x[s][n], a, qf[n][b][2 * i], qf[n][b][2 * i + 1]);
-            }
-          }
-        }
-      }
-      load_k(idx_next);
-      load_e(idx_next, eb_next);
-      // ---- logits, the references, the weights
-      float xe[MT][2];                             // V's exponents of the lane's keys
-      bool past = false;
-#pragma unroll
-      for (int s = 0; s < MT; ++s)
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          const int src = (s & 1) * 16 + a * 8 + g;
-          const bool live = __shfl_sync(0xffffffffu, idx[s / 2], src) != 0xffffffffu;
-          float ks = 1.f;
-          xe[s][a] = 0.f;
-          if constexpr (FMT == POD_KV_E4M3_BLOCK) {
-            const int e = __shfl_sync(0xffffffffu, eb[s / 2], src);
-            ks = pow2_of(e & 255);
-            xe[s][a] = (float)((e >> 8) - 127);
-          }
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float& y = x[s][n][2 * a + c];
-              if constexpr (FMT == POD_KV_E4M3_BLOCK) y = live ? y * ks * xs[n][c] : -INFINITY;
-              else y = live ? y * xs[n][c] : -INFINITY;
-              past |= y > m[n][c] + kLag;
-              if constexpr (FMT == POD_KV_E4M3_BLOCK) past |= y + xe[s][a] > mv[n][c] + kLag;
-            }
-        }
-      if (__any_sync(0xffffffffu, past)) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float top = m[n][c], topv = mv[n][c];
-#pragma unroll
-            for (int s = 0; s < MT; ++s)
-#pragma unroll
-              for (int a = 0; a < 2; ++a) {
-                top = fmaxf(top, x[s][n][2 * a + c]);
-                if constexpr (FMT == POD_KV_E4M3_BLOCK) topv = fmaxf(topv, x[s][n][2 * a + c] + xe[s][a]);
-              }
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-              if constexpr (FMT == POD_KV_E4M3_BLOCK) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, d));
-            }
-            const float f = top == -INFINITY ? 1.f : ex2(m[n][c] - top);
-            m[n][c] = top;
-            l[n][c] *= f;
-            float fo = f;
-            if constexpr (FMT == POD_KV_E4M3_BLOCK) {
-              fo = topv == -INFINITY ? 1.f : ex2(mv[n][c] - topv);
-              mv[n][c] = topv;
-            }
-#pragma unroll
-            for (int b = 0; b < S::NV; ++b)
-#pragma unroll
-              for (int i = 0; i < S::CV / 2; ++i) {
-                o[n][b][i][c] *= fo;
-                o[n][b][i][2 + c] *= fo;
-              }
-          }
-      }
-      uint32_t ph[MT][NT][2], pl[MT][NT][2];       // P^T as operand: keys 2t.., 2t + 8..; head g
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float r0 = (m[n][0] == -INFINITY ? 0.f : m[n][0]) - kUp, r1 = (m[n][1] == -INFINITY ? 0.f : m[n][1]) - kUp;
-        float rv0 = r0, rv1 = r1;
-        if constexpr (FMT == POD_KV_E4M3_BLOCK) {
-          rv0 = (mv[n][0] == -INFINITY ? 0.f : mv[n][0]) - kUp;
-          rv1 = (mv[n][1] == -INFINITY ? 0.f : mv[n][1]) - kUp;
-        }
-#pragma unroll
-        for (int s = 0; s < MT; ++s)
-#pragma unroll
-          for (int a = 0; a < 2; ++a) {
-            float p0 = ex2(x[s][n][2 * a] - r0), p1 = ex2(x[s][n][2 * a + 1] - r1);
-            l[n][0] += p0;
-            l[n][1] += p1;
-            if constexpr (FMT == POD_KV_E4M3_BLOCK) {
-              p0 = ex2(x[s][n][2 * a] + xe[s][a] - rv0);
-              p1 = ex2(x[s][n][2 * a + 1] + xe[s][a] - rv1);
-            }
-            uint32_t hi, lo;
-            Pack<M>::split(p0, p1, hi, lo);
-            ph[s][n][a] = turn8x8(hi);
-            pl[s][n][a] = turn8x8(lo);
-          }
-      }
-      // ---- O^T += V^T P^T
-#pragma unroll
-      for (int s = 0; s < MT; ++s)
-#pragma unroll
-        for (int b = 0; b < S::NV; ++b)
-#pragma unroll
-          for (int w = 0; w < S::WV; ++w) {
-            const uint32_t v0w = vr[s][0][b][w], v1w = vr[s][1][b][w], v2w = vr[s][2][b][w], v3w = vr[s][3][b][w];
-            if constexpr (FMT == POD_KV_16BIT) {
-              const uint32_t a[4] = {prmt(v0w, v1w, 0x5410), prmt(v0w, v1w, 0x7632), prmt(v2w, v3w, 0x5410),
-                                     prmt(v2w, v3w, 0x7632)};
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                mma16816<MBF>(o[n][b][w], a, ph[s][n][0], ph[s][n][1]);
-                mma16816<MBF>(o[n][b][w], a, pl[s][n][0], pl[s][n][1]);
-              }
-            } else {
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const uint32_t lo = prmt(v0w, v1w, q ? 0x7362 : 0x5140), hi = prmt(v2w, v3w, q ? 0x7362 : 0x5140);
-                const uint32_t a[4] = {e4m3x2_to<__half>((uint16_t)lo), e4m3x2_to<__half>((uint16_t)(lo >> 16)),
-                                       e4m3x2_to<__half>((uint16_t)hi), e4m3x2_to<__half>((uint16_t)(hi >> 16))};
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                  mma16816<MBF>(o[n][b][2 * w + q], a, ph[s][n][0], ph[s][n][1]);
-                  mma16816<MBF>(o[n][b][2 * w + q], a, pl[s][n][0], pl[s][n][1]);
-                }
-              }
-            }
-          }
-      load_v(idx_next);
-#pragma unroll
-      for (int j = 0; j < S::IDX; ++j) {
-        idx[j] = idx_next[j];
-        eb[j] = eb_next[j];
-      }
-    }
-
-    // ---- the warps' sums join
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], d);
-        if (g == 0) {
-          const int h = n * 8 + 2 * t + c;
-          sh_m[0][warp][h] = m[n][c];
-          sh_m[1][warp][h] = l[n][c];
-          sh_m[2][warp][h] = FMT == POD_KV_E4M3_BLOCK ? mv[n][c] : m[n][c];
-        }
-      }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float* dst = sh_o[warp][n * 8 + 2 * t + c];
-#pragma unroll
-        for (int b = 0; b < S::NV; ++b)
-#pragma unroll
-          for (int i = 0; i < S::CV / 4; ++i)
-            *reinterpret_cast<float4*>(dst + (b * 8 + g) * S::CV + 4 * i) =
-                make_float4(o[n][b][2 * i][c], o[n][b][2 * i][2 + c], o[n][b][2 * i + 1][c], o[n][b][2 * i + 1][2 + c]);
-      }
-    __syncthreads();
+    attend<T, D, FMT, NT>(P, K, row, hk, h0, heads, ua * S::U, (int)min((long long)K.count, (long long)ub * S::U), sh);
     const bool whole = ua == 0 && ub == units;
     const int slot = (int)blockIdx.x * 2 + (u == u_start ? 0 : 1);
     for (int i = tid; i < heads * (D / 4); i += kDecodeThreads) {
       const int h = i / (D / 4), c4 = i - h * (D / 4);
-      float top = -INFINITY, topv = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kDecodeWarps; ++w) {
-        top = fmaxf(top, sh_m[0][w][h]);
-        topv = fmaxf(topv, sh_m[2][w][h]);
-      }
-      const float z = top == -INFINITY ? 0.f : top, zv = topv == -INFINITY ? 0.f : topv;
-      float sum = 0.f;
-      float4 acc = make_float4(0, 0, 0, 0);
-#pragma unroll
-      for (int w = 0; w < kDecodeWarps; ++w) {
-        const float f = ex2(sh_m[0][w][h] - z), fv = ex2(sh_m[2][w][h] - zv);
-        const float4 p = *reinterpret_cast<const float4*>(&sh_o[w][h][4 * c4]);
-        sum += sh_m[1][w][h] * f;
-        acc.x += p.x * fv; acc.y += p.y * fv; acc.z += p.z * fv; acc.w += p.w * fv;
-      }
-      // (sum == 0: no visible key; a NaN stays one)
-      const float lse = sum == 0.f ? -INFINITY : z + log2f(sum) - kUp;
-      float f = sum == 0.f ? 0.f : P.v_scale / sum;
-      if (whole && P.sinks && sum != 0.f) f *= sink_factor(lse, P.sinks[h0 + h]);
-      acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
-      if constexpr (FMT == POD_KV_E4M3_BLOCK) {
-        const float back = ex2(zv - z);            // O's own reference
-        acc.x *= back; acc.y *= back; acc.z *= back; acc.w *= back;
-      }
+      float lse;
+      const float4 o = join<FMT>(1, weight_up<T, FMT>(), P.v_scale, lse,
+                                 [&](int w, int what) { return sh.m[what][w][h]; },
+                                 [&](int w) { return *reinterpret_cast<const float4*>(&sh.o[w][h][4 * c4]); });
       if (whole) {
-        store_row4<T, D>(static_cast<T*>(P.out) + (long long)row * P.out_stride + (long long)(h0 + h) * D + 4 * c4, acc);
-        if (c4 == 0 && P.lse) P.lse[(long long)row * P.H + h0 + h] = lse;
+        store_out<T>(P, row, h0 + h, D, c4, o, lse);
       } else {
-        *reinterpret_cast<float4*>(P.piece_o + ((long long)slot * HT + h) * D + 4 * c4) = acc;
+        *reinterpret_cast<float4*>(P.piece_o + ((long long)slot * HT + h) * D + 4 * c4) = o;
         if (c4 == 0) P.piece_lse[slot * HT + h] = lse;
       }
     }
@@ -592,6 +650,55 @@ __global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
     row_first += units;
     if (++row == P.batch) { row = 0; row_first = 0; ++plane; }
   }
+}
+
+// Short rows: a cluster of CL CTAs for each (plane, request), which share its units and join
+// them through each other's shared memory: one launch, no workspace.
+template <typename T, int D, int FMT, int NT, int CL>
+__global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
+    decode_short_kernel(const __grid_constant__ DecodeParams P) {
+  using S = DecodeShape<D, FMT, NT>;
+  constexpr int HT = S::HT;
+  __shared__ DecodeShared<D, HT> sh;
+  asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, rank = CL > 1 ? (int)(blockIdx.x % CL) : 0;
+  const int item = (int)(blockIdx.x / CL), plane = item / P.batch, row = item - plane * P.batch;
+  const Keys K = keys_of(P, row);
+  const int units = (K.count + S::U - 1) / S::U;
+  const int hk = plane % P.Hk, h0 = hk * P.G + plane / P.Hk * HT;
+  const int heads = min(HT, P.G - plane / P.Hk * HT);
+  if (plane == 0 && rank == 0 && tid == 0 && P.status && P.lens[row] != K.len) atomicOr(P.status, kStatusSlot);
+  const int v0 = units * rank / CL * S::U, v1 = min(K.count, units * (rank + 1) / CL * S::U);
+  attend<T, D, FMT, NT>(P, K, row, hk, h0, heads, v0, v1, sh);
+  if (CL > 1)
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  // CL neighbouring threads join one float4, each the four pieces of a CTA
+  const uint32_t mine = smem_u32(&sh);
+  uint32_t base = mine;
+  if (CL > 1) asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(base) : "r"(mine), "r"(tid % CL));
+  const int per = kDecodeThreads / CL;             // float4s of a CTA at a time
+  for (int i0 = rank * per; i0 < heads * (D / 4); i0 += per * CL) {
+    const int i = i0 + tid / CL, j = min(i, heads * (D / 4) - 1), h = j / (D / 4), c4 = j - h * (D / 4);
+    float lse;
+    const float4 o = join<FMT>(
+        CL, weight_up<T, FMT>(), P.v_scale, lse,
+        [&](int w, int what) {
+          float x;
+          const uint32_t a = base + (uint32_t)offsetof_m<D, HT>(what, w, h);
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
+          return x;
+        },
+        [&](int w) {
+          float4 x;
+          const uint32_t a = base + (uint32_t)(((w * HT + h) * D + 4 * c4) * 4);
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(a) : "memory");
+          return x;
+        });
+    if (i == j && tid % CL == 0) store_out<T>(P, row, h0 + h, D, c4, o, lse);
+  }
+  if (CL > 1)                                      // (nobody leaves while others read its memory)
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Rows whose keys were cut: the pieces in the order of the keys, weighted by
@@ -695,6 +802,23 @@ cudaError_t launch_beside(void (*kernel)(A...), unsigned grid, unsigned threads,
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+template <typename... A, typename... B>
+cudaError_t launch_clusters(void (*kernel)(A...), unsigned grid, unsigned cluster, cudaStream_t st, const B&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kDecodeThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <typename T, int D, int FMT, int NT>
 cudaError_t launch_decode_nt(DecodeParams& P, cudaStream_t st) {
   using S = DecodeShape<D, FMT, NT>;
@@ -702,12 +826,20 @@ cudaError_t launch_decode_nt(DecodeParams& P, cudaStream_t st) {
   P.planes = P.Hk * tiles;
   constexpr int per_sm = (D == 256 || NT == 2) ? 2 : 3;
   P.grid = 152 * per_sm;
+  // Units of the longest row that the table (the list of pages, the window) allows.
+  const long long items = (long long)P.batch * P.planes;
+  const long long keys = P.pages ? (long long)min(P.num_selected, P.width) * P.ps
+                                 : min((long long)P.width * P.ps, P.window < 0 ? LLONG_MAX : P.window + 1ll);
+  const long long units = (keys + S::U - 1) / S::U;
+  // Short rows whose clusters all fit the GPU at once.
+  if (items * 8 <= P.grid && units <= 8 * kShortUnits)
+    return launch_clusters(decode_short_kernel<T, D, FMT, NT, 8>, (unsigned)items * 8, 8, st, P);
   cudaError_t e = launch_beside(decode_kernel<T, D, FMT, NT>, (unsigned)P.grid, kDecodeThreads, st, P);
   if (e != cudaSuccess) return e;
   // a warp for each (request, head), or a block of four where a row may have many pieces
-  const long long items = (long long)P.batch * P.H;
-  if (items <= 2048) return launch_beside(decode_merge_kernel<T, D, S::HT, S::U, 4>, (unsigned)items, 128, st, P);
-  return launch_beside(decode_merge_kernel<T, D, S::HT, S::U, 1>, (unsigned)((items + 3) / 4), 128, st, P);
+  const long long rows = (long long)P.batch * P.H;
+  if (rows <= 2048) return launch_beside(decode_merge_kernel<T, D, S::HT, S::U, 4>, (unsigned)rows, 128, st, P);
+  return launch_beside(decode_merge_kernel<T, D, S::HT, S::U, 1>, (unsigned)((rows + 3) / 4), 128, st, P);
 }
 
 template <typename T, int FMT>

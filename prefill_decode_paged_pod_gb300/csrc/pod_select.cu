@@ -9,13 +9,12 @@
 //   up_j = sum_g max(q_gj, 0), down_j = sum_g min(q_gj, 0).
 //
 // The choice is that of the scores in 64 bits, without computing them so: an fp32
-// score is off by at most E = (24 + G) 2^-24 times the sum of its terms' magnitudes (8
-// or 16 fused steps a lane, five additions across lanes, G - 1 in a weight), of which
-// a bound is kept per 32 pages. Pages further than 2 E from the last place are decided;
+// score is off by at most E = (13 + G) 2^-24 times the sum of its terms' magnitudes (8
+// fused steps a lane, 16 at D = 256, five additions across lanes, G - 1 in a weight), of which
+// a bound is kept per warp. Pages further than 2 E from the last place are decided;
 // the others, where they are more than the places left, are scored again in 64
 // bits (of which this GPU does two a clock and SM).
 #include <cuda_runtime.h>
-#include <float.h>
 #include <math.h>
 
 #include <string>
@@ -30,10 +29,11 @@ using namespace pod;
 
 namespace {
 
-constexpr int kBoundThreads = 256, kBoundRows = 128;
-constexpr int kScoreThreads = 256, kScorePages = 32;   // pages of a warp
-constexpr int kPickThreads = 256, kBins = 1024;
-constexpr int kKeysInShared = 8192;                    // pages whose scores a block holds
+constexpr int kBoundThreads = 256, kBoundRows = 64;
+constexpr int kScoreThreads = 128, kLeastPages = 16;   // pages of a warp at least
+constexpr int kBinBits = 11, kBins = 1 << kBinBits, kNear = 256;
+constexpr int kHeld = 8;                               // keys of a lane
+constexpr int kHeldPages = 1024 * kHeld;               // pages whose keys a block holds
 
 template <typename T>
 struct Pair;
@@ -79,15 +79,19 @@ struct BoundParams {
   float k_scale;
 };
 
-// A block takes `span` rows of the write; a row whose page differs from that of
-// the row before owns the page, and a warp brings in the keys of one (page, head): eight
-// 16-byte loads a lane in flight, 32 / LPR keys each. Read once: bound by memory.
+// A block takes `span` rows of the write. A row whose page differs from that of the row
+// before owns the page; a warp finds how far its run of rows goes. Then a warp brings in
+// the keys of one (page, head) at a time, eight elements a lane and eight loads in
+// flight, 32 / LPR keys each. Read once: bound by memory, so the registers are kept few and
+// the warps many (bytes in flight).
 template <typename T, int D, int FMT>
-__global__ void __launch_bounds__(kBoundThreads) bounds_kernel(const __grid_constant__ BoundParams P) {
-  constexpr int E = FMT == POD_KV_16BIT ? 2 : 1, LPR = D * E / 16, KPL = 32 / LPR, U = 8;
-  constexpr int N = 16 / E;                            // elements of a lane's chunk
+__global__ void __launch_bounds__(kBoundThreads, FMT == POD_KV_E4M3 ? 5 : 4)
+    bounds_kernel(const __grid_constant__ BoundParams P) {
+  constexpr int E = FMT == POD_KV_16BIT ? 2 : 1, LPR = D / 8, KPL = 32 / LPR, U = 8;
   using M = typename std::conditional<FMT == POD_KV_16BIT, T, __half>::type;
-  __shared__ long long own[kBoundRows];
+  using Chunk = typename std::conditional<FMT == POD_KV_16BIT, uint4, uint2>::type;
+  __shared__ long long page_of[kBoundRows];
+  __shared__ int row_of[kBoundRows], keys_of[kBoundRows];
   __shared__ int owners;
   asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -95,143 +99,171 @@ __global__ void __launch_bounds__(kBoundThreads) bounds_kernel(const __grid_cons
   __syncthreads();
   const long long row0 = (long long)blockIdx.x * P.span;
   if (tid < P.span && row0 + tid < P.rows) {
-    const long long r = row0 + tid, s = P.slots[r];
+    const long long r = row0 + tid, s = P.slots[r], b = r ? P.slots[r - 1] : -1;
     if (s >= P.num_slots && P.status) atomicOr(P.status, kStatusSlot);
-    if (s >= 0 && s < P.num_slots) {
-      const long long b = r ? P.slots[r - 1] : -1;
-      if (b < 0 || b / P.ps != s / P.ps) own[atomicAdd(&owners, 1)] = r;
+    if (s >= 0 && s < P.num_slots && (b < 0 || b / P.ps != s / P.ps)) {
+      const int at = atomicAdd(&owners, 1);
+      row_of[at] = tid;
+      page_of[at] = s / P.ps;
     }
   }
   __syncthreads();
-  const int tasks = owners * P.Hk;
-  for (int i = warp; i < tasks; i += kBoundThreads / 32) {
-    const long long r = own[i / P.Hk];
-    const int h = i - i / P.Hk * P.Hk;
-    const long long page = P.slots[r] / P.ps;
-    // the page's rows of the write stand behind r
+  const int n = owners;
+  for (int i = warp; i < n; i += kBoundThreads / 32) {
+    // the page's rows of the write stand behind the first
+    const long long page = page_of[i];
     int valid = 0;
-    for (long long a = r; a < P.rows; a += 32) {
+    for (long long a = row0 + row_of[i]; a < P.rows; a += 32) {
       const long long s = a + lane < P.rows ? P.slots[a + lane] : -1;
-      const unsigned same = __ballot_sync(0xffffffffu, s >= 0 && s / P.ps == page);
+      const unsigned same = __ballot_sync(0xffffffffu, s >= page * P.ps && s - page * P.ps < P.ps);
       const int run = same == 0xffffffffu ? 32 : __ffs(~same) - 1;
       valid = max(valid, __reduce_max_sync(0xffffffffu, lane < run ? (int)(s - page * P.ps) + 1 : 0));
       if (run < 32) break;
     }
-    const long long row = (page * 2 * P.Hk * P.ps + (P.hnd ? (long long)h * P.ps : h));   // of key 0, in rows of D
+    if (lane == 0) keys_of[i] = valid;
+  }
+  __syncthreads();
+  const int part = lane % LPR, sub = lane / LPR;
+  for (int i = warp; i < n * P.Hk; i += kBoundThreads / 32) {
+    const int o = i / P.Hk, h = i - o * P.Hk, valid = keys_of[o];
+    const long long page = page_of[o];
+    const long long row = page * 2 * P.Hk * P.ps + (P.hnd ? (long long)h * P.ps : h);   // of key 0, in rows of D
     const int step = P.hnd ? 1 : P.Hk;
-    const int part = lane % LPR, sub = lane / LPR;
     uint32_t lo2[4], hi2[4];                           // packed extremes (not with block scales)
-    float lo[N], hi[N];
+    float lo[8], hi[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       lo2[e] = Pair<M>::kInf;
       hi2[e] = Pair<M>::kInf | 0x80008000u;
     }
-    uint32_t lo3[4], hi3[4];                           // (the upper half of a chunk of 16 codes)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      lo3[e] = lo2[e];
-      hi3[e] = hi2[e];
-    }
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
+    for (int e = 0; e < 8; ++e) {
       lo[e] = INFINITY;
       hi[e] = -INFINITY;
     }
     for (int k0 = 0; k0 < valid; k0 += KPL * U) {
-      uint4 x[U];
+      Chunk x[U];
       int eb[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int k = k0 + u * KPL + sub;
         if (k < valid) {
           const long long at = row + (long long)k * step;
-          x[u] = __ldcs(reinterpret_cast<const uint4*>(P.cache + at * (D * E)) + part);
+          x[u] = __ldcs(reinterpret_cast<const Chunk*>(P.cache + at * (D * E)) + part);
           if (FMT == POD_KV_E4M3_BLOCK) eb[u] = P.scales[at];
         }
       }
+      if constexpr (FMT == POD_KV_16BIT) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (k0 + u * KPL + sub >= valid) continue;
-        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        for (int u = 0; u < U; ++u) {
+          if (k0 + u * KPL + sub >= valid) continue;
+          const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (FMT == POD_KV_16BIT) {
+          for (int e = 0; e < 4; ++e) {
             lo2[e] = min2<M>(lo2[e], w[e]);
             hi2[e] = max2<M>(hi2[e], w[e]);
-          } else {
-            const uint32_t a = e4m3x2_to<__half>((uint16_t)w[e]), b = e4m3x2_to<__half>((uint16_t)(w[e] >> 16));
-            if constexpr (FMT == POD_KV_E4M3) {
+          }
+        }
+      } else {
+        // Block scales: the keys' values relative to the largest exponent among them are exact
+        // in fp16 down to 15 binades below it; pages whose exponents lie further apart take
+        // the fp32 way. (Packed, the kernel has half the instructions, which bound it.)
+        int e_hi = 0, e_lo = 255;
+        bool close = true;
+        if constexpr (FMT == POD_KV_E4M3_BLOCK) {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (k0 + u * KPL + sub < valid) {
+              e_hi = max(e_hi, eb[u]);
+              e_lo = min(e_lo, eb[u]);
+            }
+          e_hi = __reduce_max_sync(0xffffffffu, e_hi);
+          e_lo = __reduce_min_sync(0xffffffffu, e_lo);
+          close = e_hi - e_lo <= 15;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (k0 + u * KPL + sub >= valid) continue;
+          const uint32_t w[2] = {x[u].x, x[u].y};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t a = e4m3x2_to<__half>((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+            if (FMT == POD_KV_E4M3 || close) {
+              if constexpr (FMT == POD_KV_E4M3_BLOCK) {
+                // 2^(eb - e_hi) twice: fp16's exponent bias is 15, a normal number down to 2^-14
+                const int f = eb[u] - e_hi;
+                const uint32_t s = f < -14 ? 0x02000200u : (uint32_t)(f + 15) << 10 | (uint32_t)(f + 15) << 26;
+                const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<const __half2*>(&s));
+                a = *reinterpret_cast<const uint32_t*>(&y);
+              }
               lo2[e] = min2<M>(lo2[e], a);
               hi2[e] = max2<M>(hi2[e], a);
-              lo3[e] = min2<M>(lo3[e], b);
-              hi3[e] = max2<M>(hi3[e], b);
             } else {
               const float s = eb[u] ? __uint_as_float((uint32_t)eb[u] << 23) : 5.877471754111438e-39f;
-              const float2 fa = Pack<__half>::unpack(a), fb = Pack<__half>::unpack(b);
-              const float y[4] = {fa.x * s, fa.y * s, fb.x * s, fb.y * s};
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                lo[4 * e + c] = fminf(lo[4 * e + c], y[c]);
-                hi[4 * e + c] = fmaxf(hi[4 * e + c], y[c]);
-              }
+              const float2 f = Pack<__half>::unpack(a);
+              const float y0 = f.x * s, y1 = f.y * s;
+              lo[2 * e] = fminf(lo[2 * e], y0);
+              hi[2 * e] = fmaxf(hi[2 * e], y0);
+              lo[2 * e + 1] = fminf(lo[2 * e + 1], y1);
+              hi[2 * e + 1] = fmaxf(hi[2 * e + 1], y1);
             }
           }
         }
-      }
-    }
-    // packed extremes as values
-    if constexpr (FMT != POD_KV_E4M3_BLOCK) {
+        if (FMT == POD_KV_E4M3_BLOCK && close) {
+          // these keys' extremes, as values (the infinities of an empty lane stay what they are)
+          const float s = e_hi ? __uint_as_float((uint32_t)e_hi << 23) : 5.877471754111438e-39f;
 #pragma unroll
-      for (int o = LPR; o < 32; o <<= 1)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          lo2[e] = min2<M>(lo2[e], __shfl_xor_sync(0xffffffffu, lo2[e], o));
-          hi2[e] = max2<M>(hi2[e], __shfl_xor_sync(0xffffffffu, hi2[e], o));
-          if constexpr (FMT == POD_KV_E4M3) {
-            lo3[e] = min2<M>(lo3[e], __shfl_xor_sync(0xffffffffu, lo3[e], o));
-            hi3[e] = max2<M>(hi3[e], __shfl_xor_sync(0xffffffffu, hi3[e], o));
+          for (int e = 0; e < 4; ++e) {
+            const float2 a = Pack<__half>::unpack(lo2[e]), b = Pack<__half>::unpack(hi2[e]);
+            lo[2 * e] = fminf(lo[2 * e], a.x * s);
+            lo[2 * e + 1] = fminf(lo[2 * e + 1], a.y * s);
+            hi[2 * e] = fmaxf(hi[2 * e], b.x * s);
+            hi[2 * e + 1] = fmaxf(hi[2 * e + 1], b.y * s);
+            lo2[e] = Pair<M>::kInf;
+            hi2[e] = Pair<M>::kInf | 0x80008000u;
           }
         }
+      }
+    }
+    if constexpr (FMT != POD_KV_E4M3_BLOCK) {
+      // packed extremes as values
       const float s = FMT == POD_KV_E4M3 ? P.k_scale : 1.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 a = Pack<M>::unpack(lo2[e]), b = Pack<M>::unpack(hi2[e]);
-        if constexpr (FMT == POD_KV_16BIT) {
-          lo[2 * e] = a.x; lo[2 * e + 1] = a.y;
-          hi[2 * e] = b.x; hi[2 * e + 1] = b.y;
-        } else {
-          const float2 c = Pack<M>::unpack(lo3[e]), d = Pack<M>::unpack(hi3[e]);
-          lo[4 * e] = a.x * s; lo[4 * e + 1] = a.y * s; lo[4 * e + 2] = c.x * s; lo[4 * e + 3] = c.y * s;
-          hi[4 * e] = b.x * s; hi[4 * e + 1] = b.y * s; hi[4 * e + 2] = d.x * s; hi[4 * e + 3] = d.y * s;
+#pragma unroll
+        for (int d = LPR; d < 32; d <<= 1) {
+          lo2[e] = min2<M>(lo2[e], __shfl_xor_sync(0xffffffffu, lo2[e], d));
+          hi2[e] = max2<M>(hi2[e], __shfl_xor_sync(0xffffffffu, hi2[e], d));
         }
+        const float2 a = Pack<M>::unpack(lo2[e]), b = Pack<M>::unpack(hi2[e]);
+        lo[2 * e] = FMT == POD_KV_E4M3 ? a.x * s : a.x;
+        lo[2 * e + 1] = FMT == POD_KV_E4M3 ? a.y * s : a.y;
+        hi[2 * e] = FMT == POD_KV_E4M3 ? b.x * s : b.x;
+        hi[2 * e + 1] = FMT == POD_KV_E4M3 ? b.y * s : b.y;
       }
     } else {
 #pragma unroll
-      for (int o = LPR; o < 32; o <<= 1)
+      for (int d = LPR; d < 32; d <<= 1)
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          lo[e] = fminf(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], o));
-          hi[e] = fmaxf(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], o));
+        for (int e = 0; e < 8; ++e) {
+          lo[e] = fminf(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], d));
+          hi[e] = fmaxf(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], d));
         }
     }
-    T* dst = static_cast<T*>(P.bounds) + (page * P.Hk + h) * 2 * D + part * N;
+    T* dst = static_cast<T*>(P.bounds) + (page * P.Hk + h) * 2 * D + part * 8;
     auto put = [&](T* to, const float* v, bool upper) {
-      T y[N];
+      uint32_t w[4];
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float c = fminf(fmaxf(v[e], -Pair<T>::kMax), Pair<T>::kMax);
-        y[e] = upper ? Pair<T>::up(c) : Pair<T>::down(c);
+      for (int e = 0; e < 4; ++e) {
+        T y[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float z = fminf(fmaxf(v[2 * e + c], -Pair<T>::kMax), Pair<T>::kMax);
+          y[c] = upper ? Pair<T>::up(z) : Pair<T>::down(z);
+        }
+        w[e] = (uint32_t)*reinterpret_cast<uint16_t*>(&y[0]) | (uint32_t)*reinterpret_cast<uint16_t*>(&y[1]) << 16;
       }
-#pragma unroll
-      for (int e = 0; e < N; e += 8) {
-        uint32_t w[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          w[c] = (uint32_t)*reinterpret_cast<uint16_t*>(&y[e + 2 * c]) |
-                 (uint32_t)*reinterpret_cast<uint16_t*>(&y[e + 2 * c + 1]) << 16;
-        *reinterpret_cast<uint4*>(to + e) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
     };
     if (sub == 0) put(dst, lo, false);
     if (sub == KPL - 1) put(dst + D, hi, true);
@@ -251,7 +283,7 @@ struct PickParams {
   double* again;                   // [batch, Hk, width]: scores computed again
   long long q_stride, table_stride;
   unsigned num_pages;
-  int batch, Hk, G, width, chunks, ps, k, first, last;
+  int batch, Hk, G, width, per, chunks, ps, k, first, last;   // per: pages of a warp, a chunk
 };
 
 POD_DEV int pages_of(const PickParams& P, int row) {
@@ -259,11 +291,20 @@ POD_DEV int pages_of(const PickParams& P, int row) {
   return (min(max(len, 0), most) + P.ps - 1) / P.ps;
 }
 
-// A warp scores 32 pages for one head: a page's bounds are 4 D bytes, 16 a lane, eight
-// loads in flight; the eight sums cross the lanes together (nine shuffles). Bound by memory.
+// A warp scores `per` pages for one head: a page's bounds are 4 D bytes, 16 a lane. Each
+// lane copies its own 16 bytes of eight pages into a ring of its own in shared memory,
+// two sets ahead of the one that is summed (asynchronous copies: no registers, and no
+// other lane to wait for); the eight sums cross the lanes together (nine shuffles).
+// Bound by memory. With the sets held in registers instead: 67 us (one set, 24 warps
+// an SM) and 91 us (two sets, 16 warps) where the ring takes RING_US.
+constexpr int kRing = 3;
+constexpr int kScoreShared = kScoreThreads / 32 * kRing * 8 * 32 * 16;
+static_assert(kScoreShared <= 48 * 1024, "what a launch may ask for without an attribute of the kernel");
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_constant__ PickParams P) {
-  constexpr int LPP = D == 64 ? 16 : 32, NC = D == 256 ? 2 : 1, PPL = 32 / LPP, U = 8;
+__global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_constant__ PickParams P) {
+  constexpr int LPP = D == 64 ? 16 : 32, NC = D == 256 ? 2 : 1, PPL = 32 / LPP, U = 8 / NC, STEP = U * PPL;
+  extern __shared__ uint4 ring[];
   asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const long long task = (long long)blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);
@@ -272,19 +313,49 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_const
   const int chunk = (int)(rest % P.chunks);
   const int row = (int)(rest / P.chunks);
   if (row >= P.batch) return;
-  const int n = pages_of(P, row), page0 = chunk * kScorePages;
-  if (page0 >= n || n <= P.k) return;                  // (then all are chosen)
-  int id = -1;
-  if (page0 + lane < n) {
-    id = P.table[row * P.table_stride + page0 + lane];
-    if ((unsigned)id >= P.num_pages) {
-      id = -1;
-      if (P.status) atomicOr(P.status, kStatusSlot);
-    }
-  }
-  // this lane's channels and its weights: smallest values first, then largest
+  const int page0 = chunk * P.per;
+  // (the table's entries and q do not wait for the length: one trip to memory)
+  const int32_t* table = P.table + row * P.table_stride + page0;
+  int id = page0 + lane < P.width && lane < P.per ? table[lane] : -1;
+  int after = page0 + 32 + lane < P.width && 32 + lane < P.per ? table[32 + lane] : -1;
+  const int n = pages_of(P, row), mine = min(P.per, n - page0);
+  if (mine <= 0 || n <= P.k) return;                   // (n <= k: all are chosen)
   const int c = lane % LPP;
-  float w[NC][8], mag = 0.f;
+  const T* bounds = static_cast<const T*>(P.bounds) + (long long)hk * 2 * D + c * 8;
+  float* score = P.score + ((long long)row * P.Hk + hk) * P.width + page0;
+  // entries 32 i + lane of the table, one set ahead
+  auto checked = [&](int x, int p) {
+    if (p >= mine) return -1;
+    if ((unsigned)x < P.num_pages) return x;
+    if (P.status) atomicOr(P.status, kStatusSlot);
+    return -1;
+  };
+  id = checked(id, lane);                              // of the pages that are asked for
+  int asked = 0;
+  uint4* slots = ring + (threadIdx.x >> 5) * (kRing * 256) + lane;
+  auto ask = [&]() {
+    if (asked < mine) {
+      if (asked && asked % 32 == 0) {
+        id = checked(after, asked + lane);
+        after = asked + 32 + lane < mine ? table[asked + 32 + lane] : -1;
+      }
+      uint4* to = slots + asked / STEP % kRing * 256;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int at = __shfl_sync(0xffffffffu, id, (asked + u * PPL + lane / LPP) & 31);
+        const T* from = bounds + (long long)(at < 0 ? 0 : at) * P.Hk * 2 * D;
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+          cp_async16(smem_u32(to + (u * NC + i) * 32), from + i * D, at < 0 ? 0u : 16u);
+      }
+    }
+    cp_async_commit();
+    asked += STEP;
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) ask();
+  // this lane's channels and its weights: smallest values first, then largest
+  float w[NC][8];
 #pragma unroll
   for (int i = 0; i < NC; ++i)
 #pragma unroll
@@ -293,7 +364,7 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_const
     const int j0 = c * 8 % D;
     const bool largest = c * 8 >= D;
     const T* q = static_cast<const T*>(P.q) + row * P.q_stride + (long long)hk * P.G * D + j0;
-#pragma unroll 4
+#pragma unroll 8
     for (int g = 0; g < P.G; ++g) {
       const uint4 r = *reinterpret_cast<const uint4*>(q + (long long)g * D);
       const uint32_t u[4] = {r.x, r.y, r.z, r.w};
@@ -310,73 +381,69 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_const
       }
     }
   }
-  const T* bounds = static_cast<const T*>(P.bounds) + (long long)hk * 2 * D + c * 8;
-  float* score = P.score + ((long long)row * P.Hk + hk) * P.width;
-  uint32_t top[NC];                                    // largest magnitudes seen
+  uint32_t top[NC][4];                                 // largest magnitudes seen, per channel
 #pragma unroll
-  for (int i = 0; i < NC; ++i) top[i] = 0u;
-  for (int p0 = 0; p0 < kScorePages && page0 + p0 < n; p0 += U * PPL) {
-    uint4 x[U][NC];
-    int at[U];
+  for (int i = 0; i < NC; ++i)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      at[u] = __shfl_sync(0xffffffffu, id, p0 + u * PPL + lane / LPP);
+    for (int e = 0; e < 4; ++e) top[i][e] = 0u;
+  for (int p0 = 0; p0 < mine; p0 += STEP) {
+    ask();
+    cp_async_wait<kRing - 1>();
+    const uint4* from = slots + p0 / STEP % kRing * 256;
+    float s[8];
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        x[u][i] = make_uint4(0, 0, 0, 0);
-        if (at[u] >= 0)
-          x[u][i] = __ldcs(reinterpret_cast<const uint4*>(bounds + (long long)at[u] * P.Hk * 2 * D + i * D));
-      }
-    }
-    float s[U];
+    for (int u = 0; u < 8; ++u) s[u] = 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      s[u] = 0.f;
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const uint32_t v[4] = {x[u][i].x, x[u][i].y, x[u][i].z, x[u][i].w};
+        const uint4 x = from[(u * NC + i) * 32];
+        const uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 f = Pack<T>::unpack(v[e]);
           s[u] = fmaf(f.x, w[i][2 * e], s[u]);
           s[u] = fmaf(f.y, w[i][2 * e + 1], s[u]);
-          top[i] = max2<T>(top[i], v[e] & 0x7fff7fffu);
+          top[i][e] = max2<T>(top[i][e], v[e] & 0x7fff7fffu);
         }
       }
-    }
-    // sums over the lanes of a page: halves of the eight go to halves of the lanes
+    // sums over the lanes of a page: halves of the sums go to halves of the lanes
     constexpr int O1 = LPP / 2, O2 = LPP / 4, O3 = LPP / 8;
     float s4[4], s2[2], s1;
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      s4[u] = (lane & O1 ? s[u + 4] : s[u]) + __shfl_xor_sync(0xffffffffu, lane & O1 ? s[u] : s[u + 4], O1);
+    for (int u = 0; u < 4; ++u) {
+      if (U == 8) s4[u] = (lane & O1 ? s[u + 4] : s[u]) + __shfl_xor_sync(0xffffffffu, lane & O1 ? s[u] : s[u + 4], O1);
+      else s4[u] = s[u] + __shfl_xor_sync(0xffffffffu, s[u], O1);
+    }
 #pragma unroll
     for (int u = 0; u < 2; ++u)
       s2[u] = (lane & O2 ? s4[u + 2] : s4[u]) + __shfl_xor_sync(0xffffffffu, lane & O2 ? s4[u] : s4[u + 2], O2);
     s1 = (lane & O3 ? s2[1] : s2[0]) + __shfl_xor_sync(0xffffffffu, lane & O3 ? s2[0] : s2[1], O3);
 #pragma unroll
     for (int o = O3 / 2; o; o >>= 1) s1 += __shfl_xor_sync(0xffffffffu, s1, o);
-    const int u = (lane & O1 ? 4 : 0) + (lane & O2 ? 2 : 0) + (lane & O3 ? 1 : 0);
+    const int u = (U == 8 && (lane & O1) ? 4 : 0) + (lane & O2 ? 2 : 0) + (lane & O3 ? 1 : 0);
     const int p = p0 + u * PPL + lane / LPP;
-    const int mine = __shfl_sync(0xffffffffu, id, p);
-    if ((lane & (O3 - 1)) == 0 && page0 + p < n) score[page0 + p] = mine < 0 ? -INFINITY : s1;
+    const bool writes = (lane & (O3 - 1)) == 0 && (U == 8 || !(lane & O1));
+    if (writes && p < mine) score[p] = s1;
   }
+  // (pages outside the pool: few, and known by now)
+  for (int p = lane; p < mine; p += 32)
+    if ((unsigned)table[p] >= P.num_pages) score[p] = -INFINITY;
+  float mag = 0.f;
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const float2 m = Pack<T>::unpack(top[i]);
-    float sum = 0.f;
+  for (int i = 0; i < NC; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum += fabsf(w[i][e]);
-    // (0 times an infinity is a NaN, as a term of that kind is)
-    mag += sum * fmaxf(m.x, m.y);
-  }
+    for (int e = 0; e < 4; ++e) {
+      // (0 times an infinity is a NaN, as a term of that kind is)
+      const float2 m = Pack<T>::unpack(top[i][e]);
+      mag += fabsf(w[i][2 * e]) * m.x + fabsf(w[i][2 * e + 1]) * m.y;
+    }
 #pragma unroll
-  for (int o = LPP / 2; o; o >>= 1) mag += __shfl_xor_sync(0xffffffffu, mag, o);
-  if (PPL == 2) mag = mag + __shfl_xor_sync(0xffffffffu, mag, 16);
+  for (int o = 16; o; o >>= 1) mag += __shfl_xor_sync(0xffffffffu, mag, o);
   if (lane == 0)
     // (products of the smallest numbers are off by more than their part)
     P.off[((long long)row * P.Hk + hk) * P.chunks + chunk] =
-        mag == 0.f ? 0.f : mag * ((24.f + P.G) * 0x1.04p-24f) + 0x1p-140f;
+        mag == 0.f ? 0.f : mag * ((float)(8 * NC + 5 + P.G) * 0x1.04p-24f) + 0x1p-140f;
 }
 
 // ------------------------------------------------------------------ the choice
@@ -395,13 +462,18 @@ POD_DEV uint64_t key_of(double x) {
 
 struct PickShared {
   int bins[kBins];
-  int sums[kPickThreads / 32 + 1];
-  unsigned long long lo[kPickThreads / 32], hi[kPickThreads / 32];
-  int bin, above;
+  unsigned long long lo[32], hi[32];
+  int sums[32];
+  uint32_t near[kNear];            // keys, or pages
+  double exact[kNear];
+  uint32_t chosen[kHeldPages / 32];
+  int nears, bin, above;
+  uint32_t kth;
 };
 
-POD_DEV int block_sum_before(int x, int& all, PickShared& S) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Sum of x over the threads before this one.
+POD_DEV int block_sum_before(int x, PickShared& S) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   int s = x;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -411,30 +483,54 @@ POD_DEV int block_sum_before(int x, int& all, PickShared& S) {
   __syncthreads();
   if (lane == 31) S.sums[warp] = s;
   __syncthreads();
-  int before = 0;
-  all = 0;
-#pragma unroll
-  for (int w = 0; w < kPickThreads / 32; ++w) {
-    before += w < warp ? S.sums[w] : 0;
-    all += S.sums[w];
-  }
-  return before + s - x;
+  const int w = lane < warps && lane < warp ? S.sums[lane] : 0;
+  return s - x + __reduce_add_sync(0xffffffffu, w);
 }
 
-// The need-th largest (1 is the largest) of the keys key(i), i in [a, b), that are in
-// [lo, hi], of which there are at least `need`; `above` receives how many are larger.
-// The range between the smallest and the largest is cut into 1024 bins, then the bin
+// Two counts of a warp (the same in its lanes): those of the warps before it, and of all.
+POD_DEV int2 warp_sums_before(int x, int y, int2& all, PickShared& S) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  __syncthreads();
+  if (lane == 0) S.lo[warp] = (unsigned long long)(unsigned)x << 32 | (unsigned)y;
+  __syncthreads();
+  const unsigned long long w = lane < warps ? S.lo[lane] : 0ull;
+  const int wx = (int)(w >> 32), wy = (int)(unsigned)w;
+  all = make_int2(__reduce_add_sync(0xffffffffu, wx), __reduce_add_sync(0xffffffffu, wy));
+  return make_int2(__reduce_add_sync(0xffffffffu, lane < warp ? wx : 0), __reduce_add_sync(0xffffffffu, lane < warp ? wy : 0));
+}
+
+// In which bin, counted from the top, is the need-th largest? `above` keys are larger
+// than all bins. Leaves the bin and the number of keys above it in S.
+POD_DEV void find_bin(int need, int above, PickShared& S) {
+  const int per = kBins / blockDim.x, top = kBins - 1 - (int)threadIdx.x * per;   // (blockDim divides kBins)
+  int sum = 0;
+  for (int i = 0; i < per; ++i) sum += S.bins[top - i];
+  int before = above + block_sum_before(sum, S);
+  if (before < need && before + sum >= need)
+    for (int i = 0; i < per; ++i) {
+      const int n = S.bins[top - i];
+      if (before < need && before + n >= need) {
+        S.bin = top - i;
+        S.above = before;
+      }
+      before += n;
+    }
+  __syncthreads();
+}
+
+// The need-th largest (1 is the largest) of the keys that each() hands out, those that are
+// at least `from`, of which there are at least `need`; `above` receives how many are larger.
+// The range between the smallest and the largest is cut into bins, then the bin
 // with the wanted key again, until a bin is one key.
-template <typename K, typename F>
-POD_DEV K kth_largest(F key, int a, int b, K from, K to, int need, int& above, PickShared& S) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+template <typename F>
+POD_DEV uint64_t kth_largest(F each, uint64_t from, int need, int& above, PickShared& S) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x;
   unsigned long long lo = ~0ull, hi = 0;
-  for (int i = a + tid; i < b; i += kPickThreads) {
-    const K x = key(i);
-    if (x < from || x > to) continue;
+  each([&](int, uint64_t x) {
+    if (x < from) return;
     lo = min(lo, (unsigned long long)x);
     hi = max(hi, (unsigned long long)x);
-  }
+  });
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
@@ -446,54 +542,179 @@ POD_DEV K kth_largest(F key, int a, int b, K from, K to, int need, int& above, P
     S.hi[warp] = hi;
   }
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kPickThreads / 32; ++w) {
+  for (int w = 0; w < T / 32; ++w) {
     lo = min(lo, S.lo[w]);
     hi = max(hi, S.hi[w]);
   }
   above = 0;
   while (lo < hi) {
-    const int bits = 64 - __clzll((long long)(hi - lo)), shift = max(0, bits - 10);
-    for (int i = tid; i < kBins; i += kPickThreads) S.bins[i] = 0;
+    const int bits = 64 - __clzll((long long)(hi - lo)), shift = max(0, bits - kBinBits);
+    for (int i = tid; i < kBins; i += T) S.bins[i] = 0;
     __syncthreads();
-    for (int i = a + tid; i < b; i += kPickThreads) {
-      const unsigned long long x = key(i);
+    each([&](int, uint64_t x) {
       if (x >= lo && x <= hi) atomicAdd(&S.bins[(x - lo) >> shift], 1);
-    }
+    });
     __syncthreads();
-    // from the top: a thread's four bins, the sum of those above them
-    constexpr int PER = kBins / kPickThreads;
-    int mine[PER], sum = 0, all;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      mine[i] = S.bins[kBins - 1 - (tid * PER + i)];
-      sum += mine[i];
-    }
-    int before = above + block_sum_before(sum, all, S);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if (before < need && before + mine[i] >= need) {
-        S.bin = kBins - 1 - (tid * PER + i);
-        S.above = before;
-      }
-      before += mine[i];
-    }
-    __syncthreads();
+    find_bin(need, above, S);
     above = S.above;
     lo += (unsigned long long)S.bin << shift;
     hi = lo + min(hi - lo, (1ull << shift) - 1);
     __syncthreads();
   }
-  return (K)lo;
+  return lo;
 }
 
+// The exact score of the page at position i: a warp's lanes share the channels.
 template <typename T, int D>
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constant__ PickParams P) {
-  extern __shared__ uint32_t sh_keys[];
+POD_DEV double score_64(const PickParams& P, int row, int hk, int i, const double (*weight)[D]) {
+  const unsigned page = (unsigned)P.table[row * P.table_stride + i];
+  if (page >= P.num_pages) return -INFINITY;
+  const int lane = threadIdx.x & 31;
+  const T* m = static_cast<const T*>(P.bounds) + ((long long)page * P.Hk + hk) * 2 * D;
+  double s = 0.;
+#pragma unroll
+  for (int j = lane; j < D; j += 32)
+    s += (double)(float)m[j] * weight[0][j] + (double)(float)m[D + j] * weight[1][j];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+// The pages [a, b) whose fp32 keys are in [least, sure], `close` of them, scored again in
+// 64 bits; of them `ties` are chosen. Few, whose positions stand in S.near: the chosen
+// ones' bits are set in S.chosen, and 0 is returned. Many: their scores are kept, the last
+// chosen one's key is returned, and in `ties` how many of that score.
+template <typename T, int D>
+__device__ __noinline__ uint64_t score_again(const PickParams& P, bool few, int row, int hk, int a, int b, uint32_t least,
+                                             uint32_t sure, int close, int& ties, PickShared& S) {
+  __shared__ double weight[2][D];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+  const long long item = (long long)row * P.Hk + hk;
+  const T* q = static_cast<const T*>(P.q) + row * P.q_stride + (long long)hk * P.G * D;
+  for (int j = tid; j < D; j += threads) {
+    double up = 0., down = 0.;
+    for (int g = 0; g < P.G; ++g) {
+      const double x = (double)(float)q[(long long)g * D + j];
+      up += x < 0. ? 0. : x;
+      down += x > 0. ? 0. : x;
+    }
+    weight[0][j] = down;
+    weight[1][j] = up;
+  }
+  __syncthreads();
+  if (few) {
+    for (int c = warp; c < close; c += threads / 32) {
+      const double s = score_64<T, D>(P, row, hk, (int)S.near[c], weight);
+      if (lane == 0) S.exact[c] = s;
+    }
+    __syncthreads();
+    for (int c = tid; c < close; c += threads) {
+      const uint64_t x = key_of(S.exact[c]);
+      const int i = (int)S.near[c];
+      int before = 0;
+      for (int d = 0; d < close; ++d) {
+        const uint64_t y = key_of(S.exact[d]);
+        before += y > x || (y == x && (int)S.near[d] < i);
+      }
+      if (before < ties) atomicOr(&S.chosen[i >> 5], 1u << (i & 31));
+    }
+    __syncthreads();
+    return 0;
+  }
+  const float* score = P.score + item * P.width;
+  double* again = P.again + item * P.width;
+  auto is_close = [&](int i) {
+    const uint32_t x = key_of(score[i]);
+    return x >= least && x <= sure;
+  };
+  for (int i = a + warp; i < b; i += threads / 32) {
+    if (!is_close(i)) continue;
+    const double s = score_64<T, D>(P, row, hk, i, weight);
+    if (lane == 0) again[i] = s;
+  }
+  __syncthreads();
+  int larger;
+  const uint64_t last = kth_largest(
+      [&](auto f) {
+        for (int i = a + tid; i < b; i += threads)
+          if (is_close(i)) f(i, key_of(again[i]));
+      },
+      1ull, ties, larger, S);
+  ties -= larger;
+  return last;
+}
+
+// The need-th largest of the keys that each() hands out, all of them of finite numbers, 0 for
+// none: bins over the range of the values, then the keys of the wanted bin by their
+// ranks among themselves, where they are few.
+template <typename F>
+POD_DEV uint32_t kth_score(F each, int need, PickShared& S) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x;
+  uint32_t lo = 0xffffffffu, hi = 0u;
+  each([&](int, uint32_t x) {
+    lo = min(lo, x - 1);                               // (0 is not the smallest)
+    hi = max(hi, x);
+  });
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    S.lo[warp] = lo;
+    S.hi[warp] = hi;
+  }
+  for (int i = tid; i < kBins; i += T) S.bins[i] = 0;
+  if (tid == 0) S.nears = 0;
+  __syncthreads();
+  {
+    const int w = lane < T / 32 ? lane : 0;
+    lo = __reduce_min_sync(0xffffffffu, (uint32_t)S.lo[w]) + 1;
+    hi = __reduce_max_sync(0xffffffffu, (uint32_t)S.hi[w]);
+  }
+  if (lo == hi) return lo;
+  // (monotone: a difference, a product and a truncation, each rounded in order)
+  const float v0 = value_of(lo), scale = (kBins - 1) / fmaxf(value_of(hi) - v0, 1e-30f);
+  auto bin_of = [&](uint32_t x) { return min(kBins - 1, (int)((value_of(x) - v0) * scale)); };
+  each([&](int, uint32_t x) {
+    if (x) atomicAdd(&S.bins[bin_of(x)], 1);
+  });
+  __syncthreads();
+  find_bin(need, 0, S);
+  const int bin = S.bin, above = S.above, count = S.bins[bin];
+  if (count <= kNear) {
+    each([&](int, uint32_t x) {
+      if (x && bin_of(x) == bin) S.near[atomicAdd(&S.nears, 1)] = x;
+    });
+    __syncthreads();
+    for (int i = tid; i < count; i += T) {
+      const uint32_t x = S.near[i];
+      int larger = above, same = 0;
+      for (int j = 0; j < count; ++j) {
+        larger += S.near[j] > x;
+        same += S.near[j] == x;
+      }
+      if (larger < need && larger + same >= need) S.kth = x;
+    }
+    __syncthreads();
+    return S.kth;
+  }
+  int larger;
+  return (uint32_t)kth_largest(
+      [&](auto f) {
+        each([&](int i, uint32_t x) {
+          if (x && bin_of(x) == bin) f(i, (uint64_t)x);
+        });
+      },
+      1ull, need - above, larger, S);
+}
+
+// A block makes one choice. HELD: the keys of up to 256 pages a warp, eight a lane, stay in
+// registers (read from memory in every pass instead, for more pages than a block can hold,
+// and three times the instructions). A run of pages is a warp's, so that the chosen
+// ones come out in order.
+template <typename T, int D, bool HELD>
+__global__ void __launch_bounds__(1024) pick_kernel(const __grid_constant__ PickParams P) {
   __shared__ PickShared S;
-  __shared__ double sh_w[2][D];
   asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
   const long long item = blockIdx.x;
   const int row = (int)(item / P.Hk), hk = (int)(item - (long long)row * P.Hk);
   const int n = pages_of(P, row);
@@ -501,136 +722,114 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
     atomicOr(P.status, kStatusSlot);
   int32_t* out = P.pages + item * P.k;
   if (n <= P.k) {
-    for (int i = tid; i < P.k; i += kPickThreads) out[i] = i < n ? i : -1;
+    for (int i = tid; i < P.k; i += threads) out[i] = i < n ? i : -1;
     return;
   }
   // pages [a, b) compete for `need` places
   const int a = P.first, b = n - P.last, need = P.k - P.first - P.last;
   const float* score = P.score + item * P.width;
-  double* again = P.again + item * P.width;
+  const int run = HELD ? 32 * kHeld : ((n + 31) / 32 + warps - 1) / warps * 32;
+  const int i0 = min(n, warp * run), i1 = min(n, i0 + run);
   float off = 0.f;
-  bool odd = false;                                    // (an infinite or NaN bound)
-  for (int i = tid; i < (n + kScorePages - 1) / kScorePages; i += kPickThreads) {
+  bool odd = false;                                    // (an infinite or NaN bound or score)
+  for (int i = tid; i < (n + P.per - 1) / P.per; i += threads) {
     const float e = P.off[item * P.chunks + i];
     odd |= !(e < 0x1p100f);
     off = fmaxf(off, e);
   }
-  const bool held = n <= kKeysInShared;
-  if (held)
-    for (int i = tid; i < n; i += kPickThreads) sh_keys[i] = key_of(score[i]);
+  uint32_t held[HELD ? kHeld : 1];                     // 0: does not compete
+  auto read = [&](int i) {
+    if (i < a || i >= b || i >= i1) return 0u;
+    const float x = score[i];
+    odd |= !(fabsf(x) < 0x1p120f);
+    return key_of(x);
+  };
+  if constexpr (HELD) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) off = fmaxf(off, __shfl_xor_sync(0xffffffffu, off, o));
-  if (lane == 0) S.sums[warp] = __float_as_int(off);
-  odd = __syncthreads_or(odd);
-#pragma unroll
-  for (int w = 0; w < kPickThreads / 32; ++w) off = fmaxf(off, __int_as_float(S.sums[w]));
-  auto key = [&](int i) { return held ? sh_keys[i] : key_of(score[i]); };
-
-  // keys above `sure` are in, those from `least` to it compete on, by their score in 64
-  // bits where `exactly`
-  uint32_t sure = 0xffffffffu, least = 0xffffffffu;
-  uint64_t last64 = 0;
-  int ties = 0;
-  bool exactly = false;
-  if (need > 0) {
-    int above;
-    const uint32_t kth = kth_largest<uint32_t>(key, a, b, 0u, 0xffffffffu, need, above, S);
-    const float v = value_of(kth);
-    sure = least = kth;
-    if (off != 0.f || odd) {
-      if (odd || !(fabsf(v) < 0x1p120f)) {
-        sure = 0xffffffffu;
-        least = 0u;
-      } else {
-        sure = key_of(v + 2.5f * off);
-        least = key_of(v - 2.5f * off);
-      }
-    }
-    int in = 0, close = 0;
-    for (int i = a + tid; i < b; i += kPickThreads) {
-      const uint32_t x = key(i);
-      in += x > sure;
-      close += x >= least && x <= sure;
-    }
-    int all;
-    block_sum_before(in | close << 16, all, S);
-    // (counts past 16 bits: summed apart)
-    if (b - a >= 32768) {
-      block_sum_before(in, in, S);
-      block_sum_before(close, close, S);
-    } else {
-      in = all & 0xffff;
-      close = all >> 16;
-    }
-    ties = need - in;                                  // places for the close ones
-    if (close > ties && (off != 0.f || odd)) {
-      exactly = true;
-      // the weights, then a warp a page
-      const T* q = static_cast<const T*>(P.q) + row * P.q_stride + (long long)hk * P.G * D;
-      for (int j = tid; j < D; j += kPickThreads) {
-        double up = 0., down = 0.;
-        for (int g = 0; g < P.G; ++g) {
-          const double x = (double)(float)q[(long long)g * D + j];
-          up += x < 0. ? 0. : x;
-          down += x > 0. ? 0. : x;
-        }
-        sh_w[0][j] = down;
-        sh_w[1][j] = up;
-      }
-      __syncthreads();
-      for (int i = a + warp; i < b; i += kPickThreads / 32) {
-        const uint32_t x = key(i);
-        if (x < least || x > sure) continue;
-        const unsigned page = (unsigned)P.table[row * P.table_stride + i];
-        double s = 0.;
-        if (page < P.num_pages) {
-          const T* m = static_cast<const T*>(P.bounds) + ((long long)page * P.Hk + hk) * 2 * D;
-#pragma unroll 4
-          for (int j = lane; j < D; j += 32)
-            s += (double)(float)m[j] * sh_w[0][j] + (double)(float)m[D + j] * sh_w[1][j];
-#pragma unroll
-          for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        } else {
-          s = -INFINITY;
-        }
-        if (lane == 0) again[i] = s;
-      }
-      __syncthreads();
-      auto key64 = [&](int i) {
-        const uint32_t x = key(i);
-        return x >= least && x <= sure ? key_of(again[i]) : 0ull;
-      };
-      int larger;
-      last64 = kth_largest<uint64_t>(key64, a, b, 1ull, ~0ull, ties, larger, S);
-      ties -= larger;
-    }                                                  // (without an error, equal scores are ties)
+    for (int j = 0; j < kHeld; ++j) held[j] = read(i0 + j * 32 + lane);
+  } else {
+    for (int i = i0 + lane; i < i1; i += 32) read(i);
   }
-  // ---- in order: a run of pages a thread
-  const int per = (n + kPickThreads - 1) / kPickThreads, i0 = min(n, tid * per), i1 = min(n, i0 + per);
-  auto grade = [&](int i) {                            // 2: in, 1: in as far as places are left
+  auto each = [&](auto f) {                            // (the lanes of a warp together)
+    if constexpr (HELD) {
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) f(i0 + j * 32 + lane, held[j]);
+    } else {
+      for (int i = i0; i < i1; i += 32) {
+        const int k = i + lane;
+        f(k, k < a || k >= b || k >= i1 ? 0u : key_of(score[k]));
+      }
+    }
+  };
+  off = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(off)));
+  if (lane == 0) S.sums[warp] = __float_as_int(off);
+  if (tid < kHeldPages / 32) S.chosen[tid] = 0;
+  odd = __syncthreads_or(odd);
+  off = __uint_as_float(__reduce_max_sync(0xffffffffu, (unsigned)S.sums[lane < warps ? lane : 0]));
+
+  // keys above `sure` are in, those from `least` to it as far as places are left: the
+  // lowest positions, or by their scores in 64 bits
+  uint32_t sure = 0xffffffffu, least = 1u;
+  if (need > 0 && !odd) {
+    const uint32_t kth = kth_score(each, need, S);
+    const float v = value_of(kth);
+    sure = off == 0.f ? kth : key_of(v + 2.5f * off);
+    least = off == 0.f ? kth : key_of(v - 2.5f * off);
+  }
+  if (need == 0) least = 0xffffffffu, sure = 0xffffffffu;
+  uint64_t last64 = 0;
+  int again = 0;                                       // 1: the few are marked, 2: their scores are kept
+  const double* exact = P.again + item * P.width;
+  auto grade = [&](int i, uint32_t x) {                // 2: in, 1: in as far as places are left
+    if (i >= i1) return 0;
     if (i < a || i >= b) return 2;
-    if (need == 0) return 0;
-    const uint32_t x = key(i);
     if (x > sure) return 2;
-    if (x < least) return 0;
-    if (!exactly) return 1;
-    const uint64_t y = key_of(again[i]);
+    if (x < least || need == 0) return 0;
+    if (again == 0) return 1;
+    if (again == 1) return S.chosen[i >> 5] >> (i & 31) & 1 ? 2 : 0;
+    const uint64_t y = key_of(exact[i]);
     return y > last64 ? 2 : y == last64 ? 1 : 0;
   };
-  int full = 0, tied = 0, all;
-  for (int i = i0; i < i1; ++i) {
-    const int g = grade(i);
-    full += g == 2;
-    tied += g == 1;
+  int full, tied;
+  auto count = [&]() {
+    full = tied = 0;
+    each([&](int i, uint32_t x) {
+      const int g = grade(i, x);
+      full += __popc(__ballot_sync(0xffffffffu, g == 2));
+      tied += __popc(__ballot_sync(0xffffffffu, g == 1));
+    });
+  };
+  count();
+  int2 all, at = warp_sums_before(full, tied, all, S);
+  int ties = P.k - all.x;                              // places for the close ones
+  if (all.y > ties && (off != 0.f || odd)) {           // (without an error, equal scores are ties)
+    const bool few = HELD && all.y <= kNear;
+    if (few) {
+      if (tid == 0) S.nears = 0;
+      __syncthreads();
+      each([&](int i, uint32_t x) {
+        if (x >= least && x <= sure) S.near[atomicAdd(&S.nears, 1)] = (uint32_t)i;
+      });
+    }
+    last64 = score_again<T, D>(P, few, row, hk, a, b, least, sure, all.y, ties, S);
+    again = few ? 1 : 2;
+    count();
+    at = warp_sums_before(full, tied, all, S);
+    ties = P.k - all.x;
   }
-  int tied_at = block_sum_before(tied, all, S);
-  const int taken = min(max(ties - tied_at, 0), tied);
-  int to = block_sum_before(full + taken, all, S);
-  for (int i = i0; i < i1; ++i) {
-    const int g = grade(i);
-    if ((g == 2 || (g == 1 && tied_at < ties)) && to < P.k) out[to++] = i;
-    tied_at += g == 1;
-  }
+  // (full and tied of the warps before: at most `ties` of the tied are in)
+  int tied_at = at.y, to = at.x + min(at.y, ties);
+  const unsigned below = (1u << lane) - 1;
+  each([&](int i, uint32_t x) {
+    const int g = grade(i, x);
+    const unsigned m1 = __ballot_sync(0xffffffffu, g == 1);
+    const bool in = g == 2 || (g == 1 && tied_at + __popc(m1 & below) < ties);
+    const unsigned m = __ballot_sync(0xffffffffu, in);
+    const int slot = to + __popc(m & below);
+    if (in && slot < P.k) out[slot] = i;
+    to += __popc(m);
+    tied_at += __popc(m1);
+  });
 }
 
 // ------------------------------------------------------------------ host
@@ -676,11 +875,14 @@ cudaError_t launch_pick(const PickParams& P, cudaStream_t st) {
   const long long blocks = (warps + per - 1) / per, items = (long long)P.batch * P.Hk;
   if (blocks > 0x7fffffff || items > 0x7fffffff) return cudaErrorInvalidConfiguration;
   if (P.width > P.k) {                                 // (else every page is chosen)
-    const cudaError_t e = launch_beside(score_kernel<T, D>, (unsigned)blocks, kScoreThreads, 0, st, P);
+    const cudaError_t e = launch_beside(score_kernel<T, D>, (unsigned)blocks, kScoreThreads, kScoreShared, st, P);
     if (e != cudaSuccess) return e;
   }
-  const unsigned shared = 4u * (unsigned)(P.width < kKeysInShared ? P.width : kKeysInShared);
-  return launch_beside(pick_kernel<T, D>, (unsigned)items, kPickThreads, shared, st, P);
+  if (P.width > kHeldPages) return launch_beside(pick_kernel<T, D, false>, (unsigned)items, 1024, 0, st, P);
+  // threads that hold the longest row's keys
+  unsigned threads = 256;
+  while ((int)threads * kHeld < P.width) threads *= 2;
+  return launch_beside(pick_kernel<T, D, true>, (unsigned)items, threads, 0, st, P);
 }
 template <typename T>
 cudaError_t launch_pick_d(const PickParams& P, int d, cudaStream_t st) {
@@ -766,7 +968,7 @@ pod_status pod_page_bounds(const pod_decode_args* a, void* stream) {
   P.hnd = a->kv_layout;
   P.k_scale = a->k_scale;
   // few rows a block where there are few, so that every SM gets some
-  const int64_t span = (a->rows + 152 * 4 - 1) / (152 * 4);
+  const int64_t span = (a->rows + 152 * 8 - 1) / (152 * 8);
   P.span = (int)(span < kBoundRows ? span : kBoundRows);
   cudaStream_t s = (cudaStream_t)stream;
   const cudaError_t e = a->dtype == POD_BF16 ? launch_bounds_d<__nv_bfloat16>(P, a->head_dim, a->kv_format, s)
@@ -778,7 +980,7 @@ pod_status pod_page_bounds(const pod_decode_args* a, void* stream) {
 size_t pod_select_pages_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t table_width) {
   if (batch < 0 || num_kv_heads < 1 || table_width < 1) return 0;
   const size_t items = (size_t)batch * num_kv_heads;
-  const size_t chunks = ((size_t)table_width + kScorePages - 1) / kScorePages;
+  const size_t chunks = ((size_t)table_width + kLeastPages - 1) / kLeastPages;
   return round256(items * table_width * sizeof(double)) + round256(items * table_width * sizeof(float)) +
          round256(items * chunks * sizeof(float));
 }
@@ -813,7 +1015,11 @@ pod_status pod_select_pages(const pod_decode_args* a, void* stream) {
   P.Hk = a->num_kv_heads;
   P.G = a->num_qo_heads / a->num_kv_heads;
   P.width = a->table_width;
-  P.chunks = (a->table_width + kScorePages - 1) / kScorePages;
+  // pages of a warp: few where the SMs would not all be busy otherwise, more where that
+  // makes the weights less often
+  const int64_t pages = (int64_t)a->batch * a->num_kv_heads * a->table_width;
+  P.per = pages <= 152 * 16 * 32 ? kLeastPages : 64;
+  P.chunks = (a->table_width + P.per - 1) / P.per;
   P.ps = a->page_size;
   P.k = a->num_selected;
   P.first = a->keep_first;

@@ -8,7 +8,7 @@
 // are 64 bits wide, so no lengths can wrap them.
 //
 // Work split. The prefix sums depend on all requests, so one block makes them, a thread
-// a request (in rounds past its threads), and moves the pages, a warp a request. Where
+// a request (in rounds past its threads), and moves the pages, a thread a page. Where
 // the step may have many rows, or the page table is asked for, a second kernel
 // of many blocks writes them (a thread an entry, which finds its request by bisection
 // of the offsets); otherwise the first block does it too and the launch is spared.
@@ -30,6 +30,7 @@ namespace {
 
 constexpr int kStepThreads = 1024;
 constexpr int kRowThreads = 256;
+constexpr int kInFlight = 4;       // pages that a thread moves at a time
 
 struct StepParams {
   int32_t* table;
@@ -51,27 +52,37 @@ struct StepParams {
   int batch, width, ps, capacity, max_rows, max_pages, rows_here;
 };
 
-// Sum of x over the threads before this one, and over all of them.
-POD_DEV long long block_scan(long long x, long long& all, long long* sh) {
+// Sums of x[0..N) over the threads before this one (in place), and over all of them.
+template <int N>
+POD_DEV void block_scan(long long* x, long long* all, long long (*sh)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  long long s = x;
+  long long s[N];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += y;
+  for (int i = 0; i < N; ++i) {
+    s[i] = x[i];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, s[i], o);
+      if (lane >= o) s[i] += y;
+    }
   }
   __syncthreads();                                 // (sh may still be read)
-  if (lane == 31) sh[warp] = s;
-  __syncthreads();
-  const long long w = lane < warps ? sh[lane] : 0;
-  long long t = w;
+  if (lane == 31)
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, t, o);
-    if (lane >= o) t += y;
+    for (int i = 0; i < N; ++i) sh[warp][i] = s[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const long long w = lane < warps ? sh[lane][i] : 0;
+    long long t = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) t += y;
+    }
+    all[i] = __shfl_sync(0xffffffffu, t, 31);
+    x[i] = s[i] - x[i] + __shfl_sync(0xffffffffu, t - w, warp);
   }
-  all = __shfl_sync(0xffffffffu, t, 31);
-  return s - x + (warp ? __shfl_sync(0xffffffffu, t, (warp + 31) & 31) : 0);
 }
 
 struct Step {
@@ -123,12 +134,22 @@ POD_DEV void write_row(const StepParams& P, int i, int rows, const int32_t* indp
   P.slots[i] = slot;
 }
 
+// Last k < n with off[k] <= x (off ascending from off[0] <= x).
+POD_DEV int find_off(const int* off, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
 __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constant__ StepParams P) {
-  __shared__ long long sh[32];
-  __shared__ long long sh_off[kStepThreads];
-  __shared__ int sh_n[kStepThreads], sh_first[kStepThreads];
+  __shared__ long long sh2[32][2], sh3[32][3];
+  __shared__ int sh_off[kStepThreads], sh_first[kStepThreads];   // of the round's requests: pages before, first page moved
   asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x;
+  const int tid = threadIdx.x, T = blockDim.x;
   const long long count = min(max((long long)*P.free_count, 0ll), (long long)P.capacity);
   int bad = 0;                                     // status bits
   // ---- pages of shrinking requests go onto the stack
@@ -142,22 +163,31 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constan
       first = s.has;
     }
     if (!__syncthreads_or(n)) continue;            // (most steps take nothing back)
-    long long all;
-    const long long off = given + block_scan(n, all, sh);
-    sh_off[tid] = off;
-    sh_n[tid] = n;
+    long long x[2] = {n, 0}, all[2];
+    block_scan<2>(x, all, sh2);
+    // (a round gives back more than 2^31 pages only where the stack is long full)
+    sh_off[tid] = (int)min(x[0], 0x7fffffffll);
     sh_first[tid] = first;
-    __syncwarp();                                  // a warp moves its own lanes' requests
-    for (unsigned m = __ballot_sync(0xffffffffu, n > 0); m; m &= m - 1) {
-      const int k = warp * 32 + __ffs(m) - 1;
-      const int32_t* src = P.table + (long long)(base + k) * P.table_stride + sh_first[k];
-      for (int i = lane; i < sh_n[k]; i += 32) {
-        const long long to = count + sh_off[k] + i;
-        if (to < P.capacity) P.free_pages[to] = src[i];
-        else bad |= kStatusNoRoom;
-      }
+    __syncthreads();
+    const int moved = (int)min(all[0], max(0ll, P.capacity - count - given));
+    if (moved < all[0]) bad |= kStatusNoRoom;
+    const int32_t* from[kInFlight];
+    for (int i = tid; i < moved; i += T * kInFlight) {   // a thread a page, some at a time
+      int32_t page[kInFlight];
+#pragma unroll
+      for (int j = 0; j < kInFlight; ++j)
+        if (i + j * T < moved) {
+          const int k = find_off(sh_off, T, i + j * T);
+          from[j] = P.table + (long long)(base + k) * P.table_stride + sh_first[k] + i + j * T - sh_off[k];
+        }
+#pragma unroll
+      for (int j = 0; j < kInFlight; ++j)
+        if (i + j * T < moved) page[j] = *from[j];
+#pragma unroll
+      for (int j = 0; j < kInFlight; ++j)
+        if (i + j * T < moved) P.free_pages[count + given + i + j * T] = page[j];
     }
-    given += all;
+    given += all[0];
   }
   const long long top = min(count + given, (long long)P.capacity);
   // ---- growing requests take theirs off its top (pages pushed above are seen behind
@@ -170,9 +200,9 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constan
     bad |= s.status;
     const int need = s.wants ? s.has - s.had : 0;
     const long long n = s.wants ? s.now - s.old : 0;
-    long long all_pages, all_rows, all_kv, taken;
-    const long long p0 = pages + block_scan(need, all_pages, sh);
-    const long long r0 = rows + block_scan(n, all_rows, sh);
+    long long x[2] = {need, n}, all[2];
+    block_scan<2>(x, all, sh2);
+    const long long p0 = pages + x[0], r0 = rows + x[1];
     const bool granted = s.wants && p0 + need <= top && r0 + n <= P.max_rows;
     if (s.wants && !granted) {
       bad |= kStatusNoRoom;
@@ -180,32 +210,37 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constan
       s.has = s.had;
     }
     // (the granted ones come before every refused one)
-    block_scan(granted ? need : 0, taken, sh);
-    pages_taken += taken;
-    block_scan(granted ? n : 0, taken, sh);
-    rows_taken += taken;
-    const long long k0 = kv + block_scan(r < P.batch ? s.has : 0, all_kv, sh);
+    long long y[3] = {granted ? need : 0, granted ? n : 0, r < P.batch ? s.has : 0}, sums[3];
+    block_scan<3>(y, sums, sh3);
+    rows_taken += sums[1];
     if (r < P.batch) {
       P.lens_out[r] = (int)s.now;
       P.q_indptr[r + 1] = (int)min(r0 + n, rows_taken);
       if (P.kv_indptr) {
-        P.kv_indptr[r + 1] = (int)min(k0 + s.has, (long long)INT_MAX);
+        P.kv_indptr[r + 1] = (int)min(kv + y[2] + s.has, (long long)INT_MAX);
         P.last_page_len[r] = s.now ? (int)((s.now - 1) % P.ps) + 1 : 0;
       }
     }
-    sh_off[tid] = top - 1 - p0;
-    sh_n[tid] = need;
+    sh_off[tid] = (int)y[0];
     sh_first[tid] = s.had;
-    __syncwarp();
-    for (unsigned m = __ballot_sync(0xffffffffu, granted && need > 0); m; m &= m - 1) {
-      const int k = warp * 32 + __ffs(m) - 1;
-      int32_t* dst = P.table + (long long)(base + k) * P.table_stride + sh_first[k];
-      for (int i = lane; i < sh_n[k]; i += 32) dst[i] = P.free_pages[sh_off[k] - i];
+    __syncthreads();
+    for (int i = tid; i < (int)sums[0]; i += T * kInFlight) {
+      int32_t page[kInFlight];
+#pragma unroll
+      for (int j = 0; j < kInFlight; ++j)
+        if (i + j * T < (int)sums[0]) page[j] = P.free_pages[top - 1 - pages_taken - i - j * T];
+#pragma unroll
+      for (int j = 0; j < kInFlight; ++j)
+        if (i + j * T < (int)sums[0]) {
+          const int k = find_off(sh_off, T, i + j * T);
+          P.table[(long long)(base + k) * P.table_stride + sh_first[k] + i + j * T - sh_off[k]] = page[j];
+        }
     }
-    pages += all_pages;
-    rows += all_rows;
-    kv += all_kv;
-    __syncwarp();
+    pages += all[0];
+    rows += all[1];
+    kv += sums[2];
+    pages_taken += sums[0];
+    __syncthreads();                               // (the arrays are the next round's)
   }
   if (P.kv_indptr && kv > P.max_pages) bad |= kStatusNoRoom;
   if (tid == 0) {
@@ -213,9 +248,9 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constan
     P.q_indptr[0] = 0;
     if (P.kv_indptr) P.kv_indptr[0] = 0;
   }
-  if (__syncthreads_or(bad) && P.status) {          // (the rows below read what the block wrote above)
+  if (__syncthreads_or(bad) && P.status) {         // (the rows below read what the block wrote above)
     const int bits = __reduce_or_sync(0xffffffffu, bad);
-    if (lane == 0 && bits) atomicOr(P.status, bits);
+    if ((tid & 31) == 0 && bits) atomicOr(P.status, bits);
   }
   if (P.rows_here)
     for (int i = tid; i < P.max_rows; i += T) write_row(P, i, (int)rows_taken, P.q_indptr, P.lens_out);

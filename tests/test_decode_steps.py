@@ -148,10 +148,12 @@ DECODES = [
 
 
 @gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("H,hk,d,ps,fmt,layout,dtype,lens,window,sinks", DECODES)
-def test_decode(H, hk, d, ps, fmt, layout, dtype, lens, window, sinks):
+def test_decode(H, hk, d, ps, fmt, layout, dtype, lens, window, sinks, wide):
+    """Short rows under a narrow table go to clusters, under a wide one to the split kernel."""
     dt = DT[dtype]
-    tab, pages = table_of(lens, ps, 1, pad=2)
+    tab, pages = table_of(lens, ps, 1, pad=9000 // ps if wide else 2)
     kv, sc = make_cache(pages, ps, hk, d, layout, fmt, dt, 2)
     # slots behind a request's keys hold NaN (the code 0x7f, or an exponent byte of 255)
     raw = kv.view(torch.uint8) if fmt != "16bit" else kv
@@ -183,19 +185,22 @@ def test_decode(H, hk, d, ps, fmt, layout, dtype, lens, window, sinks):
 
 
 @gpu
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("ps,fmt,layout,dtype,d", [(16, "16bit", "NHD", "bf16", 128), (1, "scaled", "HND", "fp16", 128),
                                                    (3, "block", "NHD", "bf16", 64), (64, "16bit", "HND", "fp16", 256)])
-def test_decode_of_listed_pages(ps, fmt, layout, dtype, d):
+def test_decode_of_listed_pages(ps, fmt, layout, dtype, d, wide):
     """Pages per KV head in any order, a page twice, entries that are skipped."""
     dt, hk, G = DT[dtype], 2, 4
     lens = [10 * ps, 7 * ps - min(2, ps - 1), ps, 0, 4 * ps]
-    tab, pages = table_of(lens, ps, 5)
+    more = 9000 // ps if wide else 0
+    tab, pages = table_of(lens, ps, 5, pad=more)
     kv, sc = make_cache(pages, ps, hk, d, layout, fmt, dt, 6)
     sel = np.array([[[3, 1, 9, -1, 0], [2, 2, 8, 5, 10]],        # 10: past the request's pages
                     [[6, 0, -1, -1, -1], [5, 6, 4, 3, 2]],
                     [[0, -1, -1, -1, -1], [-1, 0, 0, 0, 0]],     # one page: only one entry is read
                     [[0, 1, 2, 3, 4], [-1, -1, -1, -1, -1]],
                     [[1 << 30, -7, 2, 1, 0], [99, 4, -1, 77, 0]]], dtype=np.int32)
+    sel = np.concatenate([sel, np.full((5, hk, more), -1, np.int32)], -1)
     q = torch.randn((5, hk * G, d), generator=torch.Generator().manual_seed(7)).to(dt).cuda()
     out, lse = pod.pod_paged_decode(q, kv, torch.from_numpy(tab).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"),
                                     pages=torch.from_numpy(sel).cuda(), sm_scale=0.1, kv_layout=layout,
