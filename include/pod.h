@@ -634,7 +634,7 @@ typedef struct pod_step_args {
 pod_status pod_step_tables(const pod_step_args* args, void* stream);
 
 /* Arguments of the calls below; each reads the fields that its text names. All
- * pointers DEVICE, 16-byte aligned. */
+ * pointers DEVICE; q, bounds and out 16-byte, kv_cache 32-byte aligned. */
 typedef struct pod_decode_args {
     const void* q;              /* [batch, num_qo_heads, head_dim], q_stride */
     const void* kv_cache;       /* [num_pages, 2, ...] */
@@ -711,7 +711,8 @@ size_t pod_select_pages_workspace_size(int32_t batch, int32_t num_kv_heads, int3
  * lse = -inf, whatever its sink. Slots past a request's keys may hold anything.
  * Logits, sums and the output are fp32; the softmax weights are two 16-bit
  * parts (off by 2^-17 of a weight in bf16, 2^-22 in fp16); over FP8 caches
- * fp16 carries q (all bits but for 2^-38 of a row's largest magnitude) and V.
+ * fp16 carries q (all bits but for 2^-38 of a row's largest magnitude), V and,
+ * for bf16 results, the weights in one part (off by 2^-12 of each).
  * workspace: pod_paged_decode_workspace_size bytes, 256-byte aligned, whose contents
  * need not survive between calls; calls that share it must not overlap.
  * Two calls with the same inputs give the same bits.

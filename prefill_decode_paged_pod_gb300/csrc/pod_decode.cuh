@@ -17,7 +17,8 @@
 // its elements of K's fragments, and of V's as rows, and K and V go from memory to the
 // matrix unit without shared memory in between. P^T changes from accumulator to operand by
 // movmatrix. P is carried in two 16-bit parts (off by 2^-17 of a weight in bf16, 2^-22 in
-// fp16): the matrix unit has time. Codes of FP8 caches are widened to fp16, exactly.
+// fp16): the matrix unit has time. Codes of FP8 caches are widened to fp16, exactly; bf16
+// results over them take P in one fp16 part.
 //
 // Work split. The keys of every (KV head, request) are cut into units of one tile a
 // warp; the units of all, laid out head by head, are dealt to the CTAs of one
@@ -38,31 +39,39 @@ namespace {
 constexpr int kShortUnits = 4;                     // units of a CTA of the kernel for short rows
 constexpr float kLag = 8.f;                        // log2 of how far m may lie below the maximum
 
-template <int D, int FMT, int NT>
+template <typename T, int D, int FMT, int NT>
 struct DecodeShape {
   static constexpr int E = FMT == POD_KV_16BIT ? 2 : 1;           // bytes of an element
   static constexpr int MT = FMT == POD_KV_16BIT ? (D == 64 ? 2 : 1) : (D == 64 ? 4 : D == 128 ? 2 : 1);
   static constexpr int TK = 16 * MT;                              // keys of a warp's tile
   static constexpr int U = TK * kDecodeWarps;                     // keys of a unit
   static constexpr int HT = 8 * NT;                               // query heads of a tile
-  static constexpr int CK = 16 / E;                               // elements of a lane's chunk of K
-  static constexpr int NK = D / (4 * CK);                         // chunks of K a lane takes of a key
-  static constexpr int CV = D / 8 < CK ? D / 8 : CK;              // of V
-  static constexpr int NV = D / (8 * CV);
-  static constexpr int WV = CV * E / 4;                           // 32-bit words of a chunk of V
+  // A lane's chunk of a key: a quarter of K's row, an eighth of V's, at most 32 bytes.
+  static constexpr int WK = D * E / 16 < 8 ? D * E / 16 : 8;      // 32-bit words of a chunk of K
+  static constexpr int CK = WK * 4 / E, NK = D / (4 * CK);        // its elements; chunks of a key
+  static constexpr int WV = D * E / 32 < 8 ? D * E / 32 : 8;      // of V
+  static constexpr int CV = WV * 4 / E, NV = D / (8 * CV);
   static constexpr int IDX = (TK + 31) / 32;                      // tile keys of a lane
+  // 16-bit parts of a weight: two, but for fp16 weights of bf16 results, where one is off by
+  // 2^-12 of the weight, an eighth of the result's own rounding.
+  static constexpr int PARTS = FMT != POD_KV_16BIT && Pack<T>::kBF16 ? 1 : 2;
 };
 
-POD_DEV uint4 load16(const uint8_t* p) {
-  uint4 r;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
-  return r;
-}
-POD_DEV uint2 load8(const uint8_t* p) {
-  uint2 r;
-  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-  return r;
+// N 32-bit words, read once (zeros where not `live`)
+template <int N>
+POD_DEV void load_words(uint32_t* r, const uint8_t* p, bool live) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = 0u;
+  if (!live) return;
+  if constexpr (N == 8)
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "l"(p));
+  else if constexpr (N == 4)
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "l"(p));
+  else
+    asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "l"(p));
 }
 // 8 x 8 matrix of 16-bit values, a register's pair in row lane / 4: its transpose
 POD_DEV uint32_t turn8x8(uint32_t a) {
@@ -124,7 +133,7 @@ POD_DEV int offsetof_m(int what, int w, int h) {
 template <typename T, int D, int FMT, int NT>
 POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h0, int heads, int v0, int v1,
                     DecodeShared<D, 8 * NT>& sh) {
-  using S = DecodeShape<D, FMT, NT>;
+  using S = DecodeShape<T, D, FMT, NT>;
   using M = typename std::conditional<FMT == POD_KV_16BIT, T, __half>::type;   // operands of the products
   constexpr bool MBF = Pack<M>::kBF16;
   constexpr float kUp = weight_up<T, FMT>();
@@ -203,110 +212,97 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
   const int32_t* table = P.table + (long long)row * P.table_stride;
   const int32_t* sel = P.pages ? P.pages + ((long long)row * P.Hk + hk) * P.num_selected : nullptr;
 
-  // Tile key i of a tile at v: its place in the table (stage 1), then its row (stage
-  // 2), each asked for a tile ahead of its use. 0xffffffff: not visible.
+  // Where a tile's keys lie, lane i: key i. Three steps, an iteration of the loop apart so
+  // that none waits for its load: the position in the table (its entry in the list of
+  // pages), the page, the keys' rows.
   struct Place {
     int page, in;
   };
-  auto place = [&](int v) {
-    Place p;
-    p.page = -1;
-    p.in = 0;
-    if (v < v1) {
-      const int w = v + K.first, at_page = w / P.ps;
-      p.in = w - at_page * P.ps;
-      p.page = at_page;
-      if (sel) {
-        p.page = sel[at_page];
-        // (a page past the request's last, or a slot past its last key: not visible)
-        if (p.page >= 0 && (p.page >= P.width || p.page * P.ps + p.in >= K.len)) p.page = -1;
-      }
+  auto place = [&](int v, int j) {
+    Place p = {-1, -1};
+    v += j * 32 + lane;
+    if ((TK >= 32 || lane < TK) && v < v1) {
+      const int w = v + K.first, at = w / P.ps;
+      p.in = w - at * P.ps;
+      p.page = sel ? sel[at] : at;
     }
     return p;
   };
-  auto index_of = [&](Place p) {
-    if (p.page < 0) return 0xffffffffu;
-    const unsigned page = (unsigned)table[p.page];
-    if (page >= P.num_pages) {
+  auto page_at = [&](Place& p) {
+    // (a page past the request's last, or a slot past its last key: not visible)
+    if (sel && p.in >= 0 && (p.page < 0 || p.page >= P.width || p.page * P.ps + p.in >= K.len)) p.in = -1;
+    if (p.in >= 0) p.page = table[p.page];
+  };
+  auto index_of = [&](const Place& p) {            // 0xffffffff: not visible
+    if (p.in < 0) return 0xffffffffu;
+    if ((unsigned)p.page >= P.num_pages) {
       if (P.status) atomicOr(P.status, kStatusSlot);
       return 0xffffffffu;
     }
-    return page * page_step + (unsigned)p.in;
+    return (unsigned)p.page * page_step + (unsigned)p.in;
   };
 
-  uint4 kr[MT][2][S::NK];
-  uint32_t vr[MT][4][S::NV][S::WV];
-  unsigned idx[S::IDX];                          // rows of the tile in flight, lane i: key i
-  Place nxt[S::IDX];
-  auto load_k = [&](const unsigned* ix) {
+  uint32_t kr[MT][2][S::NK][S::WK], vr[MT][4][S::NV][S::WV];
+  unsigned idx[S::IDX], seen[S::IDX];              // rows of the tile that is loaded next; visible keys of the one at hand
+  uint32_t ek[S::IDX], ev[S::IDX];                 // exponent bytes of K and V, a lane's own keys
+  auto load_k = [&]() {
 #pragma unroll
     for (int s = 0; s < MT; ++s)
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
-        const unsigned i = __shfl_sync(0xffffffffu, ix[s / 2], (s & 1) * 16 + a * 8 + g);
-        const uint8_t* p = kbase + (long long)i * key_step + t * 16;
+        const unsigned i = __shfl_sync(0xffffffffu, idx[s / 2], (s & 1) * 16 + a * 8 + g);
+        const uint8_t* p = kbase + (long long)i * key_step + t * (S::WK * 4);
 #pragma unroll
-        for (int b = 0; b < S::NK; ++b) {
-          kr[s][a][b] = make_uint4(0, 0, 0, 0);
-          if (i != 0xffffffffu) kr[s][a][b] = load16(p + b * 64);
-        }
+        for (int b = 0; b < S::NK; ++b) load_words<S::WK>(kr[s][a][b], p + b * (S::WK * 16), i != 0xffffffffu);
       }
-  };
-  auto load_v = [&](const unsigned* ix) {
-#pragma unroll
-    for (int s = 0; s < MT; ++s)
-#pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const unsigned i = __shfl_sync(0xffffffffu, ix[s / 2], (s & 1) * 16 + (a >> 1) * 8 + 2 * t + (a & 1));
-        const uint8_t* p = kbase + v_off + (long long)i * key_step + g * (S::WV * 4);
-#pragma unroll
-        for (int b = 0; b < S::NV; ++b) {
-          if constexpr (S::WV == 4) {
-            uint4 r = make_uint4(0, 0, 0, 0);
-            if (i != 0xffffffffu) r = load16(p + b * 128);
-            vr[s][a][b][0] = r.x; vr[s][a][b][1] = r.y; vr[s][a][b][2] = r.z; vr[s][a][b][3] = r.w;
-          } else {
-            uint2 r = make_uint2(0, 0);
-            if (i != 0xffffffffu) r = load8(p + b * 64);
-            vr[s][a][b][0] = r.x; vr[s][a][b][1] = r.y;
-          }
-        }
-      }
-  };
-  // exponent bytes of K (low) and V of the tile's keys, a lane's own
-  auto load_e = [&](const unsigned* ix, int* eb) {
     if constexpr (FMT == POD_KV_E4M3_BLOCK) {
 #pragma unroll
       for (int j = 0; j < S::IDX; ++j) {
-        eb[j] = 127 | 127 << 8;
-        if (ix[j] != 0xffffffffu) {
-          const uint8_t* p = P.scales + (P.hnd ? (long long)ix[j] + (long long)hk * P.ps : (long long)ix[j] * P.Hk + hk);
-          eb[j] = p[0] | p[(long long)P.ps * P.Hk] << 8;
+        ek[j] = ev[j] = 127;
+        if (idx[j] != 0xffffffffu) {
+          const uint8_t* p =
+              P.scales + (P.hnd ? (long long)idx[j] + (long long)hk * P.ps : (long long)idx[j] * P.Hk + hk);
+          ek[j] = p[0];
+          ev[j] = p[(long long)P.ps * P.Hk];
         }
       }
     }
   };
+  auto load_v = [&]() {
+#pragma unroll
+    for (int s = 0; s < MT; ++s)
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const unsigned i = __shfl_sync(0xffffffffu, idx[s / 2], (s & 1) * 16 + (a >> 1) * 8 + 2 * t + (a & 1));
+        const uint8_t* p = kbase + v_off + (long long)i * key_step + g * (S::WV * 4);
+#pragma unroll
+        for (int b = 0; b < S::NV; ++b) load_words<S::WV>(vr[s][a][b], p + b * (S::WV * 32), i != 0xffffffffu);
+      }
+  };
 
   int v = v0 + warp * TK;
-  int eb[S::IDX], eb_next[S::IDX];
+  Place p1[S::IDX], p2[S::IDX];                    // with their position, with their page
 #pragma unroll
   for (int j = 0; j < S::IDX; ++j) {
-    const bool mine = TK >= 32 || lane < TK;
-    idx[j] = index_of(mine ? place(v + j * 32 + lane) : Place{-1, 0});
-    nxt[j] = mine ? place(v + S::U + j * 32 + lane) : Place{-1, 0};
+    Place p0 = place(v, j);
+    p2[j] = place(v + S::U, j);
+    p1[j] = place(v + 2 * S::U, j);
+    page_at(p0);
+    page_at(p2[j]);
+    idx[j] = index_of(p0);
   }
   if (v < v1) {
-    load_k(idx);
-    load_e(idx, eb);
-    load_v(idx);
+    load_k();
+    load_v();
   }
   for (; v < v1; v += S::U) {
-    unsigned idx_next[S::IDX];
 #pragma unroll
     for (int j = 0; j < S::IDX; ++j) {
-      const bool mine = TK >= 32 || lane < TK;
-      idx_next[j] = index_of(nxt[j]);
-      nxt[j] = mine ? place(v + 2 * S::U + j * 32 + lane) : Place{-1, 0};
+      seen[j] = __ballot_sync(0xffffffffu, idx[j] != 0xffffffffu);
+      idx[j] = index_of(p2[j]);
+      p2[j] = p1[j];
+      page_at(p2[j]);
+      p1[j] = place(v + 3 * S::U, j);
     }
     // ---- S^T, a key a row (g, g + 8 of every 16), the heads 2t and 2t + 1 of every 8
     float x[MT][NT][4];
@@ -318,29 +314,34 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
         for (int c = 0; c < 4; ++c) x[s][n][c] = 0.f;
 #pragma unroll
       for (int b = 0; b < S::NK; ++b) {
-        const uint32_t w0[4] = {kr[s][0][b].x, kr[s][0][b].y, kr[s][0][b].z, kr[s][0][b].w};
-        const uint32_t w1[4] = {kr[s][1][b].x, kr[s][1][b].y, kr[s][1][b].z, kr[s][1][b].w};
-        if constexpr (FMT == POD_KV_16BIT) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < S::WK / 2; ++i) {
+          const uint32_t* w0 = kr[s][0][b];
+          const uint32_t* w1 = kr[s][1][b];
+          if constexpr (FMT == POD_KV_16BIT) {
             const uint32_t a[4] = {w0[2 * i], w1[2 * i], w0[2 * i + 1], w1[2 * i + 1]};
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma16816<MBF>(x[s][n], a, qf[n][b][2 * i], qf[n][b][2 * i + 1]);
-          }
-        } else {
+          } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t a[4] = {e4m3x2_to<__half>((uint16_t)w0[i]), e4m3x2_to<__half>((uint16_t)w1[i]),
-                                   e4m3x2_to<__half>((uint16_t)(w0[i] >> 16)),
-                                   e4m3x2_to<__half>((uint16_t)(w1[i] >> 16))};
+            for (int j = 2 * i; j < 2 * i + 2; ++j) {
+              const uint32_t a[4] = {e4m3x2_to<__half>((uint16_t)w0[j]), e4m3x2_to<__half>((uint16_t)w1[j]),
+                                     e4m3x2_to<__half>((uint16_t)(w0[j] >> 16)),
+                                     e4m3x2_to<__half>((uint16_t)(w1[j] >> 16))};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816<MBF>(x[s][n], a, qf[n][b][2 * i], qf[n][b][2 * i + 1]);
+              for (int n = 0; n < NT; ++n) mma16816<MBF>(x[s][n], a, qf[n][b][2 * j], qf[n][b][2 * j + 1]);
+            }
           }
         }
       }
     }
-    load_k(idx_next);
-    load_e(idx_next, eb_next);
+    uint32_t ek_now[S::IDX], ev_now[S::IDX];
+#pragma unroll
+    for (int j = 0; j < S::IDX; ++j) {
+      ek_now[j] = ek[j];
+      ev_now[j] = ev[j];
+    }
+    load_k();
     // ---- logits, the references, the weights
     float xe[MT][2];                             // V's exponents of the lane's keys
     bool past = false;
@@ -349,13 +350,12 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
         const int src = (s & 1) * 16 + a * 8 + g;
-        const bool live = __shfl_sync(0xffffffffu, idx[s / 2], src) != 0xffffffffu;
+        const bool live = seen[s / 2] >> src & 1;
         float ks = 1.f;
         xe[s][a] = 0.f;
         if constexpr (FMT == POD_KV_E4M3_BLOCK) {
-          const int e = __shfl_sync(0xffffffffu, eb[s / 2], src);
-          ks = pow2_of(e & 255);
-          xe[s][a] = (float)((e >> 8) - 127);
+          ks = pow2_of((int)__shfl_sync(0xffffffffu, ek_now[s / 2], src));
+          xe[s][a] = (float)((int)__shfl_sync(0xffffffffu, ev_now[s / 2], src) - 127);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -423,10 +423,14 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
             p0 = ex2(x[s][n][2 * a] + xe[s][a] - rv0);
             p1 = ex2(x[s][n][2 * a + 1] + xe[s][a] - rv1);
           }
-          uint32_t hi, lo;
-          Pack<M>::split(p0, p1, hi, lo);
-          ph[s][n][a] = turn8x8(hi);
-          pl[s][n][a] = turn8x8(lo);
+          if constexpr (S::PARTS == 2) {
+            uint32_t hi, lo;
+            Pack<M>::split(p0, p1, hi, lo);
+            ph[s][n][a] = turn8x8(hi);
+            pl[s][n][a] = turn8x8(lo);
+          } else {
+            ph[s][n][a] = turn8x8(Pack<M>::two(p0, p1));
+          }
         }
     }
     // ---- O^T += V^T P^T
@@ -443,7 +447,7 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               mma16816<MBF>(o[n][b][w], a, ph[s][n][0], ph[s][n][1]);
-              mma16816<MBF>(o[n][b][w], a, pl[s][n][0], pl[s][n][1]);
+              if constexpr (S::PARTS == 2) mma16816<MBF>(o[n][b][w], a, pl[s][n][0], pl[s][n][1]);
             }
           } else {
 #pragma unroll
@@ -454,17 +458,12 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
                 mma16816<MBF>(o[n][b][2 * w + q], a, ph[s][n][0], ph[s][n][1]);
-                mma16816<MBF>(o[n][b][2 * w + q], a, pl[s][n][0], pl[s][n][1]);
+                if constexpr (S::PARTS == 2) mma16816<MBF>(o[n][b][2 * w + q], a, pl[s][n][0], pl[s][n][1]);
               }
             }
           }
         }
-    load_v(idx_next);
-#pragma unroll
-    for (int j = 0; j < S::IDX; ++j) {
-      idx[j] = idx_next[j];
-      eb[j] = eb_next[j];
-    }
+    load_v();
   }
 
   // ---- the warps' sums join
@@ -558,7 +557,7 @@ POD_DEV void store_out(const DecodeParams& P, int row, int head, int D, int c4, 
 template <typename T, int D, int FMT, int NT>
 __global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
     decode_kernel(const __grid_constant__ DecodeParams P) {
-  using S = DecodeShape<D, FMT, NT>;
+  using S = DecodeShape<T, D, FMT, NT>;
   constexpr int HT = S::HT;
   __shared__ DecodeShared<D, HT> sh;
   __shared__ long long sh_scan[kDecodeWarps + 2];
@@ -657,7 +656,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
 template <typename T, int D, int FMT, int NT, int CL>
 __global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
     decode_short_kernel(const __grid_constant__ DecodeParams P) {
-  using S = DecodeShape<D, FMT, NT>;
+  using S = DecodeShape<T, D, FMT, NT>;
   constexpr int HT = S::HT;
   __shared__ DecodeShared<D, HT> sh;
   asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
@@ -821,7 +820,7 @@ cudaError_t launch_clusters(void (*kernel)(A...), unsigned grid, unsigned cluste
 
 template <typename T, int D, int FMT, int NT>
 cudaError_t launch_decode_nt(DecodeParams& P, cudaStream_t st) {
-  using S = DecodeShape<D, FMT, NT>;
+  using S = DecodeShape<T, D, FMT, NT>;
   const int tiles = (P.G + S::HT - 1) / S::HT;
   P.planes = P.Hk * tiles;
   constexpr int per_sm = (D == 256 || NT == 2) ? 2 : 3;

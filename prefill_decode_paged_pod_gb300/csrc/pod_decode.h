@@ -31,6 +31,7 @@ struct DecodeParams {
   float* piece_o;                  // [grid * 2][heads of a tile][d], normalised
   float* piece_lse;                // [grid * 2][heads of a tile], base 2
   long long q_stride, out_stride, table_stride;
+  long long scale_bytes;           // of the pool's exponent bytes
   unsigned num_pages;
   int batch, H, Hk, G, width, ps, hnd, num_selected, window;
   int planes;                      // Hk * head tiles

@@ -912,8 +912,8 @@ pod_status check_decode_cache(const pod_decode_args& a) {
   if (a.kv_format != POD_KV_16BIT && a.kv_format != POD_KV_E4M3 && a.kv_format != POD_KV_E4M3_BLOCK)
     return fail(POD_ERR_INVALID_ARG, "unknown cache format");
   if (a.kv_layout != 0 && a.kv_layout != 1) return fail(POD_ERR_INVALID_ARG, "kv_layout must be 0 (NHD) or 1 (HND)");
-  if (!a.kv_cache || reinterpret_cast<uintptr_t>(a.kv_cache) % 16)
-    return fail(POD_ERR_INVALID_ARG, "the cache must be a 16-byte aligned pointer");
+  if (!a.kv_cache || reinterpret_cast<uintptr_t>(a.kv_cache) % 32)
+    return fail(POD_ERR_INVALID_ARG, "the cache must be a 32-byte aligned pointer");
   if (a.kv_format == POD_KV_E4M3_BLOCK && !a.kv_scales)
     return fail(POD_ERR_INVALID_ARG, "a block-scaled cache needs its scales");
   if (a.kv_format != POD_KV_E4M3_BLOCK && a.kv_scales)

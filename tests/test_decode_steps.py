@@ -5,8 +5,8 @@ step that serves later ones, and the refusals on the CPU.
 Tolerances, fixed before the first run. A logit s q.k is a sum of d products in
 fp32 (exact products; an addition of the matrix unit is off by 2^-23 at most):
 d 2^-23 A, with A = s sum |q_j k_j|, so a weight is off by that much of itself, by
-2^-17 for its two 16-bit parts, by 2^-21 for the exponential and the scales of the
-joins; the output by twice the sum (numerator and denominator) of B = sum p |v|, and
+2^-17 for its two 16-bit parts (2^-12 for the one fp16 part that bf16 results over FP8
+caches take), by 2^-21 for the exponential and the scales of the joins; the output by twice the sum (numerator and denominator) of B = sum p |v|, and
 then by its rounding, eps / 2. The base-2 LSE: the same relative error times log2(e),
 and 2^-22 of itself. Weights below 2^-24 of the largest fp16 operand are off by up to
 2^-39 of the largest weight each, which 2^20 keys leave below 2^-19.
@@ -104,10 +104,12 @@ def attend64(q, x, keys, scale, sinks):
     return out, lse, A, B
 
 
-def check(got, lse, want, wlse, A, B, d, dtype):
+def check(got, lse, want, wlse, A, B, d, dtype, fmt="16bit"):
     got, lse = got.double().cpu().numpy(), lse.double().cpu().numpy()
     rel = d * 2.0 ** -23 * A + 2.0 ** -16
-    tol = np.abs(want) * torch.finfo(dtype).eps / 2 * (1 + 2.0 ** -7) + 2 * rel[..., None] * B + torch.finfo(dtype).tiny
+    part = 2.0 ** -12 if fmt != "16bit" and dtype == torch.bfloat16 else 0.0       # (not in the sum of the weights)
+    tol = np.abs(want) * torch.finfo(dtype).eps / 2 * (1 + 2.0 ** -7) + (2 * rel[..., None] + part) * B \
+        + torch.finfo(dtype).tiny
     bad = ~(np.abs(got - want) <= tol)
     assert not bad.any(), (np.argwhere(bad)[:4], np.abs(got - want)[bad][:4], tol[bad][:4])
     none = np.isneginf(wlse)
@@ -177,7 +179,7 @@ def test_decode(H, hk, d, ps, fmt, layout, dtype, lens, window, sinks, wide):
     scale = 1 / math.sqrt(d)
     ref = [attend64(q[i].double().cpu().numpy(), x, dense_keys(tab[i], n, ps, hk, window), scale,
                     None if snk is None else snk.double().cpu().numpy()) for i, n in enumerate(lens)]
-    check(out, lse, *(np.stack(y) for y in zip(*ref)), d, dt)
+    check(out, lse, *(np.stack(y) for y in zip(*ref)), d, dt, fmt)
     assert status.item() == 0
     for i, n in enumerate(lens):
         if n == 0:
@@ -214,7 +216,7 @@ def test_decode_of_listed_pages(ps, fmt, layout, dtype, d, wide):
             t = np.concatenate(t + [np.zeros(0, int)]).astype(int)
             keys.append((tab[i][t // ps].astype(np.int64), t % ps))
         ref.append(attend64(q[i].double().cpu().numpy(), x, keys, 0.1, None))
-    check(out, lse, *(np.stack(y) for y in zip(*ref)), d, dt)
+    check(out, lse, *(np.stack(y) for y in zip(*ref)), d, dt, fmt)
 
 
 @gpu
@@ -255,7 +257,7 @@ def test_block_scales_far_apart(dtype):
                                     kv_scales=sc)
     ref = [attend64(q[0].double().cpu().numpy(), values64(kv, sc, "NHD", "block"), dense_keys(tab[0], n, ps, hk, -1),
                     1 / math.sqrt(d), None)]
-    check(out, lse, *(np.stack(y) for y in zip(*ref)), d, dt)
+    check(out, lse, *(np.stack(y) for y in zip(*ref)), d, dt, "block")
 
 
 @gpu
@@ -744,7 +746,7 @@ def test_one_captured_step_serves_the_later_ones(fmt, layout, dtype):
                         c = np.concatenate(c + [np.zeros(0, int)]).astype(int)
                         keys.append((tab[q_][c // ps].astype(np.int64), c % ps))
                 ref.append(attend64(last[q_].double().cpu().numpy(), x, keys, 1 / 8, None))
-            check(out, lse, *(np.stack(y) for y in zip(*ref)), d, dt)
+            check(out, lse, *(np.stack(y) for y in zip(*ref)), d, dt, fmt)
 
 
 @gpu
