@@ -9,8 +9,8 @@
 //   up_j = sum_g max(q_gj, 0), down_j = sum_g min(q_gj, 0).
 //
 // The choice is that of the scores in 64 bits, without computing them so: an fp32
-// score is off by at most E = (13 + G) 2^-24 times the sum of its terms' magnitudes (8
-// fused steps a lane, 16 at D = 256, five additions across lanes, G - 1 in a weight), of which
+// score is off by at most E = (10 + G) 2^-24 times the sum of its terms' magnitudes (4
+// fused steps a lane, 8 at D = 256, six additions, G - 1 in a weight), of which
 // a bound is kept per warp. Pages further than 2 E from the last place are decided;
 // the others, where they are more than the places left, are scored again in 64
 // bits (of which this GPU does two a clock and SM).
@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kBoundThreads = 256, kBoundRows = 64;
 constexpr int kScoreThreads = 128, kLeastPages = 16;   // pages of a warp at least
-constexpr int kBinBits = 11, kBins = 1 << kBinBits, kNear = 256;
+constexpr int kBinBits = 10, kBins = 1 << kBinBits, kNear = 256;
 constexpr int kHeld = 8;                               // keys of a lane
 constexpr int kHeldPages = 1024 * kHeld;               // pages whose keys a block holds
 
@@ -67,6 +67,15 @@ POD_DEV uint32_t max2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// the larger magnitudes (the signs are of no use)
+template <typename T>
+POD_DEV uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (Pack<T>::kBF16) asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // ------------------------------------------------------------------ bounds
 struct BoundParams {
   const uint8_t* cache;
@@ -79,17 +88,51 @@ struct BoundParams {
   float k_scale;
 };
 
+// Two values rounded outward to T, within its finite values.
+template <typename T>
+POD_DEV uint32_t outward2(float x, float y, bool upper) {
+  x = fminf(fmaxf(x, -Pair<T>::kMax), Pair<T>::kMax);
+  y = fminf(fmaxf(y, -Pair<T>::kMax), Pair<T>::kMax);
+  T r[2] = {upper ? Pair<T>::up(x) : Pair<T>::down(x), upper ? Pair<T>::up(y) : Pair<T>::down(y)};
+  return (uint32_t)*reinterpret_cast<uint16_t*>(&r[0]) | (uint32_t)*reinterpret_cast<uint16_t*>(&r[1]) << 16;
+}
+
+// A warp's (page, head) whose exponents lie more than 15 binades apart: in fp32, a lane some
+// channels, key by key.
+template <typename T, int D>
+__device__ __noinline__ void bounds_of_far_scales(const BoundParams& P, const uint8_t* keys, const uint8_t* scales,
+                                                  long long row_bytes, int step, int valid, long long to) {
+  for (int c = 2 * (threadIdx.x & 31); c < D; c += 64) {
+    float lo0 = INFINITY, lo1 = INFINITY, hi0 = -INFINITY, hi1 = -INFINITY;
+    for (int k = 0; k < valid; ++k) {
+      const int e = scales[(long long)k * step];
+      const float s = e ? __uint_as_float((uint32_t)e << 23) : 5.877471754111438e-39f;
+      const uint32_t a = e4m3x2_to<__half>(*reinterpret_cast<const uint16_t*>(keys + k * row_bytes + c));
+      const float2 f = Pack<__half>::unpack(a);
+      lo0 = fminf(lo0, f.x * s);
+      hi0 = fmaxf(hi0, f.x * s);
+      lo1 = fminf(lo1, f.y * s);
+      hi1 = fmaxf(hi1, f.y * s);
+    }
+    T* dst = static_cast<T*>(P.bounds) + to + c;
+    *reinterpret_cast<uint32_t*>(dst) = outward2<T>(lo0, lo1, false);
+    *reinterpret_cast<uint32_t*>(dst + D) = outward2<T>(hi0, hi1, true);
+  }
+}
+
 // A block takes `span` rows of the write. A row whose page differs from that of the row
 // before owns the page; a warp finds how far its run of rows goes. Then a warp brings in
-// the keys of one (page, head) at a time, eight elements a lane and eight loads in
-// flight, 32 / LPR keys each. Read once: bound by memory, so the registers are kept few and
-// the warps many (bytes in flight).
+// the keys of one (page, head) at a time, 16 bytes a lane, four loads in flight of 32 / LPR
+// keys each, and keeps the extremes packed, two 16-bit values a register. Codes go to fp16,
+// under block scales relative to the largest exponent of the page's keys: exact down to 15
+// binades below it (pages whose exponents lie further apart take a slow way). Half the
+// instructions of the same in fp32, which bound it: 38000 pages and heads of block-scaled codes
+// 45 -> BOUNDS_US us.
 template <typename T, int D, int FMT>
-__global__ void __launch_bounds__(kBoundThreads, FMT == POD_KV_E4M3 ? 5 : 4)
-    bounds_kernel(const __grid_constant__ BoundParams P) {
-  constexpr int E = FMT == POD_KV_16BIT ? 2 : 1, LPR = D / 8, KPL = 32 / LPR, U = 8;
+__global__ void __launch_bounds__(kBoundThreads, 4) bounds_kernel(const __grid_constant__ BoundParams P) {
+  constexpr int E = FMT == POD_KV_16BIT ? 2 : 1, LPR = D * E / 16, KPL = 32 / LPR, U = 4;
+  constexpr int R = E == 2 ? 4 : 8, PARTS = 2 * R / 4;    // packed pairs of a lane's chunk; 16-byte outputs of it
   using M = typename std::conditional<FMT == POD_KV_16BIT, T, __half>::type;
-  using Chunk = typename std::conditional<FMT == POD_KV_16BIT, uint4, uint2>::type;
   __shared__ long long page_of[kBoundRows];
   __shared__ int row_of[kBoundRows], keys_of[kBoundRows];
   __shared__ int owners;
@@ -124,149 +167,97 @@ __global__ void __launch_bounds__(kBoundThreads, FMT == POD_KV_E4M3 ? 5 : 4)
   }
   __syncthreads();
   const int part = lane % LPR, sub = lane / LPR;
+  const long long row_bytes = (long long)D * E * (P.hnd ? 1 : P.Hk);          // from a key to the next
   for (int i = warp; i < n * P.Hk; i += kBoundThreads / 32) {
     const int o = i / P.Hk, h = i - o * P.Hk, valid = keys_of[o];
     const long long page = page_of[o];
     const long long row = page * 2 * P.Hk * P.ps + (P.hnd ? (long long)h * P.ps : h);   // of key 0, in rows of D
+    const uint8_t* keys = P.cache + row * (D * E) + part * 16;
+    const uint8_t* scales = FMT == POD_KV_E4M3_BLOCK ? P.scales + row : nullptr;
     const int step = P.hnd ? 1 : P.Hk;
-    uint32_t lo2[4], hi2[4];                           // packed extremes (not with block scales)
-    float lo[8], hi[8];
+    uint32_t lo[R], hi[R];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      lo2[e] = Pair<M>::kInf;
-      hi2[e] = Pair<M>::kInf | 0x80008000u;
+    for (int e = 0; e < R; ++e) {
+      lo[e] = Pair<M>::kInf;
+      hi[e] = Pair<M>::kInf | 0x80008000u;
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      lo[e] = INFINITY;
-      hi[e] = -INFINITY;
+    // the exponents of the page's keys: those of 32 at a time, and their extremes
+    int eb = 0, top = 0, low = 255;
+    if constexpr (FMT == POD_KV_E4M3_BLOCK) {
+      for (int k = lane; k < valid; k += 32) {
+        const int e = scales[(long long)k * step];
+        if (k < 32) eb = e;
+        top = max(top, e);
+        low = min(low, e);
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      low = __reduce_min_sync(0xffffffffu, low);
+      if (top - low > 15) {
+        bounds_of_far_scales<T, D>(P, keys - part * 16, scales, row_bytes, step, valid, (page * P.Hk + h) * 2 * D);
+        continue;
+      }
     }
     for (int k0 = 0; k0 < valid; k0 += KPL * U) {
-      Chunk x[U];
-      int eb[U];
+      uint4 x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (k0 + u * KPL + sub < valid)
+          x[u] = __ldcs(reinterpret_cast<const uint4*>(keys + (long long)(k0 + u * KPL + sub) * row_bytes));
+      if (FMT == POD_KV_E4M3_BLOCK && k0 && k0 % 32 == 0) eb = k0 + lane < valid ? scales[(long long)(k0 + lane) * step] : 0;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int k = k0 + u * KPL + sub;
-        if (k < valid) {
-          const long long at = row + (long long)k * step;
-          x[u] = __ldcs(reinterpret_cast<const Chunk*>(P.cache + at * (D * E)) + part);
-          if (FMT == POD_KV_E4M3_BLOCK) eb[u] = P.scales[at];
-        }
-      }
-      if constexpr (FMT == POD_KV_16BIT) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (k0 + u * KPL + sub >= valid) continue;
-          const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            lo2[e] = min2<M>(lo2[e], w[e]);
-            hi2[e] = max2<M>(hi2[e], w[e]);
-          }
-        }
-      } else {
-        // Block scales: the keys' values relative to the largest exponent among them are exact
-        // in fp16 down to 15 binades below it; pages whose exponents lie further apart take
-        // the fp32 way. (Packed, the kernel has half the instructions, which bound it.)
-        int e_hi = 0, e_lo = 255;
-        bool close = true;
+        uint32_t s = 0u;
         if constexpr (FMT == POD_KV_E4M3_BLOCK) {
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (k0 + u * KPL + sub < valid) {
-              e_hi = max(e_hi, eb[u]);
-              e_lo = min(e_lo, eb[u]);
-            }
-          e_hi = __reduce_max_sync(0xffffffffu, e_hi);
-          e_lo = __reduce_min_sync(0xffffffffu, e_lo);
-          close = e_hi - e_lo <= 15;
+          // 2^(exponent - top), twice: fp16's exponent bias is 15, a normal number down to 2^-14
+          const int f = __shfl_sync(0xffffffffu, eb, k & 31) - top;
+          s = f < -14 ? 0x02000200u : (uint32_t)(f + 15) * 0x04000400u;
         }
+        if (k >= valid) continue;
+        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (k0 + u * KPL + sub >= valid) continue;
-          const uint32_t w[2] = {x[u].x, x[u].y};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t a = e4m3x2_to<__half>((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
-            if (FMT == POD_KV_E4M3 || close) {
-              if constexpr (FMT == POD_KV_E4M3_BLOCK) {
-                // 2^(eb - e_hi) twice: fp16's exponent bias is 15, a normal number down to 2^-14
-                const int f = eb[u] - e_hi;
-                const uint32_t s = f < -14 ? 0x02000200u : (uint32_t)(f + 15) << 10 | (uint32_t)(f + 15) << 26;
-                const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<const __half2*>(&s));
-                a = *reinterpret_cast<const uint32_t*>(&y);
-              }
-              lo2[e] = min2<M>(lo2[e], a);
-              hi2[e] = max2<M>(hi2[e], a);
-            } else {
-              const float s = eb[u] ? __uint_as_float((uint32_t)eb[u] << 23) : 5.877471754111438e-39f;
-              const float2 f = Pack<__half>::unpack(a);
-              const float y0 = f.x * s, y1 = f.y * s;
-              lo[2 * e] = fminf(lo[2 * e], y0);
-              hi[2 * e] = fmaxf(hi[2 * e], y0);
-              lo[2 * e + 1] = fminf(lo[2 * e + 1], y1);
-              hi[2 * e + 1] = fmaxf(hi[2 * e + 1], y1);
+        for (int e = 0; e < R; ++e) {
+          uint32_t a;
+          if constexpr (FMT == POD_KV_16BIT) {
+            a = w[e];
+          } else {
+            a = e4m3x2_to<__half>((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+            if constexpr (FMT == POD_KV_E4M3_BLOCK) {
+              const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<const __half2*>(&s));
+              a = *reinterpret_cast<const uint32_t*>(&y);
             }
           }
-        }
-        if (FMT == POD_KV_E4M3_BLOCK && close) {
-          // these keys' extremes, as values (the infinities of an empty lane stay what they are)
-          const float s = e_hi ? __uint_as_float((uint32_t)e_hi << 23) : 5.877471754111438e-39f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 a = Pack<__half>::unpack(lo2[e]), b = Pack<__half>::unpack(hi2[e]);
-            lo[2 * e] = fminf(lo[2 * e], a.x * s);
-            lo[2 * e + 1] = fminf(lo[2 * e + 1], a.y * s);
-            hi[2 * e] = fmaxf(hi[2 * e], b.x * s);
-            hi[2 * e + 1] = fmaxf(hi[2 * e + 1], b.y * s);
-            lo2[e] = Pair<M>::kInf;
-            hi2[e] = Pair<M>::kInf | 0x80008000u;
-          }
+          lo[e] = min2<M>(lo[e], a);
+          hi[e] = max2<M>(hi[e], a);
         }
       }
     }
-    if constexpr (FMT != POD_KV_E4M3_BLOCK) {
-      // packed extremes as values
-      const float s = FMT == POD_KV_E4M3 ? P.k_scale : 1.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+    for (int d = LPR; d < 32; d <<= 1)
 #pragma unroll
-        for (int d = LPR; d < 32; d <<= 1) {
-          lo2[e] = min2<M>(lo2[e], __shfl_xor_sync(0xffffffffu, lo2[e], d));
-          hi2[e] = max2<M>(hi2[e], __shfl_xor_sync(0xffffffffu, hi2[e], d));
-        }
-        const float2 a = Pack<M>::unpack(lo2[e]), b = Pack<M>::unpack(hi2[e]);
-        lo[2 * e] = FMT == POD_KV_E4M3 ? a.x * s : a.x;
-        lo[2 * e + 1] = FMT == POD_KV_E4M3 ? a.y * s : a.y;
-        hi[2 * e] = FMT == POD_KV_E4M3 ? b.x * s : b.x;
-        hi[2 * e + 1] = FMT == POD_KV_E4M3 ? b.y * s : b.y;
+      for (int e = 0; e < R; ++e) {
+        lo[e] = min2<M>(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], d));
+        hi[e] = max2<M>(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], d));
       }
-    } else {
+    const float s = FMT == POD_KV_E4M3 ? P.k_scale
+                    : FMT == POD_KV_E4M3_BLOCK ? (top ? __uint_as_float((uint32_t)top << 23) : 5.877471754111438e-39f) : 1.f;
+    // the lanes that hold the same chunk share its outputs: eight smallest values, the next
+    // eight, the largest ones
+    T* dst = static_cast<T*>(P.bounds) + (page * P.Hk + h) * 2 * D + part * (2 * R);
 #pragma unroll
-      for (int d = LPR; d < 32; d <<= 1)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          lo[e] = fminf(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], d));
-          hi[e] = fmaxf(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], d));
-        }
-    }
-    T* dst = static_cast<T*>(P.bounds) + (page * P.Hk + h) * 2 * D + part * 8;
-    auto put = [&](T* to, const float* v, bool upper) {
+    for (int o = 0; o < PARTS; o += KPL) {
+      const int mine = o + sub;
+      if (KPL > PARTS && mine >= PARTS) break;
+      const bool upper = mine >= PARTS / 2;
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        T y[2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float z = fminf(fmaxf(v[2 * e + c], -Pair<T>::kMax), Pair<T>::kMax);
-          y[c] = upper ? Pair<T>::up(z) : Pair<T>::down(z);
-        }
-        w[e] = (uint32_t)*reinterpret_cast<uint16_t*>(&y[0]) | (uint32_t)*reinterpret_cast<uint16_t*>(&y[1]) << 16;
+        const uint32_t a = upper ? hi[e] : lo[e], b = upper ? hi[R - 4 + e] : lo[R - 4 + e];
+        const float2 f = Pack<M>::unpack(PARTS == 4 && (mine & 1) ? b : a);
+        w[e] = outward2<T>(FMT == POD_KV_16BIT ? f.x : f.x * s, FMT == POD_KV_16BIT ? f.y : f.y * s, upper);
       }
-      *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-    };
-    if (sub == 0) put(dst, lo, false);
-    if (sub == KPL - 1) put(dst + D, hi, true);
+      *reinterpret_cast<uint4*>(dst + (upper ? D : 0) + (PARTS == 4 ? (mine & 1) * 8 : 0)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
 }
 
@@ -322,6 +313,7 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_co
   if (mine <= 0 || n <= P.k) return;                   // (n <= k: all are chosen)
   const int c = lane % LPP;
   const T* bounds = static_cast<const T*>(P.bounds) + (long long)hk * 2 * D + c * 8;
+  const long long page_step = (long long)P.Hk * 2 * D;
   float* score = P.score + ((long long)row * P.Hk + hk) * P.width + page0;
   // entries 32 i + lane of the table, one set ahead
   auto checked = [&](int x, int p) {
@@ -331,7 +323,7 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_co
     return -1;
   };
   id = checked(id, lane);                              // of the pages that are asked for
-  int asked = 0;
+  int asked = 0, next = 0, at = 0;                     // pages asked for; the ring's sets to fill and to read
   uint4* slots = ring + (threadIdx.x >> 5) * (kRing * 256) + lane;
   auto ask = [&]() {
     if (asked < mine) {
@@ -339,14 +331,15 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_co
         id = checked(after, asked + lane);
         after = asked + 32 + lane < mine ? table[asked + 32 + lane] : -1;
       }
-      uint4* to = slots + asked / STEP % kRing * 256;
+      uint4* to = slots + next * 256;
+      next = next + 1 == kRing ? 0 : next + 1;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int at = __shfl_sync(0xffffffffu, id, (asked + u * PPL + lane / LPP) & 31);
-        const T* from = bounds + (long long)(at < 0 ? 0 : at) * P.Hk * 2 * D;
+        const int page = __shfl_sync(0xffffffffu, id, (asked + u * PPL + lane / LPP) & 31);
+        const T* from = bounds + max(page, 0) * page_step;
 #pragma unroll
         for (int i = 0; i < NC; ++i)
-          cp_async16(smem_u32(to + (u * NC + i) * 32), from + i * D, at < 0 ? 0u : 16u);
+          cp_async16(smem_u32(to + (u * NC + i) * 32), from + i * D, page < 0 ? 0u : 16u);
       }
     }
     cp_async_commit();
@@ -389,12 +382,14 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_co
   for (int p0 = 0; p0 < mine; p0 += STEP) {
     ask();
     cp_async_wait<kRing - 1>();
-    const uint4* from = slots + p0 / STEP % kRing * 256;
+    const uint4* from = slots + at * 256;
+    at = at + 1 == kRing ? 0 : at + 1;
     float s[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) s[u] = 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      uint64_t two = 0;                                // even and odd channels
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const uint4 x = from[(u * NC + i) * 32];
@@ -402,11 +397,14 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_co
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 f = Pack<T>::unpack(v[e]);
-          s[u] = fmaf(f.x, w[i][2 * e], s[u]);
-          s[u] = fmaf(f.y, w[i][2 * e + 1], s[u]);
-          top[i][e] = max2<T>(top[i][e], v[e] & 0x7fff7fffu);
+          two = fma2(pack2(f.x, f.y), pack2(w[i][2 * e], w[i][2 * e + 1]), two);
+          top[i][e] = max_abs2<T>(top[i][e], v[e]);
         }
       }
+      float a, b;
+      unpack2(two, a, b);
+      s[u] = a + b;
+    }
     // sums over the lanes of a page: halves of the sums go to halves of the lanes
     constexpr int O1 = LPP / 2, O2 = LPP / 4, O3 = LPP / 8;
     float s4[4], s2[2], s1;
@@ -435,7 +433,7 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_co
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       // (0 times an infinity is a NaN, as a term of that kind is)
-      const float2 m = Pack<T>::unpack(top[i][e]);
+      const float2 m = Pack<T>::unpack(top[i][e] & 0x7fff7fffu);
       mag += fabsf(w[i][2 * e]) * m.x + fabsf(w[i][2 * e + 1]) * m.y;
     }
 #pragma unroll
@@ -443,7 +441,7 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_co
   if (lane == 0)
     // (products of the smallest numbers are off by more than their part)
     P.off[((long long)row * P.Hk + hk) * P.chunks + chunk] =
-        mag == 0.f ? 0.f : mag * ((float)(8 * NC + 5 + P.G) * 0x1.04p-24f) + 0x1p-140f;
+        mag == 0.f ? 0.f : mag * ((float)(4 * NC + 6 + P.G) * 0x1.04p-24f) + 0x1p-140f;
 }
 
 // ------------------------------------------------------------------ the choice
@@ -461,60 +459,67 @@ POD_DEV uint64_t key_of(double x) {
 }
 
 struct PickShared {
-  int bins[kBins];
+  alignas(16) int bins[kBins];
   unsigned long long lo[32], hi[32];
-  int sums[32];
+  int2 sums[32];
+  float off[32];
   uint32_t near[kNear];            // keys, or pages
   double exact[kNear];
   uint32_t chosen[kHeldPages / 32];
-  int nears, bin, above;
+  int nears, bin, above, inside;
   uint32_t kth;
 };
-
-// Sum of x over the threads before this one.
-POD_DEV int block_sum_before(int x, PickShared& S) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  int s = x;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += y;
-  }
-  __syncthreads();
-  if (lane == 31) S.sums[warp] = s;
-  __syncthreads();
-  const int w = lane < warps && lane < warp ? S.sums[lane] : 0;
-  return s - x + __reduce_add_sync(0xffffffffu, w);
-}
 
 // Two counts of a warp (the same in its lanes): those of the warps before it, and of all.
 POD_DEV int2 warp_sums_before(int x, int y, int2& all, PickShared& S) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  if (lane == 0) S.sums[warp] = make_int2(x, y);
   __syncthreads();
-  if (lane == 0) S.lo[warp] = (unsigned long long)(unsigned)x << 32 | (unsigned)y;
-  __syncthreads();
-  const unsigned long long w = lane < warps ? S.lo[lane] : 0ull;
-  const int wx = (int)(w >> 32), wy = (int)(unsigned)w;
-  all = make_int2(__reduce_add_sync(0xffffffffu, wx), __reduce_add_sync(0xffffffffu, wy));
-  return make_int2(__reduce_add_sync(0xffffffffu, lane < warp ? wx : 0), __reduce_add_sync(0xffffffffu, lane < warp ? wy : 0));
+  const int2 w = lane < warps ? S.sums[lane] : make_int2(0, 0);
+  all = make_int2(__reduce_add_sync(0xffffffffu, w.x), __reduce_add_sync(0xffffffffu, w.y));
+  return make_int2(__reduce_add_sync(0xffffffffu, lane < warp ? w.x : 0), __reduce_add_sync(0xffffffffu, lane < warp ? w.y : 0));
 }
 
 // In which bin, counted from the top, is the need-th largest? `above` keys are larger
-// than all bins. Leaves the bin and the number of keys above it in S.
+// than all bins. Leaves the bin, its keys and the number of keys above it in S. (The first
+// warp's work, 32 bins a lane: two barriers less than a scan by the block.)
 POD_DEV void find_bin(int need, int above, PickShared& S) {
-  const int per = kBins / blockDim.x, top = kBins - 1 - (int)threadIdx.x * per;   // (blockDim divides kBins)
-  int sum = 0;
-  for (int i = 0; i < per; ++i) sum += S.bins[top - i];
-  int before = above + block_sum_before(sum, S);
-  if (before < need && before + sum >= need)
-    for (int i = 0; i < per; ++i) {
-      const int n = S.bins[top - i];
-      if (before < need && before + n >= need) {
-        S.bin = top - i;
-        S.above = before;
-      }
-      before += n;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    const int4* fours = reinterpret_cast<const int4*>(S.bins) + lane;      // a lane's stand 32 fours apart
+    int total[kBins / 128];
+#pragma unroll
+    for (int i = 0; i < kBins / 128; ++i) {
+      const int4 n = fours[i * 32];
+      total[i] = __reduce_add_sync(0xffffffffu, n.x + n.y + n.z + n.w);
     }
+    int set = -1;                                    // of 128 bins, the one with the wanted key
+#pragma unroll
+    for (int i = kBins / 128 - 1; i >= 0; --i) {
+      if (set >= 0) continue;
+      if (above + total[i] >= need) set = i;
+      else above += total[i];
+    }
+    const int4 n = fours[max(set, 0) * 32];
+    const int own = n.x + n.y + n.z + n.w;
+    int s = own;                                     // of the fours from this lane's up
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_down_sync(0xffffffffu, s, o);
+      if (lane + o < 32) s += y;
+    }
+    int over = above + s - own;                      // keys above this four
+    if (over < need && over + own >= need) {
+      int bin = 3, inside = n.w;
+      if (over + inside < need) { over += inside; inside = n.z; bin = 2; }
+      if (over + inside < need) { over += inside; inside = n.y; bin = 1; }
+      if (over + inside < need) { over += inside; inside = n.x; bin = 0; }
+      S.bin = (max(set, 0) * 32 + lane) * 4 + bin;
+      S.above = over;
+      S.inside = inside;
+    }
+  }
   __syncthreads();
 }
 
@@ -554,7 +559,6 @@ POD_DEV uint64_t kth_largest(F each, uint64_t from, int need, int& above, PickSh
     each([&](int, uint64_t x) {
       if (x >= lo && x <= hi) atomicAdd(&S.bins[(x - lo) >> shift], 1);
     });
-    __syncthreads();
     find_bin(need, above, S);
     above = S.above;
     lo += (unsigned long long)S.bin << shift;
@@ -644,31 +648,13 @@ __device__ __noinline__ uint64_t score_again(const PickParams& P, bool few, int 
   return last;
 }
 
-// The need-th largest of the keys that each() hands out, all of them of finite numbers, 0 for
-// none: bins over the range of the values, then the keys of the wanted bin by their
-// ranks among themselves, where they are few.
+// The need-th largest of the keys that each() hands out, all of them of finite numbers
+// between those of lo and hi, 0 for none: bins over the range of the values, then the keys of
+// the wanted bin by their ranks among themselves, where they are few. (S.bins and S.nears are
+// zero.)
 template <typename F>
-POD_DEV uint32_t kth_score(F each, int need, PickShared& S) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, T = blockDim.x;
-  uint32_t lo = 0xffffffffu, hi = 0u;
-  each([&](int, uint32_t x) {
-    lo = min(lo, x - 1);                               // (0 is not the smallest)
-    hi = max(hi, x);
-  });
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  if (lane == 0) {
-    S.lo[warp] = lo;
-    S.hi[warp] = hi;
-  }
-  for (int i = tid; i < kBins; i += T) S.bins[i] = 0;
-  if (tid == 0) S.nears = 0;
-  __syncthreads();
-  {
-    const int w = lane < T / 32 ? lane : 0;
-    lo = __reduce_min_sync(0xffffffffu, (uint32_t)S.lo[w]) + 1;
-    hi = __reduce_max_sync(0xffffffffu, (uint32_t)S.hi[w]);
-  }
+POD_DEV uint32_t kth_score(F each, uint32_t lo, uint32_t hi, int need, PickShared& S) {
+  const int tid = threadIdx.x, T = blockDim.x;
   if (lo == hi) return lo;
   // (monotone: a difference, a product and a truncation, each rounded in order)
   const float v0 = value_of(lo), scale = (kBins - 1) / fmaxf(value_of(hi) - v0, 1e-30f);
@@ -676,9 +662,8 @@ POD_DEV uint32_t kth_score(F each, int need, PickShared& S) {
   each([&](int, uint32_t x) {
     if (x) atomicAdd(&S.bins[bin_of(x)], 1);
   });
-  __syncthreads();
   find_bin(need, 0, S);
-  const int bin = S.bin, above = S.above, count = S.bins[bin];
+  const int bin = S.bin, above = S.above, count = S.inside;
   if (count <= kNear) {
     each([&](int, uint32_t x) {
       if (x && bin_of(x) == bin) S.near[atomicAdd(&S.nears, 1)] = x;
@@ -761,17 +746,36 @@ __global__ void __launch_bounds__(1024) pick_kernel(const __grid_constant__ Pick
       }
     }
   };
+  // the scores' range, and what they may be off by
+  uint32_t lo = 0xffffffffu, hi = 0u;
+  each([&](int, uint32_t x) {
+    lo = min(lo, x - 1);                               // (0 is not the smallest)
+    hi = max(hi, x);
+  });
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
   off = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(off)));
-  if (lane == 0) S.sums[warp] = __float_as_int(off);
+  if (lane == 0) {
+    S.sums[warp] = make_int2((int)lo, (int)hi);
+    S.off[warp] = off;
+  }
+  for (int i = tid; i < kBins; i += threads) S.bins[i] = 0;
   if (tid < kHeldPages / 32) S.chosen[tid] = 0;
+  if (tid == 0) S.nears = 0;
   odd = __syncthreads_or(odd);
-  off = __uint_as_float(__reduce_max_sync(0xffffffffu, (unsigned)S.sums[lane < warps ? lane : 0]));
+  {
+    const int w = lane < warps ? lane : 0;
+    const int2 range = S.sums[w];
+    lo = __reduce_min_sync(0xffffffffu, (uint32_t)range.x) + 1;
+    hi = __reduce_max_sync(0xffffffffu, (uint32_t)range.y);
+    off = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(S.off[w])));
+  }
 
   // keys above `sure` are in, those from `least` to it as far as places are left: the
   // lowest positions, or by their scores in 64 bits
   uint32_t sure = 0xffffffffu, least = 1u;
   if (need > 0 && !odd) {
-    const uint32_t kth = kth_score(each, need, S);
+    const uint32_t kth = kth_score(each, lo, hi, need, S);
     const float v = value_of(kth);
     sure = off == 0.f ? kth : key_of(v + 2.5f * off);
     least = off == 0.f ? kth : key_of(v - 2.5f * off);
@@ -800,6 +804,7 @@ __global__ void __launch_bounds__(1024) pick_kernel(const __grid_constant__ Pick
     });
   };
   count();
+  __syncthreads();                                     // (S.sums is read above)
   int2 all, at = warp_sums_before(full, tied, all, S);
   int ties = P.k - all.x;                              // places for the close ones
   if (all.y > ties && (off != 0.f || odd)) {           // (without an error, equal scores are ties)
@@ -814,6 +819,7 @@ __global__ void __launch_bounds__(1024) pick_kernel(const __grid_constant__ Pick
     last64 = score_again<T, D>(P, few, row, hk, a, b, least, sure, all.y, ties, S);
     again = few ? 1 : 2;
     count();
+    __syncthreads();
     at = warp_sums_before(full, tied, all, S);
     ties = P.k - all.x;
   }
