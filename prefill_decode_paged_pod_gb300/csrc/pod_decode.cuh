@@ -30,6 +30,7 @@
 #include <limits.h>
 #include <math.h>
 
+#include "pod_beside.h"
 #include "pod_decode.h"
 #include "pod_device.cuh"
 
@@ -787,37 +788,6 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
   if (lane == 0 && P.lse) P.lse[item] = lse;
 }
 
-template <typename... A, typename... B>
-cudaError_t launch_beside(void (*kernel)(A...), unsigned grid, unsigned threads, cudaStream_t st, const B&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-template <typename... A, typename... B>
-cudaError_t launch_clusters(void (*kernel)(A...), unsigned grid, unsigned cluster, cudaStream_t st, const B&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kDecodeThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <typename T, int D, int FMT, int NT>
 cudaError_t launch_decode_nt(DecodeParams& P, cudaStream_t st) {
   using S = DecodeShape<T, D, FMT, NT>;
@@ -832,13 +802,13 @@ cudaError_t launch_decode_nt(DecodeParams& P, cudaStream_t st) {
   const long long units = (keys + S::U - 1) / S::U;
   // Short rows whose clusters all fit the GPU at once.
   if (items * 8 <= P.grid && units <= 8 * kShortUnits)
-    return launch_clusters(decode_short_kernel<T, D, FMT, NT, 8>, (unsigned)items * 8, 8, st, P);
-  cudaError_t e = launch_beside(decode_kernel<T, D, FMT, NT>, (unsigned)P.grid, kDecodeThreads, st, P);
+    return launch_beside(decode_short_kernel<T, D, FMT, NT, 8>, (unsigned)items * 8, kDecodeThreads, 0, 8, st, P);
+  cudaError_t e = launch_beside(decode_kernel<T, D, FMT, NT>, (unsigned)P.grid, kDecodeThreads, 0, 1, st, P);
   if (e != cudaSuccess) return e;
   // a warp for each (request, head), or a block of four where a row may have many pieces
   const long long rows = (long long)P.batch * P.H;
-  if (rows <= 2048) return launch_beside(decode_merge_kernel<T, D, S::HT, S::U, 4>, (unsigned)rows, 128, st, P);
-  return launch_beside(decode_merge_kernel<T, D, S::HT, S::U, 1>, (unsigned)((rows + 3) / 4), 128, st, P);
+  if (rows <= 2048) return launch_beside(decode_merge_kernel<T, D, S::HT, S::U, 4>, (unsigned)rows, 128, 0, 1, st, P);
+  return launch_beside(decode_merge_kernel<T, D, S::HT, S::U, 1>, (unsigned)((rows + 3) / 4), 128, 0, 1, st, P);
 }
 
 template <typename T, int FMT>

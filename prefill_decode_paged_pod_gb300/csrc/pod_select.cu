@@ -20,6 +20,7 @@
 #include <string>
 
 #include "../../include/pod.h"
+#include "pod_beside.h"
 #include "pod_decode.h"
 #include "pod_device.cuh"
 
@@ -32,8 +33,7 @@ namespace {
 constexpr int kBoundThreads = 256, kBoundRows = 64;
 constexpr int kScoreThreads = 128, kLeastPages = 16;   // pages of a warp at least
 constexpr int kBinBits = 10, kBins = 1 << kBinBits, kNear = 256;
-constexpr int kHeld = 8;                               // keys of a lane
-constexpr int kHeldPages = 1024 * kHeld;               // pages whose keys a block holds
+constexpr int kHeldPages = 1024 * 8;                   // pages whose keys a block holds
 
 template <typename T>
 struct Pair;
@@ -445,11 +445,13 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_co
 }
 
 // ------------------------------------------------------------------ the choice
-// keys in the order of the values; every NaN above all numbers
+// keys in the order of the values; every NaN above all numbers, or (fp32, where scores with
+// one are computed again) anywhere. fp32 keys lie in [1, kForced): 0 is a page that does not
+// compete, kForced one that is chosen whatever its score.
+constexpr uint32_t kForced = 0xffffffffu;
 POD_DEV uint32_t key_of(float x) {
-  if (x != x) return 0xffffffffu;
-  const uint32_t b = __float_as_uint(x == 0.f ? 0.f : x);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  const uint32_t b = __float_as_uint(x + 0.f);         // (-0 is 0)
+  return min(max(b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u), 1u), kForced - 1);
 }
 POD_DEV float value_of(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
 POD_DEV uint64_t key_of(double x) {
@@ -465,7 +467,7 @@ struct PickShared {
   float off[32];
   uint32_t near[kNear];            // keys, or pages
   double exact[kNear];
-  uint32_t chosen[kHeldPages / 32];
+  bool in[kNear];
   int nears, bin, above, inside;
   uint32_t kth;
 };
@@ -568,26 +570,41 @@ POD_DEV uint64_t kth_largest(F each, uint64_t from, int need, int& above, PickSh
   return lo;
 }
 
-// The exact score of the page at position i: a warp's lanes share the channels.
+// A warp's share of a page's bounds, and with it the page's score in 64 bits.
 template <typename T, int D>
-POD_DEV double score_64(const PickParams& P, int row, int hk, int i, const double (*weight)[D]) {
-  const unsigned page = (unsigned)P.table[row * P.table_stride + i];
-  if (page >= P.num_pages) return -INFINITY;
-  const int lane = threadIdx.x & 31;
-  const T* m = static_cast<const T*>(P.bounds) + ((long long)page * P.Hk + hk) * 2 * D;
-  double s = 0.;
+struct PageBounds {
+  float lo[D / 32], hi[D / 32];
+  bool there;
+  POD_DEV void load(const PickParams& P, int row, int hk, int i) {
+    const unsigned page = (unsigned)P.table[row * P.table_stride + i];
+    const int lane = threadIdx.x & 31;
+    there = page < P.num_pages;
+    if (!there) return;
+    const T* m = static_cast<const T*>(P.bounds) + ((long long)page * P.Hk + hk) * 2 * D + lane;
 #pragma unroll
-  for (int j = lane; j < D; j += 32)
-    s += (double)(float)m[j] * weight[0][j] + (double)(float)m[D + j] * weight[1][j];
+    for (int j = 0; j < D / 32; ++j) {
+      lo[j] = (float)m[j * 32];
+      hi[j] = (float)m[D + j * 32];
+    }
+  }
+  POD_DEV double score(const double (*weight)[D]) const {
+    if (!there) return -INFINITY;
+    const int lane = threadIdx.x & 31;
+    double s = 0.;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
+    for (int j = 0; j < D / 32; ++j)
+      s += (double)lo[j] * weight[0][j * 32 + lane] + (double)hi[j] * weight[1][j * 32 + lane];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+  }
+};
 
 // The pages [a, b) whose fp32 keys are in [least, sure], `close` of them, scored again in
-// 64 bits; of them `ties` are chosen. Few, whose positions stand in S.near: the chosen
-// ones' bits are set in S.chosen, and 0 is returned. Many: their scores are kept, the last
-// chosen one's key is returned, and in `ties` how many of that score.
+// 64 bits; of them `ties` are chosen. Few, whose positions stand in S.near: which of
+// them are chosen stands in S.in, and 0 is returned. Many: their scores are kept, the last
+// chosen one's key is returned, and in `ties` how many of that score. (A block that comes
+// here ends later than the others, so its loads are asked for together.)
 template <typename T, int D>
 __device__ __noinline__ uint64_t score_again(const PickParams& P, bool few, int row, int hk, int a, int b, uint32_t least,
                                              uint32_t sure, int close, int& ties, PickShared& S) {
@@ -595,20 +612,35 @@ __device__ __noinline__ uint64_t score_again(const PickParams& P, bool few, int 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   const long long item = (long long)row * P.Hk + hk;
   const T* q = static_cast<const T*>(P.q) + row * P.q_stride + (long long)hk * P.G * D;
+  __syncthreads();                                     // (S.near is written)
+  PageBounds<T, D> page;
+  if (few && warp < close) page.load(P, row, hk, (int)S.near[warp]);
   for (int j = tid; j < D; j += threads) {
-    double up = 0., down = 0.;
-    for (int g = 0; g < P.G; ++g) {
-      const double x = (double)(float)q[(long long)g * D + j];
-      up += x < 0. ? 0. : x;
-      down += x > 0. ? 0. : x;
+    // sums of the heads, exact as pairs of fp32 numbers (a sum and what its rounding left)
+    float up = 0.f, up2 = 0.f, down = 0.f, down2 = 0.f;
+    for (int g = 0; g < P.G; g += 8) {                 // (eight loads at a time)
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = g + i < P.G ? (float)q[(long long)(g + i) * D + j] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float u = x[i] < 0.f ? 0.f : x[i], d = x[i] > 0.f ? 0.f : x[i];
+        const float su = up + u, sd = down + d, tu = su - up, td = sd - down;
+        up2 += (up - (su - tu)) + (u - tu);
+        down2 += (down - (sd - td)) + (d - td);
+        up = su;
+        down = sd;
+      }
     }
-    weight[0][j] = down;
-    weight[1][j] = up;
+    // (an infinity leaves a NaN as its remainder)
+    weight[0][j] = fabsf(down) < INFINITY ? (double)down + (double)down2 : (double)down;
+    weight[1][j] = fabsf(up) < INFINITY ? (double)up + (double)up2 : (double)up;
   }
   __syncthreads();
   if (few) {
     for (int c = warp; c < close; c += threads / 32) {
-      const double s = score_64<T, D>(P, row, hk, (int)S.near[c], weight);
+      if (c != warp) page.load(P, row, hk, (int)S.near[c]);
+      const double s = page.score(weight);
       if (lane == 0) S.exact[c] = s;
     }
     __syncthreads();
@@ -620,7 +652,7 @@ __device__ __noinline__ uint64_t score_again(const PickParams& P, bool few, int 
         const uint64_t y = key_of(S.exact[d]);
         before += y > x || (y == x && (int)S.near[d] < i);
       }
-      if (before < ties) atomicOr(&S.chosen[i >> 5], 1u << (i & 31));
+      S.in[c] = before < ties;
     }
     __syncthreads();
     return 0;
@@ -633,7 +665,8 @@ __device__ __noinline__ uint64_t score_again(const PickParams& P, bool few, int 
   };
   for (int i = a + warp; i < b; i += threads / 32) {
     if (!is_close(i)) continue;
-    const double s = score_64<T, D>(P, row, hk, i, weight);
+    page.load(P, row, hk, i);
+    const double s = page.score(weight);
     if (lane == 0) again[i] = s;
   }
   __syncthreads();
@@ -648,8 +681,8 @@ __device__ __noinline__ uint64_t score_again(const PickParams& P, bool few, int 
   return last;
 }
 
-// The need-th largest of the keys that each() hands out, all of them of finite numbers
-// between those of lo and hi, 0 for none: bins over the range of the values, then the keys of
+// The need-th largest of the competing keys that each() hands out, all of them of finite
+// numbers between those of lo and hi: bins over the range of the values, then the keys of
 // the wanted bin by their ranks among themselves, where they are few. (S.bins and S.nears are
 // zero.)
 template <typename F>
@@ -660,13 +693,13 @@ POD_DEV uint32_t kth_score(F each, uint32_t lo, uint32_t hi, int need, PickShare
   const float v0 = value_of(lo), scale = (kBins - 1) / fmaxf(value_of(hi) - v0, 1e-30f);
   auto bin_of = [&](uint32_t x) { return min(kBins - 1, (int)((value_of(x) - v0) * scale)); };
   each([&](int, uint32_t x) {
-    if (x) atomicAdd(&S.bins[bin_of(x)], 1);
+    if (x - 1 < kForced - 1) atomicAdd(&S.bins[bin_of(x)], 1);
   });
   find_bin(need, 0, S);
   const int bin = S.bin, above = S.above, count = S.inside;
   if (count <= kNear) {
     each([&](int, uint32_t x) {
-      if (x && bin_of(x) == bin) S.near[atomicAdd(&S.nears, 1)] = x;
+      if (bin_of(x) == bin && x - 1 < kForced - 1) S.near[atomicAdd(&S.nears, 1)] = x;
     });
     __syncthreads();
     for (int i = tid; i < count; i += T) {
@@ -685,18 +718,19 @@ POD_DEV uint32_t kth_score(F each, uint32_t lo, uint32_t hi, int need, PickShare
   return (uint32_t)kth_largest(
       [&](auto f) {
         each([&](int i, uint32_t x) {
-          if (x && bin_of(x) == bin) f(i, (uint64_t)x);
+          if (bin_of(x) == bin && x - 1 < kForced - 1) f(i, (uint64_t)x);
         });
       },
       1ull, need - above, larger, S);
 }
 
-// A block makes one choice. HELD: the keys of up to 256 pages a warp, eight a lane, stay in
-// registers (read from memory in every pass instead, for more pages than a block can hold,
-// and three times the instructions). A run of pages is a warp's, so that the chosen
-// ones come out in order.
-template <typename T, int D, bool HELD>
-__global__ void __launch_bounds__(1024) pick_kernel(const __grid_constant__ PickParams P) {
+// A block makes one choice. HELD > 0: a lane's keys stay in registers (0: they are read in every
+// pass, for more pages than a block can hold). A run of pages is a warp's, so that the chosen
+// ones come out in order. Many choices take blocks of few warps with 16 keys a lane: the
+// work besides the keys, and the waits at barriers, grow with the warps (512 choices of
+// some 1300 pages: 19 us by eight warps each, PICK_US by four).
+template <typename T, int D, int HELD>
+__global__ void __launch_bounds__(HELD == 16 ? 256 : 1024) pick_kernel(const __grid_constant__ PickParams P) {
   __shared__ PickShared S;
   asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
@@ -713,44 +747,42 @@ __global__ void __launch_bounds__(1024) pick_kernel(const __grid_constant__ Pick
   // pages [a, b) compete for `need` places
   const int a = P.first, b = n - P.last, need = P.k - P.first - P.last;
   const float* score = P.score + item * P.width;
-  const int run = HELD ? 32 * kHeld : ((n + 31) / 32 + warps - 1) / warps * 32;
+  const int run = HELD ? 32 * HELD : ((n + 31) / 32 + warps - 1) / warps * 32;
   const int i0 = min(n, warp * run), i1 = min(n, i0 + run);
   float off = 0.f;
   bool odd = false;                                    // (an infinite or NaN bound or score)
+  auto key_at = [&](int i, float x) {
+    if (i >= i1) return 0u;
+    if (i < a || i >= b) return kForced;
+    odd |= !(fabsf(x) < 0x1p120f);
+    return key_of(x);
+  };
+  uint32_t held[HELD ? HELD : 1];
+  if constexpr (HELD > 0) {
+    float x[HELD];                                     // (all loads before the first use)
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) x[j] = i0 + j * 32 + lane < i1 ? score[i0 + j * 32 + lane] : 0.f;
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) held[j] = key_at(i0 + j * 32 + lane, x[j]);
+  }
   for (int i = tid; i < (n + P.per - 1) / P.per; i += threads) {
     const float e = P.off[item * P.chunks + i];
     odd |= !(e < 0x1p100f);
     off = fmaxf(off, e);
   }
-  uint32_t held[HELD ? kHeld : 1];                     // 0: does not compete
-  auto read = [&](int i) {
-    if (i < a || i >= b || i >= i1) return 0u;
-    const float x = score[i];
-    odd |= !(fabsf(x) < 0x1p120f);
-    return key_of(x);
-  };
-  if constexpr (HELD) {
-#pragma unroll
-    for (int j = 0; j < kHeld; ++j) held[j] = read(i0 + j * 32 + lane);
-  } else {
-    for (int i = i0 + lane; i < i1; i += 32) read(i);
-  }
   auto each = [&](auto f) {                            // (the lanes of a warp together)
-    if constexpr (HELD) {
+    if constexpr (HELD > 0) {
 #pragma unroll
-      for (int j = 0; j < kHeld; ++j) f(i0 + j * 32 + lane, held[j]);
+      for (int j = 0; j < HELD; ++j) f(i0 + j * 32 + lane, held[j]);
     } else {
-      for (int i = i0; i < i1; i += 32) {
-        const int k = i + lane;
-        f(k, k < a || k >= b || k >= i1 ? 0u : key_of(score[k]));
-      }
+      for (int i = i0; i < i1; i += 32) f(i + lane, key_at(i + lane, i + lane < i1 ? score[i + lane] : 0.f));
     }
   };
   // the scores' range, and what they may be off by
   uint32_t lo = 0xffffffffu, hi = 0u;
   each([&](int, uint32_t x) {
-    lo = min(lo, x - 1);                               // (0 is not the smallest)
-    hi = max(hi, x);
+    lo = min(lo, x - 1);                               // (0 is not the smallest, kForced not the largest)
+    hi = max(hi, x + 1);
   });
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
@@ -760,55 +792,43 @@ __global__ void __launch_bounds__(1024) pick_kernel(const __grid_constant__ Pick
     S.off[warp] = off;
   }
   for (int i = tid; i < kBins; i += threads) S.bins[i] = 0;
-  if (tid < kHeldPages / 32) S.chosen[tid] = 0;
   if (tid == 0) S.nears = 0;
   odd = __syncthreads_or(odd);
   {
     const int w = lane < warps ? lane : 0;
     const int2 range = S.sums[w];
     lo = __reduce_min_sync(0xffffffffu, (uint32_t)range.x) + 1;
-    hi = __reduce_max_sync(0xffffffffu, (uint32_t)range.y);
+    hi = __reduce_max_sync(0xffffffffu, (uint32_t)range.y) - 1;
     off = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(S.off[w])));
   }
 
   // keys above `sure` are in, those from `least` to it as far as places are left: the
   // lowest positions, or by their scores in 64 bits
-  uint32_t sure = 0xffffffffu, least = 1u;
+  uint32_t sure = kForced - 1, least = need > 0 ? 1u : kForced;
   if (need > 0 && !odd) {
     const uint32_t kth = kth_score(each, lo, hi, need, S);
     const float v = value_of(kth);
     sure = off == 0.f ? kth : key_of(v + 2.5f * off);
     least = off == 0.f ? kth : key_of(v - 2.5f * off);
   }
-  if (need == 0) least = 0xffffffffu, sure = 0xffffffffu;
-  uint64_t last64 = 0;
-  int again = 0;                                       // 1: the few are marked, 2: their scores are kept
-  const double* exact = P.again + item * P.width;
-  auto grade = [&](int i, uint32_t x) {                // 2: in, 1: in as far as places are left
-    if (i >= i1) return 0;
-    if (i < a || i >= b) return 2;
-    if (x > sure) return 2;
-    if (x < least || need == 0) return 0;
-    if (again == 0) return 1;
-    if (again == 1) return S.chosen[i >> 5] >> (i & 31) & 1 ? 2 : 0;
-    const uint64_t y = key_of(exact[i]);
-    return y > last64 ? 2 : y == last64 ? 1 : 0;
-  };
-  int full, tied;
+  int full, close;
   auto count = [&]() {
-    full = tied = 0;
-    each([&](int i, uint32_t x) {
-      const int g = grade(i, x);
-      full += __popc(__ballot_sync(0xffffffffu, g == 2));
-      tied += __popc(__ballot_sync(0xffffffffu, g == 1));
+    full = close = 0;
+    each([&](int, uint32_t x) {
+      full += x > sure;
+      close += x >= least;
     });
+    full = __reduce_add_sync(0xffffffffu, full);
+    close = __reduce_add_sync(0xffffffffu, close) - full;
   };
   count();
   __syncthreads();                                     // (S.sums is read above)
-  int2 all, at = warp_sums_before(full, tied, all, S);
+  int2 all, at = warp_sums_before(full, close, all, S);
   int ties = P.k - all.x;                              // places for the close ones
+  uint64_t last64 = 0;
+  bool exactly = false;
   if (all.y > ties && (off != 0.f || odd)) {           // (without an error, equal scores are ties)
-    const bool few = HELD && all.y <= kNear;
+    const bool few = HELD > 0 && all.y <= kNear;
     if (few) {
       if (tid == 0) S.nears = 0;
       __syncthreads();
@@ -817,15 +837,59 @@ __global__ void __launch_bounds__(1024) pick_kernel(const __grid_constant__ Pick
       });
     }
     last64 = score_again<T, D>(P, few, row, hk, a, b, least, sure, all.y, ties, S);
-    again = few ? 1 : 2;
-    count();
+    if (few) {                                         // the chosen ones are in, the others out
+      if constexpr (HELD > 0) {
+#pragma unroll
+        for (int j = 0; j < HELD; ++j)
+          if (held[j] >= least && held[j] <= sure) {
+            held[j] = 0u;
+            for (int c = 0; c < all.y; ++c)
+              if (S.near[c] == (uint32_t)(i0 + j * 32 + lane)) held[j] = S.in[c] ? kForced : 0u;
+          }
+      }
+      least = sure + 1;
+      count();
+      __syncthreads();
+      at = warp_sums_before(full, close, all, S);
+      ties = 0;
+    } else {
+      exactly = true;
+    }
+  }
+  const unsigned below = (1u << lane) - 1;
+  if (!exactly && all.y <= ties) {                     // all close ones are in
+    int to = at.x + at.y;
+    each([&](int i, uint32_t x) {
+      const unsigned m = __ballot_sync(0xffffffffu, x >= least);
+      const int slot = to + __popc(m & below);
+      if (x >= least && slot < P.k) out[slot] = i;
+      to += __popc(m);
+    });
+    return;
+  }
+  // some close ones are: by position, or by their scores in 64 bits and then by position
+  const double* exact = P.again + item * P.width;
+  auto grade = [&](int i, uint32_t x) {                // 2: in, 1: in as far as places are left
+    if (x > sure) return 2;
+    if (x < least) return 0;
+    if (!exactly) return 1;
+    const uint64_t y = key_of(exact[i]);
+    return y > last64 ? 2 : y == last64 ? 1 : 0;
+  };
+  if (exactly) {
+    full = close = 0;
+    each([&](int i, uint32_t x) {
+      const int g = grade(i, x);
+      full += g == 2;
+      close += g == 1;
+    });
+    full = __reduce_add_sync(0xffffffffu, full);
+    close = __reduce_add_sync(0xffffffffu, close);
     __syncthreads();
-    at = warp_sums_before(full, tied, all, S);
+    at = warp_sums_before(full, close, all, S);
     ties = P.k - all.x;
   }
-  // (full and tied of the warps before: at most `ties` of the tied are in)
   int tied_at = at.y, to = at.x + min(at.y, ties);
-  const unsigned below = (1u << lane) - 1;
   each([&](int i, uint32_t x) {
     const int g = grade(i, x);
     const unsigned m1 = __ballot_sync(0xffffffffu, g == 1);
@@ -844,30 +908,14 @@ pod_status fail(pod_status code, const std::string& msg) {
   return code;
 }
 
-template <typename... A, typename... B>
-cudaError_t launch_beside(void (*kernel)(A...), unsigned grid, unsigned threads, unsigned shared, cudaStream_t st,
-                          const B&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = shared;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <typename T, int D>
 cudaError_t launch_bounds(const BoundParams& P, int fmt, cudaStream_t st) {
   const long long blocks = (P.rows + P.span - 1) / P.span;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const unsigned grid = (unsigned)blocks;
-  return fmt == POD_KV_16BIT ? launch_beside(bounds_kernel<T, D, POD_KV_16BIT>, grid, kBoundThreads, 0, st, P)
-         : fmt == POD_KV_E4M3 ? launch_beside(bounds_kernel<T, D, POD_KV_E4M3>, grid, kBoundThreads, 0, st, P)
-                              : launch_beside(bounds_kernel<T, D, POD_KV_E4M3_BLOCK>, grid, kBoundThreads, 0, st, P);
+  return fmt == POD_KV_16BIT ? launch_beside(bounds_kernel<T, D, POD_KV_16BIT>, grid, kBoundThreads, 0, 1, st, P)
+         : fmt == POD_KV_E4M3 ? launch_beside(bounds_kernel<T, D, POD_KV_E4M3>, grid, kBoundThreads, 0, 1, st, P)
+                              : launch_beside(bounds_kernel<T, D, POD_KV_E4M3_BLOCK>, grid, kBoundThreads, 0, 1, st, P);
 }
 template <typename T>
 cudaError_t launch_bounds_d(const BoundParams& P, int d, int fmt, cudaStream_t st) {
@@ -881,14 +929,17 @@ cudaError_t launch_pick(const PickParams& P, cudaStream_t st) {
   const long long blocks = (warps + per - 1) / per, items = (long long)P.batch * P.Hk;
   if (blocks > 0x7fffffff || items > 0x7fffffff) return cudaErrorInvalidConfiguration;
   if (P.width > P.k) {                                 // (else every page is chosen)
-    const cudaError_t e = launch_beside(score_kernel<T, D>, (unsigned)blocks, kScoreThreads, kScoreShared, st, P);
+    const cudaError_t e = launch_beside(score_kernel<T, D>, (unsigned)blocks, kScoreThreads, kScoreShared, 1, st, P);
     if (e != cudaSuccess) return e;
   }
-  if (P.width > kHeldPages) return launch_beside(pick_kernel<T, D, false>, (unsigned)items, 1024, 0, st, P);
   // threads that hold the longest row's keys
+  const unsigned grid = (unsigned)items;
+  if (items >= 2 * 152 && P.width <= 256 * 16)
+    return launch_beside(pick_kernel<T, D, 16>, grid, P.width <= 128 * 16 ? 128 : 256, 0, 1, st, P);
   unsigned threads = 256;
-  while ((int)threads * kHeld < P.width) threads *= 2;
-  return launch_beside(pick_kernel<T, D, true>, (unsigned)items, threads, 0, st, P);
+  while (threads < 1024 && (int)threads * 8 < P.width) threads *= 2;
+  return P.width <= kHeldPages ? launch_beside(pick_kernel<T, D, 8>, grid, threads, 0, 1, st, P)
+                               : launch_beside(pick_kernel<T, D, 0>, grid, 1024, 0, 1, st, P);
 }
 template <typename T>
 cudaError_t launch_pick_d(const PickParams& P, int d, cudaStream_t st) {

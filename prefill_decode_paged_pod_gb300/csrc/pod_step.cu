@@ -19,6 +19,7 @@
 #include <string>
 
 #include "../../include/pod.h"
+#include "pod_beside.h"
 #include "pod_decode.h"
 #include "pod_device.cuh"
 
@@ -281,20 +282,6 @@ pod_status fail(pod_status code, const std::string& msg) {
   return code;
 }
 
-template <typename... A, typename... B>
-cudaError_t launch_beside(void (*kernel)(A...), unsigned grid, unsigned threads, cudaStream_t st, const B&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 }  // namespace
 
 extern "C" pod_status pod_step_tables(const pod_step_args* a, void* stream) {
@@ -339,11 +326,12 @@ extern "C" pod_status pod_step_tables(const pod_step_args* a, void* stream) {
   P.rows_here = !a->kv_indptr && a->max_rows <= 2 * kStepThreads;
   cudaStream_t st = (cudaStream_t)stream;
   const int threads = a->batch <= 128 ? 128 : a->batch >= kStepThreads ? kStepThreads : (a->batch + 31) / 32 * 32;
-  cudaError_t e = launch_beside(step_kernel, 1, (unsigned)threads, st, P);
+  cudaError_t e = launch_beside(step_kernel, 1, (unsigned)threads, 0, 1, st, P);
   const int64_t entries = (int64_t)a->max_rows + (a->kv_indptr ? a->max_pages : 0);
   if (e == cudaSuccess && !P.rows_here && entries) {
     const int64_t blocks = (entries + kRowThreads - 1) / kRowThreads;
-    e = launch_beside(step_rows_kernel, (unsigned)(blocks < 152 * 8 ? blocks : 152 * 8), kRowThreads, st, P);
+    e = launch_beside(step_rows_kernel, (unsigned)(blocks < 152 * 8 ? blocks : 152 * 8), kRowThreads, 0, 1, st,
+                      P);
   }
   if (e != cudaSuccess) return fail(POD_ERR_CUDA, std::string("step tables launch: ") + cudaGetErrorString(e));
   return POD_OK;
