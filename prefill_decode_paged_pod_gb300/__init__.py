@@ -980,18 +980,23 @@ def pod_step_tables(block_table, kv_lens, new_lens, free_pages, free_count, page
     lo = _whole("kv_lens_out", kv_lens_out, (batch,), i32, dev)
     co = _whole("free_count_out", free_count_out, (1,), i32, dev)
     if out is None:
-        # one allocation for the int32 arrays, each 16-byte aligned
-        a, b, r, p = ((n + 3) // 4 * 4 for n in (batch + 1, batch, rows, pages))
-        buf = _empty((a + 2 * r + (a + b + p if pages else 0),), i32, kv_lens, stream)
-        slots = _empty((rows,), torch.int64, kv_lens, stream)
-        q_indptr, requests, positions = buf[:batch + 1], buf[a:a + rows], buf[a + r:a + r + rows]
-        indptr = indices = last = None
+        # one allocation, cut into the arrays (slots first: they are 64 bits wide)
+        sizes = (2 * rows, batch + 1, rows, rows, batch + 1, batch, pages) if pages else (2 * rows, batch + 1, rows, rows)
+        buf = _empty((sum(sizes),), i32, kv_lens, stream)
+        sl = buf.data_ptr()
+        qi = sl + 8 * rows
+        rq = qi + 4 * (batch + 1)
+        po = rq + 4 * rows
+        ip = la = ix = 0
         if pages:
-            o = a + 2 * r
-            indptr, last, indices = buf[o:o + batch + 1], buf[o + a:o + a + batch], buf[o + a + b:o + a + b + pages]
-        base = buf.data_ptr()
-        qi, rq, po, sl = base, base + 4 * a, base + 4 * (a + r), slots.data_ptr()
-        ip, la, ix = (base + 4 * o, base + 4 * (o + a), base + 4 * (o + a + b)) if pages else (0, 0, 0)
+            ip = po + 4 * rows
+            la = ip + 4 * (batch + 1)
+            ix = la + 4 * batch
+            slots, q_indptr, requests, positions, indptr, last, indices = buf.split_with_sizes(sizes)
+        else:
+            slots, q_indptr, requests, positions = buf.split_with_sizes(sizes)
+            indptr = last = indices = None
+        slots = slots.view(torch.int64)
     else:
         _, q_indptr, requests, positions, slots, indptr, indices, last = out
         qi = _whole("q_indptr", q_indptr, (batch + 1,), i32, dev)

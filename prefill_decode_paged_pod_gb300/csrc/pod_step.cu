@@ -87,26 +87,23 @@ POD_DEV void block_scan(long long* x, long long* all, long long (*sh)[N]) {
 }
 
 struct Step {
-  int had, has;                                    // pages before and after
-  long long old, now;                              // keys
+  int old, now;                                    // keys before and after
+  int had, has;                                    // their pages
   bool wants;                                      // grows
   int status;                                      // bits for a length out of range, or past its row
 };
-POD_DEV Step step_of(const StepParams& P, int r) {
+POD_DEV int pages_for(const StepParams& P, int keys) { return (int)(((unsigned)keys + P.ps - 1) / (unsigned)P.ps); }
+POD_DEV Step step_of(const StepParams& P, int len, int n) {
   Step s;
-  const long long most = (long long)P.width * P.ps;
-  const int len = P.lens[r], n = P.news[r];
-  s.old = min(max((long long)len, 0ll), most);
+  const int most = P.width * P.ps;                 // (at most 2^30)
+  s.old = min(max(len, 0), most);
   s.status = len != s.old ? kStatusSlot : 0;
-  s.now = max(0ll, s.old + n);
-  s.wants = n > 0;
-  if (s.now > most) {
-    s.wants = false;
-    s.status |= kStatusNoRoom;
-    s.now = s.old;
-  }
-  s.had = (int)((s.old + P.ps - 1) / P.ps);
-  s.has = (int)((s.now + P.ps - 1) / P.ps);
+  const long long now = max(0ll, (long long)s.old + n);
+  s.wants = n > 0 && now <= most;
+  if (now > most) s.status |= kStatusNoRoom;
+  s.now = now > most ? s.old : (int)now;
+  s.had = pages_for(P, s.old);
+  s.has = pages_for(P, s.now);
   return s;
 }
 
@@ -147,7 +144,7 @@ POD_DEV int find_off(const int* off, int n, int x) {
 }
 
 __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constant__ StepParams P) {
-  __shared__ long long sh2[32][2], sh3[32][3];
+  __shared__ long long sh1[32][1], sh3[32][3];
   __shared__ int sh_off[kStepThreads], sh_first[kStepThreads];   // of the round's requests: pages before, first page moved
   asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, T = blockDim.x;
@@ -159,13 +156,13 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constan
     const int r = base + tid;
     int n = 0, first = 0;
     if (r < P.batch) {
-      const Step s = step_of(P, r);
+      const Step s = step_of(P, P.lens[r], P.news[r]);
       n = max(0, s.had - s.has);
       first = s.has;
     }
     if (!__syncthreads_or(n)) continue;            // (most steps take nothing back)
-    long long x[2] = {n, 0}, all[2];
-    block_scan<2>(x, all, sh2);
+    long long x[1] = {n}, all[1];
+    block_scan<1>(x, all, sh1);
     // (a round gives back more than 2^31 pages only where the stack is long full)
     sh_off[tid] = (int)min(x[0], 0x7fffffffll);
     sh_first[tid] = first;
@@ -197,29 +194,34 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constan
   for (int base = 0; base < P.batch; base += T) {
     const int r = base + tid;
     Step s = {};
-    if (r < P.batch) s = step_of(P, r);
+    if (r < P.batch) s = step_of(P, P.lens[r], P.news[r]);
     bad |= s.status;
-    const int need = s.wants ? s.has - s.had : 0;
-    const long long n = s.wants ? s.now - s.old : 0;
-    long long x[2] = {need, n}, all[2];
-    block_scan<2>(x, all, sh2);
+    const int need = s.wants ? s.has - s.had : 0, n = s.wants ? s.now - s.old : 0;
+    // pages and rows asked for, and the pages of all, each as sums over the requests before
+    long long x[3] = {need, n, s.has}, all[3];
+    block_scan<3>(x, all, sh3);
+    long long y[3] = {x[0], x[1], x[2]}, sums[3] = {all[0], all[1], all[2]};   // of those that are granted
     const long long p0 = pages + x[0], r0 = rows + x[1];
-    const bool granted = s.wants && p0 + need <= top && r0 + n <= P.max_rows;
-    if (s.wants && !granted) {
-      bad |= kStatusNoRoom;
-      s.now = s.old;
-      s.has = s.had;
+    if (pages + all[0] > top || rows + all[1] > P.max_rows) {
+      // (the granted ones come before every refused one)
+      const bool granted = s.wants && p0 + need <= top && r0 + n <= P.max_rows;
+      if (s.wants && !granted) {
+        bad |= kStatusNoRoom;
+        s.now = s.old;
+        s.has = s.had;
+      }
+      y[0] = granted ? need : 0;
+      y[1] = granted ? n : 0;
+      y[2] = s.has;
+      block_scan<3>(y, sums, sh3);
     }
-    // (the granted ones come before every refused one)
-    long long y[3] = {granted ? need : 0, granted ? n : 0, r < P.batch ? s.has : 0}, sums[3];
-    block_scan<3>(y, sums, sh3);
     rows_taken += sums[1];
     if (r < P.batch) {
-      P.lens_out[r] = (int)s.now;
+      P.lens_out[r] = s.now;
       P.q_indptr[r + 1] = (int)min(r0 + n, rows_taken);
       if (P.kv_indptr) {
         P.kv_indptr[r + 1] = (int)min(kv + y[2] + s.has, (long long)INT_MAX);
-        P.last_page_len[r] = s.now ? (int)((s.now - 1) % P.ps) + 1 : 0;
+        P.last_page_len[r] = s.now ? (int)((unsigned)(s.now - 1) % (unsigned)P.ps) + 1 : 0;
       }
     }
     sh_off[tid] = (int)y[0];
