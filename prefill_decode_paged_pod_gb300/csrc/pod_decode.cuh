@@ -45,7 +45,6 @@ struct DecodeShape {
   static constexpr int E = FMT == POD_KV_16BIT ? 2 : 1;           // bytes of an element
   static constexpr int MT = FMT == POD_KV_16BIT ? (D == 64 ? 2 : 1) : (D == 64 ? 4 : D == 128 ? 2 : 1);
   static constexpr int TK = 16 * MT;                              // keys of a warp's tile
-  static constexpr int U = TK * kDecodeWarps;                     // keys of a unit
   static constexpr int HT = 8 * NT;                               // query heads of a tile
   // A lane's chunk of a key: a quarter of K's row, an eighth of V's, at most 32 bytes.
   static constexpr int WK = D * E / 16 < 8 ? D * E / 16 : 8;      // 32-bit words of a chunk of K
@@ -130,9 +129,9 @@ POD_DEV int offsetof_m(int what, int w, int h) {
   return (kDecodeWarps * HT * D + (what * kDecodeWarps + w) * HT + h) * 4;
 }
 
-// Keys v0 to v1 of a request, for `heads` query heads from h0 on, dealt to the warps tile by tile.
+// A warp's tiles at v, v + step, ... below v1 of a request's keys, for `heads` query heads from h0 on.
 template <typename T, int D, int FMT, int NT>
-POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h0, int heads, int v0, int v1,
+POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h0, int heads, int v, int step, int v1,
                     DecodeShared<D, 8 * NT>& sh) {
   using S = DecodeShape<T, D, FMT, NT>;
   using M = typename std::conditional<FMT == POD_KV_16BIT, T, __half>::type;   // operands of the products
@@ -140,57 +139,6 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
   constexpr float kUp = weight_up<T, FMT>();
   constexpr int MT = S::MT, TK = S::TK;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  // ---- Q as the columns of S^T, and the factor that takes a column to base-2 logits
-  uint32_t qf[NT][S::NK][S::CK / 2];
-  float xs[NT][2];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int h = n * 8 + g;
-    const T* src = static_cast<const T*>(P.q) + (long long)row * P.q_stride + (long long)(h0 + h) * D;
-    uint32_t w[S::NK][S::CK / 2];
-#pragma unroll
-    for (int b = 0; b < S::NK; ++b)
-#pragma unroll
-      for (int c = 0; c < S::CK / 8; ++c) {
-        uint4 r = make_uint4(0, 0, 0, 0);
-        if (h < heads) r = *reinterpret_cast<const uint4*>(src + (b * 4 + t) * S::CK + c * 8);
-        w[b][4 * c] = r.x; w[b][4 * c + 1] = r.y; w[b][4 * c + 2] = r.z; w[b][4 * c + 3] = r.w;
-      }
-    if constexpr (FMT == POD_KV_16BIT) {
-      xs[n][0] = xs[n][1] = P.scale_log2;
-#pragma unroll
-      for (int b = 0; b < S::NK; ++b)
-#pragma unroll
-        for (int i = 0; i < S::CK / 2; ++i) qf[n][b][i] = w[b][i];
-    } else {
-      // fp16 operands: the row by the power of two that brings its largest element to
-      // [2^14, 2^15), so that bf16 rows keep all bits down to 2^-38 of it
-      float am = 0.f;
-#pragma unroll
-      for (int b = 0; b < S::NK; ++b)
-#pragma unroll
-        for (int i = 0; i < S::CK / 2; ++i) {
-          const float2 f = Pack<T>::unpack(w[b][i]);
-          am = fmaxf(am, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
-      am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-      am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-      const int ex = (int)(__float_as_uint(am) >> 23) - 127;            // (-127: zeros and subnormals)
-      const int e = ex >= 128 ? 0 : min(14 - ex, 126);
-      const float up = __uint_as_float((uint32_t)(127 + e) << 23), down = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-      for (int b = 0; b < S::NK; ++b)
-#pragma unroll
-        for (int i = 0; i < S::CK / 2; ++i) {
-          const float2 f = Pack<T>::unpack(w[b][i]);
-          qf[n][b][i] = Pack<M>::two(f.x * up, f.y * up);
-        }
-      const float d0 = __shfl_sync(0xffffffffu, down, 8 * t), d1 = __shfl_sync(0xffffffffu, down, 8 * t + 4);
-      xs[n][0] = d0 * P.scale_log2;
-      xs[n][1] = d1 * P.scale_log2;
-    }
-  }
-
   float o[NT][S::NV][S::CV / 2][4], m[NT][2], mv[NT][2], l[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -281,29 +229,83 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
       }
   };
 
-  int v = v0 + warp * TK;
-  Place p1[S::IDX], p2[S::IDX];                    // with their position, with their page
+  Place p0[S::IDX], p1[S::IDX], p2[S::IDX];        // with their position, with their page
 #pragma unroll
   for (int j = 0; j < S::IDX; ++j) {
-    Place p0 = place(v, j);
-    p2[j] = place(v + S::U, j);
-    p1[j] = place(v + 2 * S::U, j);
-    page_at(p0);
-    page_at(p2[j]);
-    idx[j] = index_of(p0);
+    p0[j] = place(v, j);
+    p2[j] = place(v + step, j);
+    p1[j] = place(v + 2 * step, j);
   }
+#pragma unroll
+  for (int j = 0; j < S::IDX; ++j) {
+    page_at(p0[j]);
+    page_at(p2[j]);
+  }
+  // ---- Q as the columns of S^T, and the factor that takes a column to base-2 logits
+  uint32_t qf[NT][S::NK][S::CK / 2];
+  float xs[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int h = n * 8 + g;
+    const T* src = static_cast<const T*>(P.q) + (long long)row * P.q_stride + (long long)(h0 + h) * D;
+    uint32_t w[S::NK][S::CK / 2];
+#pragma unroll
+    for (int b = 0; b < S::NK; ++b)
+#pragma unroll
+      for (int c = 0; c < S::CK / 8; ++c) {
+        uint4 r = make_uint4(0, 0, 0, 0);
+        if (h < heads) r = *reinterpret_cast<const uint4*>(src + (b * 4 + t) * S::CK + c * 8);
+        w[b][4 * c] = r.x; w[b][4 * c + 1] = r.y; w[b][4 * c + 2] = r.z; w[b][4 * c + 3] = r.w;
+      }
+    if constexpr (FMT == POD_KV_16BIT) {
+      xs[n][0] = xs[n][1] = P.scale_log2;
+#pragma unroll
+      for (int b = 0; b < S::NK; ++b)
+#pragma unroll
+        for (int i = 0; i < S::CK / 2; ++i) qf[n][b][i] = w[b][i];
+    } else {
+      // fp16 operands: the row by the power of two that brings its largest element to
+      // [2^14, 2^15), so that bf16 rows keep all bits down to 2^-38 of it
+      float am = 0.f;
+#pragma unroll
+      for (int b = 0; b < S::NK; ++b)
+#pragma unroll
+        for (int i = 0; i < S::CK / 2; ++i) {
+          const float2 f = Pack<T>::unpack(w[b][i]);
+          am = fmaxf(am, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+      am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+      const int ex = (int)(__float_as_uint(am) >> 23) - 127;            // (-127: zeros and subnormals)
+      const int e = ex >= 128 ? 0 : min(14 - ex, 126);
+      const float up = __uint_as_float((uint32_t)(127 + e) << 23), down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+      for (int b = 0; b < S::NK; ++b)
+#pragma unroll
+        for (int i = 0; i < S::CK / 2; ++i) {
+          const float2 f = Pack<T>::unpack(w[b][i]);
+          qf[n][b][i] = Pack<M>::two(f.x * up, f.y * up);
+        }
+      const float d0 = __shfl_sync(0xffffffffu, down, 8 * t), d1 = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+      xs[n][0] = d0 * P.scale_log2;
+      xs[n][1] = d1 * P.scale_log2;
+    }
+  }
+
+#pragma unroll
+  for (int j = 0; j < S::IDX; ++j) idx[j] = index_of(p0[j]);
   if (v < v1) {
     load_k();
     load_v();
   }
-  for (; v < v1; v += S::U) {
+  for (; v < v1; v += step) {
 #pragma unroll
     for (int j = 0; j < S::IDX; ++j) {
       seen[j] = __ballot_sync(0xffffffffu, idx[j] != 0xffffffffu);
       idx[j] = index_of(p2[j]);
       p2[j] = p1[j];
       page_at(p2[j]);
-      p1[j] = place(v + 3 * S::U, j);
+      p1[j] = place(v + 3 * step, j);
     }
     // ---- S^T, a key a row (g, g + 8 of every 16), the heads 2t and 2t + 1 of every 8
     float x[MT][NT][4];
@@ -496,16 +498,20 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
   __syncthreads();
 }
 
-// The sum of a CTA's four pieces at one float4 of a row, normalised, and the row's LSE;
-// `lanes` neighbouring lanes with four pieces each share it. Piece w has its m, l and O's
+// The sum of a CTA's n <= 4 pieces at one float4 of a row, normalised, and the row's LSE;
+// `lanes` neighbouring lanes with n pieces each share it. Piece w has its m, l and O's
 // reference at stat(w, 0..2) and its O at value(w).
 template <int FMT, typename A, typename B>
-POD_DEV float4 join(int lanes, float up, float v_scale, float& lse, A stat, B value) {
+POD_DEV float4 join(int n, int lanes, float up, float v_scale, float& lse, A stat, B value) {
   float m[kDecodeWarps], mo[kDecodeWarps], l[kDecodeWarps];
   float4 p[kDecodeWarps];
   float top = -INFINITY, topv = -INFINITY;
 #pragma unroll
   for (int w = 0; w < kDecodeWarps; ++w) {
+    m[w] = mo[w] = -INFINITY;
+    l[w] = 0.f;
+    p[w] = make_float4(0, 0, 0, 0);
+    if (w >= n) continue;
     m[w] = stat(w, 0);
     l[w] = stat(w, 1);
     mo[w] = stat(w, 2);
@@ -566,10 +572,11 @@ __global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
 
   asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int parts = kDecodeWarps / P.hw, unit = S::TK * parts;      // warps of a KV head, keys of a unit
 
   // ---- this CTA's run of units
   long long total = 0;                             // units of a plane
-  for (int r = tid; r < P.batch; r += kDecodeThreads) total += (keys_of(P, r).count + S::U - 1) / S::U;
+  for (int r = tid; r < P.batch; r += kDecodeThreads) total += (keys_of(P, r).count + unit - 1) / unit;
 #pragma unroll
   for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   if (lane == 0) sh_scan[warp] = total;
@@ -589,7 +596,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
   int row = 0;
   for (int base = 0;; base += kDecodeThreads) {
     const int r = base + tid;
-    const long long n = r < P.batch ? (keys_of(P, r).count + S::U - 1) / S::U : 0;
+    const long long n = r < P.batch ? (keys_of(P, r).count + unit - 1) / unit : 0;
     long long x = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -619,30 +626,35 @@ __global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
   // ---- segments: the units of one (plane, request)
   while (u < u_end) {
     const Keys K = keys_of(P, row);
-    const int units = (K.count + S::U - 1) / S::U;
+    const int units = (K.count + unit - 1) / unit;
     if (units == 0) {                              // (an empty request: the merge kernel's)
       if (++row == P.batch) { row = 0; row_first = 0; ++plane; }
       continue;
     }
     const long long seg0 = (long long)plane * total + row_first;      // of the whole request
     const int ua = (int)(u - seg0), ub = (int)min((long long)units, u_end - seg0);
-    const int hk = plane % P.Hk, h0 = hk * P.G + plane / P.Hk * HT;
-    const int heads = min(HT, P.G - plane / P.Hk * HT);
+    const int groups = P.Hk / P.hw, hk0 = plane % groups * P.hw, tile0 = plane / groups * HT;
+    const int heads = min(HT, P.G - tile0);        // of every KV head
     if (tid == 0 && plane == 0 && ua == 0) P.first[row] = row_first;
-    attend<T, D, FMT, NT>(P, K, row, hk, h0, heads, ua * S::U, (int)min((long long)K.count, (long long)ub * S::U), sh);
+    {
+      const int hk = hk0 + warp % P.hw;
+      attend<T, D, FMT, NT>(P, K, row, hk, hk * P.G + tile0, heads, ua * unit + warp / P.hw * S::TK, unit,
+                            (int)min((long long)K.count, (long long)ub * unit), sh);
+    }
     const bool whole = ua == 0 && ub == units;
     const int slot = (int)blockIdx.x * 2 + (u == u_start ? 0 : 1);
-    for (int i = tid; i < heads * (D / 4); i += kDecodeThreads) {
-      const int h = i / (D / 4), c4 = i - h * (D / 4);
+    for (int i = tid; i < P.hw * heads * (D / 4); i += kDecodeThreads) {
+      const int c4 = i % (D / 4), k = i / (D / 4) / heads, h = i / (D / 4) - k * heads;   // of KV head hk0 + k
       float lse;
-      const float4 o = join<FMT>(1, weight_up<T, FMT>(), P.v_scale, lse,
-                                 [&](int w, int what) { return sh.m[what][w][h]; },
-                                 [&](int w) { return *reinterpret_cast<const float4*>(&sh.o[w][h][4 * c4]); });
+      const float4 o = join<FMT>(parts, 1, weight_up<T, FMT>(), P.v_scale, lse,
+                                 [&](int w, int what) { return sh.m[what][k + w * P.hw][h]; },
+                                 [&](int w) { return *reinterpret_cast<const float4*>(&sh.o[k + w * P.hw][h][4 * c4]); });
       if (whole) {
-        store_out<T>(P, row, h0 + h, D, c4, o, lse);
+        store_out<T>(P, row, (hk0 + k) * P.G + tile0 + h, D, c4, o, lse);
       } else {
-        *reinterpret_cast<float4*>(P.piece_o + ((long long)slot * HT + h) * D + 4 * c4) = o;
-        if (c4 == 0) P.piece_lse[slot * HT + h] = lse;
+        const long long piece = ((long long)slot * P.hw + k) * HT + h;
+        *reinterpret_cast<float4*>(P.piece_o + piece * D + 4 * c4) = o;
+        if (c4 == 0) P.piece_lse[piece] = lse;
       }
     }
     __syncthreads();                               // (the buffers are the next segment's)
@@ -664,12 +676,13 @@ __global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
   const int tid = threadIdx.x, rank = CL > 1 ? (int)(blockIdx.x % CL) : 0;
   const int item = (int)(blockIdx.x / CL), plane = item / P.batch, row = item - plane * P.batch;
   const Keys K = keys_of(P, row);
-  const int units = (K.count + S::U - 1) / S::U;
+  constexpr int U = S::TK * kDecodeWarps;          // keys of a unit
+  const int units = (K.count + U - 1) / U;
   const int hk = plane % P.Hk, h0 = hk * P.G + plane / P.Hk * HT;
   const int heads = min(HT, P.G - plane / P.Hk * HT);
   if (plane == 0 && rank == 0 && tid == 0 && P.status && P.lens[row] != K.len) atomicOr(P.status, kStatusSlot);
-  const int v0 = units * rank / CL * S::U, v1 = min(K.count, units * (rank + 1) / CL * S::U);
-  attend<T, D, FMT, NT>(P, K, row, hk, h0, heads, v0, v1, sh);
+  const int v0 = units * rank / CL * U, v1 = min(K.count, units * (rank + 1) / CL * U);
+  attend<T, D, FMT, NT>(P, K, row, hk, h0, heads, v0 + (tid >> 5) * S::TK, U, v1, sh);
   if (CL > 1)
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   // CL neighbouring threads join one float4, each the four pieces of a CTA
@@ -681,7 +694,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
     const int i = i0 + tid / CL, j = min(i, heads * (D / 4) - 1), h = j / (D / 4), c4 = j - h * (D / 4);
     float lse;
     const float4 o = join<FMT>(
-        CL, weight_up<T, FMT>(), P.v_scale, lse,
+        kDecodeWarps, CL, weight_up<T, FMT>(), P.v_scale, lse,
         [&](int w, int what) {
           float x;
           const uint32_t a = base + (uint32_t)offsetof_m<D, HT>(what, w, h);
@@ -703,7 +716,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
 
 // Rows whose keys were cut: the pieces in the order of the keys, weighted by
 // 2^(lse - M). Rows without keys: 0 and -inf. WPR warps work on a (request, head).
-template <typename T, int D, int HT, int UNIT, int WPR>
+template <typename T, int D, int HT, int TK, int WPR>
 __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant__ DecodeParams P) {
   constexpr int PL = D / 32 < 4 ? D / 32 : 4, NP = D / (32 * PL);      // elements and chunks of a lane
   __shared__ float sh[WPR > 1 ? WPR : 1][D];
@@ -714,7 +727,7 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
   if (item >= (long long)P.batch * P.H) return;    // (uniform over the block where its warps meet)
   const int row = (int)(item / P.H), head = (int)(item - (long long)row * P.H);
   const Keys K = keys_of(P, row);
-  const int units = (K.count + UNIT - 1) / UNIT;
+  const int unit = TK * (kDecodeWarps / P.hw), units = (K.count + unit - 1) / unit;
   T* out = static_cast<T*>(P.out) + (long long)row * P.out_stride + (long long)head * D;
   if (head == 0 && (threadIdx.x & (WPR * 32 - 1)) == 0 && P.status && P.lens[row] != K.len) atomicOr(P.status, kStatusSlot);
   if (units == 0) {
@@ -727,8 +740,8 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
     if (lane == 0 && P.lse) P.lse[item] = -INFINITY;
     return;
   }
-  const int hk = head / P.G, gh = head - hk * P.G, h = gh % HT;
-  const long long plane = (long long)(gh / HT) * P.Hk + hk, total = *P.total, all = total * P.planes;
+  const int hk = head / P.G, gh = head - hk * P.G, h = hk % P.hw * HT + gh % HT, per = P.hw * HT;
+  const long long plane = (long long)(gh / HT) * (P.Hk / P.hw) + hk / P.hw, total = *P.total, all = total * P.planes;
   const long long runs = min((long long)P.grid, all);
   const long long g0 = plane * total + P.first[row], g1 = g0 + units;
   const int c0 = (int)(((g0 + 1) * runs - 1) / all), c1 = (int)((g1 * runs - 1) / all);   // CTAs of the first and last unit
@@ -742,13 +755,13 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
     for (int e = 0; e < PL; ++e) acc[j][e] = 0.f;
   // the largest LSE first (its loads all at once), then the weighted sum
   auto slot_of = [&](int c) { return c > c0 || all * c / runs == g0 ? 2 * c : 2 * c + 1; };
-  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, P.piece_lse[(long long)slot_of(c) * HT + h]);
+  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, P.piece_lse[(long long)slot_of(c) * per + h]);
 #pragma unroll
   for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   const float z = top == -INFINITY ? 0.f : top;
 #pragma unroll 4
   for (int c = c0 + w0; c <= c1; c += WPR) {
-    const long long s = (long long)slot_of(c) * HT + h;
+    const long long s = (long long)slot_of(c) * per + h;
     const float f = ex2(P.piece_lse[s] - z);
     sum += f;
     const float* src = P.piece_o + s * D;
@@ -792,23 +805,30 @@ template <typename T, int D, int FMT, int NT>
 cudaError_t launch_decode_nt(DecodeParams& P, cudaStream_t st) {
   using S = DecodeShape<T, D, FMT, NT>;
   const int tiles = (P.G + S::HT - 1) / S::HT;
-  P.planes = P.Hk * tiles;
   constexpr int per_sm = (D == 256 || NT == 2) ? 2 : 3;
   P.grid = 152 * per_sm;
+  // A CTA's warps take four KV heads instead of four parts of one head's keys where a head's
+  // rows in a page of an NHD cache are few: neighbouring heads' rows are neighbours in memory.
+  // (96 block-scaled requests with pages of one slot 342 -> 283 us, per-tensor scales 304 ->
+  // 267; with pages of 16 slots nothing to 2 %; one long request, whose pieces get four times as
+  // many, 91 -> 111.)
+  P.hw = !P.hnd && P.ps < 8 && P.Hk % 4 == 0 && (long long)P.batch * P.Hk * tiles >= P.grid ? 4 : 1;
+  P.planes = P.Hk / P.hw * tiles;
   // Units of the longest row that the table (the list of pages, the window) allows.
   const long long items = (long long)P.batch * P.planes;
+  constexpr int U = S::TK * kDecodeWarps;
   const long long keys = P.pages ? (long long)min(P.num_selected, P.width) * P.ps
                                  : min((long long)P.width * P.ps, P.window < 0 ? LLONG_MAX : P.window + 1ll);
-  const long long units = (keys + S::U - 1) / S::U;
+  const long long units = (keys + U - 1) / U, clusters = (long long)P.batch * P.Hk * tiles;
   // Short rows whose clusters all fit the GPU at once.
-  if (items * 8 <= P.grid && units <= 8 * kShortUnits)
-    return launch_beside(decode_short_kernel<T, D, FMT, NT, 8>, (unsigned)items * 8, kDecodeThreads, 0, 8, st, P);
+  if (clusters * 8 <= P.grid && units <= 8 * kShortUnits)
+    return launch_beside(decode_short_kernel<T, D, FMT, NT, 8>, (unsigned)clusters * 8, kDecodeThreads, 0, 8, st, P);
   cudaError_t e = launch_beside(decode_kernel<T, D, FMT, NT>, (unsigned)P.grid, kDecodeThreads, 0, 1, st, P);
   if (e != cudaSuccess) return e;
   // a warp for each (request, head), or a block of four where a row may have many pieces
   const long long rows = (long long)P.batch * P.H;
-  if (rows <= 2048) return launch_beside(decode_merge_kernel<T, D, S::HT, S::U, 4>, (unsigned)rows, 128, 0, 1, st, P);
-  return launch_beside(decode_merge_kernel<T, D, S::HT, S::U, 1>, (unsigned)((rows + 3) / 4), 128, 0, 1, st, P);
+  if (items * 4 <= P.grid) return launch_beside(decode_merge_kernel<T, D, S::HT, S::TK, 4>, (unsigned)rows, 128, 0, 1, st, P);
+  return launch_beside(decode_merge_kernel<T, D, S::HT, S::TK, 1>, (unsigned)((rows + 3) / 4), 128, 0, 1, st, P);
 }
 
 template <typename T, int FMT>

@@ -28,13 +28,14 @@ struct DecodeParams {
   // workspace: total units of one plane, first unit of every request, the pieces
   long long* total;
   long long* first;
-  float* piece_o;                  // [grid * 2][heads of a tile][d], normalised
-  float* piece_lse;                // [grid * 2][heads of a tile], base 2
+  float* piece_o;                  // [grid * 2][hw][heads of a tile][d], normalised
+  float* piece_lse;                // [grid * 2][hw][heads of a tile], base 2
   long long q_stride, out_stride, table_stride;
   long long scale_bytes;           // of the pool's exponent bytes
   unsigned num_pages;
   int batch, H, Hk, G, width, ps, hnd, num_selected, window;
-  int planes;                      // Hk * head tiles
+  int hw;                          // KV heads of a CTA
+  int planes;                      // Hk / hw * head tiles
   int grid;                        // CTAs of the attention kernel
   float scale_log2;                // sm_scale * log2(e) (* k_scale)
   float v_scale;

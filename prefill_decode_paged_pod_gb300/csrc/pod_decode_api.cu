@@ -26,10 +26,13 @@ pod_status fail(pod_status code, const std::string& msg) {
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
-// the first units, and two pieces for each of the kernel's CTAs
-constexpr int kMostCtas = 152 * 3, kMostHeads = 16;
-size_t pieces_bytes(int d) { return round256((size_t)kMostCtas * 2 * kMostHeads * d * 4); }
-size_t lse_bytes() { return round256((size_t)kMostCtas * 2 * kMostHeads * 4); }
+// The first units of the requests, and for each CTA of the kernel (three an SM, or two that hold
+// 16 heads a tile or heads of 256) two pieces of up to four KV heads.
+constexpr int kMostCtas = 152 * 3;
+size_t piece_rows(int heads, int kv_heads, int d) {
+  const bool wide = d < 256 && heads / kv_heads > 8;
+  return (size_t)(wide || d == 256 ? 152 * 2 : kMostCtas) * 2 * 4 * (wide ? 16 : 8);
+}
 size_t first_bytes(int batch) { return round256(8 + (size_t)batch * 8); }
 
 }  // namespace
@@ -40,7 +43,8 @@ size_t pod_paged_decode_workspace_size(int32_t batch, int32_t num_qo_heads, int3
   if (batch < 0 || num_kv_heads < 1 || num_qo_heads < 1 || num_qo_heads % num_kv_heads ||
       (head_dim != 64 && head_dim != 128 && head_dim != 256))
     return 0;
-  return first_bytes(batch) + lse_bytes() + pieces_bytes(head_dim);
+  const size_t rows = piece_rows(num_qo_heads, num_kv_heads, head_dim);
+  return first_bytes(batch) + round256(rows * 4) + rows * head_dim * 4;
 }
 
 pod_status pod_paged_decode(const pod_decode_args* a, void* stream) {
@@ -82,7 +86,7 @@ pod_status pod_paged_decode(const pod_decode_args* a, void* stream) {
   P.first = P.total + 1;
   w += first_bytes(a->batch);
   P.piece_lse = reinterpret_cast<float*>(w);
-  w += lse_bytes();
+  w += round256(piece_rows(a->num_qo_heads, a->num_kv_heads, a->head_dim) * 4);
   P.piece_o = reinterpret_cast<float*>(w);
   P.q_stride = a->q_stride;
   P.out_stride = a->out_stride;
