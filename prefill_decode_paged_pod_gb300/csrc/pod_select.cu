@@ -30,7 +30,7 @@ using namespace pod;
 
 namespace {
 
-constexpr int kBoundThreads = 256, kBoundRows = 64;
+constexpr int kBoundThreads = 256, kBoundRows = 256;
 constexpr int kScoreThreads = 128, kLeastPages = 16;   // pages of a warp at least
 constexpr int kBinBits = 10, kBins = 1 << kBinBits, kNear = 256;
 constexpr int kHeldPages = 1024 * 8;                   // pages whose keys a block holds
@@ -181,12 +181,23 @@ __global__ void __launch_bounds__(kBoundThreads, 4) bounds_kernel(const __grid_c
       lo[e] = Pair<M>::kInf;
       hi[e] = Pair<M>::kInf | 0x80008000u;
     }
-    // the exponents of the page's keys: those of 32 at a time, and their extremes
+    // the exponents of the page's keys, of 32 at a time, and the first keys' loads beside them
     int eb = 0, top = 0, low = 255;
+    if (FMT == POD_KV_E4M3_BLOCK && lane < valid) eb = scales[(long long)lane * step];
+    uint4 x[U];
+    const uint8_t* at = keys + sub * row_bytes;          // of this lane's next key
+    auto load = [&](int k0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (k0 + u * KPL + sub < valid) x[u] = __ldcs(reinterpret_cast<const uint4*>(at));
+        at += KPL * row_bytes;
+      }
+    };
+    load(0);
     if constexpr (FMT == POD_KV_E4M3_BLOCK) {
-      for (int k = lane; k < valid; k += 32) {
+      if (lane < valid) top = low = eb;
+      for (int k = 32 + lane; k < valid; k += 32) {
         const int e = scales[(long long)k * step];
-        if (k < 32) eb = e;
         top = max(top, e);
         low = min(low, e);
       }
@@ -198,11 +209,7 @@ __global__ void __launch_bounds__(kBoundThreads, 4) bounds_kernel(const __grid_c
       }
     }
     for (int k0 = 0; k0 < valid; k0 += KPL * U) {
-      uint4 x[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (k0 + u * KPL + sub < valid)
-          x[u] = __ldcs(reinterpret_cast<const uint4*>(keys + (long long)(k0 + u * KPL + sub) * row_bytes));
+      if (k0) load(k0);
       if (FMT == POD_KV_E4M3_BLOCK && k0 && k0 % 32 == 0) eb = k0 + lane < valid ? scales[(long long)(k0 + lane) * step] : 0;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -1025,7 +1032,7 @@ pod_status pod_page_bounds(const pod_decode_args* a, void* stream) {
   P.hnd = a->kv_layout;
   P.k_scale = a->k_scale;
   // few rows a block where there are few, so that every SM gets some
-  const int64_t span = (a->rows + 152 * 8 - 1) / (152 * 8);
+  const int64_t span = (a->rows + 152 * 4 - 1) / (152 * 4);
   P.span = (int)(span < kBoundRows ? span : kBoundRows);
   cudaStream_t s = (cudaStream_t)stream;
   const cudaError_t e = a->dtype == POD_BF16 ? launch_bounds_d<__nv_bfloat16>(P, a->head_dim, a->kv_format, s)
