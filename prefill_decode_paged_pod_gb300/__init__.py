@@ -927,6 +927,16 @@ _STEP_ARGS = struct.Struct("@15Qq6i")
 _DECODE_ARGS = struct.Struct("@13Q5qQ13i3f")
 
 
+def _code_of(dtype) -> int:
+    """pod_dtype of a torch dtype (a lookup: these calls take as long as their host side)."""
+    torch = _torch_module
+    if dtype is torch.bfloat16:
+        return 1
+    if dtype is torch.float16:
+        return 0
+    raise PodError(2, f"unsupported dtype {dtype}")
+
+
 class PodStep(NamedTuple):
     """The arrays of a step (CUDA tensors), as pod_step_tables writes them."""
     kv_lens: object          # [batch] int32, keys after the step
@@ -941,9 +951,10 @@ class PodStep(NamedTuple):
 
 def _table(t, rows, dev):
     """(pointer, width, row stride) of an int32 block table [rows, width]."""
-    if t.dtype != _torch_module.int32 or t.dim() != 2 or t.get_device() != dev or t.shape[0] != rows:
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or t.dtype is not _torch_module.int32 or t.get_device() != dev:
         raise PodError(1, f"block_table must be an int32 tensor [{rows}, pages] on cuda:{dev}")
-    width, (sr, sc) = t.shape[1], t.stride()
+    width, (sr, sc) = shape[1], t.stride()
     if (sc != 1 and width > 1) or (rows > 1 and sr < width):
         raise PodError(1, "the entries of a block table row must be contiguous, its rows apart")
     return t.data_ptr(), width, sr if rows > 1 else max(sr, width)
@@ -1027,7 +1038,7 @@ def pod_page_bounds(kv_cache, bounds, slots, *, kv_scales=None, k_scale=1.0, kv_
     lib = _lib or load_library()
     torch = _torch()
     dev, dtype = _device_of(kv_cache), bounds.dtype
-    code = _dtype_code(dtype)
+    code = _code_of(dtype)
     cache, scales, pages, ps, hk, d, hnd, fmt = _cache_args(kv_cache, kv_scales, kv_layout, dtype, dev)
     bp = _whole("bounds", bounds, (pages, hk, 2, d), dtype, dev)
     rows = slots.numel()
@@ -1042,9 +1053,9 @@ def _scratch(workspace, need, like, dev, stream):
     """(tensor, pointer, bytes) of a call's workspace: the caller's, or a new one."""
     if workspace is None:
         workspace = _empty((max(need, 256),), _torch_module.uint8, like, stream)
-    elif workspace.get_device() != dev:
-        raise PodError(1, f"the workspace must be on cuda:{dev}")
-    return (workspace,) + _workspace(workspace)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise PodError(1, f"the workspace must be a contiguous tensor on cuda:{dev}")
+    return workspace, workspace.data_ptr(), workspace.nbytes
 
 
 def pod_select_pages_workspace_size(batch: int, num_kv_heads: int, table_width: int) -> int:
@@ -1063,7 +1074,7 @@ def pod_select_pages(q, bounds, block_table, kv_lens, num_selected: int, page_si
     lib = _lib or load_library()
     torch = _torch()
     dev, dtype = _device_of(q), q.dtype
-    code = _dtype_code(dtype)
+    code = _code_of(dtype)
     batch, H, d, qs = _heads("q", q, dtype, dev)
     if bounds.dim() != 4 or bounds.shape[3] != d:
         raise PodError(1, f"bounds must be [pages, kv heads, 2, {d}]")
@@ -1105,7 +1116,7 @@ def pod_paged_decode(q, kv_cache, block_table, kv_lens, *, pages=None, sm_scale=
     lib = _lib or load_library()
     torch = _torch()
     dev, dtype = _device_of(q), q.dtype
-    code = _dtype_code(dtype)
+    code = _code_of(dtype)
     batch, H, d, qs = _heads("q", q, dtype, dev)
     cache, scales, n, ps, hk, dk, hnd, fmt = _cache_args(kv_cache, kv_scales, kv_layout, dtype, dev)
     if dk != d:
