@@ -991,23 +991,15 @@ def pod_step_tables(block_table, kv_lens, new_lens, free_pages, free_count, page
     lo = _whole("kv_lens_out", kv_lens_out, (batch,), i32, dev)
     co = _whole("free_count_out", free_count_out, (1,), i32, dev)
     if out is None:
-        # one allocation, cut into the arrays (slots first: they are 64 bits wide)
-        sizes = (2 * rows, batch + 1, rows, rows, batch + 1, batch, pages) if pages else (2 * rows, batch + 1, rows, rows)
-        buf = _empty((sum(sizes),), i32, kv_lens, stream)
-        sl = buf.data_ptr()
-        qi = sl + 8 * rows
-        rq = qi + 4 * (batch + 1)
-        po = rq + 4 * rows
+        # (an allocation each: cutting one into views costs more)
+        new = lambda n, t=i32: _empty((n,), t, kv_lens, stream)    # noqa: E731
+        slots, q_indptr, requests, positions = new(rows, torch.int64), new(batch + 1), new(rows), new(rows)
+        sl, qi, rq, po = slots.data_ptr(), q_indptr.data_ptr(), requests.data_ptr(), positions.data_ptr()
+        indptr = last = indices = None
         ip = la = ix = 0
         if pages:
-            ip = po + 4 * rows
-            la = ip + 4 * (batch + 1)
-            ix = la + 4 * batch
-            slots, q_indptr, requests, positions, indptr, last, indices = buf.split_with_sizes(sizes)
-        else:
-            slots, q_indptr, requests, positions = buf.split_with_sizes(sizes)
-            indptr = last = indices = None
-        slots = slots.view(torch.int64)
+            indptr, last, indices = new(batch + 1), new(batch), new(pages)
+            ip, la, ix = indptr.data_ptr(), last.data_ptr(), indices.data_ptr()
     else:
         _, q_indptr, requests, positions, slots, indptr, indices, last = out
         qi = _whole("q_indptr", q_indptr, (batch + 1,), i32, dev)

@@ -299,7 +299,7 @@ extern "C" pod_status pod_step_tables(const pod_step_args* a, void* stream) {
       (a->batch && (!a->block_table || !a->kv_lens || !a->new_lens || !a->kv_lens_out)) ||
       (a->free_capacity && !a->free_pages) || (a->max_rows && (!a->requests || !a->positions || !a->slots)))
     return fail(POD_ERR_INVALID_ARG, "an array is NULL");
-  if (!a->kv_indptr != !a->last_page_len || (a->kv_indptr && a->max_pages && !a->kv_indices))
+  if ((a->batch && !a->kv_indptr != !a->last_page_len) || (a->kv_indptr && a->max_pages && !a->kv_indices))
     return fail(POD_ERR_INVALID_ARG, "kv_indptr, kv_indices and last_page_len come together");
   StepParams P = {};
   P.table = a->block_table;

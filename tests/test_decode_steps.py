@@ -321,6 +321,58 @@ def test_many_requests_and_many_heads():
 
 
 @gpu
+@pytest.mark.parametrize("H,hk,d,ps,fmt,dtype", [(16, 8, 128, 1, "16bit", "bf16"), (48, 4, 64, 3, "block", "fp16"),
+                                                 (8, 4, 256, 1, "scaled", "bf16"), (96, 8, 128, 2, "16bit", "fp16")])
+def test_small_pages_of_many_requests(H, hk, d, ps, fmt, dtype):
+    """Four KV heads a CTA: one warp a head, requests cut between CTAs and empty ones among them."""
+    dt, B = DT[dtype], 120
+    r = np.random.RandomState(4)
+    lens = [int(x) for x in r.choice([0, 1, 5, 63, 64, 65, 200], B)]
+    lens[7], lens[60] = 3000, 1111
+    tab, pages = table_of(lens, ps, 1, pad=9000 // ps)
+    kv, sc = make_cache(pages, ps, hk, d, "NHD", fmt, dt, 2)
+    q = torch.randn((B, H, d), generator=torch.Generator().manual_seed(3)).to(dt).cuda()
+    snk = torch.randn(H, generator=torch.Generator().manual_seed(8)).cuda()
+    out, lse = pod.pod_paged_decode(q, kv, torch.from_numpy(tab).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                    sinks=snk, **fmt_args(fmt, sc))
+    x = values64(kv, sc, "NHD", fmt)
+    at = [7, 60] + list(range(20, 50)) + [B - 1]
+    ref = [attend64(q[i].double().cpu().numpy(), x, dense_keys(tab[i], lens[i], ps, hk, -1), 1 / math.sqrt(d),
+                    snk.double().cpu().numpy()) for i in at]
+    check(out[at], lse[at], *(np.stack(y) for y in zip(*ref)), d, dt, fmt)
+
+
+@gpu
+def test_two_calls_at_once():
+    """Two streams, each with a workspace of its own (given, and made by the call)."""
+    ps, hk, H, d, dt = 16, 8, 32, 128, torch.bfloat16
+    lens = [3000 + 17 * i for i in range(24)]
+    tab, pages = table_of(lens, ps, 1)
+    kv, _ = make_cache(pages, ps, hk, d, "NHD", "16bit", dt, 4)
+    g = torch.Generator().manual_seed(3)
+    qs = [torch.randn((24, H, d), generator=g).to(dt).cuda() for _ in range(2)]
+    bounds = make_bounds(pages, hk, d, dt, 5)
+    t, ln = torch.from_numpy(tab).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+    def step(q, ws=None):
+        sel = pod.pod_select_pages(q, bounds, t, ln, 20, ps)
+        return (sel,) + pod.pod_paged_decode(q, kv, t, ln, workspace=ws) + pod.pod_paged_decode(q, kv, t, ln, pages=sel)
+
+    want = [step(q) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    ws = torch.empty(pod.pod_paged_decode_workspace_size(24, H, hk, d), dtype=torch.uint8, device="cuda")
+    got = []
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((i, step(qs[i], ws if i == 0 else None)))
+    torch.cuda.synchronize()
+    for i, out in got:
+        assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+
+
+@gpu
 def test_pool_past_4_gb():
     """Pages whose offsets pass 32 bits, in every call that reads them."""
     ps, hk, H, d, dt = 16, 8, 8, 128, torch.bfloat16
@@ -355,16 +407,13 @@ def select64(q, bounds, table, lens, ps, k, first, last):
     for r, length in enumerate(lens):
         n = -(-min(max(length, 0), table.shape[1] * ps) // ps)
         for h in range(hk):
-            score = np.zeros(n)
-            for p in range(n):
-                page = int(table[r, p])
-                if not 0 <= page < b.shape[0]:
-                    score[p] = -np.inf
-                    continue
-                x = q[r, h * G:(h + 1) * G]
-                with np.errstate(invalid="ignore"):
-                    up, down = np.where(x < 0, 0, x).sum(0), np.where(x > 0, 0, x).sum(0)
-                    score[p] = (b[page, h, 0] * down + b[page, h, 1] * up).sum()
+            pages = table[r, :n].astype(np.int64)
+            known = (pages >= 0) & (pages < b.shape[0])
+            x = q[r, h * G:(h + 1) * G]
+            with np.errstate(invalid="ignore"):
+                up, down = np.where(x < 0, 0, x).sum(0), np.where(x > 0, 0, x).sum(0)
+                at = b[np.where(known, pages, 0), h]
+                score = np.where(known, (at[:, 0] * down + at[:, 1] * up).sum(-1), -np.inf)
             rank = np.where(np.isnan(score), np.inf, score)
             must = set(range(min(first, n))) | set(range(max(0, n - last), n))
             rest = [i for i in np.lexsort((np.arange(n), ~np.isnan(score), -rank)).tolist() if i not in must]
@@ -397,6 +446,23 @@ def test_select(H, hk, d, ps, dtype, lens, k, first, last):
                                torch.tensor(lens, dtype=torch.int32, device="cuda"), k, ps, keep_first=first,
                                keep_last=last)
     assert torch.equal(got.cpu(), select64(wide[:, 1:], bounds, tab, lens, ps, k, first, last))
+
+
+@gpu
+@pytest.mark.parametrize("width,dtype", [(90, "bf16"), (2100, "fp16"), (4200, "bf16")])
+def test_select_of_many_rows(width, dtype):
+    """More choices than SMs, rows of every length, pages that requests share (so many
+    scores of a row are equal)."""
+    dt, B, hk, d, k = DT[dtype], 160, 2, 64, 40
+    r = np.random.RandomState(width)
+    tab = r.randint(0, 300, (B, width)).astype(np.int32)
+    tab[::2] = r.permutation(300)[:min(width, 300)][np.arange(width) % min(width, 300)]
+    lens = r.randint(0, width * 4 + 1, B).tolist()
+    bounds = make_bounds(300, hk, d, dt, 4)
+    q = torch.randn((B, 8, d), generator=torch.Generator().manual_seed(5)).to(dt).cuda()
+    got = pod.pod_select_pages(q, bounds, torch.from_numpy(tab).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                               k, 4, keep_first=2, keep_last=3)
+    assert torch.equal(got.cpu(), select64(q, bounds, tab, lens, 4, k, 2, 3))
 
 
 @gpu
