@@ -33,7 +33,8 @@ namespace {
 constexpr int kBoundThreads = 256, kBoundRows = 256;
 constexpr int kScoreThreads = 128, kLeastPages = 16;   // pages of a warp at least
 constexpr int kBinBits = 10, kBins = 1 << kBinBits, kNear = 256;
-constexpr int kHeldPages = 1024 * 8;                   // pages whose keys a block holds
+constexpr int kPickThreads = 512;                      // at most
+constexpr int kHeldPages = kPickThreads * 16;          // pages whose keys a block holds
 
 template <typename T>
 struct Pair;
@@ -580,27 +581,29 @@ POD_DEV uint64_t kth_largest(F each, uint64_t from, int need, int& above, PickSh
 // A warp's share of a page's bounds, and with it the page's score in 64 bits.
 template <typename T, int D>
 struct PageBounds {
-  float lo[D / 32], hi[D / 32];
+  T lo[D / 32], hi[D / 32];                            // (converted where they are used, not where they are asked for)
   bool there;
   POD_DEV void load(const PickParams& P, int row, int hk, int i) {
     const unsigned page = (unsigned)P.table[row * P.table_stride + i];
-    const int lane = threadIdx.x & 31;
     there = page < P.num_pages;
     if (!there) return;
-    const T* m = static_cast<const T*>(P.bounds) + ((long long)page * P.Hk + hk) * 2 * D + lane;
+    const T* m = static_cast<const T*>(P.bounds) + ((long long)page * P.Hk + hk) * 2 * D + (threadIdx.x & 31);
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {
-      lo[j] = (float)m[j * 32];
-      hi[j] = (float)m[D + j * 32];
+      lo[j] = m[j * 32];
+      hi[j] = m[D + j * 32];
     }
   }
   POD_DEV double score(const double (*weight)[D]) const {
     if (!there) return -INFINITY;
     const int lane = threadIdx.x & 31;
-    double s = 0.;
+    double s = 0., t = 0.;
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j)
-      s += (double)lo[j] * weight[0][j * 32 + lane] + (double)hi[j] * weight[1][j * 32 + lane];
+    for (int j = 0; j < D / 32; ++j) {
+      s = fma((double)(float)lo[j], weight[0][j * 32 + lane], s);
+      t = fma((double)(float)hi[j], weight[1][j * 32 + lane], t);
+    }
+    s += t;
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s;
@@ -737,7 +740,7 @@ POD_DEV uint32_t kth_score(F each, uint32_t lo, uint32_t hi, int need, PickShare
 // work besides the keys, and the waits at barriers, grow with the warps (512 choices of
 // some 1300 pages: 19 us by eight warps each, PICK_US by four).
 template <typename T, int D, int HELD>
-__global__ void __launch_bounds__(HELD == 16 ? 256 : 1024) pick_kernel(const __grid_constant__ PickParams P) {
+__global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constant__ PickParams P) {
   __shared__ PickShared S;
   asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
@@ -765,6 +768,7 @@ __global__ void __launch_bounds__(HELD == 16 ? 256 : 1024) pick_kernel(const __g
     return key_of(x);
   };
   uint32_t held[HELD ? HELD : 1];
+  const float first_off = P.off[item * P.chunks + min(tid, (n + P.per - 1) / P.per - 1)];
   if constexpr (HELD > 0) {
     float x[HELD];                                     // (all loads before the first use)
 #pragma unroll
@@ -772,10 +776,12 @@ __global__ void __launch_bounds__(HELD == 16 ? 256 : 1024) pick_kernel(const __g
 #pragma unroll
     for (int j = 0; j < HELD; ++j) held[j] = key_at(i0 + j * 32 + lane, x[j]);
   }
-  for (int i = tid; i < (n + P.per - 1) / P.per; i += threads) {
-    const float e = P.off[item * P.chunks + i];
+  const int offs = (n + P.per - 1) / P.per;
+  float e = first_off;
+  for (int i = tid; i < offs;) {
     odd |= !(e < 0x1p100f);
     off = fmaxf(off, e);
+    if ((i += threads) < offs) e = P.off[item * P.chunks + i];
   }
   auto each = [&](auto f) {                            // (the lanes of a warp together)
     if constexpr (HELD > 0) {
@@ -939,14 +945,14 @@ cudaError_t launch_pick(const PickParams& P, cudaStream_t st) {
     const cudaError_t e = launch_beside(score_kernel<T, D>, (unsigned)blocks, kScoreThreads, kScoreShared, 1, st, P);
     if (e != cudaSuccess) return e;
   }
-  // threads that hold the longest row's keys
+  // threads that hold the longest row's keys: few warps a choice where there are many choices
   const unsigned grid = (unsigned)items;
-  if (items >= 2 * 152 && P.width <= 256 * 16)
-    return launch_beside(pick_kernel<T, D, 16>, grid, P.width <= 128 * 16 ? 128 : 256, 0, 1, st, P);
-  unsigned threads = 256;
-  while (threads < 1024 && (int)threads * 8 < P.width) threads *= 2;
-  return P.width <= kHeldPages ? launch_beside(pick_kernel<T, D, 8>, grid, threads, 0, 1, st, P)
-                               : launch_beside(pick_kernel<T, D, 0>, grid, 1024, 0, 1, st, P);
+  if (P.width > kHeldPages) return launch_beside(pick_kernel<T, D, 0>, grid, kPickThreads, 0, 1, st, P);
+  const bool many = items >= 2 * 152 && P.width <= 256 * 16;
+  if (many || P.width > kPickThreads * 8)
+    return launch_beside(pick_kernel<T, D, 16>, grid, P.width <= 128 * 16 ? 128 : P.width <= 256 * 16 ? 256 : kPickThreads, 0,
+                         1, st, P);
+  return launch_beside(pick_kernel<T, D, 8>, grid, P.width <= 256 * 8 ? 256 : kPickThreads, 0, 1, st, P);
 }
 template <typename T>
 cudaError_t launch_pick_d(const PickParams& P, int d, cudaStream_t st) {
