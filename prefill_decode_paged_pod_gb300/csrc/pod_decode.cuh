@@ -171,7 +171,7 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
     Place p = {-1, -1};
     v += j * 32 + lane;
     if ((TK >= 32 || lane < TK) && v < v1) {
-      const int w = v + K.first, at = w / P.ps;
+      const int w = v + K.first, at = P.ps_shift >= 0 ? w >> P.ps_shift : w / P.ps;
       p.in = w - at * P.ps;
       p.page = sel ? sel[at] : at;
     }

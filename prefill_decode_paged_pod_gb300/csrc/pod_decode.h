@@ -33,7 +33,7 @@ struct DecodeParams {
   long long q_stride, out_stride, table_stride;
   long long scale_bytes;           // of the pool's exponent bytes
   unsigned num_pages;
-  int batch, H, Hk, G, width, ps, hnd, num_selected, window;
+  int batch, H, Hk, G, width, ps, ps_shift, hnd, num_selected, window;   // ps_shift: -1 where ps is no power of two
   int hw;                          // KV heads of a CTA
   int planes;                      // Hk / hw * head tiles
   int grid;                        // CTAs of the attention kernel

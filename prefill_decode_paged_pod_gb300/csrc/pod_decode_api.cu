@@ -99,6 +99,7 @@ pod_status pod_paged_decode(const pod_decode_args* a, void* stream) {
   P.G = a->num_qo_heads / a->num_kv_heads;
   P.width = a->table_width;
   P.ps = a->page_size;
+  P.ps_shift = (P.ps & (P.ps - 1)) == 0 ? __builtin_ctz((unsigned)P.ps) : -1;
   P.hnd = a->kv_layout;
   P.num_selected = a->num_selected;
   P.window = a->window_left;
