@@ -720,7 +720,6 @@ template <typename T, int D, int HT, int TK, int WPR>
 __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant__ DecodeParams P) {
   constexpr int PL = D / 32 < 4 ? D / 32 : 4, NP = D / (32 * PL);      // elements and chunks of a lane
   __shared__ float sh[WPR > 1 ? WPR : 1][D];
-  __shared__ float sh_w[WPR > 1 ? WPR : 1][2];
   asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long item = WPR > 1 ? (long long)blockIdx.x : (long long)blockIdx.x * 4 + warp;
@@ -746,41 +745,59 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
   const long long g0 = plane * total + P.first[row], g1 = g0 + units;
   const int c0 = (int)(((g0 + 1) * runs - 1) / all), c1 = (int)((g1 * runs - 1) / all);   // CTAs of the first and last unit
   if (c0 == c1) return;                            // written whole
-  const int w0 = WPR > 1 ? warp : 0;
+  const int w0 = WPR > 1 ? warp : 0, n = c1 - c0 + 1;
+  // piece k of the row: the CTA's first segment, or its second where the row begins inside its run
+  const bool inside = all * c0 / runs != g0;
+  auto lse_of = [&](int k) { return P.piece_lse[((long long)2 * (c0 + k) + (k == 0 && inside)) * per + h]; };
+  // the largest LSE, then the weights, a lane a piece: their loads all at once
   float top = -INFINITY, sum = 0.f;
+  float mine = lane < n ? lse_of(lane) : -INFINITY;
+  for (int k = lane; k < n; k += 32) top = fmaxf(top, k == lane ? mine : lse_of(k));
+#pragma unroll
+  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const float z = top == -INFINITY ? 0.f : top;
   float acc[NP][PL];
 #pragma unroll
   for (int j = 0; j < NP; ++j)
 #pragma unroll
     for (int e = 0; e < PL; ++e) acc[j][e] = 0.f;
-  // the largest LSE first (its loads all at once), then the weighted sum
-  auto slot_of = [&](int c) { return c > c0 || all * c / runs == g0 ? 2 * c : 2 * c + 1; };
-  for (int c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, P.piece_lse[(long long)slot_of(c) * per + h]);
+  constexpr int U = WPR > 1 ? 8 : 4;               // pieces in flight
+  for (int k32 = 0; k32 < n; k32 += 32) {
+    if (k32) mine = k32 + lane < n ? lse_of(k32 + lane) : -INFINITY;
+    const float f = k32 + lane < n ? ex2(mine - z) : 0.f;
+    sum += f;                                      // (of all warps' pieces: every warp has them)
+    const int end = min(32, n - k32);
+    for (int k0 = w0; k0 < end; k0 += WPR * U) {
+      float x[U][NP][PL];
 #pragma unroll
-  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  const float z = top == -INFINITY ? 0.f : top;
-#pragma unroll 4
-  for (int c = c0 + w0; c <= c1; c += WPR) {
-    const long long s = (long long)slot_of(c) * per + h;
-    const float f = ex2(P.piece_lse[s] - z);
-    sum += f;
-    const float* src = P.piece_o + s * D;
+      for (int i = 0; i < U; ++i) {
+        const int k = k32 + min(k0 + i * WPR, end - 1);
+        const float* src = P.piece_o + (((long long)2 * (c0 + k) + (k == 0 && inside)) * per + h) * D + lane * PL;
 #pragma unroll
-    for (int j = 0; j < NP; ++j)
+        for (int j = 0; j < NP; ++j) {
+          if constexpr (PL == 4) *reinterpret_cast<float4*>(x[i][j]) = *reinterpret_cast<const float4*>(src + j * 128);
+          else *reinterpret_cast<float2*>(x[i][j]) = *reinterpret_cast<const float2*>(src);
+        }
+      }
 #pragma unroll
-      for (int e = 0; e < PL; ++e) acc[j][e] += src[(j * 32 + lane) * PL + e] * f;
+      for (int i = 0; i < U; ++i) {
+        const float w = __shfl_sync(0xffffffffu, f, min(k0 + i * WPR, 31));
+#pragma unroll
+        for (int j = 0; j < NP; ++j)
+#pragma unroll
+          for (int e = 0; e < PL; ++e) acc[j][e] += k0 + i * WPR < end ? x[i][j][e] * w : 0.f;
+      }
+    }
   }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   if constexpr (WPR > 1) {
 #pragma unroll
     for (int j = 0; j < NP; ++j)
 #pragma unroll
       for (int e = 0; e < PL; ++e) sh[warp][(j * 32 + lane) * PL + e] = acc[j][e];
-    if (lane == 0) sh_w[warp][0] = sum;
     __syncthreads();
     if (warp) return;
-    sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < WPR; ++w) sum += sh_w[w][0];
 #pragma unroll
     for (int j = 0; j < NP; ++j)
 #pragma unroll
