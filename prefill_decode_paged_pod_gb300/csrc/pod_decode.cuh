@@ -93,6 +93,11 @@ constexpr float weight_up() {
   return FMT == POD_KV_16BIT && Pack<T>::kBF16 ? -24.f : 7.f;
 }
 
+// a / b of numbers that are not negative: 32 bits where they do (a third of the instructions)
+POD_DEV long long quotient(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
+}
+
 // Keys of request r that the call reads, as indices v in [0, count): key first + v
 // of the cache, or slot v % ps of the selected page v / ps.
 struct Keys {
@@ -587,9 +592,9 @@ __global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
   if (blockIdx.x == 0 && tid == 0) *P.total = total;
   const long long all = total * P.planes, runs = min((long long)P.grid, all);
   if (blockIdx.x >= runs) return;                  // (as many runs as units at most: none is empty)
-  long long u = all * blockIdx.x / runs;
-  const long long u_end = all * (blockIdx.x + 1) / runs, u_start = u;
-  int plane = (int)(u / total);
+  long long u = quotient(all * blockIdx.x, runs);
+  const long long u_end = quotient(all * (blockIdx.x + 1), runs), u_start = u;
+  int plane = (int)quotient(u, total);
   // the request of the first unit
   long long at = u - (long long)plane * total;     // unit within the plane
   long long before = 0;                            // units of the requests up to here
@@ -724,7 +729,7 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long item = WPR > 1 ? (long long)blockIdx.x : (long long)blockIdx.x * 4 + warp;
   if (item >= (long long)P.batch * P.H) return;    // (uniform over the block where its warps meet)
-  const int row = (int)(item / P.H), head = (int)(item - (long long)row * P.H);
+  const int row = (int)quotient(item, P.H), head = (int)(item - (long long)row * P.H);
   const Keys K = keys_of(P, row);
   const int unit = TK * (kDecodeWarps / P.hw), units = (K.count + unit - 1) / unit;
   T* out = static_cast<T*>(P.out) + (long long)row * P.out_stride + (long long)head * D;
@@ -743,11 +748,11 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
   const long long plane = (long long)(gh / HT) * (P.Hk / P.hw) + hk / P.hw, total = *P.total, all = total * P.planes;
   const long long runs = min((long long)P.grid, all);
   const long long g0 = plane * total + P.first[row], g1 = g0 + units;
-  const int c0 = (int)(((g0 + 1) * runs - 1) / all), c1 = (int)((g1 * runs - 1) / all);   // CTAs of the first and last unit
+  const int c0 = (int)quotient((g0 + 1) * runs - 1, all), c1 = (int)quotient(g1 * runs - 1, all);   // CTAs of the first and last unit
   if (c0 == c1) return;                            // written whole
   const int w0 = WPR > 1 ? warp : 0, n = c1 - c0 + 1;
   // piece k of the row: the CTA's first segment, or its second where the row begins inside its run
-  const bool inside = all * c0 / runs != g0;
+  const bool inside = quotient(all * c0, runs) != g0;
   auto lse_of = [&](int k) { return P.piece_lse[((long long)2 * (c0 + k) + (k == 0 && inside)) * per + h]; };
   // the largest LSE, then the weights, a lane a piece: their loads all at once
   float top = -INFINITY, sum = 0.f;
