@@ -37,7 +37,7 @@
 namespace pod {
 namespace {
 
-constexpr int kShortUnits = 4;                     // units of a CTA of the kernel for short rows
+constexpr int kShortUnits = 4, kMostClusters = 36; // of the kernel for short rows: units of a CTA
 constexpr float kLag = 8.f;                        // log2 of how far m may lie below the maximum
 
 template <typename T, int D, int FMT, int NT>
@@ -842,8 +842,11 @@ cudaError_t launch_decode_nt(DecodeParams& P, cudaStream_t st) {
   const long long keys = P.pages ? (long long)min(P.num_selected, P.width) * P.ps
                                  : min((long long)P.width * P.ps, P.window < 0 ? LLONG_MAX : P.window + 1ll);
   const long long units = (keys + U - 1) / U, clusters = (long long)P.batch * P.Hk * tiles;
-  // Short rows whose clusters all fit the GPU at once.
-  if (clusters * 8 <= P.grid && units <= 8 * kShortUnits)
+  // Few clusters of short rows. (Every cluster costs some 0.15 us of the launch: with 32 of
+  // them and 256 / 1024 / 2048 keys a row, bf16, 9.2 / 12.0 / 15.0 us against 9.8 / 13.4 / 18.9
+  // split over the GPU; with 56 of them 13.5 / 19.9 / 25.8 against 11.5 / 17.3 / 22.2. With 8, of
+  // rows of 2048 / 4096 keys, 8.3 / 15.1 against 10.9 / 14.4.)
+  if (clusters <= kMostClusters && units <= 8 * kShortUnits)
     return launch_beside(decode_short_kernel<T, D, FMT, NT, 8>, (unsigned)clusters * 8, kDecodeThreads, 0, 8, st, P);
   cudaError_t e = launch_beside(decode_kernel<T, D, FMT, NT>, (unsigned)P.grid, kDecodeThreads, 0, 1, st, P);
   if (e != cudaSuccess) return e;
