@@ -146,6 +146,8 @@ DECODES = [
     (8, 1, 64, 3, "block", "NHD", "fp16", [300, 2], 128, False),
     (9, 1, 64, 16, "block", "HND", "bf16", [700, 70], -1, False),
     (7, 1, 256, 32, "block", "NHD", "fp16", [100, 1], -1, True),
+    (130, 2, 64, 16, "16bit", "NHD", "bf16", [70, 200, 1], -1, True),        # 65 heads a KV head
+    (66, 1, 256, 16, "scaled", "HND", "fp16", [50], 20, True),
 ]
 
 
@@ -577,6 +579,27 @@ def test_bounds(hk, d, ps, fmt, layout, dtype, runs):
 
 
 @gpu
+@pytest.mark.parametrize("hk,d,ps,layout,dtype", [(2, 128, 16, "NHD", "bf16"), (1, 64, 40, "HND", "fp16"),
+                                                  (3, 256, 70, "NHD", "bf16"), (1, 128, 5, "HND", "fp16")])
+def test_bounds_of_scales_far_apart(hk, d, ps, layout, dtype):
+    """Exponents of a page within 15 binades, at 16, and over the whole range; results past fp16's."""
+    dt, pages = DT[dtype], 5
+    kv, sc = make_cache(pages, ps, hk, d, layout, "block", dt, 2)
+    g = torch.Generator().manual_seed(7)
+    half = sc[:, 0]
+    for p, (lo, hi) in enumerate([(110, 126), (110, 127), (0, 255), (0, 16), (120, 160)]):
+        half[p] = torch.randint(lo, hi, half[p].shape, generator=g, dtype=torch.int64).to(torch.uint8).cuda()
+        half[p].view(-1)[0], half[p].view(-1)[-1] = lo, hi - 1
+    slots = torch.arange(pages * ps, device="cuda")
+    bounds = torch.zeros((pages, hk, 2, d), dtype=dt, device="cuda")
+    pod.pod_page_bounds(kv, bounds, slots, kv_scales=sc, kv_layout=layout)
+    x = kv.cpu().float() * torch.exp2(sc.cpu().double() - 127).float()[..., None]
+    x = (x if layout == "NHD" else x.transpose(2, 3))[:, 0]
+    want = torch.stack([outward(x[p].amin(0), x[p].amax(0), dt) for p in range(pages)])
+    assert torch.equal(bounds.cpu(), want)
+
+
+@gpu
 def test_bounds_of_odd_values():
     """Infinities end at the largest number, NaN does not count, fp16 bounds of small codes."""
     kv = torch.zeros((1, 2, 4, 1, 64), dtype=torch.float16, device="cuda")
@@ -939,7 +962,7 @@ def test_refusals_of_the_c_calls():
                             dict(kv_indptr=256), dict(kv_indptr=256, last=256, max_pages=3), dict(batch=-1), dict(ps=0),
                             dict(width=0), dict(width=1 << 27), dict(stride=7), dict(max_rows=-1), dict(max_pages=-1),
                             dict(capacity=-1)],
-        "pod_page_bounds": [dict(cache=0), dict(cache=8), dict(bounds=0), dict(bounds=8), dict(slots=0), dict(rows=-1),
+        "pod_page_bounds": [dict(cache=0), dict(cache=8), dict(cache=272), dict(bounds=0), dict(bounds=8), dict(slots=0), dict(rows=-1),
                             dict(rows=1 << 31), dict(d=96), dict(dtype=2), dict(fmt=3), dict(fmt=2), dict(scales=256),
                             dict(layout=2), dict(Hk=0), dict(ps=0), dict(num_pages=0), dict(num_pages=1 << 40),
                             dict(fmt=1, k_scale=0.0), dict(fmt=1, k_scale=math.inf)],
