@@ -19,6 +19,10 @@
  * pod_plan_set_prefill_mask and pod_plan_set_graph_capacity (then
  * pod_replan plans each new step into the same workspace).
  *
+ * Beside these, operators around the paged cache (norm, rotation, writes,
+ * reads), attention of drafted token trees, and decode steps whose lengths and
+ * tables live on the device; their sections say what they take.
+ *
  * Conventions shared by every entry point
  *  - Errors are returned as pod_status codes; nothing aborts or throws.
  *    pod_last_error() returns a thread-local message for the last failure.

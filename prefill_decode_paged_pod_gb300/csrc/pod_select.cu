@@ -128,7 +128,7 @@ __device__ __noinline__ void bounds_of_far_scales(const BoundParams& P, const ui
 // under block scales relative to the largest exponent of the page's keys: exact down to 15
 // binades below it (pages whose exponents lie further apart take a slow way). Half the
 // instructions of the same in fp32, which bound it: 38000 pages and heads of block-scaled codes
-// 45 -> BOUNDS_US us.
+// 45 -> 21.7 us.
 template <typename T, int D, int FMT>
 __global__ void __launch_bounds__(kBoundThreads, 4) bounds_kernel(const __grid_constant__ BoundParams P) {
   constexpr int E = FMT == POD_KV_16BIT ? 2 : 1, LPR = D * E / 16, KPL = 32 / LPR, U = 4;
@@ -295,7 +295,8 @@ POD_DEV int pages_of(const PickParams& P, int row) {
 // two sets ahead of the one that is summed (asynchronous copies: no registers, and no
 // other lane to wait for); the eight sums cross the lanes together (nine shuffles).
 // Bound by memory. With the sets held in registers instead: 67 us (one set, 24 warps
-// an SM) and 91 us (two sets, 16 warps) where the ring takes RING_US.
+// an SM) and 91 us (two sets, 16 warps) where the ring takes 56 (655000
+// pages and heads of 128, 333 MB).
 constexpr int kRing = 3;
 constexpr int kScoreShared = kScoreThreads / 32 * kRing * 8 * 32 * 16;
 static_assert(kScoreShared <= 48 * 1024, "what a launch may ask for without an attribute of the kernel");
@@ -736,9 +737,8 @@ POD_DEV uint32_t kth_score(F each, uint32_t lo, uint32_t hi, int need, PickShare
 
 // A block makes one choice. HELD > 0: a lane's keys stay in registers (0: they are read in every
 // pass, for more pages than a block can hold). A run of pages is a warp's, so that the chosen
-// ones come out in order. Many choices take blocks of few warps with 16 keys a lane: the
-// work besides the keys, and the waits at barriers, grow with the warps (512 choices of
-// some 1300 pages: 19 us by eight warps each, PICK_US by four).
+// ones come out in order. Bound by latency: two trips to memory and seven barriers, some 4 us; a
+// block with close calls takes 4 more, and among hundreds of blocks some have them.
 template <typename T, int D, int HELD>
 __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constant__ PickParams P) {
   __shared__ PickShared S;
@@ -945,14 +945,13 @@ cudaError_t launch_pick(const PickParams& P, cudaStream_t st) {
     const cudaError_t e = launch_beside(score_kernel<T, D>, (unsigned)blocks, kScoreThreads, kScoreShared, 1, st, P);
     if (e != cudaSuccess) return e;
   }
-  // threads that hold the longest row's keys: few warps a choice where there are many choices
+  // Threads that hold the longest row's keys, eight a lane, or sixteen. (Sixteen a lane and half the
+  // threads for shorter rows too: 512 choices of some 1300 pages the same, 256 of them 7 us more.)
   const unsigned grid = (unsigned)items;
-  if (P.width > kHeldPages) return launch_beside(pick_kernel<T, D, 0>, grid, kPickThreads, 0, 1, st, P);
-  const bool many = items >= 2 * 152 && P.width <= 256 * 16;
-  if (many || P.width > kPickThreads * 8)
-    return launch_beside(pick_kernel<T, D, 16>, grid, P.width <= 128 * 16 ? 128 : P.width <= 256 * 16 ? 256 : kPickThreads, 0,
-                         1, st, P);
-  return launch_beside(pick_kernel<T, D, 8>, grid, P.width <= 256 * 8 ? 256 : kPickThreads, 0, 1, st, P);
+  if (P.width <= 256 * 8) return launch_beside(pick_kernel<T, D, 8>, grid, 256, 0, 1, st, P);
+  if (P.width <= kPickThreads * 8) return launch_beside(pick_kernel<T, D, 8>, grid, kPickThreads, 0, 1, st, P);
+  if (P.width <= kHeldPages) return launch_beside(pick_kernel<T, D, 16>, grid, kPickThreads, 0, 1, st, P);
+  return launch_beside(pick_kernel<T, D, 0>, grid, kPickThreads, 0, 1, st, P);
 }
 template <typename T>
 cudaError_t launch_pick_d(const PickParams& P, int d, cudaStream_t st) {
@@ -1085,8 +1084,9 @@ pod_status pod_select_pages(const pod_decode_args* a, void* stream) {
   P.Hk = a->num_kv_heads;
   P.G = a->num_qo_heads / a->num_kv_heads;
   P.width = a->table_width;
-  // pages of a warp: few where the SMs would not all be busy otherwise, more where that
-  // makes the weights less often
+  // Pages of a warp: few where the SMs would not all be busy otherwise, more where that makes
+  // the weights less often (16 / 64 a warp: 2 rows of 8 heads and some 250 pages 9.2 / 11.3 us, 64
+  // rows of 1300 pages 93 / 69).
   const int64_t pages = (int64_t)a->batch * a->num_kv_heads * a->table_width;
   P.per = pages <= 152 * 16 * 32 ? kLeastPages : 64;
   P.chunks = (a->table_width + P.per - 1) / P.per;

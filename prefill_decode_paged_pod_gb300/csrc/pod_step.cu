@@ -12,7 +12,10 @@
 // the step may have many rows, or the page table is asked for, a second kernel
 // of many blocks writes them (a thread an entry, which finds its request by bisection
 // of the offsets); otherwise the first block does it too and the launch is spared.
-// Bound by latency: a chain of some ten trips to L2 and as many block barriers.
+// Bound by latency: a chain of some ten trips to L2 and as many block barriers. Measured on
+// a GB300, in graphs: 64 requests of one token 3.6 us; 768 requests, prompts and tokens
+// given back among them (some 14000 pages moved, 80000 rows, 400000 page-table entries) 23 us,
+// of which the one block's bisections and moves take 15.
 #include <cuda_runtime.h>
 #include <limits.h>
 
@@ -324,10 +327,11 @@ extern "C" pod_status pod_step_tables(const pod_step_args* a, void* stream) {
   P.capacity = a->free_capacity;
   P.max_rows = a->max_rows;
   P.max_pages = a->max_pages;
-  // few rows: the first block writes them, a few each thread
-  P.rows_here = !a->kv_indptr && a->max_rows <= 2 * kStepThreads;
   cudaStream_t st = (cudaStream_t)stream;
   const int threads = a->batch <= 128 ? 128 : a->batch >= kStepThreads ? kStepThreads : (a->batch + 31) / 32 * 32;
+  // No more rows than threads: the first block writes them (64 requests of one token 3.2 us,
+  // by a second kernel 4.7; 1024 of them 6.2 and 7.5; 8 requests with 2048 rows 10.3 and 4.7).
+  P.rows_here = !a->kv_indptr && a->max_rows <= threads;
   cudaError_t e = launch_beside(step_kernel, 1, (unsigned)threads, 0, 1, st, P);
   const int64_t entries = (int64_t)a->max_rows + (a->kv_indptr ? a->max_pages : 0);
   if (e == cudaSuccess && !P.rows_here && entries) {

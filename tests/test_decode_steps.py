@@ -737,6 +737,27 @@ def test_step_tables_at_their_limits():
 
 
 @gpu
+def test_step_tables_into_kept_arrays():
+    """The arrays of an earlier step, with and without the page table; other memory stays."""
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")    # noqa: E731
+    table = torch.arange(24, dtype=torch.int32, device="cuda").view(4, 6) + 100
+    free, count = dev(list(range(60))), dev([50])
+    lens = dev([15, 0, 33, 96])
+    first = pod.pod_step_tables(table, lens, dev([1, 5, -3, 0]), free, count, 16, max_rows=9, max_pages=30)
+    kept = [x.clone() for x in first]
+    again = pod.pod_step_tables(table, lens, dev([2, 1, 1, -96]), free, count, 16, max_rows=9, max_pages=30, out=first)
+    assert all(a is b for a, b in zip(again, first)) and again.kv_lens is lens
+    assert again.kv_lens.tolist() == [18, 6, 31, 0] and again.q_indptr.tolist() == [0, 2, 3, 4, 4]
+    assert again.positions.tolist() == [16, 17, 5, 30, 0, 0, 0, 0, 0] and again.slots.tolist()[4:] == [-1] * 5
+    assert again.last_page_len.tolist() == [2, 6, 15, 0] and kept[1].tolist() == [0, 1, 6, 6, 6]
+    plain = pod.pod_step_tables(table, lens, dev([1, 1, 1, 1]), free, count, 16, max_rows=9, out=first)
+    assert plain.kv_indptr is None and plain.slots is first.slots and first.kv_indptr.tolist() == [0, 2, 3, 5, 5]
+    for bad in (first._replace(slots=first.slots[:8]), first._replace(requests=first.slots), first._replace(kv_indices=None)):
+        with pytest.raises(pod.PodError):
+            pod.pod_step_tables(table, lens, dev([1, 1, 1, 1]), free, count, 16, max_rows=9, max_pages=30, out=bad)
+
+
+@gpu
 def test_step_tables_of_nothing():
     empty = torch.empty(0, dtype=torch.int32, device="cuda")
     count = torch.tensor([2], dtype=torch.int32, device="cuda")
