@@ -287,7 +287,7 @@ struct PickParams {
 
 POD_DEV int pages_of(const PickParams& P, int row) {
   const int most = P.width * P.ps, len = P.lens[row];
-  return (min(max(len, 0), most) + P.ps - 1) / P.ps;
+  return (int)(((unsigned)min(max(len, 0), most) + P.ps - 1) / (unsigned)P.ps);
 }
 
 // A warp scores `per` pages for one head: a page's bounds are 4 D bytes, 16 a lane. Each
@@ -307,11 +307,9 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_co
   extern __shared__ uint4 ring[];
   asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
-  const long long task = (long long)blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);
-  const int hk = (int)(task % P.Hk);
-  const long long rest = task / P.Hk;
-  const int chunk = (int)(rest % P.chunks);
-  const int row = (int)(rest / P.chunks);
+  const unsigned task = blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5), rest = task / (unsigned)P.Hk;
+  const int hk = (int)(task - rest * P.Hk), row = (int)(rest / (unsigned)P.chunks);
+  const int chunk = (int)(rest - (unsigned)row * P.chunks);
   if (row >= P.batch) return;
   const int page0 = chunk * P.per;
   // (the table's entries and q do not wait for the length: one trip to memory)
@@ -745,7 +743,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(const __grid_constan
   asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
   const long long item = blockIdx.x;
-  const int row = (int)(item / P.Hk), hk = (int)(item - (long long)row * P.Hk);
+  const int row = (int)(blockIdx.x / (unsigned)P.Hk), hk = (int)(blockIdx.x - (unsigned)row * P.Hk);
   const int n = pages_of(P, row);
   if (hk == 0 && tid == 0 && P.status && (P.lens[row] < 0 || P.lens[row] > P.width * P.ps))
     atomicOr(P.status, kStatusSlot);
@@ -940,7 +938,7 @@ template <typename T, int D>
 cudaError_t launch_pick(const PickParams& P, cudaStream_t st) {
   const long long warps = (long long)P.batch * P.chunks * P.Hk, per = kScoreThreads / 32;
   const long long blocks = (warps + per - 1) / per, items = (long long)P.batch * P.Hk;
-  if (blocks > 0x7fffffff || items > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  if (warps > 0x7fffffff) return cudaErrorInvalidConfiguration;      // (counted in 32 bits)
   if (P.width > P.k) {                                 // (else every page is chosen)
     const cudaError_t e = launch_beside(score_kernel<T, D>, (unsigned)blocks, kScoreThreads, kScoreShared, 1, st, P);
     if (e != cudaSuccess) return e;
