@@ -582,23 +582,42 @@ __global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
   using S = DecodeShape<T, D, FMT, NT>;
   constexpr int HT = S::HT;
   __shared__ DecodeShared<D, HT> sh;
-  __shared__ long long sh_scan[kDecodeWarps + 2];
+  __shared__ long long sh_scan[kDecodeWarps], sh_rest[kDecodeWarps], sh_first;
   __shared__ int sh_row;
 
   asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int parts = kDecodeWarps / P.hw, unit = S::TK * parts;      // warps of a KV head, keys of a unit
 
-  // ---- this CTA's run of units
-  long long total = 0;                             // units of a plane
-  for (int r = tid; r < P.batch; r += kDecodeThreads) total += (keys_of(P, r).count + unit - 1) / unit;
+  // ---- this CTA's run of units. The first requests, a thread one, are scanned once; those
+  // behind them are summed, and scanned where the run begins among them.
+  auto units_of = [&](int r) { return r < P.batch ? (long long)((keys_of(P, r).count + unit - 1) / unit) : 0ll; };
+  auto scan = [&](long long n) {                   // the sum up to this thread's, within its warp
 #pragma unroll
-  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if (lane == 0) sh_scan[warp] = total;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, n, o);
+      if (lane >= o) n += y;
+    }
+    return n;
+  };
+  long long n = units_of(tid), x = scan(n), rest = 0;
+  for (int r = tid + kDecodeThreads; r < P.batch; r += kDecodeThreads) rest += units_of(r);
+  if (P.batch > kDecodeThreads)
+#pragma unroll
+    for (int o = 16; o; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+  if (lane == 31) {
+    sh_scan[warp] = x;
+    sh_rest[warp] = rest;
+  }
+  if (tid == 0) sh_row = -1;
   __syncthreads();
-  total = 0;
+  long long total = 0, head = 0;                   // units of a plane, and of the scanned requests
 #pragma unroll
-  for (int w = 0; w < kDecodeWarps; ++w) total += sh_scan[w];
+  for (int w = 0; w < kDecodeWarps; ++w) {
+    head += sh_scan[w];
+    total += sh_rest[w];
+  }
+  total += head;
   if (blockIdx.x == 0 && tid == 0) *P.total = total;
   const long long all = total * P.planes, runs = min((long long)P.grid, all);
   if (blockIdx.x >= runs) return;                  // (as many runs as units at most: none is empty)
@@ -606,37 +625,31 @@ __global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
   const long long u_end = quotient(all * (blockIdx.x + 1), runs), u_start = u;
   int plane = (int)quotient(u, total);
   // the request of the first unit
-  long long at = u - (long long)plane * total;     // unit within the plane
-  long long before = 0;                            // units of the requests up to here
-  int row = 0;
+  const long long at = u - (long long)plane * total;   // unit within the plane
+  long long before = 0;                            // units of the requests up to this round
   for (int base = 0;; base += kDecodeThreads) {
-    const int r = base + tid;
-    const long long n = r < P.batch ? (keys_of(P, r).count + unit - 1) / unit : 0;
-    long long x = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+    if (base) {
+      n = units_of(base + tid);
+      x = scan(n);
+      __syncthreads();                             // (sh_scan is read)
+      if (lane == 31) sh_scan[warp] = x;
+      __syncthreads();
     }
-    __syncthreads();                               // (sh_scan is read above, and by the round before)
-    if (lane == 31) sh_scan[warp] = x;
-    if (tid == 0) sh_row = -1;
-    __syncthreads();
     long long off = before;
 #pragma unroll
-    for (int w = 0; w < kDecodeWarps; ++w)
+    for (int w = 0; w < kDecodeWarps; ++w) {
       if (w < warp) off += sh_scan[w];
-    if (at >= off + x - n && at < off + x) {
-      sh_row = r;
-      sh_scan[kDecodeWarps] = off + x - n;
+      before += sh_scan[w];
     }
-#pragma unroll
-    for (int w = 0; w < kDecodeWarps; ++w) before += sh_scan[w];
+    if (at >= off + x - n && at < off + x) {
+      sh_row = base + tid;
+      sh_first = off + x - n;
+    }
     __syncthreads();
     if (sh_row >= 0 || base + kDecodeThreads >= P.batch) break;
   }
-  row = sh_row;
-  long long row_first = sh_scan[kDecodeWarps];     // first unit of the request in its plane
+  int row = sh_row;
+  long long row_first = sh_first;                  // first unit of the request in its plane
 
   // ---- segments: the units of one (plane, request)
   while (u < u_end) {
