@@ -753,6 +753,7 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
   const long long item = WPR > 1 ? (long long)blockIdx.x : (long long)blockIdx.x * 4 + warp;
   if (item >= (long long)P.batch * P.H) return;    // (uniform over the block where its warps meet)
   const int row = (int)quotient(item, P.H), head = (int)(item - (long long)row * P.H);
+  const long long total = *P.total, first = P.first[row];           // (beside the length; of no use for an empty row)
   const Keys K = keys_of(P, row);
   const int unit = TK * (kDecodeWarps / P.hw), units = (K.count + unit - 1) / unit;
   T* out = static_cast<T*>(P.out) + (long long)row * P.out_stride + (long long)head * D;
@@ -768,18 +769,34 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
     return;
   }
   const int hk = head / P.G, gh = head - hk * P.G, h = hk % P.hw * HT + gh % HT, per = P.hw * HT;
-  const long long plane = (long long)(gh / HT) * (P.Hk / P.hw) + hk / P.hw, total = *P.total, all = total * P.planes;
+  const long long plane = (long long)(gh / HT) * (P.Hk / P.hw) + hk / P.hw, all = total * P.planes;
   const long long runs = min((long long)P.grid, all);
-  const long long g0 = plane * total + P.first[row], g1 = g0 + units;
+  const long long g0 = plane * total + first, g1 = g0 + units;
   const int c0 = (int)quotient((g0 + 1) * runs - 1, all), c1 = (int)quotient(g1 * runs - 1, all);   // CTAs of the first and last unit
   if (c0 == c1) return;                            // written whole
   const int w0 = WPR > 1 ? warp : 0, n = c1 - c0 + 1;
   // piece k of the row: the CTA's first segment, or its second where the row begins inside its run
   const bool inside = quotient(all * c0, runs) != g0;
   auto lse_of = [&](int k) { return P.piece_lse[((long long)2 * (c0 + k) + (k == 0 && inside)) * per + h]; };
-  // the largest LSE, then the weights, a lane a piece: their loads all at once
+  // The largest LSE, then the weights, a lane a piece; the first pieces are asked for beside the
+  // LSEs.
+  constexpr int U = WPR > 1 ? 8 : 4;               // pieces in flight
+  float x[U][NP][PL];
+  auto load = [&](int k0, int end) {               // pieces k0, k0 + WPR, ... (the last one for those past the end)
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int k = min(k0 + i * WPR, end - 1);
+      const float* src = P.piece_o + (((long long)2 * (c0 + k) + (k == 0 && inside)) * per + h) * D + lane * PL;
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        if constexpr (PL == 4) *reinterpret_cast<float4*>(x[i][j]) = *reinterpret_cast<const float4*>(src + j * 128);
+        else *reinterpret_cast<float2*>(x[i][j]) = *reinterpret_cast<const float2*>(src);
+      }
+    }
+  };
   float top = -INFINITY, sum = 0.f;
   float mine = lane < n ? lse_of(lane) : -INFINITY;
+  load(w0, n);
   for (int k = lane; k < n; k += 32) top = fmaxf(top, k == lane ? mine : lse_of(k));
 #pragma unroll
   for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -789,24 +806,13 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
   for (int j = 0; j < NP; ++j)
 #pragma unroll
     for (int e = 0; e < PL; ++e) acc[j][e] = 0.f;
-  constexpr int U = WPR > 1 ? 8 : 4;               // pieces in flight
   for (int k32 = 0; k32 < n; k32 += 32) {
     if (k32) mine = k32 + lane < n ? lse_of(k32 + lane) : -INFINITY;
     const float f = k32 + lane < n ? ex2(mine - z) : 0.f;
     sum += f;                                      // (of all warps' pieces: every warp has them)
     const int end = min(32, n - k32);
     for (int k0 = w0; k0 < end; k0 += WPR * U) {
-      float x[U][NP][PL];
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int k = k32 + min(k0 + i * WPR, end - 1);
-        const float* src = P.piece_o + (((long long)2 * (c0 + k) + (k == 0 && inside)) * per + h) * D + lane * PL;
-#pragma unroll
-        for (int j = 0; j < NP; ++j) {
-          if constexpr (PL == 4) *reinterpret_cast<float4*>(x[i][j]) = *reinterpret_cast<const float4*>(src + j * 128);
-          else *reinterpret_cast<float2*>(x[i][j]) = *reinterpret_cast<const float2*>(src);
-        }
-      }
+      if (k32 + k0 != w0) load(k32 + k0, n);
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const float w = __shfl_sync(0xffffffffu, f, min(k0 + i * WPR, 31));
