@@ -47,7 +47,7 @@
 namespace pod {
 namespace {
 
-constexpr int kShortUnits = 4, kMostClusters = 36; // of the kernel for short rows: units of a CTA
+constexpr int kShortUnits = 8, kShortCtas = 256;    // of the kernel for short rows: units a CTA, CTAs in clusters
 constexpr float kLag = 8.f;                        // log2 of how far m may lie below the maximum
 
 template <typename T, int D, int FMT, int NT>
@@ -870,13 +870,23 @@ cudaError_t launch_decode_nt(DecodeParams& P, cudaStream_t st) {
   constexpr int U = S::TK * kDecodeWarps;
   const long long keys = P.pages ? (long long)min(P.num_selected, P.width) * P.ps
                                  : min((long long)P.width * P.ps, P.window < 0 ? LLONG_MAX : P.window + 1ll);
-  const long long units = (keys + U - 1) / U, clusters = (long long)P.batch * P.Hk * tiles;
-  // Few clusters of short rows. (Every cluster costs some 0.15 us of the launch: with 32 of
-  // them and 256 / 1024 / 2048 keys a row, bf16, 9.2 / 12.0 / 15.0 us against 9.8 / 13.4 / 18.9
-  // split over the GPU; with 56 of them 13.5 / 19.9 / 25.8 against 11.5 / 17.3 / 22.2. With 8, of
-  // rows of 2048 / 4096 keys, 8.3 / 15.1 against 10.9 / 14.4.)
-  if (clusters <= kMostClusters && units <= 8 * kShortUnits)
-    return launch_beside(decode_short_kernel<T, D, FMT, NT, 8>, (unsigned)clusters * 8, kDecodeThreads, 0, 8, st, P);
+  const long long units = (keys + U - 1) / U, pairs = (long long)P.batch * P.Hk * tiles;
+  // Short rows: one CTA, or a cluster of two, four or eight, for each (request, plane), while its
+  // CTAs get at most eight units each; half the cluster where they would get fewer than two. A
+  // cluster's launch costs time that grows with its size, so no more than kShortCtas CTAs come in
+  // clusters. (us with 1 / 2 / 4 / 8 CTAs and split over the GPU, bf16, 8 KV heads: 1 request of
+  // 256 keys 5.4 / 4.9 / 4.6 / 6.1 / 8.4, of 2048 keys 25.5 / 15.2 / 9.9 / 8.6 / 10.1; 4 of 512
+  // 8.7 / 6.9 / 7.1 / 9.2 / 10.8; 8 of 2048 39.7 / 25.3 / 18.7 / 27.3 / 23.3; 16 of 1024
+  // 24.1 / 18.0 / 24.0 / 32.8 / 23.0; 32 of 512 17.0 / 22.7 / 27.1 / 47.5 / 23.3; 128 of 64 to
+  // 512 31.9 / 41.9 / 71.1 / 169 / 42.0. 128 of 1024: 95.0 by one CTA each, 92.0 split.)
+  int cl = 1;
+  while (cl < 8 && pairs * cl * 2 <= kShortCtas) cl *= 2;
+  if (P.hw == 1 && pairs <= INT_MAX && units <= kShortUnits * cl) {
+    while (cl > 1 && units < 2 * cl) cl /= 2;
+    const auto kernel = cl == 1 ? decode_short_kernel<T, D, FMT, NT, 1> : cl == 2 ? decode_short_kernel<T, D, FMT, NT, 2>
+                      : cl == 4 ? decode_short_kernel<T, D, FMT, NT, 4> : decode_short_kernel<T, D, FMT, NT, 8>;
+    return launch_beside(kernel, (unsigned)(pairs * cl), kDecodeThreads, 0, (unsigned)cl, st, P);
+  }
   cudaError_t e = launch_beside(decode_kernel<T, D, FMT, NT>, (unsigned)P.grid, kDecodeThreads, 0, 1, st, P);
   if (e != cudaSuccess) return e;
   // A warp for each (request, head), or a block of four where a row may have many pieces (one

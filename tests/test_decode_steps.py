@@ -155,9 +155,9 @@ DECODES = [
 @pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("H,hk,d,ps,fmt,layout,dtype,lens,window,sinks", DECODES)
 def test_decode(H, hk, d, ps, fmt, layout, dtype, lens, window, sinks, wide):
-    """Short rows under a narrow table go to clusters, under a wide one to the split kernel."""
+    """Rows under a narrow table go to a CTA or a cluster each, under a wide one to the split kernel."""
     dt = DT[dtype]
-    tab, pages = table_of(lens, ps, 1, pad=9000 // ps if wide else 2)
+    tab, pages = table_of(lens, ps, 1, pad=33000 // ps if wide else 2)
     kv, sc = make_cache(pages, ps, hk, d, layout, fmt, dt, 2)
     # slots behind a request's keys hold NaN (the code 0x7f, or an exponent byte of 255)
     raw = kv.view(torch.uint8) if fmt != "16bit" else kv
@@ -189,6 +189,32 @@ def test_decode(H, hk, d, ps, fmt, layout, dtype, lens, window, sinks, wide):
 
 
 @gpu
+@pytest.mark.parametrize("hk", [1, 8])
+@pytest.mark.parametrize("batch", [1, 5, 9, 17, 40, 130])
+def test_decode_widths(batch, hk):
+    """One batch under tables of every width: one to eight CTAs a row, and the split kernel."""
+    dt, d, ps, H = torch.bfloat16, 128, 16, 4 * hk
+    r = np.random.RandomState(batch)
+    lens = [int(x) for x in r.randint(0, 400, batch)]
+    lens[0], lens[-1] = 0, 5
+    tab, pages = table_of(lens, ps, batch + 1)
+    kv, _ = make_cache(pages, ps, hk, d, "NHD", "16bit", dt, 3)
+    q = torch.from_numpy(r.standard_normal((batch, H, d))).to(dt).cuda()
+    x = values64(kv, None, "NHD", "16bit")
+    scale = 1 / math.sqrt(d)
+    ref = [attend64(q[i].double().cpu().numpy(), x, dense_keys(tab[i], n, ps, hk, -1), scale, None)
+           for i, n in enumerate(lens)]
+    ref = [np.stack(y) for y in zip(*ref)]
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for keys in (0, 500, 1000, 2000, 4000, 9000):
+        t = np.concatenate([tab, np.full((batch, keys // ps), -1, np.int32)], 1)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = pod.pod_paged_decode(q, kv, torch.from_numpy(t).cuda(), n, status=status)
+        check(out, lse, *ref, d, dt)
+        assert status.item() == 0
+
+
+@gpu
 @pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("ps,fmt,layout,dtype,d", [(16, "16bit", "NHD", "bf16", 128), (1, "scaled", "HND", "fp16", 128),
                                                    (3, "block", "NHD", "bf16", 64), (64, "16bit", "HND", "fp16", 256)])
@@ -196,7 +222,7 @@ def test_decode_of_listed_pages(ps, fmt, layout, dtype, d, wide):
     """Pages per KV head in any order, a page twice, entries that are skipped."""
     dt, hk, G = DT[dtype], 2, 4
     lens = [10 * ps, 7 * ps - min(2, ps - 1), ps, 0, 4 * ps]
-    more = 9000 // ps if wide else 0
+    more = 33000 // ps if wide else 0
     tab, pages = table_of(lens, ps, 5, pad=more)
     kv, sc = make_cache(pages, ps, hk, d, layout, fmt, dt, 6)
     sel = np.array([[[3, 1, 9, -1, 0], [2, 2, 8, 5, 10]],        # 10: past the request's pages
