@@ -248,12 +248,14 @@ def test_decode_of_listed_pages(ps, fmt, layout, dtype, d, wide):
 
 
 @gpu
-def test_bad_pages_and_lengths_are_masked_and_reported():
+@pytest.mark.parametrize("width", [5, 2200])
+def test_bad_pages_and_lengths_are_masked_and_reported(width):
     """A page outside the pool in front of a request's end, a negative length and
     one past the table: nothing outside is read."""
     ps, hk, H, d, dt = 16, 2, 4, 128, torch.bfloat16
-    lens = [80, -5, 1000, 33]
+    lens = [80, -5, width * ps + 920, 33]
     tab = np.array([[0, 7, 2, 3, 4], [1, 1, 1, 1, 1], [5, 6, 0, 1, 2], [3, -1, 1 << 30, 0, 0]], dtype=np.int32)
+    tab = np.concatenate([tab, np.random.RandomState(4).randint(-1, 8, (4, width - 5)).astype(np.int32)], 1)
     kv, _ = make_cache(7, ps, hk, d, "NHD", "16bit", dt, 1)
     q = torch.randn((4, H, d), generator=torch.Generator().manual_seed(2)).to(dt).cuda()
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -262,7 +264,7 @@ def test_bad_pages_and_lengths_are_masked_and_reported():
     x = values64(kv, None, "NHD", "16bit")
     ref = []
     for i, n in enumerate(lens):
-        t = np.arange(min(max(n, 0), 80))
+        t = np.arange(min(max(n, 0), width * ps))
         t = t[(tab[i][t // ps] >= 0) & (tab[i][t // ps] < 7)]
         ref.append(attend64(q[i].double().cpu().numpy(), x, [(tab[i][t // ps].astype(np.int64), t % ps)] * hk,
                             1 / math.sqrt(d), None))
@@ -271,11 +273,12 @@ def test_bad_pages_and_lengths_are_masked_and_reported():
 
 
 @gpu
+@pytest.mark.parametrize("pad", [0, 2100])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-def test_block_scales_far_apart(dtype):
+def test_block_scales_far_apart(dtype, pad):
     """K and V exponents over many binades; the largest V scale under a small weight."""
     dt, hk, H, d, ps, n = DT[dtype], 1, 4, 128, 16, 400
-    tab, pages = table_of([n], ps, 1)
+    tab, pages = table_of([n], ps, 1, pad=pad)
     kv, sc = make_cache(pages, ps, hk, d, "NHD", "block", dt, 4, 112, 121)
     g = torch.Generator().manual_seed(9)
     sc[:, 1] = torch.randint(100, 126, sc[:, 1].shape, generator=g, dtype=torch.uint8).cuda()
