@@ -123,16 +123,19 @@ __device__ __noinline__ void bounds_of_far_scales(const BoundParams& P, const ui
 
 // A block takes `span` rows of the write. A row whose page differs from that of the row
 // before owns the page; a warp finds how far its run of rows goes. Then a warp brings in
-// the keys of one (page, head) at a time, 16 bytes a lane, four loads in flight of 32 / LPR
-// keys each, and keeps the extremes packed, two 16-bit values a register. Codes go to fp16,
-// under block scales relative to the largest exponent of the page's keys: exact down to 15
-// binades below it (pages whose exponents lie further apart take a slow way). Half the
-// instructions of the same in fp32, which bound it: 38000 pages and heads of block-scaled codes
-// 45 -> 21.7 us.
+// the keys of one (page, head) at a time, eight channels a lane, 32 / LPR keys at once, the
+// loads of a page of 16 in flight together, and keeps the extremes packed, two 16-bit values a
+// register. Codes go to fp16, under block scales relative to the largest exponent of the page's
+// keys: exact down to 15 binades below it (pages whose exponents lie further apart take a slow
+// way). Bound by instructions, of which this is half those of the same in fp32: 38000 pages and
+// heads of block-scaled codes 45 -> 20.4 us. (Codes 16 a lane, with twice the extremes to join
+// across lanes: 21.7. The next page's keys asked for ahead, into registers of their own: 22.5;
+// 5 or 6 blocks an SM in 48 or 40 registers a thread: 22.8, 25.4.)
 template <typename T, int D, int FMT>
 __global__ void __launch_bounds__(kBoundThreads, 4) bounds_kernel(const __grid_constant__ BoundParams P) {
-  constexpr int E = FMT == POD_KV_16BIT ? 2 : 1, LPR = D * E / 16, KPL = 32 / LPR, U = 4;
-  constexpr int R = E == 2 ? 4 : 8, PARTS = 2 * R / 4;    // packed pairs of a lane's chunk; 16-byte outputs of it
+  // eight channels a lane: LPR lanes a key, KPL keys at a time, U of these in flight
+  constexpr int E = FMT == POD_KV_16BIT ? 2 : 1, LPR = D / 8, KPL = 32 / LPR, U = 8 / E, R = 4;
+  using Chunk = typename std::conditional<E == 2, uint4, uint2>::type;
   using M = typename std::conditional<FMT == POD_KV_16BIT, T, __half>::type;
   __shared__ long long page_of[kBoundRows];
   __shared__ int row_of[kBoundRows], keys_of[kBoundRows];
@@ -173,7 +176,7 @@ __global__ void __launch_bounds__(kBoundThreads, 4) bounds_kernel(const __grid_c
     const int o = i / P.Hk, h = i - o * P.Hk, valid = keys_of[o];
     const long long page = page_of[o];
     const long long row = page * 2 * P.Hk * P.ps + (P.hnd ? (long long)h * P.ps : h);   // of key 0, in rows of D
-    const uint8_t* keys = P.cache + row * (D * E) + part * 16;
+    const uint8_t* keys = P.cache + row * (D * E) + part * (8 * E);
     const uint8_t* scales = FMT == POD_KV_E4M3_BLOCK ? P.scales + row : nullptr;
     const int step = P.hnd ? 1 : P.Hk;
     uint32_t lo[R], hi[R];
@@ -185,12 +188,12 @@ __global__ void __launch_bounds__(kBoundThreads, 4) bounds_kernel(const __grid_c
     // the exponents of the page's keys, of 32 at a time, and the first keys' loads beside them
     int eb = 0, top = 0, low = 255;
     if (FMT == POD_KV_E4M3_BLOCK && lane < valid) eb = scales[(long long)lane * step];
-    uint4 x[U];
+    Chunk x[U];
     const uint8_t* at = keys + sub * row_bytes;          // of this lane's next key
     auto load = [&](int k0) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (k0 + u * KPL + sub < valid) x[u] = __ldcs(reinterpret_cast<const uint4*>(at));
+        if (k0 + u * KPL + sub < valid) x[u] = __ldcs(reinterpret_cast<const Chunk*>(at));
         at += KPL * row_bytes;
       }
     };
@@ -205,38 +208,41 @@ __global__ void __launch_bounds__(kBoundThreads, 4) bounds_kernel(const __grid_c
       top = __reduce_max_sync(0xffffffffu, top);
       low = __reduce_min_sync(0xffffffffu, low);
       if (top - low > 15) {
-        bounds_of_far_scales<T, D>(P, keys - part * 16, scales, row_bytes, step, valid, (page * P.Hk + h) * 2 * D);
+        bounds_of_far_scales<T, D>(P, keys - part * 8, scales, row_bytes, step, valid, (page * P.Hk + h) * 2 * D);
         continue;
       }
     }
+    // 2^(exponent - top), twice: fp16's exponent bias is 15, a normal number down to 2^-14
+    auto factor = [&]() { return eb - top < -14 ? 0x02000200u : (uint32_t)(eb - top + 15) * 0x04000400u; };
+    uint32_t mine = FMT == POD_KV_E4M3_BLOCK ? factor() : 0u;
     for (int k0 = 0; k0 < valid; k0 += KPL * U) {
       if (k0) load(k0);
-      if (FMT == POD_KV_E4M3_BLOCK && k0 && k0 % 32 == 0) eb = k0 + lane < valid ? scales[(long long)(k0 + lane) * step] : 0;
+      if (FMT == POD_KV_E4M3_BLOCK && k0 && k0 % 32 == 0) {
+        eb = k0 + lane < valid ? scales[(long long)(k0 + lane) * step] : top;
+        mine = factor();
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int k = k0 + u * KPL + sub;
-        uint32_t s = 0u;
-        if constexpr (FMT == POD_KV_E4M3_BLOCK) {
-          // 2^(exponent - top), twice: fp16's exponent bias is 15, a normal number down to 2^-14
-          const int f = __shfl_sync(0xffffffffu, eb, k & 31) - top;
-          s = f < -14 ? 0x02000200u : (uint32_t)(f + 15) * 0x04000400u;
-        }
+        const uint32_t s = FMT == POD_KV_E4M3_BLOCK ? __shfl_sync(0xffffffffu, mine, k & 31) : 0u;
         if (k >= valid) continue;
-        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        uint32_t w[R];
+        if constexpr (E == 2) {
+          w[0] = x[u].x; w[1] = x[u].y; w[2] = x[u].z; w[3] = x[u].w;
+        } else {
+          w[0] = e4m3x2_to<__half>((uint16_t)x[u].x);
+          w[1] = e4m3x2_to<__half>((uint16_t)(x[u].x >> 16));
+          w[2] = e4m3x2_to<__half>((uint16_t)x[u].y);
+          w[3] = e4m3x2_to<__half>((uint16_t)(x[u].y >> 16));
+        }
 #pragma unroll
         for (int e = 0; e < R; ++e) {
-          uint32_t a;
-          if constexpr (FMT == POD_KV_16BIT) {
-            a = w[e];
-          } else {
-            a = e4m3x2_to<__half>((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
-            if constexpr (FMT == POD_KV_E4M3_BLOCK) {
-              const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<const __half2*>(&s));
-              a = *reinterpret_cast<const uint32_t*>(&y);
-            }
+          if constexpr (FMT == POD_KV_E4M3_BLOCK) {
+            const __half2 y = __hmul2(*reinterpret_cast<__half2*>(&w[e]), *reinterpret_cast<const __half2*>(&s));
+            w[e] = *reinterpret_cast<const uint32_t*>(&y);
           }
-          lo[e] = min2<M>(lo[e], a);
-          hi[e] = max2<M>(hi[e], a);
+          lo[e] = min2<M>(lo[e], w[e]);
+          hi[e] = max2<M>(hi[e], w[e]);
         }
       }
     }
@@ -249,22 +255,19 @@ __global__ void __launch_bounds__(kBoundThreads, 4) bounds_kernel(const __grid_c
       }
     const float s = FMT == POD_KV_E4M3 ? P.k_scale
                     : FMT == POD_KV_E4M3_BLOCK ? (top ? __uint_as_float((uint32_t)top << 23) : 5.877471754111438e-39f) : 1.f;
-    // the lanes that hold the same chunk share its outputs: eight smallest values, the next
-    // eight, the largest ones
-    T* dst = static_cast<T*>(P.bounds) + (page * P.Hk + h) * 2 * D + part * (2 * R);
+    // the lanes that hold the same channels share their outputs: the smallest values, the largest
+    T* dst = static_cast<T*>(P.bounds) + (page * P.Hk + h) * 2 * D + part * 8;
 #pragma unroll
-    for (int o = 0; o < PARTS; o += KPL) {
-      const int mine = o + sub;
-      if (KPL > PARTS && mine >= PARTS) break;
-      const bool upper = mine >= PARTS / 2;
-      uint32_t w[4];
+    for (int o = 0; o < 2; o += KPL) {
+      const int side = o + sub;
+      if (KPL > 2 && side >= 2) break;
+      uint32_t w[R];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t a = upper ? hi[e] : lo[e], b = upper ? hi[R - 4 + e] : lo[R - 4 + e];
-        const float2 f = Pack<M>::unpack(PARTS == 4 && (mine & 1) ? b : a);
-        w[e] = outward2<T>(FMT == POD_KV_16BIT ? f.x : f.x * s, FMT == POD_KV_16BIT ? f.y : f.y * s, upper);
+      for (int e = 0; e < R; ++e) {
+        const float2 f = Pack<M>::unpack(side ? hi[e] : lo[e]);
+        w[e] = outward2<T>(FMT == POD_KV_16BIT ? f.x : f.x * s, FMT == POD_KV_16BIT ? f.y : f.y * s, side);
       }
-      *reinterpret_cast<uint4*>(dst + (upper ? D : 0) + (PARTS == 4 ? (mine & 1) * 8 : 0)) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(dst + side * D) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
