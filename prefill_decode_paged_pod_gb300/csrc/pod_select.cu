@@ -128,9 +128,10 @@ __device__ __noinline__ void bounds_of_far_scales(const BoundParams& P, const ui
 // register. Codes go to fp16, under block scales relative to the largest exponent of the page's
 // keys: exact down to 15 binades below it (pages whose exponents lie further apart take a slow
 // way). Bound by instructions, of which this is half those of the same in fp32: 38000 pages and
-// heads of block-scaled codes 45 -> 20.4 us. (Codes 16 a lane, with twice the extremes to join
-// across lanes: 21.7. The next page's keys asked for ahead, into registers of their own: 22.5;
-// 5 or 6 blocks an SM in 48 or 40 registers a thread: 22.8, 25.4.)
+// heads of block-scaled codes 45 -> 18.6 us. (Codes 16 a lane, with twice the extremes to join
+// across lanes: 1.3 us more; branches around the keys past the last, where NaN stands now, and a
+// division a page and head: 1.8. The next page's keys asked for ahead, into registers of their
+// own: 2 more; 5 or 6 blocks an SM in 48 or 40 registers a thread: 2.4, 5.)
 template <typename T, int D, int FMT>
 __global__ void __launch_bounds__(kBoundThreads, 4) bounds_kernel(const __grid_constant__ BoundParams P) {
   // eight channels a lane: LPR lanes a key, KPL keys at a time, U of these in flight
@@ -172,8 +173,17 @@ __global__ void __launch_bounds__(kBoundThreads, 4) bounds_kernel(const __grid_c
   __syncthreads();
   const int part = lane % LPR, sub = lane / LPR;
   const long long row_bytes = (long long)D * E * (P.hnd ? 1 : P.Hk);          // from a key to the next
-  for (int i = warp; i < n * P.Hk; i += kBoundThreads / 32) {
-    const int o = i / P.Hk, h = i - o * P.Hk, valid = keys_of[o];
+  // (page, head) pairs warp, warp + 8, ...: a division once
+  constexpr int W = kBoundThreads / 32;
+  const int o_step = W / P.Hk, h_step = W - o_step * P.Hk;
+  int o = warp / P.Hk, h = warp - o * P.Hk;
+  auto next = [&]() {
+    o += o_step;
+    h += h_step;
+    if (h >= P.Hk) { h -= P.Hk; ++o; }
+  };
+  for (; o < n; next()) {
+    const int valid = keys_of[o];
     const long long page = page_of[o];
     const long long row = page * 2 * P.Hk * P.ps + (P.hnd ? (long long)h * P.ps : h);   // of key 0, in rows of D
     const uint8_t* keys = P.cache + row * (D * E) + part * (8 * E);
@@ -188,11 +198,13 @@ __global__ void __launch_bounds__(kBoundThreads, 4) bounds_kernel(const __grid_c
     // the exponents of the page's keys, of 32 at a time, and the first keys' loads beside them
     int eb = 0, top = 0, low = 255;
     if (FMT == POD_KV_E4M3_BLOCK && lane < valid) eb = scales[(long long)lane * step];
-    Chunk x[U];
+    Chunk x[U], no_key;                                  // (NaN, which does not count)
+    memset(&no_key, E == 2 ? 0xff : 0x7f, sizeof no_key);
     const uint8_t* at = keys + sub * row_bytes;          // of this lane's next key
     auto load = [&](int k0) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
+        x[u] = no_key;
         if (k0 + u * KPL + sub < valid) x[u] = __ldcs(reinterpret_cast<const Chunk*>(at));
         at += KPL * row_bytes;
       }
@@ -223,9 +235,7 @@ __global__ void __launch_bounds__(kBoundThreads, 4) bounds_kernel(const __grid_c
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int k = k0 + u * KPL + sub;
-        const uint32_t s = FMT == POD_KV_E4M3_BLOCK ? __shfl_sync(0xffffffffu, mine, k & 31) : 0u;
-        if (k >= valid) continue;
+        const uint32_t s = FMT == POD_KV_E4M3_BLOCK ? __shfl_sync(0xffffffffu, mine, (k0 + u * KPL + sub) & 31) : 0u;
         uint32_t w[R];
         if constexpr (E == 2) {
           w[0] = x[u].x; w[1] = x[u].y; w[2] = x[u].z; w[3] = x[u].w;
