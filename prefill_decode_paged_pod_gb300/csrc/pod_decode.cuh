@@ -30,7 +30,7 @@
 // Bound by memory: twelve warps an SM with up to 8 KB of keys each on their way. Measured on a
 // GB300, in graphs, of the measured copy rate: 64 requests of 512 to 16384 keys, 32/8 heads of
 // 128, bf16: 330 us, 101 %; one request of 131072 keys, 64/8 heads: 88 us, 90 %; 96 requests of
-// 4096 to 12288 keys over block-scaled FP8: 258 to 266 us, 84 to 87 % (per-tensor scales 250 to
+// 4096 to 12288 keys over block-scaled FP8: 253 to 263 us, 85 to 88 % (per-tensor scales 250 to
 // 256; HND pages 249 and 238): the conversions and the softmax of twice as many keys a byte,
 // and rows of 128 bytes a kilobyte apart. 32-byte loads and page numbers two tiles
 // ahead made 332 of 352 and 260 of 307 us. K and V through a ring of asynchronous
@@ -353,11 +353,13 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
         }
       }
     }
-    uint32_t ek_now[S::IDX], ev_now[S::IDX];
+    float k_of[S::IDX], v_of[S::IDX];            // K's scale and V's exponent of the lane's own keys
+    if constexpr (FMT == POD_KV_E4M3_BLOCK) {
 #pragma unroll
-    for (int j = 0; j < S::IDX; ++j) {
-      ek_now[j] = ek[j];
-      ev_now[j] = ev[j];
+      for (int j = 0; j < S::IDX; ++j) {
+        k_of[j] = pow2_of((int)ek[j]);
+        v_of[j] = (float)((int)ev[j] - 127);
+      }
     }
     load_k();
     // ---- logits, the references, the weights
@@ -372,8 +374,8 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
         float ks = 1.f;
         xe[s][a] = 0.f;
         if constexpr (FMT == POD_KV_E4M3_BLOCK) {
-          ks = pow2_of((int)__shfl_sync(0xffffffffu, ek_now[s / 2], src));
-          xe[s][a] = (float)((int)__shfl_sync(0xffffffffu, ev_now[s / 2], src) - 127);
+          ks = __shfl_sync(0xffffffffu, k_of[s / 2], src);
+          xe[s][a] = __shfl_sync(0xffffffffu, v_of[s / 2], src);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
