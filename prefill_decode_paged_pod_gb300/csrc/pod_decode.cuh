@@ -27,14 +27,14 @@
 // run's pieces of a request that is cut go to the workspace; the merge kernel joins them in
 // the order of the keys.
 //
-// Bound by memory: twelve warps an SM with up to 8 KB of keys each on their way. Measured on a
-// GB300, in graphs, of the measured copy rate: 64 requests of 512 to 16384 keys, 32/8 heads of
-// 128, bf16: 330 us, 101 %; one request of 131072 keys, 64/8 heads: 88 us, 90 %; 96 requests of
-// 4096 to 12288 keys over block-scaled FP8: 253 to 263 us, 85 to 88 % (per-tensor scales 250 to
-// 256; HND pages 249 and 238): the conversions and the softmax of twice as many keys a byte,
-// and rows of 128 bytes a kilobyte apart. 32-byte loads and page numbers two tiles
-// ahead made 332 of 352 and 260 of 307 us. K and V through a ring of asynchronous
-// copies in shared memory took 430 and 310, K's codes as E4M3 operands (the legacy E4M3
+// Bound by memory: twelve warps an SM with up to 8 KB of keys each on their way, and the next
+// tile's rows asked for into L2. Measured on a GB300, in graphs, of the measured copy rate: 64
+// requests of 512 to 16384 keys, 32/8 heads of 128, bf16: 332 us, 101 %; one request of 131072
+// keys, 64/8 heads: 87 us, 91 %; 96 requests of 4096 to 12288 keys over block-scaled FP8: 242 to
+// 251 us, 89 to 93 % (per-tensor scales 246; HND pages 236 and 231): the conversions and the
+// softmax of twice as many keys a byte, and rows of 128 bytes a kilobyte apart. 32-byte loads
+// and page numbers two tiles ahead made 332 of 352 and 260 of 307 us. K and V through a ring of
+// asynchronous copies in shared memory took 430 and 310, K's codes as E4M3 operands (the legacy E4M3
 // mma) 295, the next segment's first tile asked for before the warps' sums join 331 and 270.
 #pragma once
 #include <limits.h>
@@ -321,6 +321,23 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
       p2[j] = p1[j];
       page_at(p2[j]);
       p1[j] = place(v + 3 * step, j);
+    }
+    // The next tile's rows set out for L2, a lane a key, before there are registers for them
+    // (block-scaled FP8 263 -> 250 us, 16 query heads a KV head over it 350 -> 308; 16-bit rows 336 ->
+    // 332 and 378 -> 360). Rows of 64 bytes would bring in their neighbours (158 -> 173), and pages of one
+    // or two slots ask for too many places at once (of one slot 262 -> 464, in HND 349 -> 535; of four
+    // 259 -> 250).
+    if (D * S::E >= 128 && P.ps >= 4) {
+#pragma unroll
+      for (int j = 0; j < S::IDX; ++j)
+        if (idx[j] != 0xffffffffu) {
+          const uint8_t* p = kbase + (long long)idx[j] * key_step;
+#pragma unroll
+          for (int c = 0; c < D * S::E; c += 128) {
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p + c));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p + v_off + c));
+          }
+        }
     }
     // ---- S^T, a key a row (g, g + 8 of every 16), the heads 2t and 2t + 1 of every 8
     float x[MT][NT][4];
@@ -900,8 +917,9 @@ cudaError_t launch_decode_nt(DecodeParams& P, cudaStream_t st) {
 
 template <typename T, int FMT>
 cudaError_t launch_decode(int d, DecodeParams& P, cudaStream_t st) {
-  // (16 query heads a KV head: 380 us for 64 ragged requests over bf16, 350 for 96 over
-  // block-scaled FP8; as two tiles of eight 457 and 456)
+  // (16 query heads a KV head: 360 us for 64 ragged requests over bf16, 301 for 96 over
+  // block-scaled FP8; as two tiles of eight 457 and 456 before rows were asked for ahead, when one
+  // tile took 380 and 350)
   const bool wide = P.G > 8;
   switch (d) {
     case 64: return wide ? launch_decode_nt<T, 64, FMT, 2>(P, st) : launch_decode_nt<T, 64, FMT, 1>(P, st);
