@@ -444,7 +444,8 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_co
     const bool writes = (lane & (O3 - 1)) == 0 && (U == 8 || !(lane & O1));
     if (writes && p < mine) score[p] = s1;
   }
-  // (pages outside the pool: few, and known by now)
+  // (pages outside the pool: few, and known by now; their sums, 0, are other lanes' stores)
+  __syncwarp();
   for (int p = lane; p < mine; p += 32)
     if ((unsigned)table[p] >= P.num_pages) score[p] = -INFINITY;
   float mag = 0.f;
