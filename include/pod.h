@@ -714,9 +714,12 @@ size_t pod_select_pages_workspace_size(int32_t batch, int32_t num_kv_heads, int3
  * lse: base 2, without the sink; a row without visible keys gives out = 0 and
  * lse = -inf, whatever its sink. Slots past a request's keys may hold anything.
  * Logits, sums and the output are fp32; the softmax weights are two 16-bit
- * parts (off by 2^-17 of a weight in bf16, 2^-22 in fp16); over FP8 caches
- * fp16 carries q (all bits but for 2^-38 of a row's largest magnitude), V and,
- * for bf16 results, the weights in one part (off by 2^-12 of each).
+ * parts (off by 2^-17 of a weight in bf16; in fp16 by 2^-22 of it, or by 2^-43
+ * of the row's largest weight where that is more); over FP8 caches fp16 carries
+ * q (all bits but for 2^-38 of a row's largest magnitude), V and, for bf16
+ * results, the weights in one part (off by 2^-11 of each, or by 2^-38 of the
+ * largest). Under block scales the largest is that of a weight times its V's
+ * scale.
  * workspace: pod_paged_decode_workspace_size bytes, 256-byte aligned, whose contents
  * need not survive between calls; calls that share it must not overlap.
  * Two calls with the same inputs give the same bits.

@@ -2,9 +2,9 @@
 // lengths, block table and (optionally) selected pages on the device.
 //
 // Mathematics. For the G query heads of a KV head: x = s q.k over the visible keys,
-// p = 2^(x - m), l = sum p, o = sum p v / l. m is a reference that is at most 2^8
-// below the running maximum: it moves, and O with it, only when a logit passes it by
-// more than 8 (one vote a tile instead of shuffles for the maximum; the lag is a factor
+// p = 2^(x - m), l = sum p, o = sum p v / l. m is a reference that may lag behind the
+// running maximum, by 8 or 2 at most: it moves, and O with it, only when a logit passes it by
+// more than that (one vote a tile instead of shuffles for the maximum; the lag is a factor
 // that l and O share). Pieces of a request's keys join by their base-2 LSE. Over a
 // block-scaled cache O has a reference of its own, that of p * 2^(V's exponent).
 //
@@ -18,7 +18,10 @@
 // matrix unit without shared memory in between. P^T changes from accumulator to operand by
 // movmatrix. P is carried in two 16-bit parts (off by 2^-17 of a weight in bf16, 2^-22 in
 // fp16): the matrix unit has time. Codes of FP8 caches are widened to fp16, exactly; bf16
-// results over them take P in one fp16 part.
+// results over them take P in one fp16 part. fp16 ends at 2^-24, so the second part is carried
+// times 2^11, in a sum of its own: weights down to 2^-21 of the largest keep all these bits, and
+// those below are off by 2^-43 of the largest (in one sum they were off by 2^-32 of it, which is
+// much where one key takes nearly all the weight and its V is small).
 //
 // Work split. The keys of every (KV head, request) are cut into units of one tile a
 // warp; the units of all, laid out head by head, are dealt to the CTAs of one
@@ -48,7 +51,6 @@ namespace pod {
 namespace {
 
 constexpr int kShortUnits = 8, kShortCtas = 256;    // of the kernel for short rows: units a CTA, CTAs in clusters
-constexpr float kLag = 8.f;                        // log2 of how far m may lie below the maximum
 
 template <typename T, int D, int FMT, int NT>
 struct DecodeShape {
@@ -62,8 +64,10 @@ struct DecodeShape {
   static constexpr int WV = D * E / 32 < 8 ? D * E / 32 : 8;      // of V
   static constexpr int CV = WV * 4 / E, NV = D / (8 * CV);
   static constexpr int IDX = (TK + 31) / 32;                      // tile keys of a lane
-  // 16-bit parts of a weight: two, but for fp16 weights of bf16 results, where one is off by
-  // 2^-12 of the weight, an eighth of the result's own rounding.
+  // 16-bit parts of a weight: two, but for fp16 weights of bf16 results, where one is off by at
+  // most 2^-11 of the weight, an eighth of what the result's own rounding may be off by. (Two
+  // there: 96 block-scaled requests 244 -> 248 us, with 16 query heads a KV head 307 -> 353, of
+  // head_dim 64 159 -> 168; per-tensor scales 238 -> 242.)
   static constexpr int PARTS = FMT != POD_KV_16BIT && Pack<T>::kBF16 ? 1 : 2;
 };
 
@@ -95,12 +99,39 @@ POD_DEV float pow2_of(int byte) {
   return byte == 0 ? 5.877471754111438e-39f : __uint_as_float((uint32_t)byte << 23);
 }
 
-// Weights leave the exponential times 2^this: fp16's small weights keep their bits
-// (2^(7 + kLag) is below its largest value), and sums of the largest bf16 values stay
-// below fp32's.
+// Weights leave the exponential times 2^weight_up, under a reference that is at most lag()
+// below the maximum. Sums of the largest bf16 values stay below fp32's. fp16 weights stay below
+// 2^15, and what is left below the largest counts: fp16's numbers end at 2^-24, so one part is off
+// by up to 2^-(25 + weight_up) of the largest weight. So a single part has little lag (8 and 2^7
+// left 2^-32 of the largest weight, 2^-38 now; 16 query heads a KV head over block scales 299 ->
+// 306 us, for the reference moves more often, the others nothing to 1 %); two parts reach 2^-43
+// with the larger one.
 template <typename T, int FMT>
 constexpr float weight_up() {
-  return FMT == POD_KV_16BIT && Pack<T>::kBF16 ? -24.f : 7.f;
+  return !Pack<T>::kBF16 ? 7.f : FMT == POD_KV_16BIT ? -24.f : 13.f;
+}
+template <typename T, int FMT>
+constexpr float lag() {
+  return Pack<T>::kBF16 && FMT != POD_KV_16BIT ? 2.f : 8.f;
+}
+
+// o += a * hi, + a * lo where PARTS is 2. fp16's lo comes times 2^11 and is summed by itself (in
+// o's own sum, without the factor: 16 query heads a KV head over block scales 331 us, 353 now;
+// head_dim 64 163 and 167; the others the same to 1 %).
+template <bool BF16, int PARTS>
+POD_DEV void mma_parts(float* o, const uint32_t* a, const uint32_t* hi, const uint32_t* lo) {
+  if constexpr (PARTS == 2 && !BF16) {
+    float x[4];
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(lo[0]), "r"(lo[1]), "f"(0.f));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = fmaf(x[i], 0x1p-11f, o[i]);
+  }
+  mma16816<BF16>(o, a, hi[0], hi[1]);
+  if constexpr (PARTS == 2 && BF16) mma16816<BF16>(o, a, lo[0], lo[1]);
 }
 
 // a / b of numbers that are not negative: 32 bits where they do (a third of the instructions)
@@ -151,7 +182,7 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
   using S = DecodeShape<T, D, FMT, NT>;
   using M = typename std::conditional<FMT == POD_KV_16BIT, T, __half>::type;   // operands of the products
   constexpr bool MBF = Pack<M>::kBF16;
-  constexpr float kUp = weight_up<T, FMT>();
+  constexpr float kUp = weight_up<T, FMT>(), kLag = lag<T, FMT>();
   constexpr int MT = S::MT, TK = S::TK;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   float o[NT][S::NV][S::CV / 2][4], m[NT][2], mv[NT][2], l[NT][2];
@@ -462,7 +493,13 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
           }
           if constexpr (S::PARTS == 2) {
             uint32_t hi, lo;
-            Pack<M>::split(p0, p1, hi, lo);
+            if constexpr (MBF) {
+              Pack<M>::split(p0, p1, hi, lo);
+            } else {
+              hi = Pack<M>::two(p0, p1);
+              const float2 h = Pack<M>::unpack(hi);
+              lo = Pack<M>::two((p0 - h.x) * 0x1p11f, (p1 - h.y) * 0x1p11f);
+            }
             ph[s][n][a] = turn8x8(hi);
             pl[s][n][a] = turn8x8(lo);
           } else {
@@ -482,10 +519,8 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
             const uint32_t a[4] = {prmt(v0w, v1w, 0x5410), prmt(v0w, v1w, 0x7632), prmt(v2w, v3w, 0x5410),
                                    prmt(v2w, v3w, 0x7632)};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma16816<MBF>(o[n][b][w], a, ph[s][n][0], ph[s][n][1]);
-              if constexpr (S::PARTS == 2) mma16816<MBF>(o[n][b][w], a, pl[s][n][0], pl[s][n][1]);
-            }
+            for (int n = 0; n < NT; ++n)
+              mma_parts<MBF, S::PARTS>(o[n][b][w], a, ph[s][n], pl[s][n]);
           } else {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -493,10 +528,8 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
               const uint32_t a[4] = {e4m3x2_to<__half>((uint16_t)lo), e4m3x2_to<__half>((uint16_t)(lo >> 16)),
                                      e4m3x2_to<__half>((uint16_t)hi), e4m3x2_to<__half>((uint16_t)(hi >> 16))};
 #pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                mma16816<MBF>(o[n][b][2 * w + q], a, ph[s][n][0], ph[s][n][1]);
-                if constexpr (S::PARTS == 2) mma16816<MBF>(o[n][b][2 * w + q], a, pl[s][n][0], pl[s][n][1]);
-              }
+              for (int n = 0; n < NT; ++n)
+                mma_parts<MBF, S::PARTS>(o[n][b][2 * w + q], a, ph[s][n], pl[s][n]);
             }
           }
         }

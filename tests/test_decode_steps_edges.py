@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import prefill_decode_paged_pod_gb300 as pod
-from test_decode_steps import built, select64, table_of    # noqa: F401
+from test_decode_steps import built, dense_keys, fmt_args, make_cache, select64, table_of, values64    # noqa: F401
 
 gpu = pytest.mark.gpu
 DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
@@ -37,3 +37,74 @@ def test_select_passes_over_pages_outside_the_pool(d, dtype, n, batch):
                                    k, ps, keep_last=last, status=status)
         assert torch.equal(got.cpu(), select64(q, bounds, tab, lens, ps, k, 0, last))
         assert status.item() == 4
+
+
+# ------------------------------------------------------------------ decode
+@gpu
+@pytest.mark.parametrize("n,pad", [(16, 0), (40, 0), (40, 3000), (3000, 0)])
+@pytest.mark.parametrize("nats", [16, 20])
+@pytest.mark.parametrize("fmt,dtype,d,G", [("16bit", "bf16", 128, 4), ("16bit", "fp16", 128, 4), ("16bit", "fp16", 64, 12),
+                                           ("scaled", "bf16", 128, 8), ("scaled", "fp16", 64, 3), ("scaled", "bf16", 256, 4),
+                                           ("block", "bf16", 128, 8), ("block", "fp16", 128, 16), ("block", "bf16", 64, 16),
+                                           ("block", "fp16", 256, 5)])
+def test_one_key_takes_the_weight_and_has_no_value(fmt, dtype, d, G, nats, n, pad):
+    """One key lies 16 or 20 nats above the others and its V is 0, so the output is made of small
+    weights alone. A weight is off by `part` of itself (2^-17 and 2^-22 in two parts of bf16 and fp16,
+    2^-11 in one part of fp16) and, where fp16 carries it, by `floor` of the largest (2^-43, 2^-38 in one
+    part; under block scales, of the largest weight times its V's scale); by d 2^-23 A for the sum of its logit
+    (A: that of the products' magnitudes; 0 for the one key, a single product), by 2^-23 |s| log2(e) for each of two
+    roundings of the logit s, and by 2^-21 for exponentials and joins, which the denominator has too; the output is
+    rounded to eps / 2, or half a step of the type's smallest numbers."""
+    dt, hk, ps = DT[dtype], 2, 16
+    tab, pages = table_of([n], ps, 1, pad=pad)
+    kv, sc = make_cache(pages, ps, hk, d, "NHD", fmt, dt, 2)
+    top, scale = 5, 1 / math.sqrt(d)
+    at = (int(tab[0, top // ps]), slice(None), top % ps)
+    kv[:, 0, :, :, 0] = 0
+    # (V of some thousands, so that fp16 holds what is left of it)
+    args = fmt_args(fmt, sc)
+    if fmt == "16bit":
+        kv[:, 1] *= 4096
+    elif fmt == "scaled":
+        args["v_scale"] *= 4096
+    else:
+        sc[:, 1] += 12
+    kv[at] = 0
+    # (logits of the others: N(0, 0.25) or so, under one block scale)
+    q = torch.randn((1, hk * G, d), generator=torch.Generator().manual_seed(3)) * 0.25
+    q[..., 0] = 32.0
+    q = q.to(dt).cuda()
+    if fmt == "block":
+        sc[:, 0] = 120
+        sc[at] = 127
+    code = nats / scale / 32 / (0.034375 if fmt == "scaled" else 1.0)
+    assert code < 448
+    kv[at[0], 0, at[2], :, 0] = torch.tensor(code).to(kv.dtype)
+    out, lse = pod.pod_paged_decode(q, kv, torch.from_numpy(tab).cuda(), torch.tensor([n], dtype=torch.int32, device="cuda"),
+                                    **args)
+    x = values64(kv, sc, "NHD", fmt)
+    if fmt == "scaled":
+        x[:, 1] *= 4096
+    page, slot = dense_keys(tab[0], n, ps, 1, -1)[0]
+    got = out[0].double().cpu()
+    for h in range(hk * G):
+        k, v, qh = x[page, 0, slot, h // G], x[page, 1, slot, h // G], q[0, h].double().cpu()
+        s = k @ qh * scale
+        p = torch.exp(s - s.max())
+        assert s.argmax() == top and (v[top] == 0).all()
+        z = p.sum()
+        want, B = p @ v / z, p @ v.abs() / z
+        A = scale * (k.abs() @ qh.abs())
+        A[top] = 0
+        rel = 2.0 ** -22 * 1.4427 * s.abs().max() + 2.0 ** -21
+        part, floor = (2.0 ** -17, 0.0) if fmt == "16bit" and dt == torch.bfloat16 else (2.0 ** -22, 2.0 ** -43)
+        if fmt != "16bit" and dt == torch.bfloat16:
+            part, floor = 2.0 ** -11, 2.0 ** -38
+        unit = torch.ones(n, dtype=torch.float64)
+        if fmt == "block":
+            unit = torch.exp2(sc.cpu().double()[page, 1, slot, h // G] - 127)
+        low = floor * (p * unit).max() * (v.abs() / unit[:, None]).sum(0) / z
+        tol = torch.finfo(dt).eps / 2 * want.abs() * (1 + 2.0 ** -7) + (2 * rel + part) * B + low \
+            + d * 2.0 ** -23 * (p * A) @ v.abs() / z + torch.finfo(dt).tiny * torch.finfo(dt).eps / 2
+        err = (got[h] - want).abs()
+        assert (err <= tol).all(), (h, (err / tol).max(), (err / B).max())
