@@ -611,8 +611,10 @@ POD_DEV float4 join(int n, int lanes, float up, float v_scale, float& lse, A sta
   const float f = sum == 0.f ? 0.f : v_scale / sum;
   acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
   if constexpr (FMT == POD_KV_E4M3_BLOCK) {
-    const float back = ex2(zv - z);                // O's own reference
-    acc.x *= back; acc.y *= back; acc.z *= back; acc.w *= back;
+    // O's own reference, in two steps (2^-127, the smallest scale, is 0 to the exponential)
+    const float back = ex2(0.5f * (zv - z));
+    acc.x = acc.x * back * back; acc.y = acc.y * back * back;
+    acc.z = acc.z * back * back; acc.w = acc.w * back * back;
   }
   return acc;
 }

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import prefill_decode_paged_pod_gb300 as pod
-from test_decode_steps import built, dense_keys, fmt_args, make_cache, select64, table_of, values64    # noqa: F401
+from test_decode_steps import attend64, built, dense_keys, fmt_args, make_cache, select64, table_of, values64    # noqa: F401
 
 gpu = pytest.mark.gpu
 DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
@@ -108,3 +108,26 @@ def test_one_key_takes_the_weight_and_has_no_value(fmt, dtype, d, G, nats, n, pa
             + d * 2.0 ** -23 * (p * A) @ v.abs() / z + torch.finfo(dt).tiny * torch.finfo(dt).eps / 2
         err = (got[h] - want).abs()
         assert (err <= tol).all(), (h, (err / tol).max(), (err / B).max())
+
+
+@gpu
+@pytest.mark.parametrize("byte,most", [(0, 448.0), (1, 448.0), (254, 1.0)])
+@pytest.mark.parametrize("n,pad", [(1, 0), (50, 0), (3000, 0), (50, 3000)])
+def test_smallest_and_largest_scales_of_values(byte, most, n, pad):
+    """V scales at the ends of the exponent byte: 2^-127 times a code is a bf16 number."""
+    dt, hk, G, d, ps = torch.bfloat16, 2, 4, 64, 16
+    tab, pages = table_of([n], ps, 1, pad=pad)
+    kv, sc = make_cache(pages, ps, hk, d, "NHD", "block", dt, 2)
+    codes = torch.rand(kv[:, 1].shape, generator=torch.Generator().manual_seed(4)) * most
+    kv[:, 1] = codes.to(kv.dtype).cuda()
+    sc[:, 1] = byte
+    q = torch.randn((1, hk * G, d), generator=torch.Generator().manual_seed(3)).to(dt).cuda()
+    out, lse = pod.pod_paged_decode(q, kv, torch.from_numpy(tab).cuda(), torch.tensor([n], dtype=torch.int32, device="cuda"),
+                                    kv_scales=sc)
+    x = values64(kv, sc, "NHD", "block")
+    want, wlse, A, B = attend64(q[0].double().cpu().numpy(), x, dense_keys(tab[0], n, ps, hk, -1), 1 / 8, None)
+    # weights in one part: 2^-11; x + e is rounded twice at some 2^7: 2^-17 of log2 each; the rest as in check()
+    rel = 2 * (d * 2.0 ** -23 * A + 2.0 ** -16)[:, None] + 2.0 ** -11
+    tol = np.abs(want) * 2.0 ** -8 * (1 + 2.0 ** -7) + rel * B
+    assert (np.abs(out[0].double().cpu().numpy() - want) <= tol).all()
+    assert (np.abs(lse[0].double().cpu().numpy() - wlse) <= 1e-3).all() and want.any()
