@@ -449,20 +449,23 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const __grid_co
   for (int p = lane; p < mine; p += 32)
     if ((unsigned)table[p] >= P.num_pages) score[p] = -INFINITY;
   float mag = 0.f;
+  bool some = false;                                   // a term that is not 0, though its fp32 product may be
 #pragma unroll
   for (int i = 0; i < NC; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       // (0 times an infinity is a NaN, as a term of that kind is)
       const float2 m = Pack<T>::unpack(top[i][e] & 0x7fff7fffu);
+      some |= (w[i][2 * e] != 0.f && m.x != 0.f) || (w[i][2 * e + 1] != 0.f && m.y != 0.f);
       mag += fabsf(w[i][2 * e]) * m.x + fabsf(w[i][2 * e + 1]) * m.y;
     }
 #pragma unroll
   for (int o = 16; o; o >>= 1) mag += __shfl_xor_sync(0xffffffffu, mag, o);
+  some = __any_sync(0xffffffffu, some || mag != mag);
   if (lane == 0)
-    // (products of the smallest numbers are off by more than their part)
+    // (products of the smallest numbers are off by more than their part: each by up to 2^-150)
     P.off[((long long)row * P.Hk + hk) * P.chunks + chunk] =
-        mag == 0.f ? 0.f : mag * ((float)(4 * NC + 6 + P.G) * 0x1.04p-24f) + 0x1p-140f;
+        some ? mag * ((float)(4 * NC + 6 + P.G) * 0x1.04p-24f) + 0x1p-140f : 0.f;
 }
 
 // ------------------------------------------------------------------ the choice

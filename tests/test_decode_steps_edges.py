@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import prefill_decode_paged_pod_gb300 as pod
-from test_decode_steps import attend64, built, dense_keys, fmt_args, make_cache, select64, table_of, values64    # noqa: F401
+from test_decode_steps import attend64, built, dense_keys, fmt_args, make_bounds, make_cache, select64, table_of, values64    # noqa: F401
 
 gpu = pytest.mark.gpu
 DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
@@ -37,6 +37,22 @@ def test_select_passes_over_pages_outside_the_pool(d, dtype, n, batch):
                                    k, ps, keep_last=last, status=status)
         assert torch.equal(got.cpu(), select64(q, bounds, tab, lens, ps, k, 0, last))
         assert status.item() == 4
+
+
+@gpu
+@pytest.mark.parametrize("e", [-64, -70, -76, -100, -125])
+@pytest.mark.parametrize("d,n,G", [(64, 90, 4), (128, 700, 2), (256, 9000, 1)])
+def test_select_with_products_below_fp32(e, d, n, G):
+    """Queries and bounds of some 2^e: their products are subnormal in fp32, or 0, and the choice is still that of 64 bits."""
+    dt, hk, ps = torch.bfloat16, 2, 16
+    tab, pages = table_of([n * ps, n * ps - 5], ps, 3)
+    bounds = make_bounds(pages, hk, d, torch.float32, 4).mul(2.0 ** e).to(dt)
+    q = (torch.randn((2, hk * G, d), generator=torch.Generator().manual_seed(5)) * 2.0 ** e).to(dt).cuda()
+    lens = [n * ps, n * ps - 5]
+    for k in (5, n // 3):
+        got = pod.pod_select_pages(q, bounds, torch.from_numpy(tab).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                   k, ps)
+        assert torch.equal(got.cpu(), select64(q, bounds, tab, lens, ps, k, 0, 1))
 
 
 # ------------------------------------------------------------------ decode
