@@ -670,8 +670,8 @@ typedef struct pod_decode_args {
  * pod_step_tables lists them; the keys of a page are those up to its last row
  * here, all read from the cache (so the call can be repeated, and what keys
  * taken back left behind goes with the next write). Values are code * scale in fp32,
- * rounded outward to dtype within its finite values; NaN does not count. Bounds of other pages are
- * left as they are. Padding rows are skipped; a slot past the pool joins 4 into
+ * rounded outward to dtype within its finite values. NaN does not count; where all of a
+ * channel's values are NaN, both bounds are. Bounds of other pages are left as they are. Padding rows are skipped; a slot past the pool joins 4 into
  * *status.
  * Reads kv_cache, kv_scales, slots, rows, num_pages, page_size, num_kv_heads,
  * head_dim, kv_layout, kv_format, dtype, k_scale, status; writes bounds.

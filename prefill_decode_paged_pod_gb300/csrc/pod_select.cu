@@ -41,7 +41,6 @@ struct Pair;
 template <>
 struct Pair<__nv_bfloat16> {
   using type = __nv_bfloat162;
-  static constexpr uint32_t kInf = 0x7f807f80u;
   static constexpr float kMax = 3.3895313892515355e38f;
   static POD_DEV __nv_bfloat16 down(float x) { return __float2bfloat16_rd(x); }
   static POD_DEV __nv_bfloat16 up(float x) { return __float2bfloat16_ru(x); }
@@ -49,7 +48,6 @@ struct Pair<__nv_bfloat16> {
 template <>
 struct Pair<__half> {
   using type = __half2;
-  static constexpr uint32_t kInf = 0x7c007c00u;
   static constexpr float kMax = 65504.f;
   static POD_DEV __half down(float x) { return __float2half_rd(x); }
   static POD_DEV __half up(float x) { return __float2half_ru(x); }
@@ -89,11 +87,17 @@ struct BoundParams {
   float k_scale;
 };
 
+// x within +-most; a NaN stays one
+POD_DEV float within(float x, float most) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(-most));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(x) : "f"(most));
+  return x;
+}
 // Two values rounded outward to T, within its finite values.
 template <typename T>
 POD_DEV uint32_t outward2(float x, float y, bool upper) {
-  x = fminf(fmaxf(x, -Pair<T>::kMax), Pair<T>::kMax);
-  y = fminf(fmaxf(y, -Pair<T>::kMax), Pair<T>::kMax);
+  x = within(x, Pair<T>::kMax);
+  y = within(y, Pair<T>::kMax);
   T r[2] = {upper ? Pair<T>::up(x) : Pair<T>::down(x), upper ? Pair<T>::up(y) : Pair<T>::down(y)};
   return (uint32_t)*reinterpret_cast<uint16_t*>(&r[0]) | (uint32_t)*reinterpret_cast<uint16_t*>(&r[1]) << 16;
 }
@@ -104,7 +108,7 @@ template <typename T, int D>
 __device__ __noinline__ void bounds_of_far_scales(const BoundParams& P, const uint8_t* keys, const uint8_t* scales,
                                                   long long row_bytes, int step, int valid, long long to) {
   for (int c = 2 * (threadIdx.x & 31); c < D; c += 64) {
-    float lo0 = INFINITY, lo1 = INFINITY, hi0 = -INFINITY, hi1 = -INFINITY;
+    float lo0 = NAN, lo1 = NAN, hi0 = NAN, hi1 = NAN;
     for (int k = 0; k < valid; ++k) {
       const int e = scales[(long long)k * step];
       const float s = e ? __uint_as_float((uint32_t)e << 23) : 5.877471754111438e-39f;
@@ -191,10 +195,7 @@ __global__ void __launch_bounds__(kBoundThreads, 4) bounds_kernel(const __grid_c
     const int step = P.hnd ? 1 : P.Hk;
     uint32_t lo[R], hi[R];
 #pragma unroll
-    for (int e = 0; e < R; ++e) {
-      lo[e] = Pair<M>::kInf;
-      hi[e] = Pair<M>::kInf | 0x80008000u;
-    }
+    for (int e = 0; e < R; ++e) lo[e] = hi[e] = 0x7fff7fffu;   // (NaN, which stays where no key is a number)
     // the exponents of the page's keys, of 32 at a time, and the first keys' loads beside them
     int eb = 0, top = 0, low = 255;
     if (FMT == POD_KV_E4M3_BLOCK && lane < valid) eb = scales[(long long)lane * step];

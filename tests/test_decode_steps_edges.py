@@ -55,6 +55,48 @@ def test_select_with_products_below_fp32(e, d, n, G):
         assert torch.equal(got.cpu(), select64(q, bounds, tab, lens, ps, k, 0, 1))
 
 
+# ------------------------------------------------------------------ bounds
+@gpu
+@pytest.mark.parametrize("fmt,dtype,d,ps,layout,far", [("16bit", "bf16", 128, 16, "NHD", False), ("16bit", "fp16", 64, 3, "HND", False),
+                                                      ("scaled", "bf16", 256, 40, "HND", False), ("block", "fp16", 128, 16, "NHD", False),
+                                                      ("block", "bf16", 64, 33, "HND", True), ("scaled", "fp16", 128, 1, "NHD", False)])
+def test_bounds_of_channels_without_a_number(fmt, dtype, d, ps, layout, far):
+    """Both are NaN, so the page is attended and its NaN shows as it does over all keys; one number among
+    NaNs is the bound."""
+    dt, hk, n = DT[dtype], 2, 12
+    lens = [n * ps]
+    tab, pages = table_of(lens, ps, 1)
+    kv, sc = make_cache(pages, ps, hk, d, layout, fmt, dt, 2)
+    if far:
+        sc[:, 0, :, ::2] = 90
+    raw = kv.view(torch.int16) if fmt == "16bit" else kv.view(torch.uint8)
+    nan = 0x7fff if fmt == "16bit" else 0x7f
+    page = int(tab[0, 4])
+    keys = raw[page, 0] if layout == "NHD" else raw[page, 0].transpose(0, 1)       # [ps, hk, d]
+    keys[:, 1, 5] = nan
+    keys[1:, 0, 6] = nan
+    bounds = torch.zeros((pages, hk, 2, d), dtype=dt, device="cuda")
+    args = fmt_args(fmt, sc)
+    args.pop("v_scale", None)
+    slots = torch.from_numpy((tab[0, :n, None].astype(np.int64) * ps + np.arange(ps)).reshape(-1)).cuda()
+    pod.pod_page_bounds(kv, bounds, slots, kv_layout=layout, **args)
+    want = torch.zeros((pages, hk, 2, d), dtype=torch.bool)
+    want[page, 1, :, 5] = True
+    assert torch.equal(bounds.isnan().cpu(), want)
+    b = bounds.double().cpu()
+    one = values64(kv, sc, layout, fmt)[page, 0, 0, 0, 6].float().double()       # (code * scale in fp32)
+    near = abs(one) * torch.finfo(dt).eps + torch.finfo(dt).tiny * torch.finfo(dt).eps
+    assert one - near <= b[page, 0, 0, 6] <= one <= b[page, 0, 1, 6] <= one + near
+    q = torch.randn((1, 2 * hk, d), generator=torch.Generator().manual_seed(3)).to(dt).cuda()
+    t, ln = torch.from_numpy(tab).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    sel = pod.pod_select_pages(q, bounds, t, ln, 2, ps)
+    assert 4 in sel[0, 1].tolist()
+    args = fmt_args(fmt, sc)
+    for pages_ in (sel, None):
+        out, lse = pod.pod_paged_decode(q, kv, t, ln, pages=pages_, kv_layout=layout, **args)
+        assert out[0, 2:].isnan().all() and lse[0, 2:].isnan().all()
+
+
 # ------------------------------------------------------------------ decode
 @gpu
 @pytest.mark.parametrize("n,pad", [(16, 0), (40, 0), (40, 3000), (3000, 0)])
