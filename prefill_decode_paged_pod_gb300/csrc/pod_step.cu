@@ -170,16 +170,17 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constan
     sh_off[tid] = (int)min(x[0], 0x7fffffffll);
     sh_first[tid] = first;
     __syncthreads();
-    const int moved = (int)min(all[0], max(0ll, P.capacity - count - given));
+    // (unsigned: an index a few rounds past the last page stays past it)
+    const unsigned moved = (unsigned)min(all[0], max(0ll, P.capacity - count - given));
     if (moved < all[0]) bad |= kStatusNoRoom;
     const int32_t* from[kInFlight];
-    for (int i = tid; i < moved; i += T * kInFlight) {   // a thread a page, some at a time
+    for (unsigned i = tid; i < moved; i += T * kInFlight) {   // a thread a page, some at a time
       int32_t page[kInFlight];
 #pragma unroll
       for (int j = 0; j < kInFlight; ++j)
         if (i + j * T < moved) {
           const int k = find_off(sh_off, T, i + j * T);
-          from[j] = P.table + (long long)(base + k) * P.table_stride + sh_first[k] + i + j * T - sh_off[k];
+          from[j] = P.table + (long long)(base + k) * P.table_stride + sh_first[k] + (int)(i + j * T - sh_off[k]);
         }
 #pragma unroll
       for (int j = 0; j < kInFlight; ++j)
@@ -230,16 +231,17 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constan
     sh_off[tid] = (int)y[0];
     sh_first[tid] = s.had;
     __syncthreads();
-    for (int i = tid; i < (int)sums[0]; i += T * kInFlight) {
+    const unsigned taken = (unsigned)sums[0];
+    for (unsigned i = tid; i < taken; i += T * kInFlight) {
       int32_t page[kInFlight];
 #pragma unroll
       for (int j = 0; j < kInFlight; ++j)
-        if (i + j * T < (int)sums[0]) page[j] = P.free_pages[top - 1 - pages_taken - i - j * T];
+        if (i + j * T < taken) page[j] = P.free_pages[top - 1 - pages_taken - i - j * T];
 #pragma unroll
       for (int j = 0; j < kInFlight; ++j)
-        if (i + j * T < (int)sums[0]) {
+        if (i + j * T < taken) {
           const int k = find_off(sh_off, T, i + j * T);
-          P.table[(long long)(base + k) * P.table_stride + sh_first[k] + i + j * T - sh_off[k]] = page[j];
+          P.table[(long long)(base + k) * P.table_stride + sh_first[k] + (int)(i + j * T - sh_off[k])] = page[j];
         }
     }
     pages += all[0];

@@ -189,3 +189,23 @@ def test_smallest_and_largest_scales_of_values(byte, most, n, pad):
     tol = np.abs(want) * 2.0 ** -8 * (1 + 2.0 ** -7) + rel * B
     assert (np.abs(out[0].double().cpu().numpy() - want) <= tol).all()
     assert (np.abs(lse[0].double().cpu().numpy() - wlse) <= 1e-3).all() and want.any()
+
+
+# ------------------------------------------------------------------ step tables
+@gpu
+def test_step_tables_of_the_largest_stack():
+    """2^31 - 1 places for 2^31 pages that are given back: indices end at the last place of 31 bits."""
+    batch, width = 1024, 1 << 21
+    total = batch * width
+    table = torch.arange(total, dtype=torch.int32, device="cuda").view(batch, width)
+    stack = torch.full((total + 63,), -9, dtype=torch.int32, device="cuda")
+    lens = torch.full((batch,), width, dtype=torch.int32, device="cuda")
+    count, status = (torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2))
+    t = pod.pod_step_tables(table, lens, -lens, stack[32:32 + total - 1], count, 1, max_rows=1, status=status)
+    assert count.item() == total - 1 and status.item() == 8 and t.kv_lens.tolist() == [0] * batch
+    assert (stack[:32] == -9).all() and (stack[32 + total - 1:] == -9).all()
+    assert torch.equal(stack[32:32 + total - 1], table.view(-1)[:-1])
+    # a step with room for one row leaves them all there
+    new = torch.full((batch,), width, dtype=torch.int32, device="cuda")
+    t = pod.pod_step_tables(table, lens, new, stack[32:32 + total - 1], count, 1, max_rows=1, status=status)
+    assert count.item() == total - 1 and t.kv_lens.tolist() == [0] * batch and t.requests.tolist() == [-1]
