@@ -987,6 +987,7 @@ pod_status check_decode_sizes(const pod_decode_args& a) {
     return fail(POD_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256");
   if (a.num_kv_heads < 1 || a.num_kv_heads > 4096) return fail(POD_ERR_INVALID_ARG, "num_kv_heads must be in [1, 4096]");
   if (a.page_size < 1 || a.num_pages < 1) return fail(POD_ERR_INVALID_ARG, "the page pool is empty");
+  if (a.page_size > (1 << 30)) return fail(POD_ERR_INVALID_ARG, "page_size must be at most 2^30");
   // rows of head_dim elements are counted in 32 bits (a pool past this would be 2^38 bytes or more)
   if (a.num_pages > 0xfffffff0ll / (2 * (int64_t)a.page_size * a.num_kv_heads))
     return fail(POD_ERR_INVALID_ARG, "the page pool is too large");

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import prefill_decode_paged_pod_gb300 as pod
-from test_decode_steps import attend64, built, dense_keys, fmt_args, make_bounds, make_cache, select64, table_of, values64    # noqa: F401
+from test_decode_steps import DEC, attend64, built, c_call, dense_keys, fmt_args, make_bounds, make_cache, select64, table_of, values64    # noqa: F401
 
 gpu = pytest.mark.gpu
 DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
@@ -209,3 +209,14 @@ def test_step_tables_of_the_largest_stack():
     new = torch.full((batch,), width, dtype=torch.int32, device="cuda")
     t = pod.pod_step_tables(table, lens, new, stack[32:32 + total - 1], count, 1, max_rows=1, status=status)
     assert count.item() == total - 1 and t.kv_lens.tolist() == [0] * batch and t.requests.tolist() == [-1]
+
+
+# ------------------------------------------------------------------ refusals
+def test_pages_of_more_than_2_30_slots_are_refused():
+    """By all calls that read a pool (two refuse them for their tables already). Nothing is launched."""
+    lib = pod.load_library()
+    for name in ("pod_page_bounds", "pod_select_pages", "pod_paged_decode"):
+        for ps in ((1 << 30) + 1, (1 << 31) - 1):
+            code = c_call(getattr(lib, name), DEC, pod._DECODE_ARGS, ps=ps, num_pages=1, Hk=1, rows=0, batch=0, width=1)
+            assert code == 1 and pod.pod_last_error(), (name, ps)
+    assert c_call(lib.pod_page_bounds, DEC, pod._DECODE_ARGS, ps=1 << 30, num_pages=1, Hk=1, rows=0) == 0
