@@ -586,7 +586,8 @@ pod_status pod_tree_destroy(pod_tree_handle h);
  * num_pages (or negative) in front of that reads as if its keys were masked,
  * and joins the value 4 into *status by OR, as does a length outside
  * [0, table_width * page_size], which is cut to that range. status, streams
- * and pointers' alignment as above; table_width * page_size is at most 2^30.
+ * and pointers' alignment as above; table_width * page_size, and page_size
+ * where there is no table, are at most 2^30.
  * ------------------------------------------------------------------------ */
 
 /* Arguments of pod_step_tables. All pointers DEVICE. */
@@ -596,7 +597,7 @@ typedef struct pod_step_args {
     const int32_t* new_lens;    /* [batch] tokens of the step; negative: keys taken back */
     int32_t* kv_lens_out;       /* [batch] keys after it; may be kv_lens */
     int32_t* free_pages;        /* [free_capacity], a stack: the top is entry *free_count - 1 */
-    const int32_t* free_count;  /* [1] */
+    const int32_t* free_count;  /* [1]; cut to [0, free_capacity] */
     int32_t* free_count_out;    /* [1]; may be free_count */
     int32_t* q_indptr;          /* [batch + 1] */
     int32_t* requests;          /* [max_rows] */
@@ -681,7 +682,9 @@ pod_status pod_page_bounds(const pod_decode_args* args, void* stream);
 
 /*
  * pod_select_pages — for every request and KV head the num_selected pages that
- * promise its query the largest logits.
+ * promise its query the largest logits. Row r of q is request r's query. The
+ * rows of pod_step_tables stand otherwise (a request may have none, or several):
+ * that of request r's last token is q_indptr[r + 1] - 1, where it has any.
  * The score of a page is the sum over the KV head's query heads and the
  * channels of max(q * smallest, q * largest): what the query's logits with the
  * page's keys can reach, before sm_scale. The first keep_first and the last
@@ -702,8 +705,8 @@ pod_status pod_select_pages(const pod_decode_args* args, void* stream);
 size_t pod_select_pages_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t table_width);
 
 /*
- * pod_paged_decode — attention of one token per request: query row r over keys
- * t < kv_lens[r] of request r, with window_left >= 0 over
+ * pod_paged_decode — attention of one token per request: query row r (request
+ * r's, as in pod_select_pages) over keys t < kv_lens[r] of request r, with window_left >= 0 over
  * t >= kv_lens[r] - 1 - window_left only, or, where `pages` is given, over the
  * keys of these pages (positions in the table row, per KV head; entries that
  * are negative or past the request's pages are skipped, and a page listed

@@ -1059,7 +1059,8 @@ def pod_select_pages_workspace_size(batch: int, num_kv_heads: int, table_width: 
 def pod_select_pages(q, bounds, block_table, kv_lens, num_selected: int, page_size: int, *, keep_first=0, keep_last=1,
                      pages=None, workspace=None, status=None, stream=None):
     """The ``num_selected`` pages of every request and KV head whose ``bounds``
-    (pod_page_bounds) promise the heads of q [batch, H, d] the largest logits:
+    (pod_page_bounds) promise the heads of q [batch, H, d] (a row a request; the
+    last one of pod_step_tables' rows is ``q_indptr[1:] - 1``) the largest logits:
     int32 [batch, Hk, num_selected], positions in the request's ``block_table``
     row, ascending, -1 behind them. The first ``keep_first`` and the last
     ``keep_last`` pages are among them whatever their score."""
@@ -1099,8 +1100,8 @@ def pod_paged_decode_workspace_size(batch: int, num_qo_heads: int, num_kv_heads:
 def pod_paged_decode(q, kv_cache, block_table, kv_lens, *, pages=None, sm_scale=None, window_left=-1, sinks=None,
                      kv_scales=None, k_scale=1.0, v_scale=1.0, kv_layout="NHD", out=None, lse=None, workspace=None,
                      status=None, stream=None):
-    """Attention of one token per request, q [batch, H, d] (any row stride that is
-    a multiple of 8), over the first ``kv_lens`` keys of its pages, over the last
+    """Attention of one token per request, q [batch, H, d] (a row a request, as for
+    pod_select_pages; any row stride that is a multiple of 8), over the first ``kv_lens`` keys of its pages, over the last
     ``window_left`` + 1 of them, or over the selected ``pages``
     (pod_select_pages). The cache is a 16-bit or an FP8 one, as for
     pod_append_kv. Lengths and tables are read on the device, so a captured call

@@ -2,13 +2,16 @@
 beside tests/test_decode_steps.py, whose 64-bit definitions these use.
 """
 import math
+import os
+import re
 
 import numpy as np
 import pytest
 import torch
 
 import prefill_decode_paged_pod_gb300 as pod
-from test_decode_steps import DEC, attend64, built, c_call, dense_keys, fmt_args, make_bounds, make_cache, select64, table_of, values64    # noqa: F401
+from test_decode_steps import (DEC, attend64, built, c_call, check, dense_keys, fmt_args, make_bounds,    # noqa: F401
+                               make_cache, select64, table_of, values64)
 
 gpu = pytest.mark.gpu
 DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
@@ -189,6 +192,44 @@ def test_smallest_and_largest_scales_of_values(byte, most, n, pad):
     tol = np.abs(want) * 2.0 ** -8 * (1 + 2.0 ** -7) + rel * B
     assert (np.abs(out[0].double().cpu().numpy() - want) <= tol).all()
     assert (np.abs(lse[0].double().cpu().numpy() - wlse) <= 1e-3).all() and want.any()
+
+
+# ------------------------------------------------------------------ the step as a whole
+@gpu
+@pytest.mark.parametrize("new", [[1, 1, 1, 1], [1, 0, 1, 1], [0, 5, 0, 1], [3, 0, -2, 0]])
+def test_the_step_of_the_readme(new):
+    """Its text as it stands: every request with rows attends its own keys, others sitting out or not."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "README.md")) as f:
+        code, = (x for x in re.findall(r"```python\n(.*?)```", f.read(), re.S) if "pod_step_tables" in x)
+    dt, H, Hk, d, page_size, B = torch.bfloat16, 8, 2, 64, 16, 4
+    lens, pages = [40, 100, 7, 64], 40
+    kv, _ = make_cache(pages, page_size, Hk, d, "NHD", "16bit", dt, 2)
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")    # noqa: E731
+    rows = max(B, sum(max(0, n) for n in new))
+    qkv = torch.randn((rows, H + 2 * Hk, d), generator=torch.Generator().manual_seed(3)).to(dt).cuda()
+    w = torch.ones(d, dtype=dt, device="cuda")
+    env = dict(pod=pod, block_table=torch.zeros((B, 9), dtype=torch.int32, device="cuda"), kv_lens=dev([0] * B),
+               new_lens=dev(new), free_pages=dev(np.random.RandomState(1).permutation(pages)), free_count=dev([pages]),
+               page_size=page_size, batch=B, qkv=qkv, H=H, Hk=Hk, kv_cache=kv, wq=w, wk=w,
+               bounds=torch.zeros((pages, Hk, 2, d), dtype=dt, device="cuda"))
+    first = pod.pod_step_tables(env["block_table"], env["kv_lens"], dev(lens), env["free_pages"], env["free_count"], page_size,
+                                max_rows=sum(lens))
+    pod.pod_page_bounds(kv, env["bounds"], first.slots)
+    exec(code, env)
+    now = [max(0, a + b) for a, b in zip(lens, new)]
+    assert env["kv_lens"].tolist() == now
+    table = env["block_table"].cpu().numpy()
+    qn, _ = pod.pod_qk_norm_rope(qkv[:, :H], None, env["t"].positions, q_weight=w)
+    x = values64(kv, None, "NHD", "16bit")
+    row = 0
+    for r, n in enumerate(new):
+        if n <= 0:
+            continue
+        row += n
+        want = attend64(qn[row - 1].double().cpu().numpy(), x, dense_keys(table[r], now[r], page_size, Hk, -1), 1 / math.sqrt(d),
+                        None)
+        check(env["out"][r:r + 1], env["lse"][r:r + 1], *(y[None] for y in want), d, dt)
 
 
 # ------------------------------------------------------------------ step tables
