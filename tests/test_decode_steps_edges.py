@@ -194,6 +194,90 @@ def test_smallest_and_largest_scales_of_values(byte, most, n, pad):
     assert (np.abs(lse[0].double().cpu().numpy() - wlse) <= 1e-3).all() and want.any()
 
 
+@gpu
+@pytest.mark.parametrize("H,hk,d,ps,fmt,dtype", [(72, 4, 128, 1, "16bit", "bf16"), (40, 4, 256, 2, "block", "fp16"),
+                                                 (160, 8, 64, 3, "scaled", "bf16")])
+def test_small_pages_and_two_tiles_of_heads(H, hk, d, ps, fmt, dtype):
+    """Four KV heads a CTA, and more query heads a KV head than one tile holds."""
+    dt, B = DT[dtype], 130
+    r = np.random.RandomState(4)
+    lens = [int(x) for x in r.choice([0, 1, 5, 63, 64, 65, 200], B)]
+    lens[7], lens[60] = 3000, 1111
+    tab, pages = table_of(lens, ps, 1, pad=9000 // ps)
+    kv, sc = make_cache(pages, ps, hk, d, "NHD", fmt, dt, 2)
+    q = torch.randn((B, H, d), generator=torch.Generator().manual_seed(3)).to(dt).cuda()
+    out, lse = pod.pod_paged_decode(q, kv, torch.from_numpy(tab).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                    **fmt_args(fmt, sc))
+    x = values64(kv, sc, "NHD", fmt)
+    at = [7, 60] + list(range(20, 30)) + [B - 1]
+    ref = [attend64(q[i].double().cpu().numpy(), x, dense_keys(tab[i], lens[i], ps, hk, -1), 1 / math.sqrt(d), None) for i in at]
+    check(out[at], lse[at], *(np.stack(y) for y in zip(*ref)), d, dt, fmt)
+
+
+@gpu
+@pytest.mark.parametrize("extra", [0, 2100])
+def test_tables_that_are_slices(extra):
+    """A wider table's columns and every other row: selection and both decode kernels."""
+    dt, hk, H, d, ps = torch.float16, 2, 8, 64, 16
+    lens = [300, 17, 0, 640]
+    tab, pages = table_of(lens, ps, 1, pad=extra)
+    kv, _ = make_cache(pages, ps, hk, d, "NHD", "16bit", dt, 2)
+    bounds = make_bounds(pages, hk, d, dt, 4)
+    big = torch.full((8, tab.shape[1] + 5), 1 << 30, dtype=torch.int32, device="cuda")
+    t = big[::2, 3:-2]
+    t.copy_(torch.from_numpy(tab))
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = torch.randn((4, H, d), generator=torch.Generator().manual_seed(3)).to(dt).cuda()
+    sel = pod.pod_select_pages(q, bounds, t, ln, 4, ps)
+    assert torch.equal(sel.cpu(), select64(q, bounds, tab, lens, ps, 4, 0, 1))
+    for pages_ in (None, sel):
+        want = pod.pod_paged_decode(q, kv, t.contiguous(), ln, pages=pages_)
+        got = pod.pod_paged_decode(q, kv, t, ln, pages=pages_)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@gpu
+def test_captured_between_copies_fills_and_other_branches():
+    """In a graph whose nodes before the calls are a copy, a fill and a kernel of another stream."""
+    dt, hk, H, d, ps, B = torch.bfloat16, 2, 8, 64, 16, 5
+    lens = [300, 17, 0, 640, 4000]
+    tab, pages = table_of(lens, ps, 1)
+    kv, _ = make_cache(pages, ps, hk, d, "NHD", "16bit", dt, 2)
+    bounds = make_bounds(pages, hk, d, dt, 4)
+    t, ln = torch.from_numpy(tab).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    host = torch.randn((B, H, d), generator=torch.Generator().manual_seed(3)).to(dt).pin_memory()
+    q, side = torch.empty((B, H, d), dtype=dt, device="cuda"), torch.zeros((B, H, d), dtype=dt, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def step():
+        q.copy_(host, non_blocking=True)
+        status.zero_()
+        sel = pod.pod_select_pages(q, bounds, t, ln, 4, ps, status=status)
+        now, other = torch.cuda.current_stream(), streams[1]
+        other.wait_stream(now)
+        with torch.cuda.stream(other):
+            side.copy_(q).mul_(2)
+            beside = pod.pod_paged_decode(side, kv, t, ln)
+        here = pod.pod_paged_decode(q, kv, t, ln, pages=sel)
+        now.wait_stream(other)
+        return (sel,) + here + beside + pod.pod_paged_decode(side, kv, t, ln, status=status)
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    with torch.cuda.stream(streams[0]):
+        want = step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        got = step()
+    for _ in range(5):
+        for x in got:
+            x.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and status.item() == 0
+    assert torch.equal(want[3], want[5])
+
+
 # ------------------------------------------------------------------ the step as a whole
 @gpu
 @pytest.mark.parametrize("new", [[1, 1, 1, 1], [1, 0, 1, 1], [0, 5, 0, 1], [3, 0, -2, 0]])
