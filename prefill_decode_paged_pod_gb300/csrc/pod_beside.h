@@ -1,6 +1,6 @@
-// pod_beside.h — launches of the decode step's kernels: beside the kernel before
-// (programmatic stream serialization; the kernels wait for it inside), in clusters
-// where asked.
+// pod_beside.h — launches of the cache operators' and the decode step's kernels: beside
+// the kernel before (programmatic stream serialization; the kernels wait for it inside), in
+// clusters where asked.
 #pragma once
 #include <cuda_runtime.h>
 

@@ -45,6 +45,7 @@
 #include <string>
 
 #include "../../include/pod.h"
+#include "pod_beside.h"
 #include "pod_device.cuh"
 #include "pod_turns.h"
 
@@ -94,19 +95,6 @@ struct IoFreq {                  // (a kernel parameter: no longer than it has t
 // -> 30.8, 65536 read 66.5 -> 64.3.
 POD_DEV void after_the_last_kernel() {
   asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
-}
-template <typename... A, typename... B>
-cudaError_t launch_beside(void (*kernel)(A...), unsigned grid, cudaStream_t st, const B&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kIoThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Element offset of (slot, K half, head 0) in the cache, and the steps to the
@@ -611,9 +599,9 @@ cudaError_t launch_io(IoParams& P, bool fused, const Turns& f, cudaStream_t st) 
   if (fused) {
     IoFreq<D> fd;
     memcpy(&fd, f.f, sizeof(fd));
-    return launch_beside(cache_io_kernel<T, D, FMT, true>, grid, st, P, fd);
+    return launch_beside(cache_io_kernel<T, D, FMT, true>, grid, kIoThreads, 0, 1, st, P, fd);
   } else if constexpr (cache) {
-    return launch_beside(cache_io_kernel<T, D, FMT, false>, grid, st, P, IoFreq<2>{});
+    return launch_beside(cache_io_kernel<T, D, FMT, false>, grid, kIoThreads, 0, 1, st, P, IoFreq<2>{});
   }
   return cudaErrorInvalidValue;                  // (a write without a cache is not asked for)
 }
@@ -638,9 +626,9 @@ cudaError_t launch_read(IoParams& P, int fmt, cudaStream_t st) {
   const long long blocks = cut_of(P.cut[0], 0, P.rows, 2 * P.Hk, tasks_of(P, 2 * P.Hk, round, 2));
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const unsigned grid = (unsigned)blocks;
-  return fmt == FMT_16 ? launch_beside(cache_read_kernel<T, D, FMT_16>, grid, st, P)
-         : fmt == FMT_SCALED ? launch_beside(cache_read_kernel<T, D, FMT_SCALED>, grid, st, P)
-                             : launch_beside(cache_read_kernel<T, D, FMT_BLOCK>, grid, st, P);
+  return fmt == FMT_16 ? launch_beside(cache_read_kernel<T, D, FMT_16>, grid, kIoThreads, 0, 1, st, P)
+         : fmt == FMT_SCALED ? launch_beside(cache_read_kernel<T, D, FMT_SCALED>, grid, kIoThreads, 0, 1, st, P)
+                             : launch_beside(cache_read_kernel<T, D, FMT_BLOCK>, grid, kIoThreads, 0, 1, st, P);
 }
 
 pod_status check_rows(const char* what, const void* p, int64_t stride, int64_t heads, int d) {

@@ -31,7 +31,6 @@ struct DecodeParams {
   float* piece_o;                  // [grid * 2][hw][heads of a tile][d], normalised
   float* piece_lse;                // [grid * 2][hw][heads of a tile], base 2
   long long q_stride, out_stride, table_stride;
-  long long scale_bytes;           // of the pool's exponent bytes
   unsigned num_pages;
   int batch, H, Hk, G, width, ps, ps_shift, hnd, num_selected, window;   // ps_shift: -1 where ps is no power of two
   int hw;                          // KV heads of a CTA
@@ -41,8 +40,8 @@ struct DecodeParams {
   float v_scale;
 };
 
-// CTAs of the attention kernel on the current device (its partition of the work and
-// so the workspace depend on them) and the launches.
+// The launches. The attention kernel's partition of the work, and with it the workspace, is
+// made for the CTAs that 152 SMs hold.
 cudaError_t decode_launch_16(int d, bool bf16, DecodeParams& P, cudaStream_t st);
 cudaError_t decode_launch_scaled(int d, bool bf16, DecodeParams& P, cudaStream_t st);
 cudaError_t decode_launch_block(int d, bool bf16, DecodeParams& P, cudaStream_t st);

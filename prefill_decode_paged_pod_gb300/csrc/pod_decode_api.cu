@@ -92,7 +92,6 @@ pod_status pod_paged_decode(const pod_decode_args* a, void* stream) {
   P.out_stride = a->out_stride;
   P.table_stride = a->table_stride;
   P.num_pages = (unsigned)a->num_pages;
-  P.scale_bytes = a->num_pages * 2 * a->page_size * a->num_kv_heads;
   P.batch = a->batch;
   P.H = a->num_qo_heads;
   P.Hk = a->num_kv_heads;

@@ -110,7 +110,7 @@ POD_DEV Step step_of(const StepParams& P, int len, int n) {
   return s;
 }
 
-// last i with at[i] <= x (at ascending from 0; x < at[n])
+// last i < n with at[i] <= x (at ascending from at[0] <= x)
 POD_DEV int find_row(const int32_t* at, int n, int x) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
@@ -133,17 +133,6 @@ POD_DEV void write_row(const StepParams& P, int i, int rows, const int32_t* indp
   P.requests[i] = req;
   P.positions[i] = pos;
   P.slots[i] = slot;
-}
-
-// Last k < n with off[k] <= x (off ascending from off[0] <= x).
-POD_DEV int find_off(const int* off, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (off[mid] <= x) lo = mid;
-    else hi = mid;
-  }
-  return lo;
 }
 
 __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constant__ StepParams P) {
@@ -179,7 +168,7 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constan
 #pragma unroll
       for (int j = 0; j < kInFlight; ++j)
         if (i + j * T < moved) {
-          const int k = find_off(sh_off, T, i + j * T);
+          const int k = find_row(sh_off, T, i + j * T);
           from[j] = P.table + (long long)(base + k) * P.table_stride + sh_first[k] + (int)(i + j * T - sh_off[k]);
         }
 #pragma unroll
@@ -240,7 +229,7 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constan
 #pragma unroll
       for (int j = 0; j < kInFlight; ++j)
         if (i + j * T < taken) {
-          const int k = find_off(sh_off, T, i + j * T);
+          const int k = find_row(sh_off, T, i + j * T);
           P.table[(long long)(base + k) * P.table_stride + sh_first[k] + (int)(i + j * T - sh_off[k])] = page[j];
         }
     }
