@@ -408,7 +408,8 @@ size_t pod_static_scratch_capacity(void);
  *  POD_KV_E4M3_BLOCK  E4M3 codes and one exponent byte b for each (token, KV
  *                     head) of K and of V: value = code * 2^(b - 127), with
  *                     the smallest b that keeps the head row's codes within
- *                     +-448. kv_scales holds the bytes,
+ *                     +-448 (b is at most 254: what reading a key with 255
+ *                     gives is not defined). kv_scales holds the bytes,
  *                     [num_pages, 2, page_size, Hk] or, HND,
  *                     [num_pages, 2, Hk, page_size].
  * Codes are rounded to nearest even and saturate at +-448; NaN stays NaN.

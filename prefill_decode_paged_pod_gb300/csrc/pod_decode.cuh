@@ -31,10 +31,10 @@
 // the order of the keys.
 //
 // Bound by memory: twelve warps an SM with up to 8 KB of keys each on their way, and the next
-// tile's rows asked for into L2. Measured on a GB300, in graphs, of the measured copy rate: 64
-// requests of 512 to 16384 keys, 32/8 heads of 128, bf16: 332 us, 101 %; one request of 131072
-// keys, 64/8 heads: 87 us, 91 %; 96 requests of 4096 to 12288 keys over block-scaled FP8: 242 to
-// 251 us, 89 to 93 % (per-tensor scales 246; HND pages 236 and 231): the conversions and the
+// tile's rows asked for into L2. Measured on two GB300s, in graphs, of the measured copy rate: 64
+// requests of 512 to 16384 keys, 32/8 heads of 128, bf16: 326 to 333 us, 101 to 103 %; one request
+// of 131072 keys, 64/8 heads: 86 to 88 us, 91 %; 96 requests of 4096 to 12288 keys over block-scaled
+// FP8: 243 to 252 us, 89 to 92 % (per-tensor scales 238 to 247; HND pages 237 and 230): the conversions and the
 // softmax of twice as many keys a byte, and rows of 128 bytes a kilobyte apart. 32-byte loads
 // and page numbers two tiles ahead made 332 of 352 and 260 of 307 us. K and V through a ring of
 // asynchronous copies in shared memory took 430 and 310, K's codes as E4M3 operands (the legacy E4M3
@@ -116,8 +116,9 @@ constexpr float lag() {
 }
 
 // o += a * hi, + a * lo where PARTS is 2. fp16's lo comes times 2^11 and is summed by itself (in
-// o's own sum, without the factor: 16 query heads a KV head over block scales 331 us, 353 now;
-// head_dim 64 163 and 167; the others the same to 1 %).
+// o's own sum, without the factor: 16 query heads a KV head over block scales 331 us, 353 now, over
+// per-tensor scales 317 and 334; block scales with head_dim 64 163 and 167, 256 260 and 268; the
+// other forms the same to 1 %).
 template <bool BF16, int PARTS>
 POD_DEV void mma_parts(float* o, const uint32_t* a, const uint32_t* hi, const uint32_t* lo) {
   if constexpr (PARTS == 2 && !BF16) {
@@ -356,7 +357,7 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
     // The next tile's rows set out for L2, a lane a key, before there are registers for them
     // (block-scaled FP8 263 -> 250 us, 16 query heads a KV head over it 350 -> 308; 16-bit rows 336 ->
     // 332 and 378 -> 360). Rows of 64 bytes would bring in their neighbours (158 -> 173), and pages of one
-    // or two slots ask for too many places at once (of one slot 262 -> 464, in HND 349 -> 535; of four
+    // slot ask for too many places at once (279 -> 488, in HND 330 -> 593; of two slots 269 and 261, of four
     // 259 -> 250).
     if (D * S::E >= 128 && P.ps >= 4) {
 #pragma unroll
@@ -914,9 +915,9 @@ cudaError_t launch_decode_nt(DecodeParams& P, cudaStream_t st) {
   P.grid = 152 * per_sm;
   // A CTA's warps take four KV heads instead of four parts of one head's keys where a head's
   // rows in a page of an NHD cache are few: neighbouring heads' rows are neighbours in memory.
-  // (96 block-scaled requests with pages of one slot 342 -> 283 us, per-tensor scales 304 ->
-  // 267; with pages of 16 slots nothing to 2 %; one long request, whose pieces get four times as
-  // many, 91 -> 111.)
+  // (96 block-scaled requests with pages of one slot 334 -> 279 us, of two 273 -> 269, per-tensor
+  // scales 304 -> 262; with pages of 16 slots nothing to 2 %; one long request, whose pieces get four
+  // times as many, 91 -> 111.)
   P.hw = !P.hnd && P.ps < 8 && P.Hk % 4 == 0 && (long long)P.batch * P.Hk * tiles >= P.grid ? 4 : 1;
   P.planes = P.Hk / P.hw * tiles;
   // Units of the longest row that the table (the list of pages, the window) allows.
@@ -952,9 +953,10 @@ cudaError_t launch_decode_nt(DecodeParams& P, cudaStream_t st) {
 
 template <typename T, int FMT>
 cudaError_t launch_decode(int d, DecodeParams& P, cudaStream_t st) {
-  // (16 query heads a KV head: 360 us for 64 ragged requests over bf16, 301 for 96 over
+  // (16 query heads a KV head: 359 us for 64 ragged requests over bf16, 306 for 96 over
   // block-scaled FP8; as two tiles of eight 457 and 456 before rows were asked for ahead, when one
-  // tile took 380 and 350)
+  // tile took 380 and 350. Heads of 256 go as two tiles, which read the keys twice: 427 and 454 us,
+  // of 343 and 229 at the copy rate.)
   const bool wide = P.G > 8;
   switch (d) {
     case 64: return wide ? launch_decode_nt<T, 64, FMT, 2>(P, st) : launch_decode_nt<T, 64, FMT, 1>(P, st);

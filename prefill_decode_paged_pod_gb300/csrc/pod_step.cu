@@ -320,8 +320,8 @@ extern "C" pod_status pod_step_tables(const pod_step_args* a, void* stream) {
   P.max_pages = a->max_pages;
   cudaStream_t st = (cudaStream_t)stream;
   const int threads = a->batch <= 128 ? 128 : a->batch >= kStepThreads ? kStepThreads : (a->batch + 31) / 32 * 32;
-  // No more rows than threads: the first block writes them (64 requests of one token 3.2 us,
-  // by a second kernel 4.7; 1024 of them 6.2 and 7.5; 8 requests with 2048 rows 10.3 and 4.7).
+  // No more rows than threads: the first block writes them (64 requests of one token 3.6 us,
+  // by a second kernel 5.2; 1024 of them 6.6 and 8.5; 8 requests with 2048 rows 10.2 and 4.8).
   P.rows_here = !a->kv_indptr && a->max_rows <= threads;
   cudaError_t e = launch_beside(step_kernel, 1, (unsigned)threads, 0, 1, st, P);
   const int64_t entries = (int64_t)a->max_rows + (a->kv_indptr ? a->max_pages : 0);
