@@ -114,6 +114,8 @@ template <typename T, int FMT>
 constexpr float lag() {
   return Pack<T>::kBF16 && FMT != POD_KV_16BIT ? 2.f : 8.f;
 }
+constexpr float kNoKey = -3.4028234663852886e38f;    // the reference before the first key: the lowest number
+constexpr float kFar = 65536.f;                      // base-2 logits to which V's exponent is not added as they are
 
 // o += a * hi, + a * lo where PARTS is 2. fp16's lo comes times 2^11 and is summed by itself (in
 // o's own sum, without the factor: 16 query heads a KV head over block scales 331 us, 353 now, over
@@ -168,7 +170,7 @@ POD_DEV float sink_factor(float lse, float sink) {
 template <int D, int HT>
 struct alignas(16) DecodeShared {
   float o[kDecodeWarps][HT][D];
-  float m[3][kDecodeWarps][HT];    // m, l, and O's reference
+  float m[3][kDecodeWarps][HT];    // r, l, and O's reference from r on
 };
 
 template <int D, int HT>
@@ -186,7 +188,12 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
   constexpr float kUp = weight_up<T, FMT>(), kLag = lag<T, FMT>();
   constexpr int MT = S::MT, TK = S::TK;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  float o[NT][S::NV][S::CV / 2][4], m[NT][2], mv[NT][2], l[NT][2];
+  // r: the reference of l, less the weights' factor 2^kUp; rv: that of O, counted from r on. (V's
+  // exponent is added to a logit only once r is off it, and every rounding of a reference is one
+  // towards smaller weights, so logits of any size neither lose V's exponent nor pass fp16's range.
+  // As sums of logit and exponent, which lost it from some 2^20 on, over block scales: 251.3 us, 252.3
+  // now, with 16 query heads a KV head 306 and 321.)
+  float o[NT][S::NV][S::CV / 2][4], r[NT][2], rv[NT][2], l[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -195,8 +202,8 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
       for (int i = 0; i < S::CV / 2; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[n][b][i][c] = 0.f;
-    m[n][0] = m[n][1] = mv[n][0] = mv[n][1] = -INFINITY;
-    l[n][0] = l[n][1] = 0.f;
+    r[n][0] = r[n][1] = kNoKey;
+    rv[n][0] = rv[n][1] = l[n][0] = l[n][1] = 0.f;
   }
 
   // ---- addresses: rows of d elements; a key's K row is index * key_step + rows of the head
@@ -433,64 +440,89 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
             float& y = x[s][n][2 * a + c];
             if constexpr (FMT == POD_KV_E4M3_BLOCK) y = live ? y * ks * xs[n][c] : -INFINITY;
             else y = live ? y * xs[n][c] : -INFINITY;
-            past |= y > m[n][c] + kLag;
-            if constexpr (FMT == POD_KV_E4M3_BLOCK) past |= y + xe[s][a] > mv[n][c] + kLag;
+            past |= y > __fadd_rd(r[n][c], kUp + kLag);
+          }
+        if constexpr (FMT == POD_KV_E4M3_BLOCK)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float t0, t1;
+            const uint64_t e2 = add2(pack2(x[s][n][2 * a], x[s][n][2 * a + 1]), pack2(-r[n][0], -r[n][1]));
+            unpack2(add2(e2, pack2(xe[s][a], xe[s][a])), t0, t1);
+            past |= t0 > rv[n][0] + (kUp + kLag) || t1 > rv[n][1] + (kUp + kLag);
           }
       }
     if (__any_sync(0xffffffffu, past)) {
+      auto below = [](float top) { return kUp > 0.f ? __fadd_ru(top, -kUp) : top - kUp; };
+      auto most = [&](int n, int c, auto value) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int s = 0; s < MT; ++s)
+#pragma unroll
+          for (int a = 0; a < 2; ++a) top = fmaxf(top, value(x[s][n][2 * a + c], xe[s][a]));
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        return top;
+      };
+      float to[NT][2], tov[NT][2];                 // the new r; the largest of logit and exponent
+      bool large = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float top = m[n][c], topv = mv[n][c];
+          const float top = most(n, c, [](float y, float) { return y; });
+          if constexpr (FMT == POD_KV_E4M3_BLOCK) tov[n][c] = most(n, c, [](float y, float e) { return y + e; });
+          to[n][c] = fmaxf(r[n][c], below(top));
+          large |= fabsf(top) >= kFar && top > kNoKey;
+        }
+      if constexpr (FMT == POD_KV_E4M3_BLOCK) {
+        const bool far = __any_sync(0xffffffffu, large);
 #pragma unroll
-          for (int s = 0; s < MT; ++s)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
-              top = fmaxf(top, x[s][n][2 * a + c]);
-              if constexpr (FMT == POD_KV_E4M3_BLOCK) topv = fmaxf(topv, x[s][n][2 * a + c] + xe[s][a]);
-            }
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) {
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            if constexpr (FMT == POD_KV_E4M3_BLOCK) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, d));
+          for (int c = 0; c < 2; ++c) {
+            tov[n][c] -= to[n][c];
+            if (far) tov[n][c] = most(n, c, [&](float y, float e) { return y - to[n][c] + e; });
           }
-          const float f = top == -INFINITY ? 1.f : ex2(m[n][c] - top);
-          m[n][c] = top;
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float by = r[n][c] - to[n][c];
+          float f = ex2(by);
+          r[n][c] = to[n][c];
           l[n][c] *= f;
-          float fo = f;
           if constexpr (FMT == POD_KV_E4M3_BLOCK) {
-            fo = topv == -INFINITY ? 1.f : ex2(mv[n][c] - topv);
-            mv[n][c] = topv;
+            const float old = rv[n][c] + by;
+            rv[n][c] = fmaxf(old, below(tov[n][c]));
+            f = ex2(old - rv[n][c]);
           }
 #pragma unroll
           for (int b = 0; b < S::NV; ++b)
 #pragma unroll
             for (int i = 0; i < S::CV / 2; ++i) {
-              o[n][b][i][c] *= fo;
-              o[n][b][i][2 + c] *= fo;
+              o[n][b][i][c] *= f;
+              o[n][b][i][2 + c] *= f;
             }
         }
     }
     uint32_t ph[MT][NT][2], pl[MT][NT][2];       // P^T as operand: keys 2t.., 2t + 8..; head g
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const float r0 = (m[n][0] == -INFINITY ? 0.f : m[n][0]) - kUp, r1 = (m[n][1] == -INFINITY ? 0.f : m[n][1]) - kUp;
-      float rv0 = r0, rv1 = r1;
-      if constexpr (FMT == POD_KV_E4M3_BLOCK) {
-        rv0 = (mv[n][0] == -INFINITY ? 0.f : mv[n][0]) - kUp;
-        rv1 = (mv[n][1] == -INFINITY ? 0.f : mv[n][1]) - kUp;
-      }
 #pragma unroll
       for (int s = 0; s < MT; ++s)
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
-          float p0 = ex2(x[s][n][2 * a] - r0), p1 = ex2(x[s][n][2 * a + 1] - r1);
+          float e0, e1;
+          const uint64_t e2 = add2(pack2(x[s][n][2 * a], x[s][n][2 * a + 1]), pack2(-r[n][0], -r[n][1]));
+          unpack2(e2, e0, e1);
+          float p0 = ex2(e0), p1 = ex2(e1);
           l[n][0] += p0;
           l[n][1] += p1;
           if constexpr (FMT == POD_KV_E4M3_BLOCK) {
-            p0 = ex2(x[s][n][2 * a] + xe[s][a] - rv0);
-            p1 = ex2(x[s][n][2 * a + 1] + xe[s][a] - rv1);
+            unpack2(add2(add2(e2, pack2(xe[s][a], xe[s][a])), pack2(-rv[n][0], -rv[n][1])), e0, e1);
+            p0 = ex2(e0);
+            p1 = ex2(e1);
           }
           if constexpr (S::PARTS == 2) {
             uint32_t hi, lo;
@@ -546,9 +578,9 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
       for (int d = 4; d < 32; d <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], d);
       if (g == 0) {
         const int h = n * 8 + 2 * t + c;
-        sh.m[0][warp][h] = m[n][c];
+        sh.m[0][warp][h] = r[n][c];
         sh.m[1][warp][h] = l[n][c];
-        sh.m[2][warp][h] = FMT == POD_KV_E4M3_BLOCK ? mv[n][c] : m[n][c];
+        if constexpr (FMT == POD_KV_E4M3_BLOCK) sh.m[2][warp][h] = rv[n][c];
       }
     }
 #pragma unroll
@@ -567,36 +599,39 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
 }
 
 // The sum of a CTA's n <= 4 pieces at one float4 of a row, normalised, and the row's LSE;
-// `lanes` neighbouring lanes with n pieces each share it. Piece w has its m, l and O's
-// reference at stat(w, 0..2) and its O at value(w).
+// `lanes` neighbouring lanes with n pieces each share it. Piece w has its r, l and O's
+// reference from r on at stat(w, 0..2) and its O at value(w).
 template <int FMT, typename A, typename B>
-POD_DEV float4 join(int n, int lanes, float up, float v_scale, float& lse, A stat, B value) {
+POD_DEV float4 join(int n, int lanes, float v_scale, float& lse, A stat, B value) {
   float m[kDecodeWarps], mo[kDecodeWarps], l[kDecodeWarps];
   float4 p[kDecodeWarps];
   float top = -INFINITY, topv = -INFINITY;
 #pragma unroll
   for (int w = 0; w < kDecodeWarps; ++w) {
-    m[w] = mo[w] = -INFINITY;
-    l[w] = 0.f;
+    m[w] = -INFINITY;
+    mo[w] = l[w] = 0.f;
     p[w] = make_float4(0, 0, 0, 0);
     if (w >= n) continue;
     m[w] = stat(w, 0);
     l[w] = stat(w, 1);
-    mo[w] = stat(w, 2);
+    if constexpr (FMT == POD_KV_E4M3_BLOCK) mo[w] = stat(w, 2);
     p[w] = value(w);
     top = fmaxf(top, m[w]);
+  }
+  for (int o = 1; o < lanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+  for (int w = 0; w < kDecodeWarps; ++w) {
+    m[w] -= top;
+    mo[w] += m[w];
     topv = fmaxf(topv, mo[w]);
   }
-  for (int o = 1; o < lanes; o <<= 1) {
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, o));
-  }
-  const float z = top == -INFINITY ? 0.f : top, zv = topv == -INFINITY ? 0.f : topv;
+  if constexpr (FMT == POD_KV_E4M3_BLOCK)
+    for (int o = 1; o < lanes; o <<= 1) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, o));
   float sum = 0.f;
   float4 acc = make_float4(0, 0, 0, 0);
 #pragma unroll
   for (int w = 0; w < kDecodeWarps; ++w) {
-    const float f = ex2(m[w] - z), fv = ex2(mo[w] - zv);
+    const float f = ex2(m[w]), fv = FMT == POD_KV_E4M3_BLOCK ? ex2(mo[w] - topv) : f;
     sum += l[w] * f;
     acc.x += p[w].x * fv; acc.y += p[w].y * fv; acc.z += p[w].z * fv; acc.w += p[w].w * fv;
   }
@@ -608,12 +643,12 @@ POD_DEV float4 join(int n, int lanes, float up, float v_scale, float& lse, A sta
     acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
   }
   // (sum == 0: no visible key; a NaN stays one)
-  lse = sum == 0.f ? -INFINITY : z + log2f(sum) - up;
+  lse = sum == 0.f ? -INFINITY : top + log2f(sum);
   const float f = sum == 0.f ? 0.f : v_scale / sum;
   acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
   if constexpr (FMT == POD_KV_E4M3_BLOCK) {
     // O's own reference, in two steps (2^-127, the smallest scale, is 0 to the exponential)
-    const float back = ex2(0.5f * (zv - z));
+    const float back = ex2(0.5f * topv);
     acc.x = acc.x * back * back; acc.y = acc.y * back * back;
     acc.z = acc.z * back * back; acc.w = acc.w * back * back;
   }
@@ -729,7 +764,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
     for (int i = tid; i < P.hw * heads * (D / 4); i += kDecodeThreads) {
       const int c4 = i % (D / 4), k = i / (D / 4) / heads, h = i / (D / 4) - k * heads;   // of KV head hk0 + k
       float lse;
-      const float4 o = join<FMT>(parts, 1, weight_up<T, FMT>(), P.v_scale, lse,
+      const float4 o = join<FMT>(parts, 1, P.v_scale, lse,
                                  [&](int w, int what) { return sh.m[what][k + w * P.hw][h]; },
                                  [&](int w) { return *reinterpret_cast<const float4*>(&sh.o[k + w * P.hw][h][4 * c4]); });
       if (whole) {
@@ -777,7 +812,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
     const int i = i0 + tid / CL, j = min(i, heads * (D / 4) - 1), h = j / (D / 4), c4 = j - h * (D / 4);
     float lse;
     const float4 o = join<FMT>(
-        kDecodeWarps, CL, weight_up<T, FMT>(), P.v_scale, lse,
+        kDecodeWarps, CL, P.v_scale, lse,
         [&](int w, int what) {
           float x;
           const uint32_t a = base + (uint32_t)offsetof_m<D, HT>(what, w, h);

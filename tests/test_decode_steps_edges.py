@@ -195,6 +195,45 @@ def test_smallest_and_largest_scales_of_values(byte, most, n, pad):
 
 
 @gpu
+@pytest.mark.parametrize("n,pad", [(1, 0), (40, 0), (3000, 0), (40, 3000)])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("fmt,dtype,mag", [(f, t, m) for f in ("16bit", "scaled", "block") for t in ("bf16", "fp16")
+                                           for m in (1e5, 2e7, 7e7, 3e8, 1e12, 1e30) if t == "bf16" or m < 4e8])
+def test_logits_of_any_size(fmt, dtype, mag, sign, n, pad):
+    """Logits of some `mag`, single products whose nearest neighbours are a sixteenth of that apart, so that the keys
+    of the largest one share the weight. In fp32 a logit is then off by more than its exponential can bear, but equal
+    ones are equal: the result is the mean of these keys' values, off by 2^-11 of each weight (and of their sum) at
+    most, and by its own rounding."""
+    dt, hk, G, d, ps = DT[dtype], 2, 4, 64, 16
+    tab, pages = table_of([n], ps, 1, pad=pad)
+    kv, sc = make_cache(pages, ps, hk, d, "NHD", fmt, dt, 2)
+    g = torch.Generator().manual_seed(3)
+    kv[:, 0] = 0
+    kv[:, 0, ..., 0] = (torch.randint(16, 32, kv[:, 0, ..., 0].shape, generator=g).float() * sign).to(kv.dtype).cuda()
+    if fmt == "block":
+        sc[:, 0] = 127
+    q = torch.zeros((1, hk * G, d))
+    q[..., 0] = mag / 2 if mag > 4e8 else mag * 8 / 24            # (s = 1/8, k of 16 to 31)
+    args = fmt_args(fmt, sc)
+    x = values64(kv, sc, "NHD", fmt)
+    if mag <= 4e8 and dtype == "fp16":                            # (fp16 ends at 65504: the scale takes the rest)
+        args["sm_scale"] = mag / 24 / 4096
+        q[..., 0] = 4096.0
+    q = q.to(dt).cuda()
+    out, lse = pod.pod_paged_decode(q, kv, torch.from_numpy(tab).cuda(), torch.tensor([n], dtype=torch.int32, device="cuda"),
+                                    **args)
+    page, slot = dense_keys(tab[0], n, ps, 1, -1)[0]
+    for h in range(hk * G):
+        k, v = x[page, 0, slot, h // G, 0], x[page, 1, slot, h // G]
+        top = v[k == k.max()]
+        err = (out[0, h].double().cpu() - top.mean(0)).abs()
+        tol = torch.finfo(dt).eps / 2 * top.mean(0).abs() * (1 + 2.0 ** -7) + 2 * (2.0 ** -11 + 2.0 ** -20) * top.abs().mean(0)
+        assert (err <= tol + torch.finfo(dt).tiny).all(), (h, err.max())
+        want = float(q[0, h, 0].double() * k.max() * (args.get("sm_scale") or 1 / 8)) * 1.4426950408889634
+        assert abs(lse[0, h].item() - want) <= abs(want) * 2.0 ** -20 + 13
+
+
+@gpu
 @pytest.mark.parametrize("H,hk,d,ps,fmt,dtype", [(72, 4, 128, 1, "16bit", "bf16"), (40, 4, 256, 2, "block", "fp16"),
                                                  (160, 8, 64, 3, "scaled", "bf16")])
 def test_small_pages_and_two_tiles_of_heads(H, hk, d, ps, fmt, dtype):
