@@ -34,7 +34,7 @@
 // tile's rows asked for into L2. Measured on two GB300s, in graphs, of the measured copy rate: 64
 // requests of 512 to 16384 keys, 32/8 heads of 128, bf16: 326 to 333 us, 101 to 103 %; one request
 // of 131072 keys, 64/8 heads: 86 to 88 us, 91 %; 96 requests of 4096 to 12288 keys over block-scaled
-// FP8: 243 to 252 us, 89 to 92 % (per-tensor scales 238 to 247; HND pages 237 and 230): the conversions and the
+// FP8: 244 to 253 us, 89 to 92 % (per-tensor scales 238 to 247; HND pages 238 and 230): the conversions and the
 // softmax of twice as many keys a byte, and rows of 128 bytes a kilobyte apart. 32-byte loads
 // and page numbers two tiles ahead made 332 of 352 and 260 of 307 us. K and V through a ring of
 // asynchronous copies in shared memory took 430 and 310, K's codes as E4M3 operands (the legacy E4M3
@@ -950,7 +950,7 @@ cudaError_t launch_decode_nt(DecodeParams& P, cudaStream_t st) {
   P.grid = 152 * per_sm;
   // A CTA's warps take four KV heads instead of four parts of one head's keys where a head's
   // rows in a page of an NHD cache are few: neighbouring heads' rows are neighbours in memory.
-  // (96 block-scaled requests with pages of one slot 334 -> 279 us, of two 273 -> 269, per-tensor
+  // (96 block-scaled requests with pages of one slot 334 -> 280 us, of two 273 -> 270, per-tensor
   // scales 304 -> 262; with pages of 16 slots nothing to 2 %; one long request, whose pieces get four
   // times as many, 91 -> 111.)
   P.hw = !P.hnd && P.ps < 8 && P.Hk % 4 == 0 && (long long)P.batch * P.Hk * tiles >= P.grid ? 4 : 1;
@@ -988,9 +988,9 @@ cudaError_t launch_decode_nt(DecodeParams& P, cudaStream_t st) {
 
 template <typename T, int FMT>
 cudaError_t launch_decode(int d, DecodeParams& P, cudaStream_t st) {
-  // (16 query heads a KV head: 359 us for 64 ragged requests over bf16, 306 for 96 over
+  // (16 query heads a KV head: 359 us for 64 ragged requests over bf16, 321 for 96 over
   // block-scaled FP8; as two tiles of eight 457 and 456 before rows were asked for ahead, when one
-  // tile took 380 and 350. Heads of 256 go as two tiles, which read the keys twice: 427 and 454 us,
+  // tile took 380 and 350. Heads of 256 go as two tiles, which read the keys twice: 435 and 445 us,
   // of 343 and 229 at the copy rate.)
   const bool wide = P.G > 8;
   switch (d) {
