@@ -34,8 +34,8 @@
 // tile's rows asked for into L2. Measured on two GB300s, in graphs, of the measured copy rate: 64
 // requests of 512 to 16384 keys, 32/8 heads of 128, bf16: 326 to 333 us, 101 to 103 %; one request
 // of 131072 keys, 64/8 heads: 86 to 88 us, 91 %; 96 requests of 4096 to 12288 keys over block-scaled
-// FP8: 244 to 253 us, 89 to 92 % (per-tensor scales 238 to 247; HND pages 238 and 230): the conversions and the
-// softmax of twice as many keys a byte, and rows of 128 bytes a kilobyte apart. 32-byte loads
+// FP8: 244 to 253 us, 89 to 92 % (per-tensor scales 238 to 247; HND pages 238 and 230): the
+// conversions and the softmax of twice as many keys a byte, and rows of 128 bytes a kilobyte apart. 32-byte loads
 // and page numbers two tiles ahead made 332 of 352 and 260 of 307 us. K and V through a ring of
 // asynchronous copies in shared memory took 430 and 310, K's codes as E4M3 operands (the legacy E4M3
 // mma) 295, the next segment's first tile asked for before the warps' sums join 331 and 270.
