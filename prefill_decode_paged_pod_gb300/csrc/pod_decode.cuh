@@ -5,7 +5,8 @@
 // p = 2^(x - m), l = sum p, o = sum p v / l. m is a reference that may lag behind the
 // running maximum, by 8 or 2 at most: it moves, and O with it, only when a logit passes it by
 // more than that (one vote a tile instead of shuffles for the maximum; the lag is a factor
-// that l and O share). Pieces of a request's keys join by their base-2 LSE. Over a
+// that l and O share). Pieces of a request's keys join by reference and sum (a base-2 LSE would
+// lose the sum beside large references). Over a
 // block-scaled cache O has a reference of its own, that of p * 2^(V's exponent).
 //
 // Layout. Both products run transposed, S^T = K Q^T and O^T = V^T P^T, as
@@ -598,11 +599,12 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
   __syncthreads();
 }
 
-// The sum of a CTA's n <= 4 pieces at one float4 of a row, normalised, and the row's LSE;
+// The sum of a CTA's n <= 4 pieces at one float4 of a row, normalised, and in `at` the row's
+// reference and the sum of its weights;
 // `lanes` neighbouring lanes with n pieces each share it. Piece w has its r, l and O's
 // reference from r on at stat(w, 0..2) and its O at value(w).
 template <int FMT, typename A, typename B>
-POD_DEV float4 join(int n, int lanes, float v_scale, float& lse, A stat, B value) {
+POD_DEV float4 join(int n, int lanes, float v_scale, float2& at, A stat, B value) {
   float m[kDecodeWarps], mo[kDecodeWarps], l[kDecodeWarps];
   float4 p[kDecodeWarps];
   float top = -INFINITY, topv = -INFINITY;
@@ -643,7 +645,7 @@ POD_DEV float4 join(int n, int lanes, float v_scale, float& lse, A stat, B value
     acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
   }
   // (sum == 0: no visible key; a NaN stays one)
-  lse = sum == 0.f ? -INFINITY : top + log2f(sum);
+  at = make_float2(top, sum);
   const float f = sum == 0.f ? 0.f : v_scale / sum;
   acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
   if constexpr (FMT == POD_KV_E4M3_BLOCK) {
@@ -655,8 +657,12 @@ POD_DEV float4 join(int n, int lanes, float v_scale, float& lse, A stat, B value
   return acc;
 }
 
+// base-2 LSE of a row
+POD_DEV float lse_of(float2 at) { return at.y == 0.f ? -INFINITY : at.x + log2f(at.y); }
+
 template <typename T>
-POD_DEV void store_out(const DecodeParams& P, int row, int head, int D, int c4, float4 o, float lse) {
+POD_DEV void store_out(const DecodeParams& P, int row, int head, int D, int c4, float4 o, float2 at) {
+  const float lse = lse_of(at);
   if (P.sinks && lse != -INFINITY) {
     const float f = sink_factor(lse, P.sinks[head]);
     o.x *= f; o.y *= f; o.z *= f; o.w *= f;
@@ -763,16 +769,16 @@ __global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
     const int slot = (int)blockIdx.x * 2 + (u == u_start ? 0 : 1);
     for (int i = tid; i < P.hw * heads * (D / 4); i += kDecodeThreads) {
       const int c4 = i % (D / 4), k = i / (D / 4) / heads, h = i / (D / 4) - k * heads;   // of KV head hk0 + k
-      float lse;
-      const float4 o = join<FMT>(parts, 1, P.v_scale, lse,
+      float2 at;
+      const float4 o = join<FMT>(parts, 1, P.v_scale, at,
                                  [&](int w, int what) { return sh.m[what][k + w * P.hw][h]; },
                                  [&](int w) { return *reinterpret_cast<const float4*>(&sh.o[k + w * P.hw][h][4 * c4]); });
       if (whole) {
-        store_out<T>(P, row, (hk0 + k) * P.G + tile0 + h, D, c4, o, lse);
+        store_out<T>(P, row, (hk0 + k) * P.G + tile0 + h, D, c4, o, at);
       } else {
         const long long piece = ((long long)slot * P.hw + k) * HT + h;
         *reinterpret_cast<float4*>(P.piece_o + piece * D + 4 * c4) = o;
-        if (c4 == 0) P.piece_lse[piece] = lse;
+        if (c4 == 0) P.piece_at[piece] = at;
       }
     }
     __syncthreads();                               // (the buffers are the next segment's)
@@ -810,9 +816,9 @@ __global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
   const int per = kDecodeThreads / CL;             // float4s of a CTA at a time
   for (int i0 = rank * per; i0 < heads * (D / 4); i0 += per * CL) {
     const int i = i0 + tid / CL, j = min(i, heads * (D / 4) - 1), h = j / (D / 4), c4 = j - h * (D / 4);
-    float lse;
+    float2 at;
     const float4 o = join<FMT>(
-        kDecodeWarps, CL, P.v_scale, lse,
+        kDecodeWarps, CL, P.v_scale, at,
         [&](int w, int what) {
           float x;
           const uint32_t a = base + (uint32_t)offsetof_m<D, HT>(what, w, h);
@@ -826,14 +832,14 @@ __global__ void __launch_bounds__(kDecodeThreads, (D == 256 || NT == 2) ? 2 : 3)
                        : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(a) : "memory");
           return x;
         });
-    if (i == j && tid % CL == 0) store_out<T>(P, row, h0 + h, D, c4, o, lse);
+    if (i == j && tid % CL == 0) store_out<T>(P, row, h0 + h, D, c4, o, at);
   }
   if (CL > 1)                                      // (nobody leaves while others read its memory)
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Rows whose keys were cut: the pieces in the order of the keys, weighted by
-// 2^(lse - M). Rows without keys: 0 and -inf. WPR warps work on a (request, head).
+// sum * 2^(reference - M). Rows without keys: 0 and -inf. WPR warps work on a (request, head).
 template <typename T, int D, int HT, int TK, int WPR>
 __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant__ DecodeParams P) {
   constexpr int PL = D / 32 < 4 ? D / 32 : 4, NP = D / (32 * PL);      // elements and chunks of a lane
@@ -867,9 +873,9 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
   const int w0 = WPR > 1 ? warp : 0, n = c1 - c0 + 1;
   // piece k of the row: the CTA's first segment, or its second where the row begins inside its run
   const bool inside = quotient(all * c0, runs) != g0;
-  auto lse_of = [&](int k) { return P.piece_lse[((long long)2 * (c0 + k) + (k == 0 && inside)) * per + h]; };
-  // The largest LSE, then the weights, a lane a piece; the first pieces are asked for beside the
-  // LSEs.
+  auto at_of = [&](int k) { return P.piece_at[((long long)2 * (c0 + k) + (k == 0 && inside)) * per + h]; };
+  // The largest reference, then the weights, a lane a piece; the first pieces are asked for beside
+  // the references.
   constexpr int U = WPR > 1 ? 8 : 4;               // pieces in flight
   float x[U][NP][PL];
   auto load = [&](int k0, int end) {               // pieces k0, k0 + WPR, ... (the last one for those past the end)
@@ -885,20 +891,20 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
     }
   };
   float top = -INFINITY, sum = 0.f;
-  float mine = lane < n ? lse_of(lane) : -INFINITY;
+  const float2 none = make_float2(-INFINITY, 0.f);
+  float2 mine = lane < n ? at_of(lane) : none;
   load(w0, n);
-  for (int k = lane; k < n; k += 32) top = fmaxf(top, k == lane ? mine : lse_of(k));
+  for (int k = lane; k < n; k += 32) top = fmaxf(top, k == lane ? mine.x : at_of(k).x);
 #pragma unroll
   for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  const float z = top == -INFINITY ? 0.f : top;
   float acc[NP][PL];
 #pragma unroll
   for (int j = 0; j < NP; ++j)
 #pragma unroll
     for (int e = 0; e < PL; ++e) acc[j][e] = 0.f;
   for (int k32 = 0; k32 < n; k32 += 32) {
-    if (k32) mine = k32 + lane < n ? lse_of(k32 + lane) : -INFINITY;
-    const float f = k32 + lane < n ? ex2(mine - z) : 0.f;
+    if (k32) mine = k32 + lane < n ? at_of(k32 + lane) : none;
+    const float f = k32 + lane < n ? mine.y * ex2(mine.x - top) : 0.f;
     sum += f;                                      // (of all warps' pieces: every warp has them)
     const int end = min(32, n - k32);
     for (int k0 = w0; k0 < end; k0 += WPR * U) {
@@ -931,7 +937,7 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const __grid_constant
         for (int w = 0; w < WPR; ++w) acc[j][e] += sh[w][(j * 32 + lane) * PL + e];
       }
   }
-  const float lse = sum == 0.f ? -INFINITY : z + log2f(sum);
+  const float lse = lse_of(make_float2(top, sum));
   float f = sum == 0.f ? 0.f : 1.f / sum;
   if (P.sinks && sum != 0.f) f *= sink_factor(lse, P.sinks[head]);
 #pragma unroll

@@ -29,7 +29,7 @@ struct DecodeParams {
   long long* total;
   long long* first;
   float* piece_o;                  // [grid * 2][hw][heads of a tile][d], normalised
-  float* piece_lse;                // [grid * 2][hw][heads of a tile], base 2
+  float2* piece_at;                // [grid * 2][hw][heads of a tile]: reference and sum of its weights
   long long q_stride, out_stride, table_stride;
   unsigned num_pages;
   int batch, H, Hk, G, width, ps, ps_shift, hnd, num_selected, window;   // ps_shift: -1 where ps is no power of two

@@ -44,7 +44,7 @@ size_t pod_paged_decode_workspace_size(int32_t batch, int32_t num_qo_heads, int3
       (head_dim != 64 && head_dim != 128 && head_dim != 256))
     return 0;
   const size_t rows = piece_rows(num_qo_heads, num_kv_heads, head_dim);
-  return first_bytes(batch) + round256(rows * 4) + rows * head_dim * 4;
+  return first_bytes(batch) + round256(rows * sizeof(float2)) + rows * head_dim * 4;
 }
 
 pod_status pod_paged_decode(const pod_decode_args* a, void* stream) {
@@ -85,8 +85,8 @@ pod_status pod_paged_decode(const pod_decode_args* a, void* stream) {
   P.total = reinterpret_cast<long long*>(w);
   P.first = P.total + 1;
   w += first_bytes(a->batch);
-  P.piece_lse = reinterpret_cast<float*>(w);
-  w += round256(piece_rows(a->num_qo_heads, a->num_kv_heads, a->head_dim) * 4);
+  P.piece_at = reinterpret_cast<float2*>(w);
+  w += round256(piece_rows(a->num_qo_heads, a->num_kv_heads, a->head_dim) * sizeof(float2));
   P.piece_o = reinterpret_cast<float*>(w);
   P.q_stride = a->q_stride;
   P.out_stride = a->out_stride;

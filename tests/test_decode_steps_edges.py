@@ -195,7 +195,7 @@ def test_smallest_and_largest_scales_of_values(byte, most, n, pad):
 
 
 @gpu
-@pytest.mark.parametrize("n,pad", [(1, 0), (40, 0), (3000, 0), (40, 3000)])
+@pytest.mark.parametrize("n,pad", [(1, 0), (40, 0), (3000, 0), (40, 3000), (3000, 3000)])
 @pytest.mark.parametrize("sign", [1, -1])
 @pytest.mark.parametrize("fmt,dtype,mag", [(f, t, m) for f in ("16bit", "scaled", "block") for t in ("bf16", "fp16")
                                            for m in (1e5, 2e7, 7e7, 3e8, 1e12, 1e30) if t == "bf16" or m < 4e8])
