@@ -234,6 +234,25 @@ def test_logits_of_any_size(fmt, dtype, mag, sign, n, pad):
 
 
 @gpu
+@pytest.mark.parametrize("pad", [0, 3000])
+@pytest.mark.parametrize("fmt,dtype,e", [(f, "bf16", e) for f in ("16bit", "scaled", "block") for e in (-127, -100, 60, 110)]
+                         + [(f, "fp16", e) for f in ("16bit", "scaled", "block") for e in (-16, 12)])
+def test_queries_of_any_magnitude(fmt, dtype, e, pad):
+    """Queries of some 2^e, subnormal ones among them, under a scale of some 2^-e."""
+    dt, hk, H, d, ps = DT[dtype], 2, 10, 128, 16
+    lens = [600, 3]
+    tab, pages = table_of(lens, ps, 1, pad=pad)
+    kv, sc = make_cache(pages, ps, hk, d, "NHD", fmt, dt, 2)
+    q = (torch.randn((2, H, d), generator=torch.Generator().manual_seed(3), dtype=torch.float64) * 2.0 ** e).to(dt).cuda()
+    scale = 2.0 ** -(e + 3)
+    out, lse = pod.pod_paged_decode(q, kv, torch.from_numpy(tab).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                    sm_scale=scale, **fmt_args(fmt, sc))
+    x = values64(kv, sc, "NHD", fmt)
+    ref = [attend64(q[i].double().cpu().numpy(), x, dense_keys(tab[i], n, ps, hk, -1), scale, None) for i, n in enumerate(lens)]
+    check(out, lse, *(np.stack(y) for y in zip(*ref)), d, dt, fmt)
+
+
+@gpu
 @pytest.mark.parametrize("H,hk,d,ps,fmt,dtype", [(72, 4, 128, 1, "16bit", "bf16"), (40, 4, 256, 2, "block", "fp16"),
                                                  (160, 8, 64, 3, "scaled", "bf16")])
 def test_small_pages_and_two_tiles_of_heads(H, hk, d, ps, fmt, dtype):
