@@ -193,7 +193,8 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
   // exponent is added to a logit only once r is off it, and every rounding of a reference is one
   // towards smaller weights, so logits of any size neither lose V's exponent nor pass fp16's range.
   // As sums of logit and exponent, which lost it from some 2^20 on, over block scales: 251.3 us, 252.3
-  // now, with 16 query heads a KV head 306 and 321.)
+  // now, with 16 query heads a KV head 306 and 321, with fp16 results of these 353 and 363 to 389, as the
+  // compiler lays them out.)
   float o[NT][S::NV][S::CV / 2][4], r[NT][2], rv[NT][2], l[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
@@ -439,7 +440,8 @@ POD_DEV void attend(const DecodeParams& P, const Keys& K, int row, int hk, int h
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             float& y = x[s][n][2 * a + c];
-            if constexpr (FMT == POD_KV_E4M3_BLOCK) y = live ? y * ks * xs[n][c] : -INFINITY;
+            // (the two scales first: each by itself may take the product out of fp32)
+            if constexpr (FMT == POD_KV_E4M3_BLOCK) y = live ? y * (ks * xs[n][c]) : -INFINITY;
             else y = live ? y * xs[n][c] : -INFINITY;
             past |= y > __fadd_rd(r[n][c], kUp + kLag);
           }

@@ -253,6 +253,25 @@ def test_queries_of_any_magnitude(fmt, dtype, e, pad):
 
 
 @gpu
+@pytest.mark.parametrize("pad", [0, 3000])
+@pytest.mark.parametrize("e", [-120, -110, -90, 90, 110, 118])
+def test_keys_and_queries_far_apart(e, pad):
+    """Queries of some 2^e over keys whose block scales make up for them."""
+    dt, hk, H, d, ps = torch.bfloat16, 2, 10, 128, 16
+    lens = [600, 3]
+    tab, pages = table_of(lens, ps, 1, pad=pad)
+    kv, sc = make_cache(pages, ps, hk, d, "NHD", "block", dt, 2, 119, 122)
+    sc[:, 0] -= e
+    q = (torch.randn((2, H, d), generator=torch.Generator().manual_seed(3)) * 2.0 ** e).to(dt).cuda()
+    out, lse = pod.pod_paged_decode(q, kv, torch.from_numpy(tab).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                    kv_scales=sc)
+    x = values64(kv, sc, "NHD", "block")
+    scale = 1 / math.sqrt(d)
+    ref = [attend64(q[i].double().cpu().numpy(), x, dense_keys(tab[i], n, ps, hk, -1), scale, None) for i, n in enumerate(lens)]
+    check(out, lse, *(np.stack(y) for y in zip(*ref)), d, dt, "block")
+
+
+@gpu
 @pytest.mark.parametrize("H,hk,d,ps,fmt,dtype", [(72, 4, 128, 1, "16bit", "bf16"), (40, 4, 256, 2, "block", "fp16"),
                                                  (160, 8, 64, 3, "scaled", "bf16")])
 def test_small_pages_and_two_tiles_of_heads(H, hk, d, ps, fmt, dtype):
